@@ -290,7 +290,9 @@ def run(s):
         if op == "grow":
             slots, cu, lengths, count = api.page_grow(s["lengths"], s["new"], s["table"], s["free"], s["count"], s["page"], s["tokens"])
             return slots, cu, s["table"], lengths, count
-        cache = api.KV4Cache(s["k"], s["ks"], s["v"], s["vs"], s["key"], s["value"])
+        if "cache" not in s:  # the handle that a program makes once with its pool
+            s["cache"] = api.KV4Cache(s["k"], s["ks"], s["v"], s["vs"], s["key"], s["value"])
+        cache = s["cache"]
         if op == "store":
             api.kv4_store(s["new_k"], s["new_v"], s["slots"], cache)
         if op != "attend":
