@@ -285,7 +285,12 @@ enum {
   FA_KERNEL_FWD_MERGE = 6, /* split-KV merge of the forward's parts */
   FA_KERNEL_BWD_KVSUM = 7, /* sum of the dK/dV kernel's query-range parts */
   FA_KERNEL_BWD_QSUM = 8,  /* sum of the dQ kernel's key-range parts */
-  FA_KERNEL_KINDS = 9
+  FA_KERNEL_PAGE = 9,       /* page tables and slots (fa_paged.h) */
+  FA_KERNEL_KV4_STORE = 10, /* 4-bit cache: store */
+  FA_KERNEL_KV4_LOAD = 11,  /* 4-bit cache: load */
+  FA_KERNEL_KV4_ATTN = 12,  /* attention over the 4-bit cache */
+  FA_KERNEL_KV4_MERGE = 13, /* merge of its workers' parts */
+  FA_KERNEL_KINDS = 14
 };
 typedef struct {
   int launches[FA_KERNEL_KINDS];

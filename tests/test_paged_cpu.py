@@ -1,0 +1,160 @@
+"""The serving operators without a GPU: refusals through the C ABI and the torch layer,
+and the tests' own 64-bit restatements against hand-worked values."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv4_ref as R
+from tiled_attention_tmem_gb300 import api, binding as b, build
+
+A = 1 << 20  # an aligned fake address; never dereferenced
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build_library()
+    return b.lib()
+
+
+def test_page_validation():
+    ok = dict(B=2, width=4, page=16, T=8, free_size=9, lengths=A, new=A, table=A, free=A, count=A, slots=A, cu=A,
+              held=A, out=A)
+
+    def grow(**kw):
+        a = {**ok, **kw}
+        return b.fa_page_grow(a["lengths"], a["new"], a["table"], a["B"], a["width"], a["page"], a["free"],
+                              a["free_size"], a["count"], a["T"], a["slots"], a["cu"], a["held"], a["out"], None)
+
+    def slots(**kw):
+        a = {**ok, **kw}
+        return b.fa_page_slots(a["lengths"], a["new"], a["table"], a["B"], a["width"], a["page"], a["T"], a["slots"],
+                               a["cu"], None)
+
+    for call in (grow, slots):
+        for bad in (dict(B=-1), dict(width=-1), dict(T=-1), dict(page=0), dict(page=24), dict(page=256),
+                    dict(B=(1 << 21) + 1), dict(width=1 << 27), dict(lengths=0), dict(new=0), dict(table=0),
+                    dict(slots=0), dict(cu=0)):
+            assert call(**bad) == b.FA_ERR_INVALID_ARG, bad
+        assert call(B=0, lengths=0, new=0, table=0, slots=0, cu=0) == b.FA_OK
+    for bad in (dict(free=0), dict(count=0), dict(held=0), dict(out=0), dict(free_size=-1)):
+        assert grow(**bad) == b.FA_ERR_INVALID_ARG, bad
+
+
+def test_store_and_load_validation():
+    ok = dict(k=A, v=A, kt=256, kh=128, vt=256, vh=128, slots=A, T=4, H=2, d=128, kc=A, ks=A, vc=A, vs=A, pages=3,
+              page=16, kg=1.0, vg=1.0)
+
+    def store(**kw):
+        a = {**ok, **kw}
+        return b.fa_kv4_store(a["k"], a["v"], a["kt"], a["kh"], a["vt"], a["vh"], a["slots"], a["T"], a["H"], a["d"],
+                              a["kc"], a["ks"], a["vc"], a["vs"], a["pages"], a["page"], a["kg"], a["vg"], None)
+
+    def load(**kw):
+        a = {**ok, **kw}
+        return b.fa_kv4_load(a["slots"], a["T"], a["H"], a["d"], a["kc"], a["ks"], a["vc"], a["vs"], a["pages"],
+                             a["page"], a["kg"], a["vg"], a["k"], a["v"], None)
+
+    for call in (store, load):
+        for bad in (dict(T=-1), dict(H=-1), dict(pages=-1), dict(page=48), dict(kg=0.0), dict(vg=-1.0),
+                    dict(kg=float("nan")), dict(vg=float("inf")), dict(kg=1e-45), dict(k=0), dict(v=0), dict(slots=0),
+                    dict(kc=0), dict(vs=0)):
+            assert call(**bad) == b.FA_ERR_INVALID_ARG, bad
+        for bad in (dict(d=80), dict(d=32), dict(d=512)):
+            assert call(**bad) == b.FA_ERR_UNSUPPORTED, bad
+        for bad in (dict(k=A + 8), dict(v=A + 2), dict(kc=A + 4), dict(ks=A + 8), dict(vs=A + 1)):
+            assert call(**bad) == b.FA_ERR_MISALIGNED, bad
+        assert call(T=0, k=0, v=0, slots=0) == b.FA_OK
+    for bad in (dict(kt=255), dict(kh=4), dict(vt=1), dict(vh=132)):
+        assert store(**bad) == b.FA_ERR_MISALIGNED, bad
+
+
+def test_attention_validation():
+    ok = dict(q=A, qt=1024, qh=128, T=2, cu=A, max_q=1, kc=A, ks=A, vc=A, vs=A, pages=4, page=16, table=A, width=4,
+              lengths=A, B=2, H=8, Hkv=2, d=128, scale=0.1, kg=1.0, vg=1.0, o=A, ot=1024, oh=128, lse=A, ws=A, wsb=1 << 30)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return b.fa_kv4_attn(*(a[n] for n in ok), None)
+
+    for bad in (dict(T=-1), dict(B=-1), dict(max_q=-1), dict(H=7), dict(Hkv=0), dict(pages=-1), dict(width=-1),
+                dict(page=8), dict(scale=0.0), dict(scale=float("nan")), dict(kg=0.0), dict(vg=float("inf")),
+                dict(q=0), dict(o=0), dict(lse=0), dict(lengths=0), dict(table=0), dict(kc=0), dict(width=1 << 28),
+                dict(cu=0, T=1)):
+        assert call(**bad) == b.FA_ERR_INVALID_ARG, bad
+    for bad in (dict(d=80), dict(d=512)):
+        assert call(**bad) == b.FA_ERR_UNSUPPORTED, bad
+    for bad in (dict(q=A + 8), dict(o=A + 4), dict(vc=A + 2), dict(qt=1028), dict(qh=4), dict(ot=1), dict(oh=2)):
+        assert call(**bad) == b.FA_ERR_MISALIGNED, bad
+    need = b.fa_kv4_attn_workspace_size(2, 8, 2, 128, 1)
+    assert need > 0
+    for bad in (dict(ws=0), dict(ws=A + 16), dict(wsb=need - 1)):
+        assert call(**bad) == b.FA_ERR_WORKSPACE, bad
+    for empty in (dict(B=0), dict(T=0), dict(max_q=0)):
+        assert call(**empty, q=0, o=0, lse=0, lengths=0, ws=0) == b.FA_OK
+    for bad in ((-1, 8, 2, 128, 1), (2, 7, 2, 128, 1), (2, 8, 2, 100, 1), (2, 8, 2, 128, -1), (1 << 30, 8, 2, 128, 64)):
+        assert b.fa_kv4_attn_workspace_size(*bad) == 0
+
+
+def _cache():
+    def u8(*s):
+        return torch.zeros(s, dtype=torch.uint8)
+    return u8(4, 2, 16, 64), u8(4, 2, 16, 8), u8(4, 2, 16, 64), u8(4, 2, 16, 8)
+
+
+def test_torch_layer_refuses_host_tensors_and_wrong_kinds():
+    i32 = torch.zeros(2, dtype=torch.int32)
+    table = torch.zeros((2, 4), dtype=torch.int32)
+    one = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="contiguous CUDA"):
+        api.page_grow(i32, i32, table, i32, one, 16, 4)
+    with pytest.raises(ValueError, match="page_size"):
+        api.page_slots(i32, i32, table, 24, 4)
+    with pytest.raises(ValueError, match="num_tokens"):
+        api.page_slots(i32, i32, table, 16, -1)
+    with pytest.raises(ValueError, match="not torch.int64"):
+        api.page_slots(i32.long(), i32, table, 16, 4)
+    with pytest.raises(ValueError, match="1-D"):
+        api.page_slots(table, i32, table, 16, 4)
+    with pytest.raises(ValueError, match="contiguous CUDA"):
+        api.KV4Cache(*_cache())
+    with pytest.raises(ValueError, match="shape"):
+        api.KV4Cache(torch.zeros(4, dtype=torch.uint8), *_cache()[1:])
+    with pytest.raises(ValueError, match="uint8"):
+        api.KV4Cache(_cache()[0].int(), *_cache()[1:])
+    with pytest.raises(TypeError):
+        api.KV4Cache(None, *_cache()[1:])
+
+
+def test_reference_codes_and_scales():
+    assert R.e4m3_value(0x7E) == 448 and R.e4m3_value(0x7F) == 480 and R.e4m3_value(1) == 2.0 ** -9
+    assert R.e4m3_value(0xB8) == 1.0  # the sign bit is ignored
+    x = np.zeros((1, 16))
+    x[0, :8] = [6, -6, 0.25, 0.75, 1.25, -1.75, 2.5, 5.0]  # scale 1: the ties go to even
+    codes, scales = R.encode(x, 1.0)
+    got = R.decode(codes, scales, 1.0)[0, :8]
+    assert list(got) == [6, -6, 0, 1, 1, -2, 2, 4]
+    x = np.full((1, 16), 1e9)
+    assert np.all(R.decode(*R.encode(x, 1.0), 1.0) == 6 * 448)  # saturates
+    assert np.all(R.decode(*R.encode(np.full((1, 16), 1e-9), 1.0), 1.0) == 0)
+
+
+def test_reference_attention_on_one_key_and_two():
+    k = np.zeros((1, 1, 16, 64))
+    v = np.zeros((1, 1, 16, 64))
+    k[0, 0, 0, 0], k[0, 0, 1, 0] = 1.0, 3.0
+    v[0, 0, 0, 0], v[0, 0, 1, 0] = 10.0, 20.0
+    q = np.zeros((2, 1, 64))
+    q[:, 0, 0] = 0.5
+    o, lse, _, _, _ = R.attend(q, (k, v), np.zeros((1, 1), int), [2], [0, 2], 2, 1.0)
+    w = 1 / (1 + math.exp(1.0))
+    assert np.allclose(o[:, 0, 0], [10.0, 10 * w + 20 * (1 - w)]) and np.allclose(lse[:, 0], [0.5, math.log(math.exp(0.5) + math.exp(1.5))])
+
+
+def test_reference_pages_by_hand():
+    slots, cu, table, held, left = R.pages([15, 0, 32], [3, 1, 0], np.full((3, 2), 9), [5, 6, 7], 3, 16, 6)
+    assert list(cu) == [0, 3, 4, 4] and list(held) == [18, 1, 32] and left == 1
+    assert list(slots) == [9 * 16 + 15, 7 * 16, 7 * 16 + 1, 6 * 16, -1, -1]
+    assert table.tolist() == [[9, 7], [6, 9], [9, 9]]

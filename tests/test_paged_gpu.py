@@ -1,0 +1,580 @@
+"""Page tables, the 4-bit cache's store and load, and attention over it, against plain
+64-bit restatements (kv4_ref)."""
+
+import math
+
+import numpy as np
+import pytest
+
+import kv4_ref as R
+from helpers import to_dev, to_f64
+
+pytestmark = pytest.mark.gpu
+
+DIMS = (64, 96, 128, 192, 256, 384)
+
+
+def _dev(x, dtype):
+    import torch
+    return torch.tensor(np.asarray(x), dtype=dtype, device="cuda:0")
+
+
+def _i32(x):
+    import torch
+    return _dev(x, torch.int32)
+
+
+# ------------------------------------------------------------------ page tables
+
+def _grow_case(B, page, most, new, seed, free=None, width=None, T=None):
+    rng = np.random.default_rng(seed)
+    held = rng.integers(0, most + 1, B)
+    add = rng.integers(0, new + 1, B)
+    width = -(-(most + new) // page) if width is None else width
+    owned = np.minimum(-(-held // page), width)
+    ids = rng.permutation(int(owned.sum() + (-(-(held + add) // page)).sum()) + 7)
+    table = np.full((B, width), -7)
+    at = 0
+    for b in range(B):
+        table[b, :owned[b]] = ids[at:at + owned[b]]
+        at += owned[b]
+    stack = ids[at:]
+    count = len(stack) if free is None else free
+    return held, add, table, stack, count, int(add.sum()) + 3 if T is None else T
+
+
+@pytest.mark.parametrize("B,page,most,new,kw", [
+    (1, 16, 0, 1, {}), (1, 64, 100, 5000, {}), (3, 32, 70, 40, {}), (300, 16, 200, 1, {}), (777, 64, 900, 300, {}),
+    (40, 128, 1000, 600, {}), (5, 16, 64, 64, dict(free=3)), (64, 16, 64, 64, dict(free=0)),
+    (33, 16, 100, 60, dict(width=5)), (33, 16, 100, 60, dict(T=100)), (9, 32, 50, 50, dict(T=0)),
+    (2000, 16, 40, 3, {}), (4, 16, 50, 0, {}),
+], ids=str)
+def test_page_grow(B, page, most, new, kw):
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    held, add, table, stack, count, T = _grow_case(B, page, most, new, seed=B + page, **kw)
+    slots, cu, tab, hold, left = R.pages(held, add, table, stack, count, page, T)
+    t = _i32(table)
+    for _ in range(2):  # nothing but fresh table entries changes: a repeat gives the same
+        got = api.page_grow(_i32(held), _i32(add), t, _i32(stack), _i32([count]), page, T)
+        for g, r in zip(got, (slots, cu, hold, [left])):
+            assert np.array_equal(g.cpu().numpy(), r)
+        assert np.array_equal(t.cpu().numpy(), tab)
+    # The slots of all that is now held, from the finished table.
+    got, cu2 = api.page_slots(_i32(np.zeros(B, int)), _i32(hold), t, page, int(hold.sum()) + 2)
+    ref = R.pages(np.zeros(B, int), hold, tab, [], None, page, int(hold.sum()) + 2)
+    assert np.array_equal(got.cpu().numpy(), ref[0]) and np.array_equal(cu2.cpu().numpy(), ref[1])
+    assert got.dtype == torch.int64
+
+
+def test_page_grow_ignores_negative_counts_and_a_count_above_the_stack():
+    from tiled_attention_tmem_gb300 import api
+    held, add = [-5, 3, 20], [2, -4, 14]
+    table = np.full((3, 4), 2)
+    t = _i32(table)
+    got = api.page_grow(_i32(held), _i32(add), t, _i32([11, 12]), _i32([1000]), 16, 20)
+    ref = R.pages(held, add, table, [11, 12], 1000, 16, 20)
+    for g, r in zip(got, (ref[0], ref[1], ref[3], [ref[4]])):
+        assert np.array_equal(g.cpu().numpy(), r)
+    assert np.array_equal(t.cpu().numpy(), ref[2])
+
+
+def test_page_calls_with_no_requests_and_no_width():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    none = torch.empty(0, dtype=torch.int32, device="cuda:0")
+    slots, cu, held, count = api.page_grow(none, none, none.view(0, 0), none, _i32([0]), 16, 3)
+    assert slots.tolist() == [-1] * 3 and cu.tolist() == [0] and held.numel() == 0 and count.tolist() == [0]
+    slots, cu = api.page_slots(_i32([0]), _i32([2]), none.view(1, 0), 16, 3)
+    assert slots.tolist() == [-1] * 3 and cu.tolist() == [0, 2]
+
+
+# ------------------------------------------------------------------ store and load
+
+def _cache_arrays(cache):
+    return [t.cpu().numpy() for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
+
+
+@pytest.mark.parametrize("d", DIMS)
+@pytest.mark.parametrize("page,heads,T", [(16, 1, 1), (32, 3, 37), (64, 2, 130), (128, 5, 300)])
+def test_store_and_load(d, page, heads, T):
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    rng = np.random.default_rng(d + T)
+    pool = -(-T // page) + 3
+    x = rng.standard_normal((2, T, heads, d)) * np.exp(rng.standard_normal((2, T, heads, 1)) * 3)
+    bits = R.bf16(x)
+    # Slices of wider rows, as a fused projection leaves them.
+    wide = torch.zeros((T, 2 * heads * d + 24), dtype=torch.bfloat16, device="cuda:0")
+    k = wide[:, 8:8 + heads * d].unflatten(1, (heads, d))
+    v = wide[:, 16 + heads * d:16 + 2 * heads * d].unflatten(1, (heads, d))
+    k.copy_(to_dev(bits[0]))
+    v.copy_(to_dev(bits[1]))
+    slots = rng.permutation(pool * page)[:T].astype(np.int64)
+    slots[rng.random(T) < 0.1] = -1
+    if T > 3:
+        slots[1], slots[2] = pool * page, -(1 << 40)  # outside the pool
+    cache = api.KV4Cache.empty(pool, heads, page, d, 2.0 ** -5, 2.0 ** -6)
+    for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
+        t.fill_(0xA5)
+    api.kv4_store(k, v, _dev(slots, torch.int64), cache)
+    got = _cache_arrays(cache)
+    fine = (slots >= 0) & (slots < pool * page)
+    pg, off = slots[fine] // page, slots[fine] % page
+    for i, gain in ((0, 2.0 ** -5), (1, 2.0 ** -6)):
+        codes, scales = R.encode(to_f64(to_dev(bits[i])), gain)
+        want_c, want_s = np.full_like(got[2 * i], 0xA5), np.full_like(got[2 * i + 1], 0xA5)
+        want_c[pg, :, off], want_s[pg, :, off] = codes[fine], scales[fine]
+        assert np.array_equal(got[2 * i + 1], want_s)
+        same = got[2 * i] == want_c
+        # A zero keeps its sign in the cache; the restatement has no signed zero.
+        assert np.all(same | (R.e2m1_value(got[2 * i] & 15) == R.e2m1_value(want_c & 15))
+                      & (R.e2m1_value(got[2 * i] >> 4) == R.e2m1_value(want_c >> 4)))
+    lk, lv = api.kv4_load(_dev(slots, torch.int64), cache)
+    for i, (t, gain) in enumerate(((lk, 2.0 ** -5), (lv, 2.0 ** -6))):
+        want = np.zeros((T, heads, d))
+        want[fine] = R.decode(got[2 * i][pg, :, off], got[2 * i + 1][pg, :, off], gain)
+        assert np.array_equal(to_f64(t), want)  # gains that are powers of two: exact in bf16
+    api.check_device_error()
+
+
+def test_store_rounds_every_bf16_ratio_to_nearest_even():
+    """Every scale a row can get against every bf16 mantissa: ties and their neighbours."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    tops, small = [], []
+    for m in range(128, 256):  # the largest of a group sets the scale: amax / 6
+        for k in (128 + np.arange(128)):
+            tops.append(m / 128.0)
+            small.append(k / 128.0)
+    tops, small = np.array(tops), np.array(small)
+    x = np.zeros((len(tops), 16))
+    x[:, 0] = tops
+    for j in range(1, 8):
+        x[:, j] = np.minimum(small * 2.0 ** (1 - j), tops)
+        x[:, 15 - j] = -x[:, j]
+    x = np.concatenate([x, x * 2.0 ** -8, x * 2.0 ** 9])
+    x = x.reshape(-1, 4, 1, 16).transpose(0, 2, 1, 3).reshape(-1, 1, 64)
+    T = len(x)
+    cache = api.KV4Cache.empty(-(-T // 64), 1, 64, 64)
+    k = to_dev(R.bf16(x))
+    slots = torch.arange(T, device="cuda:0")
+    api.kv4_store(k, k, slots, cache)
+    codes, scales = R.encode(x, 1.0)
+    got = _cache_arrays(cache)
+    n = T // 64 * 64
+    assert np.array_equal(got[1].reshape(-1, 4)[:n], scales[:n, 0])
+    both = np.stack([got[0] & 15, got[0] >> 4], -1).reshape(-1, 64)[:n]
+    want = np.stack([codes & 15, codes >> 4], -1).reshape(-1, 64)[:n]
+    assert np.array_equal(R.e2m1_value(both), R.e2m1_value(want))
+
+
+def test_store_of_infinities_nan_and_zeros_stays_finite():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    x = np.zeros((4, 1, 64), np.float32)
+    x[0, 0, :4] = [np.inf, 1.0, -2.0, 3.0]
+    x[0, 0, 16:20] = [-np.inf, 1e30, -1e30, 0]
+    x[1, 0, :4] = [np.nan, 6.0, -3.0, 0.5]
+    x[2, 0, 0] = 1e-30
+    k = to_dev(R.bf16(x))
+    cache = api.KV4Cache.empty(1, 1, 16, 64)
+    slots = torch.arange(4, device="cuda:0")
+    api.kv4_store(k, k, slots, cache)
+    lk, _ = api.kv4_load(slots, cache)
+    got = to_f64(lk)
+    assert np.all(np.isfinite(got))
+    assert got[0, 0, 0] == 2688 and list(got[0, 0, 16:20]) == [-2688, 2688, -2688, 0]
+    assert list(got[1, 0, :4]) == [6, 6, -3, 0.5]  # NaN: code 6 under the scale of the others
+    assert np.all(got[2:] == 0)
+
+
+def test_load_of_every_byte():
+    """All codes under all scale bytes, the sign bit of a scale and 0x7f included; a gain
+    that is no power of two is rounded once."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    cache = api.KV4Cache.empty(16, 1, 16, 64, 0.3, 1.0)
+    cache.k_codes.copy_(torch.arange(32, device="cuda:0").to(torch.uint8).mul_(8).add_(3).expand(16, 1, 16, 32))
+    cache.v_codes.copy_(torch.arange(8, device="cuda:0").repeat(4).to(torch.uint8).mul_(16).add_(9).expand(16, 1, 16, 32))
+    every = torch.arange(256, device="cuda:0").to(torch.uint8).view(16, 1, 16, 1).expand(16, 1, 16, 4)
+    cache.k_scales.copy_(every)
+    cache.v_scales.copy_(every)
+    lk, lv = api.kv4_load(torch.arange(256, device="cuda:0"), cache)
+    a = _cache_arrays(cache)
+    assert np.array_equal(to_f64(lv), R.decode(a[2], a[3], 1.0).reshape(256, 1, 64))
+    want = R.decode(a[0], a[1], float(np.float32(0.3))).reshape(256, 1, 64)
+    # fp32 product (2^-24) and bf16 (2^-8), relative.
+    assert np.all(np.abs(to_f64(lk) - want) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(want))
+
+
+# ------------------------------------------------------------------ attention
+
+def _problem(d, page, heads, kv, lengths, queries, seed, spread=1.0, spare=3, pad=0, gains=(2.0 ** -6, 2.0 ** -5)):
+    """A pool with the requests' pages scattered, everything else filled with 0xff."""
+    rng = np.random.default_rng(seed)
+    need = [-(-max(n, 0) // page) for n in lengths]
+    pool = sum(need) + spare
+    ids = rng.permutation(pool)
+    width = max(need + [1]) + 1
+    table = np.full((len(lengths), width), -1)
+    at = 0
+    arrays = [np.full((pool, kv, page, d // 2), 0xFF, np.uint8), np.full((pool, kv, page, d // 16), 0xFF, np.uint8),
+              np.full((pool, kv, page, d // 2), 0xFF, np.uint8), np.full((pool, kv, page, d // 16), 0xFF, np.uint8)]
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        at += n
+        for i, gain in enumerate(gains):
+            x = rng.standard_normal((n, kv, page, d)) * (spread if i == 0 else 1.0)
+            codes, scales = R.encode(x, gain)
+            last = max(lengths[b], 0) - (n - 1) * page
+            if n:  # slots behind the last token keep their 0xff
+                codes[-1, :, last:], scales[-1, :, last:] = 0xFF, 0xFF
+            arrays[2 * i][table[b, :n]], arrays[2 * i + 1][table[b, :n]] = codes, scales
+    cu = np.concatenate([[0], np.cumsum(queries)])
+    q = R.bf16(rng.standard_normal((int(cu[-1]) + pad, heads, d)))
+    return arrays, table, cu, q, gains
+
+
+def _cache_of(arrays, gains):
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    return api.KV4Cache(*(torch.from_numpy(a).cuda() for a in arrays), *gains)
+
+
+def _reference(arrays, gains, table, cu, q, lengths, max_q, scale):
+    # Each byte pattern stands for a finite value, but slots behind a request's last
+    # token are no keys, so the restatement never reads their 0xff.
+    k = R.decode(arrays[0], arrays[1], gains[0])
+    v = R.decode(arrays[2], arrays[3], gains[1])
+    return R.attend(to_f64(to_dev(q, "cpu")), (k, v), table, lengths, cu, max_q, scale)
+
+
+def _attend(problem, lengths, max_q, scale=None, **kw):
+    from tiled_attention_tmem_gb300 import api
+    arrays, table, cu, q, gains = problem
+    d = q.shape[-1]
+    cache = _cache_of(arrays, gains)
+    o, lse = api.kv4_attention(to_dev(q), cache, _i32(table), _i32(lengths), _i32(cu), max_q, scale, **kw)
+    api.check_device_error()
+    ref = _reference(arrays, gains, table, cu, q, lengths, max_q, 1 / math.sqrt(d) if scale is None else scale)
+    own = int(cu[-1])
+    R.check(to_f64(o)[:own], to_f64(lse)[:own], tuple(x[:own] for x in ref), d)
+    return o, lse
+
+
+LENGTHS = [0, 1, 15, 16, 17, 63, 64, 65, 200, 333]
+
+
+@pytest.mark.parametrize("d", DIMS)
+@pytest.mark.parametrize("page,kv,group", [(16, 2, 1), (32, 1, 4), (64, 3, 8), (128, 1, 7)])
+def test_attention_one_query(d, page, kv, group):
+    problem = _problem(d, page, kv * group, kv, LENGTHS, [1] * len(LENGTHS), seed=d + page)
+    _attend(problem, LENGTHS, 1)
+
+
+@pytest.mark.parametrize("d", DIMS)
+@pytest.mark.parametrize("page,kv,group,queries", [
+    (16, 1, 1, [3, 0, 5, 1, 2, 8, 1, 4]), (64, 2, 4, [2, 6, 0, 3, 6, 6, 1, 5]), (32, 1, 16, [1, 2, 3, 3, 0, 2, 3, 1]),
+    (128, 1, 5, [9, 1, 0, 7, 3, 9, 2, 4])])
+def test_attention_several_queries(d, page, kv, group, queries):
+    """Queries a request from none to more than its tokens (rows that see nothing)."""
+    lengths = [2, 0, 5, 64, 65, 130, 1, 257]
+    problem = _problem(d, page, kv * group, kv, lengths, queries, seed=7 * d + page, pad=3)
+    _attend(problem, lengths, max(queries))
+
+
+def test_attention_without_offsets_is_one_query_a_request():
+    from tiled_attention_tmem_gb300 import api
+    lengths = [5, 0, 77]
+    arrays, table, cu, q, gains = _problem(64, 16, 4, 2, lengths, [1, 1, 1], seed=3)
+    o, lse = api.kv4_attention(to_dev(q), _cache_of(arrays, gains), _i32(table), _i32(lengths))
+    ref = _reference(arrays, gains, table, cu, q, lengths, 1, 1 / 8)
+    R.check(to_f64(o), to_f64(lse), ref, 64)
+
+
+@pytest.mark.parametrize("d,page,kv,group,lengths", [
+    (128, 64, 1, 2, [30000]), (64, 16, 2, 4, [9000, 1, 4097]), (256, 32, 1, 1, [7001, 0, 50]), (384, 128, 1, 3, [5000]),
+    (96, 64, 2, 1, [6000, 6000])], ids=str)
+def test_attention_cut_over_many_warps(d, page, kv, group, lengths):
+    """Few requests, many units: every triple is cut and its parts are merged."""
+    problem = _problem(d, page, kv * group, kv, lengths, [1] * len(lengths), seed=d)
+    _attend(problem, lengths, 1)
+
+
+def test_attention_many_requests_share_warps():
+    rng = np.random.default_rng(5)
+    lengths = [int(n) for n in rng.integers(0, 90, 700)]
+    queries = [int(n) for n in rng.integers(0, 3, 700)]
+    problem = _problem(64, 16, 4, 2, lengths, queries, seed=6)
+    _attend(problem, lengths, 2)
+
+
+def test_attention_sharp_and_far_scores():
+    """Keys far apart: running maxima that grow by more and by less than the threshold."""
+    for spread, scale in ((8.0, 1.0), (0.001, None), (30.0, 0.5)):
+        problem = _problem(128, 64, 8, 2, [1000, 129], [1, 2], seed=11, spread=spread, gains=(2.0 ** -3, 2.0 ** -5))
+        _attend(problem, [1000, 129], 2, scale)
+
+
+@pytest.mark.parametrize("power", [-100, -20, 12, 30])
+def test_attention_queries_of_any_magnitude(power):
+    arrays, table, cu, q, gains = _problem(64, 16, 4, 1, [50, 9], [1, 1], seed=13)
+    q = R.bf16(np.ldexp(to_f64(to_dev(q, "cpu")), power))
+    _attend((arrays, table, cu, q, gains), [50, 9], 1, scale=2.0 ** -power / 8)
+
+
+def test_attention_skips_bad_pages_and_keeps_foreign_rows():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    lengths = [200, 90, 64]
+    arrays, table, cu, q, gains = _problem(64, 16, 4, 2, lengths, [1, 1, 1], seed=17, pad=5)
+    table[0, 3], table[0, 12], table[1, 0] = -1, 10 ** 6, len(arrays[0])
+    table[2, :] = -3  # no page at all: the row is empty
+    o = torch.full((8, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    lse = torch.full((8, 4), 7.0, device="cuda:0")
+    _attend((arrays, table, cu, q, gains), lengths, 1, out=o, lse=lse)
+    assert torch.all(o[3:] == 7) and torch.all(lse[3:] == 7)
+    assert torch.all(o[2] == 0) and torch.all(torch.isinf(lse[2]))
+
+
+def test_attention_lengths_past_the_table_and_offsets_outside_q():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    lengths = [40, 20]
+    arrays, table, cu, q, gains = _problem(64, 16, 2, 1, lengths, [1, 1], seed=19)
+    table = np.ascontiguousarray(table[:, :2])  # 32 tokens fit
+    _attend((arrays, table, cu, q, gains), lengths, 1)
+    # Offsets that leave q, run backwards or ask for more than max_q.
+    cache = _cache_of(arrays, gains)
+    for bad in ([0, 5, 9], [-3, 1, 2], [2, 0, 1], [1 << 30, (1 << 30) + 1, 3]):
+        o = torch.full((2, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda:0")
+        api.kv4_attention(to_dev(q), cache, _i32(table), _i32(lengths), _i32(bad), 4, out=o)
+        api.check_device_error()
+        assert torch.all(torch.isfinite(o))
+
+
+def test_attention_of_nan_and_infinite_queries_stays_in_its_row():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    arrays, table, cu, q, gains = _problem(128, 16, 4, 1, [70, 33], [2, 1], seed=23)
+    x = to_dev(q)
+    clean, _ = api.kv4_attention(x, _cache_of(arrays, gains), _i32(table), _i32([70, 33]), _i32(cu), 2)
+    x[0, 1, 5] = float("nan")
+    x[2, 3, 0] = float("inf")
+    got, lse = api.kv4_attention(x, _cache_of(arrays, gains), _i32(table), _i32([70, 33]), _i32(cu), 2)
+    bad = torch.zeros((3, 4), dtype=torch.bool, device="cuda:0")
+    bad[0, 1] = bad[2, 3] = True
+    assert torch.all(torch.isnan(got[0, 1])) and torch.isnan(lse[0, 1]) and torch.all(torch.isnan(got[2, 3]))
+    assert torch.equal(got[~bad], clean[~bad])
+
+
+def test_attention_strided_query_and_output_match_dense_ones():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    lengths, queries = [100, 7, 300], [2, 1, 3]
+    arrays, table, cu, q, gains = _problem(128, 32, 8, 2, lengths, queries, seed=29)
+    cache = _cache_of(arrays, gains)
+    x = to_dev(q)
+    dense, lse = api.kv4_attention(x, cache, _i32(table), _i32(lengths), _i32(cu), 3)
+    wide = torch.randn((6, 8 * 128 + 512), device="cuda:0").to(torch.bfloat16)
+    wide[:, 256:256 + 1024].copy_(x.view(6, -1))
+    heads_first = torch.empty((8, 6, 128), dtype=torch.bfloat16, device="cuda:0")
+    got, lse2 = api.kv4_attention(wide[:, 256:256 + 1024].unflatten(1, (8, 128)), cache, _i32(table), _i32(lengths),
+                                  _i32(cu), 3, out=heads_first.transpose(0, 1))
+    assert torch.equal(got, dense) and torch.equal(lse, lse2)
+    with pytest.raises(RuntimeError, match="aligned"):
+        api.kv4_attention(wide[:, 4:4 + 1024].unflatten(1, (8, 128)), cache, _i32(table), _i32(lengths), _i32(cu), 3)
+    with pytest.raises(ValueError, match="dense"):
+        api.kv4_attention(x.transpose(1, 2).contiguous().transpose(1, 2), cache, _i32(table), _i32(lengths), _i32(cu), 3)
+    with pytest.raises(ValueError, match="channels"):
+        api.kv4_attention(x[:, :7], cache, _i32(table), _i32(lengths), _i32(cu), 3)
+
+
+def test_attention_is_reproducible_and_clean_of_its_workspace():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    lengths = [5000, 3, 0, 900]
+    arrays, table, cu, q, gains = _problem(128, 64, 8, 2, lengths, [1, 1, 1, 1], seed=31)
+    cache = _cache_of(arrays, gains)
+    args = (to_dev(q), cache, _i32(table), _i32(lengths))
+    first = api.kv4_attention(*args)
+    for fill in (0, 0xFF, 0x7F):
+        ws = torch.full((api.kv4_attention_workspace_bytes(4, 8, 2, 128),), fill, dtype=torch.uint8, device="cuda:0")
+        again = api.kv4_attention(*args, workspace=ws)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    with pytest.raises(ValueError, match="workspace holds"):
+        api.kv4_attention(*args, workspace=ws[:-1])
+
+
+def test_cache_beyond_four_gigabytes():
+    """Pages whose bytes lie past 2^32, written, read back and attended to."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    page, kv, d = 128, 2, 128
+    pool = (1 << 32) // (page * kv * d // 2) + 40
+    cache = api.KV4Cache(*(torch.empty((pool, kv, page, n), dtype=torch.uint8, device="cuda:0")
+                           for n in (d // 2, d // 16, d // 2, d // 16)), 2.0 ** -6, 2.0 ** -6)
+    rng = np.random.default_rng(37)
+    n = 300
+    ids = np.array([pool - 1, pool - 30, 2])
+    slots = (ids[:, None] * page + np.arange(page)).reshape(-1)[:n]
+    x = R.bf16(rng.standard_normal((2, n, kv, d)))
+    api.kv4_store(to_dev(x[0]), to_dev(x[1]), _dev(slots, torch.int64), cache)
+    lk, lv = api.kv4_load(_dev(slots, torch.int64), cache)
+    k, v = (R.decode(*R.encode(to_f64(to_dev(y)), 2.0 ** -6), 2.0 ** -6) for y in x)
+    assert np.array_equal(to_f64(lk), k) and np.array_equal(to_f64(lv), v)
+    q = R.bf16(rng.standard_normal((1, 4, d)))
+    o, lse = api.kv4_attention(to_dev(q), cache, _i32([ids]), _i32([n]))
+    full = [np.zeros((3, kv, page, d)) for _ in range(2)]
+    for f, y in zip(full, (k, v)):
+        f.transpose(0, 2, 1, 3).reshape(-1, kv, d)[:n] = 0  # (a copy: fill below)
+        g = f.transpose(0, 2, 1, 3).reshape(-1, kv, d).copy()
+        g[:n] = y
+        f[:] = g.reshape(3, page, kv, d).transpose(0, 2, 1, 3)
+    ref = R.attend(to_f64(to_dev(q)), full, np.array([[0, 1, 2]]), [n], [0, 1], 1, 1 / math.sqrt(d))
+    R.check(to_f64(o), to_f64(lse), ref, d)
+
+
+# ------------------------------------------------------------------ together
+
+def _serve(api, torch, page, kv, group, d, prompts, steps, seed, stream=None):
+    """Prompts admitted, stored and attended to, then decoding steps: the operators as a
+    serving loop calls them.  Yields what each step attended with."""
+    rng = np.random.default_rng(seed)
+    B, H = len(prompts), kv * group
+    pool = sum(-(-(n + steps) // page) for n in prompts) + 2
+    width = -(-(max(prompts) + steps) // page)
+    cache = api.KV4Cache.empty(pool, kv, page, d, 2.0 ** -6, 2.0 ** -6)
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda:0")
+    lengths = torch.zeros(B, dtype=torch.int32, device="cuda:0")
+    free = _i32(rng.permutation(pool))
+    count = _i32([pool])
+    keys = [np.zeros((0, kv, d)) for _ in prompts]
+    vals = [np.zeros((0, kv, d)) for _ in prompts]
+    for step in range(steps + 1):
+        new = prompts if step == 0 else [1] * B
+        T = sum(new) + 2
+        rows = R.bf16(rng.standard_normal((T, (H + 2 * kv) * d)))
+        x = to_dev(rows)
+        q, k, v = (t.unflatten(1, (-1, d)) for t in (x[:, :H * d], x[:, H * d:(H + kv) * d], x[:, (H + kv) * d:]))
+        slots, cu, lengths, count = api.page_grow(lengths, _i32(new), table, free, count, page, T, stream=stream)
+        api.kv4_store(k, v, slots, cache, stream=stream)
+        o, lse = api.kv4_attention(q, cache, table, lengths, cu, max(new), stream=stream)
+        kf, vf = (R.decode(*R.encode(to_f64(t.contiguous()), 2.0 ** -6), 2.0 ** -6) for t in (k, v))
+        at = np.concatenate([[0], np.cumsum(new)])
+        for b in range(B):
+            keys[b] = np.concatenate([keys[b], kf[at[b]:at[b + 1]]])
+            vals[b] = np.concatenate([vals[b], vf[at[b]:at[b + 1]]])
+        yield to_f64(q.contiguous()), o, lse, new, at, keys, vals, (cache, table, lengths)
+
+
+@pytest.mark.parametrize("page,kv,group,d", [(16, 2, 4, 64), (64, 1, 8, 128)])
+def test_serving_loop(page, kv, group, d):
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    prompts = [5, 70, 1, 33]
+    for q, o, lse, new, at, keys, vals, (cache, table, lengths) in _serve(api, torch, page, kv, group, d, prompts, 20, 41):
+        for b in range(len(prompts)):
+            n = len(keys[b])
+            kk, vv = (x[b].transpose(1, 0, 2)[None] for x in (keys, vals))  # one page of n tokens
+            ref = R.attend(q[at[b]:at[b + 1]], (kk, vv), np.array([[0]]), [n], [0, new[b]], new[b], 1 / math.sqrt(d))
+            R.check(to_f64(o)[at[b]:at[b + 1]], to_f64(lse)[at[b]:at[b + 1]], ref, d)
+    # What the cache holds comes back through its slots.
+    total = int(lengths.sum())
+    slots, cu = api.page_slots(torch.zeros_like(lengths), lengths, table, page, total)
+    lk, lv = api.kv4_load(slots, cache)
+    assert np.array_equal(to_f64(lk), np.concatenate(keys)) and np.array_equal(to_f64(lv), np.concatenate(vals))
+    api.check_device_error()
+
+
+def test_serving_on_another_stream_and_two_at_once():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    want = [(o.clone(), l.clone()) for _, o, l, *_ in _serve(api, torch, 16, 2, 4, 64, [5, 70], 4, 43)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    runs = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            runs.append(_serve(api, torch, 16, 2, 4, 64, [5, 70], 4, 43))
+    for i, ref in enumerate(want):
+        for s, r in zip(streams, runs):
+            with torch.cuda.stream(s):
+                out = next(r)
+            s.synchronize()
+            assert torch.equal(out[1][:-2], ref[0][:-2]) and torch.equal(out[2][:-2], ref[1][:-2])
+    # An explicit stream handle, with the current stream another one.
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    args = None
+    for _, o, l, _, _, _, _, (cache, table, lengths) in _serve(api, torch, 16, 2, 4, 64, [5, 70], 4, 43):
+        args = (cache, table, lengths)
+    q = to_dev(R.bf16(np.random.default_rng(1).standard_normal((2, 8, 64))))
+    torch.cuda.synchronize()
+    ref = api.kv4_attention(q, *args)
+    got = [api.kv4_attention(q, *args, stream=s.cuda_stream) for _ in range(5)]
+    s.synchronize()
+    for o, l in got:
+        assert torch.equal(o, ref[0]) and torch.equal(l, ref[1])
+
+
+def test_graph_capture_of_a_decoding_step():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    page, kv, group, d, B = 16, 2, 4, 128, 3
+    H, pool, width, T = kv * group, 40, 12, B
+    rng = np.random.default_rng(47)
+    cache = api.KV4Cache.empty(pool, kv, page, d, 2.0 ** -6, 2.0 ** -6)
+    free, new = _i32(rng.permutation(pool)), _i32([1] * B)
+    x = torch.zeros((T, (H + 2 * kv) * d), dtype=torch.bfloat16, device="cuda:0")
+    state = dict(table=torch.full((B, width), -1, dtype=torch.int32, device="cuda:0"),
+                 lengths=torch.zeros(B, dtype=torch.int32, device="cuda:0"), count=_i32([pool]))
+
+    def step():
+        q, k, v = (t.unflatten(1, (-1, d)) for t in (x[:, :H * d], x[:, H * d:(H + kv) * d], x[:, (H + kv) * d:]))
+        slots, cu, held, count = api.page_grow(state["lengths"], new, state["table"], free, state["count"], page, T)
+        api.kv4_store(k, v, slots, cache)
+        out = api.kv4_attention(q, cache, state["table"], held)
+        state["lengths"].copy_(held)
+        state["count"].copy_(count)
+        return out
+
+    def reset():
+        state["table"].fill_(-1)
+        state["lengths"].zero_()
+        state["count"].fill_(pool)
+        for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
+            t.zero_()
+
+    rows = [to_dev(R.bf16(rng.standard_normal((T, (H + 2 * kv) * d)))) for _ in range(50)]
+    want = []
+    for r in rows:
+        x.copy_(r)
+        want.append(tuple(t.clone() for t in step()))
+    reset()
+    torch.cuda.synchronize()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=s):
+        out = step()
+    reset()
+    for r, ref in zip(rows, want):
+        x.copy_(r)
+        graph.replay()
+        assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+    api.check_device_error()
+
+
+def test_a_set_error_word_stops_the_attention():
+    """A kernel that gave up a wait leaves the error word set; attention then writes nothing."""
+    import torch
+    from tiled_attention_tmem_gb300 import api, binding as b
+    arrays, table, cu, q, gains = _problem(64, 16, 4, 2, [300], [1], seed=53)
+    o = torch.full((1, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    assert b.lib().fa_watchdog_selftest(torch.cuda.current_stream().cuda_stream) == b.FA_OK
+    api.kv4_attention(to_dev(q), _cache_of(arrays, gains), _i32(table), _i32([300]), out=o)
+    st, _ = b.fa_get_device_error(torch.cuda.current_stream().cuda_stream)
+    assert st == b.FA_ERR_DEVICE_TIMEOUT and torch.all(o == 7)
+    api.kv4_attention(to_dev(q), _cache_of(arrays, gains), _i32(table), _i32([300]), out=o)
+    api.check_device_error()
+    assert not torch.any(o == 7)

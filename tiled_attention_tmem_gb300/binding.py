@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in ``include/fa.h`` (argument marshalling only).
+"""ctypes binding of the C ABI in ``include/fa.h`` and ``include/fa_paged.h`` (argument
+marshalling only).
 
 The functions here carry the C names and take raw device pointers (ints),
 sizes and a CUDA stream handle; every step of the computation runs in the
@@ -33,6 +34,7 @@ _VP = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "fa_fwd": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I, _VP]),
     "fa_fwd_splitkv_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
@@ -61,6 +63,14 @@ SIGNATURES = {
     "fa_fwd_launches": (_I, [_I, _I, _I, _I]),
     "fa_fwd_splitkv_launches": (_I, [_I, _I, _I, _I, _I]),
     "fa_bwd_launches": (_I, [_I, _I, _I, _I, _I, _I]),
+    # include/fa_paged.h
+    "fa_page_grow": (_I, [_VP, _VP, _VP, _I, _I, _I, _VP, _I, _VP, _I, _VP, _VP, _VP, _VP, _VP]),
+    "fa_page_slots": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP]),
+    "fa_kv4_store": (_I, [_VP, _VP, _LL, _LL, _LL, _LL, _VP, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _F, _F, _VP]),
+    "fa_kv4_load": (_I, [_VP, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _F, _F, _VP, _VP, _VP]),
+    "fa_kv4_attn": (_I, [_VP, _LL, _LL, _I, _VP, _I, _VP, _VP, _VP, _VP, _I, _I, _VP, _I, _VP, _I, _I, _I, _I,
+                         _F, _F, _F, _VP, _LL, _LL, _VP, _VP, _SZ, _VP]),
+    "fa_kv4_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
 }
 
 _lib = None
@@ -197,7 +207,41 @@ def fa_bwd_launches(B, H, N, d, variant, causal=0) -> int:
     return lib().fa_bwd_launches(B, H, N, d, variant, int(causal))
 
 
-FA_KERNEL_KINDS = 9
+def fa_page_grow(lengths, new_tokens, table, B, width, page, free_pages, free_size, free_count, T, slots, cu,
+                 lengths_out, count_out, stream) -> int:
+    return lib().fa_page_grow(lengths, new_tokens, table, B, width, page, free_pages, free_size, free_count, T,
+                              slots, cu, lengths_out, count_out, stream)
+
+
+def fa_page_slots(first, count, table, B, width, page, T, slots, cu, stream) -> int:
+    return lib().fa_page_slots(first, count, table, B, width, page, T, slots, cu, stream)
+
+
+def fa_kv4_store(k, v, k_token, k_head, v_token, v_head, slots, T, Hkv, d, k_codes, k_scales, v_codes, v_scales,
+                 pages, page, k_gain, v_gain, stream) -> int:
+    return lib().fa_kv4_store(k, v, k_token, k_head, v_token, v_head, slots, T, Hkv, d, k_codes, k_scales, v_codes,
+                              v_scales, pages, page, k_gain, v_gain, stream)
+
+
+def fa_kv4_load(slots, T, Hkv, d, k_codes, k_scales, v_codes, v_scales, pages, page, k_gain, v_gain, k, v,
+                stream) -> int:
+    return lib().fa_kv4_load(slots, T, Hkv, d, k_codes, k_scales, v_codes, v_scales, pages, page, k_gain, v_gain,
+                             k, v, stream)
+
+
+def fa_kv4_attn(q, q_token, q_head, T, cu, max_q, k_codes, k_scales, v_codes, v_scales, pages, page, table, width,
+                lengths, B, H, Hkv, d, scale, k_gain, v_gain, o, o_token, o_head, lse, workspace, workspace_bytes,
+                stream) -> int:
+    return lib().fa_kv4_attn(q, q_token, q_head, T, cu, max_q, k_codes, k_scales, v_codes, v_scales, pages, page,
+                             table, width, lengths, B, H, Hkv, d, scale, k_gain, v_gain, o, o_token, o_head, lse,
+                             workspace, workspace_bytes, stream)
+
+
+def fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q) -> int:
+    return lib().fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q)
+
+
+FA_KERNEL_KINDS = 14
 
 
 class FaProfile(ctypes.Structure):

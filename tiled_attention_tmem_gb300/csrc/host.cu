@@ -371,6 +371,11 @@ const char* fa_kernel_name(int kind) {
     case FA_KERNEL_FWD_MERGE: return "fwd_merge";
     case FA_KERNEL_BWD_KVSUM: return "bwd_kvsum";
     case FA_KERNEL_BWD_QSUM: return "bwd_qsum";
+    case FA_KERNEL_PAGE: return "page";
+    case FA_KERNEL_KV4_STORE: return "kv4_store";
+    case FA_KERNEL_KV4_LOAD: return "kv4_load";
+    case FA_KERNEL_KV4_ATTN: return "kv4_attn";
+    case FA_KERNEL_KV4_MERGE: return "kv4_merge";
   }
   return "unknown";
 }

@@ -1,0 +1,401 @@
+// Page tables and slots from request lengths, and the 4-bit cache's store and load.
+#include <algorithm>
+#include <cmath>
+#include <cuda_bf16.h>
+
+#include "fa_paged.h"
+#include "host.h"
+#include "kv4.cuh"
+
+namespace fa {
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+// ------------------------------------------------------------------ page tables
+
+struct PageParams {
+  const int* held;   // tokens held (grow) or first position (slots only)
+  const int* add;    // tokens to place
+  int* table;
+  const int* free_pages;  // NULL: slots only
+  const int* free_count;
+  long long* slots;
+  int* cu;
+  int* held_out;
+  int* count_out;
+  int B, width, page_log2, T, free_size;
+  int per_block;  // requests per block (grid.x)
+};
+
+constexpr int kPageThreads = 256;
+
+struct PageRow {
+  int held, add, cu, off, owned, need;
+};
+
+// Exclusive scan of one value a thread over the block; total through `total`.
+__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long s = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, s, d);
+    if (lane >= d) s += y;
+  }
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kPageThreads / 32; ++w) {
+    if (w < warp) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  __syncthreads();
+  return before + s - x;
+}
+
+// Everything follows from two prefix sums over the requests: of the new tokens
+// (cut at T) and of the pages they need.  The sums take a few microseconds of
+// latency, less than a second launch would, so every block computes both over
+// all requests (each thread a run of ceil(B / 256) of them) and then fills in
+// its own `per_block` requests; blockIdx.y cuts the tokens of long prompts.  The page of a
+// new token comes from the old table or from the stack, never from an entry that
+// this launch writes, so blocks do not wait for one another.
+__global__ void __launch_bounds__(kPageThreads) page_kernel(const __grid_constant__ PageParams p) {
+  __shared__ long long warp_sums[kPageThreads / 32];
+  extern __shared__ PageRow rows[];  // per_block
+  grid_dep_wait();
+  const int page = 1 << p.page_log2;
+  const int run = (p.B + kPageThreads - 1) / kPageThreads;
+  const int b0 = min((int)threadIdx.x * run, p.B), b1 = min(b0 + run, p.B);
+  long long sum = 0, total_new, total_need = 0;
+  for (int b = b0; b < b1; ++b) sum += max(p.add[b], 0);
+  const long long new0 = block_scan(sum, warp_sums, total_new);
+  const int my0 = blockIdx.x * p.per_block, my1 = min(my0 + p.per_block, p.B);
+
+  // One request: its tokens after the cut at T, and the pages they need.
+  auto place = [&](int b, long long raw, int& held, int& cu, int& add, int& owned) -> int {
+    held = max(p.held[b], 0);
+    cu = (int)min(raw, (long long)p.T);
+    add = (int)(min(raw + max(p.add[b], 0), (long long)p.T) - cu);
+    owned = (held >> p.page_log2) + ((held & (page - 1)) ? 1 : 0);
+    const long long wanted = min(((long long)held + add + page - 1) >> p.page_log2, (long long)p.width);
+    return p.free_pages ? (int)max(wanted - owned, 0LL) : 0;
+  };
+  long long need_sum = 0, raw = new0;
+  for (int b = b0; b < b1; ++b) {
+    int held, cu, add, owned;
+    need_sum += place(b, raw, held, cu, add, owned);
+    raw += max(p.add[b], 0);
+  }
+  long long off = 0;
+  if (p.free_pages) off = block_scan(need_sum, warp_sums, total_need);
+  raw = new0;
+  for (int b = b0; b < b1; ++b) {
+    int held, cu, add, owned;
+    const int need = place(b, raw, held, cu, add, owned);
+    raw += max(p.add[b], 0);
+    if (b >= my0 && b < my1) rows[b - my0] = PageRow{held, add, cu, (int)min(off, 0x7fffffffLL), owned, need};
+    off += need;
+  }
+  const int count = p.free_pages ? min(max(*p.free_count, 0), p.free_size) : 0;
+  const int total = (int)min(total_new, (long long)p.T);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    p.cu[p.B] = total;
+    if (p.count_out) *p.count_out = (int)max((long long)count - total_need, 0LL);
+  }
+  __syncthreads();
+
+  // A warp takes a request; blockIdx.y takes every gridDim.y-th run of 32 tokens.
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int b = my0 + warp; b < my1; b += kPageThreads / 32) {
+    const PageRow r = rows[b - my0];
+    int* entry = p.table + (size_t)b * p.width;
+    if (blockIdx.y == 0) {
+      if (lane == 0) {
+        p.cu[b] = r.cu;
+        if (p.held_out) {
+          const int given = min(max(count - r.off, 0), r.need);
+          const long long room = min((long long)r.owned + given, (long long)p.width) * page - r.held;
+          p.held_out[b] = r.held + (int)max(min(room, (long long)r.add), 0LL);
+        }
+      }
+      for (int i = lane; i < r.need; i += 32) {
+        const int src = count - 1 - r.off - i;
+        entry[r.owned + i] = src >= 0 ? p.free_pages[src] : -1;
+      }
+    }
+    for (long long i = blockIdx.y * 32 + lane; i < r.add; i += 32 * gridDim.y) {
+      const long long pos = r.held + i;
+      const long long col = pos >> p.page_log2;
+      int id = -1;
+      if (col < p.width) {
+        if (!p.free_pages || col < r.owned) {
+          id = entry[col];
+        } else {
+          const int src = count - 1 - r.off - (int)(col - r.owned);
+          id = src >= 0 ? p.free_pages[src] : -1;
+        }
+      }
+      p.slots[r.cu + i] = id >= 0 ? ((long long)id << p.page_log2) + (pos & (page - 1)) : -1;
+    }
+  }
+  // The rest of `slots`.
+  const long long step = (long long)gridDim.x * gridDim.y * kPageThreads;
+  for (long long t = total + ((long long)blockIdx.y * gridDim.x + blockIdx.x) * kPageThreads + threadIdx.x; t < p.T;
+       t += step)
+    p.slots[t] = -1;
+}
+
+fa_status run_pages(PageParams p, cudaStream_t st) {
+  // Requests per block: eight (one a warp) until the grid covers the SMs twice.
+  // Tokens: another block for every 256 of the mean request, within the same bound.
+  const int cap = 2 * sm_count_cached();
+  p.per_block = std::max(8, (p.B + cap - 1) / cap);
+  const int gx = (p.B + p.per_block - 1) / p.per_block;
+  const int gy = std::max(1, std::min(cap / gx, (int)((long long)p.T / std::max(1, p.B) / 256)));
+  return launch(FA_KERNEL_PAGE, page_kernel, dim3(gx, gy), dim3(kPageThreads), p.per_block * sizeof(PageRow), st, p);
+}
+
+// At most 2^21 requests (a block keeps a row for each of its own in shared memory),
+// and positions of 31 bits.
+bool pages_ok(int B, int width, int page, int T) {
+  return B >= 0 && B <= (1 << 21) && width >= 0 && T >= 0 && page_ok(page) && (long long)width * page <= 0x7fffffffLL;
+}
+
+int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+// ------------------------------------------------------------------ store and load
+
+struct Kv4IoParams {
+  const uint16_t* in[2];  // store: k, v
+  long long token[2], head[2];
+  uint16_t* out[2];  // load: k, v
+  uint8_t* codes[2];
+  uint8_t* scales[2];
+  const long long* slots;
+  float inv_gain[2], gain[2];
+  long long total;  // groups of 16 channels per tensor
+  int T, heads, groups;  // groups: d / 16
+  int page_log2;
+  long long slot_end;
+};
+
+// Group g of the T x heads x groups of a tensor: its token, head and group, and
+// the group's place in the cache (-1: the token has no slot).
+struct Kv4Place {
+  int token, head, group;
+  long long at;
+};
+__device__ __forceinline__ Kv4Place kv4_place(const Kv4IoParams& p, long long g) {
+  Kv4Place r;
+  const unsigned per = (unsigned)p.heads * p.groups;
+  r.token = (int)(g / per);
+  const unsigned rest = (unsigned)(g - (long long)r.token * per);
+  r.head = rest / (unsigned)p.groups;
+  r.group = rest - r.head * p.groups;
+  const long long slot = p.slots[r.token];
+  if (slot < 0 || slot >= p.slot_end) {
+    r.at = -1;
+  } else {
+    const long long pg = slot >> p.page_log2;
+    const long long row = ((pg * p.heads + r.head) << p.page_log2) + (slot & ((1 << p.page_log2) - 1));
+    r.at = row * p.groups + r.group;
+  }
+  return r;
+}
+
+// One thread per group of 16 channels (two 16-byte loads, one 8-byte store and
+// its scale byte); blockIdx.y chooses keys or values.  Reading bounds it: 2 bytes
+// in for 0.5625 out.  y * (1/scale) is rounded to 12 bits before its code: where
+// y has bf16's eight bits (a gain that is a power of two), a ratio that lies on
+// the border of two codes then gets there exactly although 1/scale is rounded,
+// and one that does not is at least 2^-8 of itself away.
+__global__ void __launch_bounds__(256) kv4_store_kernel(const __grid_constant__ Kv4IoParams p) {
+  grid_dep_wait();
+  const long long g = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (g >= p.total) return;
+  const int which = blockIdx.y;
+  const Kv4Place at = kv4_place(p, g);
+  if (at.at < 0) return;
+  const uint4* src = reinterpret_cast<const uint4*>(p.in[which] + at.token * p.token[which] +
+                                                    at.head * p.head[which] + at.group * kKv4Group);
+  const uint4 a = src[0], b = src[1];
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float y[16], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[2 * i] = __uint_as_float(w[i] << 16) * p.inv_gain[which];
+    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * p.inv_gain[which];
+    top = fmaxf(top, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+  }
+  uint16_t sb;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.f), "f"(__fdiv_rn(top, 6.f)));
+  const uint32_t s = sb & 0xffu;
+  // e4m3 to fp32 by way of f16 (2^-8 of the scale; exact).
+  const float sf = __half2float(__ushort_as_half((unsigned short)((s & 0x7f) << 7))) * kKv4ScaleBias;
+  const float inv = sf > 0.f ? __frcp_rn(sf) : 0.f;
+  uint32_t out[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = sf > 0.f ? y[8 * h + 2 * i] * inv : 0.f;
+      const float hi = sf > 0.f ? y[8 * h + 2 * i + 1] * inv : 0.f;
+      // To 12 bits; fminf turns a NaN into 8, which saturates to 6.
+      const float lr = __uint_as_float((__float_as_uint(fminf(lo, 8.f)) + 0x800u) & 0xfffff000u);
+      const float hr = __uint_as_float((__float_as_uint(fminf(hi, 8.f)) + 0x800u) & 0xfffff000u);
+      asm("{\n\t.reg .b8 x;\n\t.reg .b16 h;\n\t"
+          "cvt.rn.satfinite.e2m1x2.f32 x, %1, %2;\n\t"
+          "cvt.u32.u8 %0, x;\n\t}"
+          : "=r"(q[i])
+          : "f"(hr), "f"(lr));
+    }
+    out[h] = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
+  }
+  *reinterpret_cast<uint2*>(p.codes[which] + at.at * 8) = make_uint2(out[0], out[1]);
+  p.scales[which][at.at] = (uint8_t)s;
+}
+
+// The inverse, with the same split; writing bounds it.  f16 products are exact,
+// so the one rounding is the last, to bf16.
+__global__ void __launch_bounds__(256) kv4_load_kernel(const __grid_constant__ Kv4IoParams p) {
+  grid_dep_wait();
+  const long long g = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (g >= p.total) return;
+  const int which = blockIdx.y;
+  const Kv4Place at = kv4_place(p, g);
+  uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (at.at >= 0) {
+    const uint2 c = *reinterpret_cast<const uint2*>(p.codes[which] + at.at * 8);
+    const uint32_t s = kv4_scale_both(p.scales[which][at.at]);
+    uint32_t r[8];
+    kv4_codes(c.x, r);
+    kv4_codes(c.y, r + 4);
+    const float gain = p.gain[which] * kKv4ScaleBias;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t v = h2mul(r[i], s);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+      o[i] = pack_bf16(f.x * gain, f.y * gain);
+    }
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.out[which] + g * kKv4Group);
+  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+fa_status kv4_io_checks(int T, int Hkv, int d, int pages, int page, float k_gain, float v_gain) {
+  if (T < 0 || Hkv < 0 || pages < 0 || !page_ok(page)) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(k_gain) || !(k_gain > 0.f) || !std::isfinite(v_gain) || !(v_gain > 0.f)) return FA_ERR_INVALID_ARG;
+  // The reciprocal is used too.
+  if (!std::isfinite(1.f / k_gain) || !std::isfinite(1.f / v_gain)) return FA_ERR_INVALID_ARG;
+  if (padded_head_dim(d) == 0) return FA_ERR_UNSUPPORTED;
+  if ((long long)Hkv * (d / kKv4Group) > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa_status kv4_io_fill(Kv4IoParams& p, const long long* slots, int T, int Hkv, int d, const void* kc, const void* ks,
+                      const void* vc, const void* vs, int pages, int page, float k_gain, float v_gain, dim3& grid) {
+  p.codes[0] = static_cast<uint8_t*>(const_cast<void*>(kc));
+  p.codes[1] = static_cast<uint8_t*>(const_cast<void*>(vc));
+  p.scales[0] = static_cast<uint8_t*>(const_cast<void*>(ks));
+  p.scales[1] = static_cast<uint8_t*>(const_cast<void*>(vs));
+  p.slots = slots;
+  p.gain[0] = k_gain;
+  p.gain[1] = v_gain;
+  p.inv_gain[0] = 1.f / k_gain;
+  p.inv_gain[1] = 1.f / v_gain;
+  p.T = T;
+  p.heads = Hkv;
+  p.groups = d / kKv4Group;
+  p.total = (long long)T * Hkv * p.groups;
+  p.page_log2 = log2_of(page);
+  p.slot_end = (long long)pages * page;
+  const long long blocks = (p.total + 255) / 256;
+  if (blocks > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  grid = dim3((unsigned)blocks, 2);
+  return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_page_grow(const int* lengths, const int* new_tokens, int* table, int B, int width, int page,
+                       const int* free_pages, int free_size, const int* free_count, int T, long long* slots, int* cu,
+                       int* lengths_out, int* count_out, void* stream) {
+  if (!pages_ok(B, width, page, T) || free_size < 0) return FA_ERR_INVALID_ARG;
+  if (B == 0) return FA_OK;
+  if (!lengths || !new_tokens || !free_pages || !free_count || !cu || !lengths_out || !count_out)
+    return FA_ERR_INVALID_ARG;
+  if ((width > 0 && !table) || (T > 0 && !slots)) return FA_ERR_INVALID_ARG;
+  PageParams p = {lengths, new_tokens, table, free_pages, free_count, slots, cu, lengths_out, count_out,
+                  B, width, log2_of(page), T, free_size, 0};
+  return run_pages(p, (cudaStream_t)stream);
+}
+
+fa_status fa_page_slots(const int* first, const int* count, const int* table, int B, int width, int page, int T,
+                        long long* slots, int* cu, void* stream) {
+  if (!pages_ok(B, width, page, T)) return FA_ERR_INVALID_ARG;
+  if (B == 0) return FA_OK;
+  if (!first || !count || !cu || (width > 0 && !table) || (T > 0 && !slots)) return FA_ERR_INVALID_ARG;
+  PageParams p = {first, count, const_cast<int*>(table), nullptr, nullptr, slots, cu, nullptr, nullptr,
+                  B, width, log2_of(page), T, 0, 0};
+  return run_pages(p, (cudaStream_t)stream);
+}
+
+fa_status fa_kv4_store(const void* k, const void* v, long long k_token, long long k_head, long long v_token,
+                       long long v_head, const long long* slots, int T, int Hkv, int d, void* k_codes,
+                       void* k_scales, void* v_codes, void* v_scales, int pages, int page, float k_gain,
+                       float v_gain, void* stream) {
+  fa_status s = kv4_io_checks(T, Hkv, d, pages, page, k_gain, v_gain);
+  if (s != FA_OK) return s;
+  if (T == 0 || Hkv == 0 || pages == 0) return FA_OK;
+  if (!k || !v || !slots || !k_codes || !k_scales || !v_codes || !v_scales) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) ||
+      !aligned16(v_scales) || (k_token & 7) || (k_head & 7) || (v_token & 7) || (v_head & 7))
+    return FA_ERR_MISALIGNED;
+  Kv4IoParams p = {};
+  dim3 grid;
+  if ((s = kv4_io_fill(p, slots, T, Hkv, d, k_codes, k_scales, v_codes, v_scales, pages, page, k_gain, v_gain,
+                       grid)) != FA_OK)
+    return s;
+  p.in[0] = static_cast<const uint16_t*>(k);
+  p.in[1] = static_cast<const uint16_t*>(v);
+  p.token[0] = k_token;
+  p.token[1] = v_token;
+  p.head[0] = k_head;
+  p.head[1] = v_head;
+  return launch(FA_KERNEL_KV4_STORE, kv4_store_kernel, grid, dim3(256), 0, (cudaStream_t)stream, p);
+}
+
+fa_status fa_kv4_load(const long long* slots, int T, int Hkv, int d, const void* k_codes, const void* k_scales,
+                      const void* v_codes, const void* v_scales, int pages, int page, float k_gain, float v_gain,
+                      void* k, void* v, void* stream) {
+  fa_status s = kv4_io_checks(T, Hkv, d, pages, page, k_gain, v_gain);
+  if (s != FA_OK) return s;
+  if (T == 0 || Hkv == 0) return FA_OK;
+  if (!k || !v || !slots) return FA_ERR_INVALID_ARG;
+  if (pages > 0 && (!k_codes || !k_scales || !v_codes || !v_scales)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) ||
+      !aligned16(v_scales))
+    return FA_ERR_MISALIGNED;
+  Kv4IoParams p = {};
+  dim3 grid;
+  if ((s = kv4_io_fill(p, slots, T, Hkv, d, k_codes, k_scales, v_codes, v_scales, pages, page, k_gain, v_gain,
+                       grid)) != FA_OK)
+    return s;
+  p.out[0] = static_cast<uint16_t*>(k);
+  p.out[1] = static_cast<uint16_t*>(v);
+  return launch(FA_KERNEL_KV4_LOAD, kv4_load_kernel, grid, dim3(256), 0, (cudaStream_t)stream, p);
+}
+
+}  // extern "C"
