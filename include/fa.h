@@ -289,7 +289,7 @@ enum {
   FA_KERNEL_KV4_STORE = 10, /* 4-bit cache: store */
   FA_KERNEL_KV4_LOAD = 11,  /* 4-bit cache: load */
   FA_KERNEL_KV4_ATTN = 12,  /* attention over the 4-bit cache */
-  FA_KERNEL_KV4_MERGE = 13, /* merge of its workers' parts */
+  FA_KERNEL_KV4_MERGE = 13, /* merge of its warps' parts */
   FA_KERNEL_KINDS = 14
 };
 typedef struct {

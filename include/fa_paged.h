@@ -33,6 +33,20 @@
 extern "C" {
 #endif
 
+/* The cache as the calls take it (host memory; read during the call only). */
+typedef struct {
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  int pages; /* pages in the pool */
+  int page;  /* tokens per page: 16, 32, 64 or 128 */
+  int Hkv;
+  int d;
+  float k_gain;
+  float v_gain;
+} fa_kv4_cache;
+
 /*
  * Page tables and slots for the next tokens of B requests.
  *   lengths     int32 [B]         tokens each request holds (negative: 0)
@@ -74,18 +88,15 @@ fa_status fa_page_slots(const int* first, const int* count, const int* table, in
  * slots[t] < 0 or >= pages*page: token t is skipped.  The valid slots must be
  * distinct: a slot given twice ends up with bytes of either token.
  */
-fa_status fa_kv4_store(const void* k, const void* v, long long k_token, long long k_head, long long v_token,
-                       long long v_head, const long long* slots, int T, int Hkv, int d, void* k_codes,
-                       void* k_scales, void* v_codes, void* v_scales, int pages, int page, float k_gain,
-                       float v_gain, void* stream);
+fa_status fa_kv4_store(const fa_kv4_cache* cache, const void* k, const void* v, long long k_token,
+                       long long k_head, long long v_token, long long v_head, const long long* slots, int T,
+                       void* stream);
 
 /*
  * Reads T tokens back as bf16 (dense [T, Hkv, d]), each value rounded once.
  * slots[t] < 0 or >= pages*page gives zeros.
  */
-fa_status fa_kv4_load(const long long* slots, int T, int Hkv, int d, const void* k_codes, const void* k_scales,
-                      const void* v_codes, const void* v_scales, int pages, int page, float k_gain, float v_gain,
-                      void* k, void* v, void* stream);
+fa_status fa_kv4_load(const fa_kv4_cache* cache, const long long* slots, int T, void* k, void* v, void* stream);
 
 /*
  * Attention of the newest tokens of B requests over the cache.
@@ -104,11 +115,10 @@ fa_status fa_kv4_load(const long long* slots, int T, int Hkv, int d, const void*
  * H a multiple of Hkv; scale finite and > 0.  workspace: fa_kv4_attn_workspace_size
  * bytes, 256-byte aligned, not shared with a concurrent call.
  */
-fa_status fa_kv4_attn(const void* q, long long q_token, long long q_head, int T, const int* cu, int max_q,
-                      const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
-                      int pages, int page, const int* table, int width, const int* lengths, int B, int H,
-                      int Hkv, int d, float scale, float k_gain, float v_gain, void* o, long long o_token,
-                      long long o_head, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_token, long long q_head, int T,
+                      const int* cu, int max_q, const int* table, int width, const int* lengths, int B, int H,
+                      float scale, void* o, long long o_token, long long o_head, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace fa_kv4_attn needs on the current device; 0 for invalid shapes. */
 size_t fa_kv4_attn_workspace_size(int B, int H, int Hkv, int d, int max_q);

@@ -43,19 +43,30 @@ def test_page_validation():
         assert grow(**bad) == b.FA_ERR_INVALID_ARG, bad
 
 
+def cache(a):
+    c = b.FaKv4Cache(a["kc"], a["ks"], a["vc"], a["vs"], a["pages"], a["page"], a["H"], a["d"], a["kg"], a["vg"])
+    KEEP.append(c)
+    return c
+
+
+KEEP = []
+
+
 def test_store_and_load_validation():
     ok = dict(k=A, v=A, kt=256, kh=128, vt=256, vh=128, slots=A, T=4, H=2, d=128, kc=A, ks=A, vc=A, vs=A, pages=3,
               page=16, kg=1.0, vg=1.0)
 
+    assert b.fa_kv4_store(None, A, A, 0, 0, 0, 0, A, 1, None) == b.FA_ERR_INVALID_ARG
+    assert b.fa_kv4_load(None, A, 1, A, A, None) == b.FA_ERR_INVALID_ARG
+
     def store(**kw):
         a = {**ok, **kw}
-        return b.fa_kv4_store(a["k"], a["v"], a["kt"], a["kh"], a["vt"], a["vh"], a["slots"], a["T"], a["H"], a["d"],
-                              a["kc"], a["ks"], a["vc"], a["vs"], a["pages"], a["page"], a["kg"], a["vg"], None)
+        return b.fa_kv4_store(cache(a).address, a["k"], a["v"], a["kt"], a["kh"], a["vt"], a["vh"], a["slots"],
+                              a["T"], None)
 
     def load(**kw):
         a = {**ok, **kw}
-        return b.fa_kv4_load(a["slots"], a["T"], a["H"], a["d"], a["kc"], a["ks"], a["vc"], a["vs"], a["pages"],
-                             a["page"], a["kg"], a["vg"], a["k"], a["v"], None)
+        return b.fa_kv4_load(cache(a).address, a["slots"], a["T"], a["k"], a["v"], None)
 
     for call in (store, load):
         for bad in (dict(T=-1), dict(H=-1), dict(pages=-1), dict(page=48), dict(kg=0.0), dict(vg=-1.0),
@@ -72,14 +83,18 @@ def test_store_and_load_validation():
 
 
 def test_attention_validation():
-    ok = dict(q=A, qt=1024, qh=128, T=2, cu=A, max_q=1, kc=A, ks=A, vc=A, vs=A, pages=4, page=16, table=A, width=4,
-              lengths=A, B=2, H=8, Hkv=2, d=128, scale=0.1, kg=1.0, vg=1.0, o=A, ot=1024, oh=128, lse=A, ws=A, wsb=1 << 30)
+    own = dict(kc=A, ks=A, vc=A, vs=A, pages=4, page=16, H=2, d=128, kg=1.0, vg=1.0)
+    ok = dict(q=A, qt=1024, qh=128, T=2, cu=A, max_q=1, table=A, width=4, lengths=A, B=2, heads=8, scale=0.1, o=A,
+              ot=1024, oh=128, lse=A, ws=A, wsb=1 << 30)
 
     def call(**kw):
         a = {**ok, **kw}
-        return b.fa_kv4_attn(*(a[n] for n in ok), None)
+        return b.fa_kv4_attn(cache({**own, **{n: x for n, x in kw.items() if n in own}}).address,
+                             *(a[n] for n in ok), None)
 
-    for bad in (dict(T=-1), dict(B=-1), dict(max_q=-1), dict(H=7), dict(Hkv=0), dict(pages=-1), dict(width=-1),
+    assert b.fa_kv4_attn(None, *ok.values(), None) == b.FA_ERR_INVALID_ARG
+
+    for bad in (dict(T=-1), dict(B=-1), dict(max_q=-1), dict(heads=7), dict(H=0), dict(heads=-8), dict(pages=-1), dict(width=-1),
                 dict(page=8), dict(scale=0.0), dict(scale=float("nan")), dict(kg=0.0), dict(vg=float("inf")),
                 dict(q=0), dict(o=0), dict(lse=0), dict(lengths=0), dict(table=0), dict(kc=0), dict(width=1 << 28),
                 dict(cu=0, T=1)):

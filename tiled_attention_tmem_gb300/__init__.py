@@ -11,7 +11,12 @@ from .binding import (  # noqa: F401
     fa_bwd, fa_bwd_choose, fa_bwd_launches, fa_bwd_workspace_size, fa_fwd,
     fa_fwd_launches, fa_get_device_error, fa_strerror,
 )
-from .api import (  # noqa: F401
-    KV4Cache, attention_backward, attention_forward, check_device_error, kv4_attention,
-    kv4_load, kv4_store, page_grow, page_slots,
-)
+from . import api  # noqa: F401
+from .api import attention_backward, attention_forward, check_device_error  # noqa: F401
+
+
+def __getattr__(name):
+    # KV4Cache, page_grow, page_slots, kv4_store, kv4_load, kv4_attention: loaded on first use.
+    if name in api._SERVING:
+        return getattr(api, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

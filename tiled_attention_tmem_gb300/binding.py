@@ -66,10 +66,9 @@ SIGNATURES = {
     # include/fa_paged.h
     "fa_page_grow": (_I, [_VP, _VP, _VP, _I, _I, _I, _VP, _I, _VP, _I, _VP, _VP, _VP, _VP, _VP]),
     "fa_page_slots": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP]),
-    "fa_kv4_store": (_I, [_VP, _VP, _LL, _LL, _LL, _LL, _VP, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _F, _F, _VP]),
-    "fa_kv4_load": (_I, [_VP, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _F, _F, _VP, _VP, _VP]),
-    "fa_kv4_attn": (_I, [_VP, _LL, _LL, _I, _VP, _I, _VP, _VP, _VP, _VP, _I, _I, _VP, _I, _VP, _I, _I, _I, _I,
-                         _F, _F, _F, _VP, _LL, _LL, _VP, _VP, _SZ, _VP]),
+    "fa_kv4_store": (_I, [_VP, _VP, _VP, _LL, _LL, _LL, _LL, _VP, _I, _VP]),
+    "fa_kv4_load": (_I, [_VP, _VP, _I, _VP, _VP, _VP]),
+    "fa_kv4_attn": (_I, [_VP, _VP, _LL, _LL, _I, _VP, _I, _VP, _I, _VP, _I, _I, _F, _VP, _LL, _LL, _VP, _VP, _SZ, _VP]),
     "fa_kv4_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
 }
 
@@ -217,24 +216,28 @@ def fa_page_slots(first, count, table, B, width, page, T, slots, cu, stream) -> 
     return lib().fa_page_slots(first, count, table, B, width, page, T, slots, cu, stream)
 
 
-def fa_kv4_store(k, v, k_token, k_head, v_token, v_head, slots, T, Hkv, d, k_codes, k_scales, v_codes, v_scales,
-                 pages, page, k_gain, v_gain, stream) -> int:
-    return lib().fa_kv4_store(k, v, k_token, k_head, v_token, v_head, slots, T, Hkv, d, k_codes, k_scales, v_codes,
-                              v_scales, pages, page, k_gain, v_gain, stream)
+class FaKv4Cache(ctypes.Structure):
+    """fa_kv4_cache; ``address`` is what the calls take (the structure must outlive them)."""
+    _fields_ = [("k_codes", _VP), ("k_scales", _VP), ("v_codes", _VP), ("v_scales", _VP), ("pages", _I), ("page", _I),
+                ("Hkv", _I), ("d", _I), ("k_gain", _F), ("v_gain", _F)]
+
+    @property
+    def address(self) -> int:
+        return ctypes.addressof(self)
 
 
-def fa_kv4_load(slots, T, Hkv, d, k_codes, k_scales, v_codes, v_scales, pages, page, k_gain, v_gain, k, v,
-                stream) -> int:
-    return lib().fa_kv4_load(slots, T, Hkv, d, k_codes, k_scales, v_codes, v_scales, pages, page, k_gain, v_gain,
-                             k, v, stream)
+def fa_kv4_store(cache, k, v, k_token, k_head, v_token, v_head, slots, T, stream) -> int:
+    return lib().fa_kv4_store(cache, k, v, k_token, k_head, v_token, v_head, slots, T, stream)
 
 
-def fa_kv4_attn(q, q_token, q_head, T, cu, max_q, k_codes, k_scales, v_codes, v_scales, pages, page, table, width,
-                lengths, B, H, Hkv, d, scale, k_gain, v_gain, o, o_token, o_head, lse, workspace, workspace_bytes,
-                stream) -> int:
-    return lib().fa_kv4_attn(q, q_token, q_head, T, cu, max_q, k_codes, k_scales, v_codes, v_scales, pages, page,
-                             table, width, lengths, B, H, Hkv, d, scale, k_gain, v_gain, o, o_token, o_head, lse,
-                             workspace, workspace_bytes, stream)
+def fa_kv4_load(cache, slots, T, k, v, stream) -> int:
+    return lib().fa_kv4_load(cache, slots, T, k, v, stream)
+
+
+def fa_kv4_attn(cache, q, q_token, q_head, T, cu, max_q, table, width, lengths, B, H, scale, o, o_token, o_head, lse,
+                workspace, workspace_bytes, stream) -> int:
+    return lib().fa_kv4_attn(cache, q, q_token, q_head, T, cu, max_q, table, width, lengths, B, H, scale, o, o_token,
+                             o_head, lse, workspace, workspace_bytes, stream)
 
 
 def fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q) -> int:

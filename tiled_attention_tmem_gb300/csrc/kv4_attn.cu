@@ -4,8 +4,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "fa_paged.h"
-#include "host.h"
+#include "kv4_host.h"
 
 namespace fa {
 namespace {
@@ -23,10 +22,9 @@ int choose_nt(int d, long long rows) {
 }
 
 struct Plan {
-  int nt, row_tiles, workers;
-  size_t off_ml, off_meta, bytes;
+  int nt, row_tiles, triples;
+  size_t off_ml, off_cuts, bytes;
 };
-constexpr int kWarps = 8;
 
 bool make_plan(int B, int H, int Hkv, int d, int max_q, Plan& plan) {
   const long long rows = (long long)max_q * (H / Hkv);
@@ -34,11 +32,12 @@ bool make_plan(int B, int H, int Hkv, int d, int max_q, Plan& plan) {
   const long long tiles = (rows + 8 * plan.nt - 1) / (8 * plan.nt);
   if (tiles * B * Hkv > 0x7fffffffLL / (8 * plan.nt)) return false;
   plan.row_tiles = (int)tiles;
-  plan.workers = sm_count_cached() * kWarps;
-  const size_t slots = (size_t)plan.workers * 2 * 8 * plan.nt;
-  plan.off_ml = round256(slots * d * sizeof(float));
-  plan.off_meta = plan.off_ml + round256(slots * 2 * sizeof(float));
-  plan.bytes = plan.off_meta + round256((size_t)B * Hkv * tiles * sizeof(int2));
+  plan.triples = (int)(tiles * B * Hkv);
+  // Two slots of a tile's rows for every warp.
+  const size_t held = (size_t)sm_count_cached() * kv4_warps(d, plan.nt) * 2 * 8 * plan.nt;
+  plan.off_ml = round256(held * d * sizeof(float));
+  plan.off_cuts = plan.off_ml + round256(held * 2 * sizeof(float));
+  plan.bytes = plan.off_cuts + round256(plan.triples * sizeof(int2));
   return true;
 }
 
@@ -51,19 +50,15 @@ fa_status shape_checks(int B, int H, int Hkv, int d, int max_q) {
 }
 
 template <int D, int NT>
-fa_status run(Kv4AttnParams p, cudaStream_t st) {
+fa_status run(const Kv4AttnParams& p, int triples, cudaStream_t st) {
   using C = Kv4Cfg<D, NT>;
-  static_assert(C::WARPS == kWarps, "workers");
-  static_assert(C::SMEM <= 232448, "shared memory");
-  p.unit = C::UNIT;
-  p.rows = C::ROWS;
-  fa_status s = launch(FA_KERNEL_KV4_ATTN, kv4_attn_kernel<C>, dim3((unsigned)sm_count_cached()), dim3(C::THREADS),
-                       C::SMEM, st, p);
-  if (s != FA_OK) return s;
+  const int sms = sm_count_cached();
+  fa_status s = launch(FA_KERNEL_KV4_ATTN, kv4_attn_kernel<C>, dim3((unsigned)sms), dim3(C::THREADS), C::SMEM, st, p);
   // A request of one unit is never cut.
-  if (((long long)p.width << p.page_log2) <= C::UNIT) return FA_OK;
-  const unsigned blocks = (unsigned)((long long)p.B * p.Hkv * p.row_tiles * C::ROWS);
-  return launch(FA_KERNEL_KV4_MERGE, kv4_merge_kernel<D>, dim3(blocks), dim3(128), 0, st, p);
+  if (s != FA_OK || ((long long)p.width << p.page_log2) <= C::UNIT) return s;
+  // About eight blocks an SM, and no more than one warp for 16 channels of a row.
+  const int split = std::max(1, std::min(8 * sms / triples, C::ROWS * D / 16 / 8));
+  return launch(FA_KERNEL_KV4_MERGE, kv4_merge_kernel<C>, dim3((unsigned)triples, (unsigned)split), dim3(256), 0, st, p);
 }
 
 }  // namespace
@@ -80,28 +75,26 @@ size_t fa_kv4_attn_workspace_size(int B, int H, int Hkv, int d, int max_q) {
   return make_plan(B, H, Hkv, d, max_q, plan) ? plan.bytes : 0;
 }
 
-fa_status fa_kv4_attn(const void* q, long long q_token, long long q_head, int T, const int* cu, int max_q,
-                      const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
-                      int pages, int page, const int* table, int width, const int* lengths, int B, int H,
-                      int Hkv, int d, float scale, float k_gain, float v_gain, void* o, long long o_token,
-                      long long o_head, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-  fa_status s = shape_checks(B, H, Hkv, d, max_q);
+fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_token, long long q_head, int T,
+                      const int* cu, int max_q, const int* table, int width, const int* lengths, int B, int H,
+                      float scale, void* o, long long o_token, long long o_head, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  fa_status s = kv4_cache_checks(cache);
   if (s != FA_OK) return s;
-  if (T < 0 || pages < 0 || width < 0 || (page != 16 && page != 32 && page != 64 && page != 128))
-    return FA_ERR_INVALID_ARG;
-  for (float x : {scale, k_gain, v_gain})
-    if (!std::isfinite(x) || !(x > 0.f)) return FA_ERR_INVALID_ARG;
+  const int Hkv = cache->Hkv, d = cache->d;
+  if ((s = shape_checks(B, H, Hkv, d, max_q)) != FA_OK) return s;
+  if (T < 0 || width < 0 || !std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (!cu && (T < B || max_q < 1)) return FA_ERR_INVALID_ARG;
-  if ((long long)width * page > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if ((long long)width * cache->page > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   if (B == 0 || H == 0 || T == 0 || max_q == 0) return FA_OK;
   if (!q || !o || !lse || !lengths || (width > 0 && !table)) return FA_ERR_INVALID_ARG;
-  if (pages > 0 && (!k_codes || !k_scales || !v_codes || !v_scales)) return FA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(o) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) ||
-      !aligned16(v_scales) || (q_token & 7) || (q_head & 7) || (o_token & 7) || (o_head & 7))
+  if (!aligned16(q) || !aligned16(o) || (q_token & 7) || (q_head & 7) || (o_token & 7) || (o_head & 7))
     return FA_ERR_MISALIGNED;
   if (!cu) max_q = 1;
   Plan plan;
   if (!make_plan(B, H, Hkv, d, max_q, plan)) return FA_ERR_INVALID_ARG;
+  // A (request, kv head)'s units over all its row tiles are counted in 32 bits.
+  if (((long long)width * cache->page / 32 + 1) * plan.row_tiles > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.bytes)
     return FA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
@@ -109,16 +102,17 @@ fa_status fa_kv4_attn(const void* q, long long q_token, long long q_head, int T,
   p.q = static_cast<const uint16_t*>(q);
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
-  p.codes[0] = static_cast<const uint8_t*>(k_codes);
-  p.codes[1] = static_cast<const uint8_t*>(v_codes);
-  p.scales[0] = static_cast<const uint8_t*>(k_scales);
-  p.scales[1] = static_cast<const uint8_t*>(v_scales);
+  p.codes[0] = static_cast<const uint8_t*>(cache->k_codes);
+  p.codes[1] = static_cast<const uint8_t*>(cache->v_codes);
+  p.scales[0] = static_cast<const uint8_t*>(cache->k_scales);
+  p.scales[1] = static_cast<const uint8_t*>(cache->v_scales);
   p.table = table;
   p.lengths = lengths;
   p.cu = cu;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + plan.off_ml);
-  p.meta = reinterpret_cast<int2*>(ws + plan.off_meta);
+  p.cuts = reinterpret_cast<int2*>(ws + plan.off_cuts);
+  p.row_tiles = plan.row_tiles;
   p.err = device_error_word();
   if (!p.err) return record_cuda_error(cudaErrorMemoryAllocation);
   p.q_token = q_token;
@@ -131,25 +125,24 @@ fa_status fa_kv4_attn(const void* q, long long q_token, long long q_head, int T,
   p.G = H / Hkv;
   p.T = T;
   p.width = width;
-  p.pages = pages;
-  p.page_log2 = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+  p.pages = cache->pages;
+  p.page_log2 = page_log2_of(cache->page);
   p.max_q = max_q;
-  p.row_tiles = plan.row_tiles;
-  p.score = scale * kLog2e * k_gain * kKv4ScaleBias;
-  p.v_gain = v_gain * kKv4ScaleBias;
+  p.score = scale * kLog2e * cache->k_gain * kKv4ScaleBias;
+  p.v_gain = cache->v_gain * kKv4ScaleBias;
   cudaStream_t st = (cudaStream_t)stream;
   switch (d * 8 + plan.nt) {
-    case 64 * 8 + 1: return run<64, 1>(p, st);
-    case 64 * 8 + 2: return run<64, 2>(p, st);
-    case 64 * 8 + 4: return run<64, 4>(p, st);
-    case 96 * 8 + 1: return run<96, 1>(p, st);
-    case 96 * 8 + 2: return run<96, 2>(p, st);
-    case 128 * 8 + 1: return run<128, 1>(p, st);
-    case 128 * 8 + 2: return run<128, 2>(p, st);
-    case 192 * 8 + 1: return run<192, 1>(p, st);
-    case 192 * 8 + 2: return run<192, 2>(p, st);
-    case 256 * 8 + 1: return run<256, 1>(p, st);
-    case 384 * 8 + 1: return run<384, 1>(p, st);
+    case 64 * 8 + 1: return run<64, 1>(p, plan.triples, st);
+    case 64 * 8 + 2: return run<64, 2>(p, plan.triples, st);
+    case 64 * 8 + 4: return run<64, 4>(p, plan.triples, st);
+    case 96 * 8 + 1: return run<96, 1>(p, plan.triples, st);
+    case 96 * 8 + 2: return run<96, 2>(p, plan.triples, st);
+    case 128 * 8 + 1: return run<128, 1>(p, plan.triples, st);
+    case 128 * 8 + 2: return run<128, 2>(p, plan.triples, st);
+    case 192 * 8 + 1: return run<192, 1>(p, plan.triples, st);
+    case 192 * 8 + 2: return run<192, 2>(p, plan.triples, st);
+    case 256 * 8 + 1: return run<256, 1>(p, plan.triples, st);
+    case 384 * 8 + 1: return run<384, 1>(p, plan.triples, st);
   }
   return FA_ERR_UNSUPPORTED;
 }

@@ -7,11 +7,12 @@
 // [w*T/W, (w+1)*T/W), whatever requests they belong to, so ragged batches and one
 // long request load the SMs alike, and no warp waits for another.  A triple that
 // lies in one warp's range is finished there; one that is cut leaves a part
-// (unnormalised fp32 O, running maximum m, sum l) per warp for kv4_merge_kernel.
+// (unnormalised fp32 O, running maximum m, sum l) a warp for kv4_merge_kernel.
 //
-// One unit: its K and V codes and scales (UNIT*d*1.125 bytes) come by bulk copies
-// into the warp's own ring of STAGES slots; both products run on mma.m16n8k16 with
-// f16 operands and fp32 accumulators, from registers:
+// One unit: its K and its V (codes and scales, UNIT*d*0.5625 bytes each) come by bulk
+// copies into the warp's own ring of STAGES units, refilled by the warp itself as
+// soon as it is done with a K or a V; both products run on mma.m16n8k16 with f16
+// operands and fp32 accumulators, from registers:
 //   S^T = K Q^T : A = 16 tokens x 16 channels, dequantised in registers (exact in
 //                 f16), B = Q rows (f16; each row scaled by a power of two into
 //                 f16's range, which its score factor takes back)
@@ -45,12 +46,11 @@ struct Kv4AttnParams {
   const int* cu;  // NULL: one query a request
   float* part_o;   // [W][2][8*NT][D]
   float* part_ml;  // [W][2][8*NT][2]
-  int2* meta;      // [B*Hkv*row_tiles]: first warp of a cut triple and its number of parts (0: not cut)
+  int2* cuts;      // [B*Hkv*row_tiles]: a triple's first warp and its parts (0: not cut)
   int* err;
   long long q_token, q_head, o_token, o_head;
   int B, H, Hkv, G, T, width, pages, page_log2, max_q;
   int row_tiles;  // most row tiles of a request
-  int unit, rows;  // tokens of a unit and rows of a tile
   float score;    // scale * log2(e) * k_gain * 2^8
   float v_gain;   // v_gain * 2^8
 };
@@ -61,28 +61,36 @@ struct Kv4AttnParams {
 constexpr float kKv4Lift = 7.f;
 constexpr float kKv4Grow = 8.f;
 
+// Warps per SM and tokens per unit for head dim d and nt tiles of 8 rows.
+constexpr int kv4_warps(int d, int nt) {
+  return d * nt <= 128 || (nt == 1 && d <= 256) ? 12 : 8;
+}
+constexpr int kv4_unit(int d, int nt) { return d <= 128 ? 64 : 32; }
+
 template <int D_, int NT_>
 struct Kv4Cfg {
   static constexpr int D = D_, NT = NT_;
   static constexpr int ROWS = 8 * NT;
-  static constexpr int UNIT = D <= 128 ? 64 : 32;
+  static constexpr int UNIT = kv4_unit(D, NT);
   static constexpr int MT = UNIT / 16;
-  static constexpr int WARPS = 8;
-  static constexpr int CODE_ROW = D / 2, SCALE_ROW = D / 16;  // bytes a token
-  static constexpr int STAGE = 2 * UNIT * (CODE_ROW + SCALE_ROW);
-  static constexpr int FIT = (224 * 1024 - 4096) / (WARPS * STAGE);
-  static constexpr int STAGES = FIT < 4 ? FIT : 4;
-  static constexpr int OFF_KS = UNIT * CODE_ROW, OFF_V = OFF_KS + UNIT * SCALE_ROW, OFF_VS = OFF_V + UNIT * CODE_ROW;
-  static constexpr int OFF_BAR = WARPS * STAGES * STAGE;
-  static constexpr int OFF_PREFIX = OFF_BAR + WARPS * STAGES * 8;
+  static constexpr int WARPS = kv4_warps(D, NT);
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr int OFF_MISC = OFF_PREFIX + (THREADS + 1) * 8;
+  static constexpr int CODE_ROW = D / 2, SCALE_ROW = D / 16;  // bytes a token
+  static constexpr int OFF_SCALE = UNIT * CODE_ROW;
+  static constexpr int PART = UNIT * (CODE_ROW + SCALE_ROW);  // K or V of a unit
+  static constexpr int OTHER = THREADS * 20 + 1024;           // what follows the ring
+  static constexpr int FIT = (232448 - OTHER) / (WARPS * 2 * PART);
+  static constexpr int STAGES = FIT < 4 ? FIT : 4;
+  static constexpr int OFF_BAR = WARPS * STAGES * 2 * PART;       // per stage: K full, V full
+  static constexpr int OFF_PREFIX = OFF_BAR + WARPS * STAGES * 16;
+  static constexpr int OFF_REQ = OFF_PREFIX + (THREADS + 1) * 8;  // tokens, first query, queries
+  static constexpr int OFF_MISC = OFF_REQ + THREADS * 12;
   static constexpr int SMEM = OFF_MISC + 16 + WARPS * 8;
   static constexpr int WK = D / 32;         // words of 8 codes a lane reads of a K row
   static constexpr int WV = (D + 63) / 64;  // words a lane reads of a V row (d = 96: one and a half)
   static constexpr bool HALF = D % 64 != 0;
   static constexpr int CT = D / 16;  // O^T tiles of 16 channels
-  static_assert(STAGES >= 2, "shared memory");
+  static_assert(STAGES >= 2 && SMEM <= 232448, "shared memory");
 };
 
 // A position in the sequence of units.
@@ -92,7 +100,8 @@ struct Kv4Cursor {
   int n, tok0, nq;        // tokens of b, its first query token, its queries
 };
 
-__device__ __forceinline__ void kv4_request(const Kv4AttnParams& p, int b, int unit, int rows, Kv4Cursor& c) {
+// Tokens, first query and queries of request b from the caller's arrays.
+__device__ __forceinline__ void kv4_lookup(const Kv4AttnParams& p, int b, Kv4Cursor& c) {
   c.n = max(p.lengths[b], 0);
   if (p.cu) {
     c.tok0 = p.cu[b];
@@ -103,13 +112,24 @@ __device__ __forceinline__ void kv4_request(const Kv4AttnParams& p, int b, int u
     c.tok0 = b;
     c.nq = 1;
   }
-  c.tiles = (int)(((long long)c.nq * p.G + rows - 1) / rows);
-  // Tokens past the table's width are no keys.
-  const long long held = min((long long)c.n, (long long)p.width << p.page_log2);
-  c.units = c.tiles ? max((int)((held + unit - 1) / unit), 1) : 0;
 }
 
-__device__ __forceinline__ void kv4_advance(const Kv4AttnParams& p, int unit, int rows, Kv4Cursor& c) {
+// Request b, from shared memory where the block keeps all requests (req not NULL).
+template <class C>
+__device__ __forceinline__ void kv4_request(const Kv4AttnParams& p, const int* req, int b, Kv4Cursor& c) {
+  if (req) {
+    c.n = req[3 * b], c.tok0 = req[3 * b + 1], c.nq = req[3 * b + 2];
+  } else {
+    kv4_lookup(p, b, c);
+  }
+  c.tiles = (int)(((long long)c.nq * p.G + C::ROWS - 1) / C::ROWS);
+  // Tokens past the table's width are no keys.
+  const long long held = min((long long)c.n, (long long)p.width << p.page_log2);
+  c.units = c.tiles ? max((int)((held + C::UNIT - 1) / C::UNIT), 1) : 0;
+}
+
+template <class C>
+__device__ __forceinline__ void kv4_advance(const Kv4AttnParams& p, const int* req, Kv4Cursor& c) {
   if (++c.u < c.units) return;
   c.u = 0;
   if (++c.rt < c.tiles) return;
@@ -123,7 +143,7 @@ __device__ __forceinline__ void kv4_advance(const Kv4AttnParams& p, int unit, in
       c.units = c.tiles = 1;
       return;
     }
-    kv4_request(p, c.b, unit, rows, c);
+    kv4_request<C>(p, req, c.b, c);
   } while (c.units == 0);
 }
 
@@ -189,15 +209,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
   const int warp = warp_id(), lane = lane_id();
   const int g = lane >> 2, t = lane & 3;
   long long* prefix = reinterpret_cast<long long*>(smem + C::OFF_PREFIX);  // units before thread i's requests
+  int* kept = reinterpret_cast<int*>(smem + C::OFF_REQ);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
   long long* sums = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);
-  const uint32_t bar0 = smem_u32(smem + C::OFF_BAR) + warp * S * 8;
-  uint8_t* ring = smem + warp * S * C::STAGE;
+  const uint32_t bars = smem_u32(smem + C::OFF_BAR) + warp * S * 16;
+  uint8_t* ring = smem + warp * S * 2 * C::PART;
   const uint32_t ring_addr = smem_u32(ring);
 
   if (threadIdx.x == 0) *abort_flag = 0;
-  if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
+  if (lane < 2 * S) {
+    mbar_init(bars + 8 * lane, 1);
     fence_mbar_init();
   }
   grid_dep_wait();
@@ -205,12 +226,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
 
   // Units before each thread's run of ceil(B / THREADS) requests, and in all.
   const int run = (p.B + C::THREADS - 1) / C::THREADS;
+  const int* req = run == 1 ? kept : nullptr;
   {
     const int b0 = min((int)threadIdx.x * run, p.B), b1 = min(b0 + run, p.B);
     long long sum = 0;
     for (int b = b0; b < b1; ++b) {
       Kv4Cursor c;
-      kv4_request(p, b, UNIT, C::ROWS, c);
+      kv4_request<C>(p, nullptr, b, c);
+      if (run == 1) kept[3 * b] = c.n, kept[3 * b + 1] = c.tok0, kept[3 * b + 2] = c.nq;
       sum += (long long)c.units * c.tiles * p.Hkv;
     }
     long long x = sum;
@@ -233,100 +256,117 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
   if (skip) return;
   const CtaAbort ab{abort_flag, p.err};
   const long long total = prefix[C::THREADS];
-  // Neighbouring ranges go to different SMs, so that few units spread over all.
-  const int workers = (int)min((long long)gridDim.x * C::WARPS, total);
+  // `more` warps take per + 1 units and the others per.  Neighbouring ranges go to
+  // different SMs, so that few units spread over all.
+  const int workers = gridDim.x * C::WARPS;
   const int me = warp * gridDim.x + blockIdx.x;
-  if (me >= workers) return;
-  const long long x0 = total * me / workers, x1 = total * (me + 1) / workers;
-  auto worker_of = [&](long long x) -> int { return (int)(((x + 1) * workers - 1) / total); };
-
-  // Where unit x0 lies.
-  Kv4Cursor cur;
-  {
+  const int per = (int)min(total / workers, 0x7ffffffell);
+  const int more = (int)(total - (long long)per * workers);
+  const long long x0 = (long long)per * me + min(me, more);
+  const int units = per + (me < more ? 1 : 0);
+  auto locate = [&](long long x, Kv4Cursor& c) -> bool {
     int lo = 0, hi = C::THREADS;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= x0) lo = mid;
+      if (prefix[mid] <= x) lo = mid;
       else hi = mid;
     }
-    long long rest = x0 - prefix[lo];
-    cur.b = lo * run;
-    for (;; ++cur.b) {
-      if (cur.b >= p.B) return;
-      kv4_request(p, cur.b, UNIT, C::ROWS, cur);
-      const long long mine = (long long)cur.units * cur.tiles * p.Hkv;
-      if (rest < mine) break;
+    long long rest = x - prefix[lo];
+    for (c.b = lo * run; c.b < p.B; ++c.b) {
+      kv4_request<C>(p, req, c.b, c);
+      const long long mine = (long long)c.units * c.tiles * p.Hkv;
+      if (rest < mine) {
+        const int per_kvh = c.units * c.tiles;  // below 2^31: see the launcher
+        c.kvh = 0;
+        if (rest >= per_kvh) {
+          c.kvh = (int)(rest / per_kvh);
+          rest -= (long long)c.kvh * per_kvh;
+        }
+        c.rt = (int)rest / c.units;
+        c.u = (int)rest - c.rt * c.units;
+        return true;
+      }
       rest -= mine;
     }
-    const long long seg = rest / cur.units;
-    cur.u = (int)(rest - seg * cur.units);
-    cur.kvh = (int)(seg / cur.tiles);
-    cur.rt = (int)(seg - (long long)cur.kvh * cur.tiles);
-  }
+    return false;  // only if the lengths changed meanwhile
+  };
 
-  // ------------------------------------------------------------- producer side
-  // A unit is UNIT / FR fragments of FR = min(page, UNIT) tokens, each inside one
-  // page: lane 4*f + a copies array a (K codes, K scales, V codes, V scales) of
-  // fragment f, so all of a unit's copies are issued at once.
+  Kv4Cursor cur;
+  if (units == 0 || !locate(x0, cur)) return;
+  int left = units, ahead = units;  // still to compute and to copy
+
+  // ------------------------------------------------------------------- copies
+  // A K or V is UNIT / FR fragments of FR = min(page, UNIT) tokens, each inside one
+  // page: lane 2f copies fragment f's codes, lane 2f + 1 its scales.  V's source lies
+  // where K's does in its own arrays.  A unit's page ids are read a unit ahead.
   const int fr_log2 = min(p.page_log2, UNIT == 64 ? 6 : 5);
-  const int frags = UNIT >> fr_log2;
-  Kv4Cursor pre = cur;  // the next unit to copy; its page id is read one unit ahead
-  long long pre_x = x0;
-  const int frag = lane >> 2, array = lane & 3;
-  auto page_of = [&](const Kv4Cursor& c) -> int {
-    const long long tok = (long long)c.u * UNIT + ((long long)frag << fr_log2);
-    if (frag >= frags || tok >= c.n) return -1;
-    const long long col = tok >> p.page_log2;
-    if (col >= p.width) return -1;
-    const int id = p.table[(size_t)c.b * p.width + col];
+  const uint32_t all_bits = (1u << (UNIT >> fr_log2)) - 1u;
+  const int frag = lane >> 1;
+  const int row_bytes = (lane & 1) ? C::SCALE_ROW : C::CODE_ROW;
+  const uint32_t copy_bytes = (uint32_t)row_bytes << fr_log2;
+  const uint32_t copy_dst = ring_addr + ((lane & 1) ? C::OFF_SCALE : 0) + frag * copy_bytes;
+  Kv4Cursor pre = cur;
+  auto page_of = [&]() -> int {
+    const long long tok = (long long)pre.u * UNIT + ((long long)frag << fr_log2);
+    const int col = (int)(tok >> p.page_log2);
+    if (frag >= (UNIT >> fr_log2) || tok >= pre.n || col >= p.width) return -1;
+    const int id = p.table[(size_t)pre.b * p.width + col];
     return (unsigned)id < (unsigned)p.pages ? id : -1;
   };
-  int next_page = page_of(pre);
-  uint32_t valid_bits = 0;  // four bits a stage: which fragments have a page
-  auto produce = [&](int s) {
-    if (pre_x >= x1) return;
-    const int id = next_page;
-    const uint32_t have = __ballot_sync(0xffffffffu, id >= 0 && array == 0);
-    uint32_t bits = 0;
-#pragma unroll
-    for (int f = 0; f < 4; ++f) bits |= ((have >> (4 * f)) & 1u) << f;
+  int next_id = page_of();
+  uint32_t valid_bits = 0;   // four bits a stage: which fragments have a page
+  const uint8_t* v_src = nullptr;  // of the unit whose K was copied last
+  bool v_have = false, k_alone = false;  // k_alone: its V is not copied yet
+  uint32_t v_bytes = 0;
+  auto copy_k = [&](int s) {
+    if (ahead <= 0) return;
+    const int id = next_id;
+    const uint32_t have = __ballot_sync(0xffffffffu, id >= 0 && !(lane & 1));
+    const uint32_t bits = (have & 1u) | ((have >> 1) & 2u) | ((have >> 2) & 4u) | ((have >> 3) & 8u);
     valid_bits = (valid_bits & ~(0xfu << (4 * s))) | (bits << (4 * s));
-    const uint32_t bar = bar0 + 8 * s;
-    if (lane == 0) mbar_expect_tx(bar, (uint32_t)(__popc(bits) << fr_log2) * 2 * (C::CODE_ROW + C::SCALE_ROW));
+    v_bytes = (uint32_t)(__popc(bits) << fr_log2) * (C::CODE_ROW + C::SCALE_ROW);
+    v_have = id >= 0;
+    k_alone = true;
+    if (lane == 0) mbar_expect_tx(bars + 16 * s, v_bytes);
     __syncwarp();
-    if (id >= 0) {
-      const long long tok = (long long)pre.u * UNIT + ((long long)frag << fr_log2);
-      const long long row =
-          (((long long)id * p.Hkv + pre.kvh) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
-      const bool is_scale = array & 1;
-      const int row_bytes = is_scale ? C::SCALE_ROW : C::CODE_ROW;
-      const uint8_t* base = is_scale ? p.scales[array >> 1] : p.codes[array >> 1];
-      const int off = array == 0 ? 0 : array == 1 ? C::OFF_KS : array == 2 ? C::OFF_V : C::OFF_VS;
-      bulk_load(ring_addr + s * C::STAGE + off + (frag << fr_log2) * row_bytes, base + row * row_bytes,
-                (uint32_t)row_bytes << fr_log2, bar);
+    if (v_have) {
+      const uint32_t in_page = (uint32_t)((pre.u * UNIT + (frag << fr_log2)) & ((1 << p.page_log2) - 1));
+      const long long row = (((long long)id * p.Hkv + pre.kvh) << p.page_log2) + in_page;
+      const long long off = row * row_bytes;
+      bulk_load(copy_dst + s * 2 * C::PART, ((lane & 1) ? p.scales[0] : p.codes[0]) + off, copy_bytes, bars + 16 * s);
+      v_src = ((lane & 1) ? p.scales[1] : p.codes[1]) + off;
     }
-    ++pre_x;
-    if (pre_x < x1) {
-      kv4_advance(p, UNIT, C::ROWS, pre);
-      next_page = page_of(pre);
+    if (ahead > 1) {
+      kv4_advance<C>(p, req, pre);
+      next_id = page_of();
     }
   };
+  auto copy_v = [&](int s) {
+    if (ahead <= 0) return;
+    --ahead;
+    k_alone = false;
+    if (lane == 0) mbar_expect_tx(bars + 16 * s + 8, v_bytes);
+    __syncwarp();
+    if (v_have) bulk_load(copy_dst + (2 * s + 1) * C::PART, v_src, copy_bytes, bars + 16 * s + 8);
+  };
 #pragma unroll 1
-  for (int s = 0; s < S; ++s) produce(s);
+  for (int s = 0; s < S; ++s) {
+    copy_k(s);
+    copy_v(s);
+  }
 
-  // ------------------------------------------------------------- consumer side
+  // -------------------------------------------------------------- computation
   uint32_t qf[NT][WK][4];  // Q rows as B operands: per word of 8 channels, two k-steps of two registers
   float acc[NT][C::CT][4];
   float m[NT][2], l[NT][2], fac[NT][2];
   int lim[NT][2];  // last key that the lane's two columns (rows of Q) see
   int lim_min = 0;
-
-  bool ok = true;
   int stage = 0;
   uint32_t phase = 0;
   bool fresh = true;
+  long long began = x0 - cur.u;  // first unit of the current triple
 #pragma unroll 1
-  for (long long x = x0; x < x1; ++x) {
+  for (; left > 0; --left) {
     if (fresh) {
       fresh = false;
       lim_min = 0x7fffffff;
@@ -361,7 +401,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          fac[n][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
+          // (not 0, so that a masked score stays -inf)
+          fac[n][j] = fmaxf(__shfl_sync(0xffffffffu, up, (2 * t + j) * 4), 1e-37f);
           const int r = cur.rt * C::ROWS + 8 * n + 2 * t + j;
           const int qi = r / p.G;
           lim[n][j] = qi < cur.nq ? cur.n - cur.nq + qi : -1;
@@ -375,12 +416,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
       lim_min = __reduce_min_sync(0xffffffffu, lim_min);
     }
 
-    if (!wait_warp(bar0 + 8 * stage, phase, ab, (kKKv4 << 8) | 1)) {
-      ok = false;
-      break;
-    }
-    const uint8_t* sk = ring + stage * C::STAGE;
-    const uint8_t* sv = sk + C::OFF_V;
+    if (!wait_warp(bars + 16 * stage, phase, ab, (kKKv4 << 8) | 1)) break;
+    const uint8_t* sk = ring + stage * 2 * C::PART;
+    const uint8_t* sv = sk + C::PART;
     const uint32_t bits = (valid_bits >> (4 * stage)) & 0xfu;
 
     // S^T = K Q^T.
@@ -394,7 +432,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
       for (int h = 0; h < 2; ++h) {
         const int tok = 16 * a + 8 * h + g;
         lds_words<WK>(sk + tok * C::CODE_ROW + t * (4 * WK), w[h]);
-        const uint8_t* ss = sk + C::OFF_KS + tok * C::SCALE_ROW + ((t * WK) >> 1);
+        const uint8_t* ss = sk + C::OFF_SCALE + tok * C::SCALE_ROW + ((t * WK) >> 1);
         if constexpr (WK % 2 == 0) {
 #pragma unroll
           for (int i = 0; i < WK / 2; ++i) s2[h][i] = kv4_scale_both(ss[i]);
@@ -425,33 +463,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
       }
     }
 
+    __syncwarp();
+    copy_k(stage);  // every lane is done with this K
+
     // Softmax over the unit's tokens: column 2t + j of every tile belongs to this lane's (n, j).
-    const long long key0 = (long long)cur.u * UNIT;
-    const bool whole = key0 + UNIT - 1 <= lim_min && bits == (1u << frags) - 1u;
+    const int key0 = cur.u * UNIT;
+    const bool whole = key0 + UNIT - 1 <= lim_min && bits == all_bits;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float mx = -INFINITY;
-        if (whole) {
-#pragma unroll
-          for (int a = 0; a < MT; ++a) mx = max3(mx, sc[a][n][j] *= fac[n][j], sc[a][n][2 + j] *= fac[n][j]);
-        } else {
+        if (!whole) {
 #pragma unroll
           for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int tok = 16 * a + 8 * h + g;
-              const bool seen = key0 + tok <= lim[n][j] && ((bits >> (tok >> fr_log2)) & 1u);
-              const float v = seen ? sc[a][n][2 * h + j] * fac[n][j] : -INFINITY;
-              sc[a][n][2 * h + j] = v;
-              mx = fmaxf(mx, v);
+              if (key0 + tok > lim[n][j] || !((bits >> (tok >> fr_log2)) & 1u)) sc[a][n][2 * h + j] = -INFINITY;
             }
         }
+#pragma unroll
+        for (int a = 0; a < MT; ++a) mx = max3(mx, sc[a][n][j], sc[a][n][2 + j]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        mx -= kKv4Lift;
+        mx = mx * fac[n][j] - kKv4Lift;
         const bool grow = mx > m[n][j] + kKv4Grow;
         const float alpha = grow ? ex2(m[n][j] - mx) : 1.f;
         if (grow) m[n][j] = mx;
@@ -467,13 +504,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
         float sum = 0.f;
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
-          sc[a][n][j] = ex2(sc[a][n][j] - msub);
-          sc[a][n][2 + j] = ex2(sc[a][n][2 + j] - msub);
+          sc[a][n][j] = ex2(fmaf(sc[a][n][j], fac[n][j], -msub));
+          sc[a][n][2 + j] = ex2(fmaf(sc[a][n][2 + j], fac[n][j], -msub));
           sum += sc[a][n][j] + sc[a][n][2 + j];
         }
         l[n][j] += sum;
       }
     }
+
+    if (!wait_warp(bars + 16 * stage + 8, phase, ab, (kKKv4 << 8) | 2)) break;
 
     // O^T += V^T P^T.
 #pragma unroll
@@ -498,7 +537,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
           lds_words<WV>(row[k] + g * (D / 16), w[k]);
         }
       }
-      const uint8_t* ss = sk + C::OFF_VS + tok * C::SCALE_ROW;
+      const uint8_t* ss = sv + C::OFF_SCALE + tok * C::SCALE_ROW;
 #pragma unroll
       for (int i = 0; i < WV; ++i) {
         // The scales of channels 8i.. of the lane's D/8, at tokens (tok, tok+1) and (tok+8, tok+9).
@@ -535,149 +574,162 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
       }
     }
 
-    // Every lane is done with the slot: refill it.
     __syncwarp();
-    produce(stage);
+    copy_v(stage);
     if (++stage == S) {
       stage = 0;
       phase ^= 1;
     }
 
     const bool last_unit = cur.u == cur.units - 1;
-    if (last_unit || x == x1 - 1) {
-      const bool first_here = x - cur.u >= x0;  // the triple began in this warp's range
+    if (last_unit || left == 1) {
+      const bool first_here = began >= x0;  // the triple began in this warp's range
       const bool direct = last_unit && first_here;
-      float* po = nullptr;
-      if (!direct) {
-        // Slot 1: the triple begins here and goes on; slot 0: it began before.
-        const size_t slot = (size_t)me * 2 + (first_here ? 1 : 0);
-        po = p.part_o + slot * C::ROWS * D;
-        float* pml = p.part_ml + slot * C::ROWS * 2;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float s = l[n][j];
-            s += __shfl_xor_sync(0xffffffffu, s, 4);
-            s += __shfl_xor_sync(0xffffffffu, s, 8);
-            s += __shfl_xor_sync(0xffffffffu, s, 16);
-            if (g == 0) *reinterpret_cast<float2*>(pml + (8 * n + 2 * t + j) * 2) = make_float2(m[n][j], s);
-          }
-      }
+      // Slot 1: the triple begins in this range and goes on; slot 0: it began before.
+      const size_t part = (size_t)me * 2 + (first_here ? 1 : 0);
       if (first_here && lane == 0) {
-        const int seg = (cur.b * p.Hkv + cur.kvh) * p.row_tiles + cur.rt;
-        const long long start = x - cur.u;
-        p.meta[seg] = make_int2(me, direct ? 0 : worker_of(start + cur.units - 1) - me + 1);
+        int count = 0;
+        if (!direct) {
+          // And the warps after this one that the rest of the triple goes to.
+          const int rest = (int)(began + cur.units - (x0 + units));
+          const int wide = max(more - (me + 1), 0);  // of them, those that take per + 1
+          count = 1 + (rest <= (long long)wide * (per + 1) ? (rest + per) / (per + 1)
+                                                           : wide + (rest - wide * (per + 1) + per - 1) / per);
+        }
+        p.cuts[((size_t)cur.b * p.Hkv + cur.kvh) * p.row_tiles + cur.rt] = make_int2(me, count);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+          float s = l[n][j];
+          s += __shfl_xor_sync(0xffffffffu, s, 4);
+          s += __shfl_xor_sync(0xffffffffu, s, 8);
+          s += __shfl_xor_sync(0xffffffffu, s, 16);
           const int rr = 8 * n + 2 * t + j;
+          const int r = cur.rt * C::ROWS + rr;
+          const int i = r / p.G, h = cur.kvh * p.G + r - i * p.G;
+          if (i >= cur.nq) continue;
           if (!direct) {
-            float* dst = po + (size_t)rr * D + g * (D / 8);
+            float* dst = p.part_o + (part * C::ROWS + rr) * D + g * (D / 8);
 #pragma unroll
             for (int c = 0; c < C::CT; c += 2)
               *reinterpret_cast<float4*>(dst + 2 * c) =
                   make_float4(acc[n][c][j], acc[n][c][2 + j], acc[n][c + 1][j], acc[n][c + 1][2 + j]);
+            if (g == 0) *reinterpret_cast<float2*>(p.part_ml + (part * C::ROWS + rr) * 2) = make_float2(m[n][j], s);
           } else {
-            float s = l[n][j];
-            s += __shfl_xor_sync(0xffffffffu, s, 4);
-            s += __shfl_xor_sync(0xffffffffu, s, 8);
-            s += __shfl_xor_sync(0xffffffffu, s, 16);
-            const int r = cur.rt * C::ROWS + rr;
-            const int i = r / p.G, h = cur.kvh * p.G + r - i * p.G;
-            if (i < cur.nq) {
-              const float inv = s == 0.f ? 0.f : p.v_gain / s;
-              uint16_t* dst = p.o + (long long)(cur.tok0 + i) * p.o_token + (long long)h * p.o_head + g * (D / 8);
+            const float inv = s == 0.f ? 0.f : p.v_gain / s;
+            uint16_t* dst = p.o + (long long)(cur.tok0 + i) * p.o_token + (long long)h * p.o_head + g * (D / 8);
 #pragma unroll
-              for (int c = 0; c < C::CT; c += 2)
-                *reinterpret_cast<uint2*>(dst + 2 * c) =
-                    make_uint2(pack_bf16(acc[n][c][j] * inv, acc[n][c][2 + j] * inv),
-                               pack_bf16(acc[n][c + 1][j] * inv, acc[n][c + 1][2 + j] * inv));
-              if (g == 0)
-                p.lse[(long long)(cur.tok0 + i) * p.H + h] = s == 0.f ? -INFINITY : (m[n][j] + log2f(s)) * kLn2;
-            }
+            for (int c = 0; c < C::CT; c += 2)
+              *reinterpret_cast<uint2*>(dst + 2 * c) =
+                  make_uint2(pack_bf16(acc[n][c][j] * inv, acc[n][c][2 + j] * inv),
+                             pack_bf16(acc[n][c + 1][j] * inv, acc[n][c + 1][2 + j] * inv));
+            if (g == 0)
+              p.lse[(long long)(cur.tok0 + i) * p.H + h] = s == 0.f ? -INFINITY : (m[n][j] + log2f(s)) * kLn2;
           }
         }
       fresh = true;
+      began += cur.units;
     }
-    if (x + 1 < x1) kv4_advance(p, UNIT, C::ROWS, cur);
+    if (left > 1) kv4_advance<C>(p, req, cur);
   }
   // A warp that gave up lets its copies land before the block can exit.
-  if (!ok)
-    for (long long x = max(pre_x - S, x0); x < pre_x; ++x) {
-      const long long i = x - x0;
-      wait_done(bar0 + 8 * (uint32_t)(i % S), (uint32_t)((i / S) & 1));
-    }
+  if (left > 0) {
+    const int v_units = units - ahead, k_units = v_units + (k_alone ? 1 : 0);
+    for (int i = max(k_units - S, 0); i < k_units; ++i) wait_done(bars + 16 * (i % S), (uint32_t)((i / S) & 1));
+    for (int i = max(v_units - S, 0); i < v_units; ++i) wait_done(bars + 16 * (i % S) + 8, (uint32_t)((i / S) & 1));
+  }
 }
 
 // Joins the parts of cut triples: with M the largest m of a row's parts,
-// O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.  One block per row of a
-// triple; its warps take the parts in turn, each lane one to three runs of four
-// channels, and the sums are joined in shared memory in a fixed order.
-template <int D>
-__global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ Kv4AttnParams p) {
-  __shared__ float acc[4][D];
-  __shared__ float ml[4][2];
-  const int unit = p.unit, rows = p.rows;
+// O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.  blockIdx.x is the triple, and
+// blockIdx.y cuts its work further where there are few.  A warp takes 4*L channels of a
+// row at a time: L lanes of four channels for each of 32/L sets of parts, eight parts in
+// flight a lane, which are joined against the lane's own maximum; then the sets are, in a
+// fixed order.  L = 32, 8 or 4, so that a lane rarely has more than eight parts.
+// Latency bounds it: two dependent loads, the cut and the parts.
+template <class C>
+__global__ void __launch_bounds__(256, 2) kv4_merge_kernel(const __grid_constant__ Kv4AttnParams p) {
+  constexpr int D = C::D;
   grid_dep_wait();
-  if (*reinterpret_cast<volatile const int*>(p.err) != 0) return;
-  const int seg = blockIdx.x / rows, rr = blockIdx.x - seg * rows;
-  const int bk = seg / p.row_tiles, rt = seg - bk * p.row_tiles;
+  const int2 cut = p.cuts[blockIdx.x];
+  const int bk = blockIdx.x / p.row_tiles, rt = blockIdx.x - bk * p.row_tiles;
   const int b = bk / p.Hkv, kvh = bk - b * p.Hkv;
   Kv4Cursor c;
-  kv4_request(p, b, unit, rows, c);
-  const int r = rt * rows + rr;
-  const int i = r / p.G, h = kvh * p.G + r - i * p.G;
-  if (rt >= c.tiles || i >= c.nq) return;
-  const int2 meta = p.meta[seg];
-  if (meta.y == 0) return;
+  kv4_lookup(p, b, c);
+  const int rows = min(C::ROWS, c.nq * p.G - rt * C::ROWS);  // none: the triple does not exist
+  const int parts = cut.y;
+  if (rows <= 0 || parts == 0 || *reinterpret_cast<volatile const int*>(p.err) != 0) return;
   const int warp = warp_id(), lane = lane_id();
-  // Part s of the triple: slot 1 of its first warp, slot 0 of the later ones.
-  auto slot = [&](int s) -> size_t { return (size_t)(meta.x + s) * 2 + (s == 0 ? 1 : 0); };
-  float top = -INFINITY;
-  for (int s = lane; s < meta.y; s += 32) top = fmaxf(top, p.part_ml[(slot(s) * rows + rr) * 2]);
+  const int log_lanes = parts <= 8 ? 5 : parts <= 32 ? 3 : 2;
+  const int set = lane >> log_lanes, sets = 32 >> log_lanes;
+  const int chunks = (D + (4 << log_lanes) - 1) / (4 << log_lanes);
+#pragma unroll 1
+  for (int item = blockIdx.y * 8 + warp; item < rows * chunks; item += 8 * gridDim.y) {
+    const int rr = item / chunks;
+    const int col = (((item - rr * chunks) << log_lanes) + (lane & ((1 << log_lanes) - 1))) * 4;
+    const int load_col = min(col, D - 4);
+    // Part s: slot 1 of its first warp, slot 0 of the later ones.
+    auto slot = [&](int s) -> size_t { return (size_t)(2 * (cut.x + s) + (s == 0 ? 1 : 0)) * C::ROWS + rr; };
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+    for (int s0 = set; s0 < parts; s0 += 8 * sets) {
+      float2 x[8];
+      float4 y[8];
+      float high = top;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float sub = top == -INFINITY ? 0.f : top;
-  constexpr int V = (D + 127) / 128;
-  float4 o[V];
+      for (int k = 0; k < 8; ++k) {  // (loads without branches stay together)
+        const size_t at = slot(min(s0 + k * sets, parts - 1));
+        x[k] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+        y[k] = *reinterpret_cast<const float4*>(p.part_o + at * D + load_col);
+      }
 #pragma unroll
-  for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll 4
-  for (int s = warp; s < meta.y; s += 4) {
-    const float2 x = *reinterpret_cast<const float2*>(p.part_ml + (slot(s) * rows + rr) * 2);
-    const float wt = ex2(x.x - sub);
-    sum += wt * x.y;
-    const float* src = p.part_o + (slot(s) * rows + rr) * D;
+      for (int k = 0; k < 8; ++k) {
+        if (s0 + k * sets >= parts) x[k].x = -INFINITY;
+        high = fmaxf(high, x[k].x);
+      }
+      const float under = high == -INFINITY ? 0.f : high;
+      const float scale = ex2(top - under);
+      top = high;
+      sum *= scale;
+      o.x *= scale, o.y *= scale, o.z *= scale, o.w *= scale;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int col = 128 * v + 4 * lane;
-      if (col < D) {
-        const float4 y = *reinterpret_cast<const float4*>(src + col);
-        o[v].x += wt * y.x;
-        o[v].y += wt * y.y;
-        o[v].z += wt * y.z;
-        o[v].w += wt * y.w;
+      for (int k = 0; k < 8; ++k) {
+        const float w = ex2(x[k].x - under);
+        if (s0 + k * sets < parts) {  // (the weight of a row of NaN is NaN)
+          sum += w * x[k].y;
+          o.x += w * y[k].x;
+          o.y += w * y[k].y;
+          o.z += w * y[k].z;
+          o.w += w * y[k].w;
+        }
       }
     }
+#pragma unroll 1
+    for (int d = 16; d >> log_lanes; d >>= 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, top, d);
+      const float high = fmaxf(top, other);
+      const float under = high == -INFINITY ? 0.f : high;
+      const float wa = ex2(top - under), wb = ex2(other - under);
+      top = high;
+      sum = wa * sum + wb * __shfl_xor_sync(0xffffffffu, sum, d);
+      o.x = wa * o.x + wb * __shfl_xor_sync(0xffffffffu, o.x, d);
+      o.y = wa * o.y + wb * __shfl_xor_sync(0xffffffffu, o.y, d);
+      o.z = wa * o.z + wb * __shfl_xor_sync(0xffffffffu, o.z, d);
+      o.w = wa * o.w + wb * __shfl_xor_sync(0xffffffffu, o.w, d);
+    }
+    if (set == 0 && col < D) {
+      const int r = rt * C::ROWS + rr;
+      const int i = r / p.G, h = kvh * p.G + r - i * p.G;
+      const float inv = sum == 0.f ? 0.f : p.v_gain / sum;
+      *reinterpret_cast<uint2*>(p.o + (long long)(c.tok0 + i) * p.o_token + (long long)h * p.o_head + col) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      if (col == 0)
+        p.lse[(long long)(c.tok0 + i) * p.H + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (128 * v + 4 * lane < D) *reinterpret_cast<float4*>(&acc[warp][128 * v + 4 * lane]) = o[v];
-  if (lane == 0) ml[warp][0] = sum;
-  __syncthreads();
-  const float s = (ml[0][0] + ml[1][0]) + (ml[2][0] + ml[3][0]);
-  const float inv = s == 0.f ? 0.f : p.v_gain / s;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (long long)(c.tok0 + i) * p.o_token + (long long)h * p.o_head);
-  for (int k = threadIdx.x; k < D / 2; k += 128) {
-    const float lo = (acc[0][2 * k] + acc[1][2 * k]) + (acc[2][2 * k] + acc[3][2 * k]);
-    const float hi = (acc[0][2 * k + 1] + acc[1][2 * k + 1]) + (acc[2][2 * k + 1] + acc[3][2 * k + 1]);
-    dst[k] = pack_bf16(lo * inv, hi * inv);
-  }
-  if (threadIdx.x == 0) p.lse[(long long)(c.tok0 + i) * p.H + h] = s == 0.f ? -INFINITY : (top + log2f(s)) * kLn2;
 }
 
 }  // namespace fa

@@ -4,14 +4,13 @@
 #include <cuda_bf16.h>
 
 #include "fa_paged.h"
-#include "host.h"
 #include "kv4.cuh"
+#include "kv4_host.h"
 
 namespace fa {
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 
 // ------------------------------------------------------------------ page tables
 
@@ -163,10 +162,9 @@ fa_status run_pages(PageParams p, cudaStream_t st) {
 // At most 2^21 requests (a block keeps a row for each of its own in shared memory),
 // and positions of 31 bits.
 bool pages_ok(int B, int width, int page, int T) {
-  return B >= 0 && B <= (1 << 21) && width >= 0 && T >= 0 && page_ok(page) && (long long)width * page <= 0x7fffffffLL;
+  return B >= 0 && B <= (1 << 21) && width >= 0 && T >= 0 && page_log2_of(page) >= 0 && (long long)width * page <= 0x7fffffffLL;
 }
 
-int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
 // ------------------------------------------------------------------ store and load
 
@@ -289,33 +287,22 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(const __grid_constant__ K
   dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-fa_status kv4_io_checks(int T, int Hkv, int d, int pages, int page, float k_gain, float v_gain) {
-  if (T < 0 || Hkv < 0 || pages < 0 || !page_ok(page)) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(k_gain) || !(k_gain > 0.f) || !std::isfinite(v_gain) || !(v_gain > 0.f)) return FA_ERR_INVALID_ARG;
-  // The reciprocal is used too.
-  if (!std::isfinite(1.f / k_gain) || !std::isfinite(1.f / v_gain)) return FA_ERR_INVALID_ARG;
-  if (padded_head_dim(d) == 0) return FA_ERR_UNSUPPORTED;
-  if ((long long)Hkv * (d / kKv4Group) > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-  return FA_OK;
-}
-
-fa_status kv4_io_fill(Kv4IoParams& p, const long long* slots, int T, int Hkv, int d, const void* kc, const void* ks,
-                      const void* vc, const void* vs, int pages, int page, float k_gain, float v_gain, dim3& grid) {
-  p.codes[0] = static_cast<uint8_t*>(const_cast<void*>(kc));
-  p.codes[1] = static_cast<uint8_t*>(const_cast<void*>(vc));
-  p.scales[0] = static_cast<uint8_t*>(const_cast<void*>(ks));
-  p.scales[1] = static_cast<uint8_t*>(const_cast<void*>(vs));
+fa_status kv4_io_fill(const fa_kv4_cache& c, const long long* slots, int T, Kv4IoParams& p, dim3& grid) {
+  p.codes[0] = static_cast<uint8_t*>(c.k_codes);
+  p.codes[1] = static_cast<uint8_t*>(c.v_codes);
+  p.scales[0] = static_cast<uint8_t*>(c.k_scales);
+  p.scales[1] = static_cast<uint8_t*>(c.v_scales);
   p.slots = slots;
-  p.gain[0] = k_gain;
-  p.gain[1] = v_gain;
-  p.inv_gain[0] = 1.f / k_gain;
-  p.inv_gain[1] = 1.f / v_gain;
+  p.gain[0] = c.k_gain;
+  p.gain[1] = c.v_gain;
+  p.inv_gain[0] = 1.f / c.k_gain;
+  p.inv_gain[1] = 1.f / c.v_gain;
   p.T = T;
-  p.heads = Hkv;
-  p.groups = d / kKv4Group;
-  p.total = (long long)T * Hkv * p.groups;
-  p.page_log2 = log2_of(page);
-  p.slot_end = (long long)pages * page;
+  p.heads = c.Hkv;
+  p.groups = c.d / kKv4Group;
+  p.total = (long long)T * c.Hkv * p.groups;
+  p.page_log2 = page_log2_of(c.page);
+  p.slot_end = (long long)c.pages * c.page;
   const long long blocks = (p.total + 255) / 256;
   if (blocks > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   grid = dim3((unsigned)blocks, 2);
@@ -323,6 +310,20 @@ fa_status kv4_io_fill(Kv4IoParams& p, const long long* slots, int T, int Hkv, in
 }
 
 }  // namespace
+
+fa_status kv4_cache_checks(const fa_kv4_cache* c) {
+  if (!c || c->pages < 0 || c->Hkv < 0 || page_log2_of(c->page) < 0) return FA_ERR_INVALID_ARG;
+  for (float g : {c->k_gain, c->v_gain})  // the store multiplies by the reciprocal
+    if (!std::isfinite(g) || !(g > 0.f) || !std::isfinite(1.f / g)) return FA_ERR_INVALID_ARG;
+  if (padded_head_dim(c->d) == 0) return FA_ERR_UNSUPPORTED;
+  if ((long long)c->Hkv * (c->d / kKv4Group) > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if (c->pages > 0 && c->Hkv > 0 && (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
+    return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
 }  // namespace fa
 
 using namespace fa;
@@ -338,7 +339,7 @@ fa_status fa_page_grow(const int* lengths, const int* new_tokens, int* table, in
     return FA_ERR_INVALID_ARG;
   if ((width > 0 && !table) || (T > 0 && !slots)) return FA_ERR_INVALID_ARG;
   PageParams p = {lengths, new_tokens, table, free_pages, free_count, slots, cu, lengths_out, count_out,
-                  B, width, log2_of(page), T, free_size, 0};
+                  B, width, page_log2_of(page), T, free_size, 0};
   return run_pages(p, (cudaStream_t)stream);
 }
 
@@ -348,26 +349,23 @@ fa_status fa_page_slots(const int* first, const int* count, const int* table, in
   if (B == 0) return FA_OK;
   if (!first || !count || !cu || (width > 0 && !table) || (T > 0 && !slots)) return FA_ERR_INVALID_ARG;
   PageParams p = {first, count, const_cast<int*>(table), nullptr, nullptr, slots, cu, nullptr, nullptr,
-                  B, width, log2_of(page), T, 0, 0};
+                  B, width, page_log2_of(page), T, 0, 0};
   return run_pages(p, (cudaStream_t)stream);
 }
 
-fa_status fa_kv4_store(const void* k, const void* v, long long k_token, long long k_head, long long v_token,
-                       long long v_head, const long long* slots, int T, int Hkv, int d, void* k_codes,
-                       void* k_scales, void* v_codes, void* v_scales, int pages, int page, float k_gain,
-                       float v_gain, void* stream) {
-  fa_status s = kv4_io_checks(T, Hkv, d, pages, page, k_gain, v_gain);
+fa_status fa_kv4_store(const fa_kv4_cache* cache, const void* k, const void* v, long long k_token,
+                       long long k_head, long long v_token, long long v_head, const long long* slots, int T,
+                       void* stream) {
+  fa_status s = kv4_cache_checks(cache);
   if (s != FA_OK) return s;
-  if (T == 0 || Hkv == 0 || pages == 0) return FA_OK;
-  if (!k || !v || !slots || !k_codes || !k_scales || !v_codes || !v_scales) return FA_ERR_INVALID_ARG;
-  if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) ||
-      !aligned16(v_scales) || (k_token & 7) || (k_head & 7) || (v_token & 7) || (v_head & 7))
+  if (T < 0) return FA_ERR_INVALID_ARG;
+  if (T == 0 || cache->Hkv == 0 || cache->pages == 0) return FA_OK;
+  if (!k || !v || !slots) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || (k_token & 7) || (k_head & 7) || (v_token & 7) || (v_head & 7))
     return FA_ERR_MISALIGNED;
   Kv4IoParams p = {};
   dim3 grid;
-  if ((s = kv4_io_fill(p, slots, T, Hkv, d, k_codes, k_scales, v_codes, v_scales, pages, page, k_gain, v_gain,
-                       grid)) != FA_OK)
-    return s;
+  if ((s = kv4_io_fill(*cache, slots, T, p, grid)) != FA_OK) return s;
   p.in[0] = static_cast<const uint16_t*>(k);
   p.in[1] = static_cast<const uint16_t*>(v);
   p.token[0] = k_token;
@@ -377,22 +375,16 @@ fa_status fa_kv4_store(const void* k, const void* v, long long k_token, long lon
   return launch(FA_KERNEL_KV4_STORE, kv4_store_kernel, grid, dim3(256), 0, (cudaStream_t)stream, p);
 }
 
-fa_status fa_kv4_load(const long long* slots, int T, int Hkv, int d, const void* k_codes, const void* k_scales,
-                      const void* v_codes, const void* v_scales, int pages, int page, float k_gain, float v_gain,
-                      void* k, void* v, void* stream) {
-  fa_status s = kv4_io_checks(T, Hkv, d, pages, page, k_gain, v_gain);
+fa_status fa_kv4_load(const fa_kv4_cache* cache, const long long* slots, int T, void* k, void* v, void* stream) {
+  fa_status s = kv4_cache_checks(cache);
   if (s != FA_OK) return s;
-  if (T == 0 || Hkv == 0) return FA_OK;
+  if (T < 0) return FA_ERR_INVALID_ARG;
+  if (T == 0 || cache->Hkv == 0) return FA_OK;
   if (!k || !v || !slots) return FA_ERR_INVALID_ARG;
-  if (pages > 0 && (!k_codes || !k_scales || !v_codes || !v_scales)) return FA_ERR_INVALID_ARG;
-  if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) ||
-      !aligned16(v_scales))
-    return FA_ERR_MISALIGNED;
+  if (!aligned16(k) || !aligned16(v)) return FA_ERR_MISALIGNED;
   Kv4IoParams p = {};
   dim3 grid;
-  if ((s = kv4_io_fill(p, slots, T, Hkv, d, k_codes, k_scales, v_codes, v_scales, pages, page, k_gain, v_gain,
-                       grid)) != FA_OK)
-    return s;
+  if ((s = kv4_io_fill(*cache, slots, T, p, grid)) != FA_OK) return s;
   p.out[0] = static_cast<uint16_t*>(k);
   p.out[1] = static_cast<uint16_t*>(v);
   return launch(FA_KERNEL_KV4_LOAD, kv4_load_kernel, grid, dim3(256), 0, (cudaStream_t)stream, p);

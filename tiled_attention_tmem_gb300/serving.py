@@ -1,0 +1,287 @@
+"""Serving from a paged 4-bit cache: torch-tensor wrappers over ``include/fa_paged.h``.
+
+Marshalling only, like ``api`` (which offers these names too): PyTorch supplies device
+memory and the stream, the CUDA library computes.  Every operand is a CUDA tensor on
+the cache's (or the lengths') device, which need not be the current one.  A decoding
+step makes several of these calls and each takes a few microseconds on the GPU, so the
+checks are one expression per call, and only a call that fails it finds out why.
+"""
+
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import binding as _b
+
+PAGE_SIZES = (16, 32, 64, 128)
+
+_I32, _I64, _BF16, _F32, _U8 = torch.int32, torch.int64, torch.bfloat16, torch.float32, torch.uint8
+_empty = torch.empty
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _On:
+    """Makes a device and a stream current, so that what is allocated inside belongs to
+    the stream that the kernels run on: a freed workspace is not reused before they end."""
+
+    def __init__(self, index, stream):
+        self.stack = [torch.cuda.device(index)]
+        if stream is not None:
+            self.stack.append(torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index)))
+
+    def __enter__(self):
+        for c in self.stack:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.stack):
+            c.__exit__(*exc)
+
+
+def _elsewhere(index, stream):
+    """Whether a call has to leave the current device or stream."""
+    return stream is not None or index != torch.cuda.current_device()
+
+
+def _check(st, where):
+    if st != _b.FA_OK:
+        raise _b.FaError(st, where)
+
+
+def _dense(t, name, dtype, shape, index=None):
+    """Refuses all but a dense CUDA tensor of this dtype and shape (None: any size)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor, not {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and a != n for a, n in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple('any' if n is None else n for n in shape)}, "
+                         f"not {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other operands on cuda:{index}")
+
+
+def _rows(t, name, shape, index, written=False):
+    """Refuses all but a CUDA bf16 tensor [tokens, heads, d] with dense channels; returns its
+    token and head strides (0 for a dimension of one element)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != _BF16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor of shape [tokens, heads, d]")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != index:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
+        raise ValueError(f"{name} is on {t.device}, the other operands on cuda:{index}")
+    tokens, heads, d = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}: the channels must be dense")
+    st, sh = st if tokens > 1 else 0, sh if heads > 1 else 0
+    if written and ((tokens > 1 and st < d) or (heads > 1 and sh < d)):
+        raise ValueError(f"{name}: its rows overlap")
+    return st, sh
+
+
+def _explain_pages(per_request, table, page_size, num_tokens):
+    if page_size not in PAGE_SIZES:
+        raise ValueError(f"page_size must be one of {PAGE_SIZES}")
+    if num_tokens < 0:
+        raise ValueError("num_tokens must not be negative")
+    first, name = per_request[0]
+    if not isinstance(first, torch.Tensor) or first.dim() != 1:
+        raise ValueError(f"{name} must be a 1-D int32 tensor")
+    index = first.get_device() if first.is_cuda else None
+    for t, name in per_request:
+        _dense(t, name, _I32, first.shape, index)
+    _dense(table, "table", _I32, (first.shape[0], None), index)
+
+
+def page_grow(lengths, new_tokens, table, free_pages, free_count, page_size, num_tokens, stream=None):
+    """Pages and slots for the next ``new_tokens[b]`` tokens of each request.
+
+    lengths, new_tokens int32 [B]; table int32 [B, width]: the pages of each request,
+    whose entries for pages taken now are written in place; free_pages int32 [n] and
+    free_count int32 [1]: the stack of free pages (taken from its end).  Returns
+    (slots int64 [num_tokens], cu int32 [B + 1], lengths int32 [B], free_count int32
+    [1]): the slot of each new token in request order (-1: none, and past the last
+    one), where each request's tokens begin, and the lengths and the count after it.
+    A request that got fewer tokens than it asked for (pages, width or num_tokens ran
+    out) shows it in its length.  Nothing but ``table`` is changed, so the call can be
+    repeated; keep the returned lengths and count for the next one."""
+    _explain_pages([(lengths, "lengths"), (new_tokens, "new_tokens")], table, page_size, num_tokens)
+    index = lengths.get_device()
+    _dense(free_pages, "free_pages", _I32, (None,), index)
+    _dense(free_count, "free_count", _I32, (1,), index)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return page_grow(lengths, new_tokens, table, free_pages, free_count, page_size, num_tokens)
+    B, width = table.shape
+    dev = lengths.device
+    if B == 0:
+        return (torch.full((num_tokens,), -1, dtype=_I64, device=dev), torch.zeros(1, dtype=_I32, device=dev),
+                torch.empty_like(lengths), free_count.clone())
+    slots = _empty(num_tokens, dtype=_I64, device=dev)
+    cu = _empty(B + 1, dtype=_I32, device=dev)
+    held = _empty(B, dtype=_I32, device=dev)
+    count = _empty(1, dtype=_I32, device=dev)
+    _check(_b.fa_page_grow(lengths.data_ptr(), new_tokens.data_ptr(), table.data_ptr(), B, width, page_size,
+                           free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), num_tokens,
+                           slots.data_ptr(), cu.data_ptr(), held.data_ptr(), count.data_ptr(),
+                           _current_stream(index)), "fa_page_grow")
+    return slots, cu, held, count
+
+
+def page_slots(first, count, table, page_size, num_tokens, stream=None):
+    """Slots of the tokens first[b] .. first[b] + count[b] - 1 that each request holds.
+    Returns (slots int64 [num_tokens], cu int32 [B + 1]) as ``page_grow`` does."""
+    _explain_pages([(first, "first"), (count, "count")], table, page_size, num_tokens)
+    index = first.get_device()
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return page_slots(first, count, table, page_size, num_tokens)
+    B, width = table.shape
+    dev = first.device
+    if B == 0:
+        return torch.full((num_tokens,), -1, dtype=_I64, device=dev), torch.zeros(1, dtype=_I32, device=dev)
+    slots = _empty(num_tokens, dtype=_I64, device=dev)
+    cu = _empty(B + 1, dtype=_I32, device=dev)
+    _check(_b.fa_page_slots(first.data_ptr(), count.data_ptr(), table.data_ptr(), B, width, page_size, num_tokens,
+                            slots.data_ptr(), cu.data_ptr(), _current_stream(index)), "fa_page_slots")
+    return slots, cu
+
+
+class KV4Cache:
+    """A pool of pages of keys and values in 4 bits: per tensor, e2m1 codes uint8
+    [pages, kv_heads, page_size, d/2] (even channel in the low half), e4m3 scales uint8
+    [pages, kv_heads, page_size, d/16] and one gain; value = gain * scale * code.  Choose
+    the gain so that max|x| / (6 * gain) stays below 448; a power of two loses nothing."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_gain", "v_gain", "device", "index", "pages",
+                 "kv_heads", "page_size", "head_dim", "descriptor", "address")
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, k_gain: float = 1.0, v_gain: float = 1.0):
+        _dense(k_codes, "k_codes", _U8, (None,) * 4)
+        index = k_codes.get_device()
+        pages, heads, page, half = k_codes.shape
+        if page not in PAGE_SIZES:
+            raise ValueError(f"the page size must be one of {PAGE_SIZES}, not {page}")
+        if 2 * half not in (64, 96, 128, 192, 256, 384):
+            raise ValueError(f"unsupported head dimension {2 * half}")
+        _dense(v_codes, "v_codes", _U8, k_codes.shape, index)
+        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _dense(t, name, _U8, (pages, heads, page, half // 8), index)
+        for x, name in ((k_gain, "k_gain"), (v_gain, "v_gain")):
+            if not (math.isfinite(x) and x > 0):
+                raise ValueError(f"{name} must be finite and positive")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_gain, self.v_gain, self.device, self.index = float(k_gain), float(v_gain), k_codes.device, index
+        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, 2 * half
+        self.descriptor = _b.FaKv4Cache(*(t.data_ptr() for t in (k_codes, k_scales, v_codes, v_scales)), pages, page,
+                                        heads, 2 * half, k_gain, v_gain)
+        self.address = self.descriptor.address
+
+    @classmethod
+    def empty(cls, pages, kv_heads, page_size, head_dim, k_gain: float = 1.0, v_gain: float = 1.0, device="cuda"):
+        """A cache of zeros."""
+        parts = [torch.zeros((pages, kv_heads, page_size, n), dtype=_U8, device=device)
+                 for n in (head_dim // 2, head_dim // 16) * 2]
+        return cls(*parts, k_gain, v_gain)
+
+
+def kv4_store(k, v, slots, cache: KV4Cache, stream=None):
+    """Writes k and v (bf16 [T, kv_heads, d]; token and head strides free, in eights)
+    into the slots (int64 [T]) of ``cache``; tokens whose slot is outside the pool
+    (-1) are skipped.  The other slots must be distinct."""
+    c = cache
+    _dense(slots, "slots", _I64, (None,), c.index)
+    T = slots.shape[0]
+    shape = (T, c.kv_heads, c.head_dim)
+    kt, kh = _rows(k, "k", shape, c.index)
+    vt, vh = _rows(v, "v", shape, c.index)
+    if _elsewhere(c.index, stream):
+        with _On(c.index, stream):
+            return kv4_store(k, v, slots, cache)
+    _check(_b.fa_kv4_store(c.address, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(), T,
+                           _current_stream(c.index)), "fa_kv4_store")
+
+
+def kv4_load(slots, cache: KV4Cache, stream=None):
+    """Returns (k, v), bf16 [T, kv_heads, d]: what the cache holds in these slots
+    (int64 [T]); zeros for a slot outside the pool (-1)."""
+    c = cache
+    _dense(slots, "slots", _I64, (None,), c.index)
+    if _elsewhere(c.index, stream):
+        with _On(c.index, stream):
+            return kv4_load(slots, cache)
+    T = slots.shape[0]
+    shape = (T, c.kv_heads, c.head_dim)
+    k = _empty(shape, dtype=_BF16, device=c.device)
+    v = _empty(shape, dtype=_BF16, device=c.device)
+    _check(_b.fa_kv4_load(c.address, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), _current_stream(c.index)),
+           "fa_kv4_load")
+    return k, v
+
+
+def kv4_attention_workspace_bytes(batch, heads, kv_heads, head_dim, max_q=1) -> int:
+    return _b.fa_kv4_attn_workspace_size(batch, heads, kv_heads, head_dim, max_q)
+
+
+def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int = 1, scale: float | None = None,
+                  out=None, lse=None, workspace=None, stream=None):
+    """Attention of each request's newest tokens over its cached keys and values.
+
+    q bf16 [T, heads, d] (token and head strides free, in eights; heads a multiple of
+    the cache's); table int32 [B, width]; lengths int32 [B]: tokens of each request in
+    the cache, the queries' own included; cu_q int32 [B + 1]: where each request's
+    queries begin in q (None: one each), at most ``max_q`` of them.  Query i of a
+    request's n sees the tokens up to lengths - n + i.  Returns (o bf16 [T, heads, d],
+    lse fp32 [T, heads]); a query that sees nothing gets o = 0 and lse = -inf, rows of
+    no request are left as they were.  ``workspace``: a uint8 CUDA tensor of
+    ``kv4_attention_workspace_bytes``, not shared with a concurrent call, or None."""
+    c = cache
+    qt, qh = _rows(q, "q", None, c.index)
+    T, H, d = q.shape
+    kv = c.kv_heads
+    if d != c.head_dim or (H % kv if kv else H):
+        raise ValueError(f"q has {H} heads of {d} channels, the cache {kv} of {c.head_dim}")
+    _dense(table, "table", _I32, (None, None), c.index)
+    B, width = table.shape
+    _dense(lengths, "lengths", _I32, (B,), c.index)
+    if cu_q is not None:
+        _dense(cu_q, "cu_q", _I32, (B + 1,), c.index)
+        offsets = cu_q.data_ptr()
+    else:
+        offsets, max_q = None, 1
+        if T < B:
+            raise ValueError(f"q has {T} tokens for {B} requests")
+    if out is not None:
+        ot, oh = _rows(out, "out", q.shape, c.index, written=True)
+    if lse is not None:
+        _dense(lse, "lse", _F32, (T, H), c.index)
+    need = _b.fa_kv4_attn_workspace_size(B, H, kv, d, max_q)
+    if workspace is not None:
+        _dense(workspace, "workspace", _U8, (None,), c.index)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
+    if _elsewhere(c.index, stream):
+        with _On(c.index, stream):
+            return kv4_attention(q, cache, table, lengths, cu_q, max_q, scale, out, lse, workspace)
+    if out is None:
+        out = _empty((T, H, d), dtype=_BF16, device=c.device)
+        ot, oh = H * d, d
+    if lse is None:
+        lse = _empty((T, H), dtype=_F32, device=c.device)
+    if workspace is None:
+        workspace = _empty(need, dtype=_U8, device=c.device)
+    _check(_b.fa_kv4_attn(c.address, q.data_ptr(), qt, qh, T, offsets, max_q, table.data_ptr(), width,
+                          lengths.data_ptr(), B, H, d ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh,
+                          lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _current_stream(c.index)),
+           "fa_kv4_attn")
+    return out, lse
