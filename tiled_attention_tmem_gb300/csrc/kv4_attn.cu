@@ -53,7 +53,9 @@ template <int D, int NT>
 fa_status run(const Kv4AttnParams& p, int triples, cudaStream_t st) {
   using C = Kv4Cfg<D, NT>;
   const int sms = sm_count_cached();
-  fa_status s = launch(FA_KERNEL_KV4_ATTN, kv4_attn_kernel<C>, dim3((unsigned)sms), dim3(C::THREADS), C::SMEM, st, p);
+  static std::atomic<unsigned long long> raised{0};
+  fa_status s = launch_raised(FA_KERNEL_KV4_ATTN, kv4_attn_kernel<C>, dim3((unsigned)sms), dim3(C::THREADS), C::SMEM, st,
+                              p, raised);
   // A request of one unit is never cut.
   if (s != FA_OK || ((long long)p.width << p.page_log2) <= C::UNIT) return s;
   // About eight blocks an SM, and no more than one warp for 16 channels of a row.

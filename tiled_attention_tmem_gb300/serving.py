@@ -4,11 +4,13 @@ Marshalling only, like ``api`` (which offers these names too): PyTorch supplies 
 memory and the stream, the CUDA library computes.  Every operand is a CUDA tensor on
 the cache's (or the lengths') device, which need not be the current one.  A decoding
 step makes several of these calls and each takes a few microseconds on the GPU, so the
-checks are one expression per call, and only a call that fails it finds out why.
+usual case of each check is a handful of attribute reads, and only an operand that
+fails it is looked at again for the reason.
 """
 
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -18,9 +20,16 @@ from . import binding as _b
 PAGE_SIZES = (16, 32, 64, 128)
 
 _I32, _I64, _BF16, _F32, _U8 = torch.int32, torch.int64, torch.bfloat16, torch.float32, torch.uint8
-_empty = torch.empty
+_empty, _Tensor = torch.empty, torch.Tensor
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _current_device():
+    return torch.cuda.current_device()
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or _current_device
 
 
 class _On:
@@ -41,11 +50,6 @@ class _On:
             c.__exit__(*exc)
 
 
-def _elsewhere(index, stream):
-    """Whether a call has to leave the current device or stream."""
-    return stream is not None or index != torch.cuda.current_device()
-
-
 def _check(st, where):
     if st != _b.FA_OK:
         raise _b.FaError(st, where)
@@ -53,7 +57,7 @@ def _check(st, where):
 
 def _dense(t, name, dtype, shape, index=None):
     """Refuses all but a dense CUDA tensor of this dtype and shape (None: any size)."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor, not {t.dtype}")
@@ -69,9 +73,13 @@ def _dense(t, name, dtype, shape, index=None):
 def _rows(t, name, shape, index, written=False):
     """Refuses all but a CUDA bf16 tensor [tokens, heads, d] with dense channels; returns its
     token and head strides (0 for a dimension of one element)."""
-    if not isinstance(t, torch.Tensor):
+    if isinstance(t, _Tensor) and t.dtype is _BF16 and t.get_device() == index and t.dim() == 3:
+        st, sh, sd = t.stride()
+        if sd == 1 and st and sh and not written and (shape is None or t.shape == shape):
+            return st, sh
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != _BF16 or t.dim() != 3:
+    if t.dtype is not _BF16 or t.dim() != 3:
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor of shape [tokens, heads, d]")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
@@ -89,13 +97,13 @@ def _rows(t, name, shape, index, written=False):
     return st, sh
 
 
-def _explain_pages(per_request, table, page_size, num_tokens):
+def _check_pages(per_request, table, page_size, num_tokens):
     if page_size not in PAGE_SIZES:
         raise ValueError(f"page_size must be one of {PAGE_SIZES}")
     if num_tokens < 0:
         raise ValueError("num_tokens must not be negative")
     first, name = per_request[0]
-    if not isinstance(first, torch.Tensor) or first.dim() != 1:
+    if not isinstance(first, _Tensor) or first.dim() != 1:
         raise ValueError(f"{name} must be a 1-D int32 tensor")
     index = first.get_device() if first.is_cuda else None
     for t, name in per_request:
@@ -115,14 +123,25 @@ def page_grow(lengths, new_tokens, table, free_pages, free_count, page_size, num
     A request that got fewer tokens than it asked for (pages, width or num_tokens ran
     out) shows it in its length.  Nothing but ``table`` is changed, so the call can be
     repeated; keep the returned lengths and count for the next one."""
-    _explain_pages([(lengths, "lengths"), (new_tokens, "new_tokens")], table, page_size, num_tokens)
-    index = lengths.get_device()
-    _dense(free_pages, "free_pages", _I32, (None,), index)
-    _dense(free_count, "free_count", _I32, (1,), index)
-    if _elsewhere(index, stream):
+    try:
+        index = lengths.get_device()
+        (B,), (rows, width) = lengths.shape, table.shape
+        fine = (index >= 0 and rows == B and lengths.dtype is _I32 and new_tokens.dtype is _I32 and table.dtype is _I32
+                and free_pages.dtype is _I32 and free_count.dtype is _I32 and new_tokens.shape == (B,)
+                and free_count.shape == (1,) and free_pages.dim() == 1 and page_size in PAGE_SIZES and num_tokens >= 0
+                and new_tokens.get_device() == index and table.get_device() == index
+                and free_pages.get_device() == index and free_count.get_device() == index
+                and lengths.is_contiguous() and new_tokens.is_contiguous() and table.is_contiguous()
+                and free_pages.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _check_pages([(lengths, "lengths"), (new_tokens, "new_tokens")], table, page_size, num_tokens)
+        _dense(free_pages, "free_pages", _I32, (None,), lengths.get_device())
+        _dense(free_count, "free_count", _I32, (1,), lengths.get_device())
+    if stream is not None or _current_device() != index:
         with _On(index, stream):
             return page_grow(lengths, new_tokens, table, free_pages, free_count, page_size, num_tokens)
-    B, width = table.shape
     dev = lengths.device
     if B == 0:
         return (torch.full((num_tokens,), -1, dtype=_I64, device=dev), torch.zeros(1, dtype=_I32, device=dev),
@@ -141,9 +160,9 @@ def page_grow(lengths, new_tokens, table, free_pages, free_count, page_size, num
 def page_slots(first, count, table, page_size, num_tokens, stream=None):
     """Slots of the tokens first[b] .. first[b] + count[b] - 1 that each request holds.
     Returns (slots int64 [num_tokens], cu int32 [B + 1]) as ``page_grow`` does."""
-    _explain_pages([(first, "first"), (count, "count")], table, page_size, num_tokens)
+    _check_pages([(first, "first"), (count, "count")], table, page_size, num_tokens)
     index = first.get_device()
-    if _elsewhere(index, stream):
+    if stream is not None or _current_device() != index:
         with _On(index, stream):
             return page_slots(first, count, table, page_size, num_tokens)
     B, width = table.shape
@@ -195,17 +214,23 @@ class KV4Cache:
         return cls(*parts, k_gain, v_gain)
 
 
+def _slot_count(slots, index):
+    if not (isinstance(slots, _Tensor) and slots.dtype is _I64 and slots.dim() == 1 and slots.get_device() == index
+            and slots.is_contiguous()):
+        _dense(slots, "slots", _I64, (None,), index)
+    return slots.shape[0]
+
+
 def kv4_store(k, v, slots, cache: KV4Cache, stream=None):
     """Writes k and v (bf16 [T, kv_heads, d]; token and head strides free, in eights)
     into the slots (int64 [T]) of ``cache``; tokens whose slot is outside the pool
     (-1) are skipped.  The other slots must be distinct."""
     c = cache
-    _dense(slots, "slots", _I64, (None,), c.index)
-    T = slots.shape[0]
+    T = _slot_count(slots, c.index)
     shape = (T, c.kv_heads, c.head_dim)
     kt, kh = _rows(k, "k", shape, c.index)
     vt, vh = _rows(v, "v", shape, c.index)
-    if _elsewhere(c.index, stream):
+    if stream is not None or _current_device() != c.index:
         with _On(c.index, stream):
             return kv4_store(k, v, slots, cache)
     _check(_b.fa_kv4_store(c.address, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(), T,
@@ -216,11 +241,10 @@ def kv4_load(slots, cache: KV4Cache, stream=None):
     """Returns (k, v), bf16 [T, kv_heads, d]: what the cache holds in these slots
     (int64 [T]); zeros for a slot outside the pool (-1)."""
     c = cache
-    _dense(slots, "slots", _I64, (None,), c.index)
-    if _elsewhere(c.index, stream):
+    T = _slot_count(slots, c.index)
+    if stream is not None or _current_device() != c.index:
         with _On(c.index, stream):
             return kv4_load(slots, cache)
-    T = slots.shape[0]
     shape = (T, c.kv_heads, c.head_dim)
     k = _empty(shape, dtype=_BF16, device=c.device)
     v = _empty(shape, dtype=_BF16, device=c.device)
@@ -231,6 +255,12 @@ def kv4_load(slots, cache: KV4Cache, stream=None):
 
 def kv4_attention_workspace_bytes(batch, heads, kv_heads, head_dim, max_q=1) -> int:
     return _b.fa_kv4_attn_workspace_size(batch, heads, kv_heads, head_dim, max_q)
+
+
+# The same by shape and device (it is asked for in every call and depends on nothing else).
+_workspace_bytes = functools.lru_cache(maxsize=256)(
+    lambda batch, heads, kv_heads, head_dim, max_q, index: kv4_attention_workspace_bytes(
+        batch, heads, kv_heads, head_dim, max_q))
 
 
 def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int = 1, scale: float | None = None,
@@ -246,42 +276,51 @@ def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int = 1,
     no request are left as they were.  ``workspace``: a uint8 CUDA tensor of
     ``kv4_attention_workspace_bytes``, not shared with a concurrent call, or None."""
     c = cache
-    qt, qh = _rows(q, "q", None, c.index)
-    T, H, d = q.shape
+    index = c.index
+    if stream is not None or _current_device() != index:
+        with _On(index, stream):
+            return kv4_attention(q, cache, table, lengths, cu_q, max_q, scale, out, lse, workspace)
+    qt, qh = _rows(q, "q", None, index)
+    shape = T, H, d = q.shape
     kv = c.kv_heads
     if d != c.head_dim or (H % kv if kv else H):
         raise ValueError(f"q has {H} heads of {d} channels, the cache {kv} of {c.head_dim}")
-    _dense(table, "table", _I32, (None, None), c.index)
+    if not (isinstance(table, _Tensor) and table.dtype is _I32 and table.dim() == 2 and table.get_device() == index
+            and table.is_contiguous()):
+        _dense(table, "table", _I32, (None, None), index)
     B, width = table.shape
-    _dense(lengths, "lengths", _I32, (B,), c.index)
+    if not (isinstance(lengths, _Tensor) and lengths.dtype is _I32 and lengths.shape == (B,)
+            and lengths.get_device() == index and lengths.is_contiguous()):
+        _dense(lengths, "lengths", _I32, (B,), index)
     if cu_q is not None:
-        _dense(cu_q, "cu_q", _I32, (B + 1,), c.index)
+        if not (isinstance(cu_q, _Tensor) and cu_q.dtype is _I32 and cu_q.shape == (B + 1,)
+                and cu_q.get_device() == index and cu_q.is_contiguous()):
+            _dense(cu_q, "cu_q", _I32, (B + 1,), index)
         offsets = cu_q.data_ptr()
     else:
         offsets, max_q = None, 1
         if T < B:
             raise ValueError(f"q has {T} tokens for {B} requests")
-    if out is not None:
-        ot, oh = _rows(out, "out", q.shape, c.index, written=True)
-    if lse is not None:
-        _dense(lse, "lse", _F32, (T, H), c.index)
-    need = _b.fa_kv4_attn_workspace_size(B, H, kv, d, max_q)
-    if workspace is not None:
-        _dense(workspace, "workspace", _U8, (None,), c.index)
-        if workspace.numel() < need:
-            raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
-    if _elsewhere(c.index, stream):
-        with _On(c.index, stream):
-            return kv4_attention(q, cache, table, lengths, cu_q, max_q, scale, out, lse, workspace)
+    need = _workspace_bytes(B, H, kv, d, max_q, index)
     if out is None:
-        out = _empty((T, H, d), dtype=_BF16, device=c.device)
+        out = _empty(shape, dtype=_BF16, device=c.device)
         ot, oh = H * d, d
+    else:
+        ot, oh = _rows(out, "out", shape, index, written=True)
     if lse is None:
         lse = _empty((T, H), dtype=_F32, device=c.device)
+    else:
+        _dense(lse, "lse", _F32, (T, H), index)
     if workspace is None:
         workspace = _empty(need, dtype=_U8, device=c.device)
-    _check(_b.fa_kv4_attn(c.address, q.data_ptr(), qt, qh, T, offsets, max_q, table.data_ptr(), width,
-                          lengths.data_ptr(), B, H, d ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh,
-                          lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _current_stream(c.index)),
-           "fa_kv4_attn")
+    else:
+        _dense(workspace, "workspace", _U8, (None,), index)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
+        need = workspace.numel()
+    st = _b.lib().fa_kv4_attn(c.address, q.data_ptr(), qt, qh, T, offsets, max_q, table.data_ptr(), width,
+                              lengths.data_ptr(), B, H, d ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh,
+                              lse.data_ptr(), workspace.data_ptr(), need, _current_stream(index))
+    if st:
+        _check(st, "fa_kv4_attn")
     return out, lse
