@@ -51,13 +51,24 @@ fa_status shape_checks(int B, int H, int Hkv, int d, int max_q) {
 
 template <int D, int NT>
 fa_status run(const Kv4AttnParams& p, int triples, cudaStream_t st) {
-  using C = Kv4Cfg<D, NT>;
   const int sms = sm_count_cached();
+  const long long units = (((long long)p.width << p.page_log2) + kv4_unit(D, NT) - 1) / kv4_unit(D, NT);
+  using Solo = Kv4Cfg<D, NT, true>;
+  // A block per triple while all fit the SMs at once and none has many units: measured in
+  // us (solo / split) at d = 128, page 64: 64 triples of 4, 8, 16, 32 units 6.0 / 9.0,
+  // 7.4 / 9.3, 10.5 / 10.0, 16.9 / 12.5; 256 triples 6.6 / 11.4, 8.7 / 13.9, 15.0 / 20.8,
+  // 24.4 / 27.8; 4 triples of 16 units 11.0 / 8.6; 2048 triples (several waves) of 4 units
+  // 35.8 / 30.2.
+  if (triples <= Solo::BLOCKS * sms && units <= 10 + triples / 10) {
+    static std::atomic<unsigned long long> raised{0};
+    return launch_raised(FA_KERNEL_KV4_ATTN, kv4_attn_kernel<Solo>, dim3((unsigned)triples), dim3(Solo::THREADS),
+                         Solo::SMEM, st, p, raised);
+  }
+  using C = Kv4Cfg<D, NT, false>;
   static std::atomic<unsigned long long> raised{0};
   fa_status s = launch_raised(FA_KERNEL_KV4_ATTN, kv4_attn_kernel<C>, dim3((unsigned)sms), dim3(C::THREADS), C::SMEM, st,
                               p, raised);
-  // A request of one unit is never cut.
-  if (s != FA_OK || ((long long)p.width << p.page_log2) <= C::UNIT) return s;
+  if (s != FA_OK) return s;
   // About eight blocks an SM, and no more than one warp for 16 channels of a row.
   const int split = std::max(1, std::min(8 * sms / triples, C::ROWS * D / 16 / 8));
   return launch(FA_KERNEL_KV4_MERGE, kv4_merge_kernel<C>, dim3((unsigned)triples, (unsigned)split), dim3(256), 0, st, p);

@@ -67,30 +67,39 @@ constexpr int kv4_warps(int d, int nt) {
 }
 constexpr int kv4_unit(int d, int nt) { return d <= 128 ? 64 : 32; }
 
-template <int D_, int NT_>
+// SOLO: a block per triple, whose warps take its units in turn and join their parts in
+// shared memory: one launch, and no search for where a range begins.  For short
+// contexts; several of its smaller blocks share an SM.
+constexpr int kKv4SoloWarps = 4;
+template <int D_, int NT_, bool SOLO_>
 struct Kv4Cfg {
   static constexpr int D = D_, NT = NT_;
+  static constexpr bool SOLO = SOLO_;
   static constexpr int ROWS = 8 * NT;
   static constexpr int UNIT = kv4_unit(D, NT);
   static constexpr int MT = UNIT / 16;
-  static constexpr int WARPS = kv4_warps(D, NT);
+  static constexpr int WARPS = SOLO ? kKv4SoloWarps : kv4_warps(D, NT);
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int CODE_ROW = D / 2, SCALE_ROW = D / 16;  // bytes a token
   static constexpr int OFF_SCALE = UNIT * CODE_ROW;
   static constexpr int PART = UNIT * (CODE_ROW + SCALE_ROW);  // K or V of a unit
-  static constexpr int OTHER = THREADS * 20 + 1024;           // what follows the ring
-  static constexpr int FIT = (232448 - OTHER) / (WARPS * 2 * PART);
+  static constexpr int OTHER = SOLO ? 512 : THREADS * 20 + 1024;  // what follows the ring
+  static constexpr int BLOCKS = SOLO ? (NT == 1 && D <= 256 ? 3 : 2) : 1;  // an SM
+  static constexpr int FIT = (233472 / BLOCKS - 1024 - OTHER) / (WARPS * 2 * PART);
   static constexpr int STAGES = FIT < 4 ? FIT : 4;
   static constexpr int OFF_BAR = WARPS * STAGES * 2 * PART;       // per stage: K full, V full
   static constexpr int OFF_PREFIX = OFF_BAR + WARPS * STAGES * 16;
-  static constexpr int OFF_REQ = OFF_PREFIX + (THREADS + 1) * 8;  // tokens, first query, queries
-  static constexpr int OFF_MISC = OFF_REQ + THREADS * 12;
+  static constexpr int OFF_REQ = OFF_PREFIX + (SOLO ? 0 : (THREADS + 1) * 8);  // tokens, first query, queries
+  static constexpr int OFF_MISC = OFF_REQ + (SOLO ? 0 : THREADS * 12);
   static constexpr int SMEM = OFF_MISC + 16 + WARPS * 8;
   static constexpr int WK = D / 32;         // words of 8 codes a lane reads of a K row
   static constexpr int WV = (D + 63) / 64;  // words a lane reads of a V row (d = 96: one and a half)
   static constexpr bool HALF = D % 64 != 0;
   static constexpr int CT = D / 16;  // O^T tiles of 16 channels
-  static_assert(STAGES >= 2 && SMEM <= 232448, "shared memory");
+  static_assert(STAGES >= 2 && BLOCKS * (SMEM + 1024) <= 233472, "shared memory");
+  // A SOLO warp's part, O and then (m, l), lies where its ring was.
+  static constexpr int RING = STAGES * 2 * PART;
+  static_assert(ROWS * (D + 2) * 4 <= RING, "a part fits a ring");
 };
 
 // A position in the sequence of units.
@@ -203,7 +212,7 @@ __device__ __forceinline__ void lds_words(const uint8_t* s, uint32_t* w) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
+__global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
   constexpr int D = C::D, NT = C::NT, UNIT = C::UNIT, MT = C::MT, S = C::STAGES, WK = C::WK, WV = C::WV;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = warp_id(), lane = lane_id();
@@ -224,9 +233,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
   grid_dep_wait();
   const bool skip = *reinterpret_cast<volatile int*>(p.err) != 0;
 
+  const CtaAbort ab{abort_flag, p.err};
+  const int* req = nullptr;  // the requests in shared memory, if they fit there
+  Kv4Cursor cur;
+  int units = 0;                // of this warp
+  long long x0 = 0;             // its first unit in the sequence
+  int me = 0, per = 0, more = 0;
+  if constexpr (C::SOLO) {
+    __syncthreads();  // (the barriers and the abort flag)
+    if (skip) return;
+    const int bk = blockIdx.x / p.row_tiles;
+    cur.b = bk / p.Hkv;
+    kv4_request<C>(p, nullptr, cur.b, cur);
+    cur.kvh = bk - cur.b * p.Hkv;
+    cur.rt = blockIdx.x - bk * p.row_tiles;
+    cur.u = warp;
+    if (cur.rt >= cur.tiles) return;
+    units = max(cur.units - warp + C::WARPS - 1, 0) / C::WARPS;
+    if (cur.units == 1 && warp > 0) return;  // one unit: its warp finishes the triple
+  } else {
   // Units before each thread's run of ceil(B / THREADS) requests, and in all.
   const int run = (p.B + C::THREADS - 1) / C::THREADS;
-  const int* req = run == 1 ? kept : nullptr;
+  req = run == 1 ? kept : nullptr;
   {
     const int b0 = min((int)threadIdx.x * run, p.B), b1 = min(b0 + run, p.B);
     long long sum = 0;
@@ -254,16 +282,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
   }
   __syncthreads();
   if (skip) return;
-  const CtaAbort ab{abort_flag, p.err};
   const long long total = prefix[C::THREADS];
   // `more` warps take per + 1 units and the others per.  Neighbouring ranges go to
   // different SMs, so that few units spread over all.
   const int workers = gridDim.x * C::WARPS;
-  const int me = warp * gridDim.x + blockIdx.x;
-  const int per = (int)min(total / workers, 0x7ffffffell);
-  const int more = (int)(total - (long long)per * workers);
-  const long long x0 = (long long)per * me + min(me, more);
-  const int units = per + (me < more ? 1 : 0);
+  me = warp * gridDim.x + blockIdx.x;
+  per = (int)min(total / workers, 0x7ffffffell);
+  more = (int)(total - (long long)per * workers);
+  x0 = (long long)per * me + min(me, more);
+  units = per + (me < more ? 1 : 0);
   auto locate = [&](long long x, Kv4Cursor& c) -> bool {
     int lo = 0, hi = C::THREADS;
     while (hi - lo > 1) {
@@ -291,9 +318,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
     return false;  // only if the lengths changed meanwhile
   };
 
-  Kv4Cursor cur;
   if (units == 0 || !locate(x0, cur)) return;
-  int left = units, ahead = units;  // still to compute and to copy
+  }
+  int left = units, ahead = units;  // still to compute and to copy (a SOLO warp may have none)
 
   // ------------------------------------------------------------------- copies
   // A K or V is UNIT / FR fragments of FR = min(page, UNIT) tokens, each inside one
@@ -337,7 +364,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
       v_src = ((lane & 1) ? p.scales[1] : p.codes[1]) + off;
     }
     if (ahead > 1) {
-      kv4_advance<C>(p, req, pre);
+      if constexpr (C::SOLO) pre.u += C::WARPS;
+      else kv4_advance<C>(p, req, pre);
       next_id = page_of();
     }
   };
@@ -581,13 +609,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
       phase ^= 1;
     }
 
-    const bool last_unit = cur.u == cur.units - 1;
+    const bool last_unit = !C::SOLO && cur.u == cur.units - 1;
     if (last_unit || left == 1) {
       const bool first_here = began >= x0;  // the triple began in this warp's range
-      const bool direct = last_unit && first_here;
+      const bool direct = C::SOLO ? cur.units == 1 : last_unit && first_here;
       // Slot 1: the triple begins in this range and goes on; slot 0: it began before.
       const size_t part = (size_t)me * 2 + (first_here ? 1 : 0);
-      if (first_here && lane == 0) {
+      if (!C::SOLO && first_here && lane == 0) {
         int count = 0;
         if (!direct) {
           // And the warps after this one that the rest of the triple goes to.
@@ -611,12 +639,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
           const int i = r / p.G, h = cur.kvh * p.G + r - i * p.G;
           if (i >= cur.nq) continue;
           if (!direct) {
-            float* dst = p.part_o + (part * C::ROWS + rr) * D + g * (D / 8);
+            float* const po = C::SOLO ? reinterpret_cast<float*>(ring) : p.part_o + part * C::ROWS * D;
+            float* const pml = C::SOLO ? reinterpret_cast<float*>(ring) + C::ROWS * D : p.part_ml + part * C::ROWS * 2;
+            float* dst = po + rr * D + g * (D / 8);
 #pragma unroll
             for (int c = 0; c < C::CT; c += 2)
               *reinterpret_cast<float4*>(dst + 2 * c) =
                   make_float4(acc[n][c][j], acc[n][c][2 + j], acc[n][c + 1][j], acc[n][c + 1][2 + j]);
-            if (g == 0) *reinterpret_cast<float2*>(p.part_ml + (part * C::ROWS + rr) * 2) = make_float2(m[n][j], s);
+            if (g == 0) *reinterpret_cast<float2*>(pml + 2 * rr) = make_float2(m[n][j], s);
           } else {
             const float inv = s == 0.f ? 0.f : p.v_gain / s;
             uint16_t* dst = p.o + (long long)(cur.tok0 + i) * p.o_token + (long long)h * p.o_head + g * (D / 8);
@@ -632,13 +662,47 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const __grid_co
       fresh = true;
       began += cur.units;
     }
-    if (left > 1) kv4_advance<C>(p, req, cur);
+    if (left > 1) {
+      if constexpr (C::SOLO) cur.u += C::WARPS;
+      else kv4_advance<C>(p, req, cur);
+    }
   }
   // A warp that gave up lets its copies land before the block can exit.
   if (left > 0) {
     const int v_units = units - ahead, k_units = v_units + (k_alone ? 1 : 0);
     for (int i = max(k_units - S, 0); i < k_units; ++i) wait_done(bars + 16 * (i % S), (uint32_t)((i / S) & 1));
     for (int i = max(v_units - S, 0); i < v_units; ++i) wait_done(bars + 16 * (i % S) + 8, (uint32_t)((i / S) & 1));
+  }
+  if constexpr (C::SOLO) {
+    // The warps' parts of the triple, a row a warp at a time.
+    if (cur.units == 1) return;
+    __syncthreads();
+    if (*abort_flag) return;
+    const int parts = min(C::WARPS, cur.units), rows = min(C::ROWS, cur.nq * p.G - cur.rt * C::ROWS);
+    for (int rr = warp; rr < rows; rr += C::WARPS) {
+      auto part = [&](int w) -> const float* { return reinterpret_cast<const float*>(smem + w * C::RING); };
+      float top = -INFINITY, sum = 0.f;
+      for (int w = 0; w < parts; ++w) top = fmaxf(top, part(w)[C::ROWS * D + 2 * rr]);
+      const float under = top == -INFINITY ? 0.f : top;
+      for (int w = 0; w < parts; ++w)
+        sum += ex2(part(w)[C::ROWS * D + 2 * rr] - under) * part(w)[C::ROWS * D + 2 * rr + 1];
+      const float inv = sum == 0.f ? 0.f : p.v_gain / sum;
+      const int r = cur.rt * C::ROWS + rr;
+      const int i = r / p.G, h = cur.kvh * p.G + r - i * p.G;
+      uint16_t* dst = p.o + (long long)(cur.tok0 + i) * p.o_token + (long long)h * p.o_head;
+      for (int col = 2 * lane; col < D; col += 64) {
+        float a = 0.f, b = 0.f;
+        for (int w = 0; w < parts; ++w) {
+          const float wt = ex2(part(w)[C::ROWS * D + 2 * rr] - under);
+          const float2 y = *reinterpret_cast<const float2*>(part(w) + rr * D + col);
+          a += wt * y.x;
+          b += wt * y.y;
+        }
+        *reinterpret_cast<uint32_t*>(dst + col) = pack_bf16(a * inv, b * inv);
+      }
+      if (lane == 0)
+        p.lse[(long long)(cur.tok0 + i) * p.H + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
   }
 }
 
