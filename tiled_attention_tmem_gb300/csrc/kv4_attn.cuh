@@ -171,7 +171,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -449,45 +449,57 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
     const uint8_t* sv = sk + C::PART;
     const uint32_t bits = (valid_bits >> (4 * stage)) & 0xfu;
 
-    // S^T = K Q^T.
+    // S^T = K Q^T, PAIR tiles of 16 tokens at a time: the products of one tile are a chain
+    // through its accumulators, so two run between one another.  Row r of a tile's half is
+    // token r ^ ((r >> 1) & 1): of the rows that a lane's V loads take together, two are
+    // then even tokens and two odd, which halves their bank conflicts (64-byte rows).
+    constexpr int PAIR = NT == 1 ? 2 : 1;
+    const int gt = g ^ ((g >> 1) & 1);
     float sc[MT][NT][4];
 #pragma unroll
-    for (int a = 0; a < MT; ++a) {
+    for (int a0 = 0; a0 < MT; a0 += PAIR) {
+      uint32_t w[PAIR][2][WK], s2[PAIR][2][(WK + 1) / 2 + 1];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) sc[a][n][0] = sc[a][n][1] = sc[a][n][2] = sc[a][n][3] = 0.f;
-      uint32_t w[2][WK], s2[2][(WK + 1) / 2 + 1];
+      for (int q = 0; q < PAIR; ++q)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = 16 * a + 8 * h + g;
-        lds_words<WK>(sk + tok * C::CODE_ROW + t * (4 * WK), w[h]);
-        const uint8_t* ss = sk + C::OFF_SCALE + tok * C::SCALE_ROW + ((t * WK) >> 1);
-        if constexpr (WK % 2 == 0) {
+        for (int h = 0; h < 2; ++h) {
+          const int tok = 16 * (a0 + q) + 8 * h + gt;
+          lds_words<WK>(sk + tok * C::CODE_ROW + t * (4 * WK), w[q][h]);
+          const uint8_t* ss = sk + C::OFF_SCALE + tok * C::SCALE_ROW + ((t * WK) >> 1);
+          if constexpr (WK % 2 == 0) {
 #pragma unroll
-          for (int i = 0; i < WK / 2; ++i) s2[h][i] = kv4_scale_both(ss[i]);
-        } else {
-          // Three words: odd lanes start in the middle of a scale's group.
-          const uint32_t s0 = kv4_scale_both(ss[0]), s1 = kv4_scale_both(ss[1]);
-          s2[h][0] = s0;
-          s2[h][1] = (t & 1) ? s1 : s0;
-          s2[h][2] = s1;
+            for (int i = 0; i < WK / 2; ++i) s2[q][h][i] = kv4_scale_both(ss[i]);
+          } else {
+            // Three words: odd lanes start in the middle of a scale's group.
+            const uint32_t s0 = kv4_scale_both(ss[0]), s1 = kv4_scale_both(ss[1]);
+            s2[q][h][0] = s0;
+            s2[q][h][1] = (t & 1) ? s1 : s0;
+            s2[q][h][2] = s1;
+          }
         }
-      }
 #pragma unroll
       for (int i = 0; i < WK; ++i) {
-        uint32_t r0[4], r1[4];
-        kv4_codes(w[0][i], r0);
-        kv4_codes(w[1][i], r1);
         const int si = WK % 2 == 0 ? i >> 1 : i;
+        uint32_t r[PAIR][2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          r0[j] = h2mul(r0[j], s2[0][si]);
-          r1[j] = h2mul(r1[j], s2[1][si]);
-        }
+        for (int q = 0; q < PAIR; ++q)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_f16(sc[a][n], r0[0], r1[0], r0[1], r1[1], qf[n][i][0], qf[n][i][1]);
-          mma_f16(sc[a][n], r0[2], r1[2], r0[3], r1[3], qf[n][i][2], qf[n][i][3]);
-        }
+          for (int h = 0; h < 2; ++h) {
+            kv4_codes(w[q][h][i], r[q][h]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[q][h][j] = h2mul(r[q][h][j], s2[q][h][si]);
+          }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int q = 0; q < PAIR; ++q)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float* c = sc[a0 + q][n];
+              if (i == 0 && k == 0) c[0] = c[1] = c[2] = c[3] = 0.f;
+              mma_f16(c, r[q][0][2 * k], r[q][1][2 * k], r[q][0][2 * k + 1], r[q][1][2 * k + 1], qf[n][i][2 * k],
+                      qf[n][i][2 * k + 1]);
+            }
       }
     }
 
@@ -496,38 +508,64 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
 
     // Softmax over the unit's tokens: column 2t + j of every tile belongs to this lane's (n, j).
     const int key0 = cur.u * UNIT;
-    const bool whole = key0 + UNIT - 1 <= lim_min && bits == all_bits;
+    if (!(key0 + UNIT - 1 <= lim_min && bits == all_bits)) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int tok = 16 * a + 8 * h + gt;
+          const bool held = (bits >> (tok >> fr_log2)) & 1u;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (key0 + tok > lim[n][j] || !held) sc[a][n][2 * h + j] = -INFINITY;
+        }
+    }
+    float mx[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float mx = -INFINITY;
-        if (!whole) {
+        mx[n][j] = fmaxf(sc[0][n][j], sc[0][n][2 + j]);
 #pragma unroll
-          for (int a = 0; a < MT; ++a)
+        for (int a = 1; a < MT; ++a) mx[n][j] = max3(mx[n][j], sc[a][n][j], sc[a][n][2 + j]);
+      }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int tok = 16 * a + 8 * h + g;
-              if (key0 + tok > lim[n][j] || !((bits >> (tok >> fr_log2)) & 1u)) sc[a][n][2 * h + j] = -INFINITY;
-            }
-        }
+    for (int d = 4; d < 32; d <<= 1)
 #pragma unroll
-        for (int a = 0; a < MT; ++a) mx = max3(mx, sc[a][n][j], sc[a][n][2 + j]);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        mx = mx * fac[n][j] - kKv4Lift;
-        const bool grow = mx > m[n][j] + kKv4Grow;
-        const float alpha = grow ? ex2(m[n][j] - mx) : 1.f;
-        if (grow) m[n][j] = mx;
-        l[n][j] *= alpha;
-        if (__any_sync(0xffffffffu, grow)) {
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mx[n][j] = fmaxf(mx[n][j], __shfl_xor_sync(0xffffffffu, mx[n][j], d));
+    float alpha[NT][2];
+    bool grows = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float high = mx[n][j] * fac[n][j] - kKv4Lift;
+        const bool grow = high > m[n][j] + kKv4Grow;
+        alpha[n][j] = grow ? ex2(m[n][j] - high) : 1.f;
+        if (grow) m[n][j] = high;
+        grows |= grow;
+      }
+    if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          l[n][j] *= alpha[n][j];
 #pragma unroll
           for (int c = 0; c < C::CT; ++c) {
-            acc[n][c][j] *= alpha;
-            acc[n][c][2 + j] *= alpha;
+            acc[n][c][j] *= alpha[n][j];
+            acc[n][c][2 + j] *= alpha[n][j];
           }
         }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
         const float msub = m[n][j] == -INFINITY ? 0.f : m[n][j];
         float sum = 0.f;
 #pragma unroll
@@ -538,7 +576,6 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
         }
         l[n][j] += sum;
       }
-    }
 
     if (!wait_warp(bars + 16 * stage + 8, phase, ab, (kKKv4 << 8) | 2)) break;
 
@@ -551,10 +588,10 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
         pb[n][0] = transpose8(pack_f16(sc[a][n][0], sc[a][n][1]));
         pb[n][1] = transpose8(pack_f16(sc[a][n][2], sc[a][n][3]));
       }
-      const int tok = 16 * a + 2 * t;  // with tok + 1, tok + 8, tok + 9
+      const int t0 = 16 * a + (2 * t ^ (t & 1)), t1 = t0 ^ 1;  // rows 2t and 2t + 1; with 8 more each
       uint32_t w[4][WV];
-      const uint8_t* row[4] = {sv + tok * C::CODE_ROW, sv + (tok + 1) * C::CODE_ROW, sv + (tok + 8) * C::CODE_ROW,
-                               sv + (tok + 9) * C::CODE_ROW};
+      const uint8_t* row[4] = {sv + t0 * C::CODE_ROW, sv + t1 * C::CODE_ROW, sv + (t0 + 8) * C::CODE_ROW,
+                               sv + (t1 + 8) * C::CODE_ROW};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if constexpr (C::HALF) {
@@ -565,10 +602,11 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
           lds_words<WV>(row[k] + g * (D / 16), w[k]);
         }
       }
-      const uint8_t* ss = sv + C::OFF_SCALE + tok * C::SCALE_ROW;
+      const uint8_t* ss0 = sv + C::OFF_SCALE + t0 * C::SCALE_ROW;
+      const uint8_t* ss1 = sv + C::OFF_SCALE + t1 * C::SCALE_ROW;
 #pragma unroll
       for (int i = 0; i < WV; ++i) {
-        // The scales of channels 8i.. of the lane's D/8, at tokens (tok, tok+1) and (tok+8, tok+9).
+        // The scales of channels 8i.. of the lane's D/8, at tokens (t0, t1) and (t0 + 8, t1 + 8).
         uint32_t s2[2][2];  // [half of the word][token pair]
 #pragma unroll
         for (int hw = 0; hw < 2; ++hw) {
@@ -580,8 +618,8 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
             if (C::HALF && 8 * i + 4 * hw >= D / 8) {
               s2[1][0] = s2[1][1] = 0;
             } else {
-              s2[hw][0] = kv4_scale_pair(ss[grp], ss[C::SCALE_ROW + grp]);
-              s2[hw][1] = kv4_scale_pair(ss[8 * C::SCALE_ROW + grp], ss[9 * C::SCALE_ROW + grp]);
+              s2[hw][0] = kv4_scale_pair(ss0[grp], ss1[grp]);
+              s2[hw][1] = kv4_scale_pair(ss0[8 * C::SCALE_ROW + grp], ss1[8 * C::SCALE_ROW + grp]);
             }
           }
         }
