@@ -176,118 +176,164 @@ struct Kv4IoParams {
   uint8_t* scales[2];
   const long long* slots;
   float inv_gain[2], gain[2];
-  long long total;  // groups of 16 channels per tensor
-  int T, heads, groups;  // groups: d / 16
-  int page_log2;
+  int T, heads, page_log2;
+  int pieces;    // runs of eight channels a token: heads * d / 8
+  int per_warp;  // tokens a warp (above 1 only where a token has fewer than 32 pieces)
   long long slot_end;
 };
 
-// Group g of the T x heads x groups of a tensor: its token, head and group, and
-// the group's place in the cache (-1: the token has no slot).
-struct Kv4Place {
-  int token, head, group;
-  long long at;
-};
-__device__ __forceinline__ Kv4Place kv4_place(const Kv4IoParams& p, long long g) {
-  Kv4Place r;
-  const unsigned per = (unsigned)p.heads * p.groups;
-  r.token = (int)(g / per);
-  const unsigned rest = (unsigned)(g - (long long)r.token * per);
-  r.head = rest / (unsigned)p.groups;
-  r.group = rest - r.head * p.groups;
-  const long long slot = p.slots[r.token];
-  if (slot < 0 || slot >= p.slot_end) {
-    r.at = -1;
-  } else {
-    const long long pg = slot >> p.page_log2;
-    const long long row = ((pg * p.heads + r.head) << p.page_log2) + (slot & ((1 << p.page_log2) - 1));
-    r.at = row * p.groups + r.group;
+// A lane's eight channels of token `tok`: head and run in the head, and the row of the
+// cache (the token's slot, the head) that holds them.  blockIdx.y takes 32 pieces of a
+// token, so a warp's accesses to the dense side are 512 contiguous bytes and there is no
+// division by a length that is only known at run time.
+template <int D>
+struct Kv4Piece {
+  int head, run, sub;
+  bool have;
+  __device__ __forceinline__ explicit Kv4Piece(const Kv4IoParams& p) {
+    const int lane = lane_id();
+    int piece = blockIdx.y * 32 + lane;
+    sub = 0;
+    have = piece < p.pieces;
+    if (p.per_warp > 1) {
+      sub = lane / p.pieces;
+      piece = lane - sub * p.pieces;
+      have = sub < p.per_warp;
+    }
+    head = piece / (D / 8);
+    run = piece - head * (D / 8);
   }
-  return r;
-}
+  // -1: the token has no slot.
+  __device__ __forceinline__ long long row(const Kv4IoParams& p, long long slot) const {
+    if (slot < 0 || slot >= p.slot_end) return -1;
+    const long long pg = slot >> p.page_log2;
+    return ((pg * p.heads + head) << p.page_log2) + (slot & ((1 << p.page_log2) - 1));
+  }
+};
 
-// One thread per group of 16 channels (two 16-byte loads, one 8-byte store and
-// its scale byte); blockIdx.y chooses keys or values.  Reading bounds it: 2 bytes
-// in for 0.5625 out.  y * (1/scale) is rounded to 12 bits before its code: where
-// y has bf16's eight bits (a gain that is a power of two), a ratio that lies on
-// the border of two codes then gets there exactly although 1/scale is rounded,
-// and one that does not is at least 2^-8 of itself away.
+// A quotient is taken by a reciprocal and then cut to 12 bits after a push of 2^-13:
+// where x has bf16's eight bits and the gain is a power of two, a quotient on the border
+// of two results lands on it exactly, and any other is at least 2^-8 of itself away, so
+// both scale and code are those of the exact quotient.
+constexpr float kKv4Push = 1.f + 1.f / 8192.f;
+__device__ __forceinline__ float cut12(float x) { return __uint_as_float(__float_as_uint(x) & 0xfffff000u); }
+
+// Two lanes per group of 16 channels, which share its scale; keys and values, and U
+// tokens a warp, together: what bounds it is the latency of a slot and then the rows,
+// and then reading (2 bytes in for 0.5625 out).
+template <int D, int U>
 __global__ void __launch_bounds__(256) kv4_store_kernel(const __grid_constant__ Kv4IoParams p) {
   grid_dep_wait();
-  const long long g = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (g >= p.total) return;
-  const int which = blockIdx.y;
-  const Kv4Place at = kv4_place(p, g);
-  if (at.at < 0) return;
-  const uint4* src = reinterpret_cast<const uint4*>(p.in[which] + at.token * p.token[which] +
-                                                    at.head * p.head[which] + at.group * kKv4Group);
-  const uint4 a = src[0], b = src[1];
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  float y[16], top = 0.f;
+  const Kv4Piece<D> at(p);
+  const long long tok0 = ((long long)blockIdx.x * 8 + warp_id()) * U * p.per_warp + at.sub;
+  long long slot[U];
+  uint4 x[U][2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    y[2 * i] = __uint_as_float(w[i] << 16) * p.inv_gain[which];
-    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * p.inv_gain[which];
-    top = fmaxf(top, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
-  }
-  uint16_t sb;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.f), "f"(__fdiv_rn(top, 6.f)));
-  const uint32_t s = sb & 0xffu;
-  // e4m3 to fp32 by way of f16 (2^-8 of the scale; exact).
-  const float sf = __half2float(__ushort_as_half((unsigned short)((s & 0x7f) << 7))) * kKv4ScaleBias;
-  const float inv = sf > 0.f ? __frcp_rn(sf) : 0.f;
-  uint32_t out[2];
+  for (int u = 0; u < U; ++u) {
+    const long long tok = tok0 + (long long)u * p.per_warp;
+    const bool have = at.have && tok < p.T;
+    slot[u] = have ? p.slots[tok] : -1;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float lo = sf > 0.f ? y[8 * h + 2 * i] * inv : 0.f;
-      const float hi = sf > 0.f ? y[8 * h + 2 * i + 1] * inv : 0.f;
-      // To 12 bits; fminf turns a NaN into 8, which saturates to 6.
-      const float lr = __uint_as_float((__float_as_uint(fminf(lo, 8.f)) + 0x800u) & 0xfffff000u);
-      const float hr = __uint_as_float((__float_as_uint(fminf(hi, 8.f)) + 0x800u) & 0xfffff000u);
-      asm("{\n\t.reg .b8 x;\n\t.reg .b16 h;\n\t"
-          "cvt.rn.satfinite.e2m1x2.f32 x, %1, %2;\n\t"
-          "cvt.u32.u8 %0, x;\n\t}"
-          : "=r"(q[i])
-          : "f"(hr), "f"(lr));
+    for (int i = 0; i < 2; ++i) {
+      x[u][i] = make_uint4(0u, 0u, 0u, 0u);
+      if (have)
+        x[u][i] = *reinterpret_cast<const uint4*>(p.in[i] + tok * p.token[i] + at.head * p.head[i] + at.run * 8);
     }
-    out[h] = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
   }
-  *reinterpret_cast<uint2*>(p.codes[which] + at.at * 8) = make_uint2(out[0], out[1]);
-  p.scales[which][at.at] = (uint8_t)s;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long row = at.row(p, slot[u]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+      uint32_t pair = 0;  // (a NaN is passed over)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) asm("max.bf16x2 %0, %0, %1;" : "+r"(pair) : "r"(w[k] & 0x7fff7fffu));
+      float top = fmaxf(__uint_as_float(pair << 16), __uint_as_float(pair & 0xffff0000u));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      uint16_t sb;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(sb)
+          : "f"(0.f), "f"(cut12(top * p.inv_gain[i] * (kKv4Push / 6.f))));
+      const uint32_t s = sb & 0xffu;
+      // e4m3 to fp32 by way of f16 (2^-8 of the scale; exact).
+      const float sf = __half2float(__ushort_as_half((unsigned short)((s & 0x7f) << 7))) * kKv4ScaleBias;
+      float inv;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sf));
+      const float mul = sf > 0.f ? inv * p.inv_gain[i] * kKv4Push : 0.f;
+      uint32_t q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float lo = cut12(__uint_as_float(w[k] << 16) * mul);
+        const float hi = cut12(__uint_as_float(w[k] & 0xffff0000u) * mul);
+        asm("{\n\t.reg .b8 x;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 x, %1, %2;\n\t"
+            "cvt.u32.u8 %0, x;\n\t}"
+            : "=r"(q[k])
+            : "f"(hi), "f"(lo));
+      }
+      if (row >= 0) {
+        *reinterpret_cast<uint32_t*>(p.codes[i] + row * (D / 2) + at.run * 4) =
+            q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
+        if (!(at.run & 1)) p.scales[i][row * (D / 16) + (at.run >> 1)] = (uint8_t)s;
+      }
+    }
+  }
 }
 
-// The inverse, with the same split; writing bounds it.  f16 products are exact,
-// so the one rounding is the last, to bf16.
+// The inverse, with the same split.  f16 products are exact, so the one rounding is the
+// last, to bf16.
+template <int D, int U>
 __global__ void __launch_bounds__(256) kv4_load_kernel(const __grid_constant__ Kv4IoParams p) {
   grid_dep_wait();
-  const long long g = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (g >= p.total) return;
-  const int which = blockIdx.y;
-  const Kv4Place at = kv4_place(p, g);
-  uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (at.at >= 0) {
-    const uint2 c = *reinterpret_cast<const uint2*>(p.codes[which] + at.at * 8);
-    const uint32_t s = kv4_scale_both(p.scales[which][at.at]);
-    uint32_t r[8];
-    kv4_codes(c.x, r);
-    kv4_codes(c.y, r + 4);
-    const float gain = p.gain[which] * kKv4ScaleBias;
+  const Kv4Piece<D> at(p);
+  const long long tok0 = ((long long)blockIdx.x * 8 + warp_id()) * U * p.per_warp + at.sub;
+  if (!at.have) return;
+  long long slot[U];
+  uint32_t c[U][2], s[U][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t v = h2mul(r[i], s);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-      o[i] = pack_bf16(f.x * gain, f.y * gain);
+  for (int u = 0; u < U; ++u) {
+    const long long tok = tok0 + (long long)u * p.per_warp;
+    slot[u] = tok < p.T ? p.slots[tok] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long row = at.row(p, slot[u]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c[u][i] = s[u][i] = 0;
+      if (row >= 0) {
+        c[u][i] = *reinterpret_cast<const uint32_t*>(p.codes[i] + row * (D / 2) + at.run * 4);
+        s[u][i] = p.scales[i][row * (D / 16) + (at.run >> 1)];
+      }
     }
   }
-  uint4* dst = reinterpret_cast<uint4*>(p.out[which] + g * kKv4Group);
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long tok = tok0 + (long long)u * p.per_warp;
+    if (tok >= p.T) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t r[4], o[4];
+      kv4_codes(c[u][i], r);
+      const uint32_t s2 = kv4_scale_both(s[u][i]);
+      const float gain = p.gain[i] * kKv4ScaleBias;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t v = h2mul(r[k], s2);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+        o[k] = pack_bf16(f.x * gain, f.y * gain);
+      }
+      *reinterpret_cast<uint4*>(p.out[i] + (tok * p.heads + at.head) * D + at.run * 8) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
 }
 
-fa_status kv4_io_fill(const fa_kv4_cache& c, const long long* slots, int T, Kv4IoParams& p, dim3& grid) {
+// Tokens a warp (per row of tokens): four where that still leaves 32 warps an SM, else one.
+constexpr int kKv4Batch = 4;
+
+fa_status kv4_io_fill(const fa_kv4_cache& c, const long long* slots, int T, Kv4IoParams& p, dim3& grid, bool& batch) {
   p.codes[0] = static_cast<uint8_t*>(c.k_codes);
   p.codes[1] = static_cast<uint8_t*>(c.v_codes);
   p.scales[0] = static_cast<uint8_t*>(c.k_scales);
@@ -299,13 +345,14 @@ fa_status kv4_io_fill(const fa_kv4_cache& c, const long long* slots, int T, Kv4I
   p.inv_gain[1] = 1.f / c.v_gain;
   p.T = T;
   p.heads = c.Hkv;
-  p.groups = c.d / kKv4Group;
-  p.total = (long long)T * c.Hkv * p.groups;
   p.page_log2 = page_log2_of(c.page);
   p.slot_end = (long long)c.pages * c.page;
-  const long long blocks = (p.total + 255) / 256;
-  if (blocks > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-  grid = dim3((unsigned)blocks, 2);
+  const long long pieces = (long long)c.Hkv * (c.d / 8), chunks = (pieces + 31) / 32;
+  p.pieces = (int)pieces;
+  p.per_warp = std::max(1, 32 / p.pieces);
+  batch = (long long)T / p.per_warp * chunks >= 32LL * kKv4Batch * sm_count_cached();
+  const long long per_block = 8LL * p.per_warp * (batch ? kKv4Batch : 1);
+  grid = dim3((unsigned)((T + per_block - 1) / per_block), (unsigned)chunks);
   return FA_OK;
 }
 
@@ -316,7 +363,8 @@ fa_status kv4_cache_checks(const fa_kv4_cache* c) {
   for (float g : {c->k_gain, c->v_gain})  // the store multiplies by the reciprocal
     if (!std::isfinite(g) || !(g > 0.f) || !std::isfinite(1.f / g)) return FA_ERR_INVALID_ARG;
   if (padded_head_dim(c->d) == 0) return FA_ERR_UNSUPPORTED;
-  if ((long long)c->Hkv * (c->d / kKv4Group) > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  // A token's runs of eight channels, 32 at a time, have to fit a grid's second dimension.
+  if ((long long)c->Hkv * c->d > 65535LL * 256) return FA_ERR_INVALID_ARG;
   if (c->pages > 0 && c->Hkv > 0 && (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales))
     return FA_ERR_INVALID_ARG;
   if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
@@ -365,14 +413,24 @@ fa_status fa_kv4_store(const fa_kv4_cache* cache, const void* k, const void* v, 
     return FA_ERR_MISALIGNED;
   Kv4IoParams p = {};
   dim3 grid;
-  if ((s = kv4_io_fill(*cache, slots, T, p, grid)) != FA_OK) return s;
+  bool batch;
+  if ((s = kv4_io_fill(*cache, slots, T, p, grid, batch)) != FA_OK) return s;
   p.in[0] = static_cast<const uint16_t*>(k);
   p.in[1] = static_cast<const uint16_t*>(v);
   p.token[0] = k_token;
   p.token[1] = v_token;
   p.head[0] = k_head;
   p.head[1] = v_head;
-  return launch(FA_KERNEL_KV4_STORE, kv4_store_kernel, grid, dim3(256), 0, (cudaStream_t)stream, p);
+  const auto run = [&](auto kernel) { return launch(FA_KERNEL_KV4_STORE, kernel, grid, dim3(256), 0, (cudaStream_t)stream, p); };
+  switch (cache->d) {
+    case 64: return batch ? run(kv4_store_kernel<64, kKv4Batch>) : run(kv4_store_kernel<64, 1>);
+    case 96: return batch ? run(kv4_store_kernel<96, kKv4Batch>) : run(kv4_store_kernel<96, 1>);
+    case 128: return batch ? run(kv4_store_kernel<128, kKv4Batch>) : run(kv4_store_kernel<128, 1>);
+    case 192: return batch ? run(kv4_store_kernel<192, kKv4Batch>) : run(kv4_store_kernel<192, 1>);
+    case 256: return batch ? run(kv4_store_kernel<256, kKv4Batch>) : run(kv4_store_kernel<256, 1>);
+    case 384: return batch ? run(kv4_store_kernel<384, kKv4Batch>) : run(kv4_store_kernel<384, 1>);
+  }
+  return FA_ERR_UNSUPPORTED;
 }
 
 fa_status fa_kv4_load(const fa_kv4_cache* cache, const long long* slots, int T, void* k, void* v, void* stream) {
@@ -384,10 +442,20 @@ fa_status fa_kv4_load(const fa_kv4_cache* cache, const long long* slots, int T, 
   if (!aligned16(k) || !aligned16(v)) return FA_ERR_MISALIGNED;
   Kv4IoParams p = {};
   dim3 grid;
-  if ((s = kv4_io_fill(*cache, slots, T, p, grid)) != FA_OK) return s;
+  bool batch;
+  if ((s = kv4_io_fill(*cache, slots, T, p, grid, batch)) != FA_OK) return s;
   p.out[0] = static_cast<uint16_t*>(k);
   p.out[1] = static_cast<uint16_t*>(v);
-  return launch(FA_KERNEL_KV4_LOAD, kv4_load_kernel, grid, dim3(256), 0, (cudaStream_t)stream, p);
+  const auto run = [&](auto kernel) { return launch(FA_KERNEL_KV4_LOAD, kernel, grid, dim3(256), 0, (cudaStream_t)stream, p); };
+  switch (cache->d) {
+    case 64: return batch ? run(kv4_load_kernel<64, kKv4Batch>) : run(kv4_load_kernel<64, 1>);
+    case 96: return batch ? run(kv4_load_kernel<96, kKv4Batch>) : run(kv4_load_kernel<96, 1>);
+    case 128: return batch ? run(kv4_load_kernel<128, kKv4Batch>) : run(kv4_load_kernel<128, 1>);
+    case 192: return batch ? run(kv4_load_kernel<192, kKv4Batch>) : run(kv4_load_kernel<192, 1>);
+    case 256: return batch ? run(kv4_load_kernel<256, kKv4Batch>) : run(kv4_load_kernel<256, 1>);
+    case 384: return batch ? run(kv4_load_kernel<384, kKv4Batch>) : run(kv4_load_kernel<384, 1>);
+  }
+  return FA_ERR_UNSUPPORTED;
 }
 
 }  // extern "C"
