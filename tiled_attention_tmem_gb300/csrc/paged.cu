@@ -151,11 +151,11 @@ __global__ void __launch_bounds__(kPageThreads) page_kernel(const __grid_constan
 
 fa_status run_pages(PageParams p, cudaStream_t st) {
   // Requests per block: eight (one a warp) until the grid covers the SMs twice.
-  // Tokens: another block for every 256 of the mean request, within the same bound.
+  // Tokens: another block for every 64 of the mean request, within the same bound.
   const int cap = 2 * sm_count_cached();
   p.per_block = std::max(8, (p.B + cap - 1) / cap);
   const int gx = (p.B + p.per_block - 1) / p.per_block;
-  const int gy = std::max(1, std::min(cap / gx, (int)((long long)p.T / std::max(1, p.B) / 256)));
+  const int gy = std::max(1, std::min(cap / gx, (int)((long long)p.T / std::max(1, p.B) / 64)));
   return launch(FA_KERNEL_PAGE, page_kernel, dim3(gx, gy), dim3(kPageThreads), p.per_block * sizeof(PageRow), st, p);
 }
 
