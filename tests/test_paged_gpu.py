@@ -284,6 +284,50 @@ def test_attention_several_queries(d, page, kv, group, queries):
     _attend(problem, lengths, max(queries))
 
 
+@pytest.mark.parametrize("d", DIMS)
+@pytest.mark.parametrize("page,kv,group,queries", [
+    (64, 1, 16, [9, 0, 1, 4, 9, 2]), (16, 2, 8, [6, 5, 2, 6, 1, 3]), (128, 1, 33, [2, 4, 1, 3, 4, 4]),
+    (32, 1, 130, [1, 2, 1, 1, 2, 1])])
+def test_attention_many_rows(d, page, kv, group, queries):
+    """Rows enough for the tcgen05 kernel, up to more than one tile of 128, over contexts
+    that begin and end inside a block's share of the units."""
+    lengths = [2300, 0, 1, 700, 65, 129]
+    problem = _problem(d, page, kv * group, kv, lengths, queries, seed=3 * d + page, pad=2)
+    _attend(problem, lengths, max(queries))
+
+
+@pytest.mark.parametrize("d,page,lengths", [(128, 64, [9000]), (384, 32, [5001]), (256, 16, [4000, 2]), (64, 128, [20000])])
+def test_attention_many_rows_cut_over_all_blocks(d, page, lengths):
+    problem = _problem(d, page, 20, 1, lengths, [3] * len(lengths), seed=d, spread=3.0, gains=(2.0 ** -4, 2.0 ** -5))
+    _attend(problem, lengths, 3)
+
+
+def test_attention_many_rows_skips_bad_pages_and_foreign_rows():
+    import torch
+    lengths = [2000, 1500]
+    arrays, table, cu, q, gains = _problem(128, 16, 16, 1, lengths, [3, 2], seed=61, pad=2)
+    table[0, 3], table[0, 60], table[1, 0], table[1, 17] = -1, 10 ** 6, len(arrays[0]), -9
+    o = torch.full((7, 16, 128), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    lse = torch.full((7, 16), 7.0, device="cuda:0")
+    _attend((arrays, table, cu, q, gains), lengths, 3, out=o, lse=lse)
+    assert torch.all(o[5:] == 7) and torch.all(lse[5:] == 7)
+
+
+def test_attention_many_rows_keeps_nan_in_its_row():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    lengths = [3000, 900]
+    arrays, table, cu, q, gains = _problem(128, 64, 24, 1, lengths, [2, 1], seed=67)
+    x, cache = to_dev(q), _cache_of(arrays, gains)
+    clean, _ = api.kv4_attention(x, cache, _i32(table), _i32(lengths), _i32(cu), 2)
+    x[0, 1, 5], x[2, 20, 0] = float("nan"), float("inf")
+    got, lse = api.kv4_attention(x, cache, _i32(table), _i32(lengths), _i32(cu), 2)
+    bad = torch.zeros((3, 24), dtype=torch.bool, device="cuda:0")
+    bad[0, 1] = bad[2, 20] = True
+    assert torch.all(torch.isnan(got[bad])) and torch.all(torch.isnan(lse[bad]))
+    assert torch.equal(got[~bad], clean[~bad])
+
+
 def test_attention_without_offsets_is_one_query_a_request():
     from tiled_attention_tmem_gb300 import api
     lengths = [5, 0, 77]

@@ -1,5 +1,6 @@
 // Launcher of attention over the paged 4-bit cache: tile choice, workspace, checks.
 #include "kv4_attn.cuh"
+#include "kv4_wide.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -14,30 +15,41 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Tiles of 8 query rows that a warp keeps: as many as the rows need, up to what
 // its registers hold (d*NT/4 of O, d*NT/8 of Q and half a unit of scores).
-int most_nt(int d) { return d <= 64 ? 4 : d <= 192 ? 2 : 1; }
+constexpr int most_nt(int d) { return d <= 64 ? 4 : d <= 192 ? 2 : 1; }
 int choose_nt(int d, long long rows) {
   int nt = 1;
   while (nt < most_nt(d) && 8 * nt < rows) nt *= 2;
   return nt;
 }
 
+// From how many rows a kv head on the tcgen05 kernel takes a request.
+bool use_wide(int d, long long rows) { return rows > 8 * most_nt(d); }
+
+// Tiles and triples of the two kernels, and the workspace for either.
 struct Plan {
-  int nt, row_tiles, triples;
+  int nt;
+  bool wide;
+  int row_tiles, triples;            // of 8 * nt rows
+  int wide_row_tiles, wide_triples;  // of 128 rows
   size_t off_ml, off_cuts, bytes;
 };
 
 bool make_plan(int B, int H, int Hkv, int d, int max_q, Plan& plan) {
   const long long rows = (long long)max_q * (H / Hkv);
   plan.nt = choose_nt(d, rows);
-  const long long tiles = (rows + 8 * plan.nt - 1) / (8 * plan.nt);
+  plan.wide = use_wide(d, rows);
+  const long long tiles = (rows + 8 * plan.nt - 1) / (8 * plan.nt), wide_tiles = (rows + 127) / 128;
   if (tiles * B * Hkv > 0x7fffffffLL / (8 * plan.nt)) return false;
   plan.row_tiles = (int)tiles;
   plan.triples = (int)(tiles * B * Hkv);
-  // Two slots of a tile's rows for every warp.
-  const size_t held = (size_t)sm_count_cached() * kv4_warps(d, plan.nt) * 2 * 8 * plan.nt;
+  plan.wide_row_tiles = (int)wide_tiles;
+  plan.wide_triples = (int)(wide_tiles * B * Hkv);
+  // Two slots of a tile's rows for every warp, or of 128 rows for every block.
+  const size_t sms = sm_count_cached();
+  const size_t held = plan.wide ? sms * 2 * 128 : sms * kv4_warps(d, plan.nt) * 2 * 8 * plan.nt;
   plan.off_ml = round256(held * d * sizeof(float));
   plan.off_cuts = plan.off_ml + round256(held * 2 * sizeof(float));
-  plan.bytes = plan.off_cuts + round256(plan.triples * sizeof(int2));
+  plan.bytes = plan.off_cuts + round256((plan.wide ? plan.wide_triples : plan.triples) * sizeof(int2));
   return true;
 }
 
@@ -49,10 +61,20 @@ fa_status shape_checks(int B, int H, int Hkv, int d, int max_q) {
   return FA_OK;
 }
 
+// The merge of a kernel's parts: about eight blocks an SM, and no more than one warp for
+// 16 channels of a row.
+template <class C>
+fa_status run_merge(const Kv4AttnParams& p, int triples, int most_rows, cudaStream_t st) {
+  const int split = std::max(1, std::min(8 * sm_count_cached() / triples, std::min(C::ROWS, most_rows) * C::D / 16 / 8));
+  return launch(FA_KERNEL_KV4_MERGE, kv4_merge_kernel<C>, dim3((unsigned)triples, (unsigned)split), dim3(256), 0, st, p);
+}
+
 template <int D, int NT>
-fa_status run(const Kv4AttnParams& p, int triples, cudaStream_t st) {
-  const int sms = sm_count_cached();
+fa_status run(Kv4AttnParams p, const Plan& plan, cudaStream_t st) {
+  const int sms = sm_count_cached(), triples = plan.triples;
+  const int most_rows = (int)std::min<long long>((long long)p.max_q * p.G, 1 << 20);
   const long long units = (((long long)p.width << p.page_log2) + kv4_unit(D, NT) - 1) / kv4_unit(D, NT);
+  p.row_tiles = plan.row_tiles;
   using Solo = Kv4Cfg<D, NT, true>;
   // A block per triple while all fit the SMs at once and none has many units: measured in
   // us (solo / split) at d = 128, page 64: 64 triples of 4, 8, 16, 32 units 6.0 / 9.0,
@@ -64,14 +86,19 @@ fa_status run(const Kv4AttnParams& p, int triples, cudaStream_t st) {
     return launch_raised(FA_KERNEL_KV4_ATTN, kv4_attn_kernel<Solo>, dim3((unsigned)triples), dim3(Solo::THREADS),
                          Solo::SMEM, st, p, raised);
   }
+  if (NT == most_nt(D) && plan.wide) {
+    static std::atomic<unsigned long long> raised{0};
+    using W = Kv4WideCfg<D>;
+    p.row_tiles = plan.wide_row_tiles;
+    fa_status s = launch_raised(FA_KERNEL_KV4_ATTN, kv4_wide_kernel<W>, dim3((unsigned)sms), dim3(W::THREADS), W::SMEM, st,
+                                p, raised);
+    return s != FA_OK ? s : run_merge<W>(p, plan.wide_triples, most_rows, st);
+  }
   using C = Kv4Cfg<D, NT, false>;
   static std::atomic<unsigned long long> raised{0};
   fa_status s = launch_raised(FA_KERNEL_KV4_ATTN, kv4_attn_kernel<C>, dim3((unsigned)sms), dim3(C::THREADS), C::SMEM, st,
                               p, raised);
-  if (s != FA_OK) return s;
-  // About eight blocks an SM, and no more than one warp for 16 channels of a row.
-  const int split = std::max(1, std::min(8 * sms / triples, C::ROWS * D / 16 / 8));
-  return launch(FA_KERNEL_KV4_MERGE, kv4_merge_kernel<C>, dim3((unsigned)triples, (unsigned)split), dim3(256), 0, st, p);
+  return s != FA_OK ? s : run_merge<C>(p, triples, most_rows, st);
 }
 
 }  // namespace
@@ -125,7 +152,6 @@ fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_toke
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + plan.off_ml);
   p.cuts = reinterpret_cast<int2*>(ws + plan.off_cuts);
-  p.row_tiles = plan.row_tiles;
   p.err = device_error_word();
   if (!p.err) return record_cuda_error(cudaErrorMemoryAllocation);
   p.q_token = q_token;
@@ -145,17 +171,17 @@ fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_toke
   p.v_gain = cache->v_gain * kKv4ScaleBias;
   cudaStream_t st = (cudaStream_t)stream;
   switch (d * 8 + plan.nt) {
-    case 64 * 8 + 1: return run<64, 1>(p, plan.triples, st);
-    case 64 * 8 + 2: return run<64, 2>(p, plan.triples, st);
-    case 64 * 8 + 4: return run<64, 4>(p, plan.triples, st);
-    case 96 * 8 + 1: return run<96, 1>(p, plan.triples, st);
-    case 96 * 8 + 2: return run<96, 2>(p, plan.triples, st);
-    case 128 * 8 + 1: return run<128, 1>(p, plan.triples, st);
-    case 128 * 8 + 2: return run<128, 2>(p, plan.triples, st);
-    case 192 * 8 + 1: return run<192, 1>(p, plan.triples, st);
-    case 192 * 8 + 2: return run<192, 2>(p, plan.triples, st);
-    case 256 * 8 + 1: return run<256, 1>(p, plan.triples, st);
-    case 384 * 8 + 1: return run<384, 1>(p, plan.triples, st);
+    case 64 * 8 + 1: return run<64, 1>(p, plan, st);
+    case 64 * 8 + 2: return run<64, 2>(p, plan, st);
+    case 64 * 8 + 4: return run<64, 4>(p, plan, st);
+    case 96 * 8 + 1: return run<96, 1>(p, plan, st);
+    case 96 * 8 + 2: return run<96, 2>(p, plan, st);
+    case 128 * 8 + 1: return run<128, 1>(p, plan, st);
+    case 128 * 8 + 2: return run<128, 2>(p, plan, st);
+    case 192 * 8 + 1: return run<192, 1>(p, plan, st);
+    case 192 * 8 + 2: return run<192, 2>(p, plan, st);
+    case 256 * 8 + 1: return run<256, 1>(p, plan, st);
+    case 384 * 8 + 1: return run<384, 1>(p, plan, st);
   }
   return FA_ERR_UNSUPPORTED;
 }

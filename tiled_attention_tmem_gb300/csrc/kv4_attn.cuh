@@ -156,6 +156,91 @@ __device__ __forceinline__ void kv4_advance(const Kv4AttnParams& p, const int* r
   } while (c.units == 0);
 }
 
+// Where each thread's run of requests begins in the sequence of units: prefix[i] units
+// lie before thread i's ceil(B / THREADS) requests, prefix[THREADS] in all.  `kept` takes
+// the requests themselves (tokens, first query, queries) if every thread has one at most.
+// `sums` has a word for each warp.  Ends with a barrier.
+template <class C>
+__device__ __forceinline__ long long kv4_scan(const Kv4AttnParams& p, long long* prefix, int* kept, long long* sums) {
+  const int warp = warp_id(), lane = lane_id();
+  const int run = (p.B + C::THREADS - 1) / C::THREADS;
+  const int b0 = min((int)threadIdx.x * run, p.B), b1 = min(b0 + run, p.B);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    Kv4Cursor c;
+    kv4_request<C>(p, nullptr, b, c);
+    if (run == 1 && kept) kept[3 * b] = c.n, kept[3 * b + 1] = c.tok0, kept[3 * b + 2] = c.nq;
+    sum += (long long)c.units * c.tiles * p.Hkv;
+  }
+  long long x = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < C::THREADS / 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  prefix[threadIdx.x] = before + x - sum;
+  if (threadIdx.x == 0) prefix[C::THREADS] = total;
+  __syncthreads();
+  return total;
+}
+
+// Sets c to unit x of the sequence.  False only if the lengths changed meanwhile.
+template <class C>
+__device__ __forceinline__ bool kv4_locate(const Kv4AttnParams& p, const long long* prefix, const int* req, long long x,
+                                           Kv4Cursor& c) {
+  const int run = (p.B + C::THREADS - 1) / C::THREADS;
+  int lo = 0, hi = C::THREADS;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  long long rest = x - prefix[lo];
+  for (c.b = lo * run; c.b < p.B; ++c.b) {
+    kv4_request<C>(p, req, c.b, c);
+    const long long mine = (long long)c.units * c.tiles * p.Hkv;
+    if (rest < mine) {
+      const int per_kvh = c.units * c.tiles;  // below 2^31: see the launcher
+      c.kvh = 0;
+      if (rest >= per_kvh) {
+        c.kvh = (int)(rest / per_kvh);
+        rest -= (long long)c.kvh * per_kvh;
+      }
+      c.rt = (int)rest / c.units;
+      c.u = (int)rest - c.rt * c.units;
+      return true;
+    }
+    rest -= mine;
+  }
+  return false;
+}
+
+// An even share of `total` units for each of `workers`: the first `more` take per + 1,
+// the others per.  worker_parts: over how many workers from `me` on a triple runs whose
+// last unit but `rest` more lies in me's share.
+struct Kv4Share {
+  long long x0;
+  int units, per, more;
+  __device__ __forceinline__ Kv4Share(long long total, int workers, int me) {
+    per = (int)min(total / workers, 0x7ffffffell);
+    more = (int)(total - (long long)per * workers);
+    x0 = (long long)per * me + min(me, more);
+    units = per + (me < more ? 1 : 0);
+  }
+  __device__ __forceinline__ int parts(int me, int rest) const {
+    const int wide = max(more - (me + 1), 0);  // of the workers after me, those that take per + 1
+    return 1 + (rest <= (long long)wide * (per + 1) ? (rest + per) / (per + 1)
+                                                    : wide + (rest - wide * (per + 1) + per - 1) / per);
+  }
+};
+
 // Bounded wait for a copy in flight that does not give up early on an abort.
 __device__ __forceinline__ void wait_done(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -236,9 +321,8 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
   const CtaAbort ab{abort_flag, p.err};
   const int* req = nullptr;  // the requests in shared memory, if they fit there
   Kv4Cursor cur;
-  int units = 0;                // of this warp
-  long long x0 = 0;             // its first unit in the sequence
-  int me = 0, per = 0, more = 0;
+  Kv4Share share(0, 1, 0);      // of this warp
+  int units = 0, me = 0;
   if constexpr (C::SOLO) {
     __syncthreads();  // (the barriers and the abort flag)
     if (skip) return;
@@ -252,73 +336,14 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
     units = max(cur.units - warp + C::WARPS - 1, 0) / C::WARPS;
     if (cur.units == 1 && warp > 0) return;  // one unit: its warp finishes the triple
   } else {
-  // Units before each thread's run of ceil(B / THREADS) requests, and in all.
-  const int run = (p.B + C::THREADS - 1) / C::THREADS;
-  req = run == 1 ? kept : nullptr;
-  {
-    const int b0 = min((int)threadIdx.x * run, p.B), b1 = min(b0 + run, p.B);
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      Kv4Cursor c;
-      kv4_request<C>(p, nullptr, b, c);
-      if (run == 1) kept[3 * b] = c.n, kept[3 * b + 1] = c.tok0, kept[3 * b + 2] = c.nq;
-      sum += (long long)c.units * c.tiles * p.Hkv;
-    }
-    long long x = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
-    }
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < C::WARPS; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
-    }
-    prefix[threadIdx.x] = before + x - sum;
-    if (threadIdx.x == 0) prefix[C::THREADS] = total;
-  }
-  __syncthreads();
+  const long long total = kv4_scan<C>(p, prefix, kept, sums);
   if (skip) return;
-  const long long total = prefix[C::THREADS];
-  // `more` warps take per + 1 units and the others per.  Neighbouring ranges go to
-  // different SMs, so that few units spread over all.
-  const int workers = gridDim.x * C::WARPS;
+  req = p.B <= C::THREADS ? kept : nullptr;
+  // Neighbouring ranges go to different SMs, so that few units spread over all.
   me = warp * gridDim.x + blockIdx.x;
-  per = (int)min(total / workers, 0x7ffffffell);
-  more = (int)(total - (long long)per * workers);
-  x0 = (long long)per * me + min(me, more);
-  units = per + (me < more ? 1 : 0);
-  auto locate = [&](long long x, Kv4Cursor& c) -> bool {
-    int lo = 0, hi = C::THREADS;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= x) lo = mid;
-      else hi = mid;
-    }
-    long long rest = x - prefix[lo];
-    for (c.b = lo * run; c.b < p.B; ++c.b) {
-      kv4_request<C>(p, req, c.b, c);
-      const long long mine = (long long)c.units * c.tiles * p.Hkv;
-      if (rest < mine) {
-        const int per_kvh = c.units * c.tiles;  // below 2^31: see the launcher
-        c.kvh = 0;
-        if (rest >= per_kvh) {
-          c.kvh = (int)(rest / per_kvh);
-          rest -= (long long)c.kvh * per_kvh;
-        }
-        c.rt = (int)rest / c.units;
-        c.u = (int)rest - c.rt * c.units;
-        return true;
-      }
-      rest -= mine;
-    }
-    return false;  // only if the lengths changed meanwhile
-  };
-
-  if (units == 0 || !locate(x0, cur)) return;
+  share = Kv4Share(total, gridDim.x * C::WARPS, me);
+  units = share.units;
+  if (units == 0 || !kv4_locate<C>(p, prefix, req, share.x0, cur)) return;
   }
   int left = units, ahead = units;  // still to compute and to copy (a SOLO warp may have none)
 
@@ -392,7 +417,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
   int stage = 0;
   uint32_t phase = 0;
   bool fresh = true;
-  long long began = x0 - cur.u;  // first unit of the current triple
+  long long began = share.x0 - cur.u;  // first unit of the current triple
 #pragma unroll 1
   for (; left > 0; --left) {
     if (fresh) {
@@ -649,19 +674,13 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
 
     const bool last_unit = !C::SOLO && cur.u == cur.units - 1;
     if (last_unit || left == 1) {
-      const bool first_here = began >= x0;  // the triple began in this warp's range
+      const bool first_here = began >= share.x0;  // the triple began in this warp's range
       const bool direct = C::SOLO ? cur.units == 1 : last_unit && first_here;
       // Slot 1: the triple begins in this range and goes on; slot 0: it began before.
       const size_t part = (size_t)me * 2 + (first_here ? 1 : 0);
       if (!C::SOLO && first_here && lane == 0) {
-        int count = 0;
-        if (!direct) {
-          // And the warps after this one that the rest of the triple goes to.
-          const int rest = (int)(began + cur.units - (x0 + units));
-          const int wide = max(more - (me + 1), 0);  // of them, those that take per + 1
-          count = 1 + (rest <= (long long)wide * (per + 1) ? (rest + per) / (per + 1)
-                                                           : wide + (rest - wide * (per + 1) + per - 1) / per);
-        }
+        // (and the warps after this one that the rest of the triple goes to)
+        const int count = direct ? 0 : share.parts(me, (int)(began + cur.units - (share.x0 + units)));
         p.cuts[((size_t)cur.b * p.Hkv + cur.kvh) * p.row_tiles + cur.rt] = make_int2(me, count);
       }
 #pragma unroll
