@@ -28,6 +28,27 @@ __host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, bool b_mn_ma
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// wait_warp for a warp that runs ahead of the others and mostly waits: it sleeps between
+// its looks, because a polling warp takes issue slots from the softmax warp on its
+// scheduler (measured: that warp took 2000 cycles a unit beside a polling one, 1000 without).
+template <int NS>
+__device__ __forceinline__ bool wait_asleep(uint32_t bar, uint32_t parity, const CtaAbort& ab, int where) {
+  bool ok = mbar_test(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    const long long t0 = clock64();
+    while (true) {
+      ok = mbar_test(bar, parity);
+      if (__all_sync(0xffffffffu, ok) || *ab.flag) break;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        raise_timeout(ab, where);
+        break;
+      }
+      __nanosleep(NS);
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 template <int D_>
 struct Kv4WideCfg {
   static constexpr int D = D_, ROWS = 128, UNIT = 64;
@@ -39,8 +60,10 @@ struct Kv4WideCfg {
   static constexpr int TILE = PANELS * PANEL;
   static constexpr bool QT = D <= 256;  // Q in TMEM
   static constexpr int Q_PANEL = ROWS * 128, Q_BYTES = QT ? 0 : PANELS * Q_PANEL;
-  static constexpr int TILES = D <= 192 ? 6 : D == 256 ? 4 : 2;   // operand slots
-  static constexpr int STAGED = D <= 128 ? 8 : D == 192 ? 6 : D == 256 ? 5 : 2;  // staging slots
+  // Operand slots few, staging slots many: what is on its way from memory has to cover its
+  // latency (measured at d = 128: MEASURE).
+  static constexpr int TILES = D <= 256 ? 4 : 2;
+  static constexpr int STAGED = D <= 128 ? 24 : D == 192 ? 16 : D == 256 ? 8 : 2;
   static constexpr int OFF_Q = TILES * TILE, OFF_STAGE = OFF_Q + Q_BYTES;
   static constexpr int OFF_BAR = OFF_STAGE + STAGED * PART;
   // Barriers: staging full and empty, operand full and empty, then S, P, O (two each), Q, done.
@@ -59,6 +82,9 @@ struct Kv4WideCfg {
   static constexpr int NPV = (OD + 255) / 256, PVN = OD / NPV;  // O += P V as NPV MMAs
   static_assert(TMEM_Q + (QT ? D / 2 : 0) <= 512 && SMEM <= 232448 && OFF_REQ % 8 == 0 && OFF_MISC % 8 == 0, "budgets");
   static_assert((STAGED + TILES) / 2 + 4 < 32, "units in flight");
+  // Slots belong to K or to V: a slot that alternated between the warps that convert them
+  // would let each miss every other phase of its barrier, which a parity cannot tell.
+  static_assert(TILES % 2 == 0 && STAGED % 2 == 0, "even rings");
 };
 
 template <class C>
@@ -79,8 +105,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int s = 0; s < C::STAGED; ++s) mbar_init(BAR(C::B_SFULL + s), 1), mbar_init(BAR(C::B_SEMPTY + s), C::CONVERT);
-    for (int s = 0; s < C::TILES; ++s) mbar_init(BAR(C::B_TFULL + s), C::CONVERT), mbar_init(BAR(C::B_TEMPTY + s), 1);
+    for (int s = 0; s < C::STAGED; ++s) mbar_init(BAR(C::B_SFULL + s), 1), mbar_init(BAR(C::B_SEMPTY + s), C::CONVERT / 2);
+    for (int s = 0; s < C::TILES; ++s) mbar_init(BAR(C::B_TFULL + s), C::CONVERT / 2), mbar_init(BAR(C::B_TEMPTY + s), 1);
     for (int b = 0; b < 2; ++b) mbar_init(BAR(C::B_S + b), 1), mbar_init(BAR(C::B_P + b), 4), mbar_init(BAR(C::B_O + b), 1);
     mbar_init(BAR(C::B_Q), 4);
     mbar_init(BAR(C::B_DONE), 1);
@@ -117,45 +143,54 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
     const int row_bytes = (lane & 1) ? C::SCALE_ROW : C::CODE_ROW;
     const uint32_t copy_bytes = (uint32_t)row_bytes << fr_log2;
     const uint32_t copy_dst = base + C::OFF_STAGE + ((lane & 1) ? C::OFF_SCALE : 0) + frag * copy_bytes;
-    auto page_of = [&]() -> int {
-      const long long tok = (long long)cur.u * UNIT + ((long long)frag << fr_log2);
-      const int col = (int)(tok >> p.page_log2);
-      if (frag >= (UNIT >> fr_log2) || tok >= cur.n || col >= p.width) return -1;
-      const int id = p.table[(size_t)cur.b * p.width + col];
-      return (unsigned)id < (unsigned)p.pages ? id : -1;
+    // The page ids are read AHEAD units before their copies (one warp serves the block: a
+    // table read in every step would set its pace); `cur` runs that far ahead.
+    constexpr int AHEAD = 4;
+    int ids[AHEAD], heads[AHEAD], firsts[AHEAD], left = units;
+    auto look_up = [&](int k) {
+      ids[k] = -1;
+      heads[k] = cur.kvh;
+      firsts[k] = cur.u * UNIT + (frag << fr_log2);
+      if (left <= 0) return;
+      const int col = firsts[k] >> p.page_log2;
+      if (frag < (UNIT >> fr_log2) && firsts[k] < cur.n && col < p.width) ids[k] = p.table[(size_t)cur.b * p.width + col];
+      if (--left > 0) kv4_advance<C>(p, req, cur);
     };
-    int next_id = units > 0 ? page_of() : -1;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) look_up(k);
     int seq = 0, slot = 0;
     uint32_t parity = 1;
     bool ok = true;
-    for (int u = 0; u < units && ok; ++u) {
-      const int id = next_id;
-      const uint32_t have = __ballot_sync(0xffffffffu, id >= 0 && !(lane & 1));
-      const uint32_t bits = (have & 1u) | ((have >> 1) & 2u) | ((have >> 2) & 4u) | ((have >> 3) & 8u);
-      const uint32_t bytes = (uint32_t)(__popc(bits) << fr_log2) * (C::CODE_ROW + C::SCALE_ROW);
-      const uint32_t in_page = (uint32_t)((cur.u * UNIT + (frag << fr_log2)) & ((1 << p.page_log2) - 1));
-      const long long off = ((((long long)id * p.Hkv + cur.kvh) << p.page_log2) + in_page) * row_bytes;
-      if (u + 1 < units) {
-        kv4_advance<C>(p, req, cur);
-        next_id = page_of();
-      }
-      for (int kv = 0; kv < 2; ++kv) {
-        if (!wait_warp(BAR(C::B_SEMPTY + slot), parity, ab, (kKKv4 << 8) | 8)) {
-          ok = false;
-          break;
-        }
-        const uint32_t bar = BAR(C::B_SFULL + slot);
-        if (lane == 0) {
-          unit_bits[u & 31] = (uint8_t)bits;
-          mbar_expect_tx(bar, bytes);
-        }
-        __syncwarp();
-        if (id >= 0)
-          bulk_load(copy_dst + slot * C::PART, ((lane & 1) ? p.scales[kv] : p.codes[kv]) + off, copy_bytes, bar);
-        ++seq;
-        if (++slot == C::STAGED) {
-          slot = 0;
-          parity ^= 1;
+    for (int u0 = 0; u0 < units && ok; u0 += AHEAD) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int u = u0 + k;
+        if (u >= units || !ok) break;
+        const int id = (unsigned)ids[k] < (unsigned)p.pages ? ids[k] : -1;
+        const uint32_t have = __ballot_sync(0xffffffffu, id >= 0 && !(lane & 1));
+        const uint32_t bits = (have & 1u) | ((have >> 1) & 2u) | ((have >> 2) & 4u) | ((have >> 3) & 8u);
+        const uint32_t bytes = (uint32_t)(__popc(bits) << fr_log2) * (C::CODE_ROW + C::SCALE_ROW);
+        const long long off =
+            ((((long long)id * p.Hkv + heads[k]) << p.page_log2) + (firsts[k] & ((1 << p.page_log2) - 1))) * row_bytes;
+        look_up(k);
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!wait_asleep<400>(BAR(C::B_SEMPTY + slot), parity, ab, (kKKv4 << 8) | 8)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = BAR(C::B_SFULL + slot);
+          if (lane == 0) {
+            unit_bits[u & 31] = (uint8_t)bits;
+            mbar_expect_tx(bar, bytes);
+          }
+          __syncwarp();
+          if (id >= 0)
+            bulk_load(copy_dst + slot * C::PART, ((lane & 1) ? p.scales[kv] : p.codes[kv]) + off, copy_bytes, bar);
+          ++seq;
+          if (++slot == C::STAGED) {
+            slot = 0;
+            parity ^= 1;
+          }
         }
       }
     }
@@ -189,8 +224,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
           mma_ss(tmem + C::TMEM_S + (u & 1) * UNIT, desc_kmajor(base + C::OFF_Q, C::Q_PANEL, 16 * k),
                  desc_kmajor(kb, C::PANEL, 16 * k), idS, k > 0 ? 1u : 0u);
       }
-      mma_commit(BAR(C::B_S + (u & 1)));
-      mma_commit(BAR(C::B_TEMPTY + s));
+      mma_commit(BAR(C::B_S + (u & 1)));  // (the softmax warps hand K's slot back)
       return true;
     };
     int triple = 0;
@@ -229,13 +263,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
     // An item is 16 packed bytes of a token, 32 channels: four 16-byte chunks of half a
     // panel row.  Lanes take neighbouring bytes, and the order in which a lane writes its
     // chunks depends on its panel, so that eight lanes write eight chunk positions.
-    constexpr int NQ = D / 32, ITEMS = UNIT * NQ, T = 32 * C::CONVERT;
-    const int tid = threadIdx.x - 128;
-    int stage = 0, tile = 0;
+    // Half of the warps convert K, the others V, so that the latencies of the two overlap.
+    constexpr int NQ = D / 32, ITEMS = UNIT * NQ, T = 16 * C::CONVERT;
+    const int tid = (threadIdx.x - 128) % T;
+    int stage = (threadIdx.x - 128) / T, tile = stage;
     uint32_t stage_phase = 0, tile_parity = 1;
-    for (int i = 0; i < 2 * units; ++i) {
-      if (!wait_warp(BAR(C::B_SFULL + stage), stage_phase, ab, (kKKv4 << 8) | 13)) break;
-      if (!wait_warp(BAR(C::B_TEMPTY + tile), tile_parity, ab, (kKKv4 << 8) | 14)) break;
+    for (int u = 0; u < units; ++u) {
+      if (!wait_asleep<20>(BAR(C::B_SFULL + stage), stage_phase, ab, (kKKv4 << 8) | 13)) break;
+      if (!wait_asleep<20>(BAR(C::B_TEMPTY + tile), tile_parity, ab, (kKKv4 << 8) | 14)) break;
       const uint8_t* src = smem + C::OFF_STAGE + stage * C::PART;
       uint8_t* dst = smem + tile * C::TILE;
 #pragma unroll
@@ -274,12 +309,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
         mbar_arrive(BAR(C::B_TFULL + tile));
         mbar_arrive(BAR(C::B_SEMPTY + stage));
       }
-      if (++stage == C::STAGED) {
-        stage = 0;
+      if ((stage += 2) >= C::STAGED) {
+        stage -= C::STAGED;
         stage_phase ^= 1;
       }
-      if (++tile == C::TILES) {
-        tile = 0;
+      if ((tile += 2) >= C::TILES) {
+        tile -= C::TILES;
         tile_parity ^= 1;
       }
     }
@@ -290,43 +325,50 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
     const uint32_t all_bits = (1u << (UNIT >> fr_log2)) - 1u;
     // Query row r of the cursor's triple as f16, scaled by a power of two into f16's range
     // (zeros past the last row); returns the factor that takes scores to the log2 domain.
+    auto exponent = [](uint32_t top) -> int { return min(max((int)(top >> 7) - 127, -120), 120); };
     auto write_q = [&]() -> float {
       const int row = cur.rt * C::ROWS + r;
       const int i = row / p.G, h = row - i * p.G;
       const bool have = i < cur.nq;
       const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(cur.tok0 + (have ? i : 0)) * p.q_token +
                                                         (long long)(cur.kvh * p.G + h) * p.q_head);
+      // 64 channels at a time with all their loads in flight; twice, first for the largest
+      // magnitude (as bf16 bits), which gives the power of two.
       uint32_t top = 0;
-      if (have) {
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = src[c];
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-        }
-      }
-      const int e = min(max((int)(top >> 7) - 127, -120), 120);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      float down = 0.f;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t qw[16];
+      for (int c0 = 0; c0 < 2 * D; c0 += (D % 64 ? 32 : 64)) {
+        constexpr int N = D % 64 ? 4 : 8;  // loads of eight channels
+        const int c = c0 < D ? c0 : c0 - D;
+        uint4 x[N];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (have) x = src[c0 / 8 + u];
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int u = 0; u < N; ++u) x[u] = have ? src[c / 8 + u] : make_uint4(0u, 0u, 0u, 0u);
+        if (c0 == D) down = __uint_as_float((uint32_t)(127 - exponent(top)) << 23);
+        uint32_t qw[4 * N];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+        for (int u = 0; u < N; ++u) {
+          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (c0 < D) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
             qw[4 * u + k] = pack_f16(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-          if constexpr (!C::QT) {
-            const int chunk = c0 / 8 + u;
+          }
+        }
+        if (c0 < D) continue;
+        if constexpr (C::QT) {
+          __syncwarp();
+          if constexpr (N == 8)
+            tmem_st_32x32b_x32(trow + C::TMEM_Q + (c >> 1), qw);
+          else
+            tmem_st_32x32b_x16(trow + C::TMEM_Q + (c >> 1), qw);
+        } else {
+#pragma unroll
+          for (int u = 0; u < N; ++u) {
+            const int chunk = c / 8 + u;
             *reinterpret_cast<uint4*>(smem + C::OFF_Q + (chunk >> 3) * C::Q_PANEL + r * 128 + ((chunk & 7) ^ (r & 7)) * 16) =
                 make_uint4(qw[4 * u], qw[4 * u + 1], qw[4 * u + 2], qw[4 * u + 3]);
           }
         }
-        __syncwarp();
-        if constexpr (C::QT) tmem_st_32x32b_x16(trow + C::TMEM_Q + (c0 >> 1), qw);
       }
       if constexpr (C::QT) {
         tmem_wait_st();
@@ -336,7 +378,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::B_Q));
-      return fmaxf(__uint_as_float((uint32_t)(127 + e) << 23) * p.score, 1e-37f);
+      return fmaxf(__uint_as_float((uint32_t)(127 + exponent(top)) << 23) * p.score, 1e-37f);
+    };
+    // O with unit u added.  S runs one unit ahead, so a barrier for every other unit cannot
+    // be two phases ahead of its waiter.
+    auto wait_o = [&](int u) -> bool {
+      return wait_warp(BAR(C::B_O + (u & 1)), (u >> 1) & 1, ab, (kKKv4 << 8) | 16);
     };
     float fac = units > 0 ? write_q() : 0.f;
     int g = 0;
@@ -352,7 +399,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
       const int i = row / p.G, h = kvh * p.G + row - i * p.G;
       const bool have = i < nq;
       const bool busy = __any_sync(0xffffffffu, have);  // a warp past the last row only keeps pace
-      const int lim = have ? cur.n - nq + i : -1;
+      // (A row past the last sees everything: its zeros cost no masking, and are not stored.)
+      const int lim = have ? cur.n - nq + i : 0x7fffffff;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++g) {
         const uint32_t tS = trow + C::TMEM_S + (g & 1) * UNIT;
@@ -361,6 +409,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
           break;
         }
         tc_fence_after();
+        if (threadIdx.x == 0) mbar_arrive(BAR(C::B_TEMPTY + (2 * g) % C::TILES));
         if (busy) {
           uint32_t sr[UNIT];
           tmem_ld_32x32b_x32(tS, sr);
@@ -402,7 +451,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
           tmem_wait_st();
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
             // The running O, once the MMA that added to it last is done.
-            if (!wait_warp(BAR(C::B_O + ((g - 1) & 1)), ((g - 1) >> 1) & 1, ab, (kKKv4 << 8) | 16)) {
+            if (!wait_o(g - 1)) {
               ok = false;
               break;
             }
@@ -430,7 +479,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
         skip_run(n);
         fac = write_q();
       }
-      if (!wait_warp(BAR(C::B_O + ((g - 1) & 1)), ((g - 1) >> 1) & 1, ab, (kKKv4 << 8) | 17)) {
+      if (!wait_o(g - 1)) {
         ok = false;
         break;
       }
