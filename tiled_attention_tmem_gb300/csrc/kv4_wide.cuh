@@ -11,7 +11,7 @@
 //   warps 0-3    softmax: thread r owns row r (TMEM lane r) of the tile
 //   warps 4-11   conversion: packed K and V of a unit to 128-byte-swizzled panels
 //   warp 12      TMEM allocation and MMA issue, in the order S(0) S(1) PV(0) S(2) PV(1) ..
-//   warp 13      bulk copies of packed K and V into a ring of staging slots
+//   warps 13, 14 bulk copies of packed K and of V into a ring of staging slots
 //
 // A block takes an even share of the units of all (request, kv head, row tile) triples and
 // leaves a part per cut triple, as a warp does there; kv4_merge_kernel joins them.
@@ -29,41 +29,36 @@ __host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, bool b_mn_ma
 }
 
 // wait_warp for a warp that runs ahead of the others and mostly waits: it sleeps between
-// its looks, because a polling warp takes issue slots from the softmax warp on its
-// scheduler (measured: that warp took 2000 cycles a unit beside a polling one, 1000 without).
+// its looks, so that its polling takes no issue slots from the softmax warp on its
+// scheduler.
 template <int NS>
 __device__ __forceinline__ bool wait_asleep(uint32_t bar, uint32_t parity, const CtaAbort& ab, int where) {
-  bool ok = mbar_test(bar, parity);
-  if (!__all_sync(0xffffffffu, ok)) {
-    const long long t0 = clock64();
-    while (true) {
-      ok = mbar_test(bar, parity);
-      if (__all_sync(0xffffffffu, ok) || *ab.flag) break;
-      if (clock64() - t0 > kWaitLimitCycles) {
-        raise_timeout(ab, where);
-        break;
-      }
-      __nanosleep(NS);
-    }
+  const long long t0 = clock64();
+  while (true) {
+    const bool ok = mbar_test(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    // (Lanes agree on the end: one that left alone would leave the others in the vote.)
+    const bool late = clock64() - t0 > kWaitLimitCycles;
+    if (late) raise_timeout(ab, where);
+    if (__any_sync(0xffffffffu, late || *ab.flag)) return false;
+    __nanosleep(NS);
   }
-  return __all_sync(0xffffffffu, ok);
 }
 
 template <int D_>
 struct Kv4WideCfg {
   static constexpr int D = D_, ROWS = 128, UNIT = 64;
   static constexpr int CONVERT = 8;  // warps
-  static constexpr int MMA_WARP = 4 + CONVERT, COPY_WARP = MMA_WARP + 1, THREADS = 32 * (COPY_WARP + 1);
+  static constexpr int MMA_WARP = 4 + CONVERT, COPY_WARP = MMA_WARP + 1, THREADS = 32 * (COPY_WARP + 2);
   static constexpr int CODE_ROW = D / 2, SCALE_ROW = D / 16;
   static constexpr int OFF_SCALE = UNIT * CODE_ROW, PART = UNIT * (CODE_ROW + SCALE_ROW);
   static constexpr int PANELS = (D + 63) / 64, PANEL = UNIT * 128;  // operand panels of 64 channels
   static constexpr int TILE = PANELS * PANEL;
   static constexpr bool QT = D <= 256;  // Q in TMEM
   static constexpr int Q_PANEL = ROWS * 128, Q_BYTES = QT ? 0 : PANELS * Q_PANEL;
-  // Operand slots few, staging slots many: what is on its way from memory has to cover its
-  // latency (measured at d = 128: MEASURE).
-  static constexpr int TILES = D <= 256 ? 4 : 2;
-  static constexpr int STAGED = D <= 128 ? 24 : D == 192 ? 16 : D == 256 ? 8 : 2;
+  // Operand slots few, staging slots many: what is on its way has to cover memory's latency.
+  static constexpr int TILES = D <= 128 ? 6 : D <= 256 ? 4 : 2;
+  static constexpr int STAGED = D <= 128 ? 22 : D == 192 ? 16 : D == 256 ? 8 : 2;
   static constexpr int OFF_Q = TILES * TILE, OFF_STAGE = OFF_Q + Q_BYTES;
   static constexpr int OFF_BAR = OFF_STAGE + STAGED * PART;
   // Barriers: staging full and empty, operand full and empty, then S, P, O (two each), Q, done.
@@ -137,14 +132,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
   };
   const int fr_log2 = min(p.page_log2, 6);
 
-  if (warp == C::COPY_WARP) {
+  if (warp >= C::COPY_WARP) {
     // ------------------------------------------------------------------ copies
+    // One warp copies K, the other V: a unit's slot costs a warp some 600 cycles of
+    // instructions, and both by one warp set the block's pace.  The page ids are read AHEAD
+    // units before their copies; `cur` runs that far ahead.
+    const int kv = warp - C::COPY_WARP;
     const int frag = lane >> 1;
     const int row_bytes = (lane & 1) ? C::SCALE_ROW : C::CODE_ROW;
     const uint32_t copy_bytes = (uint32_t)row_bytes << fr_log2;
     const uint32_t copy_dst = base + C::OFF_STAGE + ((lane & 1) ? C::OFF_SCALE : 0) + frag * copy_bytes;
-    // The page ids are read AHEAD units before their copies (one warp serves the block: a
-    // table read in every step would set its pace); `cur` runs that far ahead.
+    const uint8_t* const array = (lane & 1) ? p.scales[kv] : p.codes[kv];
     constexpr int AHEAD = 4;
     int ids[AHEAD], heads[AHEAD], firsts[AHEAD], left = units;
     auto look_up = [&](int k) {
@@ -158,7 +156,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
     };
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) look_up(k);
-    int seq = 0, slot = 0;
+    int issued = 0, slot = kv;
     uint32_t parity = 1;
     bool ok = true;
     for (int u0 = 0; u0 < units && ok; u0 += AHEAD) {
@@ -169,89 +167,95 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
         const int id = (unsigned)ids[k] < (unsigned)p.pages ? ids[k] : -1;
         const uint32_t have = __ballot_sync(0xffffffffu, id >= 0 && !(lane & 1));
         const uint32_t bits = (have & 1u) | ((have >> 1) & 2u) | ((have >> 2) & 4u) | ((have >> 3) & 8u);
-        const uint32_t bytes = (uint32_t)(__popc(bits) << fr_log2) * (C::CODE_ROW + C::SCALE_ROW);
-        const long long off =
-            ((((long long)id * p.Hkv + heads[k]) << p.page_log2) + (firsts[k] & ((1 << p.page_log2) - 1))) * row_bytes;
+        const uint8_t* src =
+            array + ((((long long)id * p.Hkv + heads[k]) << p.page_log2) + (firsts[k] & ((1 << p.page_log2) - 1))) * row_bytes;
         look_up(k);
-        for (int kv = 0; kv < 2; ++kv) {
-          if (!wait_asleep<400>(BAR(C::B_SEMPTY + slot), parity, ab, (kKKv4 << 8) | 8)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = BAR(C::B_SFULL + slot);
-          if (lane == 0) {
-            unit_bits[u & 31] = (uint8_t)bits;
-            mbar_expect_tx(bar, bytes);
-          }
-          __syncwarp();
-          if (id >= 0)
-            bulk_load(copy_dst + slot * C::PART, ((lane & 1) ? p.scales[kv] : p.codes[kv]) + off, copy_bytes, bar);
-          ++seq;
-          if (++slot == C::STAGED) {
-            slot = 0;
-            parity ^= 1;
-          }
+        if (!wait_asleep<200>(BAR(C::B_SEMPTY + slot), parity, ab, (kKKv4 << 8) | 8)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = BAR(C::B_SFULL + slot);
+        if (lane == 0) {
+          if (kv == 0) unit_bits[u & 31] = (uint8_t)bits;
+          mbar_expect_tx(bar, (uint32_t)(__popc(bits) << fr_log2) * (C::CODE_ROW + C::SCALE_ROW));
+        }
+        __syncwarp();
+        if (id >= 0) bulk_load(copy_dst + slot * C::PART, src, copy_bytes, bar);
+        ++issued;
+        if ((slot += 2) >= C::STAGED) {
+          slot = kv;
+          parity ^= 1;
         }
       }
     }
     // Every copy lands before the block can exit.
-    for (int i = max(seq - C::STAGED, 0); i < seq; ++i)
-      wait_done(BAR(C::B_SFULL + i % C::STAGED), (uint32_t)((i / C::STAGED) & 1));
+    constexpr int OWN = C::STAGED / 2;
+    for (int i = max(issued - OWN, 0); i < issued; ++i)
+      wait_done(BAR(C::B_SFULL + 2 * (i % OWN) + kv), (uint32_t)((i / OWN) & 1));
   } else if (warp == C::MMA_WARP) {
     // --------------------------------------------------------------------- MMAs
     constexpr uint32_t idS = make_idesc_f16(128, UNIT, false);
     constexpr uint32_t idO = make_idesc_f16(128, C::PVN, true);
+    // One warp's instructions pace the block here, so the loops run on uniform registers:
+    // their bounds come out of a warp reduction (which the compiler knows to be uniform), the
+    // slots are counted instead of divided out, and the descriptors differ by additions.
+    auto uniform = [](int x) -> int { return (int)__reduce_max_sync(0xffffffffu, (unsigned)x); };
+    const uint64_t k_desc = desc_kmajor(base, C::PANEL, 0), v_desc = desc_mnmajor(base, C::PANEL, 0);
+    const uint64_t q_desc = desc_kmajor(base + C::OFF_Q, C::Q_PANEL, 0);
     bool ok = true;
-    int g = 0;
-    // The operand tiles in the order of their use: K and V of a unit are neighbours in the
-    // ring, and S runs a unit ahead.
-    auto tile_of = [&](int s, uint32_t& bar_phase) -> int {
-      bar_phase = (uint32_t)((s / C::TILES) & 1);
-      return s % C::TILES;
-    };
-    auto issue_s = [&](int u) -> bool {
-      uint32_t ph;
-      const int s = tile_of(2 * u, ph);
-      if (!wait_warp(BAR(C::B_TFULL + s), ph, ab, (kKKv4 << 8) | 9)) return false;
+    int g = 0;  // the unit of the next PV; S runs one ahead
+    int k_slot = 0, v_slot = 1;
+    uint32_t k_phase = 0, v_phase = 0;
+    auto issue_s = [&](int buffer) -> bool {
+      if (!wait_warp(BAR(C::B_TFULL + k_slot), k_phase, ab, (kKKv4 << 8) | 9)) return false;
       tc_fence_after();
-      const uint32_t kb = base + s * C::TILE;
+      const uint64_t kd = sdesc_advance(k_desc, (uint32_t)k_slot * (C::TILE >> 4));
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
+        // 16 channels on: 32 bytes in a panel row, or the next panel.
+        const uint64_t b = sdesc_advance(kd, (uint32_t)((k >> 2) * C::PANEL + (k & 3) * 32) >> 4);
         if constexpr (C::QT)
-          mma_ts(tmem + C::TMEM_S + (u & 1) * UNIT, tmem + C::TMEM_Q + 8 * k, desc_kmajor(kb, C::PANEL, 16 * k), idS,
-                 k > 0 ? 1u : 0u);
+          mma_ts(tmem + C::TMEM_S + buffer * UNIT, tmem + C::TMEM_Q + 8 * k, b, idS, k > 0 ? 1u : 0u);
         else
-          mma_ss(tmem + C::TMEM_S + (u & 1) * UNIT, desc_kmajor(base + C::OFF_Q, C::Q_PANEL, 16 * k),
-                 desc_kmajor(kb, C::PANEL, 16 * k), idS, k > 0 ? 1u : 0u);
+          mma_ss(tmem + C::TMEM_S + buffer * UNIT,
+                 sdesc_advance(q_desc, (uint32_t)((k >> 2) * C::Q_PANEL + (k & 3) * 32) >> 4), b, idS, k > 0 ? 1u : 0u);
       }
-      mma_commit(BAR(C::B_S + (u & 1)));  // (the softmax warps hand K's slot back)
+      mma_commit(BAR(C::B_S + buffer));  // (the softmax warps hand K's slot back)
+      if ((k_slot += 2) >= C::TILES) {
+        k_slot = 0;
+        k_phase ^= 1;
+      }
       return true;
     };
     int triple = 0;
-    for (int left = units; left > 0 && ok; ++triple) {
-      const int n = run_of(left);
+    for (int left = uniform(units); left > 0 && ok; ++triple) {
+      const int n = uniform(run_of(left));
       left -= n;
       if (left > 0) skip_run(n);
       ok = wait_warp(BAR(C::B_Q), triple & 1, ab, (kKKv4 << 8) | 10);
       if (ok) tc_fence_after();
-      ok = ok && issue_s(g);
+      ok = ok && issue_s(g & 1);
       for (int j = 0; j < n && ok; ++j, ++g) {
-        if (j + 1 < n && !(ok = issue_s(g + 1))) break;
-        uint32_t ph;
-        const int s = tile_of(2 * g + 1, ph);
-        ok = wait_warp(BAR(C::B_P + (g & 1)), (g >> 1) & 1, ab, (kKKv4 << 8) | 11) &&
-             wait_warp(BAR(C::B_TFULL + s), ph, ab, (kKKv4 << 8) | 12);
+        const int buffer = g & 1;
+        if (j + 1 < n && !(ok = issue_s(buffer ^ 1))) break;
+        ok = wait_warp(BAR(C::B_P + buffer), (g >> 1) & 1, ab, (kKKv4 << 8) | 11) &&
+             wait_warp(BAR(C::B_TFULL + v_slot), v_phase, ab, (kKKv4 << 8) | 12);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t vb = base + s * C::TILE;
+        const uint64_t vd = sdesc_advance(v_desc, (uint32_t)v_slot * (C::TILE >> 4));
 #pragma unroll
         for (int k = 0; k < UNIT / 16; ++k)
 #pragma unroll
           for (int c = 0; c < C::NPV; ++c)
-            mma_ts(tmem + C::TMEM_O + c * C::PVN, tmem + C::TMEM_S + (g & 1) * UNIT + 8 * k,
-                   desc_mnmajor(vb + c * (C::PVN / 64) * C::PANEL, C::PANEL, 16 * k), idO, (j > 0 || k > 0) ? 1u : 0u);
-        mma_commit(BAR(C::B_O + (g & 1)));
-        mma_commit(BAR(C::B_TEMPTY + s));
+            mma_ts(tmem + C::TMEM_O + c * C::PVN, tmem + C::TMEM_S + buffer * UNIT + 8 * k,
+                   sdesc_advance(vd, (uint32_t)(c * (C::PVN / 64) * C::PANEL + k * 2048) >> 4), idO,
+                   (j > 0 || k > 0) ? 1u : 0u);
+        mma_commit(BAR(C::B_O + buffer));
+        mma_commit(BAR(C::B_TEMPTY + v_slot));
+        if ((v_slot += 2) >= C::TILES) {
+          v_slot = 1;
+          v_phase ^= 1;
+        }
       }
     }
     // Every MMA issued above finishes before TMEM is released.
@@ -273,12 +277,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
       if (!wait_asleep<20>(BAR(C::B_TEMPTY + tile), tile_parity, ab, (kKKv4 << 8) | 14)) break;
       const uint8_t* src = smem + C::OFF_STAGE + stage * C::PART;
       uint8_t* dst = smem + tile * C::TILE;
+      // (All of a thread's reads first: the compiler cannot move them over the writes.)
+      constexpr int MINE = (ITEMS + T - 1) / T;
+      uint4 packed[MINE];
+      uint32_t scale[MINE];
 #pragma unroll
-      for (int it = tid; it < ITEMS; it += T) {
+      for (int k = 0; k < MINE; ++k) {
+        const int it = min(tid + k * T, ITEMS - 1);
         const int tok = it / NQ, q = it - tok * NQ;
-        uint4 c = *reinterpret_cast<const uint4*>(src + tok * C::CODE_ROW + q * 16);
-        const uint32_t sc = *reinterpret_cast<const uint16_t*>(src + C::OFF_SCALE + tok * C::SCALE_ROW + 2 * q);
-        uint32_t s0 = kv4_scale_both(sc), s1 = kv4_scale_both(sc >> 8);
+        packed[k] = *reinterpret_cast<const uint4*>(src + tok * C::CODE_ROW + q * 16);
+        scale[k] = *reinterpret_cast<const uint16_t*>(src + C::OFF_SCALE + tok * C::SCALE_ROW + 2 * q);
+      }
+#pragma unroll
+      for (int k0 = 0; k0 < MINE; ++k0) {
+        const int it = tid + k0 * T;
+        if (it >= ITEMS) break;
+        const int tok = it / NQ, q = it - tok * NQ;
+        const uint4 c = packed[k0];
+        uint32_t s0 = kv4_scale_both(scale[k0]), s1 = kv4_scale_both(scale[k0] >> 8);
         const int turn = NQ == 4 ? 2 * (q >> 1) : (q >> 1) & 3;
         uint32_t w[4] = {c.x, c.y, c.z, c.w};
         if (turn & 2) {
