@@ -305,10 +305,10 @@ def test_attention_many_rows_cut_over_all_blocks(d, page, lengths):
 def test_attention_many_rows_skips_bad_pages_and_foreign_rows():
     import torch
     lengths = [2000, 1500]
-    arrays, table, cu, q, gains = _problem(128, 16, 16, 1, lengths, [3, 2], seed=61, pad=2)
+    arrays, table, cu, q, gains = _problem(128, 16, 24, 1, lengths, [3, 2], seed=61, pad=2)
     table[0, 3], table[0, 60], table[1, 0], table[1, 17] = -1, 10 ** 6, len(arrays[0]), -9
-    o = torch.full((7, 16, 128), 7.0, dtype=torch.bfloat16, device="cuda:0")
-    lse = torch.full((7, 16), 7.0, device="cuda:0")
+    o = torch.full((7, 24, 128), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    lse = torch.full((7, 24), 7.0, device="cuda:0")
     _attend((arrays, table, cu, q, gains), lengths, 3, out=o, lse=lse)
     assert torch.all(o[5:] == 7) and torch.all(lse[5:] == 7)
 
@@ -317,12 +317,12 @@ def test_attention_many_rows_keeps_nan_in_its_row():
     import torch
     from tiled_attention_tmem_gb300 import api
     lengths = [3000, 900]
-    arrays, table, cu, q, gains = _problem(128, 64, 24, 1, lengths, [2, 1], seed=67)
+    arrays, table, cu, q, gains = _problem(128, 64, 40, 1, lengths, [2, 1], seed=67)
     x, cache = to_dev(q), _cache_of(arrays, gains)
     clean, _ = api.kv4_attention(x, cache, _i32(table), _i32(lengths), _i32(cu), 2)
     x[0, 1, 5], x[2, 20, 0] = float("nan"), float("inf")
     got, lse = api.kv4_attention(x, cache, _i32(table), _i32(lengths), _i32(cu), 2)
-    bad = torch.zeros((3, 24), dtype=torch.bool, device="cuda:0")
+    bad = torch.zeros((3, 40), dtype=torch.bool, device="cuda:0")
     bad[0, 1] = bad[2, 20] = True
     assert torch.all(torch.isnan(got[bad])) and torch.all(torch.isnan(lse[bad]))
     assert torch.equal(got[~bad], clean[~bad])

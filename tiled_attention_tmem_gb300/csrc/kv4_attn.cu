@@ -25,10 +25,13 @@ int choose_nt(int d, long long rows) {
 // The tcgen05 kernel takes a call whose rows would need several narrow tiles, each of
 // which reads and converts the units again (its own time hardly depends on the rows).
 // Measured in us (narrow / wide) over 8 requests up to 8192 tokens, 8 kv heads: d = 128
-// with 32, 64, 128 rows 37 / 50, 54 / 49, 85 / 55; d = 64 with 64 rows 34 / 44; d = 192 with
-// 32 rows 54 / 64; one request of 32382 tokens, 16 kv heads, d = 256, 28 rows 124 / 74; of
-// 34617 tokens, 4 kv heads, d = 384, 64 rows 107 / 71.
-bool use_wide(int d, long long rows) { return rows > 8 * most_nt(d); }
+// with 32, 48, 64, 128 rows 37 / 50, 45 / 42, 54 / 49, 85 / 55; d = 64 with 64, 128 rows
+// 34 / 42, 53 / 45; d = 192 with 32, 48 rows 54 / 62, 69 / 54; over 4096 tokens, d = 256 with
+// 24 rows 37 / 44, and 28 rows of one request of 32382 tokens 124 / 74; one request of
+// 34617 tokens, 4 kv heads, d = 384, 64 rows 107 / 67; 2 of 16384, d = 128, 512 rows 111 / 51.
+bool use_wide(int d, long long rows) {
+  return rows > 8 * most_nt(d) * (d == 192 ? 2 : d == 384 ? 5 : 3);
+}
 
 // Tiles and triples of the two kernels, and the workspace for either.
 struct Plan {

@@ -15,9 +15,10 @@
 //
 // A block takes an even share of the units of all (request, kv head, row tile) triples and
 // leaves a part per cut triple, as a warp does there; kv4_merge_kernel joins them.
-// Bounds per 64 tokens at d = 128 (cycles an SM): reading 410, shared memory 580 (32 KB of
-// operands written and read, and the packed bytes), exponentials 4 a row (512 at 128
-// rows), MMAs 256.
+// What bounds it now, in cycles per 64 tokens at d = 128 (floors: reading 410, MMAs 510,
+// exponentials 4 a row): the softmax warps, 1070 of work and 490 of hand-over between
+// units; conversion takes 800 a tile beside it, and the MMA warp sees a probability tile
+// 450 after it is written.
 #pragma once
 #include "kv4_attn.cuh"
 
@@ -134,9 +135,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
 
   if (warp >= C::COPY_WARP) {
     // ------------------------------------------------------------------ copies
-    // One warp copies K, the other V: a unit's slot costs a warp some 600 cycles of
-    // instructions, and both by one warp set the block's pace.  The page ids are read AHEAD
-    // units before their copies; `cur` runs that far ahead.
+    // One warp copies K, the other V.  The page ids are read AHEAD units before their
+    // copies; `cur` runs that far ahead.
     const int kv = warp - C::COPY_WARP;
     const int frag = lane >> 1;
     const int row_bytes = (lane & 1) ? C::SCALE_ROW : C::CODE_ROW;
