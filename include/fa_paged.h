@@ -122,8 +122,12 @@ fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_toke
                       float scale, void* o, long long o_token, long long o_head, float* lse, void* workspace,
                       size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace fa_kv4_attn needs on the current device; 0 for invalid shapes. */
-size_t fa_kv4_attn_workspace_size(int B, int H, int Hkv, int d, int max_q);
+/*
+ * Bytes of workspace fa_kv4_attn needs on the current device (fp32 partial results
+ * of requests that several SMs share); 0 where it needs none (few tokens: `workspace`
+ * may be NULL) and for invalid shapes.  max_q: 1 where `cu` is NULL.
+ */
+size_t fa_kv4_attn_workspace_size(int B, int H, int Hkv, int d, int max_q, int page, int width);
 
 #ifdef __cplusplus
 }

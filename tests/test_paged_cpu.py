@@ -103,13 +103,17 @@ def test_attention_validation():
         assert call(**bad) == b.FA_ERR_UNSUPPORTED, bad
     for bad in (dict(q=A + 8), dict(o=A + 4), dict(vc=A + 2), dict(qt=1028), dict(qh=4), dict(ot=1), dict(oh=2)):
         assert call(**bad) == b.FA_ERR_MISALIGNED, bad
-    need = b.fa_kv4_attn_workspace_size(2, 8, 2, 128, 1)
+    # Few tokens need no workspace, many do.
+    assert b.fa_kv4_attn_workspace_size(2, 8, 2, 128, 1, 16, 4) == 0
+    need = b.fa_kv4_attn_workspace_size(2, 8, 2, 128, 1, 16, 1000)
     assert need > 0
     for bad in (dict(ws=0), dict(ws=A + 16), dict(wsb=need - 1)):
-        assert call(**bad) == b.FA_ERR_WORKSPACE, bad
+        assert call(width=1000, **bad) == b.FA_ERR_WORKSPACE, bad
     for empty in (dict(B=0), dict(T=0), dict(max_q=0)):
         assert call(**empty, q=0, o=0, lse=0, lengths=0, ws=0) == b.FA_OK
-    for bad in ((-1, 8, 2, 128, 1), (2, 7, 2, 128, 1), (2, 8, 2, 100, 1), (2, 8, 2, 128, -1), (1 << 30, 8, 2, 128, 64)):
+    for bad in ((-1, 8, 2, 128, 1, 16, 1000), (2, 7, 2, 128, 1, 16, 1000), (2, 8, 2, 100, 1, 16, 1000),
+                (2, 8, 2, 128, -1, 16, 1000), (1 << 30, 8, 2, 128, 64, 16, 1000), (2, 8, 2, 128, 1, 17, 1000),
+                (2, 8, 2, 128, 1, 16, 1 << 28)):
         assert b.fa_kv4_attn_workspace_size(*bad) == 0
 
 

@@ -444,7 +444,7 @@ def test_attention_is_reproducible_and_clean_of_its_workspace():
     args = (to_dev(q), cache, _i32(table), _i32(lengths))
     first = api.kv4_attention(*args)
     for fill in (0, 0xFF, 0x7F):
-        ws = torch.full((api.kv4_attention_workspace_bytes(4, 8, 2, 128),), fill, dtype=torch.uint8, device="cuda:0")
+        ws = torch.full((api.kv4_attention_workspace_bytes(4, 8, cache, table.shape[1]),), fill, dtype=torch.uint8, device="cuda:0")
         again = api.kv4_attention(*args, workspace=ws)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     with pytest.raises(ValueError, match="workspace holds"):

@@ -69,7 +69,7 @@ SIGNATURES = {
     "fa_kv4_store": (_I, [_VP, _VP, _VP, _LL, _LL, _LL, _LL, _VP, _I, _VP]),
     "fa_kv4_load": (_I, [_VP, _VP, _I, _VP, _VP, _VP]),
     "fa_kv4_attn": (_I, [_VP, _VP, _LL, _LL, _I, _VP, _I, _VP, _I, _VP, _I, _I, _F, _VP, _LL, _LL, _VP, _VP, _SZ, _VP]),
-    "fa_kv4_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "fa_kv4_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
 }
 
 _lib = None
@@ -240,8 +240,8 @@ def fa_kv4_attn(cache, q, q_token, q_head, T, cu, max_q, table, width, lengths, 
                              o_head, lse, workspace, workspace_bytes, stream)
 
 
-def fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q) -> int:
-    return lib().fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q)
+def fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q, page, width) -> int:
+    return lib().fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q, page, width)
 
 
 FA_KERNEL_KINDS = 14

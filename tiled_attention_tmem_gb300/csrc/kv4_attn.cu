@@ -33,16 +33,16 @@ bool use_wide(int d, long long rows) {
   return rows > 8 * most_nt(d) * (d == 192 ? 2 : d == 384 ? 5 : 3);
 }
 
-// Tiles and triples of the two kernels, and the workspace for either.
+// The form a call takes, tiles and triples of its kernel, and its workspace.
 struct Plan {
   int nt;
-  bool wide;
+  bool solo, wide;
   int row_tiles, triples;            // of 8 * nt rows
   int wide_row_tiles, wide_triples;  // of 128 rows
   size_t off_ml, off_cuts, bytes;
 };
 
-bool make_plan(int B, int H, int Hkv, int d, int max_q, Plan& plan) {
+bool make_plan(int B, int H, int Hkv, int d, int max_q, int page, int width, Plan& plan) {
   const long long rows = (long long)max_q * (H / Hkv);
   plan.nt = choose_nt(d, rows);
   plan.wide = use_wide(d, rows);
@@ -52,9 +52,20 @@ bool make_plan(int B, int H, int Hkv, int d, int max_q, Plan& plan) {
   plan.triples = (int)(tiles * B * Hkv);
   plan.wide_row_tiles = (int)wide_tiles;
   plan.wide_triples = (int)(wide_tiles * B * Hkv);
+  // A (request, kv head)'s units over all its row tiles are counted in 32 bits.
+  if (((long long)width * page / 32 + 1) * tiles > 0x7fffffffLL) return false;
+  // A block per triple while all fit the SMs at once and none has many units: measured in
+  // us (solo / split) at d = 128, page 64: 64 triples of 4, 8, 16, 32 units 6.0 / 9.0,
+  // 7.4 / 9.3, 10.5 / 10.0, 16.9 / 12.5; 256 triples 6.6 / 11.4, 8.7 / 13.9, 15.0 / 20.8,
+  // 24.4 / 27.8; 4 triples of 16 units 11.0 / 8.6; 2048 triples (several waves) of 4 units
+  // 35.8 / 30.2.
+  const long long units = ((long long)width * page + kv4_unit(d, plan.nt) - 1) / kv4_unit(d, plan.nt);
+  const int sms = sm_count_cached();
+  plan.solo = plan.triples <= kv4_solo_blocks(d, plan.nt) * sms && units <= 10 + plan.triples / 10;
+  plan.bytes = plan.off_ml = plan.off_cuts = 0;
+  if (plan.solo) return true;
   // Two slots of a tile's rows for every warp, or of 128 rows for every block.
-  const size_t sms = sm_count_cached();
-  const size_t held = plan.wide ? sms * 2 * 128 : sms * kv4_warps(d, plan.nt) * 2 * 8 * plan.nt;
+  const size_t held = plan.wide ? (size_t)sms * 2 * 128 : (size_t)sms * kv4_warps(d, plan.nt) * 2 * 8 * plan.nt;
   plan.off_ml = round256(held * d * sizeof(float));
   plan.off_cuts = plan.off_ml + round256(held * 2 * sizeof(float));
   plan.bytes = plan.off_cuts + round256((plan.wide ? plan.wide_triples : plan.triples) * sizeof(int2));
@@ -81,15 +92,9 @@ template <int D, int NT>
 fa_status run(Kv4AttnParams p, const Plan& plan, cudaStream_t st) {
   const int sms = sm_count_cached(), triples = plan.triples;
   const int most_rows = (int)std::min<long long>((long long)p.max_q * p.G, 1 << 20);
-  const long long units = (((long long)p.width << p.page_log2) + kv4_unit(D, NT) - 1) / kv4_unit(D, NT);
   p.row_tiles = plan.row_tiles;
-  using Solo = Kv4Cfg<D, NT, true>;
-  // A block per triple while all fit the SMs at once and none has many units: measured in
-  // us (solo / split) at d = 128, page 64: 64 triples of 4, 8, 16, 32 units 6.0 / 9.0,
-  // 7.4 / 9.3, 10.5 / 10.0, 16.9 / 12.5; 256 triples 6.6 / 11.4, 8.7 / 13.9, 15.0 / 20.8,
-  // 24.4 / 27.8; 4 triples of 16 units 11.0 / 8.6; 2048 triples (several waves) of 4 units
-  // 35.8 / 30.2.
-  if (triples <= Solo::BLOCKS * sms && units <= 10 + triples / 10) {
+  if (plan.solo) {
+    using Solo = Kv4Cfg<D, NT, true>;
     static std::atomic<unsigned long long> raised{0};
     return launch_raised(FA_KERNEL_KV4_ATTN, kv4_attn_kernel<Solo>, dim3((unsigned)triples), dim3(Solo::THREADS),
                          Solo::SMEM, st, p, raised);
@@ -116,11 +121,12 @@ using namespace fa;
 
 extern "C" {
 
-size_t fa_kv4_attn_workspace_size(int B, int H, int Hkv, int d, int max_q) {
-  if (shape_checks(B, H, Hkv, d, max_q) != FA_OK) return 0;
+size_t fa_kv4_attn_workspace_size(int B, int H, int Hkv, int d, int max_q, int page, int width) {
+  if (shape_checks(B, H, Hkv, d, max_q) != FA_OK || page_log2_of(page) < 0 || width < 0) return 0;
+  if ((long long)width * page > 0x7fffffffLL) return 0;
   if (B == 0 || H == 0 || max_q == 0) return 0;
   Plan plan;
-  return make_plan(B, H, Hkv, d, max_q, plan) ? plan.bytes : 0;
+  return make_plan(B, H, Hkv, d, max_q, page, width, plan) ? plan.bytes : 0;
 }
 
 fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_token, long long q_head, int T,
@@ -140,10 +146,9 @@ fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_toke
     return FA_ERR_MISALIGNED;
   if (!cu) max_q = 1;
   Plan plan;
-  if (!make_plan(B, H, Hkv, d, max_q, plan)) return FA_ERR_INVALID_ARG;
-  // A (request, kv head)'s units over all its row tiles are counted in 32 bits.
-  if (((long long)width * cache->page / 32 + 1) * plan.row_tiles > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.bytes)
+  if (!make_plan(B, H, Hkv, d, max_q, cache->page, width, plan)) return FA_ERR_INVALID_ARG;
+  if (plan.bytes &&
+      (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.bytes))
     return FA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   Kv4AttnParams p = {};

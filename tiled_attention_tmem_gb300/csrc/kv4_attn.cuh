@@ -71,6 +71,7 @@ constexpr int kv4_unit(int d, int nt) { return d <= 128 ? 64 : 32; }
 // shared memory: one launch, and no search for where a range begins.  For short
 // contexts; several of its smaller blocks share an SM.
 constexpr int kKv4SoloWarps = 4;
+constexpr int kv4_solo_blocks(int d, int nt) { return nt == 1 && d <= 256 ? 3 : 2; }  // an SM
 template <int D_, int NT_, bool SOLO_>
 struct Kv4Cfg {
   static constexpr int D = D_, NT = NT_;
@@ -84,7 +85,7 @@ struct Kv4Cfg {
   static constexpr int OFF_SCALE = UNIT * CODE_ROW;
   static constexpr int PART = UNIT * (CODE_ROW + SCALE_ROW);  // K or V of a unit
   static constexpr int OTHER = SOLO ? 512 : THREADS * 20 + 1024;  // what follows the ring
-  static constexpr int BLOCKS = SOLO ? (NT == 1 && D <= 256 ? 3 : 2) : 1;  // an SM
+  static constexpr int BLOCKS = SOLO ? kv4_solo_blocks(D, NT) : 1;  // an SM
   static constexpr int FIT = (233472 / BLOCKS - 1024 - OTHER) / (WARPS * 2 * PART);
   static constexpr int STAGES = FIT < 4 ? FIT : 4;
   static constexpr int OFF_BAR = WARPS * STAGES * 2 * PART;       // per stage: K full, V full

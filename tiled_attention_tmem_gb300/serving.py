@@ -253,14 +253,14 @@ def kv4_load(slots, cache: KV4Cache, stream=None):
     return k, v
 
 
-def kv4_attention_workspace_bytes(batch, heads, kv_heads, head_dim, max_q=1) -> int:
-    return _b.fa_kv4_attn_workspace_size(batch, heads, kv_heads, head_dim, max_q)
+def kv4_attention_workspace_bytes(batch, heads, cache: KV4Cache, width, max_q=1) -> int:
+    """What ``kv4_attention`` needs for a table of ``width`` pages a request (0: none)."""
+    return _b.fa_kv4_attn_workspace_size(batch, heads, cache.kv_heads, cache.head_dim, max_q, cache.page_size, width)
 
 
 # The same by shape and device (it is asked for in every call and depends on nothing else).
-_workspace_bytes = functools.lru_cache(maxsize=256)(
-    lambda batch, heads, kv_heads, head_dim, max_q, index: kv4_attention_workspace_bytes(
-        batch, heads, kv_heads, head_dim, max_q))
+_workspace_bytes = functools.lru_cache(maxsize=1024)(lambda *shape_and_device: _b.fa_kv4_attn_workspace_size(
+    *shape_and_device[:-1]))
 
 
 def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int = 1, scale: float | None = None,
@@ -301,7 +301,7 @@ def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int = 1,
         offsets, max_q = None, 1
         if T < B:
             raise ValueError(f"q has {T} tokens for {B} requests")
-    need = _workspace_bytes(B, H, kv, d, max_q, index)
+    need = _workspace_bytes(B, H, kv, d, max_q, c.page_size, width, index)
     if out is None:
         out = _empty(shape, dtype=_BF16, device=c.device)
         ot, oh = H * d, d
@@ -311,16 +311,19 @@ def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int = 1,
         lse = _empty((T, H), dtype=_F32, device=c.device)
     else:
         _dense(lse, "lse", _F32, (T, H), index)
-    if workspace is None:
-        workspace = _empty(need, dtype=_U8, device=c.device)
-    else:
+    if workspace is not None:
         _dense(workspace, "workspace", _U8, (None,), index)
         if workspace.numel() < need:
             raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
-        need = workspace.numel()
+        need, at = workspace.numel(), workspace.data_ptr()
+    elif need:
+        workspace = _empty(need, dtype=_U8, device=c.device)
+        at = workspace.data_ptr()
+    else:
+        at = None
     st = _b.lib().fa_kv4_attn(c.address, q.data_ptr(), qt, qh, T, offsets, max_q, table.data_ptr(), width,
                               lengths.data_ptr(), B, H, d ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh,
-                              lse.data_ptr(), workspace.data_ptr(), need, _current_stream(index))
+                              lse.data_ptr(), at, need, _current_stream(index))
     if st:
         _check(st, "fa_kv4_attn")
     return out, lse
