@@ -9,7 +9,7 @@
  *   codes  uint8 [pages, Hkv, page, d/2]   two e2m1 codes a byte, channel 2c in
  *                                          the low half, 2c + 1 in the high half
  *   scales uint8 [pages, Hkv, page, d/16]  one e4m3 scale per 16 channels
- * and one fp32 gain per tensor, finite and > 0:
+ * and one fp32 gain per tensor, from 2^-100 to 2^100:
  *   value = gain * scale * code,  code in +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}.
  * A scale byte's sign bit is ignored and 0x7f reads as 480: every byte pattern
  * stands for a finite value, so slots that were never written cannot put an
@@ -111,8 +111,11 @@ fa_status fa_kv4_load(const fa_kv4_cache* cache, const long long* slots, int T, 
  * h / (H/Hkv) serves head h:
  *   s_j = scale * k_gain * q . k_j,  lse = ln sum_j exp(s_j),  o = sum_j exp(s_j - lse) v_j.
  * A query that sees no key gets o = 0 and lse = -inf.  Rows of o and lse that no
- * query of a request owns are left as they were.  A request has at most max_q
- * queries; further ones are not computed.  A token whose table entry is not in
+ * query of a request owns are left as they were.  The first max_q queries of a
+ * request are computed (max_q times H/Hkv below 2^31).  A request whose queries do
+ * not lie in [0, T) has none; requests that share a query leave either's result in
+ * its row.  o may be q itself where the strides are the same, but must not overlap
+ * it in another way.  A token whose table entry is not in
  * [0, pages), or lies past `width`, is no key.
  * H a multiple of Hkv; scale finite and > 0.  workspace: fa_kv4_attn_workspace_size
  * bytes, 256-byte aligned, not shared with a concurrent call.

@@ -110,7 +110,7 @@ def attend(q, cache, table, lengths, cu, max_q, scale):
         vals = v[at].transpose(1, 0, 2, 3).reshape(kv, -1, d)
         index = np.arange(cols * page)
         for i in range(nq):
-            see = fine & (index <= n - nq + i) & (index < n)
+            see = fine & (index <= n - (t1 - t0) + i) & (index < n)
             for h in range(H):
                 kk, vv = keys[h // G][see], vals[h // G][see]
                 if len(kk) == 0:

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import kv4_ref as R
-from tiled_attention_tmem_gb300 import api, binding as b, build
+from tiled_attention_tmem_gb300 import api, binding as b, build, serving
 
 A = 1 << 20  # an aligned fake address; never dereferenced
 
@@ -145,6 +145,36 @@ def test_torch_layer_refuses_host_tensors_and_wrong_kinds():
         api.KV4Cache(_cache()[0].int(), *_cache()[1:])
     with pytest.raises(TypeError):
         api.KV4Cache(None, *_cache()[1:])
+
+
+def test_gains_whose_products_could_overflow_are_refused():
+    for gain, want in ((2.0 ** -100, b.FA_OK), (2.0 ** 100, b.FA_OK), (2.0 ** -101, b.FA_ERR_INVALID_ARG),
+                       (2.0 ** 100 * 1.001, b.FA_ERR_INVALID_ARG)):
+        for own in (dict(kg=gain, vg=1.0), dict(kg=1.0, vg=gain)):
+            desc = cache(dict(kc=A, ks=A, vc=A, vs=A, pages=3, page=16, H=2, d=128, **own))
+            assert b.fa_kv4_store(desc.address, A, A, 256, 128, 256, 128, A, 0, None) == want
+            assert b.fa_kv4_load(desc.address, A, 0, A, A, None) == want
+
+
+def test_attention_of_row_counts_past_31_bits_is_refused():
+    desc = cache(dict(kc=A, ks=A, vc=A, vs=A, pages=4, page=16, H=1, d=128, kg=1.0, vg=1.0))
+    top = (1 << 31) - 1
+    for batch, heads, max_q in ((2, 8, top), (top, top, top), (top, 64, 1)):
+        args = [A, 1024, 128, 2, A, max_q, A, 4, A, batch, heads, 0.1, A, 1024, 128, A, A, 1 << 60]
+        assert b.fa_kv4_attn(desc.address, *args, None) == b.FA_ERR_INVALID_ARG
+        assert b.fa_kv4_attn_workspace_size(batch, heads, 1, 128, max_q, 16, 4) == 0
+
+
+def test_rows_that_overlap_are_no_output():
+    rows = serving._rows
+    x = torch.zeros(4096, dtype=torch.bfloat16)
+    def layout(*stride, shape=(3, 2, 64)):
+        return rows(x.as_strided(shape, (*stride, 1)), "out", None, -1, written=True)
+    assert layout(128, 64) == (128, 64) and layout(64, 192) == (64, 192) and layout(136, 64) == (136, 64)
+    assert layout(8, 64, shape=(1, 2, 64)) == (0, 64) and layout(64, 3, shape=(3, 1, 64)) == (64, 0)
+    for bad in ((64, 64), (64, 128), (120, 64), (0, 64), (128, 56)):
+        with pytest.raises(ValueError, match="overlap"):
+            layout(*bad)
 
 
 def test_reference_codes_and_scales():

@@ -79,6 +79,39 @@ def test_page_grow_ignores_negative_counts_and_a_count_above_the_stack():
     assert np.array_equal(t.cpu().numpy(), ref[2])
 
 
+@pytest.mark.parametrize("B", [466_700, 466_944, 1 << 21])
+def test_page_grow_of_very_many_requests(B):
+    """Block shares of about 48 KB of rows, and the most requests there can be."""
+    from tiled_attention_tmem_gb300 import api
+    rng = np.random.default_rng(B)
+    held, add = rng.integers(0, 16, B), rng.integers(0, 3, B)
+    owned = (held > 0).astype(int)
+    table = np.where(np.arange(2) < owned[:, None], np.arange(B)[:, None], -7)
+    stack = np.arange(B, 2 * B)
+    t, T = _i32(table), B // 2
+    got = api.page_grow(_i32(held), _i32(add), t, _i32(stack), _i32([B // 3]), 16, T)
+    # Without a loop: one page at most is needed beyond those owned, or two tokens' first.
+    cu = np.minimum(np.concatenate([[0], np.cumsum(add)]), T)
+    add = np.diff(cu)
+    need = -(-(held + add) // 16) - owned
+    before = np.cumsum(need) - need
+    src = B // 3 - 1 - before
+    assert need.max() == 1
+    fresh = np.where(src >= 0, stack[src], -1)
+    tab = table.copy()
+    take = need > 0
+    tab[np.nonzero(take)[0], owned[take]] = fresh[take]
+    req = np.repeat(np.arange(B), add)
+    pos = held[req] + np.arange(len(req)) - cu[req]
+    page = tab[req, pos // 16]
+    slots = np.full(T, -1)
+    slots[:len(req)] = np.where(page >= 0, page * 16 + pos % 16, -1)
+    room = (owned + (take & (src >= 0))) * 16 - held
+    for g, r in zip(got, (slots, cu, held + np.minimum(add, room), [max(B // 3 - need.sum(), 0)])):
+        assert np.array_equal(g.cpu().numpy(), r)
+    assert np.array_equal(t.cpu().numpy(), tab)
+
+
 def test_page_calls_with_no_requests_and_no_width():
     import torch
     from tiled_attention_tmem_gb300 import api
@@ -328,6 +361,59 @@ def test_attention_many_rows_keeps_nan_in_its_row():
     assert torch.equal(got[~bad], clean[~bad])
 
 
+@pytest.mark.parametrize("heads,lengths", [(4, [30, 9, 100]), (64, [30, 9, 2000])])
+def test_attention_of_more_queries_than_max_q(heads, lengths):
+    """The first max_q queries of a request, at the positions that all of them give them;
+    the rows of the others stay as they were."""
+    import torch
+    queries, max_q = [5, 2, 7], 3
+    problem = _problem(64, 16, heads, 1, lengths, queries, seed=71)
+    o = torch.full((14, heads, 64), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    _attend(problem, lengths, max_q, out=o)
+    assert torch.all(o[3:5] == 7) and torch.all(o[10:] == 7)
+
+
+def test_attention_in_place_and_on_two_streams_at_once():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    runs = []
+    for seed, (heads, lengths, queries) in enumerate([(8, [3000, 17, 400], [2, 1, 3]), (32, [40, 900], [4, 4]),
+                                                      (80, [5000, 1200], [2, 1])]):
+        arrays, table, cu, q, gains = _problem(128, 64, heads, 2 if heads < 80 else 1, lengths, queries, seed=seed)
+        args = (_cache_of(arrays, gains), _i32(table), _i32(lengths), _i32(cu), max(queries))
+        x = to_dev(q)
+        want, lse = api.kv4_attention(x, *args)
+        again = x.clone()
+        got, lse2 = api.kv4_attention(again, *args, out=again)  # the output over the queries
+        assert got is again and torch.equal(got, want) and torch.equal(lse, lse2)
+        runs.append((x, args, want, lse))
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    outs = [[] for _ in runs]
+    for _ in range(8):
+        for s, (x, args, _, _), out in zip(streams, runs, outs):
+            with torch.cuda.stream(s):
+                out.append(api.kv4_attention(x, *args))
+    torch.cuda.synchronize()
+    for (_, _, want, lse), out in zip(runs, outs):
+        for o, l in out:
+            assert torch.equal(o, want) and torch.equal(l, lse)
+    api.check_device_error()
+
+
+def test_attention_of_scores_past_the_range_of_fp32():
+    """A scale at the end of fp32: one key outweighs all others or, with a zero query, none does."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    arrays, table, cu, q, gains = _problem(64, 16, 2, 1, [20], [1], seed=73)
+    x = to_dev(q)
+    x[0, 1] = 0
+    o, lse = api.kv4_attention(x, _cache_of(arrays, gains), _i32(table), _i32([20]), scale=1e38)
+    ref = _reference(arrays, gains, table, cu, R.bf16(to_f64(x)), [20], 1, 1.0)
+    assert abs(float(lse[0, 1]) - math.log(20)) < 1e-5
+    assert np.all(np.abs(to_f64(o)[0, 1] - ref[0][0, 1]) <= 2.0 ** -7 * ref[2][0, 1])
+
+
 def test_attention_without_offsets_is_one_query_a_request():
     from tiled_attention_tmem_gb300 import api
     lengths = [5, 0, 77]
@@ -478,6 +564,45 @@ def test_cache_beyond_four_gigabytes():
         f[:] = g.reshape(3, page, kv, d).transpose(0, 2, 1, 3)
     ref = R.attend(to_f64(to_dev(q)), full, np.array([[0, 1, 2]]), [n], [0, 1], 1, 1 / math.sqrt(d))
     R.check(to_f64(o), to_f64(lse), ref, d)
+
+
+def test_operands_beyond_two_to_the_31_elements():
+    """Token strides that carry a query, an output, and a key past 2^31 elements."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    problem = _problem(64, 16, 4, 2, [40, 21, 33], [1, 1, 1], seed=79)
+    arrays, table, cu, q, gains = problem
+    cache, x = _cache_of(arrays, gains), to_dev(q)
+    want, lse = api.kv4_attention(x, cache, _i32(table), _i32([40, 21, 33]))
+    step = (1 << 30) + 64
+    far = torch.empty(2 * step + 256, dtype=torch.bfloat16, device="cuda:0").as_strided((3, 4, 64), (step, 64, 1))
+    far.copy_(x)
+    got, lse2 = api.kv4_attention(far, cache, _i32(table), _i32([40, 21, 33]), out=far)
+    assert torch.equal(got, want) and torch.equal(lse, lse2)
+    slots = torch.arange(3, device="cuda:0")
+    api.kv4_store(far[:, :2], far[:, 2:], slots, cache)
+    near = api.KV4Cache(*(torch.zeros_like(t) for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)), *gains)
+    api.kv4_store(want[:, :2].contiguous(), want[:, 2:].contiguous(), slots, near)
+    for a, b in zip(api.kv4_load(slots, cache), api.kv4_load(slots, near)):
+        assert torch.equal(a, b)
+
+
+def test_store_and_load_at_the_ends_of_the_gains():
+    """Groups that are zero but for one channel, under the smallest and largest gain."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    for power in (-100, 100):
+        cache = api.KV4Cache.empty(1, 1, 16, 64, 2.0 ** power, 2.0 ** power)
+        x = np.zeros((4, 1, 64))
+        x[0, 0, 3], x[1, 0, 17], x[2, 0, 40], x[3, 0, 0] = 2.0 ** 120, 2.0 ** -120, 1.0, -2.0 ** 99
+        slots = torch.arange(4, device="cuda:0")
+        api.kv4_store(to_dev(R.bf16(x)), to_dev(R.bf16(-x)), slots, cache)
+        a = _cache_arrays(cache)
+        codes, scales = R.encode(x, 2.0 ** power)
+        assert np.array_equal(a[0][0, 0, :4], codes[:, 0]) and np.array_equal(a[1][0, 0, :4], scales[:, 0])
+        k, v = api.kv4_load(slots, cache)
+        want = R.decode(codes, scales, 2.0 ** power)
+        assert np.all(np.abs(to_f64(k) - want) <= 2.0 ** -8 * np.abs(want)) and torch.equal(v, -k)
 
 
 # ------------------------------------------------------------------ together

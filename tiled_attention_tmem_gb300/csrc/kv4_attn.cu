@@ -44,6 +44,7 @@ struct Plan {
 
 bool make_plan(int B, int H, int Hkv, int d, int max_q, int page, int width, Plan& plan) {
   const long long rows = (long long)max_q * (H / Hkv);
+  if (rows > 0x7fffffffLL || (long long)B * Hkv > 0x7fffffffLL) return false;
   plan.nt = choose_nt(d, rows);
   plan.wide = use_wide(d, rows);
   const long long tiles = (rows + 8 * plan.nt - 1) / (8 * plan.nt), wide_tiles = (rows + 127) / 128;
@@ -180,7 +181,7 @@ fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_toke
   p.pages = cache->pages;
   p.page_log2 = page_log2_of(cache->page);
   p.max_q = max_q;
-  p.score = scale * kLog2e * cache->k_gain * kKv4ScaleBias;
+  p.score = std::min(scale * kLog2e * cache->k_gain * kKv4ScaleBias, 3e38f);
   p.v_gain = cache->v_gain * kKv4ScaleBias;
   cudaStream_t st = (cudaStream_t)stream;
   switch (d * 8 + plan.nt) {

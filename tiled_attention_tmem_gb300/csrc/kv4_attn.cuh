@@ -84,14 +84,14 @@ struct Kv4Cfg {
   static constexpr int CODE_ROW = D / 2, SCALE_ROW = D / 16;  // bytes a token
   static constexpr int OFF_SCALE = UNIT * CODE_ROW;
   static constexpr int PART = UNIT * (CODE_ROW + SCALE_ROW);  // K or V of a unit
-  static constexpr int OTHER = SOLO ? 512 : THREADS * 20 + 1024;  // what follows the ring
+  static constexpr int OTHER = SOLO ? 512 : THREADS * 24 + 1024;  // what follows the ring
   static constexpr int BLOCKS = SOLO ? kv4_solo_blocks(D, NT) : 1;  // an SM
   static constexpr int FIT = (233472 / BLOCKS - 1024 - OTHER) / (WARPS * 2 * PART);
   static constexpr int STAGES = FIT < 4 ? FIT : 4;
   static constexpr int OFF_BAR = WARPS * STAGES * 2 * PART;       // per stage: K full, V full
   static constexpr int OFF_PREFIX = OFF_BAR + WARPS * STAGES * 16;
-  static constexpr int OFF_REQ = OFF_PREFIX + (SOLO ? 0 : (THREADS + 1) * 8);  // tokens, first query, queries
-  static constexpr int OFF_MISC = OFF_REQ + (SOLO ? 0 : THREADS * 12);
+  static constexpr int OFF_REQ = OFF_PREFIX + (SOLO ? 0 : (THREADS + 1) * 8);  // the requests
+  static constexpr int OFF_MISC = OFF_REQ + (SOLO ? 0 : THREADS * 16);
   static constexpr int SMEM = OFF_MISC + 16 + WARPS * 8;
   static constexpr int WK = D / 32;         // words of 8 codes a lane reads of a K row
   static constexpr int WV = (D + 63) / 64;  // words a lane reads of a V row (d = 96: one and a half)
@@ -107,7 +107,8 @@ struct Kv4Cfg {
 struct Kv4Cursor {
   int b, kvh, rt, u;      // request, kv head, row tile, unit
   int units, tiles;       // units and row tiles of request b
-  int n, tok0, nq;        // tokens of b, its first query token, its queries
+  int n, tok0, nq;        // tokens of b, its first query token, its queries (max_q at most)
+  int first;              // position of its first query (negative: that one sees nothing)
 };
 
 // Tokens, first query and queries of request b from the caller's arrays.
@@ -117,10 +118,12 @@ __device__ __forceinline__ void kv4_lookup(const Kv4AttnParams& p, int b, Kv4Cur
     c.tok0 = p.cu[b];
     const long long nq = (long long)p.cu[b + 1] - c.tok0;
     c.nq = (int)min(max(nq, 0LL), (long long)p.max_q);
+    c.first = (int)max(c.n - max(nq, 0LL), -0x7fffffffLL);
     if (c.tok0 < 0 || c.tok0 > p.T - c.nq) c.nq = 0;  // queries outside q: not computed
   } else {
     c.tok0 = b;
     c.nq = 1;
+    c.first = c.n - 1;
   }
 }
 
@@ -128,7 +131,7 @@ __device__ __forceinline__ void kv4_lookup(const Kv4AttnParams& p, int b, Kv4Cur
 template <class C>
 __device__ __forceinline__ void kv4_request(const Kv4AttnParams& p, const int* req, int b, Kv4Cursor& c) {
   if (req) {
-    c.n = req[3 * b], c.tok0 = req[3 * b + 1], c.nq = req[3 * b + 2];
+    c.n = req[4 * b], c.tok0 = req[4 * b + 1], c.nq = req[4 * b + 2], c.first = req[4 * b + 3];
   } else {
     kv4_lookup(p, b, c);
   }
@@ -149,7 +152,7 @@ __device__ __forceinline__ void kv4_advance(const Kv4AttnParams& p, const int* r
   do {
     if (++c.b >= p.B) {  // past the last unit (only if the lengths changed meanwhile): nothing to do there
       c.b = p.B - 1;
-      c.n = c.nq = 0;
+      c.n = c.nq = c.first = 0;
       c.units = c.tiles = 1;
       return;
     }
@@ -159,7 +162,7 @@ __device__ __forceinline__ void kv4_advance(const Kv4AttnParams& p, const int* r
 
 // Where each thread's run of requests begins in the sequence of units: prefix[i] units
 // lie before thread i's ceil(B / THREADS) requests, prefix[THREADS] in all.  `kept` takes
-// the requests themselves (tokens, first query, queries) if every thread has one at most.
+// the requests themselves (tokens, first query token, queries, position) if every thread has one at most.
 // `sums` has a word for each warp.  Ends with a barrier.
 template <class C>
 __device__ __forceinline__ long long kv4_scan(const Kv4AttnParams& p, long long* prefix, int* kept, long long* sums) {
@@ -170,7 +173,7 @@ __device__ __forceinline__ long long kv4_scan(const Kv4AttnParams& p, long long*
   for (int b = b0; b < b1; ++b) {
     Kv4Cursor c;
     kv4_request<C>(p, nullptr, b, c);
-    if (run == 1 && kept) kept[3 * b] = c.n, kept[3 * b + 1] = c.tok0, kept[3 * b + 2] = c.nq;
+    if (run == 1 && kept) kept[4 * b] = c.n, kept[4 * b + 1] = c.tok0, kept[4 * b + 2] = c.nq, kept[4 * b + 3] = c.first;
     sum += (long long)c.units * c.tiles * p.Hkv;
   }
   long long x = sum;
@@ -455,11 +458,11 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          // (not 0, so that a masked score stays -inf)
-          fac[n][j] = fmaxf(__shfl_sync(0xffffffffu, up, (2 * t + j) * 4), 1e-37f);
+          // (not 0, so that a masked score stays -inf, and finite, so that a score of 0 stays 0)
+          fac[n][j] = fminf(fmaxf(__shfl_sync(0xffffffffu, up, (2 * t + j) * 4), 1e-37f), 3e38f);
           const int r = cur.rt * C::ROWS + 8 * n + 2 * t + j;
           const int qi = r / p.G;
-          lim[n][j] = qi < cur.nq ? cur.n - cur.nq + qi : -1;
+          lim[n][j] = qi < cur.nq ? cur.first + qi : -1;
           m[n][j] = -INFINITY;
           l[n][j] = 0.f;
           if (qi < cur.nq) lim_min = min(lim_min, lim[n][j]);

@@ -69,7 +69,7 @@ struct Kv4WideCfg {
   static constexpr int OFF_PREFIX = OFF_BAR + BARS * 8;
   static constexpr int OFF_REQ = OFF_PREFIX + (THREADS + 1) * 8;
   static constexpr bool KEEP = D < 384;  // room for the requests
-  static constexpr int OFF_BITS = OFF_REQ + (KEEP ? THREADS * 12 : 0);  // a byte for each of the last 32 units
+  static constexpr int OFF_BITS = OFF_REQ + (KEEP ? THREADS * 16 : 0);  // a byte for each of the last 32 units
   static constexpr int OFF_MISC = OFF_BITS + 32;
   static constexpr int SMEM = OFF_MISC + 16 + THREADS / 32 * 8 + 1024;  // and the tiles' alignment
   // O has a column for every channel of the panels: at d = 96 the last 32 are never read.
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::B_Q));
-      return fmaxf(__uint_as_float((uint32_t)(127 + exponent(top)) << 23) * p.score, 1e-37f);
+      return fminf(fmaxf(__uint_as_float((uint32_t)(127 + exponent(top)) << 23) * p.score, 1e-37f), 3e38f);
     };
     // O with unit u added.  S runs one unit ahead, so a barrier for every other unit cannot
     // be two phases ahead of its waiter.
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
       const bool have = i < nq;
       const bool busy = __any_sync(0xffffffffu, have);  // a warp past the last row only keeps pace
       // (A row past the last sees everything: its zeros cost no masking, and are not stored.)
-      const int lim = have ? cur.n - nq + i : 0x7fffffff;
+      const int lim = have ? cur.first + i : 0x7fffffff;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++g) {
         const uint32_t tS = trow + C::TMEM_S + (g & 1) * UNIT;

@@ -31,7 +31,8 @@ struct PageParams {
 constexpr int kPageThreads = 256;
 
 struct PageRow {
-  int held, add, cu, off, owned, need;
+  long long off;  // pages that the requests before need
+  int held, add, cu, owned, need;
 };
 
 // Exclusive scan of one value a thread over the block; total through `total`.
@@ -64,8 +65,8 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
 // new token comes from the old table or from the stack, never from an entry that
 // this launch writes, so blocks do not wait for one another.
 __global__ void __launch_bounds__(kPageThreads) page_kernel(const __grid_constant__ PageParams p) {
-  __shared__ long long warp_sums[kPageThreads / 32];
-  extern __shared__ PageRow rows[];  // per_block
+  extern __shared__ long long warp_sums[];  // a word a warp, then per_block rows
+  PageRow* rows = reinterpret_cast<PageRow*>(warp_sums + kPageThreads / 32);
   grid_dep_wait();
   const int page = 1 << p.page_log2;
   const int run = (p.B + kPageThreads - 1) / kPageThreads;
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kPageThreads) page_kernel(const __grid_constan
     int held, cu, add, owned;
     const int need = place(b, raw, held, cu, add, owned);
     raw += max(p.add[b], 0);
-    if (b >= my0 && b < my1) rows[b - my0] = PageRow{held, add, cu, (int)min(off, 0x7fffffffLL), owned, need};
+    if (b >= my0 && b < my1) rows[b - my0] = PageRow{off, held, add, cu, owned, need};
     off += need;
   }
   const int count = p.free_pages ? min(max(*p.free_count, 0), p.free_size) : 0;
@@ -117,13 +118,13 @@ __global__ void __launch_bounds__(kPageThreads) page_kernel(const __grid_constan
       if (lane == 0) {
         p.cu[b] = r.cu;
         if (p.held_out) {
-          const int given = min(max(count - r.off, 0), r.need);
+          const int given = (int)min(max(count - r.off, 0LL), (long long)r.need);
           const long long room = min((long long)r.owned + given, (long long)p.width) * page - r.held;
           p.held_out[b] = r.held + (int)max(min(room, (long long)r.add), 0LL);
         }
       }
       for (int i = lane; i < r.need; i += 32) {
-        const int src = count - 1 - r.off - i;
+        const long long src = count - 1 - r.off - i;
         entry[r.owned + i] = src >= 0 ? p.free_pages[src] : -1;
       }
     }
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kPageThreads) page_kernel(const __grid_constan
         if (!p.free_pages || col < r.owned) {
           id = entry[col];
         } else {
-          const int src = count - 1 - r.off - (int)(col - r.owned);
+          const long long src = count - 1 - r.off - (col - r.owned);
           id = src >= 0 ? p.free_pages[src] : -1;
         }
       }
@@ -156,7 +157,8 @@ fa_status run_pages(PageParams p, cudaStream_t st) {
   p.per_block = std::max(8, (p.B + cap - 1) / cap);
   const int gx = (p.B + p.per_block - 1) / p.per_block;
   const int gy = std::max(1, std::min(cap / gx, (int)((long long)p.T / std::max(1, p.B) / 64)));
-  return launch(FA_KERNEL_PAGE, page_kernel, dim3(gx, gy), dim3(kPageThreads), p.per_block * sizeof(PageRow), st, p);
+  return launch(FA_KERNEL_PAGE, page_kernel, dim3(gx, gy), dim3(kPageThreads),
+                kPageThreads / 32 * sizeof(long long) + p.per_block * sizeof(PageRow), st, p);
 }
 
 // At most 2^21 requests (a block keeps a row for each of its own in shared memory),
@@ -360,8 +362,10 @@ fa_status kv4_io_fill(const fa_kv4_cache& c, const long long* slots, int T, Kv4I
 
 fa_status kv4_cache_checks(const fa_kv4_cache* c) {
   if (!c || c->pages < 0 || c->Hkv < 0 || page_log2_of(c->page) < 0) return FA_ERR_INVALID_ARG;
-  for (float g : {c->k_gain, c->v_gain})  // the store multiplies by the reciprocal
-    if (!std::isfinite(g) || !(g > 0.f) || !std::isfinite(1.f / g)) return FA_ERR_INVALID_ARG;
+  // Gains whose products with 2^8 and whose reciprocals' with 2^9 (of the smallest scale) stay
+  // finite: what the kernels multiply by, so that a code of 0 never meets an infinity.
+  for (float g : {c->k_gain, c->v_gain})
+    if (!(g >= 0x1p-100f && g <= 0x1p100f)) return FA_ERR_INVALID_ARG;
   if (padded_head_dim(c->d) == 0) return FA_ERR_UNSUPPORTED;
   // A token's runs of eight channels, 32 at a time, have to fit a grid's second dimension.
   if ((long long)c->Hkv * c->d > 65535LL * 256) return FA_ERR_INVALID_ARG;

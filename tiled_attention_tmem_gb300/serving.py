@@ -11,7 +11,6 @@ fails it is looked at again for the reason.
 from __future__ import annotations
 
 import functools
-import math
 
 import torch
 
@@ -75,7 +74,7 @@ def _rows(t, name, shape, index, written=False):
     token and head strides (0 for a dimension of one element)."""
     if isinstance(t, _Tensor) and t.dtype is _BF16 and t.get_device() == index and t.dim() == 3:
         st, sh, sd = t.stride()
-        if sd == 1 and st and sh and not written and (shape is None or t.shape == shape):
+        if sd == 1 and st and sh and not (st | sh) & 7 and not written and (shape is None or t.shape == shape):
             return st, sh
     if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -92,8 +91,12 @@ def _rows(t, name, shape, index, written=False):
     if sd != 1 and d > 1:
         raise ValueError(f"{name}: the channels must be dense")
     st, sh = st if tokens > 1 else 0, sh if heads > 1 else 0
-    if written and ((tokens > 1 and st < d) or (heads > 1 and sh < d)):
-        raise ValueError(f"{name}: its rows overlap")
+    if written:
+        reach = d  # elements that the dimensions inside this one span
+        for stride, n in sorted(((st, tokens), (sh, heads))):
+            if n > 1 and stride < reach:
+                raise ValueError(f"{name}: its rows overlap")
+            reach += stride * (n - 1)
     return st, sh
 
 
@@ -179,8 +182,9 @@ def page_slots(first, count, table, page_size, num_tokens, stream=None):
 class KV4Cache:
     """A pool of pages of keys and values in 4 bits: per tensor, e2m1 codes uint8
     [pages, kv_heads, page_size, d/2] (even channel in the low half), e4m3 scales uint8
-    [pages, kv_heads, page_size, d/16] and one gain; value = gain * scale * code.  Choose
-    the gain so that max|x| / (6 * gain) stays below 448; a power of two loses nothing."""
+    [pages, kv_heads, page_size, d/16] and one gain (2^-100 to 2^100); value = gain * scale *
+    code.  Choose the gain so that max|x| / (6 * gain) stays below 448; a power of two loses
+    nothing.  The arrays' contents may change, the arrays and gains are those given here."""
 
     __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_gain", "v_gain", "device", "index", "pages",
                  "kv_heads", "page_size", "head_dim", "descriptor", "address")
@@ -197,8 +201,8 @@ class KV4Cache:
         for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
             _dense(t, name, _U8, (pages, heads, page, half // 8), index)
         for x, name in ((k_gain, "k_gain"), (v_gain, "v_gain")):
-            if not (math.isfinite(x) and x > 0):
-                raise ValueError(f"{name} must be finite and positive")
+            if not 2.0 ** -100 <= x <= 2.0 ** 100:
+                raise ValueError(f"{name} must be from 2^-100 to 2^100")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.k_gain, self.v_gain, self.device, self.index = float(k_gain), float(v_gain), k_codes.device, index
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, 2 * half
@@ -255,6 +259,9 @@ def kv4_load(slots, cache: KV4Cache, stream=None):
 
 def kv4_attention_workspace_bytes(batch, heads, cache: KV4Cache, width, max_q=1) -> int:
     """What ``kv4_attention`` needs for a table of ``width`` pages a request (0: none)."""
+    if _current_device() != cache.index:
+        with _On(cache.index, None):
+            return kv4_attention_workspace_bytes(batch, heads, cache, width, max_q)
     return _b.fa_kv4_attn_workspace_size(batch, heads, cache.kv_heads, cache.head_dim, max_q, cache.page_size, width)
 
 
@@ -270,10 +277,12 @@ def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int = 1,
     q bf16 [T, heads, d] (token and head strides free, in eights; heads a multiple of
     the cache's); table int32 [B, width]; lengths int32 [B]: tokens of each request in
     the cache, the queries' own included; cu_q int32 [B + 1]: where each request's
-    queries begin in q (None: one each), at most ``max_q`` of them.  Query i of a
-    request's n sees the tokens up to lengths - n + i.  Returns (o bf16 [T, heads, d],
-    lse fp32 [T, heads]); a query that sees nothing gets o = 0 and lse = -inf, rows of
-    no request are left as they were.  ``workspace``: a uint8 CUDA tensor of
+    queries begin in q (None: one each), of which the first ``max_q`` are computed.  Query
+    i of a request's n sees the tokens up to lengths - n + i.  Returns (o bf16 [T, heads,
+    d], lse fp32 [T, heads]); a query that sees nothing gets o = 0 and lse = -inf, rows of
+    no request are left as they were (in ``out`` and ``lse``, given or new; ``out`` may be q).
+    The table's width and ``max_q`` choose the kernel, so neither should be much larger than
+    the longest request.  ``workspace``: a uint8 CUDA tensor of
     ``kv4_attention_workspace_bytes``, not shared with a concurrent call, or None."""
     c = cache
     index = c.index
