@@ -402,7 +402,7 @@ def test_attention_in_place_and_on_two_streams_at_once():
 
 
 def test_attention_of_scores_past_the_range_of_fp32():
-    """A scale at the end of fp32: one key outweighs all others or, with a zero query, none does."""
+    """A scale at the end of fp32: a zero query still weighs all keys alike."""
     import torch
     from tiled_attention_tmem_gb300 import api
     arrays, table, cu, q, gains = _problem(64, 16, 2, 1, [20], [1], seed=73)
@@ -747,3 +747,21 @@ def test_a_set_error_word_stops_the_attention():
     api.kv4_attention(to_dev(q), _cache_of(arrays, gains), _i32(table), _i32([300]), out=o)
     api.check_device_error()
     assert not torch.any(o == 7)
+
+
+@pytest.mark.parametrize("heads,lengths", [(4, [30000, 700]), (80, [9000, 700])], ids=["split", "many_rows"])
+def test_a_set_error_word_stops_the_attention_and_its_merge(heads, lengths):
+    import torch
+    from tiled_attention_tmem_gb300 import api, binding as b
+    arrays, table, cu, q, gains = _problem(64, 64, heads, 1, lengths, [2, 2], seed=59)
+    args = (to_dev(q), _cache_of(arrays, gains), _i32(table), _i32(lengths), _i32(cu), 2)
+    assert api.kv4_attention_workspace_bytes(2, heads, args[1], table.shape[1], 2) > 0
+    want, lse = api.kv4_attention(*args)
+    o, l = torch.full_like(want, 7.0), torch.full_like(lse, 7.0)
+    assert b.lib().fa_watchdog_selftest(torch.cuda.current_stream().cuda_stream) == b.FA_OK
+    api.kv4_attention(*args, out=o, lse=l)
+    st, _ = b.fa_get_device_error(torch.cuda.current_stream().cuda_stream)
+    assert st == b.FA_ERR_DEVICE_TIMEOUT and torch.all(o == 7) and torch.all(l == 7)
+    api.kv4_attention(*args, out=o, lse=l)
+    api.check_device_error()
+    assert torch.equal(o, want) and torch.equal(l, lse)
