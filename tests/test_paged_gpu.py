@@ -361,6 +361,15 @@ def test_attention_many_rows_keeps_nan_in_its_row():
     assert torch.equal(got[~bad], clean[~bad])
 
 
+@pytest.mark.parametrize("d,page", [(96, 16), (96, 128), (128, 32), (128, 64)])
+@pytest.mark.parametrize("group,queries", [(6, 4), (17, 1), (7, 3)])
+@pytest.mark.parametrize("lengths", [[0, 3, 64, 95, 170, 333], [9000, 2, 0, 1025]], ids=["short", "long"])
+def test_attention_of_17_to_24_rows(d, page, group, queries, lengths):
+    each = [max(1, queries - b % 2) for b in range(len(lengths))]
+    problem = _problem(d, page, 2 * group, 2, lengths, each, seed=d + group, spread=2.0)
+    _attend(problem, lengths, queries)
+
+
 @pytest.mark.parametrize("heads,lengths", [(4, [30, 9, 100]), (64, [30, 9, 2000])])
 def test_attention_of_more_queries_than_max_q(heads, lengths):
     """The first max_q queries of a request, at the positions that all of them give them;

@@ -33,6 +33,13 @@ bool use_wide(int d, long long rows) {
   return rows > 8 * most_nt(d) * (d == 192 ? 2 : d == 384 ? 5 : 3);
 }
 
+// Three tiles, on units of 32 tokens, where they save the second pass of two row tiles of 16.
+// Measured in us (one of 24 / two of 16): d = 128, 20 rows, 8 requests of 16384 tokens and 8
+// kv heads 74 / 89, 64 of 4096 133 / 166; d = 96, 24 rows, 8 of 8192 41 / 47.  Two of 24 lose
+// to three of 16: 40 rows, d = 128, 16 up to 4096 28 / 25, d = 96, 8 of 8192 67 / 63; and so
+// does one in the form of a block per triple: d = 96, 20 rows, 8 of 300 11.8 / 10.4.
+constexpr bool has_three(int d) { return d == 96 || d == 128; }
+
 // The form a call takes, tiles and triples of its kernel, and its workspace.
 struct Plan {
   int nt;
@@ -65,6 +72,11 @@ bool make_plan(int B, int H, int Hkv, int d, int max_q, int page, int width, Pla
   plan.solo = plan.triples <= kv4_solo_blocks(d, plan.nt) * sms && units <= 10 + plan.triples / 10;
   plan.bytes = plan.off_ml = plan.off_cuts = 0;
   if (plan.solo) return true;
+  if (has_three(d) && rows > 16 && rows <= 24) {
+    plan.nt = 3;
+    plan.row_tiles = 1;
+    plan.triples = B * Hkv;
+  }
   // Two slots of a tile's rows for every warp, or of 128 rows for every block.
   const size_t held = plan.wide ? (size_t)sms * 2 * 128 : (size_t)sms * kv4_warps(d, plan.nt) * 2 * 8 * plan.nt;
   plan.off_ml = round256(held * d * sizeof(float));
@@ -94,7 +106,7 @@ fa_status run(Kv4AttnParams p, const Plan& plan, cudaStream_t st) {
   const int sms = sm_count_cached(), triples = plan.triples;
   const int most_rows = (int)std::min<long long>((long long)p.max_q * p.G, 1 << 20);
   p.row_tiles = plan.row_tiles;
-  if (plan.solo) {
+  if constexpr (NT != 3) if (plan.solo) {
     using Solo = Kv4Cfg<D, NT, true>;
     static std::atomic<unsigned long long> raised{0};
     return launch_raised(FA_KERNEL_KV4_ATTN, kv4_attn_kernel<Solo>, dim3((unsigned)triples), dim3(Solo::THREADS),
@@ -189,6 +201,8 @@ fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_toke
     case 64 * 8 + 2: return run<64, 2>(p, plan, st);
     case 64 * 8 + 4: return run<64, 4>(p, plan, st);
     case 96 * 8 + 1: return run<96, 1>(p, plan, st);
+    case 96 * 8 + 3: return run<96, 3>(p, plan, st);
+    case 128 * 8 + 3: return run<128, 3>(p, plan, st);
     case 96 * 8 + 2: return run<96, 2>(p, plan, st);
     case 128 * 8 + 1: return run<128, 1>(p, plan, st);
     case 128 * 8 + 2: return run<128, 2>(p, plan, st);

@@ -61,11 +61,12 @@ struct Kv4AttnParams {
 constexpr float kKv4Lift = 7.f;
 constexpr float kKv4Grow = 8.f;
 
-// Warps per SM and tokens per unit for head dim d and nt tiles of 8 rows.
+// Warps per SM and tokens per unit for head dim d and nt tiles of 8 rows (what the registers
+// hold: with three tiles and 64 tokens the scores would not fit).
 constexpr int kv4_warps(int d, int nt) {
   return d * nt <= 128 || (nt == 1 && d <= 256) ? 12 : 8;
 }
-constexpr int kv4_unit(int d, int nt) { return d <= 128 ? 64 : 32; }
+constexpr int kv4_unit(int d, int nt) { return d <= 128 && nt != 3 ? 64 : 32; }
 
 // SOLO: a block per triple, whose warps take its units in turn and join their parts in
 // shared memory: one launch, and no search for where a range begins.  For short
