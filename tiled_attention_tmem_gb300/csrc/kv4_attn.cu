@@ -22,16 +22,18 @@ int choose_nt(int d, long long rows) {
   return nt;
 }
 
-// The tcgen05 kernel takes a call whose rows would need several narrow tiles, each of
-// which reads and converts the units again (its own time hardly depends on the rows).
-// Measured in us (narrow / wide) over 8 requests up to 8192 tokens, 8 kv heads: d = 128
-// with 32, 48, 64, 128 rows 37 / 50, 45 / 42, 54 / 49, 85 / 55; d = 64 with 64, 128 rows
-// 34 / 42, 53 / 45; d = 192 with 32, 48 rows 54 / 62, 69 / 54; over 4096 tokens, d = 256 with
-// 24 rows 37 / 44, and 28 rows of one request of 32382 tokens 124 / 74; one request of
-// 34617 tokens, 4 kv heads, d = 384, 64 rows 107 / 67; 2 of 16384, d = 128, 512 rows 111 / 51.
-bool use_wide(int d, long long rows) {
-  return rows > 8 * most_nt(d) * (d == 192 ? 2 : d == 384 ? 5 : 3);
-}
+// The tcgen05 kernel takes a call whose requests have this many rows a kv head on average: the
+// narrow tiles read and convert the cache again for each, its own time hardly depends on the
+// rows.  Measured in us (narrow / wide), 8 / 32 requests of 8192 tokens and 4 kv heads:
+//   d = 64   64 rows 33 / 33, 90 / 90     96 rows 44 / 34, 127 / 93
+//   d = 96   32 rows 29 / 35, 81 / 98     40 rows 39 / 36, 114 / 98
+//   d = 128  32 rows 35 / 37, 89 / 98     40 rows 44 / 37, 125 / 98
+//   d = 192  16 rows 35 / 42, 85 / 115    17 rows 48 / 43, 141 / 115
+//   d = 256  16 rows 48 / 47, 130 / 131   20 rows 60 / 49, 181 / 132
+//   d = 384  16 rows 63 / 77, 186 / 207   20 rows 86 / 79, 270 / 212
+// With fewer tokens it starts a few us later (8 of 2048, first case above the bound: 24 / 21,
+// 20 / 21, 22 / 22, 21 / 23, 26 / 27, 36 / 42).
+bool use_wide(int d, long long rows) { return rows > 8 * most_nt(d) * (d == 192 ? 1 : 2); }
 
 // Three tiles, on units of 32 tokens, where they save the second pass of two row tiles of 16.
 // Measured in us (one of 24 / two of 16): d = 128, 20 rows, 8 requests of 16384 tokens and 8
@@ -49,11 +51,12 @@ struct Plan {
   size_t off_ml, off_cuts, bytes;
 };
 
-bool make_plan(int B, int H, int Hkv, int d, int max_q, int page, int width, Plan& plan) {
+// mean: rows of a request and kv head on average.
+bool make_plan(int B, int H, int Hkv, int d, int max_q, int page, int width, long long mean, Plan& plan) {
   const long long rows = (long long)max_q * (H / Hkv);
   if (rows > 0x7fffffffLL || (long long)B * Hkv > 0x7fffffffLL) return false;
   plan.nt = choose_nt(d, rows);
-  plan.wide = use_wide(d, rows);
+  plan.wide = use_wide(d, std::min(mean, rows));
   const long long tiles = (rows + 8 * plan.nt - 1) / (8 * plan.nt), wide_tiles = (rows + 127) / 128;
   if (tiles * B * Hkv > 0x7fffffffLL / (8 * plan.nt)) return false;
   plan.row_tiles = (int)tiles;
@@ -138,8 +141,11 @@ size_t fa_kv4_attn_workspace_size(int B, int H, int Hkv, int d, int max_q, int p
   if (shape_checks(B, H, Hkv, d, max_q) != FA_OK || page_log2_of(page) < 0 || width < 0) return 0;
   if ((long long)width * page > 0x7fffffffLL) return 0;
   if (B == 0 || H == 0 || max_q == 0) return 0;
-  Plan plan;
-  return make_plan(B, H, Hkv, d, max_q, page, width, plan) ? plan.bytes : 0;
+  // (The queries' mean, which the call knows, decides between two forms: enough for either.)
+  Plan few, many;
+  return make_plan(B, H, Hkv, d, max_q, page, width, 0, few) && make_plan(B, H, Hkv, d, max_q, page, width, 0x7fffffff, many)
+             ? std::max(few.bytes, many.bytes)
+             : 0;
 }
 
 fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_token, long long q_head, int T,
@@ -159,7 +165,8 @@ fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_toke
     return FA_ERR_MISALIGNED;
   if (!cu) max_q = 1;
   Plan plan;
-  if (!make_plan(B, H, Hkv, d, max_q, cache->page, width, plan)) return FA_ERR_INVALID_ARG;
+  const long long mean = ((long long)(cu ? T : B) * (H / Hkv) + B - 1) / B;
+  if (!make_plan(B, H, Hkv, d, max_q, cache->page, width, mean, plan)) return FA_ERR_INVALID_ARG;
   if (plan.bytes &&
       (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.bytes))
     return FA_ERR_WORKSPACE;
