@@ -23,7 +23,11 @@
 // contiguous bytes: the order of a contraction's terms is free, and O's channel
 // order is undone at the store.
 //
-// Reading the cache bounds it in principle; the work per byte is what needs care:
+// Reading the cache bounds it in principle: 64 requests up to 16384 tokens, 8 kv heads, d = 128,
+// group 4 (686 MB) take 126 us, 5450 GB/s; 163 us for each GB and, where all SMs are in
+// use, about 14 us beside that: two launches, four loads that wait for one another, and the
+// first and last units, which are not overlapped.  The issue slots are 63 % used, the ALU
+// pipe 54 %, so the work per byte is what needs care:
 // converting a code costs half a conversion (64 a cycle and SM) and half an f16
 // multiplication.  The legacy tensor path (1024 f16 MACs a cycle and SM, measured)
 // is enough for 8 rows a tile at full bandwidth (about 335 needed), and takes its
