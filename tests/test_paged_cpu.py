@@ -2,6 +2,9 @@
 and the tests' own 64-bit restatements against hand-worked values."""
 
 import math
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -175,6 +178,44 @@ def test_rows_that_overlap_are_no_output():
     for bad in ((64, 64), (64, 128), (120, 64), (0, 64), (128, 56)):
         with pytest.raises(ValueError, match="overlap"):
             layout(*bad)
+
+
+C_CLIENT = r"""
+#include <stdio.h>
+#include <stddef.h>
+#include "fa_paged.h"
+
+int main(void) {
+  int fails = 0;
+  fa_kv4_cache cache = {NULL, NULL, NULL, NULL, 0, 16, 2, 128, 1.0f, 1.0f};
+  if (fa_kv4_store(&cache, NULL, NULL, 0, 0, 0, 0, NULL, 0, NULL) != FA_OK) fails |= 1;
+  if (fa_kv4_load(&cache, NULL, 0, NULL, NULL, NULL) != FA_OK) fails |= 2;
+  cache.d = 80;
+  if (fa_kv4_load(&cache, NULL, 0, NULL, NULL, NULL) != FA_ERR_UNSUPPORTED) fails |= 4;
+  if (fa_page_grow(NULL, NULL, NULL, 0, 0, 16, NULL, 0, NULL, 0, NULL, NULL, NULL, NULL, NULL) != FA_OK) fails |= 8;
+  if (fa_page_slots(NULL, NULL, NULL, 1, 0, 16, 0, NULL, NULL, NULL) != FA_ERR_INVALID_ARG) fails |= 16;
+  if (fa_kv4_attn_workspace_size(1, 8, 2, 128, 1, 16, 100000) == 0) fails |= 32;
+  cache.d = 128;
+  if (fa_kv4_attn(&cache, NULL, 0, 0, 0, NULL, 1, NULL, 0, NULL, 0, 8, 1.0f, NULL, 0, 0, NULL, NULL, 0, NULL) != FA_OK)
+    fails |= 64;
+  printf("%d\n", fails);
+  return fails != 0;
+}
+"""
+
+
+def test_header_is_plain_c_and_a_c_program_links_the_library(tmp_path):
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc not available")
+    src, exe = tmp_path / "client.c", tmp_path / "client"
+    src.write_text(C_CLIENT)
+    libdir = os.path.dirname(b.LIB_PATH)
+    r = subprocess.run([gcc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", f"-I{build.INCLUDE}", str(src), "-o",
+                        str(exe), f"-L{libdir}", "-l:libfa_gb300.so", f"-Wl,-rpath,{libdir}"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0 and out.stdout.strip() == "0", out.stdout + out.stderr
 
 
 def test_reference_codes_and_scales():

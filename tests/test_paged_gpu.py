@@ -614,6 +614,51 @@ def test_store_and_load_at_the_ends_of_the_gains():
         assert np.all(np.abs(to_f64(k) - want) <= 2.0 ** -8 * np.abs(want)) and torch.equal(v, -k)
 
 
+def test_calls_with_nothing_to_do():
+    """No tokens, no requests, no pages, no width, no cached token: shapes, zeros and
+    nothing written."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+
+    def bf16(*shape):
+        return torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda:0")
+
+    none = torch.empty(0, dtype=torch.int64, device="cuda:0")
+    cache = api.KV4Cache.empty(3, 2, 16, 64)
+    api.kv4_store(bf16(0, 2, 64), bf16(0, 2, 64), none, cache)
+    k, v = api.kv4_load(none, cache)
+    assert k.shape == v.shape == (0, 2, 64)
+    o, lse = api.kv4_attention(bf16(0, 4, 64), cache, _i32([]).view(0, 5), _i32([]))
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    o = bf16(3, 4, 64)
+    api.kv4_attention(bf16(3, 4, 64), cache, _i32([[0, 1]] * 2), _i32([9, 9]), _i32([0, 0, 0]), 2, out=o)
+    assert torch.all(o == 7)  # requests without queries
+    for pool, width, length in ((3, 0, 9), (0, 2, 9), (3, 2, 0), (3, 2, -4)):
+        o, lse = api.kv4_attention(bf16(2, 4, 64), api.KV4Cache.empty(pool, 2, 16, 64), _i32([[0] * width] * 2).view(2, width),
+                                   _i32([length] * 2))
+        assert torch.all(o == 0) and torch.all(lse == -math.inf)
+    empty = api.KV4Cache.empty(0, 2, 16, 64)
+    api.kv4_store(bf16(1, 2, 64), bf16(1, 2, 64), torch.zeros(1, dtype=torch.int64, device="cuda:0"), empty)
+    k, v = api.kv4_load(torch.zeros(1, dtype=torch.int64, device="cuda:0"), empty)
+    assert torch.all(k == 0) and torch.all(v == 0)
+    api.check_device_error()
+
+
+def test_profile_counts_the_serving_kernels():
+    import torch
+    from tiled_attention_tmem_gb300 import api, binding as b
+    arrays, table, cu, q, gains = _problem(64, 16, 4, 2, [3000, 5], [1, 1], seed=83)
+    cache, x = _cache_of(arrays, gains), to_dev(q)
+    spare = _dev([len(arrays[0]) * 16], torch.int64)  # past the pool: nothing is stored
+    b.fa_profile_start()
+    api.page_slots(_i32([0, 0]), _i32([1, 1]), _i32(table), 16, 2)
+    api.kv4_store(x[:1, :2], x[:1, 2:], spare, cache)
+    api.kv4_load(spare, cache)
+    api.kv4_attention(x, cache, _i32(table), _i32([3000, 5]))
+    prof = b.fa_profile_stop()
+    assert {k: n for k, (n, _) in prof.items() if n} == dict(page=1, kv4_store=1, kv4_load=1, kv4_attn=1, kv4_merge=1)
+
+
 # ------------------------------------------------------------------ together
 
 def _serve(api, torch, page, kv, group, d, prompts, steps, seed, stream=None):
