@@ -25,15 +25,15 @@ int choose_nt(int d, long long rows) {
 // The tcgen05 kernel takes a call whose requests have this many rows a kv head on average: the
 // narrow tiles read and convert the cache again for each, its own time hardly depends on the
 // rows.  Measured in us (narrow / wide), 8 / 32 requests of 8192 tokens and 4 kv heads:
-//   d = 64   64 rows 33 / 33, 90 / 90     96 rows 44 / 34, 127 / 93
-//   d = 96   32 rows 29 / 35, 81 / 98     40 rows 39 / 36, 114 / 98
-//   d = 128  32 rows 35 / 37, 89 / 98     40 rows 44 / 37, 125 / 98
-//   d = 192  16 rows 35 / 42, 85 / 115    17 rows 48 / 43, 141 / 115
-//   d = 256  16 rows 48 / 47, 130 / 131   20 rows 60 / 49, 181 / 132
-//   d = 384  16 rows 63 / 77, 186 / 207   20 rows 86 / 79, 270 / 212
+//   d = 64   64 rows 32 / 32, 89 / 89     96 rows 43 / 33, 127 / 92
+//   d = 96   32 rows 29 / 34, 81 / 97     40 rows 38 / 35, 114 / 97
+//   d = 128  32 rows 34 / 36, 88 / 98     40 rows 44 / 37, 125 / 98
+//   d = 192  16 rows 35 / 41, 85 / 113    17 rows 48 / 41, 141 / 113
+//   d = 256  8 rows 34 / 42, 77 / 118     9 rows 44 / 42, 127 / 118
+//   d = 384  16 rows 63 / 67, 186 / 195   20 rows 86 / 69, 269 / 197
 // With fewer tokens it starts a few us later (8 of 2048, first case above the bound: 24 / 21,
-// 20 / 21, 22 / 22, 21 / 23, 26 / 27, 36 / 42).
-bool use_wide(int d, long long rows) { return rows > 8 * most_nt(d) * (d == 192 ? 1 : 2); }
+// 20 / 20, 22 / 21, 21 / 22, 21 / 23, 36 / 35).
+bool use_wide(int d, long long rows) { return rows > 8 * most_nt(d) * (d == 192 || d == 256 ? 1 : 2); }
 
 // Three tiles, on units of 32 tokens, where they save the second pass of two row tiles of 16.
 // Measured in us (one of 24 / two of 16): d = 128, 20 rows, 8 requests of 16384 tokens and 8

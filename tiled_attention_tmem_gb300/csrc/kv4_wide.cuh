@@ -48,7 +48,8 @@ __device__ __forceinline__ bool wait_asleep(uint32_t bar, uint32_t parity, const
 
 template <int D_>
 struct Kv4WideCfg {
-  static constexpr int D = D_, ROWS = 128, UNIT = 64;
+  // Units of 32 tokens at d = 384, so that two operand slots each for K and V fit beside Q.
+  static constexpr int D = D_, ROWS = 128, UNIT = D <= 256 ? 64 : 32;
   static constexpr int CONVERT = 8;  // warps
   static constexpr int MMA_WARP = 4 + CONVERT, COPY_WARP = MMA_WARP + 1, THREADS = 32 * (COPY_WARP + 2);
   static constexpr int CODE_ROW = D / 2, SCALE_ROW = D / 16;
@@ -58,8 +59,8 @@ struct Kv4WideCfg {
   static constexpr bool QT = D <= 256;  // Q in TMEM
   static constexpr int Q_PANEL = ROWS * 128, Q_BYTES = QT ? 0 : PANELS * Q_PANEL;
   // Operand slots few, staging slots many: what is on its way has to cover memory's latency.
-  static constexpr int TILES = D <= 128 ? 6 : D <= 256 ? 4 : 2;
-  static constexpr int STAGED = D <= 128 ? 22 : D == 192 ? 16 : D == 256 ? 8 : 2;
+  static constexpr int TILES = D <= 128 ? 6 : 4;
+  static constexpr int STAGED = D <= 128 ? 22 : D == 192 ? 16 : D == 256 ? 8 : 4;
   static constexpr int OFF_Q = TILES * TILE, OFF_STAGE = OFF_Q + Q_BYTES;
   static constexpr int OFF_BAR = OFF_STAGE + STAGED * PART;
   // Barriers: staging full and empty, operand full and empty, then S, P, O (two each), Q, done.
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
     cur.u += n - 1;
     kv4_advance<C>(p, req, cur);
   };
-  const int fr_log2 = min(p.page_log2, 6);
+  const int fr_log2 = min(p.page_log2, UNIT == 64 ? 6 : 5);
 
   if (warp >= C::COPY_WARP) {
     // ------------------------------------------------------------------ copies
@@ -348,35 +349,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
       const bool have = i < cur.nq;
       const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(cur.tok0 + (have ? i : 0)) * p.q_token +
                                                         (long long)(cur.kvh * p.G + h) * p.q_head);
-      // 64 channels at a time with all their loads in flight; twice, first for the largest
-      // magnitude (as bf16 bits), which gives the power of two.
+      // CH channels at a time with all their loads in flight: the whole row where the registers
+      // hold it, else twice, first for the largest magnitude (as bf16 bits), which gives the
+      // power of two.
+      constexpr int CH = D <= 128 ? D : D == 192 ? 96 : 128, N = CH / 8, ONCE = CH == D;
       uint32_t top = 0;
-      float down = 0.f;
 #pragma unroll 1
-      for (int c0 = 0; c0 < 2 * D; c0 += (D % 64 ? 32 : 64)) {
-        constexpr int N = D % 64 ? 4 : 8;  // loads of eight channels
+      for (int c0 = 0; c0 < (ONCE ? D : 2 * D); c0 += CH) {
         const int c = c0 < D ? c0 : c0 - D;
         uint4 x[N];
 #pragma unroll
         for (int u = 0; u < N; ++u) x[u] = have ? src[c / 8 + u] : make_uint4(0u, 0u, 0u, 0u);
-        if (c0 == D) down = __uint_as_float((uint32_t)(127 - exponent(top)) << 23);
+        if (c0 < D) {
+#pragma unroll
+          for (int u = 0; u < N; ++u) {
+            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+          }
+          if (!ONCE) continue;
+        }
+        const float down = __uint_as_float((uint32_t)(127 - exponent(top)) << 23);
         uint32_t qw[4 * N];
 #pragma unroll
         for (int u = 0; u < N; ++u) {
           const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (c0 < D) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+          for (int k = 0; k < 4; ++k)
             qw[4 * u + k] = pack_f16(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-          }
         }
-        if (c0 < D) continue;
         if constexpr (C::QT) {
           __syncwarp();
-          if constexpr (N == 8)
-            tmem_st_32x32b_x32(trow + C::TMEM_Q + (c >> 1), qw);
-          else
-            tmem_st_32x32b_x16(trow + C::TMEM_Q + (c >> 1), qw);
+#pragma unroll
+          for (int k = 0; k < 4 * N; k += 32) {
+            if (4 * N - k >= 32)
+              tmem_st_32x32b_x32(trow + C::TMEM_Q + (c >> 1) + k, qw + k);
+            else
+              tmem_st_32x32b_x16(trow + C::TMEM_Q + (c >> 1) + k, qw + k);
+          }
         } else {
 #pragma unroll
           for (int u = 0; u < N; ++u) {
@@ -429,7 +439,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
         if (busy) {
           uint32_t sr[UNIT];
           tmem_ld_32x32b_x32(tS, sr);
-          tmem_ld_32x32b_x32(tS + 32, sr + 32);
+          if constexpr (UNIT == 64) tmem_ld_32x32b_x32(tS + 32, sr + 32);
           tmem_wait_ld();
           reg_fence<UNIT>(sr);
           const uint32_t bits = unit_bits[g & 31];
@@ -463,7 +473,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
             pk[c >> 1] = pack_f16(a, b);
           }
           l += la + lb;
-          tmem_st_32x32b_x32(tS, pk);
+          if constexpr (UNIT == 64)
+            tmem_st_32x32b_x32(tS, pk);
+          else
+            tmem_st_32x32b_x16(tS, pk);
           tmem_wait_st();
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
             // The running O, once the MMA that added to it last is done.
