@@ -819,3 +819,36 @@ def test_a_set_error_word_stops_the_attention_and_its_merge(heads, lengths):
     api.kv4_attention(*args, out=o, lse=l)
     api.check_device_error()
     assert torch.equal(o, want) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("heads,kv,d", [(4, 2, 128), (20, 1, 96), (80, 1, 64), (40, 1, 384)],
+                         ids=["split", "24_rows", "many_rows", "many_rows_384"])
+def test_graphs_that_share_a_workspace_follow_new_lengths(heads, kv, d):
+    """Two captured graphs over one workspace, replayed in turn while lengths change in place."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    lengths = [6000, 1200, 3]
+    arrays, table, _, _, gains = _problem(d, 64, heads, kv, lengths, [1, 1, 1], seed=89)
+    cache, tab, held = _cache_of(arrays, gains), _i32(table), _i32(lengths)
+    qs = [torch.randn((3, heads, d), device="cuda:0").to(torch.bfloat16) for _ in range(2)]
+    ws = torch.empty(max(api.kv4_attention_workspace_bytes(3, heads, cache, table.shape[1]), 1), dtype=torch.uint8, device="cuda:0")
+    assert ws.numel() > 1
+    api.kv4_attention(qs[0], cache, tab, held, workspace=ws)
+    graphs, stream = [], torch.cuda.Stream()
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            out = api.kv4_attention(q, cache, tab, held, workspace=ws)
+        graphs.append((g, out))
+    for new in (lengths, [1, 0, 3], [6000, 1199, 2], [511, 64, 1]):
+        held.copy_(_i32(new))
+        for (g, out), q in zip(graphs, qs):
+            g.replay()
+            want = api.kv4_attention(q, cache, tab, held)
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    for g, _ in graphs * 10:  # back to back
+        g.replay()
+    for (_, out), q in zip(graphs, qs):
+        want = api.kv4_attention(q, cache, tab, held)
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    api.check_device_error()
