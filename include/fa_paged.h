@@ -83,7 +83,8 @@ fa_status fa_page_slots(const int* first, const int* count, const int* table, in
  * Writes T tokens of k and v (bf16 [T, Hkv, d], element strides of the token
  * and the head given, multiples of 8; the channels dense) into the cache.  Per
  * group of 16 channels, in fp32: scale = e4m3(max|x| / (6 gain)), code =
- * e2m1(x / (gain scale)), each rounded to nearest even and saturating.  The
+ * e2m1(x / (gain scale)), each rounded to nearest even and saturating (scale 0:
+ * codes of 0 with the signs of x).  The
  * quotients are good to 12 bits: exact in effect where the gain is a power of
  * two, else a quotient within 2^-12 of a border may go either way.  A NaN
  * becomes code 6 under the scale of the others.
