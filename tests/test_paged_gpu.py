@@ -852,3 +852,42 @@ def test_graphs_that_share_a_workspace_follow_new_lengths(heads, kv, d):
         want = api.kv4_attention(q, cache, tab, held)
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
     api.check_device_error()
+
+
+def test_stream_zero_is_the_default_stream(monkeypatch):
+    """Handle 0 as the stream of every call, while another stream is current: each kernel is
+    launched on the default stream, and what is allocated belongs to it."""
+    import torch
+    from tiled_attention_tmem_gb300 import api, binding as b, serving
+    lengths = [3000, 40]
+    arrays, table, cu, q, gains = _problem(64, 16, 4, 2, lengths, [1, 1], seed=97)
+    cache, x, tab, held = _cache_of(arrays, gains), to_dev(q), _i32(table), _i32(lengths)
+    free, count, slots = _i32([5]), _i32([1]), _dev([len(arrays[0]) * 16] * 2, torch.int64)
+    streams = []
+
+    class Lib:
+        def __getattr__(self, name):
+            call = getattr(real, name)
+            if not name.startswith(("fa_page", "fa_kv4")) or name.endswith("_size"):
+                return call
+            return lambda *a: (streams.append(a[-1]), call(*a))[1]
+
+    real = b.lib()
+    monkeypatch.setattr(b, "lib", Lib)
+    side = torch.cuda.Stream()
+    assert torch.cuda.default_stream().cuda_stream == 0 and side.cuda_stream != 0
+    want = api.kv4_attention(x, cache, tab, held)
+    torch.cuda.synchronize()
+    streams.clear()
+    with torch.cuda.stream(side):
+        api.page_grow(held, _i32([0, 0]), tab, free, count, 16, 2, stream=0)
+        api.page_slots(held, _i32([0, 0]), tab, 16, 2, stream=0)
+        api.kv4_store(x[:, :2], x[:, 2:], slots, cache, stream=0)
+        api.kv4_load(slots, cache, stream=0)
+        got = api.kv4_attention(x, cache, tab, held, stream=0)
+        with serving._On(0, 0):
+            assert torch.cuda.current_stream().cuda_stream == 0
+        assert torch.cuda.current_stream() == side
+    assert streams == [0] * 5
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -38,7 +38,9 @@ class _On:
     def __init__(self, index, stream):
         self.stack = [torch.cuda.device(index)]
         if stream is not None:
-            self.stack.append(torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index)))
+            # (0 is the default stream; ExternalStream(0) would be a new one.)
+            s = torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index)
+            self.stack.append(torch.cuda.stream(s))
 
     def __enter__(self):
         for c in self.stack:
