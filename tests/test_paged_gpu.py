@@ -891,3 +891,20 @@ def test_stream_zero_is_the_default_stream(monkeypatch):
     assert streams == [0] * 5
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("heads,kv,lengths,queries", [
+    (4, 2, [30, 9, 100], [5, 2, 7]), (64, 1, [30, 9, 2000], [3, 0, 2]), (6, 1, [3000, 1, 700], [4, 1, 2])], ids=str)
+def test_attention_with_offsets_alone_computes_every_query(heads, kv, lengths, queries):
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    arrays, table, cu, q, gains = _problem(64, 16, heads, kv, lengths, queries, seed=101, pad=2)
+    o = torch.full((len(q), heads, 64), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    lse = torch.full((len(q), heads), 7.0, device="cuda:0")
+    args = to_dev(q), _cache_of(arrays, gains), _i32(table), _i32(lengths), _i32(cu)
+    api.kv4_attention(*args, out=o, lse=lse)
+    api.check_device_error()
+    ref = _reference(arrays, gains, table, cu, q, lengths, max(queries), 1 / 8)
+    own = int(cu[-1])
+    R.check(to_f64(o)[:own], to_f64(lse)[:own], tuple(x[:own] for x in ref), 64)
+    assert torch.all(o[own:] == 7) and torch.all(lse[own:] == 7)

@@ -272,20 +272,22 @@ _workspace_bytes = functools.lru_cache(maxsize=1024)(lambda *shape_and_device: _
     *shape_and_device[:-1]))
 
 
-def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int = 1, scale: float | None = None,
-                  out=None, lse=None, workspace=None, stream=None):
+def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int | None = None,
+                  scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
     """Attention of each request's newest tokens over its cached keys and values.
 
     q bf16 [T, heads, d] (token and head strides free, in eights; heads a multiple of
     the cache's); table int32 [B, width]; lengths int32 [B]: tokens of each request in
     the cache, the queries' own included; cu_q int32 [B + 1]: where each request's
-    queries begin in q (None: one each), of which the first ``max_q`` are computed.  Query
+    queries begin in q (None: one each), of which the first ``max_q`` are computed (None:
+    all; the most that a request has is the better bound).  Query
     i of a request's n sees the tokens up to lengths - n + i.  Returns (o bf16 [T, heads,
     d], lse fp32 [T, heads]); a query that sees nothing gets o = 0 and lse = -inf, rows of
     no request are left as they were (in ``out`` and ``lse``, given or new; ``out`` may be q).
     The table's width and ``max_q`` choose the kernel, so neither should be much larger than
     the longest request.  ``workspace``: a uint8 CUDA tensor of
-    ``kv4_attention_workspace_bytes``, not shared with a concurrent call, or None."""
+    ``kv4_attention_workspace_bytes`` (of the same ``max_q``), not shared with a concurrent
+    call, or None."""
     c = cache
     index = c.index
     if stream is not None or _current_device() != index:
@@ -308,6 +310,8 @@ def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int = 1,
                 and cu_q.get_device() == index and cu_q.is_contiguous()):
             _dense(cu_q, "cu_q", _I32, (B + 1,), index)
         offsets = cu_q.data_ptr()
+        if max_q is None:
+            max_q = T
     else:
         offsets, max_q = None, 1
         if T < B:
