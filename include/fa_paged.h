@@ -52,7 +52,7 @@ typedef struct {
  *   lengths     int32 [B]         tokens each request holds (negative: 0)
  *   new_tokens  int32 [B]         tokens each request gets now (negative: 0)
  *   table       int32 [B, width]  read; entries of pages taken now are written
- *   free_pages  int32 [free_size] stack of free pages, read only
+ *   free_pages  int32 [free_size] stack of free pages, read only (NULL where free_size is 0)
  *   free_count  int32 [1]         pages on the stack (above free_size: free_size)
  *   T           capacity of `slots`
  *   slots       int64 [T]         slot of new token t, requests in order; -1 for a
@@ -64,7 +64,7 @@ typedef struct {
  * most up to `width`) are taken from the top of the stack in request order.
  * When the stack runs out, its entries become -1, and tokens on them, past
  * `width` or past T get no slot: then lengths_out[b] < lengths[b] + new_tokens[b].
- * B at most 2^21, width * page below 2^31.
+ * B at most 2^21, width * page below 2^31.  With B = 0 nothing is written.
  * Inputs are not changed except `table`, so a repeated call gives the same
  * result; the outputs must not overlap the inputs.
  */

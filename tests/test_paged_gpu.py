@@ -908,3 +908,21 @@ def test_attention_with_offsets_alone_computes_every_query(heads, kv, lengths, q
     own = int(cu[-1])
     R.check(to_f64(o)[:own], to_f64(lse)[:own], tuple(x[:own] for x in ref), 64)
     assert torch.all(o[own:] == 7) and torch.all(lse[own:] == 7)
+
+
+@pytest.mark.parametrize("page,T", [(16, 40), (64, 7)])
+def test_page_grow_with_an_empty_stack(page, T):
+    """No page is free: tokens that fit the last page owned get slots, the others none."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    held, add = [0, 5, page, 2 * page - 1, 3], [4, 2, 1, 9, 0]
+    table = np.arange(15).reshape(5, 3) + 20
+    none = torch.arange(4, dtype=torch.int32, device="cuda:0")[:0]
+    assert none.data_ptr() == 0
+    for count in (0, 5):
+        t = _i32(table)
+        got = api.page_grow(_i32(held), _i32(add), t, none, _i32([count]), page, T)
+        ref = R.pages(held, add, table, [], 0, page, T)
+        for g, r in zip(got, (ref[0], ref[1], ref[3], [0])):
+            assert np.array_equal(g.cpu().numpy(), r)
+        assert np.array_equal(t.cpu().numpy(), ref[2])

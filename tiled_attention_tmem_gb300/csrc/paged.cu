@@ -18,7 +18,7 @@ struct PageParams {
   const int* held;   // tokens held (grow) or first position (slots only)
   const int* add;    // tokens to place
   int* table;
-  const int* free_pages;  // NULL: slots only
+  const int* free_pages;  // (NULL: an empty stack)
   const int* free_count;
   long long* slots;
   int* cu;
@@ -26,6 +26,7 @@ struct PageParams {
   int* count_out;
   int B, width, page_log2, T, free_size;
   int per_block;  // requests per block (grid.x)
+  bool grow;      // else slots only
 };
 
 constexpr int kPageThreads = 256;
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(kPageThreads) page_kernel(const __grid_constan
     add = (int)(min(raw + max(p.add[b], 0), (long long)p.T) - cu);
     owned = (held >> p.page_log2) + ((held & (page - 1)) ? 1 : 0);
     const long long wanted = min(((long long)held + add + page - 1) >> p.page_log2, (long long)p.width);
-    return p.free_pages ? (int)max(wanted - owned, 0LL) : 0;
+    return p.grow ? (int)max(wanted - owned, 0LL) : 0;
   };
   long long need_sum = 0, raw = new0;
   for (int b = b0; b < b1; ++b) {
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kPageThreads) page_kernel(const __grid_constan
     raw += max(p.add[b], 0);
   }
   long long off = 0;
-  if (p.free_pages) off = block_scan(need_sum, warp_sums, total_need);
+  if (p.grow) off = block_scan(need_sum, warp_sums, total_need);
   raw = new0;
   for (int b = b0; b < b1; ++b) {
     int held, cu, add, owned;
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kPageThreads) page_kernel(const __grid_constan
     if (b >= my0 && b < my1) rows[b - my0] = PageRow{off, held, add, cu, owned, need};
     off += need;
   }
-  const int count = p.free_pages ? min(max(*p.free_count, 0), p.free_size) : 0;
+  const int count = p.grow ? min(max(*p.free_count, 0), p.free_size) : 0;
   const int total = (int)min(total_new, (long long)p.T);
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
     p.cu[p.B] = total;
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kPageThreads) page_kernel(const __grid_constan
       const long long col = pos >> p.page_log2;
       int id = -1;
       if (col < p.width) {
-        if (!p.free_pages || col < r.owned) {
+        if (!p.grow || col < r.owned) {
           id = entry[col];
         } else {
           const long long src = count - 1 - r.off - (col - r.owned);
@@ -389,11 +390,11 @@ fa_status fa_page_grow(const int* lengths, const int* new_tokens, int* table, in
                        int* lengths_out, int* count_out, void* stream) {
   if (!pages_ok(B, width, page, T) || free_size < 0) return FA_ERR_INVALID_ARG;
   if (B == 0) return FA_OK;
-  if (!lengths || !new_tokens || !free_pages || !free_count || !cu || !lengths_out || !count_out)
-    return FA_ERR_INVALID_ARG;
+  if (!lengths || !new_tokens || !free_count || !cu || !lengths_out || !count_out) return FA_ERR_INVALID_ARG;
+  if (free_size > 0 && !free_pages) return FA_ERR_INVALID_ARG;
   if ((width > 0 && !table) || (T > 0 && !slots)) return FA_ERR_INVALID_ARG;
   PageParams p = {lengths, new_tokens, table, free_pages, free_count, slots, cu, lengths_out, count_out,
-                  B, width, page_log2_of(page), T, free_size, 0};
+                  B, width, page_log2_of(page), T, free_size, 0, true};
   return run_pages(p, (cudaStream_t)stream);
 }
 
@@ -403,7 +404,7 @@ fa_status fa_page_slots(const int* first, const int* count, const int* table, in
   if (B == 0) return FA_OK;
   if (!first || !count || !cu || (width > 0 && !table) || (T > 0 && !slots)) return FA_ERR_INVALID_ARG;
   PageParams p = {first, count, const_cast<int*>(table), nullptr, nullptr, slots, cu, nullptr, nullptr,
-                  B, width, page_log2_of(page), T, 0, 0};
+                  B, width, page_log2_of(page), T, 0, 0, false};
   return run_pages(p, (cudaStream_t)stream);
 }
 
