@@ -926,3 +926,30 @@ def test_page_grow_with_an_empty_stack(page, T):
         for g, r in zip(got, (ref[0], ref[1], ref[3], [0])):
             assert np.array_equal(g.cpu().numpy(), r)
         assert np.array_equal(t.cpu().numpy(), ref[2])
+
+
+@pytest.mark.parametrize("heads,kv,lengths", [(2, 1, [40, 20]), (4, 2, [9000, 700]), (80, 1, [5000, 700])],
+                         ids=["block", "split", "many_rows"])
+def test_attention_of_offsets_that_leave_the_queries(heads, kv, lengths):
+    """Offsets that leave q or run backwards: those requests have no queries, the others'
+    rows are right, and every other byte of the buffers around q, o and lse is as it was."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    T, max_q, most, least = 6, 4, (1 << 31) - 1, -(1 << 31)
+    arrays, table, _, q, gains = _problem(64, 16, heads, kv, lengths, [T, 0], seed=103, pad=6)
+    cache, tab, held = _cache_of(arrays, gains), _i32(table), _i32(lengths)
+    wide_q = to_dev(q)  # six rows between three and three more
+    for cu, valid in (([0, 5, 9], [0]), ([-3, 1, 2], [1]), ([2, 0, 1], [1]), ([1 << 30, (1 << 30) + 1, 3], []),
+                      ([0, 7, 7], []), ([0, 2, 7], [0]), ([1, 6, 6], [0]), ([0, 2, most], [0]), ([least, most, 3], []),
+                      ([least, least, 6], []), ([most, least, 0], []), ([0, 0, 6], [1]), ([4, 6, 2], [0])):
+        o = torch.full((T + 6, heads, 64), 7.0, dtype=torch.bfloat16, device="cuda:0")
+        lse = torch.full((T + 6, heads), 7.0, device="cuda:0")
+        api.kv4_attention(wide_q[3:3 + T], cache, tab, held, _i32(cu), max_q, out=o[3:3 + T], lse=lse[3:3 + T])
+        api.check_device_error()
+        mine = torch.zeros(T + 6, dtype=torch.bool, device="cuda:0")
+        for b in valid:
+            rows = slice(cu[b], min(cu[b + 1], cu[b] + max_q))
+            mine[3 + rows.start:3 + rows.stop] = True
+            ref = _reference(arrays, gains, table[b:b + 1], [cu[b], cu[b + 1]], q[3:3 + T], lengths[b:b + 1], max_q, 1 / 8)
+            R.check(to_f64(o)[3:3 + T][rows], to_f64(lse)[3:3 + T][rows], tuple(x[rows] for x in ref), 64, str(cu))
+        assert torch.all(o[~mine] == 7) and torch.all(lse[~mine] == 7), cu

@@ -124,7 +124,7 @@ __device__ __forceinline__ void kv4_lookup(const Kv4AttnParams& p, int b, Kv4Cur
     const long long nq = (long long)p.cu[b + 1] - c.tok0;
     c.nq = (int)min(max(nq, 0LL), (long long)p.max_q);
     c.first = (int)max(c.n - max(nq, 0LL), -0x7fffffffLL);
-    if (c.tok0 < 0 || c.tok0 > p.T - c.nq) c.nq = 0;  // queries outside q: not computed
+    if (c.tok0 < 0 || c.tok0 + nq > p.T) c.nq = 0;  // queries outside q, past max_q or not: none is computed
   } else {
     c.tok0 = b;
     c.nq = 1;
