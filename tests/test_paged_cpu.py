@@ -248,3 +248,19 @@ def test_reference_pages_by_hand():
     assert list(cu) == [0, 3, 4, 4] and list(held) == [18, 1, 32] and left == 1
     assert list(slots) == [9 * 16 + 15, 7 * 16, 7 * 16 + 1, 6 * 16, -1, -1]
     assert table.tolist() == [[9, 7], [6, 9], [9, 9]]
+
+
+def test_numbers_past_31_bits_are_refused_not_cut():
+    i32 = torch.zeros(2, dtype=torch.int32)
+    table = torch.zeros((2, 4), dtype=torch.int32)
+    for tokens in (1 << 31, (1 << 32) + 4):
+        with pytest.raises(ValueError, match="2\\^31"):
+            api.page_slots(i32, i32, table, 16, tokens)
+        with pytest.raises(ValueError, match="2\\^31"):
+            api.page_grow(i32, i32, table, i32, i32[:1], 16, tokens)
+    for sizes in ((1 << 31, 8, 4, 1), (2, 1 << 32, 4, 1), (2, 8, (1 << 32) + 4, 1), (2, 8, 4, (1 << 32) + 1)):
+        batch, heads, width, max_q = sizes
+        with pytest.raises(ValueError, match="2\\^31"):
+            api.kv4_attention_workspace_bytes(batch, heads, None, width, max_q)
+    with pytest.raises(ValueError, match="2\\^31"):
+        serving._slot_count(torch.empty((1 << 32) + 1, dtype=torch.int64, device="meta"), -1)

@@ -953,3 +953,15 @@ def test_attention_of_offsets_that_leave_the_queries(heads, kv, lengths):
             ref = _reference(arrays, gains, table[b:b + 1], [cu[b], cu[b + 1]], q[3:3 + T], lengths[b:b + 1], max_q, 1 / 8)
             R.check(to_f64(o)[3:3 + T][rows], to_f64(lse)[3:3 + T][rows], tuple(x[rows] for x in ref), 64, str(cu))
         assert torch.all(o[~mine] == 7) and torch.all(lse[~mine] == 7), cu
+
+
+def test_attention_refuses_a_max_q_past_31_bits():
+    """2^32 + 1 would be cut to 1 on its way to the library: the first query of each request."""
+    from tiled_attention_tmem_gb300 import api
+    arrays, table, cu, q, gains = _problem(64, 16, 2, 1, [40, 20], [3, 2], seed=107)
+    args = to_dev(q), _cache_of(arrays, gains), _i32(table), _i32([40, 20]), _i32(cu)
+    for max_q in (1 << 31, (1 << 32) + 1):
+        with pytest.raises(ValueError, match="max_q"):
+            api.kv4_attention(*args, max_q)
+    with pytest.raises(RuntimeError, match="invalid"):
+        api.kv4_attention(*args, -1)

@@ -18,6 +18,8 @@ from . import binding as _b
 
 PAGE_SIZES = (16, 32, 64, 128)
 
+_MOST = 2 ** 31 - 1  # (the binding would cut larger numbers to their low 32 bits)
+
 _I32, _I64, _BF16, _F32, _U8 = torch.int32, torch.int64, torch.bfloat16, torch.float32, torch.uint8
 _empty, _Tensor = torch.empty, torch.Tensor
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -102,11 +104,16 @@ def _rows(t, name, shape, index, written=False):
     return st, sh
 
 
+def _check_sizes(*sizes):
+    if max(sizes) > _MOST:
+        raise ValueError("sizes must be below 2^31")
+
+
 def _check_pages(per_request, table, page_size, num_tokens):
     if page_size not in PAGE_SIZES:
         raise ValueError(f"page_size must be one of {PAGE_SIZES}")
-    if num_tokens < 0:
-        raise ValueError("num_tokens must not be negative")
+    if not 0 <= num_tokens <= _MOST:
+        raise ValueError("num_tokens must not be negative, nor 2^31 or more")
     first, name = per_request[0]
     if not isinstance(first, _Tensor) or first.dim() != 1:
         raise ValueError(f"{name} must be a 1-D int32 tensor")
@@ -114,6 +121,7 @@ def _check_pages(per_request, table, page_size, num_tokens):
     for t, name in per_request:
         _dense(t, name, _I32, first.shape, index)
     _dense(table, "table", _I32, (first.shape[0], None), index)
+    _check_sizes(*table.shape)
 
 
 def page_grow(lengths, new_tokens, table, free_pages, free_count, page_size, num_tokens, stream=None):
@@ -134,6 +142,7 @@ def page_grow(lengths, new_tokens, table, free_pages, free_count, page_size, num
         fine = (index >= 0 and rows == B and lengths.dtype is _I32 and new_tokens.dtype is _I32 and table.dtype is _I32
                 and free_pages.dtype is _I32 and free_count.dtype is _I32 and new_tokens.shape == (B,)
                 and free_count.shape == (1,) and free_pages.dim() == 1 and page_size in PAGE_SIZES and num_tokens >= 0
+                and max(B, width, num_tokens, free_pages.shape[0]) <= _MOST
                 and new_tokens.get_device() == index and table.get_device() == index
                 and free_pages.get_device() == index and free_count.get_device() == index
                 and lengths.is_contiguous() and new_tokens.is_contiguous() and table.is_contiguous()
@@ -144,6 +153,7 @@ def page_grow(lengths, new_tokens, table, free_pages, free_count, page_size, num
         _check_pages([(lengths, "lengths"), (new_tokens, "new_tokens")], table, page_size, num_tokens)
         _dense(free_pages, "free_pages", _I32, (None,), lengths.get_device())
         _dense(free_count, "free_count", _I32, (1,), lengths.get_device())
+        _check_sizes(free_pages.shape[0])
     if stream is not None or _current_device() != index:
         with _On(index, stream):
             return page_grow(lengths, new_tokens, table, free_pages, free_count, page_size, num_tokens)
@@ -195,6 +205,7 @@ class KV4Cache:
         _dense(k_codes, "k_codes", _U8, (None,) * 4)
         index = k_codes.get_device()
         pages, heads, page, half = k_codes.shape
+        _check_sizes(pages, heads)
         if page not in PAGE_SIZES:
             raise ValueError(f"the page size must be one of {PAGE_SIZES}, not {page}")
         if 2 * half not in (64, 96, 128, 192, 256, 384):
@@ -224,7 +235,10 @@ def _slot_count(slots, index):
     if not (isinstance(slots, _Tensor) and slots.dtype is _I64 and slots.dim() == 1 and slots.get_device() == index
             and slots.is_contiguous()):
         _dense(slots, "slots", _I64, (None,), index)
-    return slots.shape[0]
+    T = slots.shape[0]
+    if T > _MOST:
+        _check_sizes(T)
+    return T
 
 
 def kv4_store(k, v, slots, cache: KV4Cache, stream=None):
@@ -261,6 +275,7 @@ def kv4_load(slots, cache: KV4Cache, stream=None):
 
 def kv4_attention_workspace_bytes(batch, heads, cache: KV4Cache, width, max_q=1) -> int:
     """What ``kv4_attention`` needs for a table of ``width`` pages a request (0: none)."""
+    _check_sizes(batch, heads, width, max_q)
     if _current_device() != cache.index:
         with _On(cache.index, None):
             return kv4_attention_workspace_bytes(batch, heads, cache, width, max_q)
@@ -302,6 +317,8 @@ def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int | No
             and table.is_contiguous()):
         _dense(table, "table", _I32, (None, None), index)
     B, width = table.shape
+    if B > _MOST or width > _MOST:
+        _check_sizes(B, width)
     if not (isinstance(lengths, _Tensor) and lengths.dtype is _I32 and lengths.shape == (B,)
             and lengths.get_device() == index and lengths.is_contiguous()):
         _dense(lengths, "lengths", _I32, (B,), index)
@@ -312,6 +329,8 @@ def kv4_attention(q, cache: KV4Cache, table, lengths, cu_q=None, max_q: int | No
         offsets = cu_q.data_ptr()
         if max_q is None:
             max_q = T
+        if max_q > _MOST:
+            raise ValueError("max_q must be below 2^31")
     else:
         offsets, max_q = None, 1
         if T < B:
