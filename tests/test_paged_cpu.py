@@ -264,3 +264,11 @@ def test_numbers_past_31_bits_are_refused_not_cut():
             api.kv4_attention_workspace_bytes(batch, heads, None, width, max_q)
     with pytest.raises(ValueError, match="2\\^31"):
         serving._slot_count(torch.empty((1 << 32) + 1, dtype=torch.int64, device="meta"), -1)
+
+
+@pytest.mark.parametrize("head_dim", [65, 79, 129, 80, 0, 512])
+def test_empty_cache_of_an_unsupported_head_dimension_is_refused(head_dim, monkeypatch):
+    monkeypatch.setattr(serving, "_dense", lambda *a: None)  # (the arrays are on the host here)
+    with pytest.raises(ValueError, match="head dimension"):
+        api.KV4Cache.empty(2, 1, 16, head_dim, device="cpu")
+    assert api.KV4Cache.empty(2, 1, 16, 64, device="cpu").head_dim == 64

@@ -17,6 +17,7 @@ import torch
 from . import binding as _b
 
 PAGE_SIZES = (16, 32, 64, 128)
+HEAD_DIMS = (64, 96, 128, 192, 256, 384)
 
 _MOST = 2 ** 31 - 1  # (the binding would cut larger numbers to their low 32 bits)
 
@@ -208,7 +209,7 @@ class KV4Cache:
         _check_sizes(pages, heads)
         if page not in PAGE_SIZES:
             raise ValueError(f"the page size must be one of {PAGE_SIZES}, not {page}")
-        if 2 * half not in (64, 96, 128, 192, 256, 384):
+        if 2 * half not in HEAD_DIMS:
             raise ValueError(f"unsupported head dimension {2 * half}")
         _dense(v_codes, "v_codes", _U8, k_codes.shape, index)
         for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
@@ -226,6 +227,8 @@ class KV4Cache:
     @classmethod
     def empty(cls, pages, kv_heads, page_size, head_dim, k_gain: float = 1.0, v_gain: float = 1.0, device="cuda"):
         """A cache of zeros."""
+        if head_dim not in HEAD_DIMS:
+            raise ValueError(f"unsupported head dimension {head_dim}")
         parts = [torch.zeros((pages, kv_heads, page_size, n), dtype=_U8, device=device)
                  for n in (head_dim // 2, head_dim // 16) * 2]
         return cls(*parts, k_gain, v_gain)
