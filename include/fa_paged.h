@@ -20,7 +20,8 @@
  * stride `width`) is the page that holds tokens c*page .. c*page + page - 1 of
  * request b.  d: 64, 96, 128, 192, 256 or 384.
  *
- * Every array argument is device memory owned by the caller.  The contents of
+ * Every array argument is device memory owned by the caller, index arrays and lse
+ * aligned to their elements (else FA_ERR_MISALIGNED).  The contents of
  * index arrays are checked on the device where they are used: an index that is
  * out of range is skipped as each call states, and never read or written through.
  */

@@ -272,3 +272,25 @@ def test_empty_cache_of_an_unsupported_head_dimension_is_refused(head_dim, monke
     with pytest.raises(ValueError, match="head dimension"):
         api.KV4Cache.empty(2, 1, 16, head_dim, device="cpu")
     assert api.KV4Cache.empty(2, 1, 16, 64, device="cpu").head_dim == 64
+
+
+def test_index_arrays_off_their_alignment_are_refused():
+    """A kernel that read them would raise a misaligned-address fault."""
+    grow = dict(lengths=A, new=A, table=A, B=2, width=4, page=16, free=A, free_size=9, count=A, T=8, slots=A, cu=A,
+                held=A, out=A)
+    for name in ("lengths", "new", "table", "free", "count", "slots", "cu", "held", "out"):
+        for off in (1, 2) + ((4,) if name == "slots" else ()):
+            a = {**grow, name: A + off}
+            assert b.fa_page_grow(*a.values(), None) == b.FA_ERR_MISALIGNED, (name, off)
+            if name in ("lengths", "new", "table", "slots", "cu"):
+                assert b.fa_page_slots(*(a[n] for n in ("lengths", "new", "table", "B", "width", "page", "T", "slots", "cu")),
+                                       None) == b.FA_ERR_MISALIGNED, (name, off)
+    desc = cache(dict(kc=A, ks=A, vc=A, vs=A, pages=3, page=16, H=2, d=128, kg=1.0, vg=1.0)).address
+    for off in (1, 4):
+        assert b.fa_kv4_store(desc, A, A, 256, 128, 256, 128, A + off, 4, None) == b.FA_ERR_MISALIGNED
+        assert b.fa_kv4_load(desc, A + off, 4, A, A, None) == b.FA_ERR_MISALIGNED
+    attn = dict(q=A, qt=1024, qh=128, T=2, cu=A, max_q=1, table=A, width=4, lengths=A, B=2, heads=8, scale=0.1, o=A,
+                ot=1024, oh=128, lse=A, ws=A, wsb=1 << 30)
+    for name in ("cu", "table", "lengths", "lse"):
+        for off in (1, 2, 3):
+            assert b.fa_kv4_attn(desc, *{**attn, name: A + off}.values(), None) == b.FA_ERR_MISALIGNED, (name, off)

@@ -161,7 +161,8 @@ fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_toke
   if ((long long)width * cache->page > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   if (B == 0 || H == 0 || T == 0 || max_q == 0) return FA_OK;
   if (!q || !o || !lse || !lengths || (width > 0 && !table)) return FA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(o) || (q_token & 7) || (q_head & 7) || (o_token & 7) || (o_head & 7))
+  if (!aligned16(q) || !aligned16(o) || (q_token & 7) || (q_head & 7) || (o_token & 7) || (o_head & 7) ||
+      !all_aligned(4, cu, table, lengths, lse))
     return FA_ERR_MISALIGNED;
   if (!cu) max_q = 1;
   Plan plan;

@@ -1,6 +1,7 @@
 // Host-side helpers of the serving operators (not part of the ABI).
 #pragma once
 #include <atomic>
+#include <cstdint>
 
 #include "fa_paged.h"
 #include "host.h"
@@ -10,6 +11,12 @@ namespace fa {
 // log2 of a page size the kernels take, -1 for any other.
 inline int page_log2_of(int page) {
   return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1;
+}
+
+// Whether all of these addresses are multiples of `bytes` (a power of two).
+template <class... P>
+bool all_aligned(size_t bytes, const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ... | 0) & (bytes - 1)) == 0;
 }
 
 // Launches with programmatic stream serialization like launch() (host.h), for kernels

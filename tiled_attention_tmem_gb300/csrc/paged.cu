@@ -393,6 +393,9 @@ fa_status fa_page_grow(const int* lengths, const int* new_tokens, int* table, in
   if (!lengths || !new_tokens || !free_count || !cu || !lengths_out || !count_out) return FA_ERR_INVALID_ARG;
   if (free_size > 0 && !free_pages) return FA_ERR_INVALID_ARG;
   if ((width > 0 && !table) || (T > 0 && !slots)) return FA_ERR_INVALID_ARG;
+  if (!all_aligned(4, lengths, new_tokens, table, free_pages, free_count, cu, lengths_out, count_out) ||
+      !all_aligned(8, slots))
+    return FA_ERR_MISALIGNED;
   PageParams p = {lengths, new_tokens, table, free_pages, free_count, slots, cu, lengths_out, count_out,
                   B, width, page_log2_of(page), T, free_size, 0, true};
   return run_pages(p, (cudaStream_t)stream);
@@ -403,6 +406,7 @@ fa_status fa_page_slots(const int* first, const int* count, const int* table, in
   if (!pages_ok(B, width, page, T)) return FA_ERR_INVALID_ARG;
   if (B == 0) return FA_OK;
   if (!first || !count || !cu || (width > 0 && !table) || (T > 0 && !slots)) return FA_ERR_INVALID_ARG;
+  if (!all_aligned(4, first, count, table, cu) || !all_aligned(8, slots)) return FA_ERR_MISALIGNED;
   PageParams p = {first, count, const_cast<int*>(table), nullptr, nullptr, slots, cu, nullptr, nullptr,
                   B, width, page_log2_of(page), T, 0, 0, false};
   return run_pages(p, (cudaStream_t)stream);
@@ -416,7 +420,8 @@ fa_status fa_kv4_store(const fa_kv4_cache* cache, const void* k, const void* v, 
   if (T < 0) return FA_ERR_INVALID_ARG;
   if (T == 0 || cache->Hkv == 0 || cache->pages == 0) return FA_OK;
   if (!k || !v || !slots) return FA_ERR_INVALID_ARG;
-  if (!aligned16(k) || !aligned16(v) || (k_token & 7) || (k_head & 7) || (v_token & 7) || (v_head & 7))
+  if (!aligned16(k) || !aligned16(v) || (k_token & 7) || (k_head & 7) || (v_token & 7) || (v_head & 7) ||
+      !all_aligned(8, slots))
     return FA_ERR_MISALIGNED;
   Kv4IoParams p = {};
   dim3 grid;
@@ -446,7 +451,7 @@ fa_status fa_kv4_load(const fa_kv4_cache* cache, const long long* slots, int T, 
   if (T < 0) return FA_ERR_INVALID_ARG;
   if (T == 0 || cache->Hkv == 0) return FA_OK;
   if (!k || !v || !slots) return FA_ERR_INVALID_ARG;
-  if (!aligned16(k) || !aligned16(v)) return FA_ERR_MISALIGNED;
+  if (!aligned16(k) || !aligned16(v) || !all_aligned(8, slots)) return FA_ERR_MISALIGNED;
   Kv4IoParams p = {};
   dim3 grid;
   bool batch;
