@@ -965,3 +965,17 @@ def test_attention_refuses_a_max_q_past_31_bits():
             api.kv4_attention(*args, max_q)
     with pytest.raises(RuntimeError, match="invalid"):
         api.kv4_attention(*args, -1)
+
+
+@pytest.mark.parametrize("heads,kv,lengths", [(4, 2, [50, 9]), (4, 2, [6000, 700]), (80, 1, [5000, 700])],
+                         ids=["block", "split", "many_rows"])
+@pytest.mark.parametrize("scale,gain,keys,power", [
+    (1.5 * 2.0 ** 127, -100, -94, -35), (2.0 ** 62, 60, 58, -123), (2.0 ** -120, 0, 6, 112),
+    (2.0 ** 30, -100, -94, 62)], ids=["scale", "product", "tiny_scale", "gain"])
+def test_attention_of_ordinary_scores_from_extreme_factors(heads, kv, lengths, scale, gain, keys, power):
+    """scale, k_gain and q at the ends of their ranges, with products that fp32 does not hold
+    and scores of ordinary size."""
+    arrays, table, cu, q, gains = _problem(64, 16, heads, kv, lengths, [2, 1], seed=109, spread=2.0 ** keys,
+                                           gains=(2.0 ** gain, 2.0 ** -5))
+    q = R.bf16(np.ldexp(to_f64(to_dev(q, "cpu")), power))
+    _attend((arrays, table, cu, q, gains), lengths, 2, scale=scale)

@@ -201,7 +201,9 @@ fa_status fa_kv4_attn(const fa_kv4_cache* cache, const void* q, long long q_toke
   p.pages = cache->pages;
   p.page_log2 = page_log2_of(cache->page);
   p.max_q = max_q;
-  p.score = std::min(scale * kLog2e * cache->k_gain * kKv4ScaleBias, 3e38f);
+  // (in fp64, which holds the product of any scale and gain)
+  p.score = (float)(2.0 * std::frexp((double)scale * 1.4426950408889634 * cache->k_gain * kKv4ScaleBias, &p.score_exp));
+  p.score_exp -= 1;
   p.v_gain = cache->v_gain * kKv4ScaleBias;
   cudaStream_t st = (cudaStream_t)stream;
   switch (d * 8 + plan.nt) {

@@ -55,7 +55,8 @@ struct Kv4AttnParams {
   long long q_token, q_head, o_token, o_head;
   int B, H, Hkv, G, T, width, pages, page_log2, max_q;
   int row_tiles;  // most row tiles of a request
-  float score;    // scale * log2(e) * k_gain * 2^8
+  float score;    // scale * log2(e) * k_gain * 2^8 = score * 2^score_exp, score in [1, 2]
+  int score_exp;
   float v_gain;   // v_gain * 2^8
 };
 
@@ -64,6 +65,15 @@ struct Kv4AttnParams {
 // 2^-32 below the largest.
 constexpr float kKv4Lift = 7.f;
 constexpr float kKv4Grow = 8.f;
+
+// What takes scores of a row that was scaled by 2^-e to the log2 domain.  The exponents are
+// added before they meet fp32: a scale at one end of its range and a gain or a query at the
+// other give ordinary scores.  Not 0, so that a masked score stays -inf, and finite, so that a
+// score of 0 stays 0.
+__device__ __forceinline__ float kv4_score_factor(const Kv4AttnParams& p, int e) {
+  const int x = min(max(e + p.score_exp, -126), 127);
+  return fminf(fmaxf(__uint_as_float((uint32_t)(127 + x) << 23) * p.score, 1e-37f), 3e38f);
+}
 
 // Warps per SM and tokens per unit for head dim d and nt tiles of 8 rows (what the registers
 // hold: with three tiles and 64 tokens the scores would not fit).
@@ -452,10 +462,10 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
         for (int c = 0; c < D / 8; ++c) top = max(top, max(w[c] & 0x7fffu, (w[c] >> 16) & 0x7fffu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^-e with e the exponent of the largest, both factors normal fp32.
+        // 2^-e with e the exponent of the largest, kept where 2^-e is normal fp32.
         const int e = min(max((int)(top >> 7) - 127, -120), 120);
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23) * p.score;
+        const float up = kv4_score_factor(p, e);
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           const float lo = __uint_as_float(w[c] << 16) * down, hi = __uint_as_float(w[c] & 0xffff0000u) * down;
@@ -463,8 +473,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) kv4_attn_kernel(const _
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          // (not 0, so that a masked score stays -inf, and finite, so that a score of 0 stays 0)
-          fac[n][j] = fminf(fmaxf(__shfl_sync(0xffffffffu, up, (2 * t + j) * 4), 1e-37f), 3e38f);
+          fac[n][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
           const int r = cur.rt * C::ROWS + 8 * n + 2 * t + j;
           const int qi = r / p.G;
           lim[n][j] = qi < cur.nq ? cur.first + qi : -1;

@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_wide_kernel(const __grid_co
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::B_Q));
-      return fminf(fmaxf(__uint_as_float((uint32_t)(127 + exponent(top)) << 23) * p.score, 1e-37f), 3e38f);
+      return kv4_score_factor(p, exponent(top));
     };
     // O with unit u added.  S runs one unit ahead, so a barrier for every other unit cannot
     // be two phases ahead of its waiter.
