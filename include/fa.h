@@ -285,12 +285,7 @@ enum {
   FA_KERNEL_FWD_MERGE = 6, /* split-KV merge of the forward's parts */
   FA_KERNEL_BWD_KVSUM = 7, /* sum of the dK/dV kernel's query-range parts */
   FA_KERNEL_BWD_QSUM = 8,  /* sum of the dQ kernel's key-range parts */
-  FA_KERNEL_PAGE = 9,       /* page tables and slots (fa_paged.h) */
-  FA_KERNEL_KV4_STORE = 10, /* 4-bit cache: store */
-  FA_KERNEL_KV4_LOAD = 11,  /* 4-bit cache: load */
-  FA_KERNEL_KV4_ATTN = 12,  /* attention over the 4-bit cache */
-  FA_KERNEL_KV4_MERGE = 13, /* merge of its warps' parts */
-  FA_KERNEL_KINDS = 14
+  FA_KERNEL_KINDS = 9      /* kinds of this header; those of fa_paged.h follow */
 };
 typedef struct {
   int launches[FA_KERNEL_KINDS];
@@ -298,6 +293,13 @@ typedef struct {
 } fa_profile;
 int fa_profile_start(void);
 int fa_profile_stop(fa_profile* out);
+/*
+ * fa_profile_stop for the kinds below `kinds`, those of fa_paged.h among them, into
+ * arrays of that many entries (NULL: not wanted; entries that no kind has become 0).
+ * fa_profile itself does not grow: a program passes a record of the size that it was
+ * compiled with.  FA_ERR_INVALID_ARG, and the records stay, for a negative count.
+ */
+int fa_profile_stop_kinds(int kinds, int* launches, double* ms);
 const char* fa_kernel_name(int kind);
 
 /*

@@ -34,6 +34,16 @@
 extern "C" {
 #endif
 
+/* Kernel kinds of these calls, for fa_profile_stop_kinds and fa_kernel_name. */
+enum {
+  FA_KERNEL_PAGE = 9,       /* page tables and slots */
+  FA_KERNEL_KV4_STORE = 10, /* 4-bit cache: store */
+  FA_KERNEL_KV4_LOAD = 11,  /* 4-bit cache: load */
+  FA_KERNEL_KV4_ATTN = 12,  /* attention over the 4-bit cache */
+  FA_KERNEL_KV4_MERGE = 13, /* merge of its warps' parts */
+  FA_KERNEL_ALL_KINDS = 14
+};
+
 /* The cache as the calls take it (host memory; read during the call only). */
 typedef struct {
   void* k_codes;

@@ -294,3 +294,45 @@ def test_index_arrays_off_their_alignment_are_refused():
     for name in ("cu", "table", "lengths", "lse"):
         for off in (1, 2, 3):
             assert b.fa_kv4_attn(desc, *{**attn, name: A + off}.values(), None) == b.FA_ERR_MISALIGNED, (name, off)
+
+
+OLD_PROFILE = r"""
+#include <stdio.h>
+#include <string.h>
+#include "fa_paged.h"
+
+/* The record as it was before there were serving calls, and what lies behind it. */
+struct { int launches[9]; double ms[9]; unsigned char behind[256]; } old;
+
+int main(void) {
+  int fails = 0, i, launches[20];
+  double ms[20];
+  memset(&old, 0xa5, sizeof(old));
+  fa_profile_start();
+  if (fa_profile_stop((fa_profile*)&old) != FA_OK) fails |= 1;
+  for (i = 0; i < 9; ++i) if (old.launches[i] != 0 || old.ms[i] != 0) fails |= 2;
+  for (i = 0; i < 256; ++i) if (old.behind[i] != 0xa5) fails |= 4;
+  if (fa_profile_stop(NULL) != FA_OK || fa_profile_stop_kinds(5, NULL, NULL) != FA_OK) fails |= 8;
+  if (fa_profile_stop_kinds(-1, launches, ms) != FA_ERR_INVALID_ARG) fails |= 16;
+  memset(launches, 0xa5, sizeof(launches)), memset(ms, 0xa5, sizeof(ms));
+  if (fa_profile_stop_kinds(FA_KERNEL_ALL_KINDS, launches, ms) != FA_OK) fails |= 32;
+  for (i = 0; i < 20; ++i) if ((launches[i] == 0 && ms[i] == 0) != (i < FA_KERNEL_ALL_KINDS)) fails |= 64;
+  if (strcmp(fa_kernel_name(FA_KERNEL_KINDS), "page") || strcmp(fa_kernel_name(FA_KERNEL_ALL_KINDS), "unknown")) fails |= 128;
+  printf("%d\n", fails);
+  return fails != 0;
+}
+"""
+
+
+def test_a_profile_record_of_an_older_program_is_not_written_past(tmp_path):
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc not available")
+    src, exe = tmp_path / "client.c", tmp_path / "client"
+    src.write_text(OLD_PROFILE)
+    libdir = os.path.dirname(b.LIB_PATH)
+    r = subprocess.run([gcc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", f"-I{build.INCLUDE}", str(src), "-o",
+                        str(exe), f"-L{libdir}", "-l:libfa_gb300.so", f"-Wl,-rpath,{libdir}"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0 and out.stdout.strip() == "0", out.stdout + out.stderr

@@ -58,6 +58,7 @@ SIGNATURES = {
     "fa_strerror": (ctypes.c_char_p, [_I]),
     "fa_profile_start": (_I, []),
     "fa_profile_stop": (_I, [_VP]),
+    "fa_profile_stop_kinds": (_I, [_I, _VP, _VP]),
     "fa_kernel_name": (ctypes.c_char_p, [_I]),
     "fa_ex2_probe": (_I, [_VP, _I, _I, ctypes.POINTER(ctypes.c_longlong), _VP]),
     "fa_fwd_launches": (_I, [_I, _I, _I, _I]),
@@ -244,11 +245,7 @@ def fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q, page, width) -> int:
     return lib().fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q, page, width)
 
 
-FA_KERNEL_KINDS = 14
-
-
-class FaProfile(ctypes.Structure):
-    _fields_ = [("launches", _I * FA_KERNEL_KINDS), ("ms", ctypes.c_double * FA_KERNEL_KINDS)]
+FA_KERNEL_ALL_KINDS = 14
 
 
 def fa_profile_start() -> int:
@@ -257,9 +254,8 @@ def fa_profile_start() -> int:
 
 def fa_profile_stop() -> dict:
     """Returns {kernel name: (launches, total ms)} for the kernels launched since start."""
-    prof = FaProfile()
-    st = lib().fa_profile_stop(ctypes.byref(prof))
+    launches, ms = (_I * FA_KERNEL_ALL_KINDS)(), (ctypes.c_double * FA_KERNEL_ALL_KINDS)()
+    st = lib().fa_profile_stop_kinds(FA_KERNEL_ALL_KINDS, launches, ms)
     if st != FA_OK:
         raise FaError(st, "fa_profile_stop")
-    return {lib().fa_kernel_name(k).decode(): (prof.launches[k], prof.ms[k])
-            for k in range(FA_KERNEL_KINDS)}
+    return {lib().fa_kernel_name(k).decode(): (launches[k], ms[k]) for k in range(FA_KERNEL_ALL_KINDS)}

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "fa.h"
+#include "fa_paged.h"
 #include "host.h"
 
 namespace fa {
@@ -334,30 +335,32 @@ int fa_profile_start(void) {
   return FA_OK;
 }
 
-int fa_profile_stop(fa_profile* out) {
+int fa_profile_stop_kinds(int kinds, int* launches, double* ms) {
+  if (kinds < 0) return FA_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lock(g_prof_mutex);
   g_prof_on = false;
-  if (out) {
-    for (int k = 0; k < FA_KERNEL_KINDS; ++k) {
-      out->launches[k] = 0;
-      out->ms[k] = 0.0;
-    }
+  for (int k = 0; k < kinds; ++k) {
+    if (launches) launches[k] = 0;
+    if (ms) ms[k] = 0.0;
   }
   int status = FA_OK;
   for (const ProfRecord& r : g_prof) {
-    float ms = 0.f;
-    if (cudaEventSynchronize(r.b) != cudaSuccess || cudaEventElapsedTime(&ms, r.a, r.b) != cudaSuccess) {
+    float t = 0.f;
+    if (cudaEventSynchronize(r.b) != cudaSuccess || cudaEventElapsedTime(&t, r.a, r.b) != cudaSuccess) {
       status = FA_ERR_LAUNCH;
       continue;
     }
-    if (out && r.kind >= 0 && r.kind < FA_KERNEL_KINDS) {
-      out->launches[r.kind] += 1;
-      out->ms[r.kind] += ms;
-    }
+    if (r.kind < 0 || r.kind >= kinds) continue;
+    if (launches) launches[r.kind] += 1;
+    if (ms) ms[r.kind] += t;
   }
   g_prof.clear();
   g_prof_used_events = 0;
   return status;
+}
+
+int fa_profile_stop(fa_profile* out) {
+  return fa_profile_stop_kinds(FA_KERNEL_KINDS, out ? out->launches : nullptr, out ? out->ms : nullptr);
 }
 
 const char* fa_kernel_name(int kind) {
