@@ -52,7 +52,7 @@ typedef enum {
   FA_OK = 0,
   FA_ERR_INVALID_ARG = 1,    /* null pointer, negative size, non-finite or non-positive scale */
   FA_ERR_UNSUPPORTED = 2,    /* head dimension or variant not built for this library */
-  FA_ERR_MISALIGNED = 3,     /* a pointer is not 16-byte aligned (TMA requirement) */
+  FA_ERR_MISALIGNED = 3,     /* a pointer is not 16-byte aligned (TMA requirement), or an index array not to its elements */
   FA_ERR_WORKSPACE = 4,      /* workspace NULL or smaller than fa_bwd_workspace_size */
   FA_ERR_LAUNCH = 5,         /* the CUDA runtime rejected a launch (see fa_last_cuda_error) */
   FA_ERR_DEVICE_TIMEOUT = 6  /* a bounded in-kernel wait expired; results are invalid */

@@ -336,3 +336,8 @@ def test_a_profile_record_of_an_older_program_is_not_written_past(tmp_path):
     assert r.returncode == 0, r.stderr
     out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert out.returncode == 0 and out.stdout.strip() == "0", out.stdout + out.stderr
+
+
+def test_the_message_of_a_misaligned_argument_fits_index_arrays():
+    text = b.fa_strerror(b.FA_ERR_MISALIGNED)
+    assert "aligned" in text and "16" not in text

@@ -319,7 +319,7 @@ const char* fa_strerror(fa_status s) {
     case FA_OK: return "ok";
     case FA_ERR_INVALID_ARG: return "invalid argument";
     case FA_ERR_UNSUPPORTED: return "unsupported head dimension or variant";
-    case FA_ERR_MISALIGNED: return "pointer not 16-byte aligned";
+    case FA_ERR_MISALIGNED: return "pointer not aligned as the call requires";
     case FA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case FA_ERR_LAUNCH: return "CUDA launch failed";
     case FA_ERR_DEVICE_TIMEOUT: return "in-kernel wait timed out";
