@@ -30,3 +30,16 @@ def test_key_split_grid_has_few_query_tiles():
         items = (n // 128) * (2 if d == 384 else 1) * bh  # the dQ kernel's work items
         assert items < 304
         assert not (d == 384 and n == 16384)
+
+
+def test_sources_left_out_of_the_traffic_hash_are_included_by_no_other():
+    """A header shared with the workloads' kernels would change them behind the hash."""
+    import os
+    import re
+    d = os.path.join(bench.ROOT, "tiled_attention_tmem_gb300", "csrc")
+    left_out = [f for f in os.listdir(d) if f.startswith(bench.TRAFFIC_FREE_SOURCES)]
+    assert "report.cu" in left_out and "kv4.cuh" in left_out
+    for f in set(os.listdir(d)) - set(left_out):
+        with open(os.path.join(d, f), encoding="utf-8") as fh:
+            for name in re.findall(r'#include "([^"]+)"', fh.read()):
+                assert os.path.basename(name) not in left_out + ["fa_paged.h"], (f, name)
