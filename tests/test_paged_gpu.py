@@ -979,3 +979,54 @@ def test_attention_of_ordinary_scores_from_extreme_factors(heads, kv, lengths, s
                                            gains=(2.0 ** gain, 2.0 ** -5))
     q = R.bf16(np.ldexp(to_f64(to_dev(q, "cpu")), power))
     _attend((arrays, table, cu, q, gains), lengths, 2, scale=scale)
+
+
+# ------------------------------------------------------------------ many tokens, long shares
+
+@pytest.mark.parametrize("heads", [1, 5])
+@pytest.mark.parametrize("d", DIMS)
+def test_store_and_load_of_many_tokens(d, heads):
+    """Tokens enough for the kernels that keep four a warp in flight, with an end inside a
+    batch: the same bytes as in calls too short for them, and the restatement's for a sample."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    pieces = heads * d // 8
+    per_warp, chunks = max(1, 32 // pieces), -(-pieces // 32)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    T = -(-128 * sms // chunks) * per_warp  # T / per_warp * chunks tokens' rows: 128 an SM
+    T += 8 * 4 * per_warp + 4 * per_warp + 1
+    assert T % (8 * 4 * per_warp)
+    page, rng = 64, np.random.default_rng(d + heads)
+    pool = -(-T // page) + 2
+    g = torch.Generator(device="cuda:0").manual_seed(d)
+    x = torch.randn((T, 2 * heads, d), generator=g, device="cuda:0") * torch.exp(
+        3 * torch.randn((T, 2 * heads, 1), generator=g, device="cuda:0"))
+    x = x.to(torch.bfloat16)
+    k, v = x[:, :heads], x[:, heads:]
+    slots = rng.permutation(pool * page)[:T].astype(np.int64)
+    slots[rng.random(T) < 0.1] = -1
+    slots[rng.integers(0, T, 20)] = pool * page
+    slots[rng.integers(0, T, 20)] = -(1 << 40)
+    slots[-3:] = -1, slots[-2], slots[-1]
+    where = _dev(slots, torch.int64)
+    caches = []
+    for step in (T, T // 4 + 1):
+        cache = api.KV4Cache.empty(pool, heads, page, d, 2.0 ** -5, 2.0 ** -6)
+        for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
+            t.fill_(0xA5)
+        for t in range(0, T, step):
+            api.kv4_store(k[t:t + step], v[t:t + step], where[t:t + step], cache)
+        caches.append(cache)
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(caches[0], name), getattr(caches[1], name)), name
+    lk, lv = api.kv4_load(where, caches[0])
+    parts = [api.kv4_load(where[t:t + T // 4 + 1], caches[0]) for t in range(0, T, T // 4 + 1)]
+    for whole, part in ((lk, torch.cat([p[0] for p in parts])), (lv, torch.cat([p[1] for p in parts]))):
+        assert torch.equal(whole, part)
+    sample = np.unique(np.concatenate([np.arange(T - 70, T), rng.integers(0, T, 200)]))
+    fine = (slots[sample] >= 0) & (slots[sample] < pool * page)
+    for dense, out, gain in ((k, lk, 2.0 ** -5), (v, lv, 2.0 ** -6)):
+        rows = to_f64(dense[torch.from_numpy(sample).cuda()].contiguous())
+        want = np.where(fine[:, None, None], R.decode(*R.encode(rows, gain), gain), 0.0)
+        assert np.array_equal(to_f64(out[torch.from_numpy(sample).cuda()].contiguous()), want)
+    api.check_device_error()
