@@ -1030,3 +1030,128 @@ def test_store_and_load_of_many_tokens(d, heads):
         want = np.where(fine[:, None, None], R.decode(*R.encode(rows, gain), gain), 0.0)
         assert np.array_equal(to_f64(out[torch.from_numpy(sample).cuda()].contiguous()), want)
     api.check_device_error()
+
+
+def _long_problem(d, page, kv, heads, lengths, queries, seed, bad=0.02):
+    """A cache of random codes and scales on the GPU, some entries of the table no page."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    g = torch.Generator(device="cuda:0").manual_seed(seed)
+    need = [-(-n // page) for n in lengths]
+    pool, width = sum(need) + 3, max(need)
+
+    def random(n, low, high):
+        return torch.randint(low, high, (pool, kv, page, n), generator=g, device="cuda:0", dtype=torch.uint8)
+
+    # Scales from 1/4 to 2: scores with a deviation of about 3.
+    cache = api.KV4Cache(random(d // 2, 0, 256), random(d // 16, 0x28, 0x41), random(d // 2, 0, 256),
+                         random(d // 16, 0x28, 0x41), 1.0, 2.0 ** -5)
+    ids = torch.randperm(pool, generator=g, device="cuda:0").int()
+    table = torch.full((len(lengths), width), -1, dtype=torch.int32, device="cuda:0")
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    hit = torch.rand((len(lengths), width), generator=g, device="cuda:0")
+    table[hit < bad] = -1
+    table[hit > 1 - bad / 2] = pool
+    cu = np.concatenate([[0], np.cumsum(queries)])
+    q = torch.randn((int(cu[-1]), heads, d), generator=g, device="cuda:0").to(torch.bfloat16)
+    return cache, table, cu, q
+
+
+def _long_reference(cache, table, cu, q, lengths, scale):
+    """R.attend in torch's 64 bits, a request at a time."""
+    import torch
+    dev = "cuda:0"
+    pair = torch.tensor([[R.e2m1_value(b & 15), R.e2m1_value(b >> 4)] for b in range(256)], dtype=torch.float64, device=dev)
+    value = torch.tensor(R.e4m3_value(np.arange(256)), dtype=torch.float64, device=dev)
+    kv, page, d = cache.kv_heads, cache.page_size, cache.head_dim
+    T, H, _ = q.shape
+    new = dict(dtype=torch.float64, device=dev)
+    o, lse, pv, qk, sv = (torch.full((T, H, d), math.nan, **new), torch.full((T, H), math.nan, **new),
+                          torch.zeros((T, H, d), **new), torch.zeros((T, H), **new), torch.zeros((T, H, d), **new))
+    for b, n in enumerate(lengths):
+        t0, t1 = int(cu[b]), int(cu[b + 1])
+        ids = table[b, :-(-n // page)].long()
+        fine = ((ids >= 0) & (ids < cache.pages)).repeat_interleave(page)[:n]
+        ids = ids.clamp(0, cache.pages - 1)
+
+        def rows(codes, scales, gain):
+            x = pair[codes[ids].long()].flatten(-2) * value[scales[ids].long()].repeat_interleave(16, -1) * gain
+            return x.transpose(0, 1).reshape(kv, -1, d)[:, :n]
+
+        k, v = rows(cache.k_codes, cache.k_scales, cache.k_gain), rows(cache.v_codes, cache.v_scales, cache.v_gain)
+        x = q[t0:t1].double().view(t1 - t0, kv, H // kv, d)
+        see = fine & (torch.arange(n, device=dev) <= n - (t1 - t0) + torch.arange(t1 - t0, device=dev)[:, None])
+        s = torch.einsum("ighd,gjd->ighj", x, k) * scale
+        s.masked_fill_(~see[:, None, None], -math.inf)
+        l = torch.logsumexp(s, -1)
+        p = torch.where(torch.isneginf(s), 0.0, torch.exp(s - l[..., None]))
+        lse[t0:t1] = l.reshape(t1 - t0, H)
+        o[t0:t1] = torch.einsum("ighj,gjd->ighd", p, v).reshape(t1 - t0, H, d)
+        pv[t0:t1] = torch.einsum("ighj,gjd->ighd", p, v.abs()).reshape(t1 - t0, H, d)
+        size = torch.einsum("ighd,gjd->ighj", x.abs(), k.abs()) * scale
+        qk[t0:t1] = torch.where(see[:, None, None], size, 0.0).amax(-1).reshape(t1 - t0, H)
+        sv[t0:t1] = torch.einsum("ij,gjd->igd", see.double(), v.abs()).repeat_interleave(H // kv, 1)
+    return tuple(t.cpu().numpy() for t in (o, lse, pv, qk, sv))
+
+
+def _attend_long(d, page, kv, group, lengths, queries, seed, solo=False):
+    from tiled_attention_tmem_gb300 import api
+    cache, table, cu, q = _long_problem(d, page, kv, kv * group, lengths, queries, seed)
+    need = api.kv4_attention_workspace_bytes(len(lengths), kv * group, cache, table.shape[1], max(queries))
+    assert (need == 0) == solo
+    args = q, cache, table, _i32(lengths), _i32(cu), max(queries)
+    o, lse = api.kv4_attention(*args)
+    api.check_device_error()
+    R.check(to_f64(o), to_f64(lse), _long_reference(cache, table, cu, q, lengths, d ** -0.5), d)
+    again = api.kv4_attention(*args)
+    assert all(bool((a == b).all()) for a, b in zip((o, lse), again))
+
+
+# 12 warps an SM and 152 of them, units of 64 tokens: eleven units a warp and more, where its
+# ring holds four at most; past one of 256 units, a warp goes from request to request.
+LONG = [16384, 1, 3001, 8192, 15000, 64, 12345, 7777, 11111, 9000, 16000, 500, 14001, 8191, 6000, 13000, 10240, 4097, 9999,
+        15872]
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("d,group,queries", [
+    (d, group, queries) for d in DIMS for group, queries, dims in (
+        (4, 1, DIMS), (5, 3, (64, 96, 128, 192)), (9, 3, (64,)), (8, 3, (96, 128)), (11, 2, (64, 96, 128))) if d in dims],
+    ids=str)
+def test_attention_of_long_shares(d, group, queries, page):
+    """Tiles of 8, 16, 24 and 32 rows, and several, whose warps run through their rings."""
+    each = [queries if b % 3 else max(1, queries - 1) for b in range(len(LONG))]
+    _attend_long(d, page, 8, group, LONG, each, seed=d + group)
+
+
+@pytest.mark.parametrize("d", DIMS)
+def test_attention_of_long_shares_with_a_few_prompts_among_single_queries(d):
+    """One request of many queries: the others' rows decide the form, its rows take many tiles."""
+    each = [1] * len(LONG)
+    each[9] = 21
+    _attend_long(d, 64, 8, 2, LONG, each, seed=d)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("d", DIMS)
+def test_attention_of_many_rows_over_long_shares(d, page):
+    """tcgen05 kernel: 60 units a block and more, where its rings hold 14 and 32 units'
+    page bits are kept; with two row tiles too."""
+    _attend_long(d, page, 4, 24, LONG, [3 if b % 4 else 2 for b in range(len(LONG))], seed=d)
+    _attend_long(d, page, 1, 70, LONG + LONG, [2] * 40, seed=d + 1)
+
+
+@pytest.mark.parametrize("d,group,queries", [(d, 4, 1) for d in DIMS] + [(64, 8, 3), (64, 6, 2), (96, 6, 2), (128, 5, 3), (192, 16, 1)],
+                         ids=str)
+def test_attention_in_one_block_a_request_over_long_rings(d, group, queries):
+    """A block per request and kv head with ten units a warp, where its ring holds four."""
+    units = 40 if d <= 256 and group * queries <= 8 else 34  # of those that the form still takes
+    unit = 64 if d <= 128 else 32
+    batch = 38 if d <= 256 and group * queries <= 8 else 30
+    rng = np.random.default_rng(d + group)
+    lengths = [int(n) for n in rng.integers(1, units * unit + 1, batch)]
+    lengths[:3] = [units * unit, 1, units * unit - 1]
+    _attend_long(d, 16, 8, group, lengths, [queries] * batch, seed=d, solo=True)
