@@ -69,7 +69,8 @@ typedef struct {
  *   slots       int64 [T]         slot of new token t, requests in order; -1 for a
  *                                 token that has none and past the last new token
  *   cu          int32 [B + 1]     first new token of each request in `slots`
- *   lengths_out int32 [B]         lengths plus the new tokens that got a slot
+ *   lengths_out int32 [B]         lengths plus the new tokens that got a slot (or whose page
+ *                                 id is below 0, in the table or on the stack: slot -1)
  *   count_out   int32 [1]         pages left: the stack is free_pages[0 .. count_out)
  * Request b owns ceil(lengths/page) pages; the pages it needs beyond those (at
  * most up to `width`) are taken from the top of the stack in request order.
@@ -122,12 +123,16 @@ fa_status fa_kv4_load(const fa_kv4_cache* cache, const long long* slots, int T, 
  * Query i of the n_q of request b sees the keys j <= lengths[b] - n_q + i; kv head
  * h / (H/Hkv) serves head h:
  *   s_j = scale * k_gain * q . k_j,  lse = ln sum_j exp(s_j),  o = sum_j exp(s_j - lse) v_j.
- * A query that sees no key gets o = 0 and lse = -inf.  Rows of o and lse that no
+ * Scores, maxima and sums are fp32.  q is taken exactly, but for channels below 2^-17 of
+ * their row's largest magnitude, which are off by 2^-25 of it at most; exp by 2^-21 of
+ * itself; the probabilities that weigh v are rounded to f16, o to bf16 once.
+ * A query that sees no key, or whose scores are all -inf (an infinity in q), gets o = 0
+ * and lse = -inf; other infinities and NaN make their row NaN.  Rows of o and lse that no
  * query of a request owns are left as they were.  The first max_q queries of a
  * request are computed (max_q times H/Hkv below 2^31).  A request whose queries do
  * not lie in [0, T) has none; requests that share a query leave either's result in
- * its row.  o may be q itself where the strides are the same, but must not overlap
- * it in another way.  A token whose table entry is not in
+ * its row.  o may be q itself where the strides are the same and no two requests share
+ * a query, but must not overlap it in another way.  A token whose table entry is not in
  * [0, pages), or lies past `width`, is no key.
  * H a multiple of Hkv; scale finite and > 0.  workspace: fa_kv4_attn_workspace_size
  * bytes, 256-byte aligned, not shared with a concurrent call.

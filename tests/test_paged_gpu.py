@@ -1155,3 +1155,68 @@ def test_attention_in_one_block_a_request_over_long_rings(d, group, queries):
     lengths = [int(n) for n in rng.integers(1, units * unit + 1, batch)]
     lengths[:3] = [units * unit, 1, units * unit - 1]
     _attend_long(d, 16, 8, group, lengths, [queries] * batch, seed=d, solo=True)
+
+
+@pytest.mark.parametrize("heads,kv,lengths", [(4, 2, [50, 9]), (4, 2, [6000, 700]), (80, 1, [5000, 700])],
+                         ids=["block", "split", "many_rows"])
+@pytest.mark.parametrize("power", [-10, -17, -20])
+def test_attention_of_queries_with_one_channel_far_above_the_others(heads, kv, lengths, power):
+    """A channel that no key has a part in sets the row's power of two, and the scores come
+    from channels 2^power below it: exact to 2^-17 of the largest, and 2^-25 of it below that."""
+    d, far = 64, 37
+    arrays, table, cu, q, gains = _problem(d, 16, heads, kv, lengths, [2, 1], seed=113)
+    arrays[0][..., far // 2] &= 0x0F if far % 2 else 0xF0  # the keys' codes of that channel: 0
+    x = to_f64(to_dev(q, "cpu"))
+    # Between 2^power and 2^(power + 1) in magnitude.
+    x = np.where(x < 0, -1.0, 1.0) * (1 + np.abs(x) % 1.0) * 2.0 ** power
+    x[..., far] = 1.5
+    q = R.bf16(x)
+    scale = 2.0 ** -power / 8
+    problem = arrays, table, cu, q, gains
+    if power >= -17:
+        _attend(problem, lengths, 2, scale)
+        return
+    from tiled_attention_tmem_gb300 import api
+    o, lse = api.kv4_attention(to_dev(q), _cache_of(arrays, gains), _i32(table), _i32(lengths), _i32(cu), 2, scale)
+    api.check_device_error()
+    ro, rl, pv, qk, sv = _reference(arrays, gains, table, cu, q, lengths, 2, scale)
+    # sum_c |k_c| of the largest key times a channel's 2^-25 * 1.5: what a score is off by more;
+    # a weight by twice that, as exp(2 e) - 1 <= 2 e + 4 e^2 for e below 1/2.
+    k = np.abs(R.decode(arrays[0], arrays[1], gains[0])).sum(-1)
+    seen = np.zeros(k.shape, bool)
+    for b, n in enumerate(lengths):
+        seen[table[b, :-(-n // 16)]] = True
+    e = k[seen & (arrays[1] != 0xFF).all(-1)].max() * 1.5 * 2.0 ** -25 * scale
+    assert e < 0.5
+    tol_o, tol_l = R.tolerances(ro, rl, pv, qk, sv, d)
+    assert np.all(np.abs(to_f64(lse) - rl) <= tol_l + e)
+    assert np.all(np.abs(to_f64(o) - ro) <= tol_o * 2 + (2 * e + 4 * e * e) * 2 * pv)
+
+
+@pytest.mark.parametrize("heads,length", [(2, 1), (2, 6000), (80, 6000)], ids=["block", "split", "many_rows"])
+def test_attention_whose_scores_are_all_minus_infinity_is_an_empty_row(heads, length):
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    arrays, table, cu, q, gains = _problem(64, 16, heads, 1, [length], [1], seed=127)
+    arrays[0][..., 2] = arrays[0][..., 2] & 0xF0 | 0x9  # channel 4 of every key: -1/2 of its scale,
+    arrays[1][:] = 0x38                                 # which is 1
+    x = to_dev(q)
+    x[0, 0, 4], x[0, 1, 4] = math.inf, -math.inf
+    o, lse = api.kv4_attention(x, _cache_of(arrays, gains), _i32(table), _i32([length]))
+    api.check_device_error()
+    assert torch.all(o[0, 0] == 0) and lse[0, 0] == -math.inf
+    assert torch.all(torch.isnan(o[0, 1])) and torch.isnan(lse[0, 1])
+    assert torch.all(torch.isfinite(o[0, 2:])) and torch.all(torch.isfinite(lse[0, 2:]))
+
+
+def test_page_grow_of_negative_page_ids():
+    """An id below 0 is a page to the lengths and the count, and none to the slots."""
+    from tiled_attention_tmem_gb300 import api
+    held, add, table, stack = [5, 16, 0], [20, 3, 40], [[-1, 8, 8, 8], [4, 8, 8, 8], [8, 8, 8, 8]], [7, -2, 9, -5, 11, 12]
+    t = _i32(table)
+    got = api.page_grow(_i32(held), _i32(add), t, _i32(stack), _i32([6]), 16, 70)
+    ref = R.pages(held, add, table, stack, 6, 16, 70)
+    assert list(ref[3]) == [25, 19, 40] and (ref[0][:63] < 0).any()
+    for g, r in zip(got, (ref[0], ref[1], ref[3], [ref[4]])):
+        assert np.array_equal(g.cpu().numpy(), r)
+    assert np.array_equal(t.cpu().numpy(), ref[2])

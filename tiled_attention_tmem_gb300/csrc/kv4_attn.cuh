@@ -14,8 +14,10 @@
 // soon as it is done with a K or a V; both products run on mma.m16n8k16 with f16
 // operands and fp32 accumulators, from registers:
 //   S^T = K Q^T : A = 16 tokens x 16 channels, dequantised in registers (exact in
-//                 f16), B = Q rows (f16; each row scaled by a power of two into
-//                 f16's range, which its score factor takes back)
+//                 f16), B = Q rows (f16, the type that K's products are exact in and so
+//                 the MMA's; each row scaled by a power of two so that its largest channel
+//                 is in [1, 2), which its score factor takes back: bf16's eight bits are
+//                 exact down to 2^-17, and what is below is off by 2^-25 at most)
 //   O^T += V^T P^T : A = 16 channels x 16 tokens; the codes of two tokens are
 //                 interleaved before conversion, so each f16 pair is one channel at
 //                 two tokens; B = P, transposed by movmatrix from S^T's layout
@@ -60,9 +62,13 @@ struct Kv4AttnParams {
   float v_gain;   // v_gain * 2^8
 };
 
+// P is rounded to f16 for the product with V (both operands of an MMA have one type), and
+// its sum taken before that, in fp32: the rounding errors of a row are independent, 2^-11 of
+// a probability at most each, and shared between numerator and sum they would be no smaller.
 // P is kept times 2^7 (m is the maximum less 7), and the maximum is only renewed
 // when it grew by more than 8: p <= 2^15 fits f16, and what f16 flushes lies
-// 2^-32 below the largest.
+// 2^-32 below the largest.  (ex2.approx is good to 2^-22 of its value; a score
+// of a few units is no finer in fp32.)
 constexpr float kKv4Lift = 7.f;
 constexpr float kKv4Grow = 8.f;
 
