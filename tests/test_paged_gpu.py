@@ -1220,3 +1220,34 @@ def test_page_grow_of_negative_page_ids():
     for g, r in zip(got, (ref[0], ref[1], ref[3], [ref[4]])):
         assert np.array_equal(g.cpu().numpy(), r)
     assert np.array_equal(t.cpu().numpy(), ref[2])
+
+
+FIRST_CALL = """
+import sys
+import torch
+sys.path[:0] = {paths!r}
+from tiled_attention_tmem_gb300 import api
+dev = "cuda:0"
+i32 = dict(dtype=torch.int32, device=dev)
+cache = api.KV4Cache.empty(40, 1, 16, 64, device=dev)
+cache.k_scales.fill_(0x38), cache.v_scales.fill_(0x38)
+cache.v_codes.fill_(0x22)
+q, table, lengths = torch.ones(1, 2, 64, device=dev).bfloat16(), torch.arange(40, **i32)[None], torch.full((1,), 600, **i32)
+graph, out = torch.cuda.CUDAGraph(), torch.zeros(1, 2, 64, device=dev).bfloat16()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    api.kv4_attention(q, cache, table, lengths, out=out)
+graph.replay()
+api.check_device_error()
+assert torch.all(out == 1), out
+print("captured")
+"""
+
+
+def test_the_first_call_of_a_process_can_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALL.format(paths=[root])], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "captured" in out.stdout, out.stdout + out.stderr[-2000:]

@@ -56,12 +56,20 @@ int* device_error_word() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lock(g_mutex);
   if (!g_err_word[dev]) {
+    // The first call may be under stream capture, which forbids allocating, but for a thread
+    // in relaxed mode; and the zeros are written at once, on a stream that no capture is on.
     int* w = nullptr;
-    if (cudaMalloc(&w, 2 * sizeof(int)) != cudaSuccess) return nullptr;
-    if (cudaMemset(w, 0, 2 * sizeof(int)) != cudaSuccess) {
-      cudaFree(w);
-      return nullptr;
-    }
+    cudaStream_t own = nullptr;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+    const bool made = cudaMalloc(&w, 2 * sizeof(int)) == cudaSuccess &&
+                      cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking) == cudaSuccess &&
+                      cudaMemsetAsync(w, 0, 2 * sizeof(int), own) == cudaSuccess &&
+                      cudaStreamSynchronize(own) == cudaSuccess;
+    if (own) cudaStreamDestroy(own);
+    if (!made && w) cudaFree(w);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (!made) return nullptr;
     g_err_word[dev] = w;
   }
   return g_err_word[dev];
