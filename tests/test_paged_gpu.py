@@ -1073,6 +1073,9 @@ def _long_reference(cache, table, cu, q, lengths, scale):
                           torch.zeros((T, H, d), **new), torch.zeros((T, H), **new), torch.zeros((T, H, d), **new))
     for b, n in enumerate(lengths):
         t0, t1 = int(cu[b]), int(cu[b + 1])
+        if n == 0 or t0 == t1:
+            o[t0:t1], lse[t0:t1] = 0.0, -math.inf
+            continue
         ids = table[b, :-(-n // page)].long()
         fine = ((ids >= 0) & (ids < cache.pages)).repeat_interleave(page)[:n]
         ids = ids.clamp(0, cache.pages - 1)
