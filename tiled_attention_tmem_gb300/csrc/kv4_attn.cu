@@ -32,7 +32,9 @@ int choose_nt(int d, long long rows) {
 //   d = 256  8 rows 34 / 42, 77 / 118     9 rows 44 / 42, 127 / 118
 //   d = 384  16 rows 63 / 67, 186 / 195   20 rows 86 / 69, 269 / 197
 // With fewer tokens it starts a few us later (8 of 2048, first case above the bound: 24 / 21,
-// 20 / 20, 22 / 21, 21 / 22, 21 / 23, 36 / 35).
+// 20 / 20, 22 / 21, 21 / 22, 21 / 23, 36 / 35).  All with as many queries a request: where one
+// request has many and the others one, the mean gives the narrow form, which reads that
+// request's tokens for each of its tiles.
 bool use_wide(int d, long long rows) { return rows > 8 * most_nt(d) * (d == 192 || d == 256 ? 1 : 2); }
 
 // Three tiles, on units of 32 tokens, where they save the second pass of two row tiles of 16.
@@ -69,7 +71,7 @@ bool make_plan(int B, int H, int Hkv, int d, int max_q, int page, int width, lon
   // us (solo / split) at d = 128, page 64: 64 triples of 4, 8, 16, 32 units 6.0 / 9.0,
   // 7.4 / 9.3, 10.5 / 10.0, 16.9 / 12.5; 256 triples 6.6 / 11.4, 8.7 / 13.9, 15.0 / 20.8,
   // 24.4 / 27.8; 4 triples of 16 units 11.0 / 8.6; 2048 triples (several waves) of 4 units
-  // 35.8 / 30.2.
+  // 35.8 / 30.2.  (Measured with tiles of 8 rows; other d and tiles follow the same rule.)
   const long long units = ((long long)width * page + kv4_unit(d, plan.nt) - 1) / kv4_unit(d, plan.nt);
   const int sms = sm_count_cached();
   plan.solo = plan.triples <= kv4_solo_blocks(d, plan.nt) * sms && units <= 10 + plan.triples / 10;

@@ -18,7 +18,9 @@
 // What bounds it now, in cycles per 64 tokens at d = 128 (floors: reading 410, MMAs 510,
 // exponentials 4 a row): the softmax warps, 1070 of work and 490 of hand-over between
 // units; conversion takes 800 a tile beside it, and the MMA warp sees a probability tile
-// 450 after it is written.
+// 450 after it is written (clock64 stamps of an instrumented copy, which is not kept).
+// 15 warps at 128 registers fill the register file, so d = 128, 192 and 256 spill 56, 4 and
+// 24 bytes a thread.
 #pragma once
 #include "kv4_attn.cuh"
 
