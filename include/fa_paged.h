@@ -123,11 +123,11 @@ fa_status fa_kv4_load(const fa_kv4_cache* cache, const long long* slots, int T, 
  * Query i of the n_q of request b sees the keys j <= lengths[b] - n_q + i; kv head
  * h / (H/Hkv) serves head h:
  *   s_j = scale * k_gain * q . k_j,  lse = ln sum_j exp(s_j),  o = sum_j exp(s_j - lse) v_j.
- * Scores, maxima and sums are fp32.  q is taken exactly, but for channels below 2^-17 of
+ * Scores, maxima and sums are fp32 (a score past its range is an infinity).  q is taken exactly, but for channels below 2^-17 of
  * their row's largest magnitude, which are off by 2^-25 of it at most; exp by 2^-21 of
  * itself; the probabilities that weigh v are rounded to f16, o to bf16 once.
- * A query that sees no key, or whose scores are all -inf (an infinity in q), gets o = 0
- * and lse = -inf; other infinities and NaN make their row NaN.  Rows of o and lse that no
+ * A query that sees no key, or whose scores are all -inf, gets o = 0 and lse = -inf;
+ * other infinities, as from one in q, and NaN make their row NaN.  Rows of o and lse that no
  * query of a request owns are left as they were.  The first max_q queries of a
  * request are computed (max_q times H/Hkv below 2^31).  A request whose queries do
  * not lie in [0, T) has none; requests that share a query leave either's result in
