@@ -1254,3 +1254,26 @@ def test_the_first_call_of_a_process_can_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     out = subprocess.run([sys.executable, "-c", FIRST_CALL.format(paths=[root])], capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and "captured" in out.stdout, out.stdout + out.stderr[-2000:]
+
+
+@pytest.mark.parametrize("heads,kv,width", [(4, 2, 4), (4, 2, 400), (80, 1, 300)], ids=["block", "split", "many_rows"])
+def test_lengths_at_the_ends_of_their_type(heads, kv, width):
+    """2^31 - 1 tokens over a table that holds fewer, and a most negative count: attention sees
+    what the table holds, pages and slots past it are none."""
+    from tiled_attention_tmem_gb300 import api
+    most, least, page = (1 << 31) - 1, -(1 << 31), 16
+    arrays, table, cu, q, gains = _problem(64, page, heads, kv, [width * page] * 2, [2, 1], seed=131)
+    table, lengths = np.ascontiguousarray(table[:, :width]), [most, least]
+    _attend((arrays, table, cu, q, gains), lengths, 2)
+    held, add = [most, 0, width * page], [most, most, 3]
+    three, stack = np.concatenate([table, table[:1]]), np.arange(8) + 5
+    t = _i32(three)
+    got = api.page_grow(_i32(held), _i32(add), t, _i32(stack), _i32([8]), page, 50)
+    ref = R.pages(held, add, three, stack, 8, page, 50)
+    for g, r in zip(got, (ref[0], ref[1], ref[3], [ref[4]])):
+        assert np.array_equal(g.cpu().numpy(), r)
+    assert np.array_equal(t.cpu().numpy(), ref[2])
+    first, count = [most, least, width * page - 2], [9, 2, 7]
+    got = api.page_slots(_i32(first), _i32(count), t, page, 20)
+    ref = R.pages(first, count, ref[2], [], None, page, 20)
+    assert np.array_equal(got[0].cpu().numpy(), ref[0]) and np.array_equal(got[1].cpu().numpy(), ref[1])
