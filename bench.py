@@ -56,9 +56,9 @@ NCU_TRAFFIC = {
 }
 
 
-# Beginnings of the names of CUDA sources that cannot change that traffic: the serving
+# Beginnings of the names of CUDA sources that cannot change that traffic: the serving and packed
 # operators, and what the library reports of itself.  No other source includes one of them.
-TRAFFIC_FREE_SOURCES = ("kv4", "paged", "report")
+TRAFFIC_FREE_SOURCES = ("kv4", "packed", "paged", "report")
 
 
 def parse_args():

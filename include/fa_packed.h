@@ -1,0 +1,53 @@
+/*
+ * fa_packed.h - C ABI of attention over packed sequences and of the norms and
+ * rotation of its queries and keys (GB300, sm_103a).  Statuses, streams, the
+ * device error word and the profile are those of fa.h.
+ *
+ * Packed sequences: sequences of different lengths lie one behind the other in
+ * arrays [T, heads, d]; tokens cu[b] .. cu[b + 1] - 1 are sequence b, and a query
+ * sees keys of its own sequence only.  kv head h / (H / Hkv) serves head h.
+ * Arrays are bf16 device memory, 16-byte aligned, with dense channels; the
+ * strides of a token and of a head are given in elements, positive multiples of 8
+ * (of a dimension of one element any), below 2^34.  d: 64, 96, 128, 192, 256 or 384.
+ *
+ * cu (int32 [B + 1], device memory) must not decrease.  Its contents are checked
+ * on the device: a sequence whose tokens do not lie in [0, T) has none.  Sequences
+ * of no token are allowed.  Whatever cu holds, no call reads or writes
+ * outside its arrays; rows that two sequences share hold either's results.
+ */
+#ifndef TILED_ATTENTION_TMEM_GB300_FA_PACKED_H_
+#define TILED_ATTENTION_TMEM_GB300_FA_PACKED_H_
+
+#include "fa_paged.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Forward.  For query i and keys j of one sequence (causal: j <= i):
+ *   s_ij = scale * q_i . k_j,  lse_i = ln sum_j exp(s_ij),  o_i = sum_j exp(s_ij - lse_i) v_j
+ * q [T, H, d], k and v [T, Hkv, d] (read); o [T, H, d], lse fp32 [T, H] dense
+ * (written).  Scores, maxima and sums are fp32; the probabilities that weigh v are
+ * rounded to bf16, o to bf16 once.  Rows of o and lse of no sequence are left as
+ * they were, and what q, k and v hold there, or in another sequence, never reaches a
+ * result; a NaN or infinity in k or v of a token may reach any query of its own sequence.
+ * A query whose scores are all -inf gets o = 0 and lse = -inf.  o must not
+ * overlap the inputs.
+ * H a multiple of Hkv, H / Hkv at most 32 (else FA_ERR_UNSUPPORTED), (T + B) * Hkv at
+ * most 2^28, scale finite and > 0.  workspace: fa_packed_fwd_workspace_size bytes,
+ * 256-byte aligned, not shared with a concurrent call.
+ */
+fa_status fa_packed_fwd(const void* q, long long q_token, long long q_head, const void* k, long long k_token,
+                        long long k_head, const void* v, long long v_token, long long v_head, void* o,
+                        long long o_token, long long o_head, float* lse, const int* cu, int B, int T, int H, int Hkv,
+                        int d, float scale, int causal, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace fa_packed_fwd needs; 0 for shapes without work and invalid ones. */
+size_t fa_packed_fwd_workspace_size(int B, int T, int H, int Hkv, int d);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* TILED_ATTENTION_TMEM_GB300_FA_PACKED_H_ */

@@ -34,14 +34,20 @@
 extern "C" {
 #endif
 
-/* Kernel kinds of these calls, for fa_profile_stop_kinds and fa_kernel_name. */
+/* Kernel kinds of these calls and of those of fa_packed.h, for fa_profile_stop_kinds and fa_kernel_name. */
 enum {
   FA_KERNEL_PAGE = 9,       /* page tables and slots */
   FA_KERNEL_KV4_STORE = 10, /* 4-bit cache: store */
   FA_KERNEL_KV4_LOAD = 11,  /* 4-bit cache: load */
   FA_KERNEL_KV4_ATTN = 12,  /* attention over the 4-bit cache */
   FA_KERNEL_KV4_MERGE = 13, /* merge of its warps' parts */
-  FA_KERNEL_ALL_KINDS = 14
+  /* fa_packed.h (attention over packed sequences counts as the dense kernels it shares) */
+  FA_KERNEL_PACKED_PLAN = 14, /* packed sequences: order of work, tensor maps */
+  FA_KERNEL_ROTATE = 15,      /* norms and rotation of queries and keys */
+  FA_KERNEL_ROTATE_BWD = 16,  /* their gradients */
+  FA_KERNEL_ROTATE_SUM = 17,  /* the weights' gradients, summed over the blocks */
+  FA_KERNEL_KV4_APPEND = 18,  /* 4-bit cache: rotated append */
+  FA_KERNEL_ALL_KINDS = 19
 };
 
 /* The cache as the calls take it (host memory; read during the call only). */

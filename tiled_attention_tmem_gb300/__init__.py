@@ -16,7 +16,7 @@ from .api import attention_backward, attention_forward, check_device_error  # no
 
 
 def __getattr__(name):
-    # KV4Cache, page_grow, page_slots, kv4_store, kv4_load, kv4_attention: loaded on first use.
-    if name in api._SERVING:
+    # The serving operators and those of packed sequences: loaded on first use.
+    if name in api._SERVING or name in api._PACKED:
         return getattr(api, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -136,7 +136,15 @@ _SERVING = ("KV4Cache", "page_grow", "page_slots", "kv4_store", "kv4_load", "kv4
             "kv4_attention_workspace_bytes", "PAGE_SIZES")
 
 
+# Attention over packed sequences (``packed``), likewise.
+_PACKED = ("packed_attention_forward", "packed_forward_workspace_bytes")
+
+
 def __getattr__(name):
+    if name in _PACKED:
+        from . import packed
+        globals().update({n: getattr(packed, n) for n in _PACKED})
+        return globals()[name]
     if name in _SERVING:
         from . import serving
         globals().update({n: getattr(serving, n) for n in _SERVING})

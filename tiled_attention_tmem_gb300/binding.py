@@ -1,5 +1,5 @@
-"""ctypes binding of the C ABI in ``include/fa.h`` and ``include/fa_paged.h`` (argument
-marshalling only).
+"""ctypes binding of the C ABI in ``include/fa.h``, ``include/fa_paged.h`` and
+``include/fa_packed.h`` (argument marshalling only).
 
 The functions here carry the C names and take raw device pointers (ints),
 sizes and a CUDA stream handle; every step of the computation runs in the
@@ -71,6 +71,9 @@ SIGNATURES = {
     "fa_kv4_load": (_I, [_VP, _VP, _I, _VP, _VP, _VP]),
     "fa_kv4_attn": (_I, [_VP, _VP, _LL, _LL, _I, _VP, _I, _VP, _I, _VP, _I, _I, _F, _VP, _LL, _LL, _VP, _VP, _SZ, _VP]),
     "fa_kv4_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    # include/fa_packed.h
+    "fa_packed_fwd": (_I, [_VP, _LL, _LL] * 4 + [_VP, _VP, _I, _I, _I, _I, _I, _F, _I, _VP, _SZ, _VP]),
+    "fa_packed_fwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
 }
 
 _lib = None
@@ -245,7 +248,17 @@ def fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q, page, width) -> int:
     return lib().fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q, page, width)
 
 
-FA_KERNEL_ALL_KINDS = 14
+def fa_packed_fwd(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, o, o_token, o_head, lse, cu, B, T, H, Hkv,
+                  d, scale, causal, workspace, workspace_bytes, stream) -> int:
+    return lib().fa_packed_fwd(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, o, o_token, o_head, lse, cu,
+                               B, T, H, Hkv, d, float(scale), int(causal), workspace, workspace_bytes, stream)
+
+
+def fa_packed_fwd_workspace_size(B, T, H, Hkv, d) -> int:
+    return lib().fa_packed_fwd_workspace_size(B, T, H, Hkv, d)
+
+
+FA_KERNEL_ALL_KINDS = 19
 
 
 def fa_profile_start() -> int:

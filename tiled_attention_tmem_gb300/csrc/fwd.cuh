@@ -40,14 +40,20 @@
 // normalised by its own sum (fp32) and its log2-domain log-sum-exp L_s = m + log2 l
 // (-inf where no key of the part is visible to the row); fwd_merge_kernel then
 // combines the parts with the same max/sum algebra as the online softmax.
+//
+// Packed sequences (RaggedFwdParams): the same kernel over the tiles of sequences of
+// different lengths, with the G query heads of a kv head as rows of a token (ragged.cuh).
+// A scheduling warp claims the items; every other line of the pipeline is shared.
 #pragma once
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "ragged.cuh"
 
 namespace fa {
 
 struct FwdParams {
+  static constexpr bool kRagged = false;
   CUtensorMap q_map;  // 3-D {d, N, B*H} bf16, box {64, 128, 1}, 128-byte swizzle
   CUtensorMap k_map;  // same tensor shape, box {64, BN, 1}
   CUtensorMap v_map;
@@ -65,6 +71,24 @@ struct FwdParams {
   int splits;    // key-range parts per query block (1: O and LSE are written directly)
   float* opart;  // splits > 1: fp32 [splits, B*H, N, d], part s of row i = O_s(i) / l_s(i)
   float* lpart;  // splits > 1: fp32 [splits, B*H, N], log2-domain L_s(i) (-inf: no visible key)
+};
+
+// Packed sequences: q, o [T, H, d] and k, v [T, Hkv, d] with strides in elements.
+struct RaggedFwdParams {
+  static constexpr bool kRagged = true;
+  const CUtensorMap* maps;  // [B][3]: q {d, G, end, Hkv} box {64, G, tokens, 1}; k, v {d, end, Hkv} box {64, BN, 1}
+  RaggedSched sched;
+  const uint16_t* q;  // (read row by row by QT configurations)
+  uint16_t* o;
+  long long q_token, q_head, o_token, o_head;
+  float* lse;  // [T, H]
+  int* err;
+  int H, Hkv;
+  int G;       // query heads of a kv head
+  int tokens;  // tokens of a 128-row tile: 128 / G rounded down
+  int dv;
+  float scale_log2;
+  int causal;
 };
 
 // Merge of split-KV parts: for each row, L = log2 sum_s 2^(L_s) and
@@ -109,9 +133,12 @@ struct FwdCfg {
   static constexpr int B_QFULL = 0, B_KVFULL = 1, B_KVEMPTY = 1 + STAGES,
                        B_SFULL = 1 + 2 * STAGES, B_PREADY = B_SFULL + NQ * SB,
                        B_OREADY = B_PREADY + NQ * SB, B_DONE = B_OREADY + NQ * SB, B_QEMPTY = B_DONE + 1,
-                       B_QREADY = B_QEMPTY + 1, NBAR = B_QREADY + 1;
+                       B_QREADY = B_QEMPTY + 1, B_ITEMFULL = B_QREADY + 1, B_ITEMEMPTY = B_ITEMFULL + kRaggedRing,
+                       NBAR = B_ITEMEMPTY + kRaggedRing;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16 + 1024;  // + alignment slack
+  static constexpr uint32_t OFF_RING = OFF_MISC + 16;  // packed sequences: claimed items
+  static constexpr int ITEM_READERS = 2 + 4 * NQ;      // the producer, the MMA warp, the softmax warps
+  static constexpr uint32_t SMEM_BYTES = OFF_RING + kRaggedRing * kRaggedRingBytes + 1024;  // + alignment slack
   static constexpr int TMEM_S = 0;              // S_t (and P_t aliased) at (t*SB + buffer)*BN
   static constexpr int TMEM_O = NQ * SB * BN;   // O_t at TMEM_O + t*D
   static constexpr int TMEM_Q = TMEM_O + NQ * D;  // QT: Q_t as packed bf16 pairs at TMEM_Q + t*D/2
@@ -125,11 +152,47 @@ struct FwdCfg {
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
+// Per head dimension: query tiles per CTA, keys per tile, K/V ring depth.
+//  d = 64 : 2 x 128 query rows, 128 keys, 6 stages (Q 32 KiB + ring 96 KiB)
+//  d = 128: 2 x 128 query rows, 128 keys, 4 stages (Q 64 KiB + ring 128 KiB)
+//  d = 192: 1 x 128 query rows, 64 keys, 8 stages, Q in TMEM (ring 192 KiB)
+//  d = 256: 1 x 128 query rows, 64 keys, 6 stages, Q in TMEM (ring 192 KiB)
+//  d = 384: 1 x 128 query rows, 64 keys, 2 stages, Q in shared memory
+// d = 96 runs the d = 128 kernel: the TMA boxes read columns past d as zeros,
+// which leave S = QK^T unchanged and give zero output columns that are not
+// stored.
+using Fwd64 = FwdCfg<64, 2, 128, 6>;
+using Fwd128 = FwdCfg<128, 2, 128, 4>;
+using Fwd192 = FwdCfg<192, 1, 64, 8, true>;
+using Fwd256 = FwdCfg<256, 1, 64, 6, true>;
+// d = 384: 1 x 128 query rows, 64 keys, Q in shared memory (96 KiB) with S
+// double-buffered in TMEM next to the 384-column O (512 columns), two K/V slots
+// of 48 KiB.
+using Fwd384 = FwdCfg<384, 1, 64, 2, false, true>;
+
 __device__ __forceinline__ int fwd_kv_tiles(int qrow0, int N, int causal, int BN) {
   if (qrow0 >= N) return 0;
   if (!causal) return (N + BN - 1) / BN;
   const int last = min(qrow0 + 127, N - 1);
   return last / BN + 1;
+}
+
+template <int NQ, bool RAGGED>
+struct FwdItem {
+  int q0, bh, nmax;
+  int nkv[NQ];
+};
+template <int NQ>
+struct FwdItem<NQ, true> {
+  int q0, bh, nmax;  // first token of the block in its sequence, kv head
+  int nkv[NQ];
+  int start, len, seq;  // the sequence's first token, its tokens, its index
+};
+
+// The same for a tile of `tokens` tokens from `tok0` of a sequence of `len`.
+__device__ __forceinline__ int ragged_kv_tiles(int tok0, int tokens, int len, int causal, int BN) {
+  if (tok0 >= len) return 0;
+  return (causal ? min(tok0 + tokens, len) - 1 : len - 1) / BN + 1;
 }
 
 // Bounded wait used only while draining in-flight copies at teardown; it does
@@ -143,8 +206,11 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
 
 // SPLIT: the split-KV instantiation (p.splits > 1); the plain one keeps lo = 0
 // and s = 0 as constants and has no part epilogue.
-template <class C, bool SPLIT>
-__global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constant__ FwdParams p) {
+// P: FwdParams, or RaggedFwdParams (packed sequences; never split).
+template <class C, bool SPLIT, class P = FwdParams>
+__global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constant__ P p) {
+  constexpr bool RAGGED = P::kRagged;
+  static_assert(!(RAGGED && SPLIT), "packed sequences are not split");
   constexpr int D = C::D, NQ = C::NQ, BN = C::BN, S = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -171,6 +237,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
     mbar_init(bar0 + 8 * C::B_DONE, 1);
     mbar_init(bar0 + 8 * C::B_QEMPTY, 1);
     mbar_init(bar0 + 8 * C::B_QREADY, 4 * NQ);
+    if constexpr (RAGGED)
+      for (int k = 0; k < kRaggedRing; ++k) {
+        mbar_init(bar0 + 8 * (C::B_ITEMFULL + k), 1);
+        mbar_init(bar0 + 8 * (C::B_ITEMEMPTY + k), C::ITEM_READERS);
+      }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -191,7 +262,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
   // the most key tiles first.  CTA c takes items in "snake" order over rounds
   // (c, 2G-1-c, 2G+c, ...) so heavy and light items even out across CTAs.
   // Barrier phases run on across items: every role counts the same iterations.
-  const int n_qblk = (p.N + 128 * NQ - 1) / (128 * NQ);
+  int n_qblk = 0;
+  if constexpr (!RAGGED) n_qblk = (p.N + 128 * NQ - 1) / (128 * NQ);
   auto item_of = [&](int r) -> int {
     const int G = gridDim.x, c = blockIdx.x;
     return r * G + ((r & 1) ? (G - 1 - c) : c);
@@ -199,15 +271,36 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
   // Item w: query block and head from w / splits, key part s = w % splits.
   // Part s of a block whose tiles see nf key tiles at most is tiles
   // [s*nf/splits, (s+1)*nf/splits); nkv[t] counts those tile t sees (may be 0).
-  struct Item {
-    int q0, bh, nmax;
-    int nkv[NQ];
-  };
+  using Item = FwdItem<NQ, RAGGED>;
   struct Part {
     int s, lo;
   };
+  auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
+  // Packed: the t-th item of this CTA, for the whole warp or one thread.
+  volatile int* item_ring = reinterpret_cast<volatile int*>(gbase + C::OFF_RING);
+  auto ragged_at = [&](int t, Item& it, auto one) -> bool {
+    if constexpr (RAGGED) {
+      RaggedItem x;
+      if (!ragged_item<decltype(one)::value>(t, x, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY), ab,
+                                             (kKFwd << 8) | 12))
+        return false;
+      it.start = x.start, it.len = x.len, it.seq = x.seq, it.bh = x.head;
+      const int blocks = (x.len + NQ * p.tokens - 1) / (NQ * p.tokens);
+      it.q0 = (p.causal ? blocks - 1 - x.tile : x.tile) * NQ * p.tokens;
+      it.nmax = 0;
+#pragma unroll
+      for (int t2 = 0; t2 < NQ; ++t2) {
+        it.nkv[t2] = ragged_kv_tiles(it.q0 + t2 * p.tokens, p.tokens, x.len, p.causal, BN);
+        it.nmax = max(it.nmax, it.nkv[t2]);
+      }
+      return true;
+    } else {
+      return false;
+    }
+  };
   auto coords = [&](int w) {
     Item it;
+    if constexpr (!RAGGED) {
     int qb;
     const int wb = SPLIT ? w / p.splits : w;
     grouped_order(wb, n_qblk, p.BH, p.group, qb, it.bh);
@@ -231,7 +324,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         it.nmax = max(it.nmax, it.nkv[t]);
       }
     }
+    }
     return it;
+  };
+  // Item r of this CTA; false after the last one.
+  auto item_at = [&](int r, Item& it, auto one) -> bool {
+    if constexpr (RAGGED) {
+      return ragged_at(r, it, one);
+    } else {
+      const int w = item_of(r);
+      if (w >= p.items) return false;
+      it = coords(w);
+      return true;
+    }
   };
   // Split instantiation: part index s of item w and its first key tile.
   auto part_of = [&](int w) {
@@ -249,7 +354,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
     }
     return pt;
   };
-  auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
 
   // Two softmax warpgroups (384 threads, 168 registers each at launch): the
   // producer/MMA warpgroup gives registers to the softmax warpgroups;
@@ -261,9 +365,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
-        tma_prefetch_desc(&p.q_map);
-        tma_prefetch_desc(&p.k_map);
-        tma_prefetch_desc(&p.v_map);
+        const CUtensorMap *q_map, *k_map, *v_map;
+        if constexpr (!RAGGED) {
+          q_map = &p.q_map, k_map = &p.k_map, v_map = &p.v_map;
+          tma_prefetch_desc(q_map);
+          tma_prefetch_desc(k_map);
+          tma_prefetch_desc(v_map);
+        }
+        int seq = -1;  // packed: the sequence whose maps these are
         int it = 0, nitems = 0;
         bool ok = true;
         // No L2 prefetches until the CTA's first K tile has landed (at the start
@@ -276,31 +385,55 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
           return warm;
         };
         for (int r = 0; ok; ++r) {
-          const int w = item_of(r);
-          if (w >= p.items) break;
-          const Item I = coords(w);
-          const Part P = part_of(w);
+          Item I;
+          if (!item_at(r, I, ByThread{})) break;
+          const Part part = SPLIT ? part_of(item_of(r)) : Part{0, 0};
+          int row0 = 0;  // first row of the sequence in the maps
+          if constexpr (RAGGED) {
+            row0 = I.start;
+            if (I.seq != seq) {
+              seq = I.seq;
+              q_map = p.maps + 3 * (size_t)seq, k_map = q_map + 1, v_map = q_map + 2;
+              tensormap_acquire(q_map);
+              tensormap_acquire(k_map);
+              tensormap_acquire(v_map);
+            }
+          }
+          // This item's Q tiles: NQ x 128 rows, of which the packed ones are G rows a token.
+          auto load_q = [&]() {
+            if constexpr (RAGGED) {
+              mbar_expect_tx(BAR(C::B_QFULL), NQ * C::PANELS * p.tokens * p.G * 128);
+              for (int t = 0; t < NQ; ++t)
+                for (int pn = 0; pn < C::PANELS; ++pn)
+                  tma_load_4d(sbase + C::OFF_Q + t * C::Q_TILE + pn * C::Q_PANEL, q_map, BAR(C::B_QFULL), 64 * pn, 0,
+                              row0 + I.q0 + t * p.tokens, I.bh);
+            } else {
+              mbar_expect_tx(BAR(C::B_QFULL), NQ * C::Q_TILE);
+              for (int t = 0; t < NQ; ++t)
+                for (int pn = 0; pn < C::PANELS; ++pn)
+                  tma_load_3d(sbase + C::OFF_Q + t * C::Q_TILE + pn * C::Q_PANEL, q_map, BAR(C::B_QFULL), 64 * pn,
+                              I.q0 + 128 * t, I.bh);
+            }
+          };
           // The next item's Q tiles into L2 a few key steps before this item ends,
           // so that its load (or, with Q in TMEM, the softmax warps' row reads)
           // at the item change is served from L2.
           auto prefetch_next_q = [&](int j) {
+            if constexpr (!RAGGED) {
             if (j != max(0, I.nmax - C::QPF) || !is_warm()) return;
             const int w2 = item_of(r + 1);
             if (w2 >= p.items) return;
             const Item J = coords(w2);
             for (int t = 0; t < NQ; ++t)
               if (J.q0 + 128 * t < p.N)
-                for (int pn = 0; pn < C::PANELS; ++pn) tma_prefetch_l2_3d(&p.q_map, 64 * pn, J.q0 + 128 * t, J.bh);
+                for (int pn = 0; pn < C::PANELS; ++pn) tma_prefetch_l2_3d(q_map, 64 * pn, J.q0 + 128 * t, J.bh);
+            }
           };
           if constexpr (C::SD) {
             if (C::QSD && I.nmax > 0) {
               // This item's Q, once the previous item's S MMAs are done reading Q.
               if (!wait_one(BAR(C::B_QEMPTY), (nitems & 1) ^ 1, ab, (kKFwd << 8) | 10)) break;
-              mbar_expect_tx(BAR(C::B_QFULL), NQ * C::Q_TILE);
-              for (int t = 0; t < NQ; ++t)
-                for (int pn = 0; pn < C::PANELS; ++pn)
-                  tma_load_3d(sbase + C::OFF_Q + t * C::Q_TILE + pn * C::Q_PANEL, &p.q_map, BAR(C::B_QFULL), 64 * pn,
-                              I.q0 + 128 * t, I.bh);
+              load_q();
               ++nitems;
             }
             // K(0), then K(j+1) ahead of V(j): the order in which the MMAs read them.
@@ -310,29 +443,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
               mbar_expect_tx(BAR(C::B_KVFULL + s), C::KV_TILE);
               for (int pn = 0; pn < C::PANELS; ++pn)
                 tma_load_3d(sbase + C::OFF_KV + s * C::KV_TILE + pn * C::KV_PANEL, m, BAR(C::B_KVFULL + s),
-                            64 * pn, (P.lo + j) * BN, I.bh);
+                            64 * pn, row0 + (part.lo + j) * BN, I.bh);
               if (j + C::PREFETCH < I.nmax && is_warm())
                 for (int pn = 0; pn < C::PANELS; ++pn)
-                  tma_prefetch_l2_3d(m, 64 * pn, (P.lo + j + C::PREFETCH) * BN, I.bh);
+                  tma_prefetch_l2_3d(m, 64 * pn, row0 + (part.lo + j + C::PREFETCH) * BN, I.bh);
               ++it;
               return true;
             };
-            if (I.nmax > 0) ok = load(&p.k_map, 0);
+            if (I.nmax > 0) ok = load(k_map, 0);
             for (int j = 0; j < I.nmax && ok; ++j) {
               prefetch_next_q(j);
-              if (j + 1 < I.nmax) ok = load(&p.k_map, j + 1);
-              if (ok) ok = load(&p.v_map, j);
+              if (j + 1 < I.nmax) ok = load(k_map, j + 1);
+              if (ok) ok = load(v_map, j);
             }
             continue;
           }
           if (SPLIT && I.nmax == 0) continue;  // an empty key part: nothing to load or compute
           // The previous item's S MMAs must be done reading Q.
           if (!wait_one(BAR(C::B_QEMPTY), (nitems & 1) ^ 1, ab, (kKFwd << 8) | 10)) break;
-          mbar_expect_tx(BAR(C::B_QFULL), NQ * C::Q_TILE);
-          for (int t = 0; t < NQ; ++t)
-            for (int pn = 0; pn < C::PANELS; ++pn)
-              tma_load_3d(sbase + C::OFF_Q + t * C::Q_TILE + pn * C::Q_PANEL, &p.q_map, BAR(C::B_QFULL), 64 * pn,
-                          I.q0 + 128 * t, I.bh);
+          load_q();
           ++nitems;
           for (int j = 0; j < I.nmax && ok; ++j) {
             prefetch_next_q(j);
@@ -343,14 +472,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
                 break;
               }
               mbar_expect_tx(BAR(C::B_KVFULL + s), C::KV_TILE);
-              const CUtensorMap* m = wkv ? &p.v_map : &p.k_map;
+              const CUtensorMap* m = wkv ? v_map : k_map;
               for (int pn = 0; pn < C::PANELS; ++pn)
                 tma_load_3d(sbase + C::OFF_KV + s * C::KV_TILE + pn * C::KV_PANEL, m, BAR(C::B_KVFULL + s),
-                            64 * pn, (P.lo + j) * BN, I.bh);
+                            64 * pn, row0 + (part.lo + j) * BN, I.bh);
               // Pull K/V tiles a few steps beyond the ring into L2.
               if (j + C::PREFETCH < I.nmax && is_warm())
                 for (int pn = 0; pn < C::PANELS; ++pn)
-                  tma_prefetch_l2_3d(m, 64 * pn, (P.lo + j + C::PREFETCH) * BN, I.bh);
+                  tma_prefetch_l2_3d(m, 64 * pn, row0 + (part.lo + j + C::PREFETCH) * BN, I.bh);
               ++it;
             }
           }
@@ -413,9 +542,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
             mma_commit(BAR(C::B_SFULL + t * C::SB + b));
           };
           for (int r = 0; ok; ++r) {
-            const int w = item_of(r);
-            if (w >= p.items) break;
-            const Item I = coords(w);
+            Item I;
+            if (!item_at(r, I, ByWarp{})) break;
             // An empty key part has no Q hand-off (the softmax warps skip it too).
             if (I.nmax <= 0) continue;
             // QT: the softmax warps have written this item's Q into TMEM; QSD: its TMA load landed.
@@ -470,9 +598,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
           }
         } else
         for (int r = 0; ok; ++r) {
-          const int w = item_of(r);
-          if (w >= p.items) break;
-          const Item I = coords(w);
+          Item I;
+          if (!item_at(r, I, ByWarp{})) break;
           if (SPLIT && I.nmax == 0) continue;  // an empty key part (the producer loaded nothing)
           ok = wait_warp(BAR(C::B_QFULL), nitems & 1, ab, (kKFwd << 8) | 2);
           ++nitems;
@@ -538,6 +665,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         wait_drain(BAR(C::B_DONE), 0);
       }
       __syncwarp();
+    } else if (RAGGED && warp == 3) {
+      // --------------------------------------------------------- scheduling
+      if constexpr (RAGGED)
+        ragged_schedule(p.sched, NQ * p.tokens, 1, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY), ab,
+                        (kKFwd << 8) | 13);
     }
     } else {
       // ------------------------------------------------------------ softmax
@@ -556,17 +688,31 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
       // QT: item wq's query row r as packed bf16 pairs into TMEM lane r (the A
       // operand of S = Q K^T).  Called once the S MMAs of the previous item,
       // the last readers of these columns, are known to be complete.
-      auto write_q = [&](int wq) {
-        const Item J = coords(wq);
-        const int qrow = J.q0 + 128 * t + r;
-        const uint16_t* qsrc = p.q + ((size_t)J.bh * p.N + (qrow < p.N ? qrow : 0)) * p.dv;
+      // Packed: the token and head of the tile that row r is, none for the rows behind them.
+      int rtok = 0, rhead = 0;
+      bool rown = true;
+      if constexpr (RAGGED) {
+        rtok = t * p.tokens + r / p.G, rhead = r % p.G;
+        rown = r < p.tokens * p.G;
+      }
+      auto write_q = [&](const Item& J) {
+        const uint16_t* qsrc;
+        bool qok;
+        if constexpr (RAGGED) {
+          qok = rown && J.q0 + rtok < J.len;
+          qsrc = p.q + (qok ? (J.start + J.q0 + rtok) * p.q_token + (J.bh * p.G + rhead) * p.q_head : 0);
+        } else {
+          const int qrow = J.q0 + 128 * t + r;
+          qok = qrow < p.N;
+          qsrc = p.q + ((size_t)J.bh * p.N + (qok ? qrow : 0)) * p.dv;
+        }
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += 64) {
           uint32_t qw[32];
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (qrow < p.N && c0 + 8 * u < p.dv) x = *reinterpret_cast<const uint4*>(qsrc + c0 + 8 * u);
+            if (qok && c0 + 8 * u < p.dv) x = *reinterpret_cast<const uint4*>(qsrc + c0 + 8 * u);
             qw[4 * u] = x.x;
             qw[4 * u + 1] = x.y;
             qw[4 * u + 2] = x.z;
@@ -583,26 +729,45 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
       // written only for those: one QREADY phase per item the issuer waits for, so
       // the barrier never runs two phases ahead of its waiter.
       auto next_work = [&](int r0) -> int {
+        if constexpr (RAGGED) return -1;
+        else {
         if constexpr (!SPLIT) return item_of(r0) < p.items ? item_of(r0) : -1;
         for (int r2 = r0;; ++r2) {
           const int w2 = item_of(r2);
           if (w2 >= p.items) return -1;
           if (coords(w2).nmax > 0) return w2;
         }
-      };
-      for (int rr = 0; ok; ++rr) {
-        const int w = item_of(rr);
-        if (w >= p.items) break;
-        if (C::QT && rr == 0) {
-          const int wq = next_work(0);
-          if (wq >= 0) write_q(wq);
         }
-        const Item I = coords(w);
-        const Part P = part_of(w);
-        const int qi = I.q0 + 128 * t + r;
+      };
+      Item ahead;  // packed, QT: the next item, taken before this one's epilogue
+      bool have_ahead = false;
+      for (int rr = 0; ok; ++rr) {
+        Item I;
+        if constexpr (RAGGED && C::QT) {
+          if (rr == 0) {
+            have_ahead = item_at(0, ahead, ByWarp{});
+            if (have_ahead) write_q(ahead);
+          }
+          if (!have_ahead) break;
+          I = ahead;
+        } else {
+          if (!item_at(rr, I, ByWarp{})) break;
+        }
+        if (!RAGGED && C::QT && rr == 0) {
+          const int wq = next_work(0);
+          if (wq >= 0) write_q(coords(wq));
+        }
+        const Part part = SPLIT ? part_of(item_of(rr)) : Part{0, 0};
         const int n = I.nkv[t];
         const int bh = I.bh;
-        const int limit = p.causal ? min(qi, p.N - 1) : p.N - 1;
+        int qi, limit;  // this row's query and the last key that it sees
+        if constexpr (RAGGED) {
+          qi = I.q0 + rtok;
+          limit = !rown || qi >= I.len ? -1 : p.causal ? qi : I.len - 1;
+        } else {
+          qi = I.q0 + 128 * t + r;
+          limit = p.causal ? min(qi, p.N - 1) : p.N - 1;
+        }
         float m_used = -INFINITY;
         float l = 0.f;
         for (int j = 0; j < n; ++j) {
@@ -620,7 +785,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
           for (int c = 0; c < BN; c += 32) tmem_ld_32x32b_x32(tS + c, sr + c);
           tmem_wait_ld();
           reg_fence<BN>(sr);
-          const int kbase = (P.lo + j) * BN;
+          const int kbase = (part.lo + j) * BN;
           if (kbase + BN - 1 > limit) {
 #pragma unroll
             for (int c = 0; c < BN; ++c)
@@ -691,8 +856,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
           if (lane == 0) mbar_arrive(BAR(C::B_PREADY + sb));
         }
         if (C::QT && ok && I.nmax > 0) {
-          const int wn = next_work(rr + 1);
-          if (wn >= 0) write_q(wn);
+          if constexpr (RAGGED) {
+            have_ahead = item_at(rr + 1, ahead, ByWarp{});
+            if (have_ahead) write_q(ahead);
+          } else {
+            const int wn = next_work(rr + 1);
+            if (wn >= 0) write_q(coords(wn));
+          }
         }
         if (ok && n > 0) {
           if (!wait_warp(BAR(C::B_OREADY + oready_bar(g + n - 1)), oready_phase(g + n - 1), ab, (kKFwd << 8) | 9)) {
@@ -700,13 +870,52 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
             break;
           }
           tc_fence_after();
-          const bool store = qi < p.N;
           // Staged through this warp's 2 KB of shared memory, 32 columns at a
           // time: each thread writes its row, then each warp store covers 8 rows
           // x 64 contiguous bytes instead of 32 rows x 16 bytes.
           uint8_t* epi = gbase + C::OFF_EPI + (t * 4 + quad) * 2048;
           const int row0 = I.q0 + 128 * t + quad * 32;  // this warp's first query row
-          if constexpr (!SPLIT) {
+          if constexpr (RAGGED) {
+            // Rows of a token and head each: where the four rows that this lane stores go.  A row
+            // whose scores are all -inf is zero.
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint16_t* to[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int rt = quad * 32 + j * 8 + (lane >> 2);
+              const int tok = I.q0 + t * p.tokens + rt / p.G;
+              to[j] = rt < p.tokens * p.G && tok < I.len
+                          ? p.o + (I.start + tok) * p.o_token + (bh * p.G + rt % p.G) * p.o_head + 8 * (lane & 3)
+                          : nullptr;
+            }
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t orr[32];
+              tmem_ld_32x32b_x32(tO + c0, orr);
+              tmem_wait_ld();
+              reg_fence<32>(orr);
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                pk[e >> 1] = pack_bf16(__uint_as_float(orr[e]) * inv, __uint_as_float(orr[e + 1]) * inv);
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint4*>(epi + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
+                    make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int rr2 = j * 8 + (lane >> 2), u = lane & 3;
+                const uint4 val = *reinterpret_cast<const uint4*>(epi + rr2 * 64 + ((u ^ ((rr2 >> 1) & 3)) << 4));
+                if (to[j] && c0 + 8 * u < p.dv) *reinterpret_cast<uint4*>(to[j] + c0) = val;
+              }
+              __syncwarp();
+            }
+            if (limit >= 0)
+              p.lse[(long long)(I.start + qi) * p.H + bh * p.G + rhead] =
+                  l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
+          } else if constexpr (!SPLIT) {
+            const bool store = qi < p.N;
             const float inv = 1.f / l;
             uint16_t* obase = p.o + ((size_t)bh * p.N + (size_t)row0) * p.dv;
 #pragma unroll
@@ -738,8 +947,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
             // Part s of a split-KV pass: fp32 O / l and the log2-domain L_s, staged
             // 16 columns (64 bytes per row) at a time.  A row that sees no key of
             // the part (l = 0) gets O_s = 0 and L_s = -inf.
+            const bool store = qi < p.N;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            float* pbase = p.opart + (((size_t)P.s * p.BH + bh) * p.N + (size_t)row0) * p.dv;
+            float* pbase = p.opart + (((size_t)part.s * p.BH + bh) * p.N + (size_t)row0) * p.dv;
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {
               uint32_t orr[32];
@@ -769,11 +979,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
               }
             }
             if (store)
-              p.lpart[((size_t)P.s * p.BH + bh) * p.N + qi] = l > 0.f ? m_used + log2f(l) : -INFINITY;
+              p.lpart[((size_t)part.s * p.BH + bh) * p.N + qi] = l > 0.f ? m_used + log2f(l) : -INFINITY;
           }
-        } else if (SPLIT && ok && qi < p.N) {
+        } else if constexpr (SPLIT) {
           // This query tile sees no key tile of the part.
-          p.lpart[((size_t)P.s * p.BH + bh) * p.N + qi] = -INFINITY;
+          if (ok && qi < p.N) p.lpart[((size_t)part.s * p.BH + bh) * p.N + qi] = -INFINITY;
         }
         g += n;
       }
@@ -792,7 +1002,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
 // reads the row's `splits` values of L_s (cached), so no shuffles are needed.
 // A part with L_s = -inf saw no key of the row and is skipped (its O_s is
 // not read).  Skipped entirely if a kernel gave up a wait.
-__global__ void __launch_bounds__(256) fwd_merge_kernel(const __grid_constant__ FwdMergeParams p) {
+static __global__ void __launch_bounds__(256) fwd_merge_kernel(const __grid_constant__ FwdMergeParams p) {
   grid_dep_wait();
   if (*reinterpret_cast<volatile const int*>(p.err) != 0) return;
   const int tpr = p.dv / 8;

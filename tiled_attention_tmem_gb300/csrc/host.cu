@@ -117,13 +117,19 @@ fa_status record_cuda_error(cudaError_t e) {
 fa_status make_tile_map(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
                         int elem_bytes, int inner, int N, int BH, int box_inner, int box_rows,
                         CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)N, (cuuint64_t)BH};
+  const cuuint64_t strides[2] = {(cuuint64_t)inner * elem_bytes, (cuuint64_t)N * inner * elem_bytes};
+  const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1};
+  return encode_tile_map(map, base, 3, dims, strides, box, dtype, swizzle);
+}
+
+fa_status encode_tile_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                          const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapDataType dtype,
+                          CUtensorMapSwizzle swizzle) {
   auto fn = encode_fn();
   if (!fn) return record_cuda_error(cudaErrorNotSupported);
-  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)N, (cuuint64_t)BH};
-  cuuint64_t strides[2] = {(cuuint64_t)inner * elem_bytes, (cuuint64_t)N * inner * elem_bytes};
-  cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(map, dtype, 3, const_cast<void*>(base), dims, strides, box, estr,
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, dtype, rank, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return record_cuda_error(cudaErrorInvalidValue);

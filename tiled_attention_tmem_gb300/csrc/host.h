@@ -24,6 +24,13 @@ fa_status make_tile_map(CUtensorMap* map, const void* base, CUtensorMapDataType 
                         int elem_bytes, int inner, int N, int BH, int box_inner, int box_rows,
                         CUtensorMapSwizzle swizzle);
 
+// The same over any tensor of up to five dimensions (innermost first; strides in bytes, from the
+// second dimension on).
+fa_status encode_tile_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                          const cuuint64_t* strides, const cuuint32_t* box,
+                          CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+
 // Heads per launch-order group: enough heads for about two waves of blocks on
 // this device (at least 1, at most BH).  The statically scheduled kernels use
 // one group of all heads under the causal mask, where heaviest-tile-first

@@ -1,0 +1,106 @@
+// Work items of packed sequences: tokens cu[b] .. cu[b + 1] - 1 of one array are
+// sequence b, lengths known on the device only.
+//
+// Grouped heads: the G = H / Hkv query heads of a kv head are G rows of a token, so a
+// tile of M rows holds M / G tokens (rounded down) with all of their heads, row r being
+// token r / G and head r % G.  K and V tiles are then read once for the G heads, and the
+// kernels are those of equal heads over G rows a token.  The rows past (M / G) * G of a
+// tile belong to nobody.
+//
+// Tensor maps: every sequence has maps of its own (built by ragged_plan_kernel), whose token
+// dimension ends where the sequence does, so that a tile that reaches past its end reads zeros,
+// and not what the next sequence or the rows behind the last one hold: a NaN there times a
+// probability of 0 would be NaN.
+#pragma once
+#include "common.cuh"
+
+namespace fa {
+
+struct RaggedSched {
+  const int* base;   // [B + 1] first work item of each sequence, longest sequence first; [B]: their number
+  const int4* seqs;  // [B] in the same order: first token, tokens, sequence, heads per launch-order group
+  int* counter;      // items claimed beyond the first of each CTA (zero at launch)
+  int B;
+};
+
+struct RaggedItem {
+  int start, len, seq;  // first token and tokens of the sequence, its index
+  int tile, head;       // rank of the tile (the heaviest first), kv head
+};
+
+constexpr int kRaggedRing = 2;        // items that a CTA has claimed ahead of its slowest role
+constexpr int kRaggedRingBytes = 32;  // a slot of the ring
+
+// The scheduling warp of a persistent CTA: claims work items (the first is the CTA's own
+// index, the rest come from the counter, so that idle SMs take the next ones, longest sequences first),
+// looks up their sequences and passes them to the other roles through a ring in shared memory.  Claimed
+// indices only grow, so the search goes on from the last sequence, 32 at a time.
+__device__ __forceinline__ void ragged_schedule(const RaggedSched& s, int tile_tokens, int parts, int heads,
+                                                volatile int* ring, uint32_t full0, uint32_t empty0,
+                                                const CtaAbort& ab, int where) {
+  const int lane = lane_id();
+  const int total = s.base[s.B];
+  int w = blockIdx.x, rank = 0;
+  for (int t = 0;; ++t) {
+    const int k = t % kRaggedRing;
+    if (!wait_warp(empty0 + 8 * k, ((t / kRaggedRing) & 1) ^ 1, ab, where)) return;
+    if (t > 0) {
+      if (lane == 0) w = (int)gridDim.x + atomicAdd(s.counter, 1);
+      w = __shfl_sync(0xffffffffu, w, 0);
+    }
+    int start = -1, len = 0, seq = 0, tile = 0, head = 0;
+    if (w < total) {
+      for (; rank < s.B; rank += 32) {
+        const int i = rank + lane;
+        const unsigned past = __ballot_sync(0xffffffffu, i < s.B && s.base[min(i + 1, s.B)] > w);
+        if (past) {
+          rank += __ffs(past) - 1;
+          break;
+        }
+      }
+      const int4 q = s.seqs[rank];
+      start = q.x, len = q.y, seq = q.z;
+      grouped_order(w - s.base[rank], ((len + tile_tokens - 1) / tile_tokens) * parts, heads, q.w, tile, head);
+    }
+    if (lane == 0) {
+      volatile int* slot = ring + k * (kRaggedRingBytes / 4);
+      slot[0] = start, slot[1] = len, slot[2] = seq, slot[3] = tile, slot[4] = head;
+      mbar_arrive(full0 + 8 * k);
+    }
+    __syncwarp();
+    if (start < 0) return;
+  }
+}
+
+// Who reads an item: a whole warp, or a single thread.
+struct ByWarp {
+  static constexpr bool value = false;
+};
+struct ByThread {
+  static constexpr bool value = true;
+};
+
+// The t-th item of this CTA, for a whole warp or (ONE) a single thread; false after the
+// last, or if the wait gave up.
+template <bool ONE>
+__device__ __forceinline__ bool ragged_item(int t, RaggedItem& I, const volatile int* ring, uint32_t full0,
+                                            uint32_t empty0, const CtaAbort& ab, int where) {
+  const int k = t % kRaggedRing;
+  const uint32_t parity = (t / kRaggedRing) & 1;
+  if constexpr (ONE) {
+    if (!wait_one(full0 + 8 * k, parity, ab, where)) return false;
+  } else {
+    if (!wait_warp(full0 + 8 * k, parity, ab, where)) return false;
+  }
+  const volatile int* slot = ring + k * (kRaggedRingBytes / 4);
+  I.start = slot[0], I.len = slot[1], I.seq = slot[2], I.tile = slot[3], I.head = slot[4];
+  if constexpr (ONE) {
+    mbar_arrive(empty0 + 8 * k);
+  } else {
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(empty0 + 8 * k);
+  }
+  return I.start >= 0;
+}
+
+}  // namespace fa

@@ -120,6 +120,11 @@ const char* fa_kernel_name(int kind) {
     case FA_KERNEL_KV4_LOAD: return "kv4_load";
     case FA_KERNEL_KV4_ATTN: return "kv4_attn";
     case FA_KERNEL_KV4_MERGE: return "kv4_merge";
+    case FA_KERNEL_PACKED_PLAN: return "packed_plan";
+    case FA_KERNEL_ROTATE: return "rotate";
+    case FA_KERNEL_ROTATE_BWD: return "rotate_bwd";
+    case FA_KERNEL_ROTATE_SUM: return "rotate_sum";
+    case FA_KERNEL_KV4_APPEND: return "kv4_append";
   }
   return "unknown";
 }

@@ -1,0 +1,110 @@
+"""Attention over packed sequences: torch-tensor wrappers over ``include/fa_packed.h``.
+
+Marshalling only, like ``serving``, whose checks it shares (``api`` offers these names too).
+Sequences of different lengths lie one behind the other in tensors [tokens, heads, d];
+``cu`` (int32 [sequences + 1]) says where each begins, and stays on the GPU.
+"""
+
+from __future__ import annotations
+
+import functools
+
+from . import binding as _b
+from .serving import (_BF16, _F32, _I32, _MOST, _U8, _On, _Tensor, _check, _check_sizes, _current_device,
+                      _current_stream, _dense, _empty, _rows)
+
+
+def _input(t, name, shape, index):
+    """``_rows`` of an operand that is read by tiles: strides of 0 or below are refused."""
+    st, sh = _rows(t, name, shape, index)
+    if (st <= 0 and t.shape[0] > 1) or (sh <= 0 and t.shape[1] > 1):
+        raise ValueError(f"{name}: the strides of tokens and heads must be positive")
+    return st, sh
+
+
+def _device_index(t, name):
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
+    return index
+
+
+def _sequences(cu, index):
+    if not (isinstance(cu, _Tensor) and cu.dtype is _I32 and cu.dim() == 1 and cu.get_device() == index
+            and cu.is_contiguous()):
+        _dense(cu, "cu", _I32, (None,), index)
+    if not 1 <= cu.shape[0] <= _MOST:
+        raise ValueError("cu must have an entry more than there are sequences")
+    return cu.shape[0] - 1
+
+
+def _workspace(workspace, need, index, device):
+    """(tensor that keeps it alive, address, bytes) of the caller's workspace or of a new one."""
+    if workspace is not None:
+        _dense(workspace, "workspace", _U8, (None,), index)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
+        return workspace, workspace.data_ptr(), workspace.numel()
+    if need == 0:
+        return None, None, 0
+    workspace = _empty(need, dtype=_U8, device=device)
+    return workspace, workspace.data_ptr(), need
+
+
+def packed_forward_workspace_bytes(sequences, tokens, heads, kv_heads, head_dim) -> int:
+    """What ``packed_attention_forward`` needs."""
+    _check_sizes(sequences, tokens, heads, kv_heads)
+    return _b.fa_packed_fwd_workspace_size(sequences, tokens, heads, kv_heads, head_dim)
+
+
+_forward_bytes = functools.lru_cache(maxsize=1024)(packed_forward_workspace_bytes)
+
+
+def _shapes(q, k, v, index):
+    qs = _input(q, "q", None, index)
+    ks = _input(k, "k", None, index)
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != d or (H % Hkv if Hkv else H):
+        raise ValueError(f"q is {tuple(q.shape)}, k {tuple(k.shape)}: tokens and channels must be equal, "
+                         "the heads of q a multiple of those of k")
+    vs = _input(v, "v", k.shape, index)
+    _check_sizes(T, H)
+    return T, H, Hkv, d, qs, ks, vs
+
+
+def packed_attention_forward(q, k, v, cu, scale: float | None = None, causal: bool = True, out=None, lse=None,
+                             workspace=None, stream=None):
+    """Attention of packed sequences: token cu[b] + i of q sees the keys of its own sequence b (up to
+    its own, if ``causal``).
+
+    q bf16 [T, heads, d], k and v bf16 [T, kv_heads, d] (token and head strides free, in
+    eights; heads a multiple of kv_heads, at most 32 times it); cu int32 [B + 1], not decreasing.  Returns
+    (o bf16 [T, heads, d], lse fp32 [T, heads]).  Rows of no sequence are left as they were (in
+    ``out`` and ``lse``, given or new), and nothing that the inputs hold there, or in another sequence,
+    reaches a result.  ``workspace``: a uint8 CUDA tensor of ``packed_forward_workspace_bytes``,
+    not shared with a concurrent call, or None."""
+    index = _device_index(q, "q")
+    if stream is not None or _current_device() != index:
+        with _On(index, stream):
+            return packed_attention_forward(q, k, v, cu, scale, causal, out, lse, workspace)
+    T, H, Hkv, d, (qt, qh), (kt, kh), (vt, vh) = _shapes(q, k, v, index)
+    B = _sequences(cu, index)
+    if out is None:
+        out = _empty(q.shape, dtype=_BF16, device=q.device)
+        ot, oh = H * d, d
+    else:
+        ot, oh = _rows(out, "out", q.shape, index, written=True)
+    if lse is None:
+        lse = _empty((T, H), dtype=_F32, device=q.device)
+    else:
+        _dense(lse, "lse", _F32, (T, H), index)
+    workspace, at, need = _workspace(workspace, _forward_bytes(B, T, H, Hkv, d), index, q.device)
+    st = _b.lib().fa_packed_fwd(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out.data_ptr(), ot, oh,
+                                lse.data_ptr(), cu.data_ptr(), B, T, H, Hkv, d, d ** -0.5 if scale is None else scale,
+                                bool(causal), at, need, _current_stream(index))
+    if st:
+        _check(st, "fa_packed_fwd")
+    return out, lse
