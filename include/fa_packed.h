@@ -46,6 +46,34 @@ fa_status fa_packed_fwd(const void* q, long long q_token, long long q_head, cons
 /* Bytes of workspace fa_packed_fwd needs; 0 for shapes without work and invalid ones. */
 size_t fa_packed_fwd_workspace_size(int B, int T, int H, int Hkv, int d);
 
+/*
+ * Backward.  With D_i = sum_c dO_ic o_ic, dP_ij = dO_i . v_j, P_ij = exp(s_ij - lse_i) and
+ * dS_ij = P_ij (dP_ij - D_i), sums over the queries and the heads of a kv head that see key j:
+ *   dv_j = sum P_ij dO_i,  dk_j = scale sum dS_ij q_i,  dq_i = scale sum_j dS_ij k_j
+ * o and lse as fa_packed_fwd wrote them for the same arguments.  P and dS are rounded to bf16
+ * where they enter the products, the gradients once.  Rows of no sequence (before cu[0] and
+ * behind cu[B]) get gradients of zero; with B = 0 every row is one.  A NaN or
+ * infinity in a row of one sequence never reaches another.  The gradients must not overlap
+ * one another or the inputs.
+ * variant: FA_BWD_5GEMM (d <= 128; dq is summed by reductions in fp32 whose order is not fixed),
+ * FA_BWD_7GEMM (the same arguments give the same bits) or FA_BWD_AUTO (the 5-GEMM form where it
+ * exists).  workspace: fa_packed_bwd_workspace_size bytes of the same shape and variant,
+ * 256-byte aligned, not shared with a concurrent call.
+ */
+fa_status fa_packed_bwd(const void* q, long long q_token, long long q_head, const void* k, long long k_token,
+                        long long k_head, const void* v, long long v_token, long long v_head, const void* o,
+                        long long o_token, long long o_head, const void* dO, long long do_token, long long do_head,
+                        const float* lse, void* dq, long long dq_token, long long dq_head, void* dk, long long dk_token,
+                        long long dk_head, void* dv, long long dv_token, long long dv_head, const int* cu, int B, int T,
+                        int H, int Hkv, int d, float scale, int causal, int variant, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace fa_packed_bwd needs (row statistics, for the 5-GEMM form an fp32 dq, tensor
+ * maps); 0 for shapes without work and invalid ones.
+ */
+size_t fa_packed_bwd_workspace_size(int B, int T, int H, int Hkv, int d, int variant);
+
 #ifdef __cplusplus
 }
 #endif

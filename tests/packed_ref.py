@@ -47,11 +47,16 @@ def attend(q, k, v, cu, scale, causal, do=None):
             dp = g @ z.T
             D = (g * o).sum(-1, keepdim=True)
             ds = p * (dp - D)
-            # What a relative error of the probabilities, and one of dP - D, can do to dS.
-            ads = p * ((dp - D).abs() + 2.0 ** -8 * (g.abs() * o.abs()).sum(-1, keepdim=True)
-                       + 2.0 ** -14 * (g.abs() @ z.abs().T))
+            # Bounds on the errors.  P is off by e of itself, sums over keys, queries and heads by `many`
+            # of their terms, D by what o is off by, dP by its fp32 sums; dS and P are rounded to bf16.
+            e = score_error(r["qk"][at, h], d)[:, None]
+            many = n * G * 2.0 ** -23
+            off_o = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2 * e) * (1 + 2.0 ** -7) * r["pv"][at, h]
+            off = (g.abs() * off_o).sum(-1, keepdim=True) + (d + 4) * 2.0 ** -23 * (g.abs() @ z.abs().T)
+            ads = p * ((2.0 ** -8 + 2 * e + many) * (dp - D).abs() + (1 + 2 * e) * off) * (1 + 2.0 ** -7)
+            ap = p * (2.0 ** -8 + 2 * e + many) * (1 + 2.0 ** -7)
             for name, value in (("dk", ds.T @ x * scale), ("dv", p.T @ g), ("edk", ads.T @ x.abs() * scale),
-                                ("edv", p.T @ g.abs())):
+                                ("edv", ap.T @ g.abs())):
                 t = r[name][at, h // G]
                 t.copy_(value if h % G == 0 else t + value)
             r["dq"][at, h] = ds @ y * scale
@@ -59,17 +64,17 @@ def attend(q, k, v, cu, scale, causal, do=None):
     return r
 
 
-def score_error(r, d):
+def score_error(qk, d):
     """Bound on the relative error of a probability: the scores are sums of d exact products in
     fp32 (2^-23 of the sum of magnitudes each, the tensor core may truncate), times one
     factor (two roundings of 2^-24), ex2.approx and the sums and logarithms 2^-17."""
-    return (d + 4) * 2.0 ** -23 * r["qk"] + 2.0 ** -17
+    return (d + 4) * 2.0 ** -23 * qk + 2.0 ** -17
 
 
 def check_forward(o, lse, r, d, what=""):
     """Probabilities are rounded to bf16 (2^-8 of the products' magnitudes), o to bf16 once."""
     mine = ~torch.isnan(r["lse"])
-    e = score_error(r, d)
+    e = score_error(r["qk"], d)
     full = mine & torch.isfinite(r["lse"])
     assert bool((o[mine & ~full] == 0).all()) and bool((lse[mine & ~full] == -math.inf).all()), what
     tol_l = e + 2.0 ** -22 * r["lse"].abs()
@@ -80,3 +85,14 @@ def check_forward(o, lse, r, d, what=""):
         if got.numel():
             far = float(((got - ref).abs() / tol).max())
             assert far <= 1, f"{what}: {name} off by {far:.2f} of its bound"
+
+
+def check_backward(grads, r, what=""):
+    """The bounds of ``attend`` and the one rounding of a gradient to bf16."""
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        mine = ~torch.isnan(r[name])
+        ref, off, got = r[name][mine], r["e" + name][mine], got[mine].double()
+        tol = 2.0 ** -8 * ref.abs() + (1 + 2.0 ** -8) * off + 1e-30
+        assert bool(torch.isfinite(got).all()), f"{what}: {name} is not finite"
+        far = float(((got - ref).abs() / tol).max()) if got.numel() else 0.0
+        assert far <= 1, f"{what}: {name} off by {far:.2f} of its bound"

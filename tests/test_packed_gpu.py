@@ -47,3 +47,34 @@ def test_forward_one_sequence(d, causal):
 def test_forward_groups_and_ragged_lengths(d, H, Hkv):
     forward([1, 37, 0, 128, 129, 5, 400, 64], H, Hkv, d, True, seed=d + H)
     forward([63, 0, 257, 2], H, Hkv, d, False, seed=d + H + 1, spread=3.0)
+
+
+def both(lengths, H, Hkv, d, causal, variants=(0, 7), scale=None, **kw):
+    """Forward and backward in each form against the reference."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, v, cu, host = make(lengths, H, Hkv, d, **kw)
+    g = torch.Generator(device="cuda:0").manual_seed(99)
+    do = torch.randn(q.shape, generator=g, device="cuda:0").to(torch.bfloat16)
+    what = f"{lengths} {H}/{Hkv} d={d} causal={causal}"
+    o, lse = api.packed_attention_forward(q, k, v, cu, scale, causal)
+    r = R.attend(q, k, v, host, d ** -0.5 if scale is None else scale, causal, do)
+    R.check_forward(o, lse, r, d, what)
+    for variant in variants:
+        grads = api.packed_attention_backward(q, k, v, o, do, lse, cu, scale, causal, variant=variant)
+        api.check_device_error()
+        R.check_backward(grads, r, f"{what} variant={variant}")
+
+
+@pytest.mark.parametrize("causal", (True, False))
+@pytest.mark.parametrize("d", DIMS)
+def test_backward_one_sequence(d, causal):
+    both([2], 1, 1, d, causal)
+    both([300], 4, 2, d, causal)
+
+
+@pytest.mark.parametrize("d", DIMS)
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (4, 4), (8, 2), (3, 1), (14, 2), (5, 1), (32, 1), (24, 2)])
+def test_backward_groups_and_ragged_lengths(d, H, Hkv):
+    both([1, 37, 0, 128, 129, 5, 400, 64], H, Hkv, d, True, seed=d + H)
+    both([63, 0, 257, 2], H, Hkv, d, False, seed=d + H + 1, spread=3.0)

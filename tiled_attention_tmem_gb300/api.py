@@ -137,7 +137,8 @@ _SERVING = ("KV4Cache", "page_grow", "page_slots", "kv4_store", "kv4_load", "kv4
 
 
 # Attention over packed sequences (``packed``), likewise.
-_PACKED = ("packed_attention_forward", "packed_forward_workspace_bytes")
+_PACKED = ("packed_attention_forward", "packed_attention_backward", "packed_forward_workspace_bytes",
+           "packed_backward_workspace_bytes")
 
 
 def __getattr__(name):

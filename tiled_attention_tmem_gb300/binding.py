@@ -74,6 +74,9 @@ SIGNATURES = {
     # include/fa_packed.h
     "fa_packed_fwd": (_I, [_VP, _LL, _LL] * 4 + [_VP, _VP, _I, _I, _I, _I, _I, _F, _I, _VP, _SZ, _VP]),
     "fa_packed_fwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "fa_packed_bwd": (_I, [_VP, _LL, _LL] * 5 + [_VP] + [_VP, _LL, _LL] * 3
+                      + [_VP, _I, _I, _I, _I, _I, _F, _I, _I, _VP, _SZ, _VP]),
+    "fa_packed_bwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
 }
 
 _lib = None
@@ -256,6 +259,19 @@ def fa_packed_fwd(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, o,
 
 def fa_packed_fwd_workspace_size(B, T, H, Hkv, d) -> int:
     return lib().fa_packed_fwd_workspace_size(B, T, H, Hkv, d)
+
+
+def fa_packed_bwd(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, o, o_token, o_head, dO, do_token, do_head,
+                  lse, dq, dq_token, dq_head, dk, dk_token, dk_head, dv, dv_token, dv_head, cu, B, T, H, Hkv, d, scale,
+                  causal, variant, workspace, workspace_bytes, stream) -> int:
+    return lib().fa_packed_bwd(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, o, o_token, o_head, dO,
+                               do_token, do_head, lse, dq, dq_token, dq_head, dk, dk_token, dk_head, dv, dv_token,
+                               dv_head, cu, B, T, H, Hkv, d, float(scale), int(causal), variant, workspace,
+                               workspace_bytes, stream)
+
+
+def fa_packed_bwd_workspace_size(B, T, H, Hkv, d, variant) -> int:
+    return lib().fa_packed_bwd_workspace_size(B, T, H, Hkv, d, variant)
 
 
 FA_KERNEL_ALL_KINDS = 19

@@ -13,33 +13,6 @@
 namespace fa {
 namespace {
 
-// dK/dV kernel configurations <d, query rows per step, with dQ, d split, query stages, separate P/dS>.
-// d = 128 5-GEMM: bulk dQ reductions from a shared-memory tile measured faster than per-element
-// or 16-byte reductions straight from registers, worth giving up one query stage.
-// d = 64 5-GEMM: 128 query columns per step over two compute warpgroups, each packing its P^T / dS^T
-// into its own S^T / dP^T columns.
-using KV5_64 = BwdKVCfg<64, 128, true, 1, 2, false>;
-using KV5_128 = BwdKVCfg<128, 64, true, 1, 3, true>;
-using KV7_64 = BwdKVCfg<64, 128, false, 1, 3, false>;
-using KV7_128 = BwdKVCfg<128, 64, false, 1, 4, true>;
-// d = 192: dV and dK for all 192 columns fit TMEM next to S and dP, so no d split.
-using KV7_192 = BwdKVCfg<192, 64, false, 1, 2, false>;
-// d = 256: V in TMEM, and the outputs split (a dV item and a dK item per key tile, each with one
-// 256-column accumulator).
-using KV7_256 = BwdKVCfg<256, 64, false, 2, 2, false, true, true>;
-// d = 384: dV and dK cut into three column parts of 128, one work item each (every item
-// recomputes S^T and dP^T), 32 queries per step, V in TMEM: 32 + 32 + 128 + 128 + 192 = 512
-// TMEM columns next to a 96 KiB K tile and two 48 KiB query stages.
-using KV7_384 = BwdKVCfg<384, 32, false, 3, 2, false, true, false>;
-// dQ kernel configurations <d, keys per tile, K/V ring slots>.
-using Q7_64 = BwdQCfg<64, 128, 6>;
-using Q7_128 = BwdQCfg<128, 128, 4>;
-using Q7_192 = BwdQCfg<192, 64, 7, true>;
-using Q7_256 = BwdQCfg<256, 64, 5, true>;
-// d = 384: two dQ column parts of 192 per query tile (one work item each), dO in TMEM,
-// 32-key tiles, four K/V slots of 24 KiB next to the 96 KiB Q tile.
-using Q7_384 = BwdQCfg<384, 32, 4, true, 2>;
-
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Workspace {

@@ -21,10 +21,18 @@
 //   dqacc[bh][Npad][d] (5-GEMM) with the 16-byte chunks of row i permuted by
 //                   chunk ^ (i % 8), which makes the staging writes of both
 //                   dQ orientations free of shared-memory bank conflicts.
+//
+// Packed sequences (RaggedKVParams, RaggedQParams): the same kernels over sequences of
+// different lengths, with the G query heads of a kv head as rows of a token (ragged.cuh), so
+// that dK and dV of a kv head sum over its heads where they are accumulated anyway.  Their row
+// arrays go by query tiles: [Hkv][tile slots][BM], where sequence b from token s on has the slots
+// from s / tokens + b on (tokens: of a tile, BM / G rounded down); rows of a tile past its
+// tokens or the sequence's end hold lse2 = -inf and dd = 0.
 #pragma once
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "ragged.cuh"
 
 namespace fa {
 
@@ -172,6 +180,7 @@ __global__ void __launch_bounds__(256) bwd_conv_kernel(const ConvParams p) {
 // dP^T), item h = 1 computes S^T, dP^T, dS^T and dK; each keeps one 256-column
 // accumulator in the same TMEM columns.
 struct BwdKVParams {
+  static constexpr bool kRagged = false;
   CUtensorMap q_map;   // box {64, BM, 1}
   CUtensorMap k_map;   // box {64, 128, 1}
   CUtensorMap v_map;   // box {64, 128, 1}
@@ -199,6 +208,39 @@ struct BwdKVParams {
   int qsplit;
   float* dkpart;
   float* dvpart;
+};
+
+struct RaggedKVParams {
+  static constexpr bool kRagged = true;
+  const CUtensorMap* maps;  // of sequence b from maps[b * nmaps] on: q, dO (box {64, G, tokens, 1}), k, v (box {64, 128, 1})
+  int nmaps;
+  RaggedSched sched;
+  const uint16_t* v;
+  const float* lse2;
+  const float* dd;
+  float* dqacc;
+  uint16_t* dk;
+  uint16_t* dv;
+  long long v_token, v_head, dk_token, dk_head, dv_token, dv_head;
+  int* err;
+  int slots;  // tile slots of a kv head
+  int Hkv, G;
+  int tokens;  // tokens of a query tile
+  int hd;
+  float scale_log2;
+  float scale;
+  int causal;
+};
+
+template <bool RAGGED>
+struct BwdKVItem {
+  int bh, h, part, k0, qt0, n;  // head, d part, query part, first key, first query tile, query tiles
+  int rot;                      // the item's first step takes query tile qt0 + rot (see qt_at)
+};
+template <>
+struct BwdKVItem<true> {
+  int bh, h, part, k0, qt0, n, rot;
+  int start, len, seq;  // the sequence's first token, its tokens, its index
 };
 
 // Sum of the query-range parts of dK and dV: dV = sum_s dvpart[s], dK = scale *
@@ -292,10 +334,12 @@ struct BwdKVCfg {
                        B_ITEMFULL = B_KVEMPTY + 1, B_ITEMEMPTY = B_ITEMFULL + 4, B_VREADY = B_ITEMEMPTY + 4,
                        NBAR = B_VREADY + 1;
   static constexpr int IQ = 4;  // claimed work items passed from the producer to the other roles
+  static_assert(kRaggedRing <= IQ, "packed sequences use the same barriers");
   // Roles that read each work item: the MMA issuing thread(s), the compute warps, the drain warps.
   static constexpr int ITEM_READERS = (EARLY ? 2 : 1) + 4 * NCW + (DQ ? 4 : 0);
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr uint32_t SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static constexpr uint32_t OFF_RING = OFF_MISC + 32;  // packed sequences: claimed items
+  static constexpr uint32_t SMEM_BYTES = OFF_RING + kRaggedRing * kRaggedRingBytes + 1024;
   // TMEM columns
   static constexpr int T_ST = 0, T_DPT = BM;
   static constexpr int T_PT = SEP ? 2 * BM : T_ST;
@@ -330,8 +374,11 @@ struct BwdKVCfg {
 // per SM: few heads), with the query-range split (p.qsplit >= 1) and each item's
 // query-tile walk starting at its own offset; the plain one keeps one part per
 // key tile and the natural order as constants and has no partial-sum epilogue.
-template <class C, bool FEW>
-__global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_constant__ BwdKVParams p) {
+// P: BwdKVParams, or RaggedKVParams (packed sequences; without the split).
+template <class C, bool FEW, class P = BwdKVParams>
+__global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_constant__ P p) {
+  constexpr bool RAGGED = P::kRagged;
+  static_assert(!(RAGGED && FEW), "packed sequences are not split");
   constexpr int D = C::D, BM = C::BM, QS = C::QS, DH = C::DH;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -353,7 +400,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
     mbar_init(BAR(C::B_KVEMPTY), C::EARLY ? 2 : 1);
     for (int k = 0; k < C::IQ; ++k) {
       mbar_init(BAR(C::B_ITEMFULL + k), 1);
-      mbar_init(BAR(C::B_ITEMEMPTY + k), C::ITEM_READERS);
+      mbar_init(BAR(C::B_ITEMEMPTY + k), C::ITEM_READERS + (RAGGED ? 1 : 0));  // (and the producer)
     }
     for (int s = 0; s < QS; ++s) {
       mbar_init(BAR(C::B_QDFULL + s), 1);
@@ -370,6 +417,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
     mbar_init(BAR(C::B_DONE), C::EARLY ? 2 : 1);
     mbar_init(BAR(C::B_VREADY), 4 * C::NCW);
     fence_mbar_init();
+  }
+  if constexpr (RAGGED) {
+    // Rows of the query stages that no load writes: zero, once.
+    const int rows = p.tokens * p.G;
+    if (rows < BM) {
+      for (int s = 0; s < QS; ++s)
+        for (int pn = 0; pn < 2 * C::PANELS; ++pn) {
+          uint8_t* panel = gbase + C::OFF_STAGE + s * C::STAGE_BYTES + pn * C::QD_PANEL;
+          for (int i = rows * 8 + threadIdx.x; i < BM * 8; i += C::THREADS)
+            *reinterpret_cast<uint4*>(panel + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      fence_proxy_async_smem();
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
@@ -392,9 +452,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
   // longest first) and passes each claimed index through a small shared-memory
   // ring to the other roles.  Every role walks the same items and counts the
   // same query tiles, so barrier phases run on across items.
-  const int n_kt = (p.N + C::BN - 1) / C::BN;
-  const int n_qt = (p.N + BM - 1) / BM;
-  volatile int* item_ring = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 16);
+  int n_kt = 0, n_qt = 0;
+  if constexpr (!RAGGED) {
+    n_kt = (p.N + C::BN - 1) / C::BN;
+    n_qt = (p.N + BM - 1) / BM;
+  }
+  volatile int* item_ring = reinterpret_cast<volatile int*>(gbase + (RAGGED ? C::OFF_RING : C::OFF_MISC + 16));
   // Item claimed t-th by this CTA (>= p.items once the counter ran out), or -1
   // if the wait gave up.  Single-thread readers.
   auto item_one = [&](int t) -> int {
@@ -413,16 +476,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
     if (lane_id() == 0) mbar_arrive(BAR(C::B_ITEMEMPTY + k));
     return w;
   };
-  struct Item {
-    int bh, h, part, k0, qt0, n;  // head, d part, query part, first key, first query tile, query tiles
-    int rot;                      // the item's first step takes query tile qt0 + rot (see qt_at)
-  };
+  using Item = BwdKVItem<RAGGED>;
   // Item w: key tile, query part and d part from the launch order; the key tile's
   // query tiles (from the diagonal under the causal mask) are cut into p.qsplit
   // contiguous parts (some possibly empty when there are fewer tiles than parts).
-  const int qsplit = FEW ? p.qsplit : 1;
+  int qsplit = 1;
+  if constexpr (FEW) qsplit = p.qsplit;
   auto coords = [&](int w) {
-    Item I;
+    Item I = {};
+    if constexpr (!RAGGED) {
     int tile;
     grouped_order(w, n_kt * C::DSPLIT * qsplit, p.BH, p.group, tile, I.bh);
     I.h = tile % C::DSPLIT;
@@ -447,7 +509,45 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
     // with one to eight heads, -2.5 % with 64 heads of 2048 rows, where concurrent
     // items belong to different heads anyway).
     I.rot = (FEW && I.n > 0) ? (int)((long long)I.n * (I.k0 / C::BN) / n_kt) : 0;
+    }
     return I;
+  };
+  // The t-th item of this CTA for a whole warp (or, packed, for one thread); false after the last.
+  auto item_at = [&](int t, Item& I, auto one) -> bool {
+    if constexpr (RAGGED) {
+      RaggedItem x;
+      if (!ragged_item<decltype(one)::value>(t, x, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY), ab,
+                                             (kKBwdKV << 8) | 18))
+        return false;
+      I.start = x.start, I.len = x.len, I.seq = x.seq, I.bh = x.head;
+      I.h = x.tile % C::DSPLIT;
+      I.k0 = x.tile / C::DSPLIT * C::BN;
+      I.qt0 = p.causal ? I.k0 / p.tokens : 0;
+      I.n = (x.len + p.tokens - 1) / p.tokens - I.qt0;
+      I.part = I.rot = 0;
+      return true;
+    } else {
+      const int w = item_warp(t);
+      if (w < 0 || w >= p.items) return false;
+      I = coords(w);
+      return true;
+    }
+  };
+  // Row of lse2, dd and dqacc where query tile qt of item I begins.
+  auto tile_row = [&](const Item& I, int qt) -> size_t {
+    if constexpr (RAGGED) return ((size_t)I.bh * p.slots + I.start / p.tokens + I.seq + qt) * BM;
+    else return (size_t)I.bh * p.Npad + qt * BM;
+  };
+  // Keys of the item's head, and where key k0's row of an output begins and the next one does.
+  auto keys_of = [&](const Item& I) -> int {
+    if constexpr (RAGGED) return I.len;
+    else return p.N;
+  };
+  auto out_row = [&](const Item& I, int which, int key) -> uint16_t* {
+    if constexpr (RAGGED)
+      return which == 0 ? p.dv + (I.start + key) * p.dv_token + I.bh * p.dv_head
+                        : p.dk + (I.start + key) * p.dk_token + I.bh * p.dk_head;
+    else return (which == 0 ? p.dv : p.dk) + ((size_t)I.bh * p.N + key) * p.hd;
   };
   // Query tile of step i of item I.
   auto qt_at = [](const Item& I, int i) {
@@ -473,17 +573,52 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
       // issued before its K/V tile, which has to wait until the previous
       // item's last MMAs have read K and V.
       if (lane == 0) {
-        tma_prefetch_desc(&p.q_map);
-        tma_prefetch_desc(&p.k_map);
-        tma_prefetch_desc(&p.v_map);
-        tma_prefetch_desc(&p.do_map);
         int it = 0, nkv = 0;
         bool ok = true;
+        // The tensor maps of an item (packed: of its sequence).
+        struct Maps {
+          const CUtensorMap *q, *dO, *k, *v;
+        };
+        auto maps_of = [&](const Item& I) {
+          if constexpr (RAGGED) {
+            const CUtensorMap* m = p.maps + (size_t)I.seq * p.nmaps;
+            return Maps{m, m + 1, m + 2, m + 3};
+          } else {
+            return Maps{&p.q_map, &p.do_map, &p.k_map, &p.v_map};
+          }
+        };
+        int seq = -1;
+        auto ready_maps = [&](const Item& I) {
+          if constexpr (RAGGED) {
+            if (I.seq == seq) return;
+            seq = I.seq;
+            const Maps m = maps_of(I);
+            tensormap_acquire(m.q);
+            tensormap_acquire(m.dO);
+            tensormap_acquire(m.k);
+            tensormap_acquire(m.v);
+          }
+        };
+        if constexpr (!RAGGED) {
+          tma_prefetch_desc(&p.q_map);
+          tma_prefetch_desc(&p.k_map);
+          tma_prefetch_desc(&p.v_map);
+          tma_prefetch_desc(&p.do_map);
+        }
         auto prefetch_qd = [&](const Item& I, int i) {
-          const int prow = qt_at(I, i) * BM;
-          for (int pn = 0; pn < C::PANELS; ++pn) {
-            tma_prefetch_l2_3d(&p.q_map, 64 * pn, prow, I.bh);
-            tma_prefetch_l2_3d(&p.do_map, 64 * pn, prow, I.bh);
+          const Maps m = maps_of(I);
+          if constexpr (RAGGED) {
+            const int prow = I.start + qt_at(I, i) * p.tokens;
+            for (int pn = 0; pn < C::PANELS; ++pn) {
+              tma_prefetch_l2_4d(m.q, 64 * pn, 0, prow, I.bh);
+              tma_prefetch_l2_4d(m.dO, 64 * pn, 0, prow, I.bh);
+            }
+          } else {
+            const int prow = qt_at(I, i) * BM;
+            for (int pn = 0; pn < C::PANELS; ++pn) {
+              tma_prefetch_l2_3d(m.q, 64 * pn, prow, I.bh);
+              tma_prefetch_l2_3d(m.dO, 64 * pn, prow, I.bh);
+            }
           }
         };
         int published = 0;
@@ -496,6 +631,75 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           ++published;
           return true;
         };
+        // All loads of item I, the next item being J (if there is one).
+        auto load_item = [&](const Item& I, const Item& J, bool has_next) {
+          const Maps m = maps_of(I), mj = maps_of(J);
+          int key0 = 0, next0 = 0;  // first token of each sequence
+          if constexpr (RAGGED) key0 = I.start, next0 = J.start;
+          auto issue_stage = [&](int i) -> bool {
+            const int s = it % QS;
+            if (!wait_one(BAR(C::B_QDEMPTY + s), ((it / QS) & 1) ^ 1, ab, (kKBwdKV << 8) | 1)) return false;
+            const int qt = qt_at(I, i);
+            if constexpr (RAGGED) {
+              mbar_expect_tx(BAR(C::B_QDFULL + s), 2 * C::PANELS * p.tokens * p.G * 128 + 2 * BM * 4);
+              const int qrow = I.start + qt * p.tokens;
+              for (int pn = 0; pn < C::PANELS; ++pn) {
+                tma_load_4d(stage_q(s) + pn * C::QD_PANEL, m.q, BAR(C::B_QDFULL + s), 64 * pn, 0, qrow, I.bh);
+                tma_load_4d(stage_do(s) + pn * C::QD_PANEL, m.dO, BAR(C::B_QDFULL + s), 64 * pn, 0, qrow, I.bh);
+              }
+            } else {
+              mbar_expect_tx(BAR(C::B_QDFULL + s), C::STAGE_TX);
+              const int qrow = qt * BM;
+              for (int pn = 0; pn < C::PANELS; ++pn) {
+                tma_load_3d(stage_q(s) + pn * C::QD_PANEL, m.q, BAR(C::B_QDFULL + s), 64 * pn, qrow, I.bh);
+                tma_load_3d(stage_do(s) + pn * C::QD_PANEL, m.dO, BAR(C::B_QDFULL + s), 64 * pn, qrow, I.bh);
+              }
+            }
+            bulk_load(stage_lse(s), p.lse2 + tile_row(I, qt), BM * 4, BAR(C::B_QDFULL + s));
+            bulk_load(stage_dd(s), p.dd + tile_row(I, qt), BM * 4, BAR(C::B_QDFULL + s));
+            ++it;
+            // Stage loads can only start once a slot frees up (a few tiles ahead of
+            // use); pull the tiles further ahead, into the next item, into L2.
+            const int ahead = i + C::PREFETCH;
+            if (ahead < I.n) prefetch_qd(I, ahead);
+            else if (has_next && ahead - I.n < J.n) prefetch_qd(J, ahead - I.n);
+            return true;
+          };
+          const int pre = min(QS - 1, I.n);
+          int i = 0;
+          for (; ok && i < pre; ++i) ok = issue_stage(i);
+          if (!ok) return;
+          if (nkv > 0 && !wait_one(BAR(C::B_KVEMPTY), (nkv - 1) & 1, ab, (kKBwdKV << 8) | 15)) {
+            ok = false;
+            return;
+          }
+          mbar_expect_tx(BAR(C::B_KV), (C::VT ? 1 : 2) * C::KV_TILE);
+          for (int pn = 0; pn < C::PANELS; ++pn) {
+            tma_load_3d(sbase + C::OFF_K + pn * C::KV_PANEL, m.k, BAR(C::B_KV), 64 * pn, key0 + I.k0, I.bh);
+            if (!C::VT)
+              tma_load_3d(sbase + C::OFF_V + pn * C::KV_PANEL, m.v, BAR(C::B_KV), 64 * pn, key0 + I.k0, I.bh);
+          }
+          ++nkv;
+          if (has_next)
+            for (int pn = 0; pn < C::PANELS; ++pn) {
+              tma_prefetch_l2_3d(mj.k, 64 * pn, next0 + J.k0, J.bh);
+              tma_prefetch_l2_3d(mj.v, 64 * pn, next0 + J.k0, J.bh);
+            }
+          for (; ok && i < I.n; ++i) ok = issue_stage(i);
+        };
+        if constexpr (RAGGED) {
+          Item I, J;
+          bool have = item_at(0, I, ByThread{});
+          if (have) ready_maps(I);
+          for (int t = 1; have && ok; ++t) {
+            const bool has_next = item_at(t, J, ByThread{});
+            if (has_next) ready_maps(J);
+            else J = I;
+            load_item(I, J, has_next);
+            I = J;
+            have = has_next;
+          }
+        } else {
         // 5-GEMM: the first item of CTA c is item c (the grid never exceeds the
         // items) and the counter hands out the rest, so no CTA starts behind a
         // contended atomic (measured -1 % on 64 heads of 2048 rows, -4 % on one
@@ -512,43 +716,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           if (I.n <= 0) continue;
           const bool has_next = wn < p.items;
           const Item J = has_next ? coords(wn) : I;
-          auto issue_stage = [&](int i) -> bool {
-            const int s = it % QS;
-            if (!wait_one(BAR(C::B_QDEMPTY + s), ((it / QS) & 1) ^ 1, ab, (kKBwdKV << 8) | 1)) return false;
-            const int qrow = qt_at(I, i) * BM;
-            mbar_expect_tx(BAR(C::B_QDFULL + s), C::STAGE_TX);
-            for (int pn = 0; pn < C::PANELS; ++pn) {
-              tma_load_3d(stage_q(s) + pn * C::QD_PANEL, &p.q_map, BAR(C::B_QDFULL + s), 64 * pn, qrow, I.bh);
-              tma_load_3d(stage_do(s) + pn * C::QD_PANEL, &p.do_map, BAR(C::B_QDFULL + s), 64 * pn, qrow, I.bh);
-            }
-            bulk_load(stage_lse(s), p.lse2 + (size_t)I.bh * p.Npad + qrow, BM * 4, BAR(C::B_QDFULL + s));
-            bulk_load(stage_dd(s), p.dd + (size_t)I.bh * p.Npad + qrow, BM * 4, BAR(C::B_QDFULL + s));
-            ++it;
-            // Stage loads can only start once a slot frees up (a few tiles ahead of
-            // use); pull the tiles further ahead, into the next item, into L2.
-            const int ahead = i + C::PREFETCH;
-            if (ahead < I.n) prefetch_qd(I, ahead);
-            else if (has_next && ahead - I.n < J.n) prefetch_qd(J, ahead - I.n);
-            return true;
-          };
-          const int pre = min(QS - 1, I.n);
-          int i = 0;
-          for (; ok && i < pre; ++i) ok = issue_stage(i);
-          if (!ok) break;
-          if (nkv > 0 && !wait_one(BAR(C::B_KVEMPTY), (nkv - 1) & 1, ab, (kKBwdKV << 8) | 15)) break;
-          mbar_expect_tx(BAR(C::B_KV), (C::VT ? 1 : 2) * C::KV_TILE);
-          for (int pn = 0; pn < C::PANELS; ++pn) {
-            tma_load_3d(sbase + C::OFF_K + pn * C::KV_PANEL, &p.k_map, BAR(C::B_KV), 64 * pn, I.k0, I.bh);
-            if (!C::VT)
-              tma_load_3d(sbase + C::OFF_V + pn * C::KV_PANEL, &p.v_map, BAR(C::B_KV), 64 * pn, I.k0, I.bh);
-          }
-          ++nkv;
-          if (has_next)
-            for (int pn = 0; pn < C::PANELS; ++pn) {
-              tma_prefetch_l2_3d(&p.k_map, 64 * pn, J.k0, J.bh);
-              tma_prefetch_l2_3d(&p.v_map, 64 * pn, J.k0, J.bh);
-            }
-          for (; ok && i < I.n; ++i) ok = issue_stage(i);
+          load_item(I, J, has_next);
+        }
         }
         if (nkv > 0) wait_drain_bwd(BAR(C::B_KV), (nkv - 1) & 1);
         for (int j = max(0, it - QS); j < it; ++j) wait_drain_bwd(BAR(C::B_QDFULL + j % QS), (j / QS) & 1);
@@ -653,9 +822,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
         if (C::EARLY && warp == 1) {
           // S^T(g), dP^T(g) as soon as the compute warps hold S^T(g-1), dP^T(g-1) in registers.
           for (int r = 0; ok; ++r) {
-            const int w = item_warp(r);
-            if (w < 0 || w >= p.items) break;
-            const int n = coords(w).n;
+            Item I;
+            if (!item_at(r, I, ByWarp{})) break;
+            const int n = I.n;
             if (n <= 0) continue;
             if (!wait_warp(BAR(C::B_KV), nkv & 1, ab, (kKBwdKV << 8) | 2)) break;
             for (int i = 0; i < n; ++i, ++g) {
@@ -675,9 +844,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           }
         } else if (C::EARLY) {
           for (int r = 0; ok; ++r) {
-            const int w = item_warp(r);
-            if (w < 0 || w >= p.items) break;
-            const Item I = coords(w);
+            Item I;
+            if (!item_at(r, I, ByWarp{})) break;
             if (I.n <= 0) continue;
             for (int i = 0; i < I.n; ++i, ++g) {
               const int s = g % QS;
@@ -698,9 +866,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
         } else {
           int nv = 0;  // items whose V the compute warps wrote into TMEM (VT)
           for (int r = 0; ok; ++r) {
-            const int w = item_warp(r);
-            if (w < 0 || w >= p.items) break;
-            const Item I = coords(w);
+            Item I;
+            if (!item_at(r, I, ByWarp{})) break;
             if (I.n <= 0) continue;
             if (!wait_warp(BAR(C::B_KV), nkv & 1, ab, (kKBwdKV << 8) | 2) ||
                 !wait_warp(BAR(C::B_QDFULL + g % QS), (g / QS) & 1, ab, (kKBwdKV << 8) | 3))
@@ -755,6 +922,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
         wait_drain_bwd(BAR(C::B_DONE), 0);
       }
       __syncwarp();
+    } else if (RAGGED && warp == 3) {
+      // --------------------------------------------------------- scheduling
+      if constexpr (RAGGED)
+        ragged_schedule(p.sched, C::BN, C::DSPLIT, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY), ab,
+                        (kKBwdKV << 8) | 20);
     }
     } else if (warp < C::DRAIN_W0) {
       // ---------------------------------------------- P^T / dS^T (thread = key row)
@@ -769,16 +941,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
       bool ok = true;
       int g = 0;
       for (int rr = 0; ok; ++rr) {
-        const int w = item_warp(rr);
-        if (w < 0 || w >= p.items) break;
-        const Item I = coords(w);
+        Item I;
+        if (!item_at(rr, I, ByWarp{})) break;
         const int kj = I.k0 + r;
-        const bool key_ok = kj < p.N;
+        const bool key_ok = kj < keys_of(I);
+        if constexpr (!RAGGED) {
         if (I.n <= 0) {
           // No query of this item can see the key tile: zero gradients (zero partial
           // sums under the query-range split).
           const int c_off = C::OS ? 0 : I.h * DH;
-          if (FEW && p.qsplit > 1) {
+          if (FEW && qsplit > 1) {
             if (key_ok && cw == 0) {
               const size_t off = (((size_t)I.part * p.BH + I.bh) * p.Npad + kj) * D + c_off;
               for (int c = 0; c < DH; c += 4) {
@@ -799,12 +971,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
             }
           continue;
         }
+        }
         if (C::VT && (!C::OS || I.h == 1)) {
           // This item's V row kj as packed bf16 pairs into TMEM lane r: the A
           // operand of dP^T = V dO^T.  The previous item's dP^T MMAs, the last
           // readers of these columns, completed before its last S^T / dP^T
           // barrier, which these warps have waited on.
-          const uint16_t* vrow = p.v + ((size_t)I.bh * p.N + (key_ok ? kj : 0)) * p.hd;
+          const uint16_t* vrow;
+          if constexpr (RAGGED) vrow = p.v + (I.start + (key_ok ? kj : 0)) * p.v_token + I.bh * p.v_head;
+          else vrow = p.v + ((size_t)I.bh * p.N + (key_ok ? kj : 0)) * p.hd;
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 64) {
             uint32_t vw[32];
@@ -826,7 +1001,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
         }
         for (int i = 0; i < I.n; ++i, ++g) {
           const int s = g % QS;
-          const int q0 = qt_at(I, i) * BM;
           if (!wait_warp(BAR(C::B_SDP), g & 1, ab, (kKBwdKV << 8) | 7) ||
               !wait_warp(BAR(C::B_QDFULL + s), (g / QS) & 1, ab, (kKBwdKV << 8) | 8)) {
             ok = false;
@@ -835,7 +1009,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           tc_fence_after();
           const float* L = reinterpret_cast<const float*>(gbase + (stage_lse(s) - sbase));
           const float* Dd = reinterpret_cast<const float*>(gbase + (stage_dd(s) - sbase));
-          const int lim = p.causal ? kj - q0 : -1;  // columns c < lim are masked (query < key)
+          // Columns c < lim are masked (query < key; packed: G columns a token).
+          int lim;
+          if constexpr (RAGGED) lim = p.causal ? (kj - qt_at(I, i) * p.tokens) * p.G : -1;
+          else lim = p.causal ? kj - qt_at(I, i) * BM : -1;
           // Writes one 32-column chunk of P^T and dS^T (packed bf16) to TMEM and,
           // for the 5-GEMM variant, dS^T row r into the [128 keys][BM queries]
           // swizzled shared-memory tile read by the dQ MMA.
@@ -950,7 +1127,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
         // item's first query tile, whose dV / dK MMAs overwrite the accumulators.
         if (!wait_warp(BAR(C::B_MMA), (g - 1) & 1, ab, (kKBwdKV << 8) | 10)) break;
         tc_fence_after();
-        if (FEW && p.qsplit > 1) {
+        if constexpr (FEW) {
+        if (qsplit > 1) {
           // Query-range split: this part's fp32 sums (dK without the scale), one row per thread.
 #pragma unroll
           for (int which = 0; which < 2; ++which) {
@@ -977,12 +1155,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           tc_fence_before();
           continue;
         }
+        }
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
           if (C::NCW == 2 && which != cw) continue;  // two warpgroups: one stores dV, the other dK
           if (C::OS && which != I.h) continue;       // output split: this item's one accumulator
           const int c_off = C::OS ? 0 : I.h * DH;    // first column of this item's d part
-          uint16_t* dst = (which == 0 ? p.dv : p.dk) + (size_t)I.bh * p.N * p.hd + c_off;
           const int cols = min(DH, p.hd - c_off);  // stored columns of this d part
           const float mul = which == 0 ? 1.f : p.scale;
           const uint32_t tacc = trow + (which == 0 ? C::T_DV : C::T_DK);
@@ -1020,13 +1198,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
                 const int rr = quad * 32 + j * (32 / R) + lane / R;
                 const int u = lane % R;
                 const uint4 val = *ds_chunk(rr, u);
-                if (I.k0 + rr < p.N && c0 + 8 * u < cols)
-                  *reinterpret_cast<uint4*>(dst + (size_t)(I.k0 + rr) * p.hd + c0 + 8 * u) = val;
+                if (I.k0 + rr < keys_of(I) && c0 + 8 * u < cols)
+                  *reinterpret_cast<uint4*>(out_row(I, which, I.k0 + rr) + c_off + c0 + 8 * u) = val;
               }
               __syncwarp();
             }
           } else {
-            uint16_t* drow = dst + (size_t)(key_ok ? kj : 0) * p.hd;
+            uint16_t* drow = out_row(I, which, key_ok ? kj : 0) + c_off;
 #pragma unroll
             for (int c0 = 0; c0 < DH; c0 += 32) {
               uint32_t rv[32];
@@ -1060,9 +1238,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
       bool ok = true;
       int g = 0;
       for (int rr = 0; ok; ++rr) {
-        const int w = item_warp(rr);
-        if (w < 0 || w >= p.items) break;
-        const Item I = coords(w);
+        Item I;
+        if (!item_at(rr, I, ByWarp{})) break;
         for (int i = 0; i < I.n; ++i, ++g) {
           if (!wait_warp(BAR(C::B_DQFULL), g & 1, ab, (kKBwdKV << 8) | 11)) {
             ok = false;
@@ -1078,7 +1255,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(C::B_DQFREE));
-          const int q0 = qt_at(I, i) * BM;
           // The previous bulk reduction must have finished reading the staging tile.
           if (leader) {
             bulk_wait_read0();
@@ -1107,7 +1283,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           if (leader) {
             lok = wait_one(BAR(C::B_STGFULL), g & 1, ab, (kKBwdKV << 8) | 13);
             if (lok) {
-              bulk_reduce_add_f32(p.dqacc + ((size_t)I.bh * p.Npad + q0) * D, smem_u32(stg), C::STG_BYTES);
+              bulk_reduce_add_f32(p.dqacc + tile_row(I, qt_at(I, i)) * D, smem_u32(stg), C::STG_BYTES);
               bulk_commit();
             }
           }
@@ -1137,6 +1313,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
 //   written back as bf16 over dP's columns, then dQ += dS K (A = dS from TMEM,
 //   B = K MN-major).  dQ * scale is written once at the end.
 struct BwdQParams {
+  static constexpr bool kRagged = false;
   CUtensorMap q_map;   // box {64, 128, 1}
   CUtensorMap do_map;  // box {64, 128, 1}
   CUtensorMap k_map;   // box {64, BN, 1}
@@ -1161,6 +1338,36 @@ struct BwdQParams {
   // parts.
   int ksplit;
   float* dqpart;
+};
+
+struct RaggedQParams {
+  static constexpr bool kRagged = true;
+  const CUtensorMap* maps;  // of sequence b from maps[b * nmaps] on: q, dO (box {64, G, tokens, 1}), k, v (box {64, BN, 1})
+  int nmaps;
+  RaggedSched sched;
+  const uint16_t* dO;
+  const float* lse2;
+  const float* dd;
+  uint16_t* dq;
+  long long do_token, do_head, dq_token, dq_head;
+  int* err;
+  int slots, pre_tokens, pre_rows;  // the row arrays' tile slots of a kv head, tokens and rows of a slot
+  int Hkv, G;
+  int tokens;  // tokens of this kernel's 128-row tile
+  int hd;
+  float scale_log2;
+  float scale;
+  int causal;
+};
+
+template <bool RAGGED>
+struct BwdQItem {
+  int q0, bh, n, h, j0, part;  // first query row, head, key tiles, dQ column part, first key tile, key part
+};
+template <>
+struct BwdQItem<true> {
+  int q0, bh, n, h, j0, part;  // (q0: first token of the tile in its sequence)
+  int start, len, seq;
 };
 
 // Sum of the key-range parts of dQ: dQ = scale * sum_s dqpart[s] (parts in fixed
@@ -1225,8 +1432,10 @@ struct BwdQCfg {
                        B_ITEMEMPTY = B_ITEMFULL + IQ, B_SCONS = B_ITEMEMPTY + IQ, B_DOREADY = B_SCONS + 1,
                        NBAR = B_DOREADY + 1;
   static constexpr int ITEM_READERS = 1 + 4;  // the MMA warp and the four compute warps
+  static_assert(kRaggedRing <= IQ, "packed sequences use the same barriers");
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr uint32_t SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static constexpr uint32_t OFF_RING = OFF_MISC + 32;  // packed sequences: claimed items
+  static constexpr uint32_t SMEM_BYTES = OFF_RING + kRaggedRing * kRaggedRingBytes + 1024;
   static constexpr int T_S = 0, T_DP = BN, T_DQ = 2 * BN;
   static constexpr int T_DO = 2 * BN + DQW;  // DT: dO as packed bf16 pairs, D / 2 columns
   static constexpr int TMEM_USED = 2 * BN + DQW + (DT ? D / 2 : 0);
@@ -1239,8 +1448,11 @@ struct BwdQCfg {
 
 // FEW: the key-split instantiation (p.ksplit >= 1); the plain one keeps one key
 // part per query tile as a constant.
-template <class C, bool FEW>
-__global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_constant__ BwdQParams p) {
+// P: BwdQParams, or RaggedQParams (packed sequences; without the split).
+template <class C, bool FEW, class P = BwdQParams>
+__global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_constant__ P p) {
+  constexpr bool RAGGED = P::kRagged;
+  static_assert(!(RAGGED && FEW), "packed sequences are not split");
   constexpr int D = C::D, BN = C::BN, S = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -1249,7 +1461,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
   const uint32_t bar0 = sbase + C::OFF_BAR;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 4);
-  volatile int* item_ring = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 16);
+  volatile int* item_ring = reinterpret_cast<volatile int*>(gbase + (RAGGED ? C::OFF_RING : C::OFF_MISC + 16));
   const int warp = warp_id();
   const int lane = lane_id();
   auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
@@ -1268,7 +1480,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
     mbar_init(BAR(C::B_DONE), 1);
     for (int k = 0; k < C::IQ; ++k) {
       mbar_init(BAR(C::B_ITEMFULL + k), 1);
-      mbar_init(BAR(C::B_ITEMEMPTY + k), C::ITEM_READERS);
+      mbar_init(BAR(C::B_ITEMEMPTY + k), C::ITEM_READERS + (RAGGED ? 1 : 0));  // (and the producer)
     }
     mbar_init(BAR(C::B_SCONS), 4);
     mbar_init(BAR(C::B_DOREADY), 4);
@@ -1293,13 +1505,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
   // producer claims items from a global counter one item ahead and passes them
   // to the other roles through a shared-memory ring; barrier phases run on
   // across items.
-  const int n_qt = (p.N + 127) / 128;
-  const int ksplit = FEW ? p.ksplit : 1;
-  struct Item {
-    int q0, bh, n, h, j0, part;  // first query row, head, key tiles, dQ column part, first key tile, key part
-  };
+  int n_qt = 0, ksplit = 1;
+  if constexpr (!RAGGED) n_qt = (p.N + 127) / 128;
+  if constexpr (FEW) ksplit = p.ksplit;
+  using Item = BwdQItem<RAGGED>;
   auto coords = [&](int w) {
-    Item I;
+    Item I = {};
+    if constexpr (!RAGGED) {
     int t;
     grouped_order(w, n_qt * ksplit * C::DQS, p.BH, p.group, t, I.bh);
     I.h = t % C::DQS;
@@ -1317,6 +1529,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
       I.j0 = 0;
       I.n = nk;
     }
+    }
     return I;
   };
   auto item_warp = [&](int t) -> int {
@@ -1327,16 +1540,51 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
     if (lane == 0) mbar_arrive(BAR(C::B_ITEMEMPTY + k));
     return w;
   };
+  // The t-th item of this CTA for a whole warp (or, packed, for one thread); false after the last.
+  auto item_at = [&](int t, Item& I, auto one) -> bool {
+    if constexpr (RAGGED) {
+      RaggedItem x;
+      if (!ragged_item<decltype(one)::value>(t, x, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY), ab,
+                                             (kKBwdQ << 8) | 8))
+        return false;
+      I.start = x.start, I.len = x.len, I.seq = x.seq, I.bh = x.head;
+      I.h = x.tile % C::DQS;
+      const int tiles = (x.len + p.tokens - 1) / p.tokens, rank = x.tile / C::DQS;
+      I.q0 = (p.causal ? tiles - 1 - rank : rank) * p.tokens;
+      I.j0 = I.part = 0;
+      I.n = (p.causal ? min(I.q0 + p.tokens, x.len) - 1 : x.len - 1) / BN + 1;
+      return true;
+    } else {
+      const int w = item_warp(t);
+      if (w < 0 || w >= p.items) return false;
+      I = coords(w);
+      return true;
+    }
+  };
 
   if (!skip) {
     if (warp == 0) {
       if (lane == 0) {
-        tma_prefetch_desc(&p.q_map);
-        tma_prefetch_desc(&p.do_map);
-        tma_prefetch_desc(&p.k_map);
-        tma_prefetch_desc(&p.v_map);
         int it = 0, nitems = 0, published = 0;
         bool ok = true;
+        struct Maps {
+          const CUtensorMap *q, *dO, *k, *v;
+        };
+        auto maps_of = [&](const Item& I) {
+          if constexpr (RAGGED) {
+            const CUtensorMap* m = p.maps + (size_t)I.seq * p.nmaps;
+            return Maps{m, m + 1, m + 2, m + 3};
+          } else {
+            return Maps{&p.q_map, &p.do_map, &p.k_map, &p.v_map};
+          }
+        };
+        int seq = -1;
+        if constexpr (!RAGGED) {
+          tma_prefetch_desc(&p.q_map);
+          tma_prefetch_desc(&p.do_map);
+          tma_prefetch_desc(&p.k_map);
+          tma_prefetch_desc(&p.v_map);
+        }
         auto publish = [&](int w) -> bool {
           const int k = published % C::IQ;
           if (!wait_one(BAR(C::B_ITEMEMPTY + k), ((published / C::IQ) & 1) ^ 1, ab, (kKBwdQ << 8) | 9))
@@ -1346,32 +1594,34 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
           ++published;
           return true;
         };
-        int wn = atomicAdd(p.sched + 1, 1);
-        ok = publish(wn);
-        while (ok && wn < p.items) {
-          const Item I = coords(wn);
-          wn = atomicAdd(p.sched + 1, 1);
-          if (!publish(wn)) break;
-          if (FEW && I.n == 0) continue;  // an empty key part: nothing to load or compute
+        // All loads of item I; `near_end` runs a few key steps before its end.
+        auto load_item = [&](const Item& I, auto near_end) {
+          const Maps m = maps_of(I);
           // The previous item's last S / dP MMAs must be done reading Q and dO.
-          if (nitems > 0 && !wait_one(BAR(C::B_QEMPTY), (nitems - 1) & 1, ab, (kKBwdQ << 8) | 10)) break;
-          mbar_expect_tx(BAR(C::B_QFULL), (C::DT ? 1 : 2) * C::Q_TILE);
-          for (int pn = 0; pn < C::PANELS; ++pn) {
-            tma_load_3d(sbase + C::OFF_Q + pn * C::Q_PANEL, &p.q_map, BAR(C::B_QFULL), 64 * pn, I.q0, I.bh);
-            if (!C::DT)
-              tma_load_3d(sbase + C::OFF_DO + pn * C::Q_PANEL, &p.do_map, BAR(C::B_QFULL), 64 * pn, I.q0, I.bh);
+          if (nitems > 0 && !wait_one(BAR(C::B_QEMPTY), (nitems - 1) & 1, ab, (kKBwdQ << 8) | 10)) {
+            ok = false;
+            return;
+          }
+          int key0 = 0;  // first token of the sequence
+          if constexpr (RAGGED) {
+            key0 = I.start;
+            mbar_expect_tx(BAR(C::B_QFULL), (C::DT ? 1 : 2) * C::PANELS * p.tokens * p.G * 128);
+            for (int pn = 0; pn < C::PANELS; ++pn) {
+              tma_load_4d(sbase + C::OFF_Q + pn * C::Q_PANEL, m.q, BAR(C::B_QFULL), 64 * pn, 0, key0 + I.q0, I.bh);
+              if (!C::DT)
+                tma_load_4d(sbase + C::OFF_DO + pn * C::Q_PANEL, m.dO, BAR(C::B_QFULL), 64 * pn, 0, key0 + I.q0, I.bh);
+            }
+          } else {
+            mbar_expect_tx(BAR(C::B_QFULL), (C::DT ? 1 : 2) * C::Q_TILE);
+            for (int pn = 0; pn < C::PANELS; ++pn) {
+              tma_load_3d(sbase + C::OFF_Q + pn * C::Q_PANEL, m.q, BAR(C::B_QFULL), 64 * pn, I.q0, I.bh);
+              if (!C::DT)
+                tma_load_3d(sbase + C::OFF_DO + pn * C::Q_PANEL, m.dO, BAR(C::B_QFULL), 64 * pn, I.q0, I.bh);
+            }
           }
           ++nitems;
           for (int j = 0; j < I.n && ok; ++j) {
-            // The next item's Q and dO into L2 a few key steps before this item ends.
-            if (j == max(0, I.n - 3) && wn < p.items) {
-              const Item J = coords(wn);
-              if (!FEW || J.n > 0)
-                for (int pn = 0; pn < C::PANELS; ++pn) {
-                  tma_prefetch_l2_3d(&p.q_map, 64 * pn, J.q0, J.bh);
-                  tma_prefetch_l2_3d(&p.do_map, 64 * pn, J.q0, J.bh);
-                }
-            }
+            if (j == max(0, I.n - 3)) near_end();
             for (int wkv = 0; wkv < 2; ++wkv) {
               const int s = it % S;
               if (!wait_one(BAR(C::B_KVEMPTY + s), ((it / S) & 1) ^ 1, ab, (kKBwdQ << 8) | 1)) {
@@ -1379,15 +1629,49 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
                 break;
               }
               mbar_expect_tx(BAR(C::B_KVFULL + s), C::KV_TILE);
-              const CUtensorMap* m = wkv ? &p.v_map : &p.k_map;
+              const CUtensorMap* kv = wkv ? m.v : m.k;
               for (int pn = 0; pn < C::PANELS; ++pn)
-                tma_load_3d(sbase + C::OFF_KV + s * C::KV_TILE + pn * C::KV_PANEL, m, BAR(C::B_KVFULL + s),
-                            64 * pn, (I.j0 + j) * BN, I.bh);
+                tma_load_3d(sbase + C::OFF_KV + s * C::KV_TILE + pn * C::KV_PANEL, kv, BAR(C::B_KVFULL + s),
+                            64 * pn, key0 + (I.j0 + j) * BN, I.bh);
               if (j + 4 < I.n)
-                for (int pn = 0; pn < C::PANELS; ++pn) tma_prefetch_l2_3d(m, 64 * pn, (I.j0 + j + 4) * BN, I.bh);
+                for (int pn = 0; pn < C::PANELS; ++pn)
+                  tma_prefetch_l2_3d(kv, 64 * pn, key0 + (I.j0 + j + 4) * BN, I.bh);
               ++it;
             }
           }
+        };
+        if constexpr (RAGGED) {
+          Item I;
+          for (int t = 0; ok && item_at(t, I, ByThread{}); ++t) {
+            if (I.seq != seq) {
+              seq = I.seq;
+              const Maps m = maps_of(I);
+              tensormap_acquire(m.q);
+              tensormap_acquire(m.dO);
+              tensormap_acquire(m.k);
+              tensormap_acquire(m.v);
+            }
+            load_item(I, [] {});
+          }
+        } else {
+        int wn = atomicAdd(p.sched + 1, 1);
+        ok = publish(wn);
+        while (ok && wn < p.items) {
+          const Item I = coords(wn);
+          wn = atomicAdd(p.sched + 1, 1);
+          if (!publish(wn)) break;
+          if (FEW && I.n == 0) continue;  // an empty key part: nothing to load or compute
+          load_item(I, [&] {
+            // The next item's Q and dO into L2 a few key steps before this item ends.
+            if (wn >= p.items) return;
+            const Item J = coords(wn);
+            if (!FEW || J.n > 0)
+              for (int pn = 0; pn < C::PANELS; ++pn) {
+                tma_prefetch_l2_3d(&p.q_map, 64 * pn, J.q0, J.bh);
+                tma_prefetch_l2_3d(&p.do_map, 64 * pn, J.q0, J.bh);
+              }
+          });
+        }
         }
         if (nitems > 0) wait_drain_bwd(BAR(C::B_QFULL), (nitems - 1) & 1);
         for (int i = max(0, it - S); i < it; ++i) wait_drain_bwd(BAR(C::B_KVFULL + i % S), (i / S) & 1);
@@ -1425,9 +1709,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
           mma_commit(BAR(C::B_KVEMPTY + sv));
         };
         for (int r = 0; ok; ++r) {
-          const int w = item_warp(r);
-          if (w < 0 || w >= p.items) break;
-          const Item I = coords(w);
+          Item I;
+          if (!item_at(r, I, ByWarp{})) break;
           if (FEW && I.n == 0) continue;
           if (!wait_warp(BAR(C::B_QFULL), nitems & 1, ab, (kKBwdQ << 8) | 2)) break;
           ++nitems;
@@ -1475,9 +1758,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
         }
       } else
       for (int r = 0; ok; ++r) {
-        const int w = item_warp(r);
-        if (w < 0 || w >= p.items) break;
-        const Item I = coords(w);
+        Item I;
+        if (!item_at(r, I, ByWarp{})) break;
         if (FEW && I.n == 0) continue;
         if (!wait_warp(BAR(C::B_QFULL), nitems & 1, ab, (kKBwdQ << 8) | 2)) break;
         ++nitems;
@@ -1525,6 +1807,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
       mma_commit(BAR(C::B_DONE));
       wait_drain_bwd(BAR(C::B_DONE), 0);
       __syncwarp();
+    } else if (RAGGED && warp == 3) {
+      if constexpr (RAGGED)
+        ragged_schedule(p.sched, p.tokens, C::DQS, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY), ab,
+                        (kKBwdQ << 8) | 13);
     } else if (warp >= 4) {
       const int quad = warp & 3;
       const int r = quad * 32 + lane;
@@ -1534,10 +1820,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
       bool ok = true;
       int gj = 0;
       for (int rr = 0; ok; ++rr) {
-        const int w = item_warp(rr);
-        if (w < 0 || w >= p.items) break;
-        const Item I = coords(w);
-        const int qi = I.q0 + r;
+        Item I;
+        if (!item_at(rr, I, ByWarp{})) break;
+        // This row's query (packed: its token; rows past the tile's tokens are nobody's).
+        int qi;
+        bool qok;
+        if constexpr (RAGGED) {
+          qi = I.q0 + r / p.G;
+          qok = r < p.tokens * p.G && qi < I.len;
+        } else {
+          qi = I.q0 + r;
+          qok = qi < p.N;
+        }
         // Key-split partial sums: [part][bh][Npad][D] fp32, this row's dQ columns.
         float* prow = nullptr;
         if constexpr (FEW)
@@ -1551,23 +1845,36 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
             continue;
           }
         }
-        const float l2 = p.lse2[(size_t)I.bh * p.Npad + qi];  // -inf past N: every p is 0
-        const float dd = p.dd[(size_t)I.bh * p.Npad + qi];
+        float l2, dd;
+        int limit;
+        if constexpr (RAGGED) {
+          const size_t at = ((size_t)I.bh * p.slots + I.start / p.pre_tokens + I.seq + qi / p.pre_tokens) * p.pre_rows +
+                            qi % p.pre_tokens * p.G + r % p.G;
+          l2 = qok ? p.lse2[at] : -INFINITY;
+          dd = qok ? p.dd[at] : 0.f;
+          limit = !qok ? -1 : p.causal ? qi : I.len - 1;
+        } else {
+          l2 = p.lse2[(size_t)I.bh * p.Npad + qi];  // -inf past N: every p is 0
+          dd = p.dd[(size_t)I.bh * p.Npad + qi];
+          limit = p.causal ? min(qi, p.N - 1) : p.N - 1;
+        }
         const float2 l22 = make_float2(l2, l2), dd2 = make_float2(dd, dd);
-        const int limit = p.causal ? min(qi, p.N - 1) : p.N - 1;
         if constexpr (C::DT) {
           // This item's dO row qi as packed bf16 pairs into TMEM lane r: the A
           // operand of dP = dO V^T.  The previous item's dP MMAs, the last readers
           // of these columns, completed before its last SDP barrier, which these
           // warps have waited on.
-          const uint16_t* drow = p.dO + ((size_t)I.bh * p.N + (qi < p.N ? qi : 0)) * p.hd;
+          const uint16_t* drow;
+          if constexpr (RAGGED)
+            drow = p.dO + (qok ? (I.start + qi) * p.do_token + (I.bh * p.G + r % p.G) * p.do_head : 0);
+          else drow = p.dO + ((size_t)I.bh * p.N + (qok ? qi : 0)) * p.hd;
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 64) {
             uint32_t ow[32];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               uint4 x = make_uint4(0u, 0u, 0u, 0u);
-              if (qi < p.N && c0 + 8 * u < p.hd) x = *reinterpret_cast<const uint4*>(drow + c0 + 8 * u);
+              if (qok && c0 + 8 * u < p.hd) x = *reinterpret_cast<const uint4*>(drow + c0 + 8 * u);
               ow[4 * u] = x.x;
               ow[4 * u + 1] = x.y;
               ow[4 * u + 2] = x.z;
@@ -1664,8 +1971,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
             continue;
           }
         }
-        const int row0 = I.q0 + quad * 32;
-        uint16_t* obase = p.dq + ((size_t)I.bh * p.N + (size_t)row0) * p.hd + I.h * C::DQW;
+        // Where the dq row of this warp's row ri begins, NULL for nobody's.
+        auto dq_row = [&](int ri) -> uint16_t* {
+          if constexpr (RAGGED) {
+            const int rt = quad * 32 + ri, tok = I.q0 + rt / p.G;
+            return rt < p.tokens * p.G && tok < I.len ? p.dq + (I.start + tok) * p.dq_token +
+                                                            (I.bh * p.G + rt % p.G) * p.dq_head + I.h * C::DQW
+                                                      : nullptr;
+          } else {
+            const int row = I.q0 + quad * 32 + ri;
+            return row < p.N ? p.dq + ((size_t)I.bh * p.N + row) * p.hd + I.h * C::DQW : nullptr;
+          }
+        };
         const int hd_left = p.hd - I.h * C::DQW;  // columns of this part inside the head dim
         uint8_t* epi = gbase + C::OFF_EPI + quad * 2048;
 #pragma unroll
@@ -1689,13 +2006,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
             for (int jj = 0; jj < 4; ++jj) {
               const int ri = jj * 8 + (lane >> 2), u = lane & 3;
               const uint4 val = *reinterpret_cast<const uint4*>(epi + ri * 64 + ((u ^ ((ri >> 1) & 3)) << 4));
-              if (row0 + ri < p.N && c0 + 8 * u < hd_left)
-                *reinterpret_cast<uint4*>(obase + (size_t)ri * p.hd + c0 + 8 * u) = val;
+              uint16_t* const to = dq_row(ri);
+              if (to && c0 + 8 * u < hd_left) *reinterpret_cast<uint4*>(to + c0 + 8 * u) = val;
             }
             __syncwarp();
           } else {
-            if (qi < p.N) {
-              uint4* o4 = reinterpret_cast<uint4*>(obase + (size_t)lane * p.hd + c0);
+            if (qok) {
+              uint4* o4 = reinterpret_cast<uint4*>(dq_row(lane) + c0);
 #pragma unroll
               for (int v = 0; v < 4; ++v)
                 if (c0 + 8 * v < hd_left) o4[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
@@ -1714,5 +2031,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
+
+// dK/dV kernel configurations <d, query rows per step, with dQ, d split, query stages, separate P/dS>.
+// d = 128 5-GEMM: bulk dQ reductions from a shared-memory tile measured faster than per-element
+// or 16-byte reductions straight from registers, worth giving up one query stage.
+// d = 64 5-GEMM: 128 query columns per step over two compute warpgroups, each packing its P^T / dS^T
+// into its own S^T / dP^T columns.
+using KV5_64 = BwdKVCfg<64, 128, true, 1, 2, false>;
+using KV5_128 = BwdKVCfg<128, 64, true, 1, 3, true>;
+using KV7_64 = BwdKVCfg<64, 128, false, 1, 3, false>;
+using KV7_128 = BwdKVCfg<128, 64, false, 1, 4, true>;
+// d = 192: dV and dK for all 192 columns fit TMEM next to S and dP, so no d split.
+using KV7_192 = BwdKVCfg<192, 64, false, 1, 2, false>;
+// d = 256: V in TMEM, and the outputs split (a dV item and a dK item per key tile, each with one
+// 256-column accumulator).
+using KV7_256 = BwdKVCfg<256, 64, false, 2, 2, false, true, true>;
+// d = 384: dV and dK cut into three column parts of 128, one work item each (every item
+// recomputes S^T and dP^T), 32 queries per step, V in TMEM: 32 + 32 + 128 + 128 + 192 = 512
+// TMEM columns next to a 96 KiB K tile and two 48 KiB query stages.
+using KV7_384 = BwdKVCfg<384, 32, false, 3, 2, false, true, false>;
+// dQ kernel configurations <d, keys per tile, K/V ring slots>.
+using Q7_64 = BwdQCfg<64, 128, 6>;
+using Q7_128 = BwdQCfg<128, 128, 4>;
+using Q7_192 = BwdQCfg<192, 64, 7, true>;
+using Q7_256 = BwdQCfg<256, 64, 5, true>;
+// d = 384: two dQ column parts of 192 per query tile (one work item each), dO in TMEM,
+// 32-key tiles, four K/V slots of 24 KiB next to the 96 KiB Q tile.
+using Q7_384 = BwdQCfg<384, 32, 4, true, 2>;
 
 }  // namespace fa

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
     }
   };
   auto coords = [&](int w) {
-    Item it;
+    Item it = {};
     if constexpr (!RAGGED) {
     int qb;
     const int wb = SPLIT ? w / p.splits : w;

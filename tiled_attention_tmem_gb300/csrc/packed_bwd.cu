@@ -1,0 +1,295 @@
+// Backward of attention over packed sequences: the dense backward's kernels (bwd.cuh)
+// over items that ragged_plan_kernel lays out, with a preprocess and a dQ conversion that
+// go by query tiles.
+#include <algorithm>
+#include <type_traits>
+
+#include "bwd.cuh"
+#include "packed_host.h"
+
+namespace fa {
+namespace {
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct RowsIn {
+  const uint16_t* data;
+  long long token, head;
+};
+struct RowsOut {
+  uint16_t* data;
+  long long token, head;
+};
+
+// Tiles of `tokens` tokens with the G heads of a kv head: `rows` rows of the row
+// arrays, of which the last rows - tokens * G are nobody's.
+struct RowTiles {
+  const int* cu;
+  int B, T, H, Hkv, G;
+  int tokens, rows, slots;
+  int hd;
+};
+
+// The sequence that holds tile slot ts, and the slot's first token in it; false where none does.
+// Sequence b has the slots from cu[b] / tokens + b on, which grow with b.
+__device__ __forceinline__ bool tile_of_slot(const RowTiles& t, int ts, int& start, int& len, int& tok0) {
+  int lo = 0, hi = t.B;  // the last b whose first slot is not past ts
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if ((long long)min(max(t.cu[mid], 0), t.T) / t.tokens + mid <= ts) lo = mid;
+    else hi = mid;
+  }
+  if (t.B == 0) return false;
+  start = t.cu[lo];
+  const int end = t.cu[lo + 1];
+  if (start < 0 || start > end || end > t.T) return false;
+  len = end - start;
+  const long long first = (long long)ts - start / t.tokens - lo;
+  if (first < 0 || first * t.tokens >= len) return false;
+  tok0 = (int)first * t.tokens;
+  return true;
+}
+
+struct RaggedPreParams {
+  RowTiles tiles;
+  RowsIn o, dO;
+  const float* lse;
+  float* lse2;
+  float* dd;
+  float* dqacc;  // NULL for the 7-GEMM form
+  RowsOut out[3];  // dq, dk, dv: their rows of no sequence are zeroed
+};
+
+// A block a tile slot at a time, GT threads a row: D_i = sum_c dO_ic O_ic (fp32) and the log2-domain
+// LSE, both negated, and (5-GEMM) zeros for the fp32 dQ rows.  Memory bounds it.
+template <int D>
+__global__ void __launch_bounds__(256) ragged_pre_kernel(const __grid_constant__ RaggedPreParams p) {
+  grid_dep_wait();
+  constexpr int GT = D / 8 <= 32 ? D / 8 : 16;
+  constexpr int CH = D / 8 / GT;
+  const RowTiles& t = p.tiles;
+  const int sub = threadIdx.x % GT;
+  const long long work = (long long)t.slots * t.Hkv;
+  for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+    const int ts = (int)(w / t.Hkv), kvh = (int)(w - (long long)ts * t.Hkv);
+    int start, len, tok0;
+    if (!tile_of_slot(t, ts, start, len, tok0)) continue;
+    for (int r = threadIdx.x / GT; r < t.rows; r += 256 / GT) {
+      const int tok = tok0 + r / t.G, head = kvh * t.G + r % t.G;
+      const bool have = r < t.tokens * t.G && tok < len;
+      float acc = 0.f;
+      if (have) {
+        const uint16_t* o = p.o.data + (start + tok) * p.o.token + head * p.o.head;
+        const uint16_t* g = p.dO.data + (start + tok) * p.dO.token + head * p.dO.head;
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+          const int c = (ch * GT + sub) * 8;
+          if (c >= t.hd) continue;
+          const uint4 a = *reinterpret_cast<const uint4*>(o + c), b = *reinterpret_cast<const uint4*>(g + c);
+          const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc = fmaf(__uint_as_float(av[e] << 16), __uint_as_float(bv[e] << 16), acc);
+            acc = fmaf(__uint_as_float(av[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), acc);
+          }
+        }
+      }
+#pragma unroll
+      for (int d = GT / 2; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d, GT);
+      const size_t row = ((size_t)kvh * t.slots + ts) * t.rows + r;
+      if (sub == 0) {
+        p.dd[row] = -acc;
+        // (a row whose scores are all -inf has no probabilities: -inf - -inf would be NaN)
+        const float lse = have ? p.lse[(long long)(start + tok) * t.H + head] : -INFINITY;
+        p.lse2[row] = lse == -INFINITY ? -INFINITY : -(lse * kLog2e);
+      }
+      if (p.dqacc) {
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+          float4* z = reinterpret_cast<float4*>(p.dqacc + row * D + (ch * GT + sub) * 8);
+          z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+    }
+  }
+  // Gradients of the rows of no sequence: before the first one and behind the last.
+  const int lo = t.B > 0 ? min(max(t.cu[0], 0), t.T) : 0, hi = t.B > 0 ? min(max(t.cu[t.B], lo), t.T) : 0;
+  const long long spare = (long long)lo + (t.T - hi), chunks = t.hd / 8;
+#pragma unroll
+  for (int x = 0; x < 3; ++x) {
+    const int heads = x == 0 ? t.H : t.Hkv;
+    const long long n = spare * heads * chunks;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+      const long long row = i / (heads * chunks), rest = i - row * heads * chunks;
+      const long long tok = row < lo ? row : hi + (row - lo);
+      *reinterpret_cast<uint4*>(p.out[x].data + tok * p.out[x].token + rest / chunks * p.out[x].head +
+                                rest % chunks * 8) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+}
+
+struct RaggedConvParams {
+  RowTiles tiles;
+  const float* dqacc;
+  RowsOut dq;
+  int* err;
+  float scale;
+};
+
+// dq = scale * the fp32 sums (5-GEMM), bf16.  A block a tile slot, eight columns a thread.  Memory bounds it.
+template <int D>
+__global__ void __launch_bounds__(256) ragged_conv_kernel(const __grid_constant__ RaggedConvParams p) {
+  grid_dep_wait();
+  if (*reinterpret_cast<volatile const int*>(p.err) != 0) return;
+  const RowTiles& t = p.tiles;
+  const int chunks = t.hd / 8;
+  const long long work = (long long)t.slots * t.Hkv;
+  for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+    const int ts = (int)(w / t.Hkv), kvh = (int)(w - (long long)ts * t.Hkv);
+    int start, len, tok0;
+    if (!tile_of_slot(t, ts, start, len, tok0)) continue;
+    const int rows = min(t.tokens, len - tok0) * t.G;
+    for (int i = threadIdx.x; i < rows * chunks; i += 256) {
+      const int r = i / chunks, c = (i - r * chunks) * 8;
+      const float* row = p.dqacc + (((size_t)kvh * t.slots + ts) * t.rows + r) * D;
+      const float4 a = *reinterpret_cast<const float4*>(row + dq_swz(r, c));
+      const float4 b = *reinterpret_cast<const float4*>(row + dq_swz(r, c + 4));
+      *reinterpret_cast<uint4*>(p.dq.data + (start + tok0 + r / t.G) * p.dq.token + (kvh * t.G + r % t.G) * p.dq.head + c) =
+          make_uint4(pack_bf16(a.x * p.scale, a.y * p.scale), pack_bf16(a.z * p.scale, a.w * p.scale),
+                     pack_bf16(b.x * p.scale, b.y * p.scale), pack_bf16(b.z * p.scale, b.w * p.scale));
+    }
+  }
+}
+
+struct BwdCall {
+  PackedRows q, k, v, o, dO, dq, dk, dv;
+  const float* lse;
+  const int* cu;
+  PackedShape s;
+  float scale;
+  int causal;
+  void* workspace;
+  cudaStream_t st;
+};
+
+// The workspace: the plan, then lse2, dd and (5-GEMM) dqacc by query tiles.
+struct BwdLayout {
+  int cuts, nmaps, slots;
+  size_t rows, plan, total;
+  BwdLayout(const PackedShape& s, int variant, int tile_rows, int D) {
+    const bool five = variant == FA_BWD_5GEMM;
+    cuts = five ? 1 : 2, nmaps = five ? 4 : 8;
+    slots = s.T / (tile_rows / s.G()) + s.B;
+    rows = (size_t)s.Hkv * slots * tile_rows;
+    plan = packed_plan_bytes(s.B, cuts, nmaps);
+    total = plan + 2 * align256(4 * rows) + (five ? 4 * rows * D : 0);
+  }
+};
+
+RowsIn in(const PackedRows& r) { return {static_cast<const uint16_t*>(r.data), r.token, r.head}; }
+RowsOut out(const PackedRows& r) { return {static_cast<uint16_t*>(r.data), r.token, r.head}; }
+
+// KV: the dK/dV kernel; Q: the dQ kernel (void: 5-GEMM).  DP: the preprocess's head dimension.
+template <int DP, class KV, class Q>
+fa_status run(const BwdCall& c) {
+  constexpr bool five = KV::DQ;
+  const PackedShape& s = c.s;
+  const BwdLayout lay(s, five ? FA_BWD_5GEMM : FA_BWD_7GEMM, KV::BM, KV::D);
+  const PackedPlan plan = packed_plan_at(c.workspace, s.B, lay.cuts, lay.nmaps);
+  uint8_t* at = static_cast<uint8_t*>(c.workspace) + lay.plan;
+  float* const lse2 = reinterpret_cast<float*>(at);
+  float* const dd = reinterpret_cast<float*>(at + align256(4 * lay.rows));
+  float* const dqacc = five ? reinterpret_cast<float*>(at + 2 * align256(4 * lay.rows)) : nullptr;
+  int* const err = device_error_word();
+  if (!err) return record_cuda_error(cudaErrorMemoryAllocation);
+
+  // Operands that other tiles of a head read again: Q and dO of its G heads, K, V, (5-GEMM) the fp32 dQ.
+  const double token_bytes = 2.0 * s.d * (2 * s.G() + 2) + (five ? 4.0 * KV::D * s.G() : 0.0);
+  const int tokens = KV::BM / s.G();
+  CUtensorMap maps[kPackedMaxMaps];
+  PackedCut cuts[2] = {{KV::BN, KV::DSPLIT, token_bytes}, {}};
+  fa_status e;
+  if ((e = packed_query_map(&maps[0], c.q, s, tokens)) != FA_OK) return e;
+  if ((e = packed_query_map(&maps[1], c.dO, s, tokens)) != FA_OK) return e;
+  if ((e = packed_key_map(&maps[2], c.k, s, KV::BN)) != FA_OK) return e;
+  if ((e = packed_key_map(&maps[3], c.v, s, KV::BN)) != FA_OK) return e;
+  if constexpr (!five) {
+    if ((e = packed_query_map(&maps[4], c.q, s, 128 / s.G())) != FA_OK) return e;
+    if ((e = packed_query_map(&maps[5], c.dO, s, 128 / s.G())) != FA_OK) return e;
+    if ((e = packed_key_map(&maps[6], c.k, s, Q::BN)) != FA_OK) return e;
+    if ((e = packed_key_map(&maps[7], c.v, s, Q::BN)) != FA_OK) return e;
+    cuts[1] = {128 / s.G(), Q::DQS, 4.0 * s.d};
+  }
+  if (s.B > 0 && (e = run_packed_plan(plan, c.cu, s, cuts, lay.cuts, maps, lay.nmaps, c.st)) != FA_OK) return e;
+
+  const long long sms = sm_count_cached();
+  RaggedPreParams pre = {};
+  pre.tiles = {c.cu, s.B, s.T, s.H, s.Hkv, s.G(), tokens, KV::BM, lay.slots, s.d};
+  pre.o = in(c.o), pre.dO = in(c.dO);
+  pre.lse = c.lse, pre.lse2 = lse2, pre.dd = dd, pre.dqacc = dqacc;
+  pre.out[0] = out(c.dq), pre.out[1] = out(c.dk), pre.out[2] = out(c.dv);
+  const unsigned blocks = (unsigned)std::min<long long>((long long)(lay.slots + 1) * s.Hkv, 8 * sms);
+  if ((e = launch(FA_KERNEL_BWD_PRE, ragged_pre_kernel<DP>, dim3(blocks), dim3(256), 0, c.st, pre)) != FA_OK) return e;
+  if (s.B == 0) return FA_OK;  // (every row is of no sequence)
+
+  RaggedKVParams p;
+  p.maps = plan.maps, p.nmaps = lay.nmaps, p.sched = plan.sched[0];
+  p.v = in(c.v).data, p.v_token = c.v.token, p.v_head = c.v.head;
+  p.lse2 = lse2, p.dd = dd, p.dqacc = dqacc;
+  p.dk = out(c.dk).data, p.dk_token = c.dk.token, p.dk_head = c.dk.head;
+  p.dv = out(c.dv).data, p.dv_token = c.dv.token, p.dv_head = c.dv.head;
+  p.err = err, p.slots = lay.slots, p.Hkv = s.Hkv, p.G = s.G(), p.tokens = tokens, p.hd = s.d;
+  p.scale_log2 = c.scale * kLog2e, p.scale = c.scale, p.causal = c.causal;
+  const unsigned kv_grid =
+      (unsigned)std::min<long long>(((long long)s.T / KV::BN + s.B) * s.Hkv * KV::DSPLIT, sms);
+  if ((e = launch(five ? FA_KERNEL_BWD_KV5 : FA_KERNEL_BWD_KV7, bwd_kv_kernel<KV, false, RaggedKVParams>, dim3(kv_grid),
+                  dim3(KV::THREADS), KV::SMEM_BYTES, c.st, p)) != FA_OK)
+    return e;
+  if constexpr (five) {
+    RaggedConvParams conv = {pre.tiles, dqacc, out(c.dq), err, c.scale};
+    return launch(FA_KERNEL_BWD_CONV, ragged_conv_kernel<KV::D>, dim3(blocks), dim3(256), 0, c.st, conv);
+  } else {
+    RaggedQParams r;
+    r.maps = plan.maps + 4, r.nmaps = lay.nmaps, r.sched = plan.sched[1];
+    r.dO = in(c.dO).data, r.do_token = c.dO.token, r.do_head = c.dO.head;
+    r.lse2 = lse2, r.dd = dd;
+    r.dq = out(c.dq).data, r.dq_token = c.dq.token, r.dq_head = c.dq.head;
+    r.err = err, r.slots = lay.slots, r.pre_tokens = tokens, r.pre_rows = KV::BM;
+    r.Hkv = s.Hkv, r.G = s.G(), r.tokens = 128 / s.G(), r.hd = s.d;
+    r.scale_log2 = c.scale * kLog2e, r.scale = c.scale, r.causal = c.causal;
+    const unsigned q_grid = (unsigned)std::min<long long>(((long long)s.T / r.tokens + s.B) * s.Hkv * Q::DQS, sms);
+    return launch(FA_KERNEL_BWD_Q7, bwd_q_kernel<Q, false, RaggedQParams>, dim3(q_grid), dim3(Q::THREADS),
+                  Q::SMEM_BYTES, c.st, r);
+  }
+}
+
+// Query rows of a tile of the dK/dV kernels (both forms).
+int tile_rows(int d) { return d == 64 ? 128 : d == 384 ? 32 : 64; }
+static_assert(KV5_64::BM == 128 && KV7_64::BM == 128 && KV5_128::BM == 64 && KV7_128::BM == 64 && KV7_192::BM == 64 &&
+                  KV7_256::BM == 64 && KV7_384::BM == 32,
+              "tile_rows");
+
+}  // namespace
+
+size_t packed_bwd_bytes(const PackedShape& s, int variant) {
+  return BwdLayout(s, variant, tile_rows(s.d), padded_head_dim(s.d)).total;
+}
+
+fa_status run_packed_bwd(const PackedRows& q, const PackedRows& k, const PackedRows& v, const PackedRows& o,
+                         const PackedRows& dO, const float* lse, const PackedRows& dq, const PackedRows& dk,
+                         const PackedRows& dv, const int* cu, const PackedShape& s, float scale, int causal,
+                         int variant, void* workspace, cudaStream_t st) {
+  const BwdCall c = {q, k, v, o, dO, dq, dk, dv, lse, cu, s, scale, causal, workspace, st};
+  const bool five = variant == FA_BWD_5GEMM;
+  switch (s.d) {
+    case 64: return five ? run<64, KV5_64, void>(c) : run<64, KV7_64, Q7_64>(c);
+    case 96:
+    case 128: return five ? run<128, KV5_128, void>(c) : run<128, KV7_128, Q7_128>(c);
+    case 192: return run<256, KV7_192, Q7_192>(c);
+    case 256: return run<256, KV7_256, Q7_256>(c);
+    case 384: return run<384, KV7_384, Q7_384>(c);
+  }
+  return FA_ERR_UNSUPPORTED;
+}
+
+}  // namespace fa

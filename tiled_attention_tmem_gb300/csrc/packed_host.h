@@ -48,10 +48,15 @@ fa_status packed_key_map(CUtensorMap* map, const PackedRows& r, const PackedShap
 
 // Checks shared by the entry points.
 fa_status packed_shape_checks(const PackedShape& s, float scale, int causal);
-fa_status packed_rows_checks(const PackedRows& r, int T, int heads, int d);
+fa_status packed_rows_checks(const PackedRows& r, int T, int heads);
 
 fa_status run_packed_fwd(const PackedRows& q, const PackedRows& k, const PackedRows& v, const PackedRows& o, float* lse,
                          const int* cu, const PackedShape& s, float scale, int causal, void* workspace, cudaStream_t st);
 size_t packed_fwd_bytes(const PackedShape& s);
+fa_status run_packed_bwd(const PackedRows& q, const PackedRows& k, const PackedRows& v, const PackedRows& o,
+                         const PackedRows& dO, const float* lse, const PackedRows& dq, const PackedRows& dk,
+                         const PackedRows& dv, const int* cu, const PackedShape& s, float scale, int causal,
+                         int variant, void* workspace, cudaStream_t st);
+size_t packed_bwd_bytes(const PackedShape& s, int variant);
 
 }  // namespace fa

@@ -209,15 +209,20 @@ fa_status packed_shape_checks(const PackedShape& s, float scale, int causal) {
   return FA_OK;
 }
 
-fa_status packed_rows_checks(const PackedRows& r, int T, int heads, int d) {
+fa_status packed_rows_checks(const PackedRows& r, int T, int heads) {
   if (!r.data) return FA_ERR_INVALID_ARG;
   if (!aligned(r.data, 16)) return FA_ERR_MISALIGNED;
   const long long most = 1LL << 34;  // elements: strides of 2^40 bytes and more are not encoded, over 32 heads
   if ((T > 1 && (r.token <= 0 || r.token >= most)) || (heads > 1 && (r.head <= 0 || r.head >= most)))
     return FA_ERR_INVALID_ARG;
   if ((T > 1 && (r.token & 7)) || (heads > 1 && (r.head & 7))) return FA_ERR_MISALIGNED;
-  (void)d;
   return FA_OK;
+}
+
+// The form that a call of this variant runs (0: none).
+static int packed_variant(int d, int variant) {
+  if (variant == FA_BWD_AUTO) return fa_bwd_choose(1, 1, 1, d, 1);
+  return bwd_supported(d, variant) ? variant : 0;
 }
 
 }  // namespace fa
@@ -244,12 +249,48 @@ fa_status fa_packed_fwd(const void* q, long long q_token, long long q_head, cons
                    rv = {const_cast<void*>(v), v_token, v_head}, ro = {o, o_token, o_head};
   if (!lse || !cu) return FA_ERR_INVALID_ARG;
   for (const PackedRows* r : {&rq, &ro})
-    if ((st = packed_rows_checks(*r, T, H, d)) != FA_OK) return st;
+    if ((st = packed_rows_checks(*r, T, H)) != FA_OK) return st;
   for (const PackedRows* r : {&rk, &rv})
-    if ((st = packed_rows_checks(*r, T, Hkv, d)) != FA_OK) return st;
+    if ((st = packed_rows_checks(*r, T, Hkv)) != FA_OK) return st;
   if (!aligned(lse, 4) || !aligned(cu, 4)) return FA_ERR_MISALIGNED;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < packed_fwd_bytes(s)) return FA_ERR_WORKSPACE;
   return run_packed_fwd(rq, rk, rv, ro, lse, cu, s, scale, causal, workspace, (cudaStream_t)stream);
+}
+
+size_t fa_packed_bwd_workspace_size(int B, int T, int H, int Hkv, int d, int variant) {
+  const PackedShape s = {B, T, H, Hkv, d};
+  if (packed_shape_checks(s, 1.f, 0) != FA_OK || T == 0 || H == 0) return 0;
+  const int form = packed_variant(d, variant);
+  return form ? packed_bwd_bytes(s, form) : 0;
+}
+
+fa_status fa_packed_bwd(const void* q, long long q_token, long long q_head, const void* k, long long k_token,
+                        long long k_head, const void* v, long long v_token, long long v_head, const void* o,
+                        long long o_token, long long o_head, const void* dO, long long do_token, long long do_head,
+                        const float* lse, void* dq, long long dq_token, long long dq_head, void* dk, long long dk_token,
+                        long long dk_head, void* dv, long long dv_token, long long dv_head, const int* cu, int B, int T,
+                        int H, int Hkv, int d, float scale, int causal, int variant, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const PackedShape s = {B, T, H, Hkv, d};
+  fa_status st = packed_shape_checks(s, scale, causal);
+  if (st != FA_OK) return st;
+  if (variant != FA_BWD_AUTO && variant != FA_BWD_5GEMM && variant != FA_BWD_7GEMM) return FA_ERR_INVALID_ARG;
+  const int form = packed_variant(d, variant);
+  if (!form) return FA_ERR_UNSUPPORTED;
+  if (T == 0 || H == 0) return FA_OK;
+  const PackedRows rq = {const_cast<void*>(q), q_token, q_head}, rk = {const_cast<void*>(k), k_token, k_head},
+                   rv = {const_cast<void*>(v), v_token, v_head}, ro = {const_cast<void*>(o), o_token, o_head},
+                   rg = {const_cast<void*>(dO), do_token, do_head}, rdq = {dq, dq_token, dq_head},
+                   rdk = {dk, dk_token, dk_head}, rdv = {dv, dv_token, dv_head};
+  if (!lse || (B > 0 && !cu)) return FA_ERR_INVALID_ARG;
+  for (const PackedRows* r : {&rq, &ro, &rg, &rdq})
+    if ((st = packed_rows_checks(*r, T, H)) != FA_OK) return st;
+  for (const PackedRows* r : {&rk, &rv, &rdk, &rdv})
+    if ((st = packed_rows_checks(*r, T, Hkv)) != FA_OK) return st;
+  if (!aligned(lse, 4) || !aligned(cu, 4)) return FA_ERR_MISALIGNED;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < packed_bwd_bytes(s, form)) return FA_ERR_WORKSPACE;
+  return run_packed_bwd(rq, rk, rv, ro, rg, lse, rdq, rdk, rdv, cu, s, scale, causal, form, workspace,
+                        (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -108,3 +108,51 @@ def packed_attention_forward(q, k, v, cu, scale: float | None = None, causal: bo
     if st:
         _check(st, "fa_packed_fwd")
     return out, lse
+
+
+def packed_backward_workspace_bytes(sequences, tokens, heads, kv_heads, head_dim, variant=_b.FA_BWD_AUTO) -> int:
+    """What ``packed_attention_backward`` needs."""
+    _check_sizes(sequences, tokens, heads, kv_heads)
+    return _b.fa_packed_bwd_workspace_size(sequences, tokens, heads, kv_heads, head_dim, variant)
+
+
+_backward_bytes = functools.lru_cache(maxsize=1024)(packed_backward_workspace_bytes)
+
+
+def packed_attention_backward(q, k, v, o, do, lse, cu, scale: float | None = None, causal: bool = True,
+                              variant: int = _b.FA_BWD_AUTO, workspace=None, grads=None, stream=None):
+    """Returns (dq, dk, dv) bf16 of ``packed_attention_forward``'s q, k and v, given its results o and
+    lse and the gradient do (bf16 [T, heads, d], strides free like q's).  Rows of no sequence get zeros.
+    ``grads``: three tensors to write, or None; ``workspace``: a uint8 CUDA tensor of
+    ``packed_backward_workspace_bytes`` (of the same variant), not shared with a concurrent
+    call, or None.  ``variant`` as in ``attention_backward``: the 7-GEMM form gives the same bits every time."""
+    index = _device_index(q, "q")
+    if stream is not None or _current_device() != index:
+        with _On(index, stream):
+            return packed_attention_backward(q, k, v, o, do, lse, cu, scale, causal, variant, workspace, grads)
+    T, H, Hkv, d, (qt, qh), (kt, kh), (vt, vh) = _shapes(q, k, v, index)
+    ot, oh = _input(o, "o", q.shape, index)
+    gt, gh = _input(do, "do", q.shape, index)
+    if not (isinstance(lse, _Tensor) and lse.dtype is _F32 and lse.shape == (T, H) and lse.get_device() == index
+            and lse.is_contiguous()):
+        _dense(lse, "lse", _F32, (T, H), index)
+    B = _sequences(cu, index)
+    if grads is None:
+        dq = _empty(q.shape, dtype=_BF16, device=q.device)
+        dk, dv = (_empty(k.shape, dtype=_BF16, device=q.device) for _ in range(2))
+        (qgt, qgh), (kgt, kgh), (vgt, vgh) = (H * d, d), (Hkv * d, d), (Hkv * d, d)
+    else:
+        if len(grads) != 3:
+            raise ValueError("grads must be (dq, dk, dv)")
+        dq, dk, dv = grads
+        (qgt, qgh), (kgt, kgh), (vgt, vgh) = (_rows(t, name, like.shape, index, written=True) for t, name, like in
+                                              ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)))
+    workspace, at, need = _workspace(workspace, _backward_bytes(B, T, H, Hkv, d, variant), index, q.device)
+    st = _b.lib().fa_packed_bwd(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, o.data_ptr(), ot, oh,
+                                do.data_ptr(), gt, gh, lse.data_ptr(), dq.data_ptr(), qgt, qgh, dk.data_ptr(), kgt, kgh,
+                                dv.data_ptr(), vgt, vgh, cu.data_ptr(), B, T, H, Hkv, d,
+                                d ** -0.5 if scale is None else scale, bool(causal), variant, at, need,
+                                _current_stream(index))
+    if st:
+        _check(st, "fa_packed_bwd")
+    return dq, dk, dv
