@@ -74,6 +74,62 @@ fa_status fa_packed_bwd(const void* q, long long q_token, long long q_head, cons
  */
 size_t fa_packed_bwd_workspace_size(int B, int T, int H, int Hkv, int d, int variant);
 
+/*
+ * Norms of queries and keys for each head, and their rotation by the token's position.  For each
+ * head x of q [T, H, d] and k [T, Hkv, d], in fp32 and rounded to bf16 once:
+ *   n_c = x_c r w_c,  r = (sum_c x_c^2 / d + eps)^-1/2   (n = x where the weight is NULL)
+ *   y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin      for pair i < rot/2: channels
+ *   (a, b) = (i, i + rot/2), or (2i, 2i + 1) if `interleaved`;  y_c = n_c for c >= rot
+ * with cos = rotary[position[t]][i] and sin = rotary[position[t]][rot/2 + i].  The products and the
+ * sum of a rotation are rounded to fp32 one by one.
+ *   rotary    fp32 [positions, rot] dense, 16-byte aligned; rot a multiple of 32, at most d (0: no rotation)
+ *   position  int32 [T].  A token whose position is not in [0, positions) is left out: its
+ *             rows of q_out and k_out stay as they were.
+ *   q_weight, k_weight  bf16 [d], 16-byte aligned, or NULL;  eps finite and >= 0
+ * q and k with strides (elements, multiples of 8; 0 is allowed); q_out may be q itself with q's strides, k_out
+ * likewise, but no output may overlap another array in another way.  H + 2 Hkv at most 65535,
+ * T at most 2^30.
+ */
+fa_status fa_qk_norm_rope(const void* q, long long q_token, long long q_head, const void* k, long long k_token,
+                          long long k_head, const float* rotary, int positions, int rot, const int* position,
+                          const void* q_weight, const void* k_weight, float eps, int interleaved, void* q_out,
+                          long long qo_token, long long qo_head, void* k_out, long long ko_token, long long ko_head,
+                          int T, int H, int Hkv, int d, void* stream);
+
+/*
+ * Its gradients.  dq_out and dk_out: of the results; q and k: what went in (needed, and read, only where
+ * there is the weight).  With g the rotation's transpose of dy, xhat = x r and z = w g:
+ *   dx = r (z - xhat sum_c(xhat_c z_c) / d)  (dx = g where the weight is NULL),  dw = sum g xhat
+ * dq, dk bf16, rounded once (dq may be dq_out, or q, with the same strides; dk likewise); dq_weight, dk_weight fp32 [d],
+ * written where there is the weight: sums in fp32 over all tokens and heads, in a fixed order.  A token
+ * without a position has gradients of zero and is not in the sums.
+ * workspace: fa_qk_norm_rope_bwd_workspace_size bytes, 256-byte aligned, not shared with a
+ * concurrent call (NULL where both weights are).
+ */
+fa_status fa_qk_norm_rope_bwd(const void* dq_out, long long dqo_token, long long dqo_head, const void* dk_out,
+                              long long dko_token, long long dko_head, const void* q, long long q_token,
+                              long long q_head, const void* k, long long k_token, long long k_head,
+                              const float* rotary, int positions, int rot, const int* position, const void* q_weight,
+                              const void* k_weight, float eps, int interleaved, void* dq, long long dq_token,
+                              long long dq_head, void* dk, long long dk_token, long long dk_head, float* dq_weight,
+                              float* dk_weight, int T, int H, int Hkv, int d, void* workspace, size_t workspace_bytes,
+                              void* stream);
+size_t fa_qk_norm_rope_bwd_workspace_size(int T, int H, int Hkv, int d);
+
+/*
+ * New tokens on their way into the 4-bit cache (fa_paged.h) in one pass: q [T, H, d] and k
+ * [T, Hkv, d] normed and rotated as by fa_qk_norm_rope (Hkv and d those of the cache), q to q_out, k
+ * (rounded to bf16) and v stored as by fa_kv4_store in slots int64 [T].  k_out: the rotated keys too,
+ * or NULL.  A token without a position is left out altogether; one whose slot is not in
+ * [0, pages*page) is rotated but not stored.  The valid slots must be distinct.  H may be 0.
+ */
+fa_status fa_kv4_append(const fa_kv4_cache* cache, const void* q, long long q_token, long long q_head, const void* k,
+                        long long k_token, long long k_head, const void* v, long long v_token, long long v_head,
+                        const float* rotary, int positions, int rot, const int* position, const void* q_weight,
+                        const void* k_weight, float eps, int interleaved, void* q_out, long long qo_token,
+                        long long qo_head, void* k_out, long long ko_token, long long ko_head, const long long* slots,
+                        int T, int H, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

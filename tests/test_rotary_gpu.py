@@ -1,0 +1,175 @@
+"""Norms and rotation of queries and keys, and the rotated append to the 4-bit cache."""
+
+import pytest
+
+import rotary_ref as R
+
+pytestmark = pytest.mark.gpu
+
+DIMS = (64, 96, 128, 192, 256, 384)
+
+
+def make(T, H, Hkv, d, turned, seed=0, weights=True, positions=512, loose=True, value=False):
+    """q, k (and v) as slices of a fused projection's rows, a table, positions of which some are not in it."""
+    import torch
+    g = torch.Generator(device="cuda:0").manual_seed(seed)
+    x = torch.randn((T, H + 2 * Hkv, d), generator=g, device="cuda:0").to(torch.bfloat16)
+    pos = torch.randint(0, positions, (T,), generator=g, device="cuda:0", dtype=torch.int32)
+    if loose and T > 4:
+        pos[1], pos[T // 2], pos[-1] = -1, positions, -2 ** 31
+    w = [(1 + 0.3 * torch.randn(d, generator=g, device="cuda:0")).to(torch.bfloat16) if weights else None for _ in range(2)]
+    out = (x[:, :H], x[:, H:H + Hkv], R.table(positions, turned, device="cuda:0"), pos, *w)
+    return out + (x[:, H + Hkv:],) if value else out
+
+
+CASES = [(1, 1, 1), (7, 8, 2), (64, 32, 8), (33, 5, 3), (1000, 7, 1), (3000, 12, 4)]
+
+
+@pytest.mark.parametrize("interleaved", (False, True))
+@pytest.mark.parametrize("d", DIMS)
+def test_forward_and_backward(d, interleaved):
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    for n, (T, H, Hkv) in enumerate(CASES):
+        for weights in (True, False):
+            turned = (d, 32, d - 32, 0)[(n + weights) % 4]
+            q, k, rotary, pos, wq, wk = make(T, H, Hkv, d, turned, seed=n, weights=weights)
+            what = f"T={T} {H}/{Hkv} d={d} turned={turned} weights={weights}"
+            mine = R.live(pos, rotary)
+            marked = [torch.full(t.shape, 7.0, device="cuda:0").to(torch.bfloat16) for t in (q, k)]
+            got = api.qk_norm_rope(q, k, rotary, pos, wq, wk, 1e-5, interleaved, out=marked)
+            assert got[0] is marked[0] and got[1] is marked[1]
+            for y, x, w in zip(got, (q, k), (wq, wk)):
+                ref, size = R.forward(x, w, 1e-5, rotary, pos, interleaved)
+                R.check(y[mine], ref[mine], size[mine], what)
+                assert bool((y[~mine] == 7).all()), what  # tokens without a position stay as they were
+            g = torch.Generator(device="cuda:0").manual_seed(50 + n)
+            dq, dk = (torch.randn(t.shape, generator=g, device="cuda:0").to(torch.bfloat16) for t in (q, k))
+            back = api.qk_norm_rope_backward(dq, dk, q, k, rotary, pos, wq, wk, 1e-5, interleaved)
+            for dx, dw, dy, x, w in zip(back[:2], back[2:], (dq, dk), (q, k), (wq, wk)):
+                ref, size, ref_w, size_w = R.backward(dy, x, w, 1e-5, rotary, pos, interleaved)
+                R.check(dx, ref, size, what + " gradient")
+                assert (dw is None) == (w is None)
+                if dw is not None:
+                    R.check_weight(dw, ref_w, size_w, T * x.shape[1], what + " weight")
+            again = api.qk_norm_rope_backward(dq, dk, q, k, rotary, pos, wq, wk, 1e-5, interleaved)
+            assert all(a is b is None or torch.equal(a, b) for a, b in zip(back, again))  # a fixed order
+            # In place, both ways.
+            q2, k2 = q.clone(), k.clone()
+            api.qk_norm_rope(q2, k2, rotary, pos, wq, wk, 1e-5, interleaved, out=(q2, k2))
+            assert torch.equal(q2[mine], got[0][mine]) and torch.equal(k2[mine], got[1][mine])
+            assert torch.equal(q2[~mine], q[~mine])
+            api.qk_norm_rope_backward(dq, dk, q, k, rotary, pos, wq, wk, 1e-5, interleaved, grads=(dq, dk))
+            assert torch.equal(dq, back[0]) and torch.equal(dk, back[1])
+
+
+def test_one_weight_of_two_and_rows_of_zeros():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, rotary, pos, wq, wk = make(40, 6, 2, 128, 64, weights=True)
+    q = q.clone()
+    q[3] = 0
+    dq, dk = torch.ones_like(q), torch.ones_like(k)
+    for a, b in ((wq, None), (None, wk)):
+        y = api.qk_norm_rope(q, k, rotary, pos, a, b)
+        back = api.qk_norm_rope_backward(dq, dk, q, k, rotary, pos, a, b)
+        mine = R.live(pos, rotary)
+        for i, (x, w, dy) in enumerate(((q, a, dq), (k, b, dk))):
+            ref, size = R.forward(x, w, 1e-6, rotary, pos, False)
+            R.check(y[i][mine], ref[mine], size[mine])
+            ref, size, ref_w, size_w = R.backward(dy, x, w, 1e-6, rotary, pos, False)
+            R.check(back[i], ref, size)
+            assert (back[2 + i] is None) == (w is None)
+            if w is not None:
+                R.check_weight(back[2 + i], ref_w, size_w, 240)
+    # eps = 0: tokens without a position, and steps that are not full, put no NaN into a sum.
+    back = api.qk_norm_rope_backward(dq[:, :5], dk, q[:, :5].clone().fill_(1), k, rotary, pos, wq, wk, 0.0)
+    assert all(bool(torch.isfinite(t).all()) for t in back)
+
+
+def test_far_positions_and_large_magnitudes():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, _, _, wq, wk = make(64, 4, 2, 128, 128)
+    rotary = R.table(1 << 20, 128, device="cuda:0")
+    pos = torch.arange((1 << 20) - 64, 1 << 20, device="cuda:0", dtype=torch.int32)
+    for scale in (2.0 ** -60, 1.0, 2.0 ** 60):
+        x, z = q * scale, k * scale
+        y = api.qk_norm_rope(x, z, rotary, pos, wq, wk, 0.0)
+        for got, t, w in zip(y, (x, z), (wq, wk)):
+            ref, size = R.forward(t, w, 0.0, rotary, pos, False)
+            R.check(got, ref, size, f"scale {scale}")
+
+
+def test_strides_empty_calls_and_tables_without_rows():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, rotary, pos, wq, wk = make(50, 6, 3, 96, 96, loose=False)
+    heads_first = q.transpose(0, 1).contiguous().transpose(0, 1)
+    one = k[:, :1].expand(-1, 3, -1)  # a broadcast head
+    y, z = api.qk_norm_rope(heads_first, one, rotary, pos, wq, wk)
+    y2, z2 = api.qk_norm_rope(q.contiguous(), one.contiguous(), rotary, pos, wq, wk)
+    assert torch.equal(y, y2) and torch.equal(z, z2)
+    wide = torch.zeros((50, 6, 160), dtype=torch.bfloat16, device="cuda:0")
+    api.qk_norm_rope(q, k, rotary, pos, wq, wk, out=(wide[..., 8:104], torch.empty_like(k)))
+    assert torch.equal(wide[..., 8:104], y2) and not bool(wide[..., :8].any()) and not bool(wide[..., 104:].any())
+    # No tokens, no heads, no positions.
+    none = api.qk_norm_rope_backward(q[:0], k[:0], q[:0], k[:0], rotary, pos[:0], wq, wk)
+    assert none[0].shape == (0, 6, 96) and not bool(none[2].any()) and not bool(none[3].any())
+    assert api.qk_norm_rope(q[:0], k[:0], rotary, pos[:0])[0].shape == (0, 6, 96)
+    y, z = api.qk_norm_rope(q[:, :0], k, rotary, pos, wq, wk)
+    assert y.shape == (50, 0, 96) and torch.equal(z, api.qk_norm_rope(q, k, rotary, pos, wq, wk)[1])
+    y, _ = api.qk_norm_rope(q, k, rotary[:0], pos, out=(torch.zeros_like(q), torch.zeros_like(k)))
+    assert not bool(y.any())
+
+
+# ------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("d", DIMS)
+def test_append_is_rotation_then_store(d):
+    """The same bits as qk_norm_rope and kv4_store one after the other, in every layout."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    for n, (T, H, Hkv, page) in enumerate([(1, 1, 1, 16), (7, 8, 2, 64), (64, 32, 8, 64), (33, 5, 3, 32), (2500, 7, 1, 128),
+                                           (1200, 12, 4, 16)]):
+        for weights in (True, False):
+            turned, interleaved = (d, 32, d - 32, 0)[(n + weights) % 4], bool(n & 1)
+            q, k, rotary, pos, wq, wk, v = make(T, H, Hkv, d, turned, seed=n, weights=weights, value=True)
+            pages = -(-T // page) + 3
+            g = torch.Generator(device="cuda:0").manual_seed(n)
+            slots = torch.randperm(pages * page, generator=g, device="cuda:0")[:T].contiguous()
+            if T > 6:
+                slots[2], slots[3] = -1, pages * page
+            one, two = (api.KV4Cache.empty(pages, Hkv, page, d, 2.0 ** -6, 2.0 ** -7) for _ in range(2))
+            mark = dict(out=torch.full(q.shape, 7.0, device="cuda:0").to(torch.bfloat16),
+                        k_out=torch.full(k.shape, 7.0, device="cuda:0").to(torch.bfloat16))
+            y = api.kv4_append(q, k, v, rotary, pos, slots, one, wq, wk, 1e-5, interleaved, **mark)
+            assert y is mark["out"]
+            ref = api.qk_norm_rope(q, k, rotary, pos, wq, wk, 1e-5, interleaved,
+                                   out=tuple(torch.full(t.shape, 7.0, device="cuda:0").to(torch.bfloat16) for t in (q, k)))
+            mine = R.live(pos, rotary)
+            api.kv4_store(ref[1], v, torch.where(mine, slots, -1), two)
+            what = f"T={T} {H}/{Hkv} d={d} turned={turned} weights={weights}"
+            assert torch.equal(y, ref[0]) and torch.equal(mark["k_out"], ref[1]), what
+            for a in ("k_codes", "k_scales", "v_codes", "v_scales"):
+                assert torch.equal(getattr(one, a), getattr(two, a)), f"{what} {a}"
+            # Without the keys' own rows, and in place.
+            three = api.KV4Cache.empty(pages, Hkv, page, d, 2.0 ** -6, 2.0 ** -7)
+            x = q.clone()
+            api.kv4_append(x, k, v, rotary, pos, slots, three, wq, wk, 1e-5, interleaved, out=x)
+            assert torch.equal(x[mine], y[mine]) and torch.equal(x[~mine], q[~mine])
+            assert torch.equal(three.k_codes, one.k_codes) and torch.equal(three.v_codes, one.v_codes)
+
+
+def test_append_without_queries_tokens_or_pages():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, rotary, pos, wq, wk, v = make(40, 4, 2, 128, 128, value=True, loose=False)
+    slots = torch.arange(40, device="cuda:0")
+    one, two = (api.KV4Cache.empty(4, 2, 16, 128) for _ in range(2))
+    api.kv4_append(q, k, v, rotary, pos, slots, one, wq, wk)
+    api.kv4_append(q[:, :0], k, v, rotary, pos, slots, two, wq, wk)
+    assert torch.equal(one.k_codes, two.k_codes) and torch.equal(one.v_scales, two.v_scales)
+    assert api.kv4_append(q[:0], k[:0], v[:0], rotary, pos[:0], slots[:0], one).shape == (0, 4, 128)
+    y = api.kv4_append(q, k, v, rotary, pos, slots, api.KV4Cache.empty(0, 2, 16, 128), wq, wk)
+    assert torch.equal(y, api.qk_norm_rope(q, k, rotary, pos, wq, wk)[0])

@@ -1,7 +1,8 @@
 """GB300 (sm_103a) fused tiled attention: forward and 5-/7-GEMM backward.
 
-``binding`` exposes the C ABI of ``include/fa.h`` and ``include/fa_paged.h`` (serving:
-page tables, a paged 4-bit cache, attention over it) under the same names;
+``binding`` exposes the C ABI of ``include/fa.h``, ``include/fa_paged.h`` (serving:
+page tables, a paged 4-bit cache, attention over it) and ``include/fa_packed.h``
+(attention over packed sequences, norms and rotation) under the same names;
 ``api`` wraps it for torch tensors.  The CUDA library is loaded on first use
 and its absence is an error (there is no CPU path).
 """
@@ -16,7 +17,7 @@ from .api import attention_backward, attention_forward, check_device_error  # no
 
 
 def __getattr__(name):
-    # The serving operators and those of packed sequences: loaded on first use.
-    if name in api._SERVING or name in api._PACKED:
+    # The serving operators, those of packed sequences, norms and rotation: loaded on first use.
+    if name in api._SERVING + api._PACKED + api._ROTARY:
         return getattr(api, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -140,11 +140,18 @@ _SERVING = ("KV4Cache", "page_grow", "page_slots", "kv4_store", "kv4_load", "kv4
 _PACKED = ("packed_attention_forward", "packed_attention_backward", "packed_forward_workspace_bytes",
            "packed_backward_workspace_bytes")
 
+# Norms and rotation of queries and keys (``rotary``), likewise.
+_ROTARY = ("qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_workspace_bytes", "kv4_append")
+
 
 def __getattr__(name):
     if name in _PACKED:
         from . import packed
         globals().update({n: getattr(packed, n) for n in _PACKED})
+        return globals()[name]
+    if name in _ROTARY:
+        from . import rotary
+        globals().update({n: getattr(rotary, n) for n in _ROTARY})
         return globals()[name]
     if name in _SERVING:
         from . import serving

@@ -77,6 +77,13 @@ SIGNATURES = {
     "fa_packed_bwd": (_I, [_VP, _LL, _LL] * 5 + [_VP] + [_VP, _LL, _LL] * 3
                       + [_VP, _I, _I, _I, _I, _I, _F, _I, _I, _VP, _SZ, _VP]),
     "fa_packed_bwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "fa_qk_norm_rope": (_I, [_VP, _LL, _LL] * 2 + [_VP, _I, _I, _VP, _VP, _VP, _F, _I] + [_VP, _LL, _LL] * 2
+                        + [_I, _I, _I, _I, _VP]),
+    "fa_qk_norm_rope_bwd": (_I, [_VP, _LL, _LL] * 4 + [_VP, _I, _I, _VP, _VP, _VP, _F, _I] + [_VP, _LL, _LL] * 2
+                            + [_VP, _VP, _I, _I, _I, _I, _VP, _SZ, _VP]),
+    "fa_qk_norm_rope_bwd_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "fa_kv4_append": (_I, [_VP] + [_VP, _LL, _LL] * 3 + [_VP, _I, _I, _VP, _VP, _VP, _F, _I] + [_VP, _LL, _LL] * 2
+                      + [_VP, _I, _I, _VP]),
 }
 
 _lib = None
@@ -272,6 +279,35 @@ def fa_packed_bwd(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, o,
 
 def fa_packed_bwd_workspace_size(B, T, H, Hkv, d, variant) -> int:
     return lib().fa_packed_bwd_workspace_size(B, T, H, Hkv, d, variant)
+
+
+def fa_qk_norm_rope(q, q_token, q_head, k, k_token, k_head, rotary, positions, rot, position, q_weight, k_weight, eps,
+                    interleaved, q_out, qo_token, qo_head, k_out, ko_token, ko_head, T, H, Hkv, d, stream) -> int:
+    return lib().fa_qk_norm_rope(q, q_token, q_head, k, k_token, k_head, rotary, positions, rot, position, q_weight,
+                                 k_weight, float(eps), int(interleaved), q_out, qo_token, qo_head, k_out, ko_token,
+                                 ko_head, T, H, Hkv, d, stream)
+
+
+def fa_qk_norm_rope_bwd(dq_out, dqo_token, dqo_head, dk_out, dko_token, dko_head, q, q_token, q_head, k, k_token, k_head,
+                        rotary, positions, rot, position, q_weight, k_weight, eps, interleaved, dq, dq_token, dq_head,
+                        dk, dk_token, dk_head, dq_weight, dk_weight, T, H, Hkv, d, workspace, workspace_bytes,
+                        stream) -> int:
+    return lib().fa_qk_norm_rope_bwd(dq_out, dqo_token, dqo_head, dk_out, dko_token, dko_head, q, q_token, q_head, k,
+                                     k_token, k_head, rotary, positions, rot, position, q_weight, k_weight, float(eps),
+                                     int(interleaved), dq, dq_token, dq_head, dk, dk_token, dk_head, dq_weight,
+                                     dk_weight, T, H, Hkv, d, workspace, workspace_bytes, stream)
+
+
+def fa_qk_norm_rope_bwd_workspace_size(T, H, Hkv, d) -> int:
+    return lib().fa_qk_norm_rope_bwd_workspace_size(T, H, Hkv, d)
+
+
+def fa_kv4_append(cache, q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, rotary, positions, rot, position,
+                  q_weight, k_weight, eps, interleaved, q_out, qo_token, qo_head, k_out, ko_token, ko_head, slots, T, H,
+                  stream) -> int:
+    return lib().fa_kv4_append(cache, q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, rotary, positions,
+                               rot, position, q_weight, k_weight, float(eps), int(interleaved), q_out, qo_token,
+                               qo_head, k_out, ko_token, ko_head, slots, T, H, stream)
 
 
 FA_KERNEL_ALL_KINDS = 19

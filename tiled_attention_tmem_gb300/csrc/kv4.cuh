@@ -43,4 +43,41 @@ __device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
   return r;
 }
 
+// A quotient is taken by a reciprocal and then cut to 12 bits after a push of 2^-13:
+// where x has bf16's eight bits and the gain is a power of two, a quotient on the border
+// of two results lands on it exactly, and any other is at least 2^-8 of itself away, so
+// both scale and code are those of the exact quotient.
+constexpr float kKv4Push = 1.f + 1.f / 8192.f;
+__device__ __forceinline__ float cut12(float x) { return __uint_as_float(__float_as_uint(x) & 0xfffff000u); }
+
+// Eight bf16 channels (four words), half of a scale's group whose other half is this warp's lane ^ 1:
+// returns their codes, and the scale's byte.  All lanes call it together.
+__device__ __forceinline__ uint32_t kv4_quantise(const uint32_t* w, float inv_gain, uint32_t& scale) {
+  uint32_t pair = 0;  // (a NaN is passed over)
+#pragma unroll
+  for (int k = 0; k < 4; ++k) asm("max.bf16x2 %0, %0, %1;" : "+r"(pair) : "r"(w[k] & 0x7fff7fffu));
+  float top = fmaxf(__uint_as_float(pair << 16), __uint_as_float(pair & 0xffff0000u));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  uint16_t sb;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.f), "f"(cut12(top * inv_gain * (kKv4Push / 6.f))));
+  scale = sb & 0xffu;
+  // e4m3 to fp32 by way of f16 (2^-8 of the scale; exact).
+  const float sf = __half2float(__ushort_as_half((unsigned short)((scale & 0x7f) << 7))) * kKv4ScaleBias;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sf));
+  const float mul = sf > 0.f ? inv * inv_gain * kKv4Push : 0.f;
+  uint32_t q[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float lo = cut12(__uint_as_float(w[k] << 16) * mul);
+    const float hi = cut12(__uint_as_float(w[k] & 0xffff0000u) * mul);
+    asm("{\n\t.reg .b8 x;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 x, %1, %2;\n\t"
+        "cvt.u32.u8 %0, x;\n\t}"
+        : "=r"(q[k])
+        : "f"(hi), "f"(lo));
+  }
+  return q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
+}
+
 }  // namespace fa

@@ -1,0 +1,538 @@
+// Norms and rotation of queries and keys, per head and in one pass: for training with
+// their gradients, for serving on the way into the paged 4-bit cache.
+//
+//   r = (mean_c x_c^2 + eps)^-1/2,  n_c = x_c r w_c
+//   pair (a, b) of channels:  y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin
+// with pairs (i, i + rot/2) or (2i, 2i + 1) of the first rot channels; the others are n.
+//
+// Lanes: a head's d channels are d/8 chunks of 16 bytes.  Lane u of the d/16 of a head
+// holds chunks u and u + rot/16 (of the channels behind rot: chunk j and the one half of them on), so both
+// members of every pair are its own, in either pairing, and the rotation needs no
+// shuffle; chunk ^ 1, the other half of a 4-bit scale's group, is lane ^ 1's (rot is a multiple of
+// 32).  A head's lanes are padded to a power of two for the sums of its squares.
+// A warp takes one token and U times 32 lanes of its heads, all loads first, with the
+// token's cosines and sines in registers: what bounds the passes is memory.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "fa_packed.h"
+#include "kv4.cuh"
+#include "kv4_host.h"
+
+namespace fa {
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+struct HeadRows {
+  const uint16_t* in;
+  uint16_t* out;  // (NULL: not wanted)
+  long long in_token, in_head, out_token, out_head;
+  const uint16_t* weight;  // bf16 [d], or NULL: no norm
+  int heads;
+};
+
+struct RotateParams {
+  HeadRows x[3];  // q, k, and (append) v, which is neither normed nor turned
+  const float* rotary;  // [positions, rot]: cosines, then sines
+  const int* position;
+  int positions, rot, T;
+  float eps;
+  // Append to the 4-bit cache: of k and v.
+  uint8_t* codes[2];
+  uint8_t* scales[2];
+  const long long* slots;
+  float inv_gain[2];
+  int page_log2;
+  long long slot_end;
+};
+
+template <int D>
+struct HeadLanes {
+  static constexpr int LANES = D / 16;
+  static constexpr int GROUP = LANES <= 4 ? 4 : LANES <= 8 ? 8 : LANES <= 16 ? 16 : 32;
+  static constexpr int ROWS = 32 / GROUP;  // heads a warp takes at a time
+  int u, chunk[2];
+  bool active, turned;
+  __device__ __forceinline__ explicit HeadLanes(int rot) {
+    u = lane_id() % GROUP;
+    active = u < LANES;
+    const int rc = rot / 16;
+    turned = u < rc;
+    chunk[0] = turned ? u : u + rc;
+    chunk[1] = turned ? u + rc : u + LANES;
+    if (!active) chunk[0] = chunk[1] = 0;
+  }
+};
+
+__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// Cosines and sines of a lane's eight pairs.
+template <int D, bool NEXT>
+__device__ __forceinline__ void load_angles(const HeadLanes<D>& at, const float* row, int rot, float* c, float* s) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = NEXT ? 4 * at.chunk[h] : 8 * at.u + 4 * h;
+    const float4 a = *reinterpret_cast<const float4*>(row + i);
+    const float4 b = *reinterpret_cast<const float4*>(row + rot / 2 + i);
+    c[4 * h] = a.x, c[4 * h + 1] = a.y, c[4 * h + 2] = a.z, c[4 * h + 3] = a.w;
+    s[4 * h] = b.x, s[4 * h + 1] = b.y, s[4 * h + 2] = b.z, s[4 * h + 3] = b.w;
+  }
+}
+
+// Turns a lane's 16 channels (two chunks of 8) by the angles, or back.  Each product and sum is
+// rounded on its own, in this order, so that the result does not depend on how they are fused.
+template <bool NEXT, bool BACK>
+__device__ __forceinline__ void turn(float* x, const float* c, const float* s) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float& a = NEXT ? x[8 * (i / 4) + 2 * (i % 4)] : x[i];
+    float& b = NEXT ? x[8 * (i / 4) + 2 * (i % 4) + 1] : x[8 + i];
+    const float ac = __fmul_rn(a, c[i]), bs = __fmul_rn(b, s[i]), bc = __fmul_rn(b, c[i]), as = __fmul_rn(a, s[i]);
+    a = BACK ? __fadd_rn(ac, bs) : __fsub_rn(ac, bs);
+    b = BACK ? __fsub_rn(bc, as) : __fadd_rn(bc, as);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ float head_sum(float v) {
+#pragma unroll
+  for (int d = HeadLanes<D>::GROUP / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// blockIdx.x: eight tokens, one a warp; blockIdx.y: U steps of ROWS heads, those of q, then k, then v.
+template <int D, bool NEXT, bool APPEND, int U>
+__global__ void __launch_bounds__(256) rotate_kernel(const __grid_constant__ RotateParams p) {
+  using L = HeadLanes<D>;
+  grid_dep_wait();
+  const int tok = blockIdx.x * 8 + warp_id();
+  if (tok >= p.T) return;
+  const int pos = p.position[tok];
+  if (pos < 0 || pos >= p.positions) return;  // a token without a position is left out
+  const L at(p.rot);
+  const int first = blockIdx.y * U * L::ROWS + lane_id() / L::GROUP;
+  const int hq = p.x[0].heads, hk = hq + p.x[1].heads, hv = hk + (APPEND ? p.x[2].heads : 0);
+  uint4 raw[U][2];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int row = first + i * L::ROWS;
+    const int kind = row < hq ? 0 : row < hk ? 1 : 2;
+    const int head = row - (kind == 0 ? 0 : kind == 1 ? hq : hk);
+    raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (at.active && row < hv) {
+      const uint16_t* src = p.x[kind].in + tok * p.x[kind].in_token + head * p.x[kind].in_head;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) raw[i][h] = *reinterpret_cast<const uint4*>(src + 8 * at.chunk[h]);
+    }
+  }
+  float c[8], s[8];
+  if (at.turned) load_angles<D, NEXT>(at, p.rotary + (long long)pos * p.rot, p.rot, c, s);
+  long long slot = -1;
+  if constexpr (APPEND) slot = p.slots[tok];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int row = first + i * L::ROWS;
+    const int kind = row < hq ? 0 : row < hk ? 1 : 2;
+    const int head = row - (kind == 0 ? 0 : kind == 1 ? hq : hk);
+    const bool have = at.active && row < hv;
+    uint4 out[2] = {raw[i][0], raw[i][1]};
+    const uint16_t* weight = kind < 2 ? p.x[kind].weight : nullptr;
+    float x[16];
+    unpack8(raw[i][0], x);
+    unpack8(raw[i][1], x + 8);
+    // (Both kinds' weights may be wanted by one warp, so all of its lanes sum where one does.)
+    if (p.x[0].weight != nullptr || p.x[1].weight != nullptr) {
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
+      sum = head_sum<D>(sum);
+      if (weight != nullptr) {
+        const float r = rsqrtf(sum * (1.f / D) + p.eps);
+        float w[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) unpack8(*reinterpret_cast<const uint4*>(weight + 8 * at.chunk[h]), w + 8 * h);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
+      }
+    }
+    if (kind < 2) {
+      if (at.turned) turn<NEXT, false>(x, c, s);
+      out[0] = pack8(x), out[1] = pack8(x + 8);
+      if (have && p.x[kind].out != nullptr) {
+        uint16_t* dst = p.x[kind].out + tok * p.x[kind].out_token + head * p.x[kind].out_head;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(dst + 8 * at.chunk[h]) = out[h];
+      }
+    }
+    if constexpr (APPEND) {
+      const int kv = kind == 2 ? 1 : 0;
+      const bool store = have && kind > 0 && slot >= 0 && slot < p.slot_end;
+      const long long cell = (((slot >> p.page_log2) * p.x[1].heads + head) << p.page_log2) +
+                             (slot & ((1 << p.page_log2) - 1));
+      // (Steps of queries alone have nothing to store.)
+      if (first - (int)(lane_id() / L::GROUP) + (i + 1) * L::ROWS > hq) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w[4] = {out[h].x, out[h].y, out[h].z, out[h].w};
+          uint32_t scale;
+          const uint32_t codes = kv4_quantise(w, p.inv_gain[kv], scale);
+          if (store) {
+            *reinterpret_cast<uint32_t*>(p.codes[kv] + cell * (D / 2) + at.chunk[h] * 4) = codes;
+            if (!(at.u & 1)) p.scales[kv][cell * (D / 16) + (at.chunk[h] >> 1)] = (uint8_t)scale;
+          }
+        }
+      }
+    }
+  }
+}
+
+// Gradients.  With g = R^T dy, z = w g and xhat = x r:
+//   dx = r (z - xhat mean_c(xhat z)),  dw = sum over tokens and heads of g xhat
+struct RotateBwdParams {
+  HeadRows dy[2], x[2];  // dy: in the gradient of the result, out the gradient of x; x: in the pass's input
+  const float* rotary;
+  const int* position;
+  int positions, rot, T;
+  float eps;
+  int q_blocks;  // blocks of the grid that take q; the others take k
+  float* part;   // [blocks][d]: each block's sum of g xhat (NULL: no weights)
+};
+
+constexpr int kRotateBack = 4;  // steps of heads a warp loads at a time
+
+// A block takes q or k; its warps walk tokens (and runs of U steps of heads), keeping the weight's
+// gradient of their channels in registers.  Tokens without a position have a gradient of zero.
+template <int D, bool NEXT>
+__global__ void __launch_bounds__(256) rotate_bwd_kernel(const __grid_constant__ RotateBwdParams p) {
+  using L = HeadLanes<D>;
+  constexpr int U = kRotateBack;
+  __shared__ float sums[8][D];
+  grid_dep_wait();
+  const L at(p.rot);
+  const int warp = warp_id();  // (a shuffle of the whole warp: never inside a branch)
+  const int kind = (int)blockIdx.x < p.q_blocks ? 0 : 1;
+  const int block = kind ? blockIdx.x - p.q_blocks : blockIdx.x, blocks = kind ? gridDim.x - p.q_blocks : p.q_blocks;
+  const HeadRows &gy = p.dy[kind], &xx = p.x[kind];
+  const int runs = (gy.heads + U * L::ROWS - 1) / (U * L::ROWS);
+  float w[16], dw[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = 1.f, dw[e] = 0.f;
+  if (xx.weight != nullptr) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) unpack8(*reinterpret_cast<const uint4*>(xx.weight + 8 * at.chunk[h]), w + 8 * h);
+  }
+  const long long work = (long long)p.T * runs;
+  for (long long job = (long long)block * 8 + warp; job < work; job += (long long)blocks * 8) {
+    const int tok = (int)(job / runs), run = (int)(job - (long long)tok * runs);
+    const int first = run * U * L::ROWS + lane_id() / L::GROUP;
+    const int pos = p.position[tok];
+    const bool live = pos >= 0 && pos < p.positions;
+    uint4 rg[U][2], rx[U][2];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int head = first + i * L::ROWS;
+      const bool have = at.active && live && head < gy.heads;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        rg[i][h] = rx[i][h] = make_uint4(0u, 0u, 0u, 0u);
+        if (have) {
+          rg[i][h] = *reinterpret_cast<const uint4*>(gy.in + tok * gy.in_token + head * gy.in_head + 8 * at.chunk[h]);
+          if (xx.weight != nullptr)
+            rx[i][h] = *reinterpret_cast<const uint4*>(xx.in + tok * xx.in_token + head * xx.in_head + 8 * at.chunk[h]);
+        }
+      }
+    }
+    float c[8], s[8];
+    if (at.turned && live) load_angles<D, NEXT>(at, p.rotary + (long long)pos * p.rot, p.rot, c, s);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int head = first + i * L::ROWS;
+      float g[16];
+      unpack8(rg[i][0], g);
+      unpack8(rg[i][1], g + 8);
+      if (at.turned && live) turn<NEXT, true>(g, c, s);
+      if (xx.weight != nullptr) {
+        float x[16], sum = 0.f, dot = 0.f;
+        unpack8(rx[i][0], x);
+        unpack8(rx[i][1], x + 8);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          sum = fmaf(x[e], x[e], sum);
+          dot = fmaf(x[e], g[e] * w[e], dot);
+        }
+        sum = head_sum<D>(sum);
+        dot = head_sum<D>(dot);
+        // (a row that is not there must not turn eps = 0 into 0 * inf)
+        const float r = live && head < gy.heads ? rsqrtf(sum * (1.f / D) + p.eps) : 0.f;
+        const float m = dot * r * (1.f / D);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float unit = x[e] * r;
+          dw[e] = fmaf(g[e], unit, dw[e]);
+          g[e] = r * (g[e] * w[e] - unit * m);
+        }
+      }
+      if (at.active && head < gy.heads) {
+        uint16_t* dst = gy.out + tok * gy.out_token + head * gy.out_head;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(dst + 8 * at.chunk[h]) = pack8(g + 8 * h);
+      }
+    }
+  }
+  if (p.part == nullptr) return;
+  // The lanes that hold the same channels, then the warps, in a fixed order.
+#pragma unroll
+  for (int d = L::GROUP; d < 32; d <<= 1)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], d);
+  if (lane_id() < L::GROUP && at.active)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sums[warp][8 * at.chunk[e >> 3] + (e & 7)] = dw[e];
+  __syncthreads();
+  for (int e = threadIdx.x; e < D; e += 256) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += sums[i][e];
+    p.part[(long long)blockIdx.x * D + e] = v;
+  }
+}
+
+struct RotateSumParams {
+  const float* part;
+  float* out[2];
+  int q_blocks, blocks, d;
+};
+
+// A weight's gradient: the blocks' sums, 32 columns a block (blockIdx.x) of q or k (blockIdx.y), each of 32 rows
+// of threads adding every 32nd, in a fixed order.  Latency bounds it.
+__global__ void __launch_bounds__(1024) rotate_sum_kernel(const __grid_constant__ RotateSumParams p) {
+  __shared__ float sums[32][33];
+  grid_dep_wait();
+  const int kind = blockIdx.y, col = blockIdx.x * 32 + threadIdx.x % 32, row = threadIdx.x / 32;
+  if (p.out[kind] == nullptr) return;
+  const int b0 = kind ? p.q_blocks : 0, b1 = kind ? p.blocks : p.q_blocks;
+  float v = 0.f;
+  for (int b = b0 + row; b < b1; b += 32) v += p.part[(long long)b * p.d + col];
+  sums[row][threadIdx.x % 32] = v;
+  __syncthreads();
+  if (row == 0) {
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) total += sums[i][threadIdx.x];
+    p.out[kind][col] = total;
+  }
+}
+
+struct Rows {
+  const void* data;
+  long long token, head;
+};
+
+fa_status rows_checks(const Rows& r, int heads) {
+  if (heads == 0) return FA_OK;
+  if (!r.data) return FA_ERR_INVALID_ARG;
+  return aligned16(r.data) && !(r.token & 7) && !(r.head & 7) ? FA_OK : FA_ERR_MISALIGNED;
+}
+
+fa_status rotary_checks(const float* rotary, int positions, int rot, const int* position, const void* q_weight,
+                        const void* k_weight, float eps, int interleaved, int T, int H, int Hkv, int d) {
+  if (T < 0 || H < 0 || Hkv < 0 || positions < 0 || rot < 0 || (interleaved != 0 && interleaved != 1))
+    return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.f) return FA_ERR_INVALID_ARG;
+  if (padded_head_dim(d) == 0) return FA_ERR_UNSUPPORTED;
+  if (rot > d || rot % 32 != 0) return FA_ERR_UNSUPPORTED;
+  if (T > (1 << 30) || (long long)H + 2LL * Hkv > 65535) return FA_ERR_INVALID_ARG;
+  if (T == 0 || H + Hkv == 0) return FA_OK;
+  if (!position || (rot > 0 && positions > 0 && !rotary)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(rotary) || !aligned16(q_weight) || !aligned16(k_weight) || !all_aligned(4, position))
+    return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+HeadRows head_rows(const Rows& in, const Rows& out, const void* weight, int heads) {
+  return {static_cast<const uint16_t*>(in.data), static_cast<uint16_t*>(const_cast<void*>(out.data)), in.token, in.head,
+          out.token, out.head, static_cast<const uint16_t*>(weight), heads};
+}
+
+// Steps of heads a warp: four where that leaves 32 warps an SM, else one.
+template <int D, bool NEXT, bool APPEND>
+fa_status run_rotate(const RotateParams& p, cudaStream_t st) {
+  constexpr int ROWS = HeadLanes<D>::ROWS;
+  const int heads = p.x[0].heads + p.x[1].heads + (APPEND ? p.x[2].heads : 0);
+  const int steps = (heads + ROWS - 1) / ROWS;
+  const int kind = APPEND ? FA_KERNEL_KV4_APPEND : FA_KERNEL_ROTATE;
+  const unsigned gx = (unsigned)((p.T + 7) / 8);
+  if ((long long)p.T * ((steps + 3) / 4) >= 32LL * sm_count_cached())
+    return launch(kind, rotate_kernel<D, NEXT, APPEND, 4>, dim3(gx, (steps + 3) / 4), dim3(256), 0, st, p);
+  return launch(kind, rotate_kernel<D, NEXT, APPEND, 1>, dim3(gx, steps), dim3(256), 0, st, p);
+}
+
+template <bool APPEND>
+fa_status rotate_by_dim(const RotateParams& p, int d, int interleaved, cudaStream_t st) {
+  switch (d) {
+    case 64: return interleaved ? run_rotate<64, true, APPEND>(p, st) : run_rotate<64, false, APPEND>(p, st);
+    case 96: return interleaved ? run_rotate<96, true, APPEND>(p, st) : run_rotate<96, false, APPEND>(p, st);
+    case 128: return interleaved ? run_rotate<128, true, APPEND>(p, st) : run_rotate<128, false, APPEND>(p, st);
+    case 192: return interleaved ? run_rotate<192, true, APPEND>(p, st) : run_rotate<192, false, APPEND>(p, st);
+    case 256: return interleaved ? run_rotate<256, true, APPEND>(p, st) : run_rotate<256, false, APPEND>(p, st);
+    case 384: return interleaved ? run_rotate<384, true, APPEND>(p, st) : run_rotate<384, false, APPEND>(p, st);
+  }
+  return FA_ERR_UNSUPPORTED;
+}
+
+constexpr int kRotateBlocks = 4;  // blocks an SM of the gradients' kernel
+
+int rotate_bwd_blocks(int T, int H, int Hkv) {
+  const long long most = ((long long)T * (H + Hkv) + 7) / 8;  // no more than rows
+  return (int)std::max(2LL, std::min<long long>(most, (long long)kRotateBlocks * sm_count_cached()));
+}
+
+template <int D, bool NEXT>
+fa_status run_rotate_bwd(RotateBwdParams p, int blocks, float* dwq, float* dwk, cudaStream_t st) {
+  fa_status s = launch(FA_KERNEL_ROTATE_BWD, rotate_bwd_kernel<D, NEXT>, dim3(blocks), dim3(256), 0, st, p);
+  if (s != FA_OK || p.part == nullptr) return s;
+  const RotateSumParams q = {p.part, {dwq, dwk}, p.q_blocks, blocks, D};
+  return launch(FA_KERNEL_ROTATE_SUM, rotate_sum_kernel, dim3(D / 32, 2), dim3(1024), 0, st, q);
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_qk_norm_rope(const void* q, long long q_token, long long q_head, const void* k, long long k_token,
+                          long long k_head, const float* rotary, int positions, int rot, const int* position,
+                          const void* q_weight, const void* k_weight, float eps, int interleaved, void* q_out,
+                          long long qo_token, long long qo_head, void* k_out, long long ko_token, long long ko_head,
+                          int T, int H, int Hkv, int d, void* stream) {
+  fa_status s = rotary_checks(rotary, positions, rot, position, q_weight, k_weight, eps, interleaved, T, H, Hkv, d);
+  if (s != FA_OK) return s;
+  if (T == 0 || H + Hkv == 0) return FA_OK;
+  const Rows rq = {q, q_token, q_head}, rk = {k, k_token, k_head}, oq = {q_out, qo_token, qo_head},
+             ok = {k_out, ko_token, ko_head};
+  for (const Rows* r : {&rq, &oq})
+    if ((s = rows_checks(*r, H)) != FA_OK) return s;
+  for (const Rows* r : {&rk, &ok})
+    if ((s = rows_checks(*r, Hkv)) != FA_OK) return s;
+  RotateParams p = {};
+  p.x[0] = head_rows(rq, oq, q_weight, H);
+  p.x[1] = head_rows(rk, ok, k_weight, Hkv);
+  p.rotary = rotary, p.position = position, p.positions = positions, p.rot = rot, p.T = T, p.eps = eps;
+  return rotate_by_dim<false>(p, d, interleaved, (cudaStream_t)stream);
+}
+
+fa_status fa_kv4_append(const fa_kv4_cache* cache, const void* q, long long q_token, long long q_head, const void* k,
+                        long long k_token, long long k_head, const void* v, long long v_token, long long v_head,
+                        const float* rotary, int positions, int rot, const int* position, const void* q_weight,
+                        const void* k_weight, float eps, int interleaved, void* q_out, long long qo_token,
+                        long long qo_head, void* k_out, long long ko_token, long long ko_head, const long long* slots,
+                        int T, int H, void* stream) {
+  fa_status s = kv4_cache_checks(cache);
+  if (s != FA_OK) return s;
+  const int Hkv = cache->Hkv;
+  s = rotary_checks(rotary, positions, rot, position, q_weight, k_weight, eps, interleaved, T, H, Hkv, cache->d);
+  if (s != FA_OK) return s;
+  if (T == 0 || H + Hkv == 0) return FA_OK;
+  const Rows rq = {q, q_token, q_head}, rk = {k, k_token, k_head}, rv = {v, v_token, v_head},
+             oq = {q_out, qo_token, qo_head}, ok = {k_out, ko_token, ko_head};
+  for (const Rows* r : {&rq, &oq})
+    if ((s = rows_checks(*r, H)) != FA_OK) return s;
+  for (const Rows* r : {&rk, &rv})
+    if ((s = rows_checks(*r, Hkv)) != FA_OK) return s;
+  if (k_out && (s = rows_checks(ok, Hkv)) != FA_OK) return s;
+  if (!slots) return FA_ERR_INVALID_ARG;
+  if (!all_aligned(8, slots)) return FA_ERR_MISALIGNED;
+  RotateParams p = {};
+  p.x[0] = head_rows(rq, oq, q_weight, H);
+  p.x[1] = head_rows(rk, ok, k_weight, Hkv);
+  p.x[2] = head_rows(rv, {}, nullptr, Hkv);
+  p.rotary = rotary, p.position = position, p.positions = positions, p.rot = rot, p.T = T, p.eps = eps;
+  p.codes[0] = static_cast<uint8_t*>(cache->k_codes), p.codes[1] = static_cast<uint8_t*>(cache->v_codes);
+  p.scales[0] = static_cast<uint8_t*>(cache->k_scales), p.scales[1] = static_cast<uint8_t*>(cache->v_scales);
+  p.slots = slots;
+  p.inv_gain[0] = 1.f / cache->k_gain, p.inv_gain[1] = 1.f / cache->v_gain;
+  p.page_log2 = page_log2_of(cache->page);
+  p.slot_end = (long long)cache->pages * cache->page;
+  return rotate_by_dim<true>(p, cache->d, interleaved, (cudaStream_t)stream);
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_size(int T, int H, int Hkv, int d) {
+  if (T <= 0 || H < 0 || Hkv < 0 || H + (long long)Hkv == 0 || padded_head_dim(d) == 0) return 0;
+  return (size_t)rotate_bwd_blocks(T, H, Hkv) * d * sizeof(float);
+}
+
+fa_status fa_qk_norm_rope_bwd(const void* dq_out, long long dqo_token, long long dqo_head, const void* dk_out,
+                              long long dko_token, long long dko_head, const void* q, long long q_token,
+                              long long q_head, const void* k, long long k_token, long long k_head,
+                              const float* rotary, int positions, int rot, const int* position, const void* q_weight,
+                              const void* k_weight, float eps, int interleaved, void* dq, long long dq_token,
+                              long long dq_head, void* dk, long long dk_token, long long dk_head, float* dq_weight,
+                              float* dk_weight, int T, int H, int Hkv, int d, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  fa_status s = rotary_checks(rotary, positions, rot, position, q_weight, k_weight, eps, interleaved, T, H, Hkv, d);
+  if (s != FA_OK) return s;
+  // A weight's gradient is written where there is the weight.
+  if ((q_weight && !dq_weight) || (k_weight && !dk_weight)) return FA_ERR_INVALID_ARG;
+  if (!all_aligned(4, dq_weight, dk_weight)) return FA_ERR_MISALIGNED;
+  const bool weights = q_weight || k_weight;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (T == 0 || H + Hkv == 0) {
+    for (float* w : {q_weight ? dq_weight : nullptr, k_weight ? dk_weight : nullptr})
+      if (w) {
+        const cudaError_t e = cudaMemsetAsync(w, 0, d * sizeof(float), st);
+        if (e != cudaSuccess) return record_cuda_error(e);
+      }
+    return FA_OK;
+  }
+  const Rows gq = {dq_out, dqo_token, dqo_head}, gk = {dk_out, dko_token, dko_head}, rq = {q, q_token, q_head},
+             rk = {k, k_token, k_head}, oq = {dq, dq_token, dq_head}, ok = {dk, dk_token, dk_head};
+  for (const Rows* r : {&gq, &oq})
+    if ((s = rows_checks(*r, H)) != FA_OK) return s;
+  for (const Rows* r : {&gk, &ok})
+    if ((s = rows_checks(*r, Hkv)) != FA_OK) return s;
+  if ((q_weight && (s = rows_checks(rq, H)) != FA_OK) || (k_weight && (s = rows_checks(rk, Hkv)) != FA_OK)) return s;
+  const int blocks = rotate_bwd_blocks(T, H, Hkv);
+  if (weights && (!workspace || !all_aligned(256, static_cast<char*>(workspace)) ||
+                  workspace_bytes < (size_t)blocks * d * sizeof(float)))
+    return FA_ERR_WORKSPACE;
+  RotateBwdParams p = {};
+  p.dy[0] = head_rows(gq, oq, nullptr, H);
+  p.dy[1] = head_rows(gk, ok, nullptr, Hkv);
+  p.x[0] = head_rows(rq, {}, q_weight, H);
+  p.x[1] = head_rows(rk, {}, k_weight, Hkv);
+  p.rotary = rotary, p.position = position, p.positions = positions, p.rot = rot, p.T = T, p.eps = eps;
+  // Blocks by the bytes of each: a head costs more where it has a norm, whose input is read.
+  const double wq = H * (q_weight ? 3.0 : 2.0), wk = Hkv * (k_weight ? 3.0 : 2.0);
+  p.q_blocks = std::min(blocks - 1, std::max(1, (int)std::lround(blocks * wq / (wq + wk))));
+  p.part = weights ? static_cast<float*>(workspace) : nullptr;
+  float *const wq_out = q_weight ? dq_weight : nullptr, *const wk_out = k_weight ? dk_weight : nullptr;
+  const auto run = [&](auto next) -> fa_status {
+    constexpr bool NEXT = decltype(next)::value;
+    switch (d) {
+      case 64: return run_rotate_bwd<64, NEXT>(p, blocks, wq_out, wk_out, st);
+      case 96: return run_rotate_bwd<96, NEXT>(p, blocks, wq_out, wk_out, st);
+      case 128: return run_rotate_bwd<128, NEXT>(p, blocks, wq_out, wk_out, st);
+      case 192: return run_rotate_bwd<192, NEXT>(p, blocks, wq_out, wk_out, st);
+      case 256: return run_rotate_bwd<256, NEXT>(p, blocks, wq_out, wk_out, st);
+      case 384: return run_rotate_bwd<384, NEXT>(p, blocks, wq_out, wk_out, st);
+    }
+    return FA_ERR_UNSUPPORTED;
+  };
+  return interleaved ? run(std::true_type{}) : run(std::false_type{});
+}
+
+}  // extern "C"

@@ -214,13 +214,6 @@ struct Kv4Piece {
   }
 };
 
-// A quotient is taken by a reciprocal and then cut to 12 bits after a push of 2^-13:
-// where x has bf16's eight bits and the gain is a power of two, a quotient on the border
-// of two results lands on it exactly, and any other is at least 2^-8 of itself away, so
-// both scale and code are those of the exact quotient.
-constexpr float kKv4Push = 1.f + 1.f / 8192.f;
-__device__ __forceinline__ float cut12(float x) { return __uint_as_float(__float_as_uint(x) & 0xfffff000u); }
-
 // Two lanes per group of 16 channels, which share its scale; keys and values, and U
 // tokens a warp, together: what bounds it is the latency of a slot and then the rows,
 // and then reading (2 bytes in for 0.5625 out) and the ALU pipe (68 % used): 16384 tokens of 8
@@ -250,35 +243,10 @@ __global__ void __launch_bounds__(256) kv4_store_kernel(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
-      uint32_t pair = 0;  // (a NaN is passed over)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) asm("max.bf16x2 %0, %0, %1;" : "+r"(pair) : "r"(w[k] & 0x7fff7fffu));
-      float top = fmaxf(__uint_as_float(pair << 16), __uint_as_float(pair & 0xffff0000u));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      uint16_t sb;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-          : "=h"(sb)
-          : "f"(0.f), "f"(cut12(top * p.inv_gain[i] * (kKv4Push / 6.f))));
-      const uint32_t s = sb & 0xffu;
-      // e4m3 to fp32 by way of f16 (2^-8 of the scale; exact).
-      const float sf = __half2float(__ushort_as_half((unsigned short)((s & 0x7f) << 7))) * kKv4ScaleBias;
-      float inv;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sf));
-      const float mul = sf > 0.f ? inv * p.inv_gain[i] * kKv4Push : 0.f;
-      uint32_t q[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float lo = cut12(__uint_as_float(w[k] << 16) * mul);
-        const float hi = cut12(__uint_as_float(w[k] & 0xffff0000u) * mul);
-        asm("{\n\t.reg .b8 x;\n\t"
-            "cvt.rn.satfinite.e2m1x2.f32 x, %1, %2;\n\t"
-            "cvt.u32.u8 %0, x;\n\t}"
-            : "=r"(q[k])
-            : "f"(hi), "f"(lo));
-      }
+      uint32_t s;
+      const uint32_t codes = kv4_quantise(w, p.inv_gain[i], s);
       if (row >= 0) {
-        *reinterpret_cast<uint32_t*>(p.codes[i] + row * (D / 2) + at.run * 4) =
-            q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
+        *reinterpret_cast<uint32_t*>(p.codes[i] + row * (D / 2) + at.run * 4) = codes;
         if (!(at.run & 1)) p.scales[i][row * (D / 16) + (at.run >> 1)] = (uint8_t)s;
       }
     }
