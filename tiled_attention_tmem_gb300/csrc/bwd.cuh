@@ -332,7 +332,7 @@ struct BwdKVCfg {
                        B_DQFREE = B_DQFULL + 1, B_STGFREE = B_DQFREE + 1, B_STGFULL = B_STGFREE + 1,
                        B_SCONS = B_STGFULL + 1, B_DONE = B_SCONS + 1, B_KVEMPTY = B_DONE + 1,
                        B_ITEMFULL = B_KVEMPTY + 1, B_ITEMEMPTY = B_ITEMFULL + 4, B_VREADY = B_ITEMEMPTY + 4,
-                       NBAR = B_VREADY + 1;
+                       B_ITEMASK = B_VREADY + 1, NBAR = B_ITEMASK + 1;
   static constexpr int IQ = 4;  // claimed work items passed from the producer to the other roles
   static_assert(kRaggedRing <= IQ, "packed sequences use the same barriers");
   // Roles that read each work item: the MMA issuing thread(s), the compute warps, the drain warps.
@@ -416,6 +416,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
     mbar_init(BAR(C::B_SCONS), 4 * C::NCW);
     mbar_init(BAR(C::B_DONE), C::EARLY ? 2 : 1);
     mbar_init(BAR(C::B_VREADY), 4 * C::NCW);
+    mbar_init(BAR(C::B_ITEMASK), 1);
     fence_mbar_init();
   }
   if constexpr (RAGGED) {
@@ -631,11 +632,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           ++published;
           return true;
         };
-        // All loads of item I, the next item being J (if there is one).
-        auto load_item = [&](const Item& I, const Item& J, bool has_next) {
-          const Maps m = maps_of(I), mj = maps_of(J);
-          int key0 = 0, next0 = 0;  // first token of each sequence
-          if constexpr (RAGGED) key0 = I.start, next0 = J.start;
+        // All loads of item I.  The next one is J where next() says so: known from the start, but (packed)
+        // asked for with the first loads and taken when its operands may go to L2.
+        auto load_item = [&](const Item& I, const Item& J, auto next) {
+          const Maps m = maps_of(I);
+          int key0 = 0;  // first token of the sequence
+          if constexpr (RAGGED) {
+            key0 = I.start;
+            mbar_arrive(BAR(C::B_ITEMASK));
+          }
           auto issue_stage = [&](int i) -> bool {
             const int s = it % QS;
             if (!wait_one(BAR(C::B_QDEMPTY + s), ((it / QS) & 1) ^ 1, ab, (kKBwdKV << 8) | 1)) return false;
@@ -662,7 +667,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
             // use); pull the tiles further ahead, into the next item, into L2.
             const int ahead = i + C::PREFETCH;
             if (ahead < I.n) prefetch_qd(I, ahead);
-            else if (has_next && ahead - I.n < J.n) prefetch_qd(J, ahead - I.n);
+            else if (next() && ahead - I.n < J.n) prefetch_qd(J, ahead - I.n);
             return true;
           };
           const int pre = min(QS - 1, I.n);
@@ -680,22 +685,35 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
               tma_load_3d(sbase + C::OFF_V + pn * C::KV_PANEL, m.v, BAR(C::B_KV), 64 * pn, key0 + I.k0, I.bh);
           }
           ++nkv;
-          if (has_next)
+          auto prefetch_kv = [&] {
+            if (!next()) return;
+            const Maps mj = maps_of(J);
+            int next0 = 0;
+            if constexpr (RAGGED) next0 = J.start;
             for (int pn = 0; pn < C::PANELS; ++pn) {
               tma_prefetch_l2_3d(mj.k, 64 * pn, next0 + J.k0, J.bh);
               tma_prefetch_l2_3d(mj.v, 64 * pn, next0 + J.k0, J.bh);
             }
+          };
+          if constexpr (!RAGGED) prefetch_kv();
           for (; ok && i < I.n; ++i) ok = issue_stage(i);
+          if constexpr (RAGGED) prefetch_kv();
         };
         if constexpr (RAGGED) {
           Item I, J;
           bool have = item_at(0, I, ByThread{});
           if (have) ready_maps(I);
           for (int t = 1; have && ok; ++t) {
-            const bool has_next = item_at(t, J, ByThread{});
-            if (has_next) ready_maps(J);
-            else J = I;
-            load_item(I, J, has_next);
+            bool taken = false, has_next = false;
+            J = I;
+            load_item(I, J, [&] {
+              if (!taken) {
+                taken = true;
+                has_next = item_at(t, J, ByThread{});
+                if (has_next) ready_maps(J);
+              }
+              return has_next;
+            });
             I = J;
             have = has_next;
           }
@@ -716,7 +734,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           if (I.n <= 0) continue;
           const bool has_next = wn < p.items;
           const Item J = has_next ? coords(wn) : I;
-          load_item(I, J, has_next);
+          load_item(I, J, [=] { return has_next; });
         }
         }
         if (nkv > 0) wait_drain_bwd(BAR(C::B_KV), (nkv - 1) & 1);
@@ -925,8 +943,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
     } else if (RAGGED && warp == 3) {
       // --------------------------------------------------------- scheduling
       if constexpr (RAGGED)
-        ragged_schedule(p.sched, C::BN, C::DSPLIT, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY), ab,
-                        (kKBwdKV << 8) | 20);
+        ragged_schedule(p.sched, C::BN, C::DSPLIT, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
+                        BAR(C::B_ITEMASK), ab, (kKBwdKV << 8) | 20);
     }
     } else if (warp < C::DRAIN_W0) {
       // ---------------------------------------------- P^T / dS^T (thread = key row)
@@ -1430,7 +1448,7 @@ struct BwdQCfg {
   static constexpr int B_QFULL = 0, B_QEMPTY = 1, B_KVFULL = 2, B_KVEMPTY = 2 + STAGES, B_SDP = 2 + 2 * STAGES,
                        B_DS = B_SDP + 1, B_DQ = B_DS + 1, B_DONE = B_DQ + 1, B_ITEMFULL = B_DONE + 1,
                        B_ITEMEMPTY = B_ITEMFULL + IQ, B_SCONS = B_ITEMEMPTY + IQ, B_DOREADY = B_SCONS + 1,
-                       NBAR = B_DOREADY + 1;
+                       B_ITEMASK = B_DOREADY + 1, NBAR = B_ITEMASK + 1;
   static constexpr int ITEM_READERS = 1 + 4;  // the MMA warp and the four compute warps
   static_assert(kRaggedRing <= IQ, "packed sequences use the same barriers");
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
@@ -1484,6 +1502,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
     }
     mbar_init(BAR(C::B_SCONS), 4);
     mbar_init(BAR(C::B_DOREADY), 4);
+    mbar_init(BAR(C::B_ITEMASK), 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -1651,7 +1670,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
               tensormap_acquire(m.k);
               tensormap_acquire(m.v);
             }
-            load_item(I, [] {});
+            if (t > 0)
+              for (int pn = 0; pn < C::PANELS; ++pn) {
+                tma_prefetch_l2_4d(maps_of(I).q, 64 * pn, 0, I.start + I.q0, I.bh);
+                tma_prefetch_l2_4d(maps_of(I).dO, 64 * pn, 0, I.start + I.q0, I.bh);
+              }
+            load_item(I, [&] { mbar_arrive(BAR(C::B_ITEMASK)); });
           }
         } else {
         int wn = atomicAdd(p.sched + 1, 1);
@@ -1809,8 +1833,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
       __syncwarp();
     } else if (RAGGED && warp == 3) {
       if constexpr (RAGGED)
-        ragged_schedule(p.sched, p.tokens, C::DQS, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY), ab,
-                        (kKBwdQ << 8) | 13);
+        ragged_schedule(p.sched, p.tokens, C::DQS, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
+                        BAR(C::B_ITEMASK), ab, (kKBwdQ << 8) | 13);
     } else if (warp >= 4) {
       const int quad = warp & 3;
       const int r = quad * 32 + lane;

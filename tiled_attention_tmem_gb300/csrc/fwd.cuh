@@ -134,7 +134,8 @@ struct FwdCfg {
                        B_SFULL = 1 + 2 * STAGES, B_PREADY = B_SFULL + NQ * SB,
                        B_OREADY = B_PREADY + NQ * SB, B_DONE = B_OREADY + NQ * SB, B_QEMPTY = B_DONE + 1,
                        B_QREADY = B_QEMPTY + 1, B_ITEMFULL = B_QREADY + 1, B_ITEMEMPTY = B_ITEMFULL + kRaggedRing,
-                       NBAR = B_ITEMEMPTY + kRaggedRing;
+                       B_ITEMASK = B_ITEMEMPTY + kRaggedRing,
+                       NBAR = B_ITEMASK + 1;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t OFF_RING = OFF_MISC + 16;  // packed sequences: claimed items
   static constexpr int ITEM_READERS = 2 + 4 * NQ;      // the producer, the MMA warp, the softmax warps
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         mbar_init(bar0 + 8 * (C::B_ITEMFULL + k), 1);
         mbar_init(bar0 + 8 * (C::B_ITEMEMPTY + k), C::ITEM_READERS);
       }
+    if constexpr (RAGGED) mbar_init(bar0 + 8 * C::B_ITEMASK, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -398,6 +400,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
               tensormap_acquire(k_map);
               tensormap_acquire(v_map);
             }
+            // (The CTA still computes the item before: this one's Q goes to L2 until there is room for it.)
+            if (r > 0)
+              for (int t = 0; t < NQ; ++t)
+                if (I.nkv[t] > 0)
+                  for (int pn = 0; pn < C::PANELS; ++pn)
+                    tma_prefetch_l2_4d(q_map, 64 * pn, 0, row0 + I.q0 + t * p.tokens, I.bh);
           }
           // This item's Q tiles: NQ x 128 rows, of which the packed ones are G rows a token.
           auto load_q = [&]() {
@@ -419,7 +427,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
           // so that its load (or, with Q in TMEM, the softmax warps' row reads)
           // at the item change is served from L2.
           auto prefetch_next_q = [&](int j) {
-            if constexpr (!RAGGED) {
+            if constexpr (RAGGED) {
+              if (j == max(0, I.nmax - C::QPF)) mbar_arrive(BAR(C::B_ITEMASK));
+            } else {
             if (j != max(0, I.nmax - C::QPF) || !is_warm()) return;
             const int w2 = item_of(r + 1);
             if (w2 >= p.items) return;
@@ -668,8 +678,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
     } else if (RAGGED && warp == 3) {
       // --------------------------------------------------------- scheduling
       if constexpr (RAGGED)
-        ragged_schedule(p.sched, NQ * p.tokens, 1, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY), ab,
-                        (kKFwd << 8) | 13);
+        ragged_schedule(p.sched, NQ * p.tokens, 1, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
+                        BAR(C::B_ITEMASK), ab, (kKFwd << 8) | 13);
     }
     } else {
       // ------------------------------------------------------------ softmax

@@ -112,80 +112,75 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// blockIdx.x: eight tokens, one a warp; blockIdx.y: U steps of ROWS heads, those of q, then k, then v.
+// blockIdx.x: eight tokens, one a warp; blockIdx.y: U steps of ROWS heads, those of q, then k, then v
+// (a step is of one kind, so what differs between the kinds is the same for a warp).
 template <int D, bool NEXT, bool APPEND, int U>
-__global__ void __launch_bounds__(256) rotate_kernel(const __grid_constant__ RotateParams p) {
+__global__ void __launch_bounds__(256, 4) rotate_kernel(const __grid_constant__ RotateParams p) {
   using L = HeadLanes<D>;
   grid_dep_wait();
   const int tok = blockIdx.x * 8 + warp_id();
   if (tok >= p.T) return;
-  const int pos = p.position[tok];
-  if (pos < 0 || pos >= p.positions) return;  // a token without a position is left out
+  const int pos = p.position[tok];  // (the rows do not wait for it)
+  long long slot = -1;
+  if constexpr (APPEND) slot = p.slots[tok];
   const L at(p.rot);
-  const int first = blockIdx.y * U * L::ROWS + lane_id() / L::GROUP;
-  const int hq = p.x[0].heads, hk = hq + p.x[1].heads, hv = hk + (APPEND ? p.x[2].heads : 0);
+  const int sub = lane_id() / L::GROUP;
+  const int steps[2] = {(p.x[0].heads + L::ROWS - 1) / L::ROWS, (p.x[1].heads + L::ROWS - 1) / L::ROWS};
+  auto kind_of = [&](int step) { return step < steps[0] ? 0 : !APPEND || step < steps[0] + steps[1] ? 1 : 2; };
+  auto head_of = [&](int step, int kind) {
+    return (step - (kind > 0 ? steps[0] : 0) - (kind > 1 ? steps[1] : 0)) * L::ROWS + sub;
+  };
   uint4 raw[U][2];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int row = first + i * L::ROWS;
-    const int kind = row < hq ? 0 : row < hk ? 1 : 2;
-    const int head = row - (kind == 0 ? 0 : kind == 1 ? hq : hk);
-    raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (at.active && row < hv) {
-      const uint16_t* src = p.x[kind].in + tok * p.x[kind].in_token + head * p.x[kind].in_head;
+    const int step = blockIdx.y * U + i, kind = kind_of(step), head = head_of(step, kind);
+    const HeadRows& x = p.x[kind];
+    const uint16_t* src = x.in + tok * x.in_token + head * x.in_head;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) raw[i][h] = *reinterpret_cast<const uint4*>(src + 8 * at.chunk[h]);
+    for (int h = 0; h < 2; ++h) {
+      raw[i][h] = make_uint4(0u, 0u, 0u, 0u);
+      if (at.active && head < x.heads) raw[i][h] = *reinterpret_cast<const uint4*>(src + 8 * at.chunk[h]);
     }
   }
+  if (pos < 0 || pos >= p.positions) return;  // a token without a position is left out
   float c[8], s[8];
   if (at.turned) load_angles<D, NEXT>(at, p.rotary + (long long)pos * p.rot, p.rot, c, s);
-  long long slot = -1;
-  if constexpr (APPEND) slot = p.slots[tok];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int row = first + i * L::ROWS;
-    const int kind = row < hq ? 0 : row < hk ? 1 : 2;
-    const int head = row - (kind == 0 ? 0 : kind == 1 ? hq : hk);
-    const bool have = at.active && row < hv;
-    uint4 out[2] = {raw[i][0], raw[i][1]};
-    const uint16_t* weight = kind < 2 ? p.x[kind].weight : nullptr;
-    float x[16];
-    unpack8(raw[i][0], x);
-    unpack8(raw[i][1], x + 8);
-    // (Both kinds' weights may be wanted by one warp, so all of its lanes sum where one does.)
-    if (p.x[0].weight != nullptr || p.x[1].weight != nullptr) {
-      float sum = 0.f;
+    const int step = blockIdx.y * U + i, kind = kind_of(step), head = head_of(step, kind);
+    const HeadRows& row = p.x[kind];
+    const bool have = at.active && head < row.heads;
+    if (kind < 2) {
+      float x[16];
+      unpack8(raw[i][0], x);
+      unpack8(raw[i][1], x + 8);
+      if (row.weight != nullptr) {
+        float sum = 0.f, w[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
-      sum = head_sum<D>(sum);
-      if (weight != nullptr) {
-        const float r = rsqrtf(sum * (1.f / D) + p.eps);
-        float w[16];
+        for (int h = 0; h < 2; ++h) unpack8(*reinterpret_cast<const uint4*>(row.weight + 8 * at.chunk[h]), w + 8 * h);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) unpack8(*reinterpret_cast<const uint4*>(weight + 8 * at.chunk[h]), w + 8 * h);
+        for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
+        const float r = rsqrtf(head_sum<D>(sum) * (1.f / D) + p.eps);
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
       }
-    }
-    if (kind < 2) {
       if (at.turned) turn<NEXT, false>(x, c, s);
-      out[0] = pack8(x), out[1] = pack8(x + 8);
-      if (have && p.x[kind].out != nullptr) {
-        uint16_t* dst = p.x[kind].out + tok * p.x[kind].out_token + head * p.x[kind].out_head;
+      raw[i][0] = pack8(x), raw[i][1] = pack8(x + 8);
+      if (have && row.out != nullptr) {
+        uint16_t* dst = row.out + tok * row.out_token + head * row.out_head;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(dst + 8 * at.chunk[h]) = out[h];
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(dst + 8 * at.chunk[h]) = raw[i][h];
       }
     }
     if constexpr (APPEND) {
-      const int kv = kind == 2 ? 1 : 0;
-      const bool store = have && kind > 0 && slot >= 0 && slot < p.slot_end;
-      const long long cell = (((slot >> p.page_log2) * p.x[1].heads + head) << p.page_log2) +
-                             (slot & ((1 << p.page_log2) - 1));
-      // (Steps of queries alone have nothing to store.)
-      if (first - (int)(lane_id() / L::GROUP) + (i + 1) * L::ROWS > hq) {
+      if (kind > 0) {
+        const int kv = kind - 1;
+        const bool store = have && slot >= 0 && slot < p.slot_end;
+        const long long cell = (((slot >> p.page_log2) * row.heads + head) << p.page_log2) +
+                               (slot & ((1 << p.page_log2) - 1));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t w[4] = {out[h].x, out[h].y, out[h].z, out[h].w};
+          const uint32_t w[4] = {raw[i][h].x, raw[i][h].y, raw[i][h].z, raw[i][h].w};
           uint32_t scale;
           const uint32_t codes = kv4_quantise(w, p.inv_gain[kv], scale);
           if (store) {
@@ -210,12 +205,12 @@ struct RotateBwdParams {
   float* part;   // [blocks][d]: each block's sum of g xhat (NULL: no weights)
 };
 
-constexpr int kRotateBack = 4;  // steps of heads a warp loads at a time
+constexpr int kRotateBack = 2;  // steps of heads a warp loads at a time
 
 // A block takes q or k; its warps walk tokens (and runs of U steps of heads), keeping the weight's
 // gradient of their channels in registers.  Tokens without a position have a gradient of zero.
 template <int D, bool NEXT>
-__global__ void __launch_bounds__(256) rotate_bwd_kernel(const __grid_constant__ RotateBwdParams p) {
+__global__ void __launch_bounds__(256, 2) rotate_bwd_kernel(const __grid_constant__ RotateBwdParams p) {
   using L = HeadLanes<D>;
   constexpr int U = kRotateBack;
   __shared__ float sums[8][D];
@@ -226,24 +221,24 @@ __global__ void __launch_bounds__(256) rotate_bwd_kernel(const __grid_constant__
   const int block = kind ? blockIdx.x - p.q_blocks : blockIdx.x, blocks = kind ? gridDim.x - p.q_blocks : p.q_blocks;
   const HeadRows &gy = p.dy[kind], &xx = p.x[kind];
   const int runs = (gy.heads + U * L::ROWS - 1) / (U * L::ROWS);
-  float w[16], dw[16];
+  float dw[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] = 1.f, dw[e] = 0.f;
+  for (int e = 0; e < 16; ++e) dw[e] = 0.f;
+  uint4 rw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
   if (xx.weight != nullptr) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) unpack8(*reinterpret_cast<const uint4*>(xx.weight + 8 * at.chunk[h]), w + 8 * h);
+    for (int h = 0; h < 2; ++h) rw[h] = *reinterpret_cast<const uint4*>(xx.weight + 8 * at.chunk[h]);
   }
   const long long work = (long long)p.T * runs;
   for (long long job = (long long)block * 8 + warp; job < work; job += (long long)blocks * 8) {
     const int tok = (int)(job / runs), run = (int)(job - (long long)tok * runs);
     const int first = run * U * L::ROWS + lane_id() / L::GROUP;
     const int pos = p.position[tok];
-    const bool live = pos >= 0 && pos < p.positions;
     uint4 rg[U][2], rx[U][2];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int head = first + i * L::ROWS;
-      const bool have = at.active && live && head < gy.heads;
+      const bool have = at.active && head < gy.heads;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         rg[i][h] = rx[i][h] = make_uint4(0u, 0u, 0u, 0u);
@@ -254,19 +249,24 @@ __global__ void __launch_bounds__(256) rotate_bwd_kernel(const __grid_constant__
         }
       }
     }
+    const bool live = pos >= 0 && pos < p.positions;  // (the rows do not wait for it)
     float c[8], s[8];
     if (at.turned && live) load_angles<D, NEXT>(at, p.rotary + (long long)pos * p.rot, p.rot, c, s);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int head = first + i * L::ROWS;
       float g[16];
+      if (!live) rg[i][0] = rg[i][1] = make_uint4(0u, 0u, 0u, 0u);
       unpack8(rg[i][0], g);
       unpack8(rg[i][1], g + 8);
       if (at.turned && live) turn<NEXT, true>(g, c, s);
       if (xx.weight != nullptr) {
-        float x[16], sum = 0.f, dot = 0.f;
+        float x[16], w[16], sum = 0.f, dot = 0.f;
+        if (!live) rx[i][0] = rx[i][1] = make_uint4(0u, 0u, 0u, 0u);
         unpack8(rx[i][0], x);
         unpack8(rx[i][1], x + 8);
+        unpack8(rw[0], w);
+        unpack8(rw[1], w + 8);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           sum = fmaf(x[e], x[e], sum);
@@ -366,16 +366,18 @@ HeadRows head_rows(const Rows& in, const Rows& out, const void* weight, int head
           out.token, out.head, static_cast<const uint16_t*>(weight), heads};
 }
 
-// Steps of heads a warp: four where that leaves 32 warps an SM, else one.
+// Steps of heads a warp: kRotateSteps where that leaves 32 warps an SM, else one.
+constexpr int kRotateSteps = 2;
 template <int D, bool NEXT, bool APPEND>
 fa_status run_rotate(const RotateParams& p, cudaStream_t st) {
   constexpr int ROWS = HeadLanes<D>::ROWS;
-  const int heads = p.x[0].heads + p.x[1].heads + (APPEND ? p.x[2].heads : 0);
-  const int steps = (heads + ROWS - 1) / ROWS;
+  int steps = 0;
+  for (int i = 0; i < (APPEND ? 3 : 2); ++i) steps += (p.x[i].heads + ROWS - 1) / ROWS;
   const int kind = APPEND ? FA_KERNEL_KV4_APPEND : FA_KERNEL_ROTATE;
   const unsigned gx = (unsigned)((p.T + 7) / 8);
-  if ((long long)p.T * ((steps + 3) / 4) >= 32LL * sm_count_cached())
-    return launch(kind, rotate_kernel<D, NEXT, APPEND, 4>, dim3(gx, (steps + 3) / 4), dim3(256), 0, st, p);
+  const int runs = (steps + kRotateSteps - 1) / kRotateSteps;
+  if ((long long)p.T * runs >= 32LL * sm_count_cached())
+    return launch(kind, rotate_kernel<D, NEXT, APPEND, kRotateSteps>, dim3(gx, runs), dim3(256), 0, st, p);
   return launch(kind, rotate_kernel<D, NEXT, APPEND, 1>, dim3(gx, steps), dim3(256), 0, st, p);
 }
 

@@ -28,15 +28,17 @@ struct RaggedItem {
   int tile, head;       // rank of the tile (the heaviest first), kv head
 };
 
-constexpr int kRaggedRing = 2;        // items that a CTA has claimed ahead of its slowest role
+constexpr int kRaggedRing = 4;        // items between the scheduling warp and its slowest reader
 constexpr int kRaggedRingBytes = 32;  // a slot of the ring
 
 // The scheduling warp of a persistent CTA: claims work items (the first is the CTA's own
 // index, the rest come from the counter, so that idle SMs take the next ones, longest sequences first),
-// looks up their sequences and passes them to the other roles through a ring in shared memory.  Claimed
-// indices only grow, so the search goes on from the last sequence, 32 at a time.
+// looks up their sequences and passes them to the other roles through a ring in shared memory.  Each item
+// after the first is claimed when the producer asks for it (`ask`, one arrival an item), while it
+// loads the one before: earlier, a CTA that is still busy would hold items that others could start.
+// Claimed indices only grow, so the search goes on from the last sequence, 32 at a time.
 __device__ __forceinline__ void ragged_schedule(const RaggedSched& s, int tile_tokens, int parts, int heads,
-                                                volatile int* ring, uint32_t full0, uint32_t empty0,
+                                                volatile int* ring, uint32_t full0, uint32_t empty0, uint32_t ask,
                                                 const CtaAbort& ab, int where) {
   const int lane = lane_id();
   const int total = s.base[s.B];
@@ -45,6 +47,7 @@ __device__ __forceinline__ void ragged_schedule(const RaggedSched& s, int tile_t
     const int k = t % kRaggedRing;
     if (!wait_warp(empty0 + 8 * k, ((t / kRaggedRing) & 1) ^ 1, ab, where)) return;
     if (t > 0) {
+      if (!wait_warp(ask, (t - 1) & 1, ab, where)) return;
       if (lane == 0) w = (int)gridDim.x + atomicAdd(s.counter, 1);
       w = __shfl_sync(0xffffffffu, w, 0);
     }
