@@ -78,3 +78,43 @@ def test_backward_one_sequence(d, causal):
 def test_backward_groups_and_ragged_lengths(d, H, Hkv):
     both([1, 37, 0, 128, 129, 5, 400, 64], H, Hkv, d, True, seed=d + H)
     both([63, 0, 257, 2], H, Hkv, d, False, seed=d + H + 1, spread=3.0)
+
+
+@pytest.mark.parametrize("d", DIMS)
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (4, 1), (3, 1)])
+def test_nothing_of_another_sequence_or_of_no_sequence_reaches_a_result(d, H, Hkv):
+    """NaN and infinities in the rows before the first sequence, behind the last and in a whole
+    sequence: the others' results are those of clean inputs, and rows of no sequence stay as they were."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    lengths, lead, tail, bad = [70, 33, 300, 1, 129], 5, 200, 1
+    for causal in (True, False):
+        q, k, v, cu, host = make(lengths, H, Hkv, d, seed=d + H, lead=lead, tail=tail)
+        do = torch.randn(q.shape, generator=torch.Generator("cuda:0").manual_seed(3), device="cuda:0").to(torch.bfloat16)
+        dirty = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda:0")
+        dirty[:lead], dirty[host[-1]:], dirty[host[bad]:host[bad + 1]] = True, True, True
+        poison = [t.clone() for t in (q, k, v, do)]
+        for i, t in enumerate(poison):
+            t[dirty] = (math.nan, math.inf, -math.inf, math.nan)[i]
+        mark = dict(out=torch.full(q.shape, 5.0, device="cuda:0").to(torch.bfloat16),
+                    lse=torch.full(q.shape[:2], 5.0, device="cuda:0"))
+        o, lse = api.packed_attention_forward(q, k, v, cu, causal=causal)
+        o2, lse2 = api.packed_attention_forward(*poison[:3], cu, causal=causal, **mark)
+        assert o2 is mark["out"] and lse2 is mark["lse"]
+        outside = torch.ones_like(dirty)
+        outside[lead:host[-1]] = False
+        assert bool((o2[outside] == 5).all()) and bool((lse2[outside] == 5).all())
+        assert torch.equal(o2[~dirty], o[~dirty]) and torch.equal(lse2[~dirty], lse[~dirty])
+        o2[dirty], lse2[dirty] = math.nan, math.nan
+        r = R.attend(q, k, v, host, d ** -0.5, causal, do)
+        for variant in (0, 7):
+            grads = [torch.full(t.shape, 5.0, device="cuda:0").to(torch.bfloat16) for t in (q, k, v)]
+            got = api.packed_attention_backward(*poison[:3], o2, poison[3], lse2, cu, causal=causal, variant=variant,
+                                                grads=grads)
+            assert all(a is b for a, b in zip(got, grads))
+            api.check_device_error()
+            assert not any(bool(t[outside].any()) for t in got)
+            clean = {n: r[n].clone() for n in r}
+            for n in ("dq", "dk", "dv"):
+                clean[n][dirty] = math.nan
+            R.check_backward(got, clean, f"d={d} {H}/{Hkv} causal={causal} variant={variant}")

@@ -212,7 +212,11 @@ struct BwdKVParams {
 
 struct RaggedKVParams {
   static constexpr bool kRagged = true;
-  const CUtensorMap* maps;  // of sequence b from maps[b * nmaps] on: q, dO (box {64, G, tokens, 1}), k, v (box {64, 128, 1})
+  CUtensorMap q_map;        // {d, G, T, Hkv}, box {64, G, tokens, 1}
+  CUtensorMap k_map;        // {d, T, Hkv}, box {64, 128, 1}
+  CUtensorMap v_map;
+  CUtensorMap do_map;
+  const CUtensorMap* ends;  // of sequence b from ends[b * nmaps] on: q, dO, k, v cut at its end, for tiles that reach past it
   int nmaps;
   RaggedSched sched;
   const uint16_t* v;
@@ -576,49 +580,38 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
       if (lane == 0) {
         int it = 0, nkv = 0;
         bool ok = true;
-        // The tensor maps of an item (packed: of its sequence).
-        struct Maps {
-          const CUtensorMap *q, *dO, *k, *v;
-        };
-        auto maps_of = [&](const Item& I) {
+        tma_prefetch_desc(&p.q_map);
+        tma_prefetch_desc(&p.k_map);
+        tma_prefetch_desc(&p.v_map);
+        tma_prefetch_desc(&p.do_map);
+        // Packed: a query or key tile that reaches past its sequence's end goes by maps that end there,
+        // so that what lies behind enters no product (0 times a NaN is one).
+        int q_seq = -1, k_seq = -1;  // the last sequences whose maps were used
+        auto ends_of = [&](const Item& I, int& seq, int first) -> const CUtensorMap* {
           if constexpr (RAGGED) {
-            const CUtensorMap* m = p.maps + (size_t)I.seq * p.nmaps;
-            return Maps{m, m + 1, m + 2, m + 3};
+            const CUtensorMap* m = p.ends + (size_t)I.seq * p.nmaps + first;
+            if (I.seq != seq) {
+              seq = I.seq;
+              tensormap_acquire(m);
+              tensormap_acquire(m + 1);
+            }
+            return m;
           } else {
-            return Maps{&p.q_map, &p.do_map, &p.k_map, &p.v_map};
+            return nullptr;
           }
         };
-        int seq = -1;
-        auto ready_maps = [&](const Item& I) {
-          if constexpr (RAGGED) {
-            if (I.seq == seq) return;
-            seq = I.seq;
-            const Maps m = maps_of(I);
-            tensormap_acquire(m.q);
-            tensormap_acquire(m.dO);
-            tensormap_acquire(m.k);
-            tensormap_acquire(m.v);
-          }
-        };
-        if constexpr (!RAGGED) {
-          tma_prefetch_desc(&p.q_map);
-          tma_prefetch_desc(&p.k_map);
-          tma_prefetch_desc(&p.v_map);
-          tma_prefetch_desc(&p.do_map);
-        }
         auto prefetch_qd = [&](const Item& I, int i) {
-          const Maps m = maps_of(I);
           if constexpr (RAGGED) {
             const int prow = I.start + qt_at(I, i) * p.tokens;
             for (int pn = 0; pn < C::PANELS; ++pn) {
-              tma_prefetch_l2_4d(m.q, 64 * pn, 0, prow, I.bh);
-              tma_prefetch_l2_4d(m.dO, 64 * pn, 0, prow, I.bh);
+              tma_prefetch_l2_4d(&p.q_map, 64 * pn, 0, prow, I.bh);
+              tma_prefetch_l2_4d(&p.do_map, 64 * pn, 0, prow, I.bh);
             }
           } else {
             const int prow = qt_at(I, i) * BM;
             for (int pn = 0; pn < C::PANELS; ++pn) {
-              tma_prefetch_l2_3d(m.q, 64 * pn, prow, I.bh);
-              tma_prefetch_l2_3d(m.dO, 64 * pn, prow, I.bh);
+              tma_prefetch_l2_3d(&p.q_map, 64 * pn, prow, I.bh);
+              tma_prefetch_l2_3d(&p.do_map, 64 * pn, prow, I.bh);
             }
           }
         };
@@ -635,11 +628,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
         // All loads of item I.  The next one is J where next() says so: known from the start, but (packed)
         // asked for with the first loads and taken when its operands may go to L2.
         auto load_item = [&](const Item& I, const Item& J, auto next) {
-          const Maps m = maps_of(I);
+          const CUtensorMap *k_map = &p.k_map, *v_map = &p.v_map;
           int key0 = 0;  // first token of the sequence
           if constexpr (RAGGED) {
             key0 = I.start;
             mbar_arrive(BAR(C::B_ITEMASK));
+            if (I.k0 + C::BN > I.len) k_map = ends_of(I, k_seq, 2), v_map = k_map + 1;
           }
           auto issue_stage = [&](int i) -> bool {
             const int s = it % QS;
@@ -648,16 +642,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
             if constexpr (RAGGED) {
               mbar_expect_tx(BAR(C::B_QDFULL + s), 2 * C::PANELS * p.tokens * p.G * 128 + 2 * BM * 4);
               const int qrow = I.start + qt * p.tokens;
+              const CUtensorMap *q_map = &p.q_map, *do_map = &p.do_map;
+              if ((qt + 1) * p.tokens > I.len) q_map = ends_of(I, q_seq, 0), do_map = q_map + 1;
               for (int pn = 0; pn < C::PANELS; ++pn) {
-                tma_load_4d(stage_q(s) + pn * C::QD_PANEL, m.q, BAR(C::B_QDFULL + s), 64 * pn, 0, qrow, I.bh);
-                tma_load_4d(stage_do(s) + pn * C::QD_PANEL, m.dO, BAR(C::B_QDFULL + s), 64 * pn, 0, qrow, I.bh);
+                tma_load_4d(stage_q(s) + pn * C::QD_PANEL, q_map, BAR(C::B_QDFULL + s), 64 * pn, 0, qrow, I.bh);
+                tma_load_4d(stage_do(s) + pn * C::QD_PANEL, do_map, BAR(C::B_QDFULL + s), 64 * pn, 0, qrow, I.bh);
               }
             } else {
               mbar_expect_tx(BAR(C::B_QDFULL + s), C::STAGE_TX);
               const int qrow = qt * BM;
               for (int pn = 0; pn < C::PANELS; ++pn) {
-                tma_load_3d(stage_q(s) + pn * C::QD_PANEL, m.q, BAR(C::B_QDFULL + s), 64 * pn, qrow, I.bh);
-                tma_load_3d(stage_do(s) + pn * C::QD_PANEL, m.dO, BAR(C::B_QDFULL + s), 64 * pn, qrow, I.bh);
+                tma_load_3d(stage_q(s) + pn * C::QD_PANEL, &p.q_map, BAR(C::B_QDFULL + s), 64 * pn, qrow, I.bh);
+                tma_load_3d(stage_do(s) + pn * C::QD_PANEL, &p.do_map, BAR(C::B_QDFULL + s), 64 * pn, qrow, I.bh);
               }
             }
             bulk_load(stage_lse(s), p.lse2 + tile_row(I, qt), BM * 4, BAR(C::B_QDFULL + s));
@@ -680,19 +676,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           }
           mbar_expect_tx(BAR(C::B_KV), (C::VT ? 1 : 2) * C::KV_TILE);
           for (int pn = 0; pn < C::PANELS; ++pn) {
-            tma_load_3d(sbase + C::OFF_K + pn * C::KV_PANEL, m.k, BAR(C::B_KV), 64 * pn, key0 + I.k0, I.bh);
+            tma_load_3d(sbase + C::OFF_K + pn * C::KV_PANEL, k_map, BAR(C::B_KV), 64 * pn, key0 + I.k0, I.bh);
             if (!C::VT)
-              tma_load_3d(sbase + C::OFF_V + pn * C::KV_PANEL, m.v, BAR(C::B_KV), 64 * pn, key0 + I.k0, I.bh);
+              tma_load_3d(sbase + C::OFF_V + pn * C::KV_PANEL, v_map, BAR(C::B_KV), 64 * pn, key0 + I.k0, I.bh);
           }
           ++nkv;
           auto prefetch_kv = [&] {
             if (!next()) return;
-            const Maps mj = maps_of(J);
             int next0 = 0;
             if constexpr (RAGGED) next0 = J.start;
             for (int pn = 0; pn < C::PANELS; ++pn) {
-              tma_prefetch_l2_3d(mj.k, 64 * pn, next0 + J.k0, J.bh);
-              tma_prefetch_l2_3d(mj.v, 64 * pn, next0 + J.k0, J.bh);
+              tma_prefetch_l2_3d(&p.k_map, 64 * pn, next0 + J.k0, J.bh);
+              tma_prefetch_l2_3d(&p.v_map, 64 * pn, next0 + J.k0, J.bh);
             }
           };
           if constexpr (!RAGGED) prefetch_kv();
@@ -702,7 +697,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
         if constexpr (RAGGED) {
           Item I, J;
           bool have = item_at(0, I, ByThread{});
-          if (have) ready_maps(I);
           for (int t = 1; have && ok; ++t) {
             bool taken = false, has_next = false;
             J = I;
@@ -710,7 +704,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
               if (!taken) {
                 taken = true;
                 has_next = item_at(t, J, ByThread{});
-                if (has_next) ready_maps(J);
               }
               return has_next;
             });
@@ -1360,7 +1353,11 @@ struct BwdQParams {
 
 struct RaggedQParams {
   static constexpr bool kRagged = true;
-  const CUtensorMap* maps;  // of sequence b from maps[b * nmaps] on: q, dO (box {64, G, tokens, 1}), k, v (box {64, BN, 1})
+  CUtensorMap q_map;        // {d, G, T, Hkv}, box {64, G, tokens, 1}
+  CUtensorMap do_map;
+  CUtensorMap k_map;        // {d, T, Hkv}, box {64, BN, 1}
+  CUtensorMap v_map;
+  const CUtensorMap* ends;  // of sequence b from ends[b * nmaps] on: k, v cut at its end, for the tile that reaches past it
   int nmaps;
   RaggedSched sched;
   const uint16_t* dO;
@@ -1586,24 +1583,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
       if (lane == 0) {
         int it = 0, nitems = 0, published = 0;
         bool ok = true;
-        struct Maps {
-          const CUtensorMap *q, *dO, *k, *v;
-        };
-        auto maps_of = [&](const Item& I) {
-          if constexpr (RAGGED) {
-            const CUtensorMap* m = p.maps + (size_t)I.seq * p.nmaps;
-            return Maps{m, m + 1, m + 2, m + 3};
-          } else {
-            return Maps{&p.q_map, &p.do_map, &p.k_map, &p.v_map};
-          }
-        };
-        int seq = -1;
-        if constexpr (!RAGGED) {
-          tma_prefetch_desc(&p.q_map);
-          tma_prefetch_desc(&p.do_map);
-          tma_prefetch_desc(&p.k_map);
-          tma_prefetch_desc(&p.v_map);
-        }
+        int seq = -1;  // packed: the last sequence whose own maps were used
+        tma_prefetch_desc(&p.q_map);
+        tma_prefetch_desc(&p.do_map);
+        tma_prefetch_desc(&p.k_map);
+        tma_prefetch_desc(&p.v_map);
         auto publish = [&](int w) -> bool {
           const int k = published % C::IQ;
           if (!wait_one(BAR(C::B_ITEMEMPTY + k), ((published / C::IQ) & 1) ^ 1, ab, (kKBwdQ << 8) | 9))
@@ -1615,7 +1599,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
         };
         // All loads of item I; `near_end` runs a few key steps before its end.
         auto load_item = [&](const Item& I, auto near_end) {
-          const Maps m = maps_of(I);
           // The previous item's last S / dP MMAs must be done reading Q and dO.
           if (nitems > 0 && !wait_one(BAR(C::B_QEMPTY), (nitems - 1) & 1, ab, (kKBwdQ << 8) | 10)) {
             ok = false;
@@ -1626,16 +1609,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
             key0 = I.start;
             mbar_expect_tx(BAR(C::B_QFULL), (C::DT ? 1 : 2) * C::PANELS * p.tokens * p.G * 128);
             for (int pn = 0; pn < C::PANELS; ++pn) {
-              tma_load_4d(sbase + C::OFF_Q + pn * C::Q_PANEL, m.q, BAR(C::B_QFULL), 64 * pn, 0, key0 + I.q0, I.bh);
+              tma_load_4d(sbase + C::OFF_Q + pn * C::Q_PANEL, &p.q_map, BAR(C::B_QFULL), 64 * pn, 0, key0 + I.q0, I.bh);
               if (!C::DT)
-                tma_load_4d(sbase + C::OFF_DO + pn * C::Q_PANEL, m.dO, BAR(C::B_QFULL), 64 * pn, 0, key0 + I.q0, I.bh);
+                tma_load_4d(sbase + C::OFF_DO + pn * C::Q_PANEL, &p.do_map, BAR(C::B_QFULL), 64 * pn, 0, key0 + I.q0, I.bh);
             }
           } else {
             mbar_expect_tx(BAR(C::B_QFULL), (C::DT ? 1 : 2) * C::Q_TILE);
             for (int pn = 0; pn < C::PANELS; ++pn) {
-              tma_load_3d(sbase + C::OFF_Q + pn * C::Q_PANEL, m.q, BAR(C::B_QFULL), 64 * pn, I.q0, I.bh);
+              tma_load_3d(sbase + C::OFF_Q + pn * C::Q_PANEL, &p.q_map, BAR(C::B_QFULL), 64 * pn, I.q0, I.bh);
               if (!C::DT)
-                tma_load_3d(sbase + C::OFF_DO + pn * C::Q_PANEL, m.dO, BAR(C::B_QFULL), 64 * pn, I.q0, I.bh);
+                tma_load_3d(sbase + C::OFF_DO + pn * C::Q_PANEL, &p.do_map, BAR(C::B_QFULL), 64 * pn, I.q0, I.bh);
             }
           }
           ++nitems;
@@ -1648,7 +1631,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
                 break;
               }
               mbar_expect_tx(BAR(C::B_KVFULL + s), C::KV_TILE);
-              const CUtensorMap* kv = wkv ? m.v : m.k;
+              const CUtensorMap* kv = wkv ? &p.v_map : &p.k_map;
+              if constexpr (RAGGED) {
+                // A tile that reaches past the sequence's end goes by maps that end there: dS = 0 times a NaN is one.
+                if ((j + 1) * BN > I.len) {
+                  kv = p.ends + (size_t)I.seq * p.nmaps + wkv;
+                  if (I.seq != seq) {
+                    seq = I.seq;
+                    tensormap_acquire(kv);
+                    tensormap_acquire(kv + 1);
+                  }
+                }
+              }
               for (int pn = 0; pn < C::PANELS; ++pn)
                 tma_load_3d(sbase + C::OFF_KV + s * C::KV_TILE + pn * C::KV_PANEL, kv, BAR(C::B_KVFULL + s),
                             64 * pn, key0 + (I.j0 + j) * BN, I.bh);
@@ -1662,18 +1656,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
         if constexpr (RAGGED) {
           Item I;
           for (int t = 0; ok && item_at(t, I, ByThread{}); ++t) {
-            if (I.seq != seq) {
-              seq = I.seq;
-              const Maps m = maps_of(I);
-              tensormap_acquire(m.q);
-              tensormap_acquire(m.dO);
-              tensormap_acquire(m.k);
-              tensormap_acquire(m.v);
-            }
             if (t > 0)
               for (int pn = 0; pn < C::PANELS; ++pn) {
-                tma_prefetch_l2_4d(maps_of(I).q, 64 * pn, 0, I.start + I.q0, I.bh);
-                tma_prefetch_l2_4d(maps_of(I).dO, 64 * pn, 0, I.start + I.q0, I.bh);
+                tma_prefetch_l2_4d(&p.q_map, 64 * pn, 0, I.start + I.q0, I.bh);
+                tma_prefetch_l2_4d(&p.do_map, 64 * pn, 0, I.start + I.q0, I.bh);
               }
             load_item(I, [&] { mbar_arrive(BAR(C::B_ITEMASK)); });
           }

@@ -76,15 +76,18 @@ struct FwdParams {
 // Packed sequences: q, o [T, H, d] and k, v [T, Hkv, d] with strides in elements.
 struct RaggedFwdParams {
   static constexpr bool kRagged = true;
-  const CUtensorMap* maps;  // [B][3]: q {d, G, end, Hkv} box {64, G, tokens, 1}; k, v {d, end, Hkv} box {64, BN, 1}
+  CUtensorMap q_map;           // {d, G, T, Hkv}, box {64, G, tokens, 1}
+  CUtensorMap k_map;           // {d, T, Hkv}, box {64, BN, 1}
+  CUtensorMap v_map;
+  const CUtensorMap* v_ends;  // [B]: v_map cut at each sequence's end, for the tile that reaches past it
   RaggedSched sched;
-  const uint16_t* q;  // (read row by row by QT configurations)
   uint16_t* o;
-  long long q_token, q_head, o_token, o_head;
+  long long o_token, o_head;
   float* lse;  // [T, H]
   int* err;
   int H, Hkv;
   int G;       // query heads of a kv head
+  int by_G;    // 65536 / G rounded up: r / G = r * by_G >> 16 for r < 128, G <= 32
   int tokens;  // tokens of a 128-row tile: 128 / G rounded down
   int dv;
   float scale_log2;
@@ -104,9 +107,10 @@ struct FwdMergeParams {
   int splits;
 };
 
-template <int D_, int NQ_, int BN_, int STAGES_, bool QT_ = false, bool QSD_ = false>
+template <int D_, int NQ_, int BN_, int STAGES_, bool QT_ = false, bool QSD_ = false, int QB_ = 1>
 struct FwdCfg {
   static constexpr int D = D_, NQ = NQ_, BN = BN_, STAGES = STAGES_;
+  static constexpr int QB = QB_;  // packed sequences: buffers of each Q tile in shared memory
   static constexpr bool QT = QT_;    // Q in TMEM, S double-buffered
   static constexpr bool QSD = QSD_;  // Q in shared memory, S double-buffered
   static constexpr bool SD = QT || QSD;
@@ -122,7 +126,7 @@ struct FwdCfg {
   static constexpr uint32_t KV_PANEL = BN * 128;
   static constexpr uint32_t KV_TILE = PANELS * KV_PANEL;
   static constexpr uint32_t OFF_Q = 0;
-  static constexpr uint32_t OFF_KV = OFF_Q + (QT ? 0 : NQ * Q_TILE);
+  static constexpr uint32_t OFF_KV = OFF_Q + (QT ? 0 : NQ * QB * Q_TILE);
   // O epilogue staging: 2 KB per softmax warp (32 rows x 32 bf16 columns).
   static constexpr uint32_t OFF_EPI = OFF_KV + STAGES * KV_TILE;
   static constexpr uint32_t OFF_BAR = OFF_EPI + NQ * 4 * 2048;
@@ -135,7 +139,11 @@ struct FwdCfg {
                        B_OREADY = B_PREADY + NQ * SB, B_DONE = B_OREADY + NQ * SB, B_QEMPTY = B_DONE + 1,
                        B_QREADY = B_QEMPTY + 1, B_ITEMFULL = B_QREADY + 1, B_ITEMEMPTY = B_ITEMFULL + kRaggedRing,
                        B_ITEMASK = B_ITEMEMPTY + kRaggedRing,
-                       NBAR = B_ITEMASK + 1;
+                       B_QTFULL = B_ITEMASK + 1, B_QTEMPTY = B_QTFULL + NQ * QB, NBAR = B_QTEMPTY + NQ * QB;
+  // Packed, QT: Q comes through the K/V ring, its panels of 128 rows in QSLOTS slots ahead of an item's K(0).
+  static constexpr int QPANELS = QT ? KV_TILE / Q_PANEL : 1;  // panels that a slot holds
+  static constexpr int QSLOTS = QT ? (PANELS + QPANELS - 1) / QPANELS : 0;
+  static_assert(QPANELS > 0 && QSLOTS < STAGES, "a slot holds a panel of Q at least");
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t OFF_RING = OFF_MISC + 16;  // packed sequences: claimed items
   static constexpr int ITEM_READERS = 2 + 4 * NQ;      // the producer, the MMA warp, the softmax warps
@@ -170,6 +178,8 @@ using Fwd256 = FwdCfg<256, 1, 64, 6, true>;
 // double-buffered in TMEM next to the 384-column O (512 columns), two K/V slots
 // of 48 KiB.
 using Fwd384 = FwdCfg<384, 1, 64, 2, false, true>;
+// Packed sequences at d = 64: two buffers of Q (64 KiB beside the ring's 96).
+using RaggedFwd64 = FwdCfg<64, 2, 128, 6, false, false, 2>;
 
 __device__ __forceinline__ int fwd_kv_tiles(int qrow0, int N, int causal, int BN) {
   if (qrow0 >= N) return 0;
@@ -243,7 +253,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         mbar_init(bar0 + 8 * (C::B_ITEMFULL + k), 1);
         mbar_init(bar0 + 8 * (C::B_ITEMEMPTY + k), C::ITEM_READERS);
       }
-    if constexpr (RAGGED) mbar_init(bar0 + 8 * C::B_ITEMASK, 1);
+    if constexpr (RAGGED) {
+      mbar_init(bar0 + 8 * C::B_ITEMASK, 1);
+      for (int i = 0; i < NQ * C::QB; ++i) {
+        mbar_init(bar0 + 8 * (C::B_QTFULL + i), 1);
+        mbar_init(bar0 + 8 * (C::B_QTEMPTY + i), 1);
+      }
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -367,15 +383,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
-        const CUtensorMap *q_map, *k_map, *v_map;
-        if constexpr (!RAGGED) {
-          q_map = &p.q_map, k_map = &p.k_map, v_map = &p.v_map;
-          tma_prefetch_desc(q_map);
-          tma_prefetch_desc(k_map);
-          tma_prefetch_desc(v_map);
-        }
-        int seq = -1;  // packed: the sequence whose maps these are
+        const CUtensorMap *const q_map = &p.q_map, *const k_map = &p.k_map, *const v_map = &p.v_map;
+        tma_prefetch_desc(q_map);
+        tma_prefetch_desc(k_map);
+        tma_prefetch_desc(v_map);
+        int seq = -1;  // packed: the last sequence whose own map was used
         int it = 0, nitems = 0;
+        int nq[NQ] = {};  // packed: loads of each Q tile
         bool ok = true;
         // No L2 prefetches until the CTA's first K tile has landed (at the start
         // every CTA loads at once; prefetches then only delay the first tiles).
@@ -393,35 +407,64 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
           int row0 = 0;  // first row of the sequence in the maps
           if constexpr (RAGGED) {
             row0 = I.start;
-            if (I.seq != seq) {
-              seq = I.seq;
-              q_map = p.maps + 3 * (size_t)seq, k_map = q_map + 1, v_map = q_map + 2;
-              tensormap_acquire(q_map);
-              tensormap_acquire(k_map);
-              tensormap_acquire(v_map);
-            }
             // (The CTA still computes the item before: this one's Q goes to L2 until there is room for it.)
-            if (r > 0)
+            if (r > 0 && !C::QT)
               for (int t = 0; t < NQ; ++t)
                 if (I.nkv[t] > 0)
                   for (int pn = 0; pn < C::PANELS; ++pn)
                     tma_prefetch_l2_4d(q_map, 64 * pn, 0, row0 + I.q0 + t * p.tokens, I.bh);
           }
-          // This item's Q tiles: NQ x 128 rows, of which the packed ones are G rows a token.
-          auto load_q = [&]() {
+          // V of key tile j: where it reaches past the sequence's end, by a map that ends there (the rows behind
+          // meet probabilities of 0, and may hold anything).  Q and K need none: their rows and columns of
+          // S are masked.
+          auto map_of_v = [&](int j) -> const CUtensorMap* {
             if constexpr (RAGGED) {
-              mbar_expect_tx(BAR(C::B_QFULL), NQ * C::PANELS * p.tokens * p.G * 128);
-              for (int t = 0; t < NQ; ++t)
+              if ((j + 1) * BN > I.len) {
+                const CUtensorMap* m = p.v_ends + I.seq;
+                if (I.seq != seq) {
+                  seq = I.seq;
+                  tensormap_acquire(m);
+                }
+                return m;
+              }
+            }
+            return v_map;
+          };
+          // This item's Q tiles, NQ x 128 rows, once the previous item's S MMAs are done reading them.
+          // Packed: the tiles with tokens (G rows a token) one by one, each with barriers and, where QB = 2, two
+          // buffers of its own; QT: through the K/V ring, in slots that the softmax warps read.
+          auto load_q = [&]() -> bool {
+            if constexpr (RAGGED && C::QT) {
+              for (int pn = 0; pn < C::PANELS; pn += C::QPANELS) {
+                const int s = it % S, panels = min(C::QPANELS, C::PANELS - pn);
+                if (!wait_one(BAR(C::B_KVEMPTY + s), ((it / S) & 1) ^ 1, ab, (kKFwd << 8) | 14)) return false;
+                mbar_expect_tx(BAR(C::B_KVFULL + s), panels * p.tokens * p.G * 128);
+                for (int k = 0; k < panels; ++k)
+                  tma_load_4d(sbase + C::OFF_KV + s * C::KV_TILE + k * C::Q_PANEL, q_map, BAR(C::B_KVFULL + s),
+                              64 * (pn + k), 0, row0 + I.q0, I.bh);
+                ++it;
+              }
+            } else if constexpr (RAGGED) {
+              for (int t = 0; t < NQ; ++t) {
+                if (I.nkv[t] == 0) continue;
+                const int b = nq[t] % C::QB * NQ + t;
+                if (!wait_one(BAR(C::B_QTEMPTY + b), ((nq[t] / C::QB) & 1) ^ 1, ab, (kKFwd << 8) | 10)) return false;
+                ++nq[t];
+                mbar_expect_tx(BAR(C::B_QTFULL + b), C::PANELS * p.tokens * p.G * 128);
                 for (int pn = 0; pn < C::PANELS; ++pn)
-                  tma_load_4d(sbase + C::OFF_Q + t * C::Q_TILE + pn * C::Q_PANEL, q_map, BAR(C::B_QFULL), 64 * pn, 0,
+                  tma_load_4d(sbase + C::OFF_Q + b * C::Q_TILE + pn * C::Q_PANEL, q_map, BAR(C::B_QTFULL + b), 64 * pn, 0,
                               row0 + I.q0 + t * p.tokens, I.bh);
+              }
             } else {
+              if (!wait_one(BAR(C::B_QEMPTY), (nitems & 1) ^ 1, ab, (kKFwd << 8) | 10)) return false;
               mbar_expect_tx(BAR(C::B_QFULL), NQ * C::Q_TILE);
               for (int t = 0; t < NQ; ++t)
                 for (int pn = 0; pn < C::PANELS; ++pn)
                   tma_load_3d(sbase + C::OFF_Q + t * C::Q_TILE + pn * C::Q_PANEL, q_map, BAR(C::B_QFULL), 64 * pn,
                               I.q0 + 128 * t, I.bh);
+              ++nitems;
             }
+            return true;
           };
           // The next item's Q tiles into L2 a few key steps before this item ends,
           // so that its load (or, with Q in TMEM, the softmax warps' row reads)
@@ -440,12 +483,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
             }
           };
           if constexpr (C::SD) {
-            if (C::QSD && I.nmax > 0) {
-              // This item's Q, once the previous item's S MMAs are done reading Q.
-              if (!wait_one(BAR(C::B_QEMPTY), (nitems & 1) ^ 1, ab, (kKFwd << 8) | 10)) break;
-              load_q();
-              ++nitems;
-            }
+            if ((C::QSD || RAGGED) && I.nmax > 0 && !load_q()) break;
             // K(0), then K(j+1) ahead of V(j): the order in which the MMAs read them.
             auto load = [&](const CUtensorMap* m, int j) -> bool {
               const int s = it % S;
@@ -464,15 +502,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
             for (int j = 0; j < I.nmax && ok; ++j) {
               prefetch_next_q(j);
               if (j + 1 < I.nmax) ok = load(k_map, j + 1);
-              if (ok) ok = load(v_map, j);
+              if (ok) ok = load(map_of_v(j), j);
             }
             continue;
           }
           if (SPLIT && I.nmax == 0) continue;  // an empty key part: nothing to load or compute
-          // The previous item's S MMAs must be done reading Q.
-          if (!wait_one(BAR(C::B_QEMPTY), (nitems & 1) ^ 1, ab, (kKFwd << 8) | 10)) break;
-          load_q();
-          ++nitems;
+          if (!load_q()) break;
           for (int j = 0; j < I.nmax && ok; ++j) {
             prefetch_next_q(j);
             for (int wkv = 0; wkv < 2; ++wkv) {
@@ -482,7 +517,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
                 break;
               }
               mbar_expect_tx(BAR(C::B_KVFULL + s), C::KV_TILE);
-              const CUtensorMap* m = wkv ? v_map : k_map;
+              const CUtensorMap* m = wkv ? map_of_v(j) : k_map;
               for (int pn = 0; pn < C::PANELS; ++pn)
                 tma_load_3d(sbase + C::OFF_KV + s * C::KV_TILE + pn * C::KV_PANEL, m, BAR(C::B_KVFULL + s),
                             64 * pn, row0 + (part.lo + j) * BN, I.bh);
@@ -496,6 +531,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         }
         // Let every copy this thread started land before the CTA can exit.
         if (nitems > 0) wait_drain(BAR(C::B_QFULL), (nitems - 1) & 1);
+        for (int t = 0; t < NQ; ++t)
+          for (int i = max(0, nq[t] - C::QB); i < nq[t]; ++i)
+            wait_drain(BAR(C::B_QTFULL + i % C::QB * NQ + t), (i / C::QB) & 1);
         for (int i = max(0, it - S); i < it; ++i) wait_drain(BAR(C::B_KVFULL + i % S), (i / S) & 1);
       }
       __syncwarp();
@@ -511,8 +549,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
             mma_ts(tmem + C::TMEM_O + t * D + c * C::PVN, p_tmem,
                    desc_mnmajor(vb + c * (C::PVN / 64) * C::KV_PANEL, C::KV_PANEL, 16 * k), idO, acc);
         };
+        int nq[NQ] = {};  // packed: items in which each Q tile has tokens
         auto issue_s = [&](int t, int s) {
-          const uint32_t qa = sbase + C::OFF_Q + t * C::Q_TILE;
+          uint32_t qa = sbase + C::OFF_Q + t * C::Q_TILE;
+          if constexpr (RAGGED && C::QB > 1) qa += nq[t] % C::QB * (NQ * C::Q_TILE);
           const uint32_t kb = sbase + C::OFF_KV + s * C::KV_TILE;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
@@ -520,6 +560,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
                    desc_kmajor(kb, C::KV_PANEL, 16 * k), idS, k > 0 ? 1u : 0u);
           mma_commit(BAR(C::B_SFULL + t));
         };
+        // Packed: waits for tile t of the item's Q; and, after its last S, lets it be loaded again.
+        auto take_q = [&](int t) -> bool {
+          const bool got = wait_warp(BAR(C::B_QTFULL + nq[t] % C::QB * NQ + t), (nq[t] / C::QB) & 1, ab, (kKFwd << 8) | 2);
+          tc_fence_after();
+          return got;
+        };
+        auto drop_q = [&](int t) { mma_commit(BAR(C::B_QTEMPTY + nq[t] % C::QB * NQ + t)); };
         int it = 0, nitems = 0;
         int g[NQ];
 #pragma unroll
@@ -557,15 +604,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
             // An empty key part has no Q hand-off (the softmax warps skip it too).
             if (I.nmax <= 0) continue;
             // QT: the softmax warps have written this item's Q into TMEM; QSD: its TMA load landed.
-            if (!wait_warp(BAR(C::QT ? C::B_QREADY : C::B_QFULL), nitems & 1, ab, (kKFwd << 8) | 11)) break;
+            constexpr int kFull = C::QT ? C::B_QREADY : RAGGED ? C::B_QTFULL : C::B_QFULL;
+            constexpr int kEmpty = RAGGED ? C::B_QTEMPTY : C::B_QEMPTY;
+            if (!wait_warp(BAR(kFull), nitems & 1, ab, (kKFwd << 8) | 11)) break;
             ++nitems;
+            if constexpr (RAGGED && C::QT) {
+              // (and have read the ring's slots that it came through)
+              if (lane == 0)
+                for (int i = 0; i < C::QSLOTS; ++i) mbar_arrive(BAR(C::B_KVEMPTY + (it + i) % S));
+              it += C::QSLOTS;
+            }
             int sk = 0;
             if (!take(sk)) break;
             tc_fence_after();
             for (int t = 0; t < NQ; ++t)
               if (I.nkv[t] > 0) issue_sq(t, g[t] & 1, sk);
             mma_commit(BAR(C::B_KVEMPTY + sk));
-            if (C::QSD && I.nmax == 1) mma_commit(BAR(C::B_QEMPTY));  // the item's last S MMAs
+            if (C::QSD && I.nmax == 1) mma_commit(BAR(kEmpty));  // the item's last S MMAs
             for (int j = 0; ok && j < I.nmax; ++j) {
               // S_t(j+1) into the other buffer of tile t, whose P_t(j-1) was read by
               // PV_t(j-1) (issued before).
@@ -578,7 +633,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
                 for (int t = 0; t < NQ; ++t)
                   if (j + 1 < I.nkv[t]) issue_sq(t, (g[t] + j + 1) & 1, sk);
                 mma_commit(BAR(C::B_KVEMPTY + sk));
-                if (C::QSD && j + 2 == I.nmax) mma_commit(BAR(C::B_QEMPTY));  // the item's last S MMAs
+                if (C::QSD && j + 2 == I.nmax) mma_commit(BAR(kEmpty));  // the item's last S MMAs
               }
               int sv = 0;
               if (!take(sv)) {
@@ -611,18 +666,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
           Item I;
           if (!item_at(r, I, ByWarp{})) break;
           if (SPLIT && I.nmax == 0) continue;  // an empty key part (the producer loaded nothing)
-          ok = wait_warp(BAR(C::B_QFULL), nitems & 1, ab, (kKFwd << 8) | 2);
-          ++nitems;
-          if (!ok) break;
+          if constexpr (!RAGGED) {
+            ok = wait_warp(BAR(C::B_QFULL), nitems & 1, ab, (kKFwd << 8) | 2);
+            ++nitems;
+            if (!ok) break;
+          }
           {
             const int s = it % S;
             ok = wait_warp(BAR(C::B_KVFULL + s), (it / S) & 1, ab, (kKFwd << 8) | 3);
             if (!ok) break;
             tc_fence_after();
-            for (int t = 0; t < NQ; ++t)
-              if (I.nkv[t] > 0) issue_s(t, s);
+            for (int t = 0; t < NQ; ++t) {
+              if (I.nkv[t] == 0) continue;
+              if (RAGGED && !take_q(t)) {
+                ok = false;
+                break;
+              }
+              issue_s(t, s);
+              if (RAGGED && I.nkv[t] == 1) drop_q(t);
+            }
+            if (!ok) break;
             mma_commit(BAR(C::B_KVEMPTY + s));
-            if (I.nmax == 1) mma_commit(BAR(C::B_QEMPTY));
+            if (!RAGGED && I.nmax == 1) mma_commit(BAR(C::B_QEMPTY));
             ++it;
           }
           for (int j = 0; ok && j < I.nmax; ++j) {
@@ -656,6 +721,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
                   k_ready = true;
                 }
                 issue_s(t, sk);
+                if (RAGGED && j + 2 == I.nkv[t]) drop_q(t);
               }
             }
             if (!ok) break;
@@ -665,10 +731,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
               ++it;
             }
             // The item's last S MMAs have been issued: Q may be reloaded once they finish.
-            if (j + 2 == I.nmax) mma_commit(BAR(C::B_QEMPTY));
+            if (!RAGGED && j + 2 == I.nmax) mma_commit(BAR(C::B_QEMPTY));
           }
 #pragma unroll
-          for (int t = 0; t < NQ; ++t) g[t] += I.nkv[t];
+          for (int t = 0; t < NQ; ++t) {
+            g[t] += I.nkv[t];
+            nq[t] += I.nkv[t] > 0 ? 1 : 0;
+          }
         }
         // Every MMA issued above must finish before TMEM is released.
         mma_commit(BAR(C::B_DONE));
@@ -702,15 +771,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
       int rtok = 0, rhead = 0;
       bool rown = true;
       if constexpr (RAGGED) {
-        rtok = t * p.tokens + r / p.G, rhead = r % p.G;
+        rtok = (r * p.by_G) >> 16, rhead = r - rtok * p.G;
+        rtok += t * p.tokens;
         rown = r < p.tokens * p.G;
       }
-      auto write_q = [&](const Item& J) {
-        const uint16_t* qsrc;
+      int ring = 0;  // packed: slots of the K/V ring that the items so far have used
+      auto write_q = [&](const Item& J) -> bool {
+        const uint16_t* qsrc = nullptr;
         bool qok;
         if constexpr (RAGGED) {
           qok = rown && J.q0 + rtok < J.len;
-          qsrc = p.q + (qok ? (J.start + J.q0 + rtok) * p.q_token + (J.bh * p.G + rhead) * p.q_head : 0);
         } else {
           const int qrow = J.q0 + 128 * t + r;
           qok = qrow < p.N;
@@ -719,10 +789,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += 64) {
           uint32_t qw[32];
+          const uint8_t* panel = nullptr;  // packed: row r of the panel that the ring holds
+          if constexpr (RAGGED) {
+            const int pn = c0 / 64, at = ring + pn / C::QPANELS;
+            if (pn % C::QPANELS == 0 &&
+                !wait_warp(BAR(C::B_KVFULL + at % S), (at / S) & 1, ab, (kKFwd << 8) | 15))
+              return false;
+            panel = gbase + C::OFF_KV + at % S * C::KV_TILE + pn % C::QPANELS * C::Q_PANEL + r * 128;
+          }
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (qok && c0 + 8 * u < p.dv) x = *reinterpret_cast<const uint4*>(qsrc + c0 + 8 * u);
+            if constexpr (RAGGED) {
+              if (qok) x = *reinterpret_cast<const uint4*>(panel + ((u ^ (r & 7)) << 4));
+            } else {
+              if (qok && c0 + 8 * u < p.dv) x = *reinterpret_cast<const uint4*>(qsrc + c0 + 8 * u);
+            }
             qw[4 * u] = x.x;
             qw[4 * u + 1] = x.y;
             qw[4 * u + 2] = x.z;
@@ -734,6 +816,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::B_QREADY));
+        if constexpr (RAGGED) ring += C::QSLOTS + 2 * J.nmax;
+        return true;
       };
       // QT: the first item at or after round r with key tiles (-1 if none).  Q is
       // written only for those: one QREADY phase per item the issuer waits for, so
@@ -756,7 +840,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         if constexpr (RAGGED && C::QT) {
           if (rr == 0) {
             have_ahead = item_at(0, ahead, ByWarp{});
-            if (have_ahead) write_q(ahead);
+            if (have_ahead && !write_q(ahead)) break;
           }
           if (!have_ahead) break;
           I = ahead;
@@ -868,7 +952,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         if (C::QT && ok && I.nmax > 0) {
           if constexpr (RAGGED) {
             have_ahead = item_at(rr + 1, ahead, ByWarp{});
-            if (have_ahead) write_q(ahead);
+            if (have_ahead && !write_q(ahead)) {
+              ok = false;
+              break;
+            }
           } else {
             const int wn = next_work(rr + 1);
             if (wn >= 0) write_q(coords(wn));
@@ -893,10 +980,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int rt = quad * 32 + j * 8 + (lane >> 2);
-              const int tok = I.q0 + t * p.tokens + rt / p.G;
-              to[j] = rt < p.tokens * p.G && tok < I.len
-                          ? p.o + (I.start + tok) * p.o_token + (bh * p.G + rt % p.G) * p.o_head + 8 * (lane & 3)
-                          : nullptr;
+              const int of = (rt * p.by_G) >> 16, tok = I.q0 + t * p.tokens + of;
+              to[j] = of < p.tokens && tok < I.len ? p.o + (I.start + tok) * p.o_token +
+                                                         (bh * p.G + rt - of * p.G) * p.o_head + 8 * (lane & 3)
+                                                   : nullptr;
             }
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {

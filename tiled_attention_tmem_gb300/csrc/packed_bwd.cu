@@ -178,7 +178,7 @@ struct BwdLayout {
   size_t rows, plan, total;
   BwdLayout(const PackedShape& s, int variant, int tile_rows, int D) {
     const bool five = variant == FA_BWD_5GEMM;
-    cuts = five ? 1 : 2, nmaps = five ? 4 : 8;
+    cuts = five ? 1 : 2, nmaps = five ? 4 : 6;
     slots = s.T / (tile_rows / s.G()) + s.B;
     rows = (size_t)s.Hkv * slots * tile_rows;
     plan = packed_plan_bytes(s.B, cuts, nmaps);
@@ -195,7 +195,7 @@ fa_status run(const BwdCall& c) {
   constexpr bool five = KV::DQ;
   const PackedShape& s = c.s;
   const BwdLayout lay(s, five ? FA_BWD_5GEMM : FA_BWD_7GEMM, KV::BM, KV::D);
-  const PackedPlan plan = packed_plan_at(c.workspace, s.B, lay.cuts, lay.nmaps);
+  const PackedPlan plan = packed_plan_at(c.workspace, s.B, lay.cuts);
   uint8_t* at = static_cast<uint8_t*>(c.workspace) + lay.plan;
   float* const lse2 = reinterpret_cast<float*>(at);
   float* const dd = reinterpret_cast<float*>(at + align256(4 * lay.rows));
@@ -214,13 +214,11 @@ fa_status run(const BwdCall& c) {
   if ((e = packed_key_map(&maps[2], c.k, s, KV::BN)) != FA_OK) return e;
   if ((e = packed_key_map(&maps[3], c.v, s, KV::BN)) != FA_OK) return e;
   if constexpr (!five) {
-    if ((e = packed_query_map(&maps[4], c.q, s, 128 / s.G())) != FA_OK) return e;
-    if ((e = packed_query_map(&maps[5], c.dO, s, 128 / s.G())) != FA_OK) return e;
-    if ((e = packed_key_map(&maps[6], c.k, s, Q::BN)) != FA_OK) return e;
-    if ((e = packed_key_map(&maps[7], c.v, s, Q::BN)) != FA_OK) return e;
+    if ((e = packed_key_map(&maps[4], c.k, s, Q::BN)) != FA_OK) return e;
+    if ((e = packed_key_map(&maps[5], c.v, s, Q::BN)) != FA_OK) return e;
     cuts[1] = {128 / s.G(), Q::DQS, 4.0 * s.d};
   }
-  if (s.B > 0 && (e = run_packed_plan(plan, c.cu, s, cuts, lay.cuts, maps, lay.nmaps, c.st)) != FA_OK) return e;
+  if (s.B > 0 && (e = run_packed_plan(plan, c.cu, s, cuts, lay.cuts, maps, lay.nmaps, 2, c.st)) != FA_OK) return e;
 
   const long long sms = sm_count_cached();
   RaggedPreParams pre = {};
@@ -233,7 +231,8 @@ fa_status run(const BwdCall& c) {
   if (s.B == 0) return FA_OK;  // (every row is of no sequence)
 
   RaggedKVParams p;
-  p.maps = plan.maps, p.nmaps = lay.nmaps, p.sched = plan.sched[0];
+  p.q_map = maps[0], p.do_map = maps[1], p.k_map = maps[2], p.v_map = maps[3];
+  p.ends = plan.maps, p.nmaps = lay.nmaps, p.sched = plan.sched[0];
   p.v = in(c.v).data, p.v_token = c.v.token, p.v_head = c.v.head;
   p.lse2 = lse2, p.dd = dd, p.dqacc = dqacc;
   p.dk = out(c.dk).data, p.dk_token = c.dk.token, p.dk_head = c.dk.head;
@@ -250,7 +249,10 @@ fa_status run(const BwdCall& c) {
     return launch(FA_KERNEL_BWD_CONV, ragged_conv_kernel<KV::D>, dim3(blocks), dim3(256), 0, c.st, conv);
   } else {
     RaggedQParams r;
-    r.maps = plan.maps + 4, r.nmaps = lay.nmaps, r.sched = plan.sched[1];
+    if ((e = packed_query_map(&r.q_map, c.q, s, 128 / s.G())) != FA_OK) return e;
+    if ((e = packed_query_map(&r.do_map, c.dO, s, 128 / s.G())) != FA_OK) return e;
+    r.k_map = maps[4], r.v_map = maps[5];
+    r.ends = plan.maps + 4, r.nmaps = lay.nmaps, r.sched = plan.sched[1];
     r.dO = in(c.dO).data, r.do_token = c.dO.token, r.do_head = c.dO.head;
     r.lse2 = lse2, r.dd = dd;
     r.dq = out(c.dq).data, r.dq_token = c.dq.token, r.dq_head = c.dq.head;

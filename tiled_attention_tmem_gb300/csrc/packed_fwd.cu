@@ -12,24 +12,22 @@ template <class C>
 fa_status run(const PackedRows& q, const PackedRows& k, const PackedRows& v, const PackedRows& o, float* lse,
               const int* cu, const PackedShape& s, float scale, int causal, void* workspace, cudaStream_t st) {
   const int tokens = 128 / s.G();
-  CUtensorMap maps[3];
-  fa_status e;
-  if ((e = packed_query_map(&maps[0], q, s, tokens)) != FA_OK) return e;
-  if ((e = packed_key_map(&maps[1], k, s, C::BN)) != FA_OK) return e;
-  if ((e = packed_key_map(&maps[2], v, s, C::BN)) != FA_OK) return e;
-  const PackedPlan plan = packed_plan_at(workspace, s.B, 1, 3);
-  const PackedCut cut = {C::NQ * tokens, 1, 4.0 * s.d};  // K and V
-  if ((e = run_packed_plan(plan, cu, s, &cut, 1, maps, 3, st)) != FA_OK) return e;
   RaggedFwdParams p;
-  p.maps = plan.maps;
+  fa_status e;
+  if ((e = packed_query_map(&p.q_map, q, s, tokens)) != FA_OK) return e;
+  if ((e = packed_key_map(&p.k_map, k, s, C::BN)) != FA_OK) return e;
+  if ((e = packed_key_map(&p.v_map, v, s, C::BN)) != FA_OK) return e;
+  const PackedPlan plan = packed_plan_at(workspace, s.B, 1);
+  const PackedCut cut = {C::NQ * tokens, 1, 4.0 * s.d};  // K and V
+  if ((e = run_packed_plan(plan, cu, s, &cut, 1, &p.v_map, 1, 0, st)) != FA_OK) return e;
+  p.v_ends = plan.maps;
   p.sched = plan.sched[0];
-  p.q = static_cast<const uint16_t*>(q.data);
   p.o = static_cast<uint16_t*>(o.data);
-  p.q_token = q.token, p.q_head = q.head, p.o_token = o.token, p.o_head = o.head;
+  p.o_token = o.token, p.o_head = o.head;
   p.lse = lse;
   p.err = device_error_word();
   if (!p.err) return record_cuda_error(cudaErrorMemoryAllocation);
-  p.H = s.H, p.Hkv = s.Hkv, p.G = s.G(), p.tokens = tokens, p.dv = s.d;
+  p.H = s.H, p.Hkv = s.Hkv, p.G = s.G(), p.by_G = (65536 + s.G() - 1) / s.G(), p.tokens = tokens, p.dv = s.d;
   p.scale_log2 = scale * kLog2e;
   p.causal = causal;
   // One CTA an SM, and no more than there can be items.
@@ -40,12 +38,12 @@ fa_status run(const PackedRows& q, const PackedRows& k, const PackedRows& v, con
 
 }  // namespace
 
-size_t packed_fwd_bytes(const PackedShape& s) { return packed_plan_bytes(s.B, 1, 3); }
+size_t packed_fwd_bytes(const PackedShape& s) { return packed_plan_bytes(s.B, 1, 1); }
 
 fa_status run_packed_fwd(const PackedRows& q, const PackedRows& k, const PackedRows& v, const PackedRows& o, float* lse,
                          const int* cu, const PackedShape& s, float scale, int causal, void* workspace, cudaStream_t st) {
   switch (s.d) {
-    case 64: return run<Fwd64>(q, k, v, o, lse, cu, s, scale, causal, workspace, st);
+    case 64: return run<RaggedFwd64>(q, k, v, o, lse, cu, s, scale, causal, workspace, st);
     case 96:
     case 128: return run<Fwd128>(q, k, v, o, lse, cu, s, scale, causal, workspace, st);
     case 192: return run<Fwd192>(q, k, v, o, lse, cu, s, scale, causal, workspace, st);

@@ -30,18 +30,19 @@ struct PackedCut {
 
 // What ragged_plan_kernel makes of the lengths, in the caller's workspace: for each cut the order of
 // the sequences, their first work items and a counter; for each sequence its tensor maps.
-constexpr int kPackedMaxMaps = 8;
+constexpr int kPackedMaxMaps = 6;
 struct PackedPlan {
   RaggedSched sched[2];
   CUtensorMap* maps;  // [B][nmaps]
 };
 size_t packed_plan_bytes(int B, int cuts, int nmaps);
 // Lays the plan out at `at` (256-byte aligned) without launching anything.
-PackedPlan packed_plan_at(void* at, int B, int cuts, int nmaps);
+PackedPlan packed_plan_at(void* at, int B, int cuts);
 fa_status run_packed_plan(const PackedPlan& plan, const int* cu, const PackedShape& s, const PackedCut* cuts, int ncuts,
-                          const CUtensorMap* maps, int nmaps, cudaStream_t st);
+                          const CUtensorMap* maps, int nmaps, int query_maps, cudaStream_t st);
 
-// Template maps, whose token dimension the plan cuts at each sequence's end: query rows
+// Tensor maps, of which the plan makes one for each sequence that ends with it (the first query_maps of
+// them are of queries): query rows
 // {d, G, T, Hkv} with a box of `tokens` tokens of all G heads, key rows {d, T, Hkv}.
 fa_status packed_query_map(CUtensorMap* map, const PackedRows& r, const PackedShape& s, int tokens);
 fa_status packed_key_map(CUtensorMap* map, const PackedRows& r, const PackedShape& s, int box_rows);

@@ -20,7 +20,7 @@ struct PlanParams {
   RaggedSched sched[2];
   PackedCut cut[2];
   int ncuts, nmaps;
-  unsigned query;  // bit m: map m has the heads of a group in front of its tokens
+  int query_maps;  // these first ones have the heads of a group in front of their tokens
   int B, T, heads, sms;
 };
 
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kPlanThreads) ragged_plan_kernel(const __grid_
       __syncwarp();
       const uint32_t at = smem_u32(slot[warp]);
       if (lane == 0) {
-        if (p.query >> m & 1u)
+        if (m < p.query_maps)
           asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 2, %1;" ::"r"(at), "r"(end)
                        : "memory");
         else
@@ -141,7 +141,7 @@ size_t packed_plan_bytes(int B, int cuts, int nmaps) {
   return cuts * (align256(4 * ((size_t)B + 1)) + align256(16 * (size_t)B) + 256) + align256(128 * (size_t)B * nmaps);
 }
 
-PackedPlan packed_plan_at(void* at, int B, int cuts, int nmaps) {
+PackedPlan packed_plan_at(void* at, int B, int cuts) {
   uint8_t* b = static_cast<uint8_t*>(at);
   PackedPlan plan = {};
   for (int c = 0; c < cuts; ++c) {
@@ -154,13 +154,12 @@ PackedPlan packed_plan_at(void* at, int B, int cuts, int nmaps) {
     s.counter = reinterpret_cast<int*>(b);
     b += 256;
   }
-  (void)nmaps;
   plan.maps = reinterpret_cast<CUtensorMap*>(b);
   return plan;
 }
 
 fa_status run_packed_plan(const PackedPlan& plan, const int* cu, const PackedShape& s, const PackedCut* cuts, int ncuts,
-                          const CUtensorMap* maps, int nmaps, cudaStream_t st) {
+                          const CUtensorMap* maps, int nmaps, int query_maps, cudaStream_t st) {
   PlanParams p = {};
   p.cu = cu;
   p.maps = plan.maps;
@@ -172,7 +171,7 @@ fa_status run_packed_plan(const PackedPlan& plan, const int* cu, const PackedSha
   p.T = s.T;
   p.heads = s.Hkv;
   p.sms = sm_count_cached();
-  p.query = nmaps == 3 ? 0x1u : 0x33u;  // forward: q, k, v; backward: q, dO, k, v of each kernel
+  p.query_maps = query_maps;
   const long long tasks = ((long long)s.B * nmaps + kPlanWarps - 1) / kPlanWarps;
   const unsigned grid = 1 + (unsigned)std::min<long long>(tasks, 4LL * p.sms);
   return launch(FA_KERNEL_PACKED_PLAN, ragged_plan_kernel, dim3(grid), dim3(kPlanThreads), 0, st, p);

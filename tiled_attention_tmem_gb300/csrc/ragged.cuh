@@ -7,10 +7,10 @@
 // kernels are those of equal heads over G rows a token.  The rows past (M / G) * G of a
 // tile belong to nobody.
 //
-// Tensor maps: every sequence has maps of its own (built by ragged_plan_kernel), whose token
-// dimension ends where the sequence does, so that a tile that reaches past its end reads zeros,
-// and not what the next sequence or the rows behind the last one hold: a NaN there times a
-// probability of 0 would be NaN.
+// Tensor maps: a tile that reaches past its sequence's end is loaded by a map of the sequence's own (built by
+// ragged_plan_kernel), whose token dimension ends there, so that it reads zeros, and not what
+// the next sequence or the rows behind the last one hold: a NaN there times a probability of 0
+// would be NaN.  Other tiles go by the launch's maps: a new map costs a fence and a fetch.
 #pragma once
 #include "common.cuh"
 
