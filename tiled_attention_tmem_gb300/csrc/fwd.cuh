@@ -833,15 +833,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         }
         }
       };
-      Item ahead;  // packed, QT: the next item, taken before this one's epilogue
+      Item ahead;  // packed: the next item, taken before this one's epilogue
       bool have_ahead = false;
+      auto look_ahead = [&](int r2) -> bool {
+        if constexpr (RAGGED) {
+          have_ahead = item_at(r2, ahead, ByWarp{});
+          if constexpr (C::QT) return !have_ahead || write_q(ahead);
+        }
+        return true;
+      };
+      if (!look_ahead(0)) ok = false;
       for (int rr = 0; ok; ++rr) {
         Item I;
-        if constexpr (RAGGED && C::QT) {
-          if (rr == 0) {
-            have_ahead = item_at(0, ahead, ByWarp{});
-            if (have_ahead && !write_q(ahead)) break;
-          }
+        if constexpr (RAGGED) {
           if (!have_ahead) break;
           I = ahead;
         } else {
@@ -949,43 +953,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(C::B_PREADY + sb));
         }
-        if (C::QT && ok && I.nmax > 0) {
-          if constexpr (RAGGED) {
-            have_ahead = item_at(rr + 1, ahead, ByWarp{});
-            if (have_ahead && !write_q(ahead)) {
-              ok = false;
+        if constexpr (RAGGED) {
+          // While the last P V runs: the rows' lse, where the four rows of O that this lane stores go
+          // (a token and head each), the next item.  Then O, 32 columns at a time through this warp's 2 KB of
+          // shared memory (see below), in a loop that is not unrolled: it runs once an item, from
+          // instructions that are not cached (measured 2600 cycles unrolled, of an item's 10000 to 20000).
+          // A row whose scores are all -inf is zero.
+          if (!ok) break;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          if (limit >= 0)
+            p.lse[(long long)(I.start + qi) * p.H + bh * p.G + rhead] =
+                l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
+          uint16_t* to[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int rt = quad * 32 + j * 8 + (lane >> 2);
+            const int of = (rt * p.by_G) >> 16, tok = I.q0 + t * p.tokens + of;
+            to[j] = of < p.tokens && tok < I.len ? p.o + (I.start + tok) * p.o_token +
+                                                       (bh * p.G + rt - of * p.G) * p.o_head + 8 * (lane & 3)
+                                                 : nullptr;
+          }
+          if (!look_ahead(rr + 1)) break;
+          if (n > 0) {
+            if (!wait_warp(BAR(C::B_OREADY + oready_bar(g + n - 1)), oready_phase(g + n - 1), ab, (kKFwd << 8) | 9))
               break;
-            }
-          } else {
-            const int wn = next_work(rr + 1);
-            if (wn >= 0) write_q(coords(wn));
-          }
-        }
-        if (ok && n > 0) {
-          if (!wait_warp(BAR(C::B_OREADY + oready_bar(g + n - 1)), oready_phase(g + n - 1), ab, (kKFwd << 8) | 9)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          // Staged through this warp's 2 KB of shared memory, 32 columns at a
-          // time: each thread writes its row, then each warp store covers 8 rows
-          // x 64 contiguous bytes instead of 32 rows x 16 bytes.
-          uint8_t* epi = gbase + C::OFF_EPI + (t * 4 + quad) * 2048;
-          const int row0 = I.q0 + 128 * t + quad * 32;  // this warp's first query row
-          if constexpr (RAGGED) {
-            // Rows of a token and head each: where the four rows that this lane stores go.  A row
-            // whose scores are all -inf is zero.
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint16_t* to[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int rt = quad * 32 + j * 8 + (lane >> 2);
-              const int of = (rt * p.by_G) >> 16, tok = I.q0 + t * p.tokens + of;
-              to[j] = of < p.tokens && tok < I.len ? p.o + (I.start + tok) * p.o_token +
-                                                         (bh * p.G + rt - of * p.G) * p.o_head + 8 * (lane & 3)
-                                                   : nullptr;
-            }
-#pragma unroll
+            tc_fence_after();
+            uint8_t* epi = gbase + C::OFF_EPI + (t * 4 + quad) * 2048;
+#pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
               uint32_t orr[32];
               tmem_ld_32x32b_x32(tO + c0, orr);
@@ -1002,16 +996,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
               __syncwarp();
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const int rr2 = j * 8 + (lane >> 2), u = lane & 3;
-                const uint4 val = *reinterpret_cast<const uint4*>(epi + rr2 * 64 + ((u ^ ((rr2 >> 1) & 3)) << 4));
+                const int ri = j * 8 + (lane >> 2), u = lane & 3;
+                const uint4 val = *reinterpret_cast<const uint4*>(epi + ri * 64 + ((u ^ ((ri >> 1) & 3)) << 4));
                 if (to[j] && c0 + 8 * u < p.dv) *reinterpret_cast<uint4*>(to[j] + c0) = val;
               }
               __syncwarp();
             }
-            if (limit >= 0)
-              p.lse[(long long)(I.start + qi) * p.H + bh * p.G + rhead] =
-                  l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
-          } else if constexpr (!SPLIT) {
+          }
+          g += n;
+          continue;
+        }
+        if (C::QT && ok && I.nmax > 0) {
+          const int wn = next_work(rr + 1);
+          if (wn >= 0) write_q(coords(wn));
+        }
+        if constexpr (!RAGGED) {
+        if (ok && n > 0) {
+          if (!wait_warp(BAR(C::B_OREADY + oready_bar(g + n - 1)), oready_phase(g + n - 1), ab, (kKFwd << 8) | 9)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // Staged through this warp's 2 KB of shared memory, 32 columns at a
+          // time: each thread writes its row, then each warp store covers 8 rows
+          // x 64 contiguous bytes instead of 32 rows x 16 bytes.
+          uint8_t* epi = gbase + C::OFF_EPI + (t * 4 + quad) * 2048;
+          const int row0 = I.q0 + 128 * t + quad * 32;  // this warp's first query row
+          if constexpr (!SPLIT) {
             const bool store = qi < p.N;
             const float inv = 1.f / l;
             uint16_t* obase = p.o + ((size_t)bh * p.N + (size_t)row0) * p.dv;
@@ -1081,6 +1092,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         } else if constexpr (SPLIT) {
           // This query tile sees no key tile of the part.
           if (ok && qi < p.N) p.lpart[((size_t)part.s * p.BH + bh) * p.N + qi] = -INFINITY;
+        }
         }
         g += n;
       }
