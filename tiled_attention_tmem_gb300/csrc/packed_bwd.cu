@@ -74,40 +74,58 @@ __global__ void __launch_bounds__(256) ragged_pre_kernel(const __grid_constant__
     const int ts = (int)(w / t.Hkv), kvh = (int)(w - (long long)ts * t.Hkv);
     int start, len, tok0;
     if (!tile_of_slot(t, ts, start, len, tok0)) continue;
-    for (int r = threadIdx.x / GT; r < t.rows; r += 256 / GT) {
-      const int tok = tok0 + r / t.G, head = kvh * t.G + r % t.G;
-      const bool have = r < t.tokens * t.G && tok < len;
-      float acc = 0.f;
-      if (have) {
-        const uint16_t* o = p.o.data + (start + tok) * p.o.token + head * p.o.head;
-        const uint16_t* g = p.dO.data + (start + tok) * p.dO.token + head * p.dO.head;
+    // UN rows of a thread's at a time, all of their loads first.
+    constexpr int STEP = 256 / GT, UN = 4;
+#pragma unroll 1
+    for (int r0 = threadIdx.x / GT; r0 < t.rows; r0 += UN * STEP) {
+      uint4 a[UN][CH], b[UN][CH];
+      float lse[UN];
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        const int r = r0 + i * STEP, of = r / t.G, tok = tok0 + of, head = kvh * t.G + r - of * t.G;
+        const bool have = of < t.tokens && r < t.rows && tok < len;
+        const uint16_t* o = p.o.data + (have ? (start + tok) * p.o.token + head * p.o.head : 0);
+        const uint16_t* g = p.dO.data + (have ? (start + tok) * p.dO.token + head * p.dO.head : 0);
+        lse[i] = have && sub == 0 ? p.lse[(long long)(start + tok) * t.H + head] : -INFINITY;
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch) {
           const int c = (ch * GT + sub) * 8;
-          if (c >= t.hd) continue;
-          const uint4 a = *reinterpret_cast<const uint4*>(o + c), b = *reinterpret_cast<const uint4*>(g + c);
-          const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+          a[i][ch] = b[i][ch] = make_uint4(0u, 0u, 0u, 0u);
+          if (have && c < t.hd) {
+            a[i][ch] = *reinterpret_cast<const uint4*>(o + c);
+            b[i][ch] = *reinterpret_cast<const uint4*>(g + c);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        const int r = r0 + i * STEP;
+        float acc = 0.f;
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+          const uint32_t av[4] = {a[i][ch].x, a[i][ch].y, a[i][ch].z, a[i][ch].w};
+          const uint32_t bv[4] = {b[i][ch].x, b[i][ch].y, b[i][ch].z, b[i][ch].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             acc = fmaf(__uint_as_float(av[e] << 16), __uint_as_float(bv[e] << 16), acc);
             acc = fmaf(__uint_as_float(av[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), acc);
           }
         }
-      }
 #pragma unroll
-      for (int d = GT / 2; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d, GT);
-      const size_t row = ((size_t)kvh * t.slots + ts) * t.rows + r;
-      if (sub == 0) {
-        p.dd[row] = -acc;
-        // (a row whose scores are all -inf has no probabilities: -inf - -inf would be NaN)
-        const float lse = have ? p.lse[(long long)(start + tok) * t.H + head] : -INFINITY;
-        p.lse2[row] = lse == -INFINITY ? -INFINITY : -(lse * kLog2e);
-      }
-      if (p.dqacc) {
+        for (int d = GT / 2; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d, GT);
+        if (r >= t.rows) continue;
+        const size_t row = ((size_t)kvh * t.slots + ts) * t.rows + r;
+        if (sub == 0) {
+          p.dd[row] = -acc;
+          // (a row whose scores are all -inf has no probabilities: -inf - -inf would be NaN)
+          p.lse2[row] = lse[i] == -INFINITY ? -INFINITY : -(lse[i] * kLog2e);
+        }
+        if (p.dqacc) {
 #pragma unroll
-        for (int ch = 0; ch < CH; ++ch) {
-          float4* z = reinterpret_cast<float4*>(p.dqacc + row * D + (ch * GT + sub) * 8);
-          z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int ch = 0; ch < CH; ++ch) {
+            float4* z = reinterpret_cast<float4*>(p.dqacc + row * D + (ch * GT + sub) * 8);
+            z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
         }
       }
     }
@@ -149,14 +167,25 @@ __global__ void __launch_bounds__(256) ragged_conv_kernel(const __grid_constant_
     int start, len, tok0;
     if (!tile_of_slot(t, ts, start, len, tok0)) continue;
     const int rows = min(t.tokens, len - tok0) * t.G;
-    for (int i = threadIdx.x; i < rows * chunks; i += 256) {
-      const int r = i / chunks, c = (i - r * chunks) * 8;
-      const float* row = p.dqacc + (((size_t)kvh * t.slots + ts) * t.rows + r) * D;
-      const float4 a = *reinterpret_cast<const float4*>(row + dq_swz(r, c));
-      const float4 b = *reinterpret_cast<const float4*>(row + dq_swz(r, c + 4));
-      *reinterpret_cast<uint4*>(p.dq.data + (start + tok0 + r / t.G) * p.dq.token + (kvh * t.G + r % t.G) * p.dq.head + c) =
-          make_uint4(pack_bf16(a.x * p.scale, a.y * p.scale), pack_bf16(a.z * p.scale, a.w * p.scale),
-                     pack_bf16(b.x * p.scale, b.y * p.scale), pack_bf16(b.z * p.scale, b.w * p.scale));
+    const float* slot = p.dqacc + ((size_t)kvh * t.slots + ts) * t.rows * D;
+    constexpr int UN = 4;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < rows * chunks; i0 += UN * 256) {
+      float4 a[UN], b[UN];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int i = min(i0 + u * 256, rows * chunks - 1), r = i / chunks, c = (i - r * chunks) * 8;
+        a[u] = *reinterpret_cast<const float4*>(slot + r * D + dq_swz(r, c));
+        b[u] = *reinterpret_cast<const float4*>(slot + r * D + dq_swz(r, c + 4));
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int i = i0 + u * 256, r = i / chunks, c = (i - r * chunks) * 8, of = r / t.G;
+        if (i >= rows * chunks) break;
+        *reinterpret_cast<uint4*>(p.dq.data + (start + tok0 + of) * p.dq.token + (kvh * t.G + r - of * t.G) * p.dq.head + c) =
+            make_uint4(pack_bf16(a[u].x * p.scale, a[u].y * p.scale), pack_bf16(a[u].z * p.scale, a[u].w * p.scale),
+                       pack_bf16(b[u].x * p.scale, b[u].y * p.scale), pack_bf16(b[u].z * p.scale, b[u].w * p.scale));
+      }
     }
   }
 }
@@ -265,16 +294,19 @@ fa_status run(const BwdCall& c) {
   }
 }
 
-// Query rows of a tile of the dK/dV kernels (both forms).
-int tile_rows(int d) { return d == 64 ? 128 : d == 384 ? 32 : 64; }
-static_assert(KV5_64::BM == 128 && KV7_64::BM == 128 && KV5_128::BM == 64 && KV7_128::BM == 64 && KV7_192::BM == 64 &&
+// Query rows of a tile of the dK/dV kernels.
+int tile_rows(int d, int variant) {
+  if (d == 64) return variant == FA_BWD_5GEMM ? 64 : 128;
+  return d == 384 ? 32 : 64;
+}
+static_assert(RaggedKV5_64::BM == 64 && KV7_64::BM == 128 && KV5_128::BM == 64 && KV7_128::BM == 64 && KV7_192::BM == 64 &&
                   KV7_256::BM == 64 && KV7_384::BM == 32,
               "tile_rows");
 
 }  // namespace
 
 size_t packed_bwd_bytes(const PackedShape& s, int variant) {
-  return BwdLayout(s, variant, tile_rows(s.d), padded_head_dim(s.d)).total;
+  return BwdLayout(s, variant, tile_rows(s.d, variant), padded_head_dim(s.d)).total;
 }
 
 fa_status run_packed_bwd(const PackedRows& q, const PackedRows& k, const PackedRows& v, const PackedRows& o,
@@ -284,7 +316,7 @@ fa_status run_packed_bwd(const PackedRows& q, const PackedRows& k, const PackedR
   const BwdCall c = {q, k, v, o, dO, dq, dk, dv, lse, cu, s, scale, causal, workspace, st};
   const bool five = variant == FA_BWD_5GEMM;
   switch (s.d) {
-    case 64: return five ? run<64, KV5_64, void>(c) : run<64, KV7_64, Q7_64>(c);
+    case 64: return five ? run<64, RaggedKV5_64, void>(c) : run<64, KV7_64, Q7_64>(c);
     case 96:
     case 128: return five ? run<128, KV5_128, void>(c) : run<128, KV7_128, Q7_128>(c);
     case 192: return run<256, KV7_192, Q7_192>(c);
