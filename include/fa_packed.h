@@ -13,7 +13,10 @@
  * cu (int32 [B + 1], device memory) must not decrease.  Its contents are checked
  * on the device: a sequence whose tokens do not lie in [0, T) has none.  Sequences
  * of no token are allowed.  Whatever cu holds, no call reads or writes
- * outside its arrays; rows that two sequences share hold either's results.
+ * outside its arrays; the results of a call whose cu decreases are unspecified.
+ *
+ * The calls take their arguments as a structure in host memory, which is read during
+ * the call only; every call enqueues its work on `stream`.
  */
 #ifndef TILED_ATTENTION_TMEM_GB300_FA_PACKED_H_
 #define TILED_ATTENTION_TMEM_GB300_FA_PACKED_H_
@@ -23,6 +26,13 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* A [T, heads, d] array: its address and the strides of a token and a head in elements. */
+typedef struct {
+  const void* data; /* (written through where the call says so) */
+  long long token;
+  long long head;
+} fa_rows;
 
 /*
  * Forward.  For query i and keys j of one sequence (causal: j <= i):
@@ -38,10 +48,18 @@ extern "C" {
  * most 2^28, scale finite and > 0.  workspace: fa_packed_fwd_workspace_size bytes,
  * 256-byte aligned, not shared with a concurrent call.
  */
-fa_status fa_packed_fwd(const void* q, long long q_token, long long q_head, const void* k, long long k_token,
-                        long long k_head, const void* v, long long v_token, long long v_head, void* o,
-                        long long o_token, long long o_head, float* lse, const int* cu, int B, int T, int H, int Hkv,
-                        int d, float scale, int causal, void* workspace, size_t workspace_bytes, void* stream);
+typedef struct {
+  fa_rows q, k, v, o;
+  float* lse;
+  const int* cu;
+  int B, T, H, Hkv, d;
+  float scale;
+  int causal; /* 0 or 1 */
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+} fa_packed_fwd_args;
+fa_status fa_packed_fwd(const fa_packed_fwd_args* a);
 
 /* Bytes of workspace fa_packed_fwd needs; 0 for shapes without work and invalid ones. */
 size_t fa_packed_fwd_workspace_size(int B, int T, int H, int Hkv, int d);
@@ -60,13 +78,20 @@ size_t fa_packed_fwd_workspace_size(int B, int T, int H, int Hkv, int d);
  * exists).  workspace: fa_packed_bwd_workspace_size bytes of the same shape and variant,
  * 256-byte aligned, not shared with a concurrent call.
  */
-fa_status fa_packed_bwd(const void* q, long long q_token, long long q_head, const void* k, long long k_token,
-                        long long k_head, const void* v, long long v_token, long long v_head, const void* o,
-                        long long o_token, long long o_head, const void* dO, long long do_token, long long do_head,
-                        const float* lse, void* dq, long long dq_token, long long dq_head, void* dk, long long dk_token,
-                        long long dk_head, void* dv, long long dv_token, long long dv_head, const int* cu, int B, int T,
-                        int H, int Hkv, int d, float scale, int causal, int variant, void* workspace,
-                        size_t workspace_bytes, void* stream);
+typedef struct {
+  fa_rows q, k, v, o, dO;
+  const float* lse;
+  fa_rows dq, dk, dv;
+  const int* cu;
+  int B, T, H, Hkv, d;
+  float scale;
+  int causal; /* 0 or 1 */
+  int variant;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+} fa_packed_bwd_args;
+fa_status fa_packed_bwd(const fa_packed_bwd_args* a);
 
 /*
  * Bytes of workspace fa_packed_bwd needs (row statistics, for the 5-GEMM form an fp32 dq, tensor
@@ -90,11 +115,19 @@ size_t fa_packed_bwd_workspace_size(int B, int T, int H, int Hkv, int d, int var
  * likewise, but no output may overlap another array in another way.  H + 2 Hkv at most 65535,
  * T at most 2^30.
  */
-fa_status fa_qk_norm_rope(const void* q, long long q_token, long long q_head, const void* k, long long k_token,
-                          long long k_head, const float* rotary, int positions, int rot, const int* position,
-                          const void* q_weight, const void* k_weight, float eps, int interleaved, void* q_out,
-                          long long qo_token, long long qo_head, void* k_out, long long ko_token, long long ko_head,
-                          int T, int H, int Hkv, int d, void* stream);
+typedef struct {
+  fa_rows q, k, q_out, k_out;
+  const float* rotary;
+  const int* position;
+  const void* q_weight;
+  const void* k_weight;
+  int positions, rot;
+  float eps;
+  int interleaved; /* 0 or 1 */
+  int T, H, Hkv, d;
+  void* stream;
+} fa_qk_norm_rope_args;
+fa_status fa_qk_norm_rope(const fa_qk_norm_rope_args* a);
 
 /*
  * Its gradients.  dq_out and dk_out: of the results; q and k: what went in (needed, and read, only where
@@ -106,14 +139,23 @@ fa_status fa_qk_norm_rope(const void* q, long long q_token, long long q_head, co
  * workspace: fa_qk_norm_rope_bwd_workspace_size bytes, 256-byte aligned, not shared with a
  * concurrent call (NULL where both weights are).
  */
-fa_status fa_qk_norm_rope_bwd(const void* dq_out, long long dqo_token, long long dqo_head, const void* dk_out,
-                              long long dko_token, long long dko_head, const void* q, long long q_token,
-                              long long q_head, const void* k, long long k_token, long long k_head,
-                              const float* rotary, int positions, int rot, const int* position, const void* q_weight,
-                              const void* k_weight, float eps, int interleaved, void* dq, long long dq_token,
-                              long long dq_head, void* dk, long long dk_token, long long dk_head, float* dq_weight,
-                              float* dk_weight, int T, int H, int Hkv, int d, void* workspace, size_t workspace_bytes,
-                              void* stream);
+typedef struct {
+  fa_rows dq_out, dk_out, q, k, dq, dk;
+  const float* rotary;
+  const int* position;
+  const void* q_weight;
+  const void* k_weight;
+  float* dq_weight;
+  float* dk_weight;
+  int positions, rot;
+  float eps;
+  int interleaved; /* 0 or 1 */
+  int T, H, Hkv, d;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+} fa_qk_norm_rope_bwd_args;
+fa_status fa_qk_norm_rope_bwd(const fa_qk_norm_rope_bwd_args* a);
 size_t fa_qk_norm_rope_bwd_workspace_size(int T, int H, int Hkv, int d);
 
 /*
@@ -123,12 +165,21 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int T, int H, int Hkv, int d);
  * or NULL.  A token without a position is left out altogether; one whose slot is not in
  * [0, pages*page) is rotated but not stored.  The valid slots must be distinct.  H may be 0.
  */
-fa_status fa_kv4_append(const fa_kv4_cache* cache, const void* q, long long q_token, long long q_head, const void* k,
-                        long long k_token, long long k_head, const void* v, long long v_token, long long v_head,
-                        const float* rotary, int positions, int rot, const int* position, const void* q_weight,
-                        const void* k_weight, float eps, int interleaved, void* q_out, long long qo_token,
-                        long long qo_head, void* k_out, long long ko_token, long long ko_head, const long long* slots,
-                        int T, int H, void* stream);
+typedef struct {
+  const fa_kv4_cache* cache;
+  fa_rows q, k, v, q_out, k_out; /* k_out.data may be NULL */
+  const float* rotary;
+  const int* position;
+  const void* q_weight;
+  const void* k_weight;
+  const long long* slots;
+  int positions, rot;
+  float eps;
+  int interleaved; /* 0 or 1 */
+  int T, H;
+  void* stream;
+} fa_kv4_append_args;
+fa_status fa_kv4_append(const fa_kv4_append_args* a);
 
 #ifdef __cplusplus
 }

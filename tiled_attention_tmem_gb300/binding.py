@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa_gb300.so")
@@ -35,6 +36,7 @@ _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _LL = ctypes.c_longlong
+_ARGS = ctypes.c_char_p  # the bytes of a structure of arguments
 SIGNATURES = {
     "fa_fwd": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I, _VP]),
     "fa_fwd_splitkv_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
@@ -72,18 +74,14 @@ SIGNATURES = {
     "fa_kv4_attn": (_I, [_VP, _VP, _LL, _LL, _I, _VP, _I, _VP, _I, _VP, _I, _I, _F, _VP, _LL, _LL, _VP, _VP, _SZ, _VP]),
     "fa_kv4_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     # include/fa_packed.h
-    "fa_packed_fwd": (_I, [_VP, _LL, _LL] * 4 + [_VP, _VP, _I, _I, _I, _I, _I, _F, _I, _VP, _SZ, _VP]),
+    "fa_packed_fwd": (_I, [_ARGS]),
     "fa_packed_fwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
-    "fa_packed_bwd": (_I, [_VP, _LL, _LL] * 5 + [_VP] + [_VP, _LL, _LL] * 3
-                      + [_VP, _I, _I, _I, _I, _I, _F, _I, _I, _VP, _SZ, _VP]),
+    "fa_packed_bwd": (_I, [_ARGS]),
     "fa_packed_bwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
-    "fa_qk_norm_rope": (_I, [_VP, _LL, _LL] * 2 + [_VP, _I, _I, _VP, _VP, _VP, _F, _I] + [_VP, _LL, _LL] * 2
-                        + [_I, _I, _I, _I, _VP]),
-    "fa_qk_norm_rope_bwd": (_I, [_VP, _LL, _LL] * 4 + [_VP, _I, _I, _VP, _VP, _VP, _F, _I] + [_VP, _LL, _LL] * 2
-                            + [_VP, _VP, _I, _I, _I, _I, _VP, _SZ, _VP]),
+    "fa_qk_norm_rope": (_I, [_ARGS]),
+    "fa_qk_norm_rope_bwd": (_I, [_ARGS]),
     "fa_qk_norm_rope_bwd_workspace_size": (_SZ, [_I, _I, _I, _I]),
-    "fa_kv4_append": (_I, [_VP] + [_VP, _LL, _LL] * 3 + [_VP, _I, _I, _VP, _VP, _VP, _F, _I] + [_VP, _LL, _LL] * 2
-                      + [_VP, _I, _I, _VP]),
+    "fa_kv4_append": (_I, [_ARGS]),
 }
 
 _lib = None
@@ -258,56 +256,47 @@ def fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q, page, width) -> int:
     return lib().fa_kv4_attn_workspace_size(B, H, Hkv, d, max_q, page, width)
 
 
-def fa_packed_fwd(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, o, o_token, o_head, lse, cu, B, T, H, Hkv,
-                  d, scale, causal, workspace, workspace_bytes, stream) -> int:
-    return lib().fa_packed_fwd(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, o, o_token, o_head, lse, cu,
-                               B, T, H, Hkv, d, float(scale), int(causal), workspace, workspace_bytes, stream)
+# The structures of include/fa_packed.h, field by field (fa_rows: address, token and head strides; a
+# NULL pointer is 0).  Packing one and passing its bytes takes a fraction of what ctypes does
+# to convert as many arguments: 0.4 us instead of 2.8 for 27.
+_ROWS = "Pqq"
+_PACKED_FWD = struct.Struct(_ROWS * 4 + "PP" + "iiiii" + "fi" + "PNP")
+_PACKED_BWD = struct.Struct(_ROWS * 5 + "P" + _ROWS * 3 + "P" + "iiiii" + "fii" + "PNP")
+_QK_NORM_ROPE = struct.Struct(_ROWS * 4 + "PPPP" + "iifi" + "iiii" + "P")
+_QK_NORM_ROPE_BWD = struct.Struct(_ROWS * 6 + "PPPPPP" + "iifi" + "iiii" + "PNP")
+_KV4_APPEND = struct.Struct("P" + _ROWS * 5 + "PPPPP" + "iifi" + "ii" + "P")
+
+
+def fa_packed_fwd(*fields) -> int:
+    return lib().fa_packed_fwd(_PACKED_FWD.pack(*fields))
 
 
 def fa_packed_fwd_workspace_size(B, T, H, Hkv, d) -> int:
     return lib().fa_packed_fwd_workspace_size(B, T, H, Hkv, d)
 
 
-def fa_packed_bwd(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, o, o_token, o_head, dO, do_token, do_head,
-                  lse, dq, dq_token, dq_head, dk, dk_token, dk_head, dv, dv_token, dv_head, cu, B, T, H, Hkv, d, scale,
-                  causal, variant, workspace, workspace_bytes, stream) -> int:
-    return lib().fa_packed_bwd(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, o, o_token, o_head, dO,
-                               do_token, do_head, lse, dq, dq_token, dq_head, dk, dk_token, dk_head, dv, dv_token,
-                               dv_head, cu, B, T, H, Hkv, d, float(scale), int(causal), variant, workspace,
-                               workspace_bytes, stream)
+def fa_packed_bwd(*fields) -> int:
+    return lib().fa_packed_bwd(_PACKED_BWD.pack(*fields))
 
 
 def fa_packed_bwd_workspace_size(B, T, H, Hkv, d, variant) -> int:
     return lib().fa_packed_bwd_workspace_size(B, T, H, Hkv, d, variant)
 
 
-def fa_qk_norm_rope(q, q_token, q_head, k, k_token, k_head, rotary, positions, rot, position, q_weight, k_weight, eps,
-                    interleaved, q_out, qo_token, qo_head, k_out, ko_token, ko_head, T, H, Hkv, d, stream) -> int:
-    return lib().fa_qk_norm_rope(q, q_token, q_head, k, k_token, k_head, rotary, positions, rot, position, q_weight,
-                                 k_weight, float(eps), int(interleaved), q_out, qo_token, qo_head, k_out, ko_token,
-                                 ko_head, T, H, Hkv, d, stream)
+def fa_qk_norm_rope(*fields) -> int:
+    return lib().fa_qk_norm_rope(_QK_NORM_ROPE.pack(*fields))
 
 
-def fa_qk_norm_rope_bwd(dq_out, dqo_token, dqo_head, dk_out, dko_token, dko_head, q, q_token, q_head, k, k_token, k_head,
-                        rotary, positions, rot, position, q_weight, k_weight, eps, interleaved, dq, dq_token, dq_head,
-                        dk, dk_token, dk_head, dq_weight, dk_weight, T, H, Hkv, d, workspace, workspace_bytes,
-                        stream) -> int:
-    return lib().fa_qk_norm_rope_bwd(dq_out, dqo_token, dqo_head, dk_out, dko_token, dko_head, q, q_token, q_head, k,
-                                     k_token, k_head, rotary, positions, rot, position, q_weight, k_weight, float(eps),
-                                     int(interleaved), dq, dq_token, dq_head, dk, dk_token, dk_head, dq_weight,
-                                     dk_weight, T, H, Hkv, d, workspace, workspace_bytes, stream)
+def fa_qk_norm_rope_bwd(*fields) -> int:
+    return lib().fa_qk_norm_rope_bwd(_QK_NORM_ROPE_BWD.pack(*fields))
 
 
 def fa_qk_norm_rope_bwd_workspace_size(T, H, Hkv, d) -> int:
     return lib().fa_qk_norm_rope_bwd_workspace_size(T, H, Hkv, d)
 
 
-def fa_kv4_append(cache, q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, rotary, positions, rot, position,
-                  q_weight, k_weight, eps, interleaved, q_out, qo_token, qo_head, k_out, ko_token, ko_head, slots, T, H,
-                  stream) -> int:
-    return lib().fa_kv4_append(cache, q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, rotary, positions,
-                               rot, position, q_weight, k_weight, float(eps), int(interleaved), q_out, qo_token,
-                               qo_head, k_out, ko_token, ko_head, slots, T, H, stream)
+def fa_kv4_append(*fields) -> int:
+    return lib().fa_kv4_append(_KV4_APPEND.pack(*fields))
 
 
 FA_KERNEL_ALL_KINDS = 19

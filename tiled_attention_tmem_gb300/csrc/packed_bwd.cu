@@ -5,7 +5,9 @@
 #include <type_traits>
 
 #include "bwd.cuh"
+#include "kv4_host.h"
 #include "packed_host.h"
+#include "packed_plan.cuh"
 
 namespace fa {
 namespace {
@@ -51,6 +53,8 @@ __device__ __forceinline__ bool tile_of_slot(const RowTiles& t, int ts, int& sta
 }
 
 struct RaggedPreParams {
+  RaggedPlanParams plan;
+  int plan_blocks;  // the first block makes the schedule, the next plan_blocks - 1 the tensor maps (0: no sequences)
   RowTiles tiles;
   RowsIn o, dO;
   const float* lse;
@@ -60,17 +64,23 @@ struct RaggedPreParams {
   RowsOut out[3];  // dq, dk, dv: their rows of no sequence are zeroed
 };
 
-// A block a tile slot at a time, GT threads a row: D_i = sum_c dO_ic O_ic (fp32) and the log2-domain
+// The plan, and beside it the rows: a block a tile slot at a time, GT threads a row: D_i = sum_c dO_ic O_ic (fp32) and the log2-domain
 // LSE, both negated, and (5-GEMM) zeros for the fp32 dQ rows.  Memory bounds it.
 template <int D>
 __global__ void __launch_bounds__(256) ragged_pre_kernel(const __grid_constant__ RaggedPreParams p) {
   grid_dep_wait();
+  if ((int)blockIdx.x < p.plan_blocks) {
+    if (blockIdx.x == 0) plan_schedule<256>(p.plan);
+    else plan_maps<256>(p.plan, blockIdx.x - 1, p.plan_blocks - 1);
+    return;
+  }
+  const int block = blockIdx.x - p.plan_blocks, blocks = gridDim.x - p.plan_blocks;
   constexpr int GT = D / 8 <= 32 ? D / 8 : 16;
   constexpr int CH = D / 8 / GT;
   const RowTiles& t = p.tiles;
   const int sub = threadIdx.x % GT;
   const long long work = (long long)t.slots * t.Hkv;
-  for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+  for (long long w = block; w < work; w += blocks) {
     const int ts = (int)(w / t.Hkv), kvh = (int)(w - (long long)ts * t.Hkv);
     int start, len, tok0;
     if (!tile_of_slot(t, ts, start, len, tok0)) continue;
@@ -137,7 +147,7 @@ __global__ void __launch_bounds__(256) ragged_pre_kernel(const __grid_constant__
   for (int x = 0; x < 3; ++x) {
     const int heads = x == 0 ? t.H : t.Hkv;
     const long long n = spare * heads * chunks;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    for (long long i = (long long)block * 256 + threadIdx.x; i < n; i += (long long)blocks * 256) {
       const long long row = i / (heads * chunks), rest = i - row * heads * chunks;
       const long long tok = row < lo ? row : hi + (row - lo);
       *reinterpret_cast<uint4*>(p.out[x].data + tok * p.out[x].token + rest / chunks * p.out[x].head +
@@ -190,17 +200,6 @@ __global__ void __launch_bounds__(256) ragged_conv_kernel(const __grid_constant_
   }
 }
 
-struct BwdCall {
-  PackedRows q, k, v, o, dO, dq, dk, dv;
-  const float* lse;
-  const int* cu;
-  PackedShape s;
-  float scale;
-  int causal;
-  void* workspace;
-  cudaStream_t st;
-};
-
 // The workspace: the plan, then lse2, dd and (5-GEMM) dqacc by query tiles.
 struct BwdLayout {
   int cuts, nmaps, slots;
@@ -215,14 +214,15 @@ struct BwdLayout {
   }
 };
 
-RowsIn in(const PackedRows& r) { return {static_cast<const uint16_t*>(r.data), r.token, r.head}; }
-RowsOut out(const PackedRows& r) { return {static_cast<uint16_t*>(r.data), r.token, r.head}; }
+RowsIn in(const fa_rows& r) { return {static_cast<const uint16_t*>(r.data), r.token, r.head}; }
+RowsOut out(const fa_rows& r) { return {static_cast<uint16_t*>(const_cast<void*>(r.data)), r.token, r.head}; }
 
 // KV: the dK/dV kernel; Q: the dQ kernel (void: 5-GEMM).  DP: the preprocess's head dimension.
 template <int DP, class KV, class Q>
-fa_status run(const BwdCall& c) {
+fa_status run(const fa_packed_bwd_args& c, const PackedShape& s) {
+  static std::atomic<unsigned long long> kv_raised{0}, q_raised{0};
   constexpr bool five = KV::DQ;
-  const PackedShape& s = c.s;
+  const cudaStream_t st = (cudaStream_t)c.stream;
   const BwdLayout lay(s, five ? FA_BWD_5GEMM : FA_BWD_7GEMM, KV::BM, KV::D);
   const PackedPlan plan = packed_plan_at(c.workspace, s.B, lay.cuts);
   uint8_t* at = static_cast<uint8_t*>(c.workspace) + lay.plan;
@@ -247,16 +247,16 @@ fa_status run(const BwdCall& c) {
     if ((e = packed_key_map(&maps[5], c.v, s, Q::BN)) != FA_OK) return e;
     cuts[1] = {128 / s.G(), Q::DQS, 4.0 * s.d};
   }
-  if (s.B > 0 && (e = run_packed_plan(plan, c.cu, s, cuts, lay.cuts, maps, lay.nmaps, 2, c.st)) != FA_OK) return e;
-
   const long long sms = sm_count_cached();
-  RaggedPreParams pre = {};
+  RaggedPreParams pre = {packed_plan_params(plan, c.cu, s, cuts, lay.cuts, maps, lay.nmaps, 2)};
+  pre.plan_blocks = s.B > 0 ? 1 + packed_map_blocks(s.B, lay.nmaps, 256) : 0;
   pre.tiles = {c.cu, s.B, s.T, s.H, s.Hkv, s.G(), tokens, KV::BM, lay.slots, s.d};
   pre.o = in(c.o), pre.dO = in(c.dO);
   pre.lse = c.lse, pre.lse2 = lse2, pre.dd = dd, pre.dqacc = dqacc;
   pre.out[0] = out(c.dq), pre.out[1] = out(c.dk), pre.out[2] = out(c.dv);
   const unsigned blocks = (unsigned)std::min<long long>((long long)(lay.slots + 1) * s.Hkv, 8 * sms);
-  if ((e = launch(FA_KERNEL_BWD_PRE, ragged_pre_kernel<DP>, dim3(blocks), dim3(256), 0, c.st, pre)) != FA_OK) return e;
+  if ((e = launch(FA_KERNEL_BWD_PRE, ragged_pre_kernel<DP>, dim3(pre.plan_blocks + blocks), dim3(256), 0, st, pre)) != FA_OK)
+    return e;
   if (s.B == 0) return FA_OK;  // (every row is of no sequence)
 
   RaggedKVParams p;
@@ -270,12 +270,12 @@ fa_status run(const BwdCall& c) {
   p.scale_log2 = c.scale * kLog2e, p.scale = c.scale, p.causal = c.causal;
   const unsigned kv_grid =
       (unsigned)std::min<long long>(((long long)s.T / KV::BN + s.B) * s.Hkv * KV::DSPLIT, sms);
-  if ((e = launch(five ? FA_KERNEL_BWD_KV5 : FA_KERNEL_BWD_KV7, bwd_kv_kernel<KV, false, RaggedKVParams>, dim3(kv_grid),
-                  dim3(KV::THREADS), KV::SMEM_BYTES, c.st, p)) != FA_OK)
+  if ((e = launch_raised(five ? FA_KERNEL_BWD_KV5 : FA_KERNEL_BWD_KV7, bwd_kv_kernel<KV, false, RaggedKVParams>,
+                         dim3(kv_grid), dim3(KV::THREADS), KV::SMEM_BYTES, st, p, kv_raised)) != FA_OK)
     return e;
   if constexpr (five) {
     RaggedConvParams conv = {pre.tiles, dqacc, out(c.dq), err, c.scale};
-    return launch(FA_KERNEL_BWD_CONV, ragged_conv_kernel<KV::D>, dim3(blocks), dim3(256), 0, c.st, conv);
+    return launch(FA_KERNEL_BWD_CONV, ragged_conv_kernel<KV::D>, dim3(blocks), dim3(256), 0, st, conv);
   } else {
     RaggedQParams r;
     if ((e = packed_query_map(&r.q_map, c.q, s, 128 / s.G())) != FA_OK) return e;
@@ -289,8 +289,8 @@ fa_status run(const BwdCall& c) {
     r.Hkv = s.Hkv, r.G = s.G(), r.tokens = 128 / s.G(), r.hd = s.d;
     r.scale_log2 = c.scale * kLog2e, r.scale = c.scale, r.causal = c.causal;
     const unsigned q_grid = (unsigned)std::min<long long>(((long long)s.T / r.tokens + s.B) * s.Hkv * Q::DQS, sms);
-    return launch(FA_KERNEL_BWD_Q7, bwd_q_kernel<Q, false, RaggedQParams>, dim3(q_grid), dim3(Q::THREADS),
-                  Q::SMEM_BYTES, c.st, r);
+    return launch_raised(FA_KERNEL_BWD_Q7, bwd_q_kernel<Q, false, RaggedQParams>, dim3(q_grid), dim3(Q::THREADS),
+                         Q::SMEM_BYTES, st, r, q_raised);
   }
 }
 
@@ -309,19 +309,15 @@ size_t packed_bwd_bytes(const PackedShape& s, int variant) {
   return BwdLayout(s, variant, tile_rows(s.d, variant), padded_head_dim(s.d)).total;
 }
 
-fa_status run_packed_bwd(const PackedRows& q, const PackedRows& k, const PackedRows& v, const PackedRows& o,
-                         const PackedRows& dO, const float* lse, const PackedRows& dq, const PackedRows& dk,
-                         const PackedRows& dv, const int* cu, const PackedShape& s, float scale, int causal,
-                         int variant, void* workspace, cudaStream_t st) {
-  const BwdCall c = {q, k, v, o, dO, dq, dk, dv, lse, cu, s, scale, causal, workspace, st};
-  const bool five = variant == FA_BWD_5GEMM;
+fa_status run_packed_bwd(const fa_packed_bwd_args& a, const PackedShape& s, int form) {
+  const bool five = form == FA_BWD_5GEMM;
   switch (s.d) {
-    case 64: return five ? run<64, RaggedKV5_64, void>(c) : run<64, KV7_64, Q7_64>(c);
+    case 64: return five ? run<64, RaggedKV5_64, void>(a, s) : run<64, KV7_64, Q7_64>(a, s);
     case 96:
-    case 128: return five ? run<128, KV5_128, void>(c) : run<128, KV7_128, Q7_128>(c);
-    case 192: return run<256, KV7_192, Q7_192>(c);
-    case 256: return run<256, KV7_256, Q7_256>(c);
-    case 384: return run<384, KV7_384, Q7_384>(c);
+    case 128: return five ? run<128, KV5_128, void>(a, s) : run<128, KV7_128, Q7_128>(a, s);
+    case 192: return run<256, KV7_192, Q7_192>(a, s);
+    case 256: return run<256, KV7_256, Q7_256>(a, s);
+    case 384: return run<384, KV7_384, Q7_384>(a, s);
   }
   return FA_ERR_UNSUPPORTED;
 }

@@ -8,12 +8,6 @@
 
 namespace fa {
 
-// One [T, heads, d] bf16 array with dense channels: strides in elements.
-struct PackedRows {
-  void* data;
-  long long token, head;
-};
-
 struct PackedShape {
   int B, T, H, Hkv, d;
   int G() const { return H / Hkv; }
@@ -38,26 +32,27 @@ struct PackedPlan {
 size_t packed_plan_bytes(int B, int cuts, int nmaps);
 // Lays the plan out at `at` (256-byte aligned) without launching anything.
 PackedPlan packed_plan_at(void* at, int B, int cuts);
-fa_status run_packed_plan(const PackedPlan& plan, const int* cu, const PackedShape& s, const PackedCut* cuts, int ncuts,
-                          const CUtensorMap* maps, int nmaps, int query_maps, cudaStream_t st);
+// The plan's parameters (packed_plan.cuh), the blocks that its maps keep busy, and its launch.
+struct RaggedPlanParams;
+RaggedPlanParams packed_plan_params(const PackedPlan& plan, const int* cu, const PackedShape& s, const PackedCut* cuts,
+                                    int ncuts, const CUtensorMap* maps, int nmaps, int query_maps);
+int packed_map_blocks(int B, int nmaps, int threads);
+fa_status run_packed_plan(const RaggedPlanParams& p, cudaStream_t st);
 
 // Tensor maps, of which the plan makes one for each sequence that ends with it (the first query_maps of
 // them are of queries): query rows
 // {d, G, T, Hkv} with a box of `tokens` tokens of all G heads, key rows {d, T, Hkv}.
-fa_status packed_query_map(CUtensorMap* map, const PackedRows& r, const PackedShape& s, int tokens);
-fa_status packed_key_map(CUtensorMap* map, const PackedRows& r, const PackedShape& s, int box_rows);
+fa_status packed_query_map(CUtensorMap* map, const fa_rows& r, const PackedShape& s, int tokens);
+fa_status packed_key_map(CUtensorMap* map, const fa_rows& r, const PackedShape& s, int box_rows);
 
 // Checks shared by the entry points.
 fa_status packed_shape_checks(const PackedShape& s, float scale, int causal);
-fa_status packed_rows_checks(const PackedRows& r, int T, int heads);
+fa_status packed_rows_checks(const fa_rows& r, int T, int heads);
 
-fa_status run_packed_fwd(const PackedRows& q, const PackedRows& k, const PackedRows& v, const PackedRows& o, float* lse,
-                         const int* cu, const PackedShape& s, float scale, int causal, void* workspace, cudaStream_t st);
+// Arguments checked, and not without work.  form: FA_BWD_5GEMM or FA_BWD_7GEMM.
+fa_status run_packed_fwd(const fa_packed_fwd_args& a, const PackedShape& s);
 size_t packed_fwd_bytes(const PackedShape& s);
-fa_status run_packed_bwd(const PackedRows& q, const PackedRows& k, const PackedRows& v, const PackedRows& o,
-                         const PackedRows& dO, const float* lse, const PackedRows& dq, const PackedRows& dk,
-                         const PackedRows& dv, const int* cu, const PackedShape& s, float scale, int causal,
-                         int variant, void* workspace, cudaStream_t st);
-size_t packed_bwd_bytes(const PackedShape& s, int variant);
+fa_status run_packed_bwd(const fa_packed_bwd_args& a, const PackedShape& s, int form);
+size_t packed_bwd_bytes(const PackedShape& s, int form);
 
 }  // namespace fa

@@ -335,19 +335,19 @@ __global__ void __launch_bounds__(1024) rotate_sum_kernel(const __grid_constant_
   }
 }
 
-struct Rows {
-  const void* data;
-  long long token, head;
-};
-
-fa_status rows_checks(const Rows& r, int heads) {
+fa_status rows_checks(const fa_rows& r, int heads) {
   if (heads == 0) return FA_OK;
   if (!r.data) return FA_ERR_INVALID_ARG;
   return aligned16(r.data) && !(r.token & 7) && !(r.head & 7) ? FA_OK : FA_ERR_MISALIGNED;
 }
 
-fa_status rotary_checks(const float* rotary, int positions, int rot, const int* position, const void* q_weight,
-                        const void* k_weight, float eps, int interleaved, int T, int H, int Hkv, int d) {
+// A: any of the argument structures.
+template <class A>
+fa_status rotary_checks(const A& a, int Hkv, int d) {
+  const int T = a.T, H = a.H, positions = a.positions, rot = a.rot, interleaved = a.interleaved;
+  const float eps = a.eps;
+  const float* rotary = a.rotary;
+  const int* position = a.position;
   if (T < 0 || H < 0 || Hkv < 0 || positions < 0 || rot < 0 || (interleaved != 0 && interleaved != 1))
     return FA_ERR_INVALID_ARG;
   if (!std::isfinite(eps) || eps < 0.f) return FA_ERR_INVALID_ARG;
@@ -356,14 +356,21 @@ fa_status rotary_checks(const float* rotary, int positions, int rot, const int* 
   if (T > (1 << 30) || (long long)H + 2LL * Hkv > 65535) return FA_ERR_INVALID_ARG;
   if (T == 0 || H + Hkv == 0) return FA_OK;
   if (!position || (rot > 0 && positions > 0 && !rotary)) return FA_ERR_INVALID_ARG;
-  if (!aligned16(rotary) || !aligned16(q_weight) || !aligned16(k_weight) || !all_aligned(4, position))
+  if (!aligned16(rotary) || !aligned16(a.q_weight) || !aligned16(a.k_weight) || !all_aligned(4, position))
     return FA_ERR_MISALIGNED;
   return FA_OK;
 }
 
-HeadRows head_rows(const Rows& in, const Rows& out, const void* weight, int heads) {
+HeadRows head_rows(const fa_rows& in, const fa_rows& out, const void* weight, int heads) {
   return {static_cast<const uint16_t*>(in.data), static_cast<uint16_t*>(const_cast<void*>(out.data)), in.token, in.head,
           out.token, out.head, static_cast<const uint16_t*>(weight), heads};
+}
+
+template <class A>
+void rotate_fill(RotateParams& p, const A& a, int Hkv) {
+  p.x[0] = head_rows(a.q, a.q_out, a.q_weight, a.H);
+  p.x[1] = head_rows(a.k, a.k_out, a.k_weight, Hkv);
+  p.rotary = a.rotary, p.position = a.position, p.positions = a.positions, p.rot = a.rot, p.T = a.T, p.eps = a.eps;
 }
 
 // Steps of heads a warp: kRotateSteps where that leaves 32 warps an SM, else one.
@@ -416,60 +423,45 @@ using namespace fa;
 
 extern "C" {
 
-fa_status fa_qk_norm_rope(const void* q, long long q_token, long long q_head, const void* k, long long k_token,
-                          long long k_head, const float* rotary, int positions, int rot, const int* position,
-                          const void* q_weight, const void* k_weight, float eps, int interleaved, void* q_out,
-                          long long qo_token, long long qo_head, void* k_out, long long ko_token, long long ko_head,
-                          int T, int H, int Hkv, int d, void* stream) {
-  fa_status s = rotary_checks(rotary, positions, rot, position, q_weight, k_weight, eps, interleaved, T, H, Hkv, d);
+fa_status fa_qk_norm_rope(const fa_qk_norm_rope_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  fa_status s = rotary_checks(*a, a->Hkv, a->d);
   if (s != FA_OK) return s;
-  if (T == 0 || H + Hkv == 0) return FA_OK;
-  const Rows rq = {q, q_token, q_head}, rk = {k, k_token, k_head}, oq = {q_out, qo_token, qo_head},
-             ok = {k_out, ko_token, ko_head};
-  for (const Rows* r : {&rq, &oq})
-    if ((s = rows_checks(*r, H)) != FA_OK) return s;
-  for (const Rows* r : {&rk, &ok})
-    if ((s = rows_checks(*r, Hkv)) != FA_OK) return s;
+  if (a->T == 0 || a->H + a->Hkv == 0) return FA_OK;
+  for (const fa_rows* r : {&a->q, &a->q_out})
+    if ((s = rows_checks(*r, a->H)) != FA_OK) return s;
+  for (const fa_rows* r : {&a->k, &a->k_out})
+    if ((s = rows_checks(*r, a->Hkv)) != FA_OK) return s;
   RotateParams p = {};
-  p.x[0] = head_rows(rq, oq, q_weight, H);
-  p.x[1] = head_rows(rk, ok, k_weight, Hkv);
-  p.rotary = rotary, p.position = position, p.positions = positions, p.rot = rot, p.T = T, p.eps = eps;
-  return rotate_by_dim<false>(p, d, interleaved, (cudaStream_t)stream);
+  rotate_fill(p, *a, a->Hkv);
+  return rotate_by_dim<false>(p, a->d, a->interleaved, (cudaStream_t)a->stream);
 }
 
-fa_status fa_kv4_append(const fa_kv4_cache* cache, const void* q, long long q_token, long long q_head, const void* k,
-                        long long k_token, long long k_head, const void* v, long long v_token, long long v_head,
-                        const float* rotary, int positions, int rot, const int* position, const void* q_weight,
-                        const void* k_weight, float eps, int interleaved, void* q_out, long long qo_token,
-                        long long qo_head, void* k_out, long long ko_token, long long ko_head, const long long* slots,
-                        int T, int H, void* stream) {
+fa_status fa_kv4_append(const fa_kv4_append_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  const fa_kv4_cache* cache = a->cache;
   fa_status s = kv4_cache_checks(cache);
   if (s != FA_OK) return s;
   const int Hkv = cache->Hkv;
-  s = rotary_checks(rotary, positions, rot, position, q_weight, k_weight, eps, interleaved, T, H, Hkv, cache->d);
-  if (s != FA_OK) return s;
-  if (T == 0 || H + Hkv == 0) return FA_OK;
-  const Rows rq = {q, q_token, q_head}, rk = {k, k_token, k_head}, rv = {v, v_token, v_head},
-             oq = {q_out, qo_token, qo_head}, ok = {k_out, ko_token, ko_head};
-  for (const Rows* r : {&rq, &oq})
-    if ((s = rows_checks(*r, H)) != FA_OK) return s;
-  for (const Rows* r : {&rk, &rv})
+  if ((s = rotary_checks(*a, Hkv, cache->d)) != FA_OK) return s;
+  if (a->T == 0 || a->H + Hkv == 0) return FA_OK;
+  for (const fa_rows* r : {&a->q, &a->q_out})
+    if ((s = rows_checks(*r, a->H)) != FA_OK) return s;
+  for (const fa_rows* r : {&a->k, &a->v})
     if ((s = rows_checks(*r, Hkv)) != FA_OK) return s;
-  if (k_out && (s = rows_checks(ok, Hkv)) != FA_OK) return s;
-  if (!slots) return FA_ERR_INVALID_ARG;
-  if (!all_aligned(8, slots)) return FA_ERR_MISALIGNED;
+  if (a->k_out.data && (s = rows_checks(a->k_out, Hkv)) != FA_OK) return s;
+  if (!a->slots) return FA_ERR_INVALID_ARG;
+  if (!all_aligned(8, a->slots)) return FA_ERR_MISALIGNED;
   RotateParams p = {};
-  p.x[0] = head_rows(rq, oq, q_weight, H);
-  p.x[1] = head_rows(rk, ok, k_weight, Hkv);
-  p.x[2] = head_rows(rv, {}, nullptr, Hkv);
-  p.rotary = rotary, p.position = position, p.positions = positions, p.rot = rot, p.T = T, p.eps = eps;
+  rotate_fill(p, *a, Hkv);
+  p.x[2] = head_rows(a->v, {}, nullptr, Hkv);
   p.codes[0] = static_cast<uint8_t*>(cache->k_codes), p.codes[1] = static_cast<uint8_t*>(cache->v_codes);
   p.scales[0] = static_cast<uint8_t*>(cache->k_scales), p.scales[1] = static_cast<uint8_t*>(cache->v_scales);
-  p.slots = slots;
+  p.slots = a->slots;
   p.inv_gain[0] = 1.f / cache->k_gain, p.inv_gain[1] = 1.f / cache->v_gain;
   p.page_log2 = page_log2_of(cache->page);
   p.slot_end = (long long)cache->pages * cache->page;
-  return rotate_by_dim<true>(p, cache->d, interleaved, (cudaStream_t)stream);
+  return rotate_by_dim<true>(p, cache->d, a->interleaved, (cudaStream_t)a->stream);
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_size(int T, int H, int Hkv, int d) {
@@ -477,51 +469,45 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int T, int H, int Hkv, int d) {
   return (size_t)rotate_bwd_blocks(T, H, Hkv) * d * sizeof(float);
 }
 
-fa_status fa_qk_norm_rope_bwd(const void* dq_out, long long dqo_token, long long dqo_head, const void* dk_out,
-                              long long dko_token, long long dko_head, const void* q, long long q_token,
-                              long long q_head, const void* k, long long k_token, long long k_head,
-                              const float* rotary, int positions, int rot, const int* position, const void* q_weight,
-                              const void* k_weight, float eps, int interleaved, void* dq, long long dq_token,
-                              long long dq_head, void* dk, long long dk_token, long long dk_head, float* dq_weight,
-                              float* dk_weight, int T, int H, int Hkv, int d, void* workspace, size_t workspace_bytes,
-                              void* stream) {
-  fa_status s = rotary_checks(rotary, positions, rot, position, q_weight, k_weight, eps, interleaved, T, H, Hkv, d);
+fa_status fa_qk_norm_rope_bwd(const fa_qk_norm_rope_bwd_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  const int T = a->T, H = a->H, Hkv = a->Hkv, d = a->d;
+  fa_status s = rotary_checks(*a, Hkv, d);
   if (s != FA_OK) return s;
   // A weight's gradient is written where there is the weight.
-  if ((q_weight && !dq_weight) || (k_weight && !dk_weight)) return FA_ERR_INVALID_ARG;
-  if (!all_aligned(4, dq_weight, dk_weight)) return FA_ERR_MISALIGNED;
-  const bool weights = q_weight || k_weight;
-  const cudaStream_t st = (cudaStream_t)stream;
+  if ((a->q_weight && !a->dq_weight) || (a->k_weight && !a->dk_weight)) return FA_ERR_INVALID_ARG;
+  if (!all_aligned(4, a->dq_weight, a->dk_weight)) return FA_ERR_MISALIGNED;
+  const cudaStream_t st = (cudaStream_t)a->stream;
+  float *const wq_out = a->q_weight ? a->dq_weight : nullptr, *const wk_out = a->k_weight ? a->dk_weight : nullptr;
   if (T == 0 || H + Hkv == 0) {
-    for (float* w : {q_weight ? dq_weight : nullptr, k_weight ? dk_weight : nullptr})
+    for (float* w : {wq_out, wk_out})
       if (w) {
         const cudaError_t e = cudaMemsetAsync(w, 0, d * sizeof(float), st);
         if (e != cudaSuccess) return record_cuda_error(e);
       }
     return FA_OK;
   }
-  const Rows gq = {dq_out, dqo_token, dqo_head}, gk = {dk_out, dko_token, dko_head}, rq = {q, q_token, q_head},
-             rk = {k, k_token, k_head}, oq = {dq, dq_token, dq_head}, ok = {dk, dk_token, dk_head};
-  for (const Rows* r : {&gq, &oq})
+  for (const fa_rows* r : {&a->dq_out, &a->dq})
     if ((s = rows_checks(*r, H)) != FA_OK) return s;
-  for (const Rows* r : {&gk, &ok})
+  for (const fa_rows* r : {&a->dk_out, &a->dk})
     if ((s = rows_checks(*r, Hkv)) != FA_OK) return s;
-  if ((q_weight && (s = rows_checks(rq, H)) != FA_OK) || (k_weight && (s = rows_checks(rk, Hkv)) != FA_OK)) return s;
+  if ((a->q_weight && (s = rows_checks(a->q, H)) != FA_OK) || (a->k_weight && (s = rows_checks(a->k, Hkv)) != FA_OK))
+    return s;
   const int blocks = rotate_bwd_blocks(T, H, Hkv);
-  if (weights && (!workspace || !all_aligned(256, static_cast<char*>(workspace)) ||
-                  workspace_bytes < (size_t)blocks * d * sizeof(float)))
+  const bool weights = wq_out || wk_out;
+  if (weights && (!a->workspace || !all_aligned(256, static_cast<char*>(a->workspace)) ||
+                  a->workspace_bytes < (size_t)blocks * d * sizeof(float)))
     return FA_ERR_WORKSPACE;
   RotateBwdParams p = {};
-  p.dy[0] = head_rows(gq, oq, nullptr, H);
-  p.dy[1] = head_rows(gk, ok, nullptr, Hkv);
-  p.x[0] = head_rows(rq, {}, q_weight, H);
-  p.x[1] = head_rows(rk, {}, k_weight, Hkv);
-  p.rotary = rotary, p.position = position, p.positions = positions, p.rot = rot, p.T = T, p.eps = eps;
+  p.dy[0] = head_rows(a->dq_out, a->dq, nullptr, H);
+  p.dy[1] = head_rows(a->dk_out, a->dk, nullptr, Hkv);
+  p.x[0] = head_rows(a->q, {}, a->q_weight, H);
+  p.x[1] = head_rows(a->k, {}, a->k_weight, Hkv);
+  p.rotary = a->rotary, p.position = a->position, p.positions = a->positions, p.rot = a->rot, p.T = T, p.eps = a->eps;
   // Blocks by the bytes of each: a head costs more where it has a norm, whose input is read.
-  const double wq = H * (q_weight ? 3.0 : 2.0), wk = Hkv * (k_weight ? 3.0 : 2.0);
+  const double wq = H * (wq_out ? 3.0 : 2.0), wk = Hkv * (wk_out ? 3.0 : 2.0);
   p.q_blocks = std::min(blocks - 1, std::max(1, (int)std::lround(blocks * wq / (wq + wk))));
-  p.part = weights ? static_cast<float*>(workspace) : nullptr;
-  float *const wq_out = q_weight ? dq_weight : nullptr, *const wk_out = k_weight ? dk_weight : nullptr;
+  p.part = weights ? static_cast<float*>(a->workspace) : nullptr;
   const auto run = [&](auto next) -> fa_status {
     constexpr bool NEXT = decltype(next)::value;
     switch (d) {
@@ -534,7 +520,7 @@ fa_status fa_qk_norm_rope_bwd(const void* dq_out, long long dqo_token, long long
     }
     return FA_ERR_UNSUPPORTED;
   };
-  return interleaved ? run(std::true_type{}) : run(std::false_type{});
+  return a->interleaved ? run(std::true_type{}) : run(std::false_type{});
 }
 
 }  // extern "C"

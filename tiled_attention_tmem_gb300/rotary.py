@@ -33,7 +33,7 @@ def _angles(rotary, positions, T, d, index):
 
 def _weight(w, name, d, index):
     if w is None:
-        return None
+        return 0
     if not (isinstance(w, _Tensor) and w.dtype is _BF16 and w.shape == (d,) and w.get_device() == index
             and w.is_contiguous()):
         _dense(w, name, _BF16, (d,), index)
@@ -79,9 +79,9 @@ def qk_norm_rope(q, k, rotary, positions, q_weight=None, k_weight=None, eps: flo
     table, many, turned, at = _angles(rotary, positions, T, d, index)
     wq, wk = _weight(q_weight, "q_weight", d, index), _weight(k_weight, "k_weight", d, index)
     q_out, (qot, qoh), k_out, (kot, koh) = _outputs(out, ("q", "k"), q, k, index)
-    st = _b.lib().fa_qk_norm_rope(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, table, many, turned, at, wq, wk, eps,
-                                  bool(interleaved), q_out.data_ptr(), qot, qoh, k_out.data_ptr(), kot, koh, T, H, Hkv,
-                                  d, _current_stream(index))
+    st = _b.fa_qk_norm_rope(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, q_out.data_ptr(), qot, qoh, k_out.data_ptr(), kot,
+                            koh, table, at, wq, wk, many, turned, eps, bool(interleaved), T, H, Hkv, d,
+                            _current_stream(index))
     if st:
         _check(st, "fa_qk_norm_rope")
     return q_out, k_out
@@ -115,15 +115,14 @@ def qk_norm_rope_backward(dq, dk, q, k, rotary, positions, q_weight=None, k_weig
     table, many, turned, at = _angles(rotary, positions, T, d, index)
     wq, wk = _weight(q_weight, "q_weight", d, index), _weight(k_weight, "k_weight", d, index)
     q_out, (qot, qoh), k_out, (kot, koh) = _outputs(grads, ("dq", "dk"), q, k, index)
-    dwq = None if wq is None else _empty(d, dtype=_F32, device=q.device)
-    dwk = None if wk is None else _empty(d, dtype=_F32, device=q.device)
-    need = 0 if wq is None and wk is None else _sum_bytes(T, H, Hkv, d, index)
+    dwq = None if q_weight is None else _empty(d, dtype=_F32, device=q.device)
+    dwk = None if k_weight is None else _empty(d, dtype=_F32, device=q.device)
+    need = 0 if q_weight is None and k_weight is None else _sum_bytes(T, H, Hkv, d, index)
     workspace, ws, need = _workspace(workspace, need, index, q.device)
-    st = _b.lib().fa_qk_norm_rope_bwd(dq.data_ptr(), gqt, gqh, dk.data_ptr(), gkt, gkh, q.data_ptr(), qt, qh, k.data_ptr(),
-                                      kt, kh, table, many, turned, at, wq, wk, eps, bool(interleaved), q_out.data_ptr(),
-                                      qot, qoh, k_out.data_ptr(), kot, koh, None if dwq is None else dwq.data_ptr(),
-                                      None if dwk is None else dwk.data_ptr(), T, H, Hkv, d, ws, need,
-                                      _current_stream(index))
+    st = _b.fa_qk_norm_rope_bwd(dq.data_ptr(), gqt, gqh, dk.data_ptr(), gkt, gkh, q.data_ptr(), qt, qh, k.data_ptr(), kt,
+                                kh, q_out.data_ptr(), qot, qoh, k_out.data_ptr(), kot, koh, table, at, wq, wk,
+                                0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr(), many,
+                                turned, eps, bool(interleaved), T, H, Hkv, d, ws, need, _current_stream(index))
     if st:
         _check(st, "fa_qk_norm_rope_bwd")
     return q_out, k_out, dwq, dwk
@@ -158,11 +157,11 @@ def kv4_append(q, k, v, rotary, positions, slots, cache: KV4Cache, q_weight=None
         ot, oh = H * d, d
     else:
         ot, oh = _rows(out, "out", q.shape, index, written=True)
-    ko, (kot, koh) = (None, (0, 0)) if k_out is None else (
+    ko, (kot, koh) = (0, (0, 0)) if k_out is None else (
         k_out.data_ptr(), _rows(k_out, "k_out", shape, index, written=True))
-    st = _b.lib().fa_kv4_append(c.address, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, table, many,
-                                turned, at, wq, wk, eps, bool(interleaved), out.data_ptr(), ot, oh, ko, kot, koh,
-                                slots.data_ptr(), T, H, _current_stream(index))
+    st = _b.fa_kv4_append(c.address, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out.data_ptr(), ot,
+                          oh, ko, kot, koh, table, at, wq, wk, slots.data_ptr(), many, turned, eps, bool(interleaved), T,
+                          H, _current_stream(index))
     if st:
         _check(st, "fa_kv4_append")
     return out
