@@ -310,9 +310,7 @@ struct BwdKVCfg {
   static constexpr bool SPLITPACK = !SEP && NCW == 2;
   static __device__ __forceinline__ int pcol(int c) { return SPLITPACK ? (c / CW) * CW + (c % CW) / 2 : c / 2; }
   static constexpr int DRAIN_W0 = 4 + 4 * NCW;  // first dQ drain warp (5-GEMM)
-  // dQ^T (lanes = d) vs dQ (lanes = query).  With d = 64 and 64 queries the A operand K^T has 64 of the
-  // 128 rows; the panel behind K's, V's, is read for the others, whose results are dropped.
-  static constexpr bool DQ_T = DQ && (D == 128 || BM == 64);
+  static constexpr bool DQ_T = DQ && D == 128;  // dQ^T (lanes = d) vs dQ (lanes = query)
   static constexpr int BN = 128;
   static constexpr int DH = OS ? D : D / DSPLIT;  // accumulator columns per item
   static constexpr int PANELS = D / 64;
@@ -370,8 +368,8 @@ struct BwdKVCfg {
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(!SEP || QS >= 2, "overlapped order needs two query stages");
   static_assert(!DQ || DSPLIT == 1, "5-GEMM keeps all of dQ's columns");
-  static_assert(!DQ_T || (BM == 64 && (D == 128 || (D == 64 && !VT))), "dQ^T path needs 128 columns from K on");
-  static_assert(!DQ || DQ_T || (D == 64 && BM == 128), "dQ path needs M = BM = 128");
+  static_assert(!DQ || D == 64 ? true : (D == 128 && BM == 64), "dQ^T path needs M = d = 128");
+  static_assert(!(DQ && D == 64) || BM == 128, "dQ path needs M = BM = 128");
   static_assert(!VT || (!EARLY && NCW == 1), "V in TMEM is written by the single compute warpgroup");
   static_assert(!OS || (VT && !DQ && !SEP && DSPLIT == 2), "output split: dV item and dK item per key tile");
 };
@@ -1279,10 +1277,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           }
           if constexpr (C::DQ_T) {
             // lanes = d index lr, columns = query q: 32 lanes write 128 contiguous bytes of row q
-            if (D == 128 || lr < D) {
 #pragma unroll
-              for (int q = 0; q < COLS; ++q) stg[q * D + dq_swz(q, lr)] = __uint_as_float(v[q]);
-            }
+            for (int q = 0; q < COLS; ++q) stg[q * D + dq_swz(q, lr)] = __uint_as_float(v[q]);
           } else {
             // lanes = query row lr, columns = d
 #pragma unroll
@@ -2053,9 +2049,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
 // into its own S^T / dP^T columns.
 using KV5_64 = BwdKVCfg<64, 128, true, 1, 2, false>;
 using KV5_128 = BwdKVCfg<128, 64, true, 1, 3, true>;
-// Packed sequences at d = 64: the order of d = 128 (S and dP of the next tile during this one's softmax),
-// 64 queries per step.
-using RaggedKV5_64 = BwdKVCfg<64, 64, true, 1, 5, true>;
 using KV7_64 = BwdKVCfg<64, 128, false, 1, 3, false>;
 using KV7_128 = BwdKVCfg<128, 64, false, 1, 4, true>;
 // d = 192: dV and dK for all 192 columns fit TMEM next to S and dP, so no d split.

@@ -30,22 +30,32 @@ struct RowTiles {
   int B, T, H, Hkv, G;
   int tokens, rows, slots;
   int hd;
+  int by_G;  // 65536 / G rounded up: r / G = r * by_G >> 16 for r < 128, G <= 32
 };
 
 // The sequence that holds tile slot ts, and the slot's first token in it; false where none does.
-// Sequence b has the slots from cu[b] / tokens + b on, which grow with b.
+// Sequence b has the slots from cu[b] / tokens + b on, which grow with b: a warp looks at 32 of
+// them at a time.
 __device__ __forceinline__ bool tile_of_slot(const RowTiles& t, int ts, int& start, int& len, int& tok0) {
-  int lo = 0, hi = t.B;  // the last b whose first slot is not past ts
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if ((long long)min(max(t.cu[mid], 0), t.T) / t.tokens + mid <= ts) lo = mid;
-    else hi = mid;
-  }
   if (t.B == 0) return false;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, end = t.B;  // the last b in [lo, end) whose first slot is not past ts (or lo)
+  while (end - lo > 1) {
+    const int step = (end - lo + 31) / 32, b = lo + lane * step;
+    const bool past = b >= end || (long long)min(max(t.cu[b], 0), t.T) / t.tokens + b > ts;
+    const unsigned mask = __ballot_sync(0xffffffffu, past);
+    const int first = mask ? __ffs(mask) - 1 : 32;
+    if (first == 0) {
+      end = lo + 1;
+    } else {
+      lo += (first - 1) * step;
+      end = min(end, lo + step);
+    }
+  }
   start = t.cu[lo];
-  const int end = t.cu[lo + 1];
-  if (start < 0 || start > end || end > t.T) return false;
-  len = end - start;
+  const int stop = t.cu[lo + 1];
+  if (start < 0 || start > stop || stop > t.T) return false;
+  len = stop - start;
   const long long first = (long long)ts - start / t.tokens - lo;
   if (first < 0 || first * t.tokens >= len) return false;
   tok0 = (int)first * t.tokens;
@@ -67,7 +77,7 @@ struct RaggedPreParams {
 // The plan, and beside it the rows: a block a tile slot at a time, GT threads a row: D_i = sum_c dO_ic O_ic (fp32) and the log2-domain
 // LSE, both negated, and (5-GEMM) zeros for the fp32 dQ rows.  Memory bounds it.
 template <int D>
-__global__ void __launch_bounds__(256) ragged_pre_kernel(const __grid_constant__ RaggedPreParams p) {
+__global__ void __launch_bounds__(256, D <= 256 ? 4 : 2) ragged_pre_kernel(const __grid_constant__ RaggedPreParams p) {
   grid_dep_wait();
   if ((int)blockIdx.x < p.plan_blocks) {
     if (blockIdx.x == 0) plan_schedule<256>(p.plan);
@@ -92,7 +102,7 @@ __global__ void __launch_bounds__(256) ragged_pre_kernel(const __grid_constant__
       float lse[UN];
 #pragma unroll
       for (int i = 0; i < UN; ++i) {
-        const int r = r0 + i * STEP, of = r / t.G, tok = tok0 + of, head = kvh * t.G + r - of * t.G;
+        const int r = r0 + i * STEP, of = (r * t.by_G) >> 16, tok = tok0 + of, head = kvh * t.G + r - of * t.G;
         const bool have = of < t.tokens && r < t.rows && tok < len;
         const uint16_t* o = p.o.data + (have ? (start + tok) * p.o.token + head * p.o.head : 0);
         const uint16_t* g = p.dO.data + (have ? (start + tok) * p.dO.token + head * p.dO.head : 0);
@@ -164,13 +174,13 @@ struct RaggedConvParams {
   float scale;
 };
 
-// dq = scale * the fp32 sums (5-GEMM), bf16.  A block a tile slot, eight columns a thread.  Memory bounds it.
+// dq = scale * the fp32 sums (5-GEMM), bf16.  A block a tile slot, eight columns a thread, four rows at a
+// time.  Memory bounds it.
 template <int D>
 __global__ void __launch_bounds__(256) ragged_conv_kernel(const __grid_constant__ RaggedConvParams p) {
   grid_dep_wait();
   if (*reinterpret_cast<volatile const int*>(p.err) != 0) return;
   const RowTiles& t = p.tiles;
-  const int chunks = t.hd / 8;
   const long long work = (long long)t.slots * t.Hkv;
   for (long long w = blockIdx.x; w < work; w += gridDim.x) {
     const int ts = (int)(w / t.Hkv), kvh = (int)(w - (long long)ts * t.Hkv);
@@ -178,20 +188,22 @@ __global__ void __launch_bounds__(256) ragged_conv_kernel(const __grid_constant_
     if (!tile_of_slot(t, ts, start, len, tok0)) continue;
     const int rows = min(t.tokens, len - tok0) * t.G;
     const float* slot = p.dqacc + ((size_t)kvh * t.slots + ts) * t.rows * D;
-    constexpr int UN = 4;
+    constexpr int GT = D / 8, STEP = 256 / GT, UN = 4;
+    const int c = threadIdx.x % GT * 8;
+    if (c >= t.hd) continue;
 #pragma unroll 1
-    for (int i0 = threadIdx.x; i0 < rows * chunks; i0 += UN * 256) {
+    for (int r0 = threadIdx.x / GT; r0 < rows; r0 += UN * STEP) {
       float4 a[UN], b[UN];
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
-        const int i = min(i0 + u * 256, rows * chunks - 1), r = i / chunks, c = (i - r * chunks) * 8;
+        const int r = min(r0 + u * STEP, rows - 1);
         a[u] = *reinterpret_cast<const float4*>(slot + r * D + dq_swz(r, c));
         b[u] = *reinterpret_cast<const float4*>(slot + r * D + dq_swz(r, c + 4));
       }
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
-        const int i = i0 + u * 256, r = i / chunks, c = (i - r * chunks) * 8, of = r / t.G;
-        if (i >= rows * chunks) break;
+        const int r = r0 + u * STEP, of = (r * t.by_G) >> 16;
+        if (r >= rows) break;
         *reinterpret_cast<uint4*>(p.dq.data + (start + tok0 + of) * p.dq.token + (kvh * t.G + r - of * t.G) * p.dq.head + c) =
             make_uint4(pack_bf16(a[u].x * p.scale, a[u].y * p.scale), pack_bf16(a[u].z * p.scale, a[u].w * p.scale),
                        pack_bf16(b[u].x * p.scale, b[u].y * p.scale), pack_bf16(b[u].z * p.scale, b[u].w * p.scale));
@@ -250,11 +262,12 @@ fa_status run(const fa_packed_bwd_args& c, const PackedShape& s) {
   const long long sms = sm_count_cached();
   RaggedPreParams pre = {packed_plan_params(plan, c.cu, s, cuts, lay.cuts, maps, lay.nmaps, 2)};
   pre.plan_blocks = s.B > 0 ? 1 + packed_map_blocks(s.B, lay.nmaps, 256) : 0;
-  pre.tiles = {c.cu, s.B, s.T, s.H, s.Hkv, s.G(), tokens, KV::BM, lay.slots, s.d};
+  pre.tiles = {c.cu, s.B, s.T, s.H, s.Hkv, s.G(), tokens, KV::BM, lay.slots, s.d,
+               (65536 + s.G() - 1) / s.G()};
   pre.o = in(c.o), pre.dO = in(c.dO);
   pre.lse = c.lse, pre.lse2 = lse2, pre.dd = dd, pre.dqacc = dqacc;
   pre.out[0] = out(c.dq), pre.out[1] = out(c.dk), pre.out[2] = out(c.dv);
-  const unsigned blocks = (unsigned)std::min<long long>((long long)(lay.slots + 1) * s.Hkv, 8 * sms);
+  const unsigned blocks = (unsigned)std::min<long long>((long long)(lay.slots + 1) * s.Hkv, 4 * sms);
   if ((e = launch(FA_KERNEL_BWD_PRE, ragged_pre_kernel<DP>, dim3(pre.plan_blocks + blocks), dim3(256), 0, st, pre)) != FA_OK)
     return e;
   if (s.B == 0) return FA_OK;  // (every row is of no sequence)
@@ -295,24 +308,21 @@ fa_status run(const fa_packed_bwd_args& c, const PackedShape& s) {
 }
 
 // Query rows of a tile of the dK/dV kernels.
-int tile_rows(int d, int variant) {
-  if (d == 64) return variant == FA_BWD_5GEMM ? 64 : 128;
-  return d == 384 ? 32 : 64;
-}
-static_assert(RaggedKV5_64::BM == 64 && KV7_64::BM == 128 && KV5_128::BM == 64 && KV7_128::BM == 64 && KV7_192::BM == 64 &&
+int tile_rows(int d) { return d == 64 ? 128 : d == 384 ? 32 : 64; }
+static_assert(KV5_64::BM == 128 && KV7_64::BM == 128 && KV5_128::BM == 64 && KV7_128::BM == 64 && KV7_192::BM == 64 &&
                   KV7_256::BM == 64 && KV7_384::BM == 32,
               "tile_rows");
 
 }  // namespace
 
 size_t packed_bwd_bytes(const PackedShape& s, int variant) {
-  return BwdLayout(s, variant, tile_rows(s.d, variant), padded_head_dim(s.d)).total;
+  return BwdLayout(s, variant, tile_rows(s.d), padded_head_dim(s.d)).total;
 }
 
 fa_status run_packed_bwd(const fa_packed_bwd_args& a, const PackedShape& s, int form) {
   const bool five = form == FA_BWD_5GEMM;
   switch (s.d) {
-    case 64: return five ? run<64, RaggedKV5_64, void>(a, s) : run<64, KV7_64, Q7_64>(a, s);
+    case 64: return five ? run<64, KV5_64, void>(a, s) : run<64, KV7_64, Q7_64>(a, s);
     case 96:
     case 128: return five ? run<128, KV5_128, void>(a, s) : run<128, KV7_128, Q7_128>(a, s);
     case 192: return run<256, KV7_192, Q7_192>(a, s);
