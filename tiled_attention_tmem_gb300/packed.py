@@ -40,11 +40,9 @@ def _sequences(cu, index):
     return cu.shape[0] - 1
 
 
-def _scale(scale, d):
-    """fp32 of a number too large for it is an infinity, which the library refuses."""
-    if scale is None:
-        return d ** -0.5
-    return scale if -3e38 < scale < 3e38 else float("inf")
+def _f32(x):
+    """A number to pass as fp32: one too large for it is an infinity, which the library refuses."""
+    return x if -3e38 < x < 3e38 else float("inf")
 
 
 def _workspace(workspace, need, index, device):
@@ -110,8 +108,8 @@ def packed_attention_forward(q, k, v, cu, scale: float | None = None, causal: bo
         _dense(lse, "lse", _F32, (T, H), index)
     workspace, at, need = _workspace(workspace, _forward_bytes(B, T, H, Hkv, d), index, q.device)
     st = _b.fa_packed_fwd(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out.data_ptr(), ot, oh,
-                          lse.data_ptr(), cu.data_ptr(), B, T, H, Hkv, d, _scale(scale, d), bool(causal), at, need,
-                          _current_stream(index))
+                          lse.data_ptr(), cu.data_ptr(), B, T, H, Hkv, d, d ** -0.5 if scale is None else _f32(scale),
+                          bool(causal), at, need, _current_stream(index))
     if st:
         _check(st, "fa_packed_fwd")
     return out, lse
@@ -157,8 +155,9 @@ def packed_attention_backward(q, k, v, o, do, lse, cu, scale: float | None = Non
     workspace, at, need = _workspace(workspace, _backward_bytes(B, T, H, Hkv, d, variant), index, q.device)
     st = _b.fa_packed_bwd(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, o.data_ptr(), ot, oh,
                           do.data_ptr(), gt, gh, lse.data_ptr(), dq.data_ptr(), qgt, qgh, dk.data_ptr(), kgt, kgh,
-                          dv.data_ptr(), vgt, vgh, cu.data_ptr(), B, T, H, Hkv, d, _scale(scale, d), bool(causal),
-                          variant, at, need, _current_stream(index))
+                          dv.data_ptr(), vgt, vgh, cu.data_ptr(), B, T, H, Hkv, d,
+                          d ** -0.5 if scale is None else _f32(scale), bool(causal), variant, at, need,
+                          _current_stream(index))
     if st:
         _check(st, "fa_packed_bwd")
     return dq, dk, dv

@@ -10,7 +10,7 @@ from __future__ import annotations
 import functools
 
 from . import binding as _b
-from .packed import _device_index, _workspace
+from .packed import _device_index, _f32, _workspace
 from .serving import (_BF16, _F32, _I32, _MOST, KV4Cache, _On, _Tensor, _check, _check_sizes, _current_device,
                       _current_stream, _dense, _empty, _rows, _slot_count)
 
@@ -80,7 +80,7 @@ def qk_norm_rope(q, k, rotary, positions, q_weight=None, k_weight=None, eps: flo
     wq, wk = _weight(q_weight, "q_weight", d, index), _weight(k_weight, "k_weight", d, index)
     q_out, (qot, qoh), k_out, (kot, koh) = _outputs(out, ("q", "k"), q, k, index)
     st = _b.fa_qk_norm_rope(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, q_out.data_ptr(), qot, qoh, k_out.data_ptr(), kot,
-                            koh, table, at, wq, wk, many, turned, eps, bool(interleaved), T, H, Hkv, d,
+                            koh, table, at, wq, wk, many, turned, _f32(eps), bool(interleaved), T, H, Hkv, d,
                             _current_stream(index))
     if st:
         _check(st, "fa_qk_norm_rope")
@@ -122,7 +122,7 @@ def qk_norm_rope_backward(dq, dk, q, k, rotary, positions, q_weight=None, k_weig
     st = _b.fa_qk_norm_rope_bwd(dq.data_ptr(), gqt, gqh, dk.data_ptr(), gkt, gkh, q.data_ptr(), qt, qh, k.data_ptr(), kt,
                                 kh, q_out.data_ptr(), qot, qoh, k_out.data_ptr(), kot, koh, table, at, wq, wk,
                                 0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr(), many,
-                                turned, eps, bool(interleaved), T, H, Hkv, d, ws, need, _current_stream(index))
+                                turned, _f32(eps), bool(interleaved), T, H, Hkv, d, ws, need, _current_stream(index))
     if st:
         _check(st, "fa_qk_norm_rope_bwd")
     return q_out, k_out, dwq, dwk
@@ -160,8 +160,8 @@ def kv4_append(q, k, v, rotary, positions, slots, cache: KV4Cache, q_weight=None
     ko, (kot, koh) = (0, (0, 0)) if k_out is None else (
         k_out.data_ptr(), _rows(k_out, "k_out", shape, index, written=True))
     st = _b.fa_kv4_append(c.address, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out.data_ptr(), ot,
-                          oh, ko, kot, koh, table, at, wq, wk, slots.data_ptr(), many, turned, eps, bool(interleaved), T,
-                          H, _current_stream(index))
+                          oh, ko, kot, koh, table, at, wq, wk, slots.data_ptr(), many, turned, _f32(eps),
+                          bool(interleaved), T, H, _current_stream(index))
     if st:
         _check(st, "fa_kv4_append")
     return out
