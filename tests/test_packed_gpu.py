@@ -475,3 +475,16 @@ def test_serving_prompts_then_steps():
             # Probabilities to f16, o to bf16: 2^-8 of what is summed bounds both (values are below 4 here).
             assert float((o[b].double() - ref).abs().max()) <= 2.0 ** -8 * 4
     api.check_device_error()
+
+
+@pytest.mark.parametrize("causal", (True, False))
+@pytest.mark.parametrize("d", DIMS)
+@pytest.mark.parametrize("H,Hkv,lengths", [(4, 1, [1500, 3]), (2, 2, [1100, 1, 1300]), (7, 1, [900])])
+def test_backward_of_few_key_tiles(H, Hkv, lengths, d, causal):
+    """Query ranges in parts: fp32 partial sums, parts without query tiles beside short sequences."""
+    from tiled_attention_tmem_gb300 import binding as b
+    both(lengths, H, Hkv, d, causal, seed=H + d, lead=2, tail=9)
+    b.fa_profile_start()
+    both(lengths, H, Hkv, d, causal, variants=(0,))
+    # Two parts at least where a mean sequence's rows give each 512.
+    assert b.fa_profile_stop()["bwd_kvsum"][0] == (sum(lengths) // len(lengths) * (H // Hkv) >= 1024)

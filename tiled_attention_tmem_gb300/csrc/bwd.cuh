@@ -234,6 +234,11 @@ struct RaggedKVParams {
   float scale_log2;
   float scale;
   int causal;
+  // Query-range split (FEW), as in BwdKVParams; the parts' sums are [qsplit][Hkv][T][D].
+  int qsplit;
+  int T;
+  float* dkpart;
+  float* dvpart;
 };
 
 template <bool RAGGED>
@@ -378,11 +383,10 @@ struct BwdKVCfg {
 // per SM: few heads), with the query-range split (p.qsplit >= 1) and each item's
 // query-tile walk starting at its own offset; the plain one keeps one part per
 // key tile and the natural order as constants and has no partial-sum epilogue.
-// P: BwdKVParams, or RaggedKVParams (packed sequences; without the split).
+// P: BwdKVParams, or RaggedKVParams (packed sequences).
 template <class C, bool FEW, class P = BwdKVParams>
 __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_constant__ P p) {
   constexpr bool RAGGED = P::kRagged;
-  static_assert(!(RAGGED && FEW), "packed sequences are not split");
   constexpr int D = C::D, BM = C::BM, QS = C::QS, DH = C::DH;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -526,10 +530,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
         return false;
       I.start = x.start, I.len = x.len, I.seq = x.seq, I.bh = x.head;
       I.h = x.tile % C::DSPLIT;
-      I.k0 = x.tile / C::DSPLIT * C::BN;
+      const int kq = x.tile / C::DSPLIT, kt = kq / qsplit;
+      I.k0 = kt * C::BN;
       I.qt0 = p.causal ? I.k0 / p.tokens : 0;
       I.n = (x.len + p.tokens - 1) / p.tokens - I.qt0;
       I.part = I.rot = 0;
+      if constexpr (FEW) {
+        const int first = I.qt0, total = I.n;
+        I.part = kq - kt * qsplit;
+        I.qt0 = first + (int)((long long)I.part * total / qsplit);
+        I.n = first + (int)((long long)(I.part + 1) * total / qsplit) - I.qt0;
+        I.rot = I.n > 0 ? (int)((long long)I.n * kt / ((x.len + C::BN - 1) / C::BN)) : 0;
+      }
       return true;
     } else {
       const int w = item_warp(t);
@@ -543,7 +555,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
     if constexpr (RAGGED) return ((size_t)I.bh * p.slots + I.start / p.tokens + I.seq + qt) * BM;
     else return (size_t)I.bh * p.Npad + qt * BM;
   };
-  // Keys of the item's head, and where key k0's row of an output begins and the next one does.
+  // Query-range split: where key `key`'s row of a part's fp32 sums begins.
+  auto part_row = [&](const Item& I, int which, int key) -> float* {
+    if constexpr (FEW) {
+      float* const base = which == 0 ? p.dvpart : p.dkpart;
+      if constexpr (RAGGED) return base + (((size_t)I.part * p.Hkv + I.bh) * p.T + I.start + key) * D;
+      else return base + (((size_t)I.part * p.BH + I.bh) * p.Npad + key) * D;
+    } else {
+      return nullptr;
+    }
+  };
+  // Keys of the item's head, and where key `key`'s row of an output begins.
   auto keys_of = [&](const Item& I) -> int {
     if constexpr (RAGGED) return I.len;
     else return p.N;
@@ -632,7 +654,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           int key0 = 0;  // first token of the sequence
           if constexpr (RAGGED) {
             key0 = I.start;
-            mbar_arrive(BAR(C::B_ITEMASK));
             if (I.k0 + C::BN > I.len) k_map = ends_of(I, k_seq, 2), v_map = k_map + 1;
           }
           auto issue_stage = [&](int i) -> bool {
@@ -700,13 +721,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
           for (int t = 1; have && ok; ++t) {
             bool taken = false, has_next = false;
             J = I;
-            load_item(I, J, [&] {
+            auto next = [&] {
               if (!taken) {
                 taken = true;
                 has_next = item_at(t, J, ByThread{});
               }
               return has_next;
-            });
+            };
+            mbar_arrive(BAR(C::B_ITEMASK));
+            if (I.n > 0) load_item(I, J, next);
+            else next();  // (a part without query tiles)
             I = J;
             have = has_next;
           }
@@ -936,7 +960,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
     } else if (RAGGED && warp == 3) {
       // --------------------------------------------------------- scheduling
       if constexpr (RAGGED)
-        ragged_schedule(p.sched, C::BN, C::DSPLIT, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
+        ragged_schedule(p.sched, C::BN, C::DSPLIT * qsplit, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
                         BAR(C::B_ITEMASK), ab, (kKBwdKV << 8) | 20);
     }
     } else if (warp < C::DRAIN_W0) {
@@ -956,28 +980,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
         if (!item_at(rr, I, ByWarp{})) break;
         const int kj = I.k0 + r;
         const bool key_ok = kj < keys_of(I);
-        if constexpr (!RAGGED) {
+        if constexpr (!RAGGED || FEW) {
         if (I.n <= 0) {
           // No query of this item can see the key tile: zero gradients (zero partial
           // sums under the query-range split).
           const int c_off = C::OS ? 0 : I.h * DH;
-          if (FEW && qsplit > 1) {
-            if (key_ok && cw == 0) {
-              const size_t off = (((size_t)I.part * p.BH + I.bh) * p.Npad + kj) * D + c_off;
-              for (int c = 0; c < DH; c += 4) {
-                if (!C::OS || I.h == 0) *reinterpret_cast<float4*>(p.dvpart + off + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (!C::OS || I.h == 1) *reinterpret_cast<float4*>(p.dkpart + off + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+          if constexpr (FEW) {
+            if (qsplit > 1) {
+              if (key_ok && cw == 0) {
+                float *const dv = part_row(I, 0, kj) + c_off, *const dk = part_row(I, 1, kj) + c_off;
+                for (int c = 0; c < DH; c += 4) {
+                  if (!C::OS || I.h == 0) *reinterpret_cast<float4*>(dv + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (!C::OS || I.h == 1) *reinterpret_cast<float4*>(dk + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
               }
+              continue;
             }
-            continue;
           }
           if (key_ok && cw == 0)
             for (int c = 0; c < DH; c += 8) {
               if (c_off + c < p.hd) {
                 if (!C::OS || I.h == 0)
-                  *reinterpret_cast<uint4*>(p.dv + ((size_t)I.bh * p.N + kj) * p.hd + c_off + c) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(out_row(I, 0, kj) + c_off + c) = make_uint4(0, 0, 0, 0);
                 if (!C::OS || I.h == 1)
-                  *reinterpret_cast<uint4*>(p.dk + ((size_t)I.bh * p.N + kj) * p.hd + c_off + c) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(out_row(I, 1, kj) + c_off + c) = make_uint4(0, 0, 0, 0);
               }
             }
           continue;
@@ -1146,7 +1172,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
             if (C::NCW == 2 && which != cw) continue;
             if (C::OS && which != I.h) continue;
             const int c_off = C::OS ? 0 : I.h * DH;
-            float* dst = (which == 0 ? p.dvpart : p.dkpart) + (((size_t)I.part * p.BH + I.bh) * p.Npad + kj) * D + c_off;
+            float* dst = part_row(I, which, kj) + c_off;
             const uint32_t tacc = trow + (which == 0 ? C::T_DV : C::T_DK);
 #pragma unroll
             for (int c0 = 0; c0 < DH; c0 += 32) {

@@ -2,6 +2,7 @@
 // over items that ragged_plan_kernel lays out, with a preprocess and a dQ conversion that
 // go by query tiles.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "bwd.cuh"
@@ -212,17 +213,71 @@ __global__ void __launch_bounds__(256) ragged_conv_kernel(const __grid_constant_
   }
 }
 
-// The workspace: the plan, then lse2, dd and (5-GEMM) dqacc by query tiles.
+// Sum of the query-range parts: dv = sum_s dvpart[s], dk = scale sum_s dkpart[s], in a fixed order, bf16.
+struct RaggedKVSumParams {
+  const float* dkpart;
+  const float* dvpart;
+  RowsOut dk, dv;
+  const int* cu;
+  int* err;
+  int B, T, Hkv, hd, D, parts;
+  float scale;
+};
+
+__global__ void __launch_bounds__(256) ragged_kvsum_kernel(const __grid_constant__ RaggedKVSumParams p) {
+  grid_dep_wait();
+  if (*reinterpret_cast<volatile const int*>(p.err) != 0) return;
+  const int chunks = p.hd / 8;
+  const int lo = max(p.cu[0], 0), hi = min(p.cu[p.B], p.T);  // (the other rows are zeros already)
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, work = (long long)max(hi - lo, 0) * p.Hkv * chunks;
+  if (i >= work) return;
+  const long long row = i / chunks;
+  const int c = (int)(i - row * chunks) * 8, tok = lo + (int)(row / p.Hkv), head = (int)(row % p.Hkv);
+  const size_t off = ((size_t)head * p.T + tok) * p.D + c, stride = (size_t)p.Hkv * p.T * p.D;
+  float a[8] = {}, b[8] = {};
+  for (int s = 0; s < p.parts; ++s) {
+    const float4* v4 = reinterpret_cast<const float4*>(p.dvpart + s * stride + off);
+    const float4* k4 = reinterpret_cast<const float4*>(p.dkpart + s * stride + off);
+    const float4 v0 = v4[0], v1 = v4[1], k0 = k4[0], k1 = k4[1];
+    a[0] += v0.x, a[1] += v0.y, a[2] += v0.z, a[3] += v0.w, a[4] += v1.x, a[5] += v1.y, a[6] += v1.z, a[7] += v1.w;
+    b[0] += k0.x, b[1] += k0.y, b[2] += k0.z, b[3] += k0.w, b[4] += k1.x, b[5] += k1.y, b[6] += k1.z, b[7] += k1.w;
+  }
+  const float sc = p.scale;
+  *reinterpret_cast<uint4*>(p.dv.data + tok * p.dv.token + head * p.dv.head + c) =
+      make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+  *reinterpret_cast<uint4*>(p.dk.data + tok * p.dk.token + head * p.dk.head + c) =
+      make_uint4(pack_bf16(b[0] * sc, b[1] * sc), pack_bf16(b[2] * sc, b[3] * sc), pack_bf16(b[4] * sc, b[5] * sc),
+                 pack_bf16(b[6] * sc, b[7] * sc));
+}
+
+// Query parts per key tile, by the rule of the dense backward (bwd.cu, choose_qsplit) over what is known of the
+// sequences without reading them: key tiles from the tokens and half a tile a sequence, and the rows of a mean
+// sequence's group of heads, of which a part gets 512 at least.
+int packed_qsplit(const PackedShape& s, int dsplit, int causal) {
+  if (s.B == 0) return 1;
+  const double items = (s.T / 128.0 + s.B / 2.0) * s.Hkv * dsplit, sms = sm_count_cached();
+  if (items >= 2.0 * sms) return 1;
+  const long cap = std::max(1LL, std::min(8LL, (long long)s.T / s.B * s.G() / 512));
+  long parts = 1;
+  if (causal) parts = std::lround(3.0 * sms / items);
+  else if (items <= 0.85 * sms) parts = std::max(2L, std::lround(0.85 * sms / items));
+  return (int)std::max(1L, std::min(cap, parts));
+}
+
+// The workspace: the plan, then lse2, dd, (5-GEMM) dqacc by query tiles, and the parts of a split (as many as
+// either mask has).
 struct BwdLayout {
   int cuts, nmaps, slots;
-  size_t rows, plan, total;
-  BwdLayout(const PackedShape& s, int variant, int tile_rows, int D) {
+  size_t rows, plan, total, parts;  // parts: where they begin
+  BwdLayout(const PackedShape& s, int variant, int tile_rows, int D, int dsplit) {
     const bool five = variant == FA_BWD_5GEMM;
     cuts = five ? 1 : 2, nmaps = five ? 4 : 6;
     slots = s.T / (tile_rows / s.G()) + s.B;
     rows = (size_t)s.Hkv * slots * tile_rows;
     plan = packed_plan_bytes(s.B, cuts, nmaps);
-    total = plan + 2 * align256(4 * rows) + (five ? 4 * rows * D : 0);
+    parts = plan + 2 * align256(4 * rows) + (five ? align256(4 * rows * D) : 0);
+    const int most = std::max(packed_qsplit(s, dsplit, 0), packed_qsplit(s, dsplit, 1));
+    total = parts + (most > 1 ? 2 * (size_t)most * s.Hkv * s.T * D * sizeof(float) : 0);
   }
 };
 
@@ -232,10 +287,11 @@ RowsOut out(const fa_rows& r) { return {static_cast<uint16_t*>(const_cast<void*>
 // KV: the dK/dV kernel; Q: the dQ kernel (void: 5-GEMM).  DP: the preprocess's head dimension.
 template <int DP, class KV, class Q>
 fa_status run(const fa_packed_bwd_args& c, const PackedShape& s) {
-  static std::atomic<unsigned long long> kv_raised{0}, q_raised{0};
+  static std::atomic<unsigned long long> kv_raised{0}, few_raised{0}, q_raised{0};
   constexpr bool five = KV::DQ;
   const cudaStream_t st = (cudaStream_t)c.stream;
-  const BwdLayout lay(s, five ? FA_BWD_5GEMM : FA_BWD_7GEMM, KV::BM, KV::D);
+  const BwdLayout lay(s, five ? FA_BWD_5GEMM : FA_BWD_7GEMM, KV::BM, KV::D, KV::DSPLIT);
+  const int qsplit = packed_qsplit(s, KV::DSPLIT, c.causal);
   const PackedPlan plan = packed_plan_at(c.workspace, s.B, lay.cuts);
   uint8_t* at = static_cast<uint8_t*>(c.workspace) + lay.plan;
   float* const lse2 = reinterpret_cast<float*>(at);
@@ -248,7 +304,7 @@ fa_status run(const fa_packed_bwd_args& c, const PackedShape& s) {
   const double token_bytes = 2.0 * s.d * (2 * s.G() + 2) + (five ? 4.0 * KV::D * s.G() : 0.0);
   const int tokens = KV::BM / s.G();
   CUtensorMap maps[kPackedMaxMaps];
-  PackedCut cuts[2] = {{KV::BN, KV::DSPLIT, token_bytes}, {}};
+  PackedCut cuts[2] = {{KV::BN, KV::DSPLIT * qsplit, token_bytes}, {}};
   fa_status e;
   if ((e = packed_query_map(&maps[0], c.q, s, tokens)) != FA_OK) return e;
   if ((e = packed_query_map(&maps[1], c.dO, s, tokens)) != FA_OK) return e;
@@ -281,11 +337,27 @@ fa_status run(const fa_packed_bwd_args& c, const PackedShape& s) {
   p.dv = out(c.dv).data, p.dv_token = c.dv.token, p.dv_head = c.dv.head;
   p.err = err, p.slots = lay.slots, p.Hkv = s.Hkv, p.G = s.G(), p.tokens = tokens, p.hd = s.d;
   p.scale_log2 = c.scale * kLog2e, p.scale = c.scale, p.causal = c.causal;
+  p.qsplit = qsplit, p.T = s.T;
+  p.dkpart = reinterpret_cast<float*>(static_cast<uint8_t*>(c.workspace) + lay.parts);
+  p.dvpart = p.dkpart + (size_t)qsplit * s.Hkv * s.T * KV::D;
   const unsigned kv_grid =
-      (unsigned)std::min<long long>(((long long)s.T / KV::BN + s.B) * s.Hkv * KV::DSPLIT, sms);
-  if ((e = launch_raised(five ? FA_KERNEL_BWD_KV5 : FA_KERNEL_BWD_KV7, bwd_kv_kernel<KV, false, RaggedKVParams>,
-                         dim3(kv_grid), dim3(KV::THREADS), KV::SMEM_BYTES, st, p, kv_raised)) != FA_OK)
-    return e;
+      (unsigned)std::min<long long>(((long long)s.T / KV::BN + s.B) * s.Hkv * KV::DSPLIT * qsplit, sms);
+  const int kind = five ? FA_KERNEL_BWD_KV5 : FA_KERNEL_BWD_KV7;
+  if (qsplit == 1) {
+    if ((e = launch_raised(kind, bwd_kv_kernel<KV, false, RaggedKVParams>, dim3(kv_grid), dim3(KV::THREADS), KV::SMEM_BYTES,
+                           st, p, kv_raised)) != FA_OK)
+      return e;
+  } else {
+    if ((e = launch_raised(kind, bwd_kv_kernel<KV, true, RaggedKVParams>, dim3(kv_grid), dim3(KV::THREADS), KV::SMEM_BYTES,
+                           st, p, few_raised)) != FA_OK)
+      return e;
+    const RaggedKVSumParams sum = {p.dkpart, p.dvpart, out(c.dk), out(c.dv), c.cu, err, s.B, s.T, s.Hkv, s.d, KV::D, qsplit,
+                                   c.scale};
+    const long long threads = (long long)s.T * s.Hkv * (s.d / 8);
+    if ((e = launch(FA_KERNEL_BWD_KVSUM, ragged_kvsum_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st,
+                    sum)) != FA_OK)
+      return e;
+  }
   if constexpr (five) {
     RaggedConvParams conv = {pre.tiles, dqacc, out(c.dq), err, c.scale};
     return launch(FA_KERNEL_BWD_CONV, ragged_conv_kernel<KV::D>, dim3(blocks), dim3(256), 0, st, conv);
@@ -316,7 +388,9 @@ static_assert(KV5_64::BM == 128 && KV7_64::BM == 128 && KV5_128::BM == 64 && KV7
 }  // namespace
 
 size_t packed_bwd_bytes(const PackedShape& s, int variant) {
-  return BwdLayout(s, variant, tile_rows(s.d), padded_head_dim(s.d)).total;
+  // (the kernels' D and DSPLIT: run below)
+  const int D = s.d == 192 ? 192 : padded_head_dim(s.d);
+  return BwdLayout(s, variant, tile_rows(s.d), D, D == 384 ? KV7_384::DSPLIT : D == 256 ? KV7_256::DSPLIT : 1).total;
 }
 
 fa_status run_packed_bwd(const fa_packed_bwd_args& a, const PackedShape& s, int form) {
