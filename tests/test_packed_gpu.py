@@ -488,3 +488,10 @@ def test_backward_of_few_key_tiles(H, Hkv, lengths, d, causal):
     both(lengths, H, Hkv, d, causal, variants=(0,))
     # Two parts at least where a mean sequence's rows give each 512.
     assert b.fa_profile_stop()["bwd_kvsum"][0] == (sum(lengths) // len(lengths) * (H // Hkv) >= 1024)
+
+
+@pytest.mark.parametrize("d", (64, 96, 128))
+def test_items_of_two_tiles(d):
+    """More items than SMs: two query tiles each, the second of them empty at some ends."""
+    both([1500, 700, 1500, 64, 1499, 1200, 33], 16, 4, d, True, seed=d, variants=(0,))
+    both([1100, 20, 900, 1300, 1], 24, 8, d, False, seed=d, variants=(7,))

@@ -89,6 +89,7 @@ struct RaggedFwdParams {
   int G;       // query heads of a kv head
   int by_G;    // 65536 / G rounded up: r / G = r * by_G >> 16 for r < 128, G <= 32
   int tokens;  // tokens of a 128-row tile: 128 / G rounded down
+  int tiles;   // Q tiles of an item: NQ, or 1 where items are few
   int dv;
   float scale_log2;
   int causal;
@@ -303,12 +304,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
                                              (kKFwd << 8) | 12))
         return false;
       it.start = x.start, it.len = x.len, it.seq = x.seq, it.bh = x.head;
-      const int blocks = (x.len + NQ * p.tokens - 1) / (NQ * p.tokens);
-      it.q0 = (p.causal ? blocks - 1 - x.tile : x.tile) * NQ * p.tokens;
+      const int span = p.tiles * p.tokens, blocks = (x.len + span - 1) / span;
+      it.q0 = (p.causal ? blocks - 1 - x.tile : x.tile) * span;
       it.nmax = 0;
 #pragma unroll
       for (int t2 = 0; t2 < NQ; ++t2) {
-        it.nkv[t2] = ragged_kv_tiles(it.q0 + t2 * p.tokens, p.tokens, x.len, p.causal, BN);
+        it.nkv[t2] =
+            t2 < p.tiles ? ragged_kv_tiles(it.q0 + t2 * p.tokens, p.tokens, x.len, p.causal, BN) : 0;
         it.nmax = max(it.nmax, it.nkv[t2]);
       }
       return true;
@@ -747,7 +749,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
     } else if (RAGGED && warp == 3) {
       // --------------------------------------------------------- scheduling
       if constexpr (RAGGED)
-        ragged_schedule(p.sched, NQ * p.tokens, 1, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
+        ragged_schedule(p.sched, p.tiles * p.tokens, 1, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
                         BAR(C::B_ITEMASK), ab, (kKFwd << 8) | 13);
     }
     } else {

@@ -21,7 +21,12 @@ fa_status run(const fa_packed_fwd_args& a, const PackedShape& s) {
   if ((e = packed_key_map(&p.k_map, a.k, s, C::BN)) != FA_OK) return e;
   if ((e = packed_key_map(&p.v_map, a.v, s, C::BN)) != FA_OK) return e;
   const PackedPlan plan = packed_plan_at(a.workspace, s.B, 1);
-  const PackedCut cut = {C::NQ * tokens, 1, 4.0 * s.d};  // K and V
+  // Items of one tile where those of two would not fill the SMs: shorter by half, if slower a tile.  Measured in us
+  // (items of two / of one): two sequences up to 1500, four heads on two of 64: 21 / 17; one of 2048, eight on one of
+  // 128: 26 / 25; two up to 2048, eight on two of 128: 26 / 24; above an item an SM, four up to 1500: 24 / 29.
+  const double items = (s.T / (2.0 * tokens) + s.B / 2.0) * s.Hkv;
+  p.tiles = C::NQ > 1 && items < sm_count_cached() ? 1 : C::NQ;
+  const PackedCut cut = {p.tiles * tokens, 1, 4.0 * s.d};  // K and V
   if ((e = run_packed_plan(packed_plan_params(plan, a.cu, s, &cut, 1, &p.v_map, 1, 0), st)) != FA_OK) return e;
   p.v_ends = plan.maps;
   p.sched = plan.sched[0];

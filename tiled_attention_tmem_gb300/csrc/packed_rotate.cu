@@ -66,42 +66,57 @@ struct HeadLanes {
   }
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
+// Eight channels as four pairs of neighbours: the arithmetic goes two channels an instruction.
+__device__ __forceinline__ void unpack8(const uint4& v, float2* x) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const float2* x) {
+  return make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y), pack_bf16(x[2].x, x[2].y),
+                    pack_bf16(x[3].x, x[3].y));
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 
-// Cosines and sines of a lane's eight pairs.
-template <int D, bool NEXT>
-__device__ __forceinline__ void load_angles(const HeadLanes<D>& at, const float* row, int rot, float* c, float* s) {
+// Cosines and sines of a lane's eight pairs (BACK: of the angles' negatives), from where load(i) gives the
+// i-th four of the cosines, then of the sines.
+struct Angles {
+  float2 c[4], s[4];
+};
+template <bool BACK, class Load>
+__device__ __forceinline__ void load_angles(Angles& a, Load load) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int i = NEXT ? 4 * at.chunk[h] : 8 * at.u + 4 * h;
-    const float4 a = *reinterpret_cast<const float4*>(row + i);
-    const float4 b = *reinterpret_cast<const float4*>(row + rot / 2 + i);
-    c[4 * h] = a.x, c[4 * h + 1] = a.y, c[4 * h + 2] = a.z, c[4 * h + 3] = a.w;
-    s[4 * h] = b.x, s[4 * h + 1] = b.y, s[4 * h + 2] = b.z, s[4 * h + 3] = b.w;
+    const float4 c = load(h), s = load(2 + h);
+    a.c[2 * h] = make_float2(c.x, c.y), a.c[2 * h + 1] = make_float2(c.z, c.w);
+    a.s[2 * h] = make_float2(s.x, s.y), a.s[2 * h + 1] = make_float2(s.z, s.w);
+    if (BACK) a.s[2 * h] = neg2(a.s[2 * h]), a.s[2 * h + 1] = neg2(a.s[2 * h + 1]);
   }
 }
+// Where in its row of the table the h-th four of a lane's angles begin.
+template <int D, bool NEXT>
+__device__ __forceinline__ int angle_at(const HeadLanes<D>& at, int h) {
+  return NEXT ? 4 * at.chunk[h] : 8 * at.u + 4 * h;
+}
 
-// Turns a lane's 16 channels (two chunks of 8) by the angles, or back.  Each product and sum is
-// rounded on its own, in this order, so that the result does not depend on how they are fused.
-template <bool NEXT, bool BACK>
-__device__ __forceinline__ void turn(float* x, const float* c, const float* s) {
+// Turns a lane's 16 channels (two chunks of 8).  Each product and sum is rounded on its own, in this order, so
+// that the result does not depend on how they are fused.
+template <bool NEXT>
+__device__ __forceinline__ void turn(float2* x, const Angles& a) {
+  if constexpr (NEXT) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& a = NEXT ? x[8 * (i / 4) + 2 * (i % 4)] : x[i];
-    float& b = NEXT ? x[8 * (i / 4) + 2 * (i % 4) + 1] : x[8 + i];
-    const float ac = __fmul_rn(a, c[i]), bs = __fmul_rn(b, s[i]), bc = __fmul_rn(b, c[i]), as = __fmul_rn(a, s[i]);
-    a = BACK ? __fadd_rn(ac, bs) : __fsub_rn(ac, bs);
-    b = BACK ? __fsub_rn(bc, as) : __fadd_rn(bc, as);
+    for (int i = 0; i < 8; ++i) {
+      const float c = i & 1 ? a.c[i / 2].y : a.c[i / 2].x, s = i & 1 ? a.s[i / 2].y : a.s[i / 2].x;
+      x[i] = fadd2(fmul2(x[i], both(c)), fmul2(make_float2(x[i].y, x[i].x), make_float2(-s, s)));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = x[i], v = x[4 + i];
+      x[i] = fadd2(fmul2(u, a.c[i]), fmul2(v, neg2(a.s[i])));
+      x[4 + i] = fadd2(fmul2(v, a.c[i]), fmul2(u, a.s[i]));
+    }
   }
 }
 
@@ -143,29 +158,34 @@ __global__ void __launch_bounds__(256, 4) rotate_kernel(const __grid_constant__ 
     }
   }
   if (pos < 0 || pos >= p.positions) return;  // a token without a position is left out
-  float c[8], s[8];
-  if (at.turned) load_angles<D, NEXT>(at, p.rotary + (long long)pos * p.rot, p.rot, c, s);
+  Angles angles;
+  if (at.turned) {
+    const float* row = p.rotary + (long long)pos * p.rot;
+    load_angles<false>(angles, [&](int i) {
+      return *reinterpret_cast<const float4*>(row + (i >> 1) * (p.rot / 2) + angle_at<D, NEXT>(at, i & 1));
+    });
+  }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int step = blockIdx.y * U + i, kind = kind_of(step), head = head_of(step, kind);
     const HeadRows& row = p.x[kind];
     const bool have = at.active && head < row.heads;
     if (kind < 2) {
-      float x[16];
+      float2 x[8];
       unpack8(raw[i][0], x);
-      unpack8(raw[i][1], x + 8);
+      unpack8(raw[i][1], x + 4);
       if (row.weight != nullptr) {
-        float sum = 0.f, w[16];
+        float2 sum = make_float2(0.f, 0.f), w[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) unpack8(*reinterpret_cast<const uint4*>(row.weight + 8 * at.chunk[h]), w + 8 * h);
+        for (int h = 0; h < 2; ++h) unpack8(*reinterpret_cast<const uint4*>(row.weight + 8 * at.chunk[h]), w + 4 * h);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
-        const float r = rsqrtf(head_sum<D>(sum) * (1.f / D) + p.eps);
+        for (int e = 0; e < 8; ++e) sum = ffma2(x[e], x[e], sum);
+        const float r = rsqrtf(head_sum<D>(sum.x + sum.y) * (1.f / D) + p.eps);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
+        for (int e = 0; e < 8; ++e) x[e] = fmul2(fmul2(x[e], both(r)), w[e]);
       }
-      if (at.turned) turn<NEXT, false>(x, c, s);
-      raw[i][0] = pack8(x), raw[i][1] = pack8(x + 8);
+      if (at.turned) turn<NEXT>(x, angles);
+      raw[i][0] = pack8(x), raw[i][1] = pack8(x + 4);
       if (have && row.out != nullptr) {
         uint16_t* dst = row.out + tok * row.out_token + head * row.out_head;
 #pragma unroll
@@ -205,10 +225,11 @@ struct RotateBwdParams {
   float* part;   // [blocks][d]: each block's sum of g xhat (NULL: no weights)
 };
 
-constexpr int kRotateBack = 2;  // steps of heads a warp loads at a time
+constexpr int kRotateBack = 2;  // steps of heads a warp takes at a time
 
 // A block takes q or k; its warps walk tokens (and runs of U steps of heads), keeping the weight's
-// gradient of their channels in registers.  Tokens without a position have a gradient of zero.
+// gradient of their channels in registers, all loads of a run first.  Tokens without a position have a
+// gradient of zero.
 template <int D, bool NEXT>
 __global__ void __launch_bounds__(256, 2) rotate_bwd_kernel(const __grid_constant__ RotateBwdParams p) {
   using L = HeadLanes<D>;
@@ -216,90 +237,113 @@ __global__ void __launch_bounds__(256, 2) rotate_bwd_kernel(const __grid_constan
   __shared__ float sums[8][D];
   grid_dep_wait();
   const L at(p.rot);
-  const int warp = warp_id();  // (a shuffle of the whole warp: never inside a branch)
+  const int warp = warp_id(), lane = lane_id();  // (a shuffle of the whole warp: never inside a branch)
   const int kind = (int)blockIdx.x < p.q_blocks ? 0 : 1;
   const int block = kind ? blockIdx.x - p.q_blocks : blockIdx.x, blocks = kind ? gridDim.x - p.q_blocks : p.q_blocks;
   const HeadRows &gy = p.dy[kind], &xx = p.x[kind];
-  const int runs = (gy.heads + U * L::ROWS - 1) / (U * L::ROWS);
-  float dw[16];
+  const bool normed = xx.weight != nullptr;
+  const int runs = (gy.heads + U * L::ROWS - 1) / (U * L::ROWS), sub = lane / L::GROUP;
+  float2 dw[8];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) dw[e] = 0.f;
+  for (int e = 0; e < 8; ++e) dw[e] = make_float2(0.f, 0.f);
   uint4 rw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  if (xx.weight != nullptr) {
+  if (normed) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) rw[h] = *reinterpret_cast<const uint4*>(xx.weight + 8 * at.chunk[h]);
   }
-  const long long work = (long long)p.T * runs;
-  for (long long job = (long long)block * 8 + warp; job < work; job += (long long)blocks * 8) {
-    const int tok = (int)(job / runs), run = (int)(job - (long long)tok * runs);
-    const int first = run * U * L::ROWS + lane_id() / L::GROUP;
-    const int pos = p.position[tok];
+  // A run: its token and place in the token; the next of this warp is 8 * blocks runs on (without a division each).
+  struct Run {
+    int tok, at;
+  };
+  const int tok_step = runs > 0 ? 8 * blocks / runs : 0, at_step = 8 * blocks - tok_step * runs;
+  auto after = [&](Run j) {
+    j.tok += tok_step, j.at += at_step;
+    if (j.at >= runs) j.at -= runs, ++j.tok;
+    return j;
+  };
+  auto position = [&](Run j) { return j.tok < p.T ? p.position[j.tok] : -1; };
+  auto is_live = [&](int pos) { return pos >= 0 && pos < p.positions; };
+  const int begin = block * 8 + warp;
+  Run job = {runs > 0 ? begin / runs : p.T, runs > 0 ? begin % runs : 0}, next = after(job);
+  int pos = position(job);
+  while (job.tok < p.T) {
+    const int tok = job.tok, first = job.at * U * L::ROWS + sub;
+    const bool live = is_live(pos);
     uint4 rg[U][2], rx[U][2];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int head = first + i * L::ROWS;
-      const bool have = at.active && head < gy.heads;
+      const bool have = at.active && live && head < gy.heads;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         rg[i][h] = rx[i][h] = make_uint4(0u, 0u, 0u, 0u);
         if (have) {
           rg[i][h] = *reinterpret_cast<const uint4*>(gy.in + tok * gy.in_token + head * gy.in_head + 8 * at.chunk[h]);
-          if (xx.weight != nullptr)
+          if (normed)
             rx[i][h] = *reinterpret_cast<const uint4*>(xx.in + tok * xx.in_token + head * xx.in_head + 8 * at.chunk[h]);
         }
       }
     }
-    const bool live = pos >= 0 && pos < p.positions;  // (the rows do not wait for it)
-    float c[8], s[8];
-    if (at.turned && live) load_angles<D, NEXT>(at, p.rotary + (long long)pos * p.rot, p.rot, c, s);
+    Angles angles;
+    if (at.turned && live) {
+      const float* row = p.rotary + (long long)pos * p.rot;
+      load_angles<true>(angles, [&](int i) {
+        return *reinterpret_cast<const float4*>(row + (i >> 1) * (p.rot / 2) + angle_at<D, NEXT>(at, i & 1));
+      });
+    }
+    pos = position(next);  // (a run ahead: the next one's loads do not wait for it)
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int head = first + i * L::ROWS;
-      float g[16];
-      if (!live) rg[i][0] = rg[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      unpack8(rg[i][0], g);
-      unpack8(rg[i][1], g + 8);
-      if (at.turned && live) turn<NEXT, true>(g, c, s);
-      if (xx.weight != nullptr) {
-        float x[16], w[16], sum = 0.f, dot = 0.f;
-        if (!live) rx[i][0] = rx[i][1] = make_uint4(0u, 0u, 0u, 0u);
-        unpack8(rx[i][0], x);
-        unpack8(rx[i][1], x + 8);
-        unpack8(rw[0], w);
-        unpack8(rw[1], w + 8);
+      float2 g[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          sum = fmaf(x[e], x[e], sum);
-          dot = fmaf(x[e], g[e] * w[e], dot);
+      for (int h = 0; h < 2; ++h) unpack8(rg[i][h], g + 4 * h);
+      if (at.turned && live) turn<NEXT>(g, angles);
+      if (normed) {
+        float2 x[8], z[8], sum = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          unpack8(rx[i][h], x + 4 * h);
+          unpack8(rw[h], z + 4 * h);
         }
-        sum = head_sum<D>(sum);
-        dot = head_sum<D>(dot);
-        // (a row that is not there must not turn eps = 0 into 0 * inf)
-        const float r = live && head < gy.heads ? rsqrtf(sum * (1.f / D) + p.eps) : 0.f;
-        const float m = dot * r * (1.f / D);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float unit = x[e] * r;
-          dw[e] = fmaf(g[e], unit, dw[e]);
-          g[e] = r * (g[e] * w[e] - unit * m);
+        for (int e = 0; e < 8; ++e) {
+          z[e] = fmul2(g[e], z[e]);
+          sum = ffma2(x[e], x[e], sum);
+          dot = ffma2(x[e], z[e], dot);
+        }
+        const float total = head_sum<D>(sum.x + sum.y), inner = head_sum<D>(dot.x + dot.y);
+        // (a row that is not there must not turn eps = 0 into 0 * inf)
+        const float r = live && head < gy.heads ? rsqrtf(total * (1.f / D) + p.eps) : 0.f;
+        const float2 m = both(-inner * r * (1.f / D)), r2 = both(r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 unit = fmul2(x[e], r2);
+          dw[e] = ffma2(g[e], unit, dw[e]);
+          g[e] = fmul2(r2, ffma2(unit, m, z[e]));
         }
       }
       if (at.active && head < gy.heads) {
         uint16_t* dst = gy.out + tok * gy.out_token + head * gy.out_head;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(dst + 8 * at.chunk[h]) = pack8(g + 8 * h);
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(dst + 8 * at.chunk[h]) = pack8(g + 4 * h);
       }
     }
+    job = next, next = after(next);
   }
   if (p.part == nullptr) return;
   // The lanes that hold the same channels, then the warps, in a fixed order.
 #pragma unroll
   for (int d = L::GROUP; d < 32; d <<= 1)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], d);
-  if (lane_id() < L::GROUP && at.active)
+    for (int e = 0; e < 8; ++e) {
+      dw[e].x += __shfl_xor_sync(0xffffffffu, dw[e].x, d);
+      dw[e].y += __shfl_xor_sync(0xffffffffu, dw[e].y, d);
+    }
+  if (lane < L::GROUP && at.active)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) sums[warp][8 * at.chunk[e >> 3] + (e & 7)] = dw[e];
+    for (int e = 0; e < 8; ++e)
+      *reinterpret_cast<float2*>(&sums[warp][8 * at.chunk[e >> 2] + 2 * (e & 3)]) = dw[e];
   __syncthreads();
   for (int e = threadIdx.x; e < D; e += 256) {
     float v = 0.f;
@@ -401,7 +445,7 @@ fa_status rotate_by_dim(const RotateParams& p, int d, int interleaved, cudaStrea
   return FA_ERR_UNSUPPORTED;
 }
 
-constexpr int kRotateBlocks = 4;  // blocks an SM of the gradients' kernel
+constexpr int kRotateBlocks = 2;  // blocks an SM of the gradients' kernel: those that fit
 
 int rotate_bwd_blocks(int T, int H, int Hkv) {
   const long long most = ((long long)T * (H + Hkv) + 7) / 8;  // no more than rows
