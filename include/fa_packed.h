@@ -94,7 +94,7 @@ typedef struct {
 fa_status fa_packed_bwd(const fa_packed_bwd_args* a);
 
 /*
- * Bytes of workspace fa_packed_bwd needs (row statistics, for the 5-GEMM form an fp32 dq, tensor
+ * Bytes of workspace fa_packed_bwd needs on the current device (row statistics, for the 5-GEMM form an fp32 dq, tensor
  * maps); 0 for shapes without work and invalid ones.
  */
 size_t fa_packed_bwd_workspace_size(int B, int T, int H, int Hkv, int d, int variant);

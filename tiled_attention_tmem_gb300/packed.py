@@ -116,12 +116,14 @@ def packed_attention_forward(q, k, v, cu, scale: float | None = None, causal: bo
 
 
 def packed_backward_workspace_bytes(sequences, tokens, heads, kv_heads, head_dim, variant=_b.FA_BWD_AUTO) -> int:
-    """What ``packed_attention_backward`` needs."""
+    """What ``packed_attention_backward`` needs (on the current device)."""
     _check_sizes(sequences, tokens, heads, kv_heads)
     return _b.fa_packed_bwd_workspace_size(sequences, tokens, heads, kv_heads, head_dim, variant)
 
 
-_backward_bytes = functools.lru_cache(maxsize=1024)(packed_backward_workspace_bytes)
+# By shape and device, whose multiprocessors it goes by.
+_backward_bytes = functools.lru_cache(maxsize=1024)(lambda *shape_and_device: packed_backward_workspace_bytes(
+    *shape_and_device[:-1]))
 
 
 def packed_attention_backward(q, k, v, o, do, lse, cu, scale: float | None = None, causal: bool = True,
@@ -152,7 +154,7 @@ def packed_attention_backward(q, k, v, o, do, lse, cu, scale: float | None = Non
         dq, dk, dv = grads
         (qgt, qgh), (kgt, kgh), (vgt, vgh) = (_rows(t, name, like.shape, index, written=True) for t, name, like in
                                               ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)))
-    workspace, at, need = _workspace(workspace, _backward_bytes(B, T, H, Hkv, d, variant), index, q.device)
+    workspace, at, need = _workspace(workspace, _backward_bytes(B, T, H, Hkv, d, variant, index), index, q.device)
     st = _b.fa_packed_bwd(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, o.data_ptr(), ot, oh,
                           do.data_ptr(), gt, gh, lse.data_ptr(), dq.data_ptr(), qgt, qgh, dk.data_ptr(), kgt, kgh,
                           dv.data_ptr(), vgt, vgh, cu.data_ptr(), B, T, H, Hkv, d,
