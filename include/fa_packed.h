@@ -46,7 +46,7 @@ typedef struct {
  * overlap the inputs.
  * H a multiple of Hkv, H / Hkv at most 32 (else FA_ERR_UNSUPPORTED), (T + B) * Hkv at
  * most 2^28, scale finite and > 0.  workspace: fa_packed_fwd_workspace_size bytes,
- * 256-byte aligned, not shared with a concurrent call.
+ * 256-byte aligned, not shared with a concurrent call (may be NULL where that is 0: few sequences).
  */
 typedef struct {
   fa_rows q, k, v, o;
@@ -61,7 +61,8 @@ typedef struct {
 } fa_packed_fwd_args;
 fa_status fa_packed_fwd(const fa_packed_fwd_args* a);
 
-/* Bytes of workspace fa_packed_fwd needs; 0 for shapes without work and invalid ones. */
+/* Bytes of workspace fa_packed_fwd needs on the current device; 0 for few sequences, and for shapes without
+ * work and invalid ones. */
 size_t fa_packed_fwd_workspace_size(int B, int T, int H, int Hkv, int d);
 
 /*

@@ -38,7 +38,7 @@ FWD_BAD = [
     (b.FA_ERR_UNSUPPORTED, [dict(d=80), dict(d=512), dict(d=0), dict(H=66)]),
     (b.FA_ERR_MISALIGNED, [dict(q=rows(A + 8)), dict(k=rows(A + 2)), dict(q=rows(token=1028)), dict(v=rows(head=4)),
                            dict(lse=A + 2), dict(cu=A + 1)]),
-    (b.FA_ERR_WORKSPACE, [dict(ws=0), dict(ws=A + 16), dict(short=1)]),
+    (b.FA_ERR_WORKSPACE, [dict(B=40, ws=0), dict(B=40, ws=A + 16), dict(B=40, short=1)]),
 ]
 
 
@@ -81,7 +81,10 @@ def test_attention_without_work_touches_nothing():
 
 
 def test_attention_workspace_sizes():
-    assert b.fa_packed_fwd_workspace_size(3, 100, 8, 2, 128) >= 3 * 128
+    # The forward needs none for few sequences and items; both bounds (32 sequences, two items an SM).
+    assert b.fa_packed_fwd_workspace_size(3, 100, 8, 2, 128) == 0 == b.fa_packed_fwd_workspace_size(32, 100, 8, 2, 128)
+    assert b.fa_packed_fwd_workspace_size(33, 100, 8, 2, 128) >= 33 * 16
+    assert b.fa_packed_fwd_workspace_size(3, 100000, 8, 2, 128) >= 3 * 16
     five = b.fa_packed_bwd_workspace_size(3, 100, 8, 2, 128, 5)
     seven = b.fa_packed_bwd_workspace_size(3, 100, 8, 2, 128, 7)
     # The fp32 dQ of 100 tokens and what the sequences' last tiles round up; AUTO runs the 5-GEMM form.
@@ -197,7 +200,7 @@ int main(void) {
   if (fa_packed_fwd(&f) != FA_ERR_UNSUPPORTED) fails |= 2;
   r.H = 8, r.Hkv = 2, r.d = 128;
   if (fa_qk_norm_rope(&r) != FA_OK) fails |= 4;
-  if (fa_packed_fwd_workspace_size(1, 10, 8, 2, 128) == 0) fails |= 8;
+  if (fa_packed_fwd_workspace_size(40, 10, 8, 2, 128) == 0) fails |= 8;
   printf("%d %d %d %d %d %d\n", fails, (int)sizeof(fa_packed_fwd_args), (int)sizeof(fa_packed_bwd_args),
          (int)sizeof(fa_qk_norm_rope_args), (int)sizeof(fa_qk_norm_rope_bwd_args), (int)sizeof(fa_kv4_append_args));
   printf("%d %d %d %d %d %d\n", (int)offsetof(fa_packed_fwd_args, stream), (int)offsetof(fa_packed_bwd_args, variant),

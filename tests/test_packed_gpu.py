@@ -170,7 +170,10 @@ def test_refused_by_the_torch_layer():
     refuse(ValueError, "CUDA", q, k, v, cu.cpu())
     refuse(ValueError, "lse", q, k, v, cu, lse=lse[:, :3])
     refuse(ValueError, "overlap", q, k, v, cu, out=o[:, :1].expand(-1, 4, -1))
-    refuse(ValueError, "workspace", q, k, v, cu, workspace=torch.empty(16, dtype=torch.uint8, device="cuda:0"))
+    small = torch.empty(16, dtype=torch.uint8, device="cuda:0")
+    refuse(ValueError, "workspace", q, k, v, torch.zeros(42, dtype=torch.int32, device="cuda:0"), workspace=small)
+    refuse(ValueError, "workspace", q, k, v, cu, workspace=small.float())
+    refuse(ValueError, "workspace", q, k, v, o, o, lse, cu, f=api.packed_attention_backward, workspace=small)
     refuse(FaError, "invalid", q, k, v, cu, scale=0.0)
     refuse(FaError, "invalid", q, k, v, cu, scale=1e300)
     refuse(FaError, "aligned", q.as_strided(q.shape, (q.stride(0) + 4, 64, 1)), k, v, cu) if q.stride(0) % 8 == 0 else None
@@ -402,7 +405,64 @@ def test_profile_counts_the_kernels():
         o, lse = api.packed_attention_forward(q, k, v, cu)
         api.packed_attention_backward(q, k, v, o, o, lse, cu, variant=variant)
         counts = {n: c for n, (c, _) in b.fa_profile_stop().items() if c}
-        assert counts == {"packed_plan": 1, "fwd": 1, **want}
+        assert counts == {"fwd": 1, **want}
+    b.fa_profile_start()
+    api.packed_attention_forward(*make([3] * 33, 4, 2, 128)[:4])
+    assert {n: c for n, (c, _) in b.fa_profile_stop().items() if c} == {"packed_plan": 1, "fwd": 1}
+
+
+@pytest.mark.parametrize("d", (64, 96, 128, 192, 256, 384))
+def test_forward_with_and_without_a_plan(d):
+    """The same sequences among empty ones, so many that their order is made by a kernel of its own: the same bits.
+    Lengths around a tile of keys, rows of no sequence that hold NaN, entries of cu that are out of range."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    most = 64 * (sms // 2 - 2)  # in two sequences of 4 kv heads: two items an SM, so that an item has two tiles
+    for H, Hkv in ((2, 2), (8, 2), (7, 1), (8, 4)):
+        for lengths in ([1, 64, 65, 127, 128, 129, 300], [0, 0, 257, 0], [31] * 32, [700, 5]):
+            if Hkv == 4:
+                lengths = [most - 150 - 3 - 737, 737]
+            q, k, v, cu, host = make(lengths, H, Hkv, d, seed=d + len(lengths), lead=3, tail=150)
+            for t in (q, k, v):
+                t[:3], t[host[-1]:] = math.nan, math.nan
+            for bad in (None, -5, q.shape[0] + 1):
+                host[-1] = host[-1] if bad is None else bad
+                some = torch.tensor(host, dtype=torch.int32, device="cuda:0")
+                many = torch.tensor([host[0]] * 40 + host, dtype=torch.int32, device="cuda:0")
+                assert b_bytes(some, q, k) == 0 and b_bytes(many, q, k) > 0
+                for causal in (True, False):
+                    marks = [dict(out=torch.full(q.shape, 5.0, device="cuda:0").to(torch.bfloat16),
+                                  lse=torch.full(q.shape[:2], 5.0, device="cuda:0")) for _ in range(2)]
+                    api.packed_attention_forward(q, k, v, some, causal=causal, **marks[0])
+                    api.packed_attention_forward(q, k, v, many, causal=causal, **marks[1])
+                    api.check_device_error()
+                    assert all(torch.equal(marks[0][n], marks[1][n]) for n in ("out", "lse"))
+                    assert not bool(torch.isnan(marks[0]["out"]).any())
+                    assert bool((marks[0]["out"][:3] == 5).all()) and bool((marks[0]["lse"][-150:] == 5).all())
+
+
+@pytest.mark.parametrize("d", (64, 96, 128))
+def test_items_of_two_tiles_end_where_their_sequence_does(d):
+    """NaN around the sequences and in one of them, where an item holds two query tiles."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, v, cu, host = make([1900, 37, 661, 100], 16, 2, d, seed=d, lead=2, tail=130)
+    dirty = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda:0")
+    dirty[:2], dirty[host[-1]:], dirty[host[1]:host[2]] = True, True, True
+    poison = [t.clone() for t in (q, k, v)]
+    for t in poison:
+        t[dirty] = math.nan
+    for causal in (True, False):
+        o, lse = api.packed_attention_forward(q, k, v, cu, causal=causal)
+        o2, lse2 = api.packed_attention_forward(*poison, cu, causal=causal)
+        api.check_device_error()
+        assert torch.equal(o[~dirty], o2[~dirty]) and torch.equal(lse[~dirty], lse2[~dirty])
+
+
+def b_bytes(cu, q, k):
+    from tiled_attention_tmem_gb300 import api
+    return api.packed_forward_workspace_bytes(cu.numel() - 1, q.shape[0], q.shape[1], k.shape[1], q.shape[2])
 
 
 # ------------------------------------------------------------------ as they are used together

@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_kv_kernel(const __grid_cons
     } else if (RAGGED && warp == 3) {
       // --------------------------------------------------------- scheduling
       if constexpr (RAGGED)
-        ragged_schedule(p.sched, C::BN, C::DSPLIT * qsplit, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
+        ragged_schedule<false>(p.sched, C::BN, C::DSPLIT * qsplit, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
                         BAR(C::B_ITEMASK), ab, (kKBwdKV << 8) | 20);
     }
     } else if (warp < C::DRAIN_W0) {
@@ -1845,7 +1845,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) bwd_q_kernel(const __grid_const
       __syncwarp();
     } else if (RAGGED && warp == 3) {
       if constexpr (RAGGED)
-        ragged_schedule(p.sched, p.tokens, C::DQS, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
+        ragged_schedule<false>(p.sched, p.tokens, C::DQS, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
                         BAR(C::B_ITEMASK), ab, (kKBwdQ << 8) | 13);
     } else if (warp >= 4) {
       const int quad = warp & 3;

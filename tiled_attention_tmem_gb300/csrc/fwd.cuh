@@ -53,7 +53,7 @@
 namespace fa {
 
 struct FwdParams {
-  static constexpr bool kRagged = false;
+  static constexpr bool kRagged = false, kDirect = false;
   CUtensorMap q_map;  // 3-D {d, N, B*H} bf16, box {64, 128, 1}, 128-byte swizzle
   CUtensorMap k_map;  // same tensor shape, box {64, BN, 1}
   CUtensorMap v_map;
@@ -75,7 +75,7 @@ struct FwdParams {
 
 // Packed sequences: q, o [T, H, d] and k, v [T, Hkv, d] with strides in elements.
 struct RaggedFwdParams {
-  static constexpr bool kRagged = true;
+  static constexpr bool kRagged = true, kDirect = false;
   CUtensorMap q_map;           // {d, G, T, Hkv}, box {64, G, tokens, 1}
   CUtensorMap k_map;           // {d, T, Hkv}, box {64, BN, 1}
   CUtensorMap v_map;
@@ -93,6 +93,11 @@ struct RaggedFwdParams {
   int dv;
   float scale_log2;
   int causal;
+};
+
+// Packed sequences without a plan (and its v_ends): few of them.
+struct DirectFwdParams : RaggedFwdParams {
+  static constexpr bool kDirect = true;
 };
 
 // Merge of split-KV parts: for each row, L = log2 sum_s 2^(L_s) and
@@ -218,10 +223,10 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
 
 // SPLIT: the split-KV instantiation (p.splits > 1); the plain one keeps lo = 0
 // and s = 0 as constants and has no part epilogue.
-// P: FwdParams, or RaggedFwdParams (packed sequences; never split).
+// P: FwdParams, or RaggedFwdParams or DirectFwdParams (packed sequences; never split).
 template <class C, bool SPLIT, class P = FwdParams>
 __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constant__ P p) {
-  constexpr bool RAGGED = P::kRagged;
+  constexpr bool RAGGED = P::kRagged, DIRECT = P::kDirect;
   static_assert(!(RAGGED && SPLIT), "packed sequences are not split");
   constexpr int D = C::D, NQ = C::NQ, BN = C::BN, S = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
           // meet probabilities of 0, and may hold anything).  Q and K need none: their rows and columns of
           // S are masked.
           auto map_of_v = [&](int j) -> const CUtensorMap* {
-            if constexpr (RAGGED) {
+            if constexpr (RAGGED && !DIRECT) {
               if ((j + 1) * BN > I.len) {
                 const CUtensorMap* m = p.v_ends + I.seq;
                 if (I.seq != seq) {
@@ -749,7 +754,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
     } else if (RAGGED && warp == 3) {
       // --------------------------------------------------------- scheduling
       if constexpr (RAGGED)
-        ragged_schedule(p.sched, p.tiles * p.tokens, 1, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
+        ragged_schedule<DIRECT>(p.sched, p.tiles * p.tokens, 1, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
                         BAR(C::B_ITEMASK), ab, (kKFwd << 8) | 13);
     }
     } else {
@@ -777,7 +782,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
         rtok += t * p.tokens;
         rown = r < p.tokens * p.G;
       }
-      int ring = 0;  // packed: slots of the K/V ring that the items so far have used
+      int ring = 0;  // QT, DIRECT: slots of the K/V ring that the items so far use, the present one's among them
       auto write_q = [&](const Item& J) -> bool {
         const uint16_t* qsrc = nullptr;
         bool qok;
@@ -858,6 +863,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
           if (wq >= 0) write_q(coords(wq));
         }
         const Part part = SPLIT ? part_of(item_of(rr)) : Part{0, 0};
+        if constexpr (DIRECT && !C::QT) ring += 2 * I.nmax;  // (QT: write_q)
         const int n = I.nkv[t];
         const int bh = I.bh;
         int qi, limit;  // this row's query and the last key that it sees
@@ -950,6 +956,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
               tmem_st_32x32b_x32(tO + c0, orr);
             }
             tmem_wait_st();
+          }
+          if constexpr (DIRECT) {
+            // The sequence's last key tile, in the last slot of the item: rows of V past its end become zeros
+            // (the probabilities there are 0, but what lies there may be a NaN).  Each query tile's warps
+            // clear them all before its P V.
+            if (kbase + BN > I.len) {
+              if (!wait_warp(BAR(C::B_KVFULL + (ring - 1) % S), ((ring - 1) / S) & 1, ab, (kKFwd << 8) | 16)) {
+                ok = false;
+                break;
+              }
+              uint8_t* const tile = gbase + C::OFF_KV + (ring - 1) % S * C::KV_TILE;
+              for (int pn = 0; pn < C::PANELS; ++pn)
+                for (int o = (I.len - kbase) * 128 + r * 16; o < BN * 128; o += 128 * 16)
+                  *reinterpret_cast<uint4*>(tile + pn * C::KV_PANEL + o) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+            }
           }
           tc_fence_before();
           __syncwarp();

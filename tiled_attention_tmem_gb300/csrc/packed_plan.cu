@@ -140,8 +140,8 @@ fa_status fa_packed_fwd(const fa_packed_fwd_args* a) {
   for (const fa_rows* r : {&a->k, &a->v})
     if ((st = packed_rows_checks(*r, s.T, s.Hkv)) != FA_OK) return st;
   if (!all_aligned(4, a->lse, a->cu)) return FA_ERR_MISALIGNED;
-  if (!a->workspace || !all_aligned(256, static_cast<char*>(a->workspace)) ||
-      a->workspace_bytes < packed_fwd_bytes(s))
+  const size_t need = packed_fwd_bytes(s);
+  if (need > 0 && (!a->workspace || !all_aligned(256, static_cast<char*>(a->workspace)) || a->workspace_bytes < need))
     return FA_ERR_WORKSPACE;
   return run_packed_fwd(*a, s);
 }

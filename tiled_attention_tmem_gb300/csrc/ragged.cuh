@@ -7,10 +7,11 @@
 // kernels are those of equal heads over G rows a token.  The rows past (M / G) * G of a
 // tile belong to nobody.
 //
-// Tensor maps: a tile that reaches past its sequence's end is loaded by a map of the sequence's own (built by
-// ragged_plan_kernel), whose token dimension ends there, so that it reads zeros, and not what
-// the next sequence or the rows behind the last one hold: a NaN there times a probability of 0
-// would be NaN.  Other tiles go by the launch's maps: a new map costs a fence and a fetch.
+// Ends: a tile that reaches past its sequence's end must read zeros there, and not what the next
+// sequence or the rows behind the last one hold: a NaN there times a probability of 0 would be NaN.  Such tiles are
+// loaded by a map of the sequence's own (made by ragged_plan_kernel), whose token dimension ends
+// there; other tiles go by the launch's maps, since a new map costs a fence and a fetch.  The forward without a plan
+// has no such maps: its softmax warps clear those rows of V in shared memory.
 #pragma once
 #include "common.cuh"
 
@@ -21,7 +22,12 @@ struct RaggedSched {
   const int4* seqs;  // [B] in the same order: first token, tokens, sequence, heads per launch-order group
   int* counter;      // items claimed beyond the first of each CTA (zero at launch)
   int B;
+  // Without a plan the scheduling warps put the sequences, kRaggedDirect at most, in order themselves, and take their
+  // items in turn, without a counter; only B and these are set.
+  const int* cu;
+  int T;
 };
+constexpr int kRaggedDirect = 32;  // sequences that need no plan: a lane each
 
 struct RaggedItem {
   int start, len, seq;  // first token and tokens of the sequence, its index
@@ -37,22 +43,64 @@ constexpr int kRaggedRingBytes = 32;  // a slot of the ring
 // after the first is claimed when the producer asks for it (`ask`, one arrival an item), while it
 // loads the one before: earlier, a CTA that is still busy would hold items that others could start.
 // Claimed indices only grow, so the search goes on from the last sequence, 32 at a time.
+// DIRECT: without a plan; CTA c takes items c, 2G - 1 - c, 2G + c, ... of G CTAs.
+template <bool DIRECT>
 __device__ __forceinline__ void ragged_schedule(const RaggedSched& s, int tile_tokens, int parts, int heads,
                                                 volatile int* ring, uint32_t full0, uint32_t empty0, uint32_t ask,
                                                 const CtaAbort& ab, int where) {
   const int lane = lane_id();
-  const int total = s.base[s.B];
-  int w = blockIdx.x, rank = 0;
+  int total, rank = 0, w = blockIdx.x;
+  // DIRECT: lane r holds the sequence of rank r and its first item.
+  int my_start = 0, my_len = 0, my_seq = lane, my_base = 0, my_end = 0;
+  if constexpr (DIRECT) {
+    if (lane < s.B) {
+      my_start = s.cu[lane];
+      const int end = s.cu[lane + 1];
+      if (my_start >= 0 && my_start <= end && end <= s.T) my_len = end - my_start;
+    }
+    int my_rank = 0, from = lane;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const int other = __shfl_sync(0xffffffffu, my_len, k);
+      my_rank += other > my_len || (other == my_len && k < lane);
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (__shfl_sync(0xffffffffu, my_rank, k) == lane) from = k;
+    my_start = __shfl_sync(0xffffffffu, my_start, from);
+    my_len = __shfl_sync(0xffffffffu, my_len, from);
+    my_seq = from;
+    const int items = ((my_len + tile_tokens - 1) / tile_tokens) * parts * heads;
+    my_end = items;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, my_end, d);
+      if (lane >= d) my_end += y;
+    }
+    my_base = my_end - items;
+    total = __shfl_sync(0xffffffffu, my_end, 31);
+  } else {
+    total = s.base[s.B];
+  }
   for (int t = 0;; ++t) {
     const int k = t % kRaggedRing;
     if (!wait_warp(empty0 + 8 * k, ((t / kRaggedRing) & 1) ^ 1, ab, where)) return;
-    if (t > 0) {
+    if (DIRECT && t > 0) {
+      w = t * (int)gridDim.x + ((t & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x);
+    } else if (t > 0) {
       if (!wait_warp(ask, (t - 1) & 1, ab, where)) return;
       if (lane == 0) w = (int)gridDim.x + atomicAdd(s.counter, 1);
       w = __shfl_sync(0xffffffffu, w, 0);
     }
     int start = -1, len = 0, seq = 0, tile = 0, head = 0;
-    if (w < total) {
+    if (DIRECT && w < total) {
+      rank = __ffs(__ballot_sync(0xffffffffu, my_end > w)) - 1;
+      start = __shfl_sync(0xffffffffu, my_start, rank);
+      len = __shfl_sync(0xffffffffu, my_len, rank);
+      seq = __shfl_sync(0xffffffffu, my_seq, rank);
+      grouped_order(w - __shfl_sync(0xffffffffu, my_base, rank), ((len + tile_tokens - 1) / tile_tokens) * parts, heads,
+                    heads, tile, head);
+    } else if (w < total) {
       for (; rank < s.B; rank += 32) {
         const int i = rank + lane;
         const unsigned past = __ballot_sync(0xffffffffu, i < s.B && s.base[min(i + 1, s.B)] > w);

@@ -59,12 +59,14 @@ def _workspace(workspace, need, index, device):
 
 
 def packed_forward_workspace_bytes(sequences, tokens, heads, kv_heads, head_dim) -> int:
-    """What ``packed_attention_forward`` needs."""
+    """What ``packed_attention_forward`` needs on the current device (0: none)."""
     _check_sizes(sequences, tokens, heads, kv_heads)
     return _b.fa_packed_fwd_workspace_size(sequences, tokens, heads, kv_heads, head_dim)
 
 
-_forward_bytes = functools.lru_cache(maxsize=1024)(packed_forward_workspace_bytes)
+# By shape and device, whose multiprocessors it goes by.
+_forward_bytes = functools.lru_cache(maxsize=1024)(lambda *shape_and_device: packed_forward_workspace_bytes(
+    *shape_and_device[:-1]))
 
 
 def _shapes(q, k, v, index):
@@ -106,7 +108,7 @@ def packed_attention_forward(q, k, v, cu, scale: float | None = None, causal: bo
         lse = _empty((T, H), dtype=_F32, device=q.device)
     else:
         _dense(lse, "lse", _F32, (T, H), index)
-    workspace, at, need = _workspace(workspace, _forward_bytes(B, T, H, Hkv, d), index, q.device)
+    workspace, at, need = _workspace(workspace, _forward_bytes(B, T, H, Hkv, d, index), index, q.device)
     st = _b.fa_packed_fwd(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out.data_ptr(), ot, oh,
                           lse.data_ptr(), cu.data_ptr(), B, T, H, Hkv, d, d ** -0.5 if scale is None else _f32(scale),
                           bool(causal), at, need, _current_stream(index))
@@ -121,7 +123,6 @@ def packed_backward_workspace_bytes(sequences, tokens, heads, kv_heads, head_dim
     return _b.fa_packed_bwd_workspace_size(sequences, tokens, heads, kv_heads, head_dim, variant)
 
 
-# By shape and device, whose multiprocessors it goes by.
 _backward_bytes = functools.lru_cache(maxsize=1024)(lambda *shape_and_device: packed_backward_workspace_bytes(
     *shape_and_device[:-1]))
 
