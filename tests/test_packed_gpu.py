@@ -227,6 +227,33 @@ def test_sequences_outside_the_tokens_have_none():
         api.check_device_error()
 
 
+@pytest.mark.parametrize("d,H,Hkv,T", [(64, 4, 2, 90), (128, 4, 1, 1500), (192, 2, 2, 90), (256, 8, 1, 1500), (384, 2, 1, 90)])
+def test_gradients_of_rows_of_sequences_that_lie_outside(d, H, Hkv, T):
+    """cu that does not decrease, with sequences that begin below 0 or end past T: those have no tokens, their
+    rows' gradients are zeros, and the others are those of a call without them."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, v, _, _ = make([T], H, Hkv, d)
+    do = _do(q)
+    a, b = T // 5, T - T // 4
+    for cu, rows in (([-3, a, b], (a, b)), ([0, a, b, T + 1], (0, b)), ([-2 ** 31, -1, a, b, 2 ** 31 - 1], (a, b)),
+                     ([-5, T + 2], None), ([T + 1, T + 9], None), ([-9, -1], None), ([-4, 0, T], (0, T)),
+                     ([a, b, b, T + 7, T + 7], (a, b))):
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda:0")
+        o, lse = api.packed_attention_forward(q, k, v, cu)
+        for variant in (5, 7) if d <= 128 else (7,):
+            grads = [torch.full(t.shape, 5.0, device="cuda:0").to(torch.bfloat16) for t in (q, k, v)]
+            api.packed_attention_backward(q, k, v, o, do, lse, cu, variant=variant, grads=grads)
+            api.check_device_error()
+            lo, hi = rows or (0, 0)
+            assert not any(bool(t[:lo].any()) or bool(t[hi:].any()) for t in grads)
+            if rows:
+                at = slice(lo, hi)
+                host = [x - lo for x in cu.tolist() if lo <= x <= hi]
+                r = R.attend(q[at], k[at], v[at], host, d ** -0.5, True, do[at])
+                R.check_backward([t[at] for t in grads], r, f"{cu.tolist()} variant={variant}")
+
+
 @pytest.mark.parametrize("d,B", [(64, 3000), (128, 2048), (256, 2049)])
 def test_very_many_sequences(d, B):
     """More than are put in order, and more than a block has threads."""

@@ -34,6 +34,33 @@ struct RowTiles {
   int by_G;  // 65536 / G rounded up: r / G = r * by_G >> 16 for r < 128, G <= 32
 };
 
+// The rows [lo, hi) of the sequences: cu does not decrease, so those that do not lie in [0, T) are the
+// first ones and the last.  (Whatever cu holds, 0 <= lo <= hi <= T.)
+__device__ __forceinline__ void rows_of_sequences(const int* cu, int B, int T, int& lo, int& hi) {
+  auto first_at_least = [&](long long bound) {  // the first entry that is, or B + 1
+    int a = 0, b = B + 1;
+    while (a < b) {
+      const int mid = a + (b - a) / 2;
+      if (cu[mid] >= bound) b = mid;
+      else a = mid + 1;
+    }
+    return a;
+  };
+  lo = hi = 0;
+  if (B == 0) return;
+  lo = cu[0];
+  if (lo < 0) {
+    const int b = first_at_least(0);
+    lo = b <= B ? cu[b] : T;
+  }
+  hi = cu[B];
+  if (hi > T) {
+    const int b = first_at_least(T + 1LL) - 1;
+    hi = b >= 0 ? cu[b] : 0;
+  }
+  lo = min(max(lo, 0), T), hi = min(max(hi, lo), T);
+}
+
 // The sequence that holds tile slot ts, and the slot's first token in it; false where none does.
 // Sequence b has the slots from cu[b] / tokens + b on, which grow with b: a warp looks at 32 of
 // them at a time.
@@ -153,7 +180,8 @@ __global__ void __launch_bounds__(256, D <= 256 ? 4 : 2) ragged_pre_kernel(const
     }
   }
   // Gradients of the rows of no sequence: before the first one and behind the last.
-  const int lo = t.B > 0 ? min(max(t.cu[0], 0), t.T) : 0, hi = t.B > 0 ? min(max(t.cu[t.B], lo), t.T) : 0;
+  int lo, hi;
+  rows_of_sequences(t.cu, t.B, t.T, lo, hi);
   const long long spare = (long long)lo + (t.T - hi), chunks = t.hd / 8;
 #pragma unroll
   for (int x = 0; x < 3; ++x) {
@@ -229,8 +257,9 @@ __global__ void __launch_bounds__(256) ragged_kvsum_kernel(const __grid_constant
   grid_dep_wait();
   if (*reinterpret_cast<volatile const int*>(p.err) != 0) return;
   const int chunks = p.hd / 8;
-  const int lo = max(p.cu[0], 0), hi = min(p.cu[p.B], p.T);  // (the other rows are zeros already)
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, work = (long long)max(hi - lo, 0) * p.Hkv * chunks;
+  int lo, hi;  // (the other rows are zeros already)
+  rows_of_sequences(p.cu, p.B, p.T, lo, hi);
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, work = (long long)(hi - lo) * p.Hkv * chunks;
   if (i >= work) return;
   const long long row = i / chunks;
   const int c = (int)(i - row * chunks) * 8, tok = lo + (int)(row / p.Hkv), head = (int)(row % p.Hkv);
