@@ -440,8 +440,8 @@ def test_profile_counts_the_kernels():
 
 @pytest.mark.parametrize("d", (64, 96, 128, 192, 256, 384))
 def test_forward_with_and_without_a_plan(d):
-    """The same sequences among empty ones, so many that their order is made by a kernel of its own: the same bits.
-    Lengths around a tile of keys, rows of no sequence that hold NaN, entries of cu that are out of range."""
+    """The same sequences among empty ones, so many that their order is made by a kernel of its own: the same bits
+    where the tiles are the same ones (at d = 96 and 128 they go by the mean length).  Lengths around a tile of keys, rows of no sequence that hold NaN, entries of cu that are out of range."""
     import torch
     from tiled_attention_tmem_gb300 import api
     sms = torch.cuda.get_device_properties(0).multi_processor_count
@@ -464,7 +464,12 @@ def test_forward_with_and_without_a_plan(d):
                     api.packed_attention_forward(q, k, v, some, causal=causal, **marks[0])
                     api.packed_attention_forward(q, k, v, many, causal=causal, **marks[1])
                     api.check_device_error()
-                    assert all(torch.equal(marks[0][n], marks[1][n]) for n in ("out", "lse"))
+                    if d in (96, 128):
+                        r = R.attend(q, k, v, host if bad is None else host[:-1], d ** -0.5, causal)
+                        for m in marks:
+                            R.check_forward(m["out"], m["lse"], r, d, f"{lengths} {H}/{Hkv} {bad} {causal}")
+                    else:
+                        assert all(torch.equal(marks[0][n], marks[1][n]) for n in ("out", "lse"))
                     assert not bool(torch.isnan(marks[0]["out"]).any())
                     assert bool((marks[0]["out"][:3] == 5).all()) and bool((marks[0]["lse"][-150:] == 5).all())
 
@@ -485,6 +490,32 @@ def test_items_of_two_tiles_end_where_their_sequence_does(d):
         o2, lse2 = api.packed_attention_forward(*poison, cu, causal=causal)
         api.check_device_error()
         assert torch.equal(o[~dirty], o2[~dirty]) and torch.equal(lse[~dirty], lse2[~dirty])
+
+
+@pytest.mark.parametrize("d", (64, 96, 128))
+@pytest.mark.parametrize("causal", (True, False))
+@pytest.mark.parametrize("lengths", ([2900, 1500, 37, 2200], [1400, 1100, 1270, 1], [640, 641, 639, 200, 900], [320, 300, 350, 290, 7], [170, 150, 160]))
+def test_forward_on_both_sides_of_the_choice_of_tiles(lengths, causal, d):
+    """Mean lengths around those at which the tiles change, many items a multiprocessor, NaN between two of the
+    sequences; and the same sequences behind so many empty ones that the mean takes the other tiles."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, v, cu, host = make(lengths, 16, 4, d, seed=sum(lengths), spread=1.5)
+    r = R.attend(q, k, v, host, d ** -0.5, causal)
+    dirty = slice(host[1], host[2])
+    poison = [t.clone() for t in (q, k, v)]
+    for t in poison:
+        t[dirty] = math.nan
+    for before in (0, 40 * len(lengths)):
+        many = torch.tensor([0] * before + host, dtype=torch.int32, device="cuda:0")
+        o, lse = api.packed_attention_forward(q, k, v, many, causal=causal)
+        api.check_device_error()
+        R.check_forward(o, lse, r, d, f"{lengths} d={d} {before}")
+        o2, lse2 = api.packed_attention_forward(*poison, many, causal=causal)
+        api.check_device_error()
+        for got, want in ((o2, o), (lse2, lse)):
+            got[dirty] = want[dirty]
+            assert torch.equal(got, want)
 
 
 def b_bytes(cu, q, k):

@@ -158,6 +158,7 @@ struct FwdCfg {
   static constexpr uint32_t OFF_RING = OFF_MISC + 16;  // packed sequences: claimed items
   static constexpr int ITEM_READERS = 2 + 4 * NQ;      // the producer, the MMA warp, the softmax warps
   static constexpr uint32_t SMEM_BYTES = OFF_RING + kRaggedRing * kRaggedRingBytes + 1024;  // + alignment slack
+  static constexpr int CTAS = SMEM_BYTES <= 116000 ? 2 : 1;  // that an SM holds at a time (packed sequences)
   static constexpr int TMEM_S = 0;              // S_t (and P_t aliased) at (t*SB + buffer)*BN
   static constexpr int TMEM_O = NQ * SB * BN;   // O_t at TMEM_O + t*D
   static constexpr int TMEM_Q = TMEM_O + NQ * D;  // QT: Q_t as packed bf16 pairs at TMEM_Q + t*D/2
@@ -165,7 +166,7 @@ struct FwdCfg {
   static constexpr uint32_t TMEM_COLS =
       TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
   static constexpr int THREADS = 128 + 128 * NQ;
-  static_assert(TMEM_USED <= 512, "TMEM budget");
+  static_assert(CTAS * TMEM_COLS <= 512, "TMEM budget");
   static_assert(BN % 32 == 0 && BN <= 256 && D % 64 == 0 && D <= 384 && PVN % 64 == 0, "tile shape");
   static_assert(!(QT && QSD), "Q lives in one place");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -188,8 +189,12 @@ using Fwd256 = FwdCfg<256, 1, 64, 6, true>;
 // double-buffered in TMEM next to the 384-column O (512 columns), two K/V slots
 // of 48 KiB.
 using Fwd384 = FwdCfg<384, 1, 64, 2, false, true>;
-// Packed sequences at d = 64: two buffers of Q (64 KiB beside the ring's 96).
-using RaggedFwd64 = FwdCfg<64, 2, 128, 6, false, false, 2>;
+// Packed sequences, short ones: 1 x 128 query rows, 64 keys, S double-buffered, half of the SM's shared memory, TMEM and
+// registers, so that one CTA's item changes pass behind the other's work.  Its operands are read from shared memory
+// more often a product, and each CTA loads its own K and V: long sequences run better in the tiles above (packed_fwd.cu
+// has the rule).  d = 64: two buffers of Q, 8 stages of K/V (104 KiB); d = 128: 4 stages (105 KiB).
+using RaggedFwd64 = FwdCfg<64, 1, 64, 8, false, true, 2>;
+using RaggedFwd128 = FwdCfg<128, 1, 64, 4, false, true>;
 
 __device__ __forceinline__ int fwd_kv_tiles(int qrow0, int N, int causal, int BN) {
   if (qrow0 >= N) return 0;
@@ -229,7 +234,7 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
 // and s = 0 as constants and has no part epilogue.
 // P: FwdParams, or RaggedFwdParams or DirectFwdParams (packed sequences; never split).
 template <class C, bool SPLIT, class P = FwdParams>
-__global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constant__ P p) {
+__global__ void __launch_bounds__(C::THREADS, C::CTAS) fwd_kernel(const __grid_constant__ P p) {
   constexpr bool RAGGED = P::kRagged, DIRECT = P::kDirect;
   static_assert(!(RAGGED && SPLIT), "packed sequences are not split");
   constexpr int D = C::D, NQ = C::NQ, BN = C::BN, S = C::STAGES;
@@ -601,7 +606,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
                 mma_ts(tmem + C::TMEM_S + (t * C::SB + b) * BN, tmem + C::TMEM_Q + t * (D / 2) + 8 * k,
                        desc_kmajor(kb, C::KV_PANEL, 16 * k), idS, k > 0 ? 1u : 0u);
             } else {
-              const uint32_t qa = sbase + C::OFF_Q + t * C::Q_TILE;
+              uint32_t qa = sbase + C::OFF_Q + t * C::Q_TILE;
+              if constexpr (RAGGED && C::QB > 1) qa += nq[t] % C::QB * (NQ * C::Q_TILE);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
                 mma_ss(tmem + C::TMEM_S + (t * C::SB + b) * BN, desc_kmajor(qa, C::Q_PANEL, 16 * k),
@@ -615,10 +621,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
             // An empty key part has no Q hand-off (the softmax warps skip it too).
             if (I.nmax <= 0) continue;
             // QT: the softmax warps have written this item's Q into TMEM; QSD: its TMA load landed.
-            constexpr int kFull = C::QT ? C::B_QREADY : RAGGED ? C::B_QTFULL : C::B_QFULL;
-            constexpr int kEmpty = RAGGED ? C::B_QTEMPTY : C::B_QEMPTY;
-            if (!wait_warp(BAR(kFull), nitems & 1, ab, (kKFwd << 8) | 11)) break;
-            ++nitems;
+            if constexpr (RAGGED && C::QSD) {
+              static_assert(NQ == 1, "one tile an item");
+              if (!take_q(0)) break;
+            } else {
+              if (!wait_warp(BAR(C::QT ? C::B_QREADY : C::B_QFULL), nitems & 1, ab, (kKFwd << 8) | 11)) break;
+              ++nitems;
+            }
+            auto after_last_s = [&] {  // QSD: Q may be loaded again
+              if constexpr (RAGGED && C::QSD) {
+                drop_q(0);
+                ++nq[0];
+              } else if (C::QSD) {
+                mma_commit(BAR(C::B_QEMPTY));
+              }
+            };
             if constexpr (RAGGED && C::QT) {
               // (and have read the ring's slots that it came through)
               if (lane == 0)
@@ -631,7 +648,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
             for (int t = 0; t < NQ; ++t)
               if (I.nkv[t] > 0) issue_sq(t, g[t] & 1, sk);
             mma_commit(BAR(C::B_KVEMPTY + sk));
-            if (C::QSD && I.nmax == 1) mma_commit(BAR(kEmpty));  // the item's last S MMAs
+            if (I.nmax == 1) after_last_s();
             for (int j = 0; ok && j < I.nmax; ++j) {
               // S_t(j+1) into the other buffer of tile t, whose P_t(j-1) was read by
               // PV_t(j-1) (issued before).
@@ -644,7 +661,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fwd_kernel(const __grid_constan
                 for (int t = 0; t < NQ; ++t)
                   if (j + 1 < I.nkv[t]) issue_sq(t, (g[t] + j + 1) & 1, sk);
                 mma_commit(BAR(C::B_KVEMPTY + sk));
-                if (C::QSD && j + 2 == I.nmax) mma_commit(BAR(kEmpty));  // the item's last S MMAs
+                if (j + 2 == I.nmax) after_last_s();
               }
               int sv = 0;
               if (!take(sv)) {

@@ -45,11 +45,23 @@ fa_status run(const fa_packed_fwd_args& a, const PackedShape& s) {
   p.H = s.H, p.Hkv = s.Hkv, p.G = s.G(), p.by_G = (65536 + s.G() - 1) / s.G(), p.tokens = tokens, p.dv = s.d;
   p.scale_log2 = a.scale * kLog2e;
   p.causal = a.causal;
-  // One CTA an SM, and no more than there can be items.
+  // As many CTAs as the SMs hold, and no more than there can be items.
   const long long most = ((long long)s.T / (p.tiles * tokens) + s.B) * s.Hkv;
-  const unsigned grid = (unsigned)std::min<long long>(most, sm_count_cached());
+  const unsigned grid = (unsigned)std::min<long long>(most, C::CTAS * sm_count_cached());
   return launch_raised(FA_KERNEL_FWD, fwd_kernel<C, false, P>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES,
                        st, p, raised);
+}
+
+// Whether d = 96 or 128 runs two CTAs an SM: by the tokens of a mean sequence, since short items are mostly item
+// changes.  Measured with 32 heads on 8 of 128, tiles of two / two CTAs in us, lengths at random around the mean: causal,
+// 64 of 256: 99 / 80, 16 of 1024: 183 / 179, 12 of 1536: 257 / 262, 4 of 4096: 608 / 672; without the mask, where an item
+// has twice the keys and both of its tiles the same ones, 128 of 128: 103 / 92, 64 of 256: 120 / 114, 32 of 512: 149 /
+// 155.  At d = 96, whose tiles' last quarter is loaded as zeros, by half of that: causal, 32 of 512: 103 / 99, 24 of 768: 146
+// / 165.  (d = 64 always runs two: 128 of 128 86 / 60 us, 8 of 2048 202 / 181, 2 of 8192 395 / 378; eight heads on eight
+// without the mask, 2 around 8192: 207 / 224.)
+bool two_ctas(const PackedShape& s, int causal) {
+  const long long mean = s.T / s.B;
+  return (causal ? mean : 4 * mean) <= (s.d == 96 ? 640 : 1280);
 }
 
 template <class P>
@@ -57,7 +69,7 @@ fa_status run_with(const fa_packed_fwd_args& a, const PackedShape& s) {
   switch (s.d) {
     case 64: return run<RaggedFwd64, P>(a, s);
     case 96:
-    case 128: return run<Fwd128, P>(a, s);
+    case 128: return two_ctas(s, a.causal) ? run<RaggedFwd128, P>(a, s) : run<Fwd128, P>(a, s);
     case 192: return run<Fwd192, P>(a, s);
     case 256: return run<Fwd256, P>(a, s);
     case 384: return run<Fwd384, P>(a, s);
