@@ -93,7 +93,6 @@ struct RaggedFwdParams {
   int G;       // query heads of a kv head
   int by_G;    // 65536 / G rounded up: r / G = r * by_G >> 16 for r < 128, G <= 32
   int tokens;  // tokens of a 128-row tile: 128 / G rounded down
-  int tiles;   // Q tiles of an item: NQ, or 1 where items are few
   int dv;
   float scale_log2;
   int causal;
@@ -189,7 +188,7 @@ using Fwd256 = FwdCfg<256, 1, 64, 6, true>;
 // double-buffered in TMEM next to the 384-column O (512 columns), two K/V slots
 // of 48 KiB.
 using Fwd384 = FwdCfg<384, 1, 64, 2, false, true>;
-// Packed sequences, short ones: 1 x 128 query rows, 64 keys, S double-buffered, half of the SM's shared memory, TMEM and
+// Packed sequences, short ones or few items: 1 x 128 query rows, 64 keys, S double-buffered, half of the SM's shared memory, TMEM and
 // registers, so that one CTA's item changes pass behind the other's work.  Its operands are read from shared memory
 // more often a product, and each CTA loads its own K and V: long sequences run better in the tiles above (packed_fwd.cu
 // has the rule).  d = 64: two buffers of Q, 8 stages of K/V (104 KiB); d = 128: 4 stages (105 KiB).
@@ -318,13 +317,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) fwd_kernel(const __grid_c
                                              (kKFwd << 8) | 12))
         return false;
       it.start = x.start, it.len = x.len, it.seq = x.seq, it.bh = x.head;
-      const int span = p.tiles * p.tokens, blocks = (x.len + span - 1) / span;
+      const int span = NQ * p.tokens, blocks = (x.len + span - 1) / span;
       it.q0 = (p.causal ? blocks - 1 - x.tile : x.tile) * span;
       it.nmax = 0;
 #pragma unroll
       for (int t2 = 0; t2 < NQ; ++t2) {
-        it.nkv[t2] =
-            t2 < p.tiles ? ragged_kv_tiles(it.q0 + t2 * p.tokens, p.tokens, x.len, p.causal, BN) : 0;
+        it.nkv[t2] = ragged_kv_tiles(it.q0 + t2 * p.tokens, p.tokens, x.len, p.causal, BN);
         it.nmax = max(it.nmax, it.nkv[t2]);
       }
       return true;
@@ -775,7 +773,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) fwd_kernel(const __grid_c
     } else if (RAGGED && warp == 3) {
       // --------------------------------------------------------- scheduling
       if constexpr (RAGGED)
-        ragged_schedule<DIRECT>(p.sched, p.tiles * p.tokens, 1, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
+        ragged_schedule<DIRECT>(p.sched, NQ * p.tokens, 1, p.Hkv, item_ring, BAR(C::B_ITEMFULL), BAR(C::B_ITEMEMPTY),
                         BAR(C::B_ITEMASK), ab, (kKFwd << 8) | 13);
     }
     } else {
@@ -980,8 +978,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) fwd_kernel(const __grid_c
           }
           if constexpr (DIRECT) {
             // The sequence's last key tile, in the last slot of the item: rows of V past its end become zeros
-            // (the probabilities there are 0, but what lies there may be a NaN).  Each query tile's warps
-            // clear them all before its P V.
+            // (the probabilities there are 0, but what lies there may be a NaN).
+            static_assert(NQ == 1, "cleared by one tile's warps");
             if (kbase + BN > I.len) {
               if (!wait_warp(BAR(C::B_KVFULL + (ring - 1) % S), ((ring - 1) / S) & 1, ab, (kKFwd << 8) | 16)) {
                 ok = false;

@@ -21,18 +21,13 @@ fa_status run(const fa_packed_fwd_args& a, const PackedShape& s) {
   if ((e = packed_query_map(&p.q_map, a.q, s, tokens)) != FA_OK) return e;
   if ((e = packed_key_map(&p.k_map, a.k, s, C::BN)) != FA_OK) return e;
   if ((e = packed_key_map(&p.v_map, a.v, s, C::BN)) != FA_OK) return e;
-  // Items of one tile where those of two would not fill the SMs: shorter by half, if slower a tile.  Measured in us
-  // (items of two / of one): two sequences up to 1500, four heads on two of 64: 21 / 17; one of 2048, eight on one of
-  // 128: 26 / 25; two up to 2048, eight on two of 128: 26 / 24; above an item an SM, four up to 1500: 24 / 29.
-  const double items = (s.T / (2.0 * tokens) + s.B / 2.0) * s.Hkv;
-  p.tiles = C::NQ > 1 && items < sm_count_cached() ? 1 : C::NQ;
   if constexpr (P::kDirect) {
     p.v_ends = nullptr;
     p.sched = RaggedSched{};
     p.sched.B = s.B, p.sched.cu = a.cu, p.sched.T = s.T;
   } else {
     const PackedPlan plan = packed_plan_at(a.workspace, s.B, 1);
-    const PackedCut cut = {p.tiles * tokens, 1, 4.0 * s.d};  // K and V
+    const PackedCut cut = {C::NQ * tokens, 1, 4.0 * s.d};  // K and V
     if ((e = run_packed_plan(packed_plan_params(plan, a.cu, s, &cut, 1, &p.v_map, 1, 0), st)) != FA_OK) return e;
     p.v_ends = plan.maps;
     p.sched = plan.sched[0];
@@ -46,22 +41,31 @@ fa_status run(const fa_packed_fwd_args& a, const PackedShape& s) {
   p.scale_log2 = a.scale * kLog2e;
   p.causal = a.causal;
   // As many CTAs as the SMs hold, and no more than there can be items.
-  const long long most = ((long long)s.T / (p.tiles * tokens) + s.B) * s.Hkv;
+  const long long most = ((long long)s.T / (C::NQ * tokens) + s.B) * s.Hkv;
   const unsigned grid = (unsigned)std::min<long long>(most, C::CTAS * sm_count_cached());
   return launch_raised(FA_KERNEL_FWD, fwd_kernel<C, false, P>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES,
                        st, p, raised);
 }
 
-// Whether d = 96 or 128 runs two CTAs an SM: by the tokens of a mean sequence, since short items are mostly item
-// changes.  Measured with 32 heads on 8 of 128, tiles of two / two CTAs in us, lengths at random around the mean: causal,
-// 64 of 256: 99 / 80, 16 of 1024: 183 / 179, 12 of 1536: 257 / 262, 4 of 4096: 608 / 672; without the mask, where an item
-// has twice the keys and both of its tiles the same ones, 128 of 128: 103 / 92, 64 of 256: 120 / 114, 32 of 512: 149 /
-// 155.  At d = 96, whose tiles' last quarter is loaded as zeros, by half of that: causal, 32 of 512: 103 / 99, 24 of 768: 146
-// / 165.  (d = 64 always runs two: 128 of 128 86 / 60 us, 8 of 2048 202 / 181, 2 of 8192 395 / 378; eight heads on eight
-// without the mask, 2 around 8192: 207 / 224.)
+// Items of one tile that there can be, and whether the SMs take two of them each or fewer.
+bool few_items(const PackedShape& s) {
+  return ((long long)s.T / (128 / s.G()) + s.B) * s.Hkv <= 2LL * sm_count_cached();
+}
+
+// Whether d = 96 or 128 runs two CTAs an SM: where items are few, since a lone tile's MMAs do not overlap its
+// softmax in the tiles of two, and by the tokens of a mean sequence, since short items are mostly item changes.
+// Measured, tiles of two (with one of them used where items are few) / two CTAs in us, d = 128.  Few items, causal: one
+// sequence of 2048, eight heads on one, 24.9 / 20.1; one of 16384, one head, 156 / 123; two of 2048, eight on eight, 41 /
+// 27; at d = 96 41 / 33, at the worst one of 8192, four on two, 81 / 93.  Above that, one of 6000, 32 on one: 176 /
+// 203.  Many, 32 heads on 8, lengths at random around the mean: causal, 64 of 256: 99 / 80, 16 of 1024: 183 / 179, 12 of
+// 1536: 257 / 262, 4 of 4096: 608 / 672; without the mask, where an item has twice the keys and both of its tiles the same
+// ones, 128 of 128: 103 / 92, 64 of 256: 120 / 114, 32 of 512: 149 / 155.  At d = 96, whose tiles' last quarter is
+// loaded as zeros, by half of that: causal, 32 of 512: 103 / 99, 24 of 768: 146 / 165.
+// (d = 64 always runs two: 128 of 128 86 / 60 us, 8 of 2048 202 / 181, 2 of 8192 395 / 378; at the worst eight heads on
+// eight without the mask, 2 around 8192: 207 / 224.)
 bool two_ctas(const PackedShape& s, int causal) {
   const long long mean = s.T / s.B;
-  return (causal ? mean : 4 * mean) <= (s.d == 96 ? 640 : 1280);
+  return few_items(s) || (causal ? mean : 4 * mean) <= (s.d == 96 ? 640 : 1280);
 }
 
 template <class P>
@@ -69,7 +73,10 @@ fa_status run_with(const fa_packed_fwd_args& a, const PackedShape& s) {
   switch (s.d) {
     case 64: return run<RaggedFwd64, P>(a, s);
     case 96:
-    case 128: return two_ctas(s, a.causal) ? run<RaggedFwd128, P>(a, s) : run<Fwd128, P>(a, s);
+    case 128:
+      if constexpr (!P::kDirect)
+        if (!two_ctas(s, a.causal)) return run<Fwd128, P>(a, s);
+      return run<RaggedFwd128, P>(a, s);
     case 192: return run<Fwd192, P>(a, s);
     case 256: return run<Fwd256, P>(a, s);
     case 384: return run<Fwd384, P>(a, s);
@@ -79,15 +86,13 @@ fa_status run_with(const fa_packed_fwd_args& a, const PackedShape& s) {
 
 }  // namespace
 
-// Without a plan (and a workspace) where a lane each suffices for the sequences and the SMs take two items of one
-// tile or fewer.  A plan is a launch before the kernel's, and lets more items than that be claimed by whoever is free.
-// Measured in us on the GPU, and of a call's time on the host (without / with a plan): four sequences of 71 tokens in
-// all, eight heads on two of 64: 6.7 / 12.9, 19 / 25; four of 512, eight on eight of 64: 10.3 / 17.2; 1500 and 700, eight
-// on four of 384: 35 / 42; 286 items of 128: 42 / 52; at the worst, eight of 900, 240 items, where the claims
-// balance better: 28.5 / 25.7.
+// Without a plan (and a workspace) where items are few and a lane each suffices for the sequences.  A plan is a launch
+// before the kernel's, and lets more items than that be claimed by whoever is free.  Measured in us on the GPU, and of
+// a call's time on the host (without / with a plan): four sequences of 71 tokens in all, eight heads on two of
+// 64: 5.5 / 11.6, 13.7 / 19.4; four of 512, eight on eight of 64: 9.0 / 15.0; eight of 900, four on two of 128, 240 items: 17.5
+// / 23.4; 1500 and 700, eight on four of 384: 35.5 / 41.1.
 size_t packed_fwd_bytes(const PackedShape& s) {
-  const long long most = ((long long)s.T / (128 / s.G()) + s.B) * s.Hkv;
-  return s.B <= kRaggedDirect && most <= 2LL * sm_count_cached() ? 0 : packed_plan_bytes(s.B, 1, 1);
+  return s.B <= kRaggedDirect && few_items(s) ? 0 : packed_plan_bytes(s.B, 1, 1);
 }
 
 fa_status run_packed_fwd(const fa_packed_fwd_args& a, const PackedShape& s) {
