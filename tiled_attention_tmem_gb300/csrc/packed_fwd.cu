@@ -89,8 +89,8 @@ fa_status run_with(const fa_packed_fwd_args& a, const PackedShape& s) {
 // Without a plan (and a workspace) where items are few and a lane each suffices for the sequences.  A plan is a launch
 // before the kernel's, and lets more items than that be claimed by whoever is free.  Measured in us on the GPU, and of
 // a call's time on the host (without / with a plan): four sequences of 71 tokens in all, eight heads on two of
-// 64: 5.5 / 11.6, 13.7 / 19.4; four of 512, eight on eight of 64: 9.0 / 15.0; eight of 900, four on two of 128, 240 items: 17.5
-// / 23.4; 1500 and 700, eight on four of 384: 35.5 / 41.1.
+// 64: 5.2 / 8.1, 14 / 20; four of 512, eight on eight of 64: 9.0 / 11.5; eight of 900, four on two of 128, 240 items: 17.3
+// / 19.9; 1500 and 700, eight on four of 384: 35.3 / 36.9.
 size_t packed_fwd_bytes(const PackedShape& s) {
   return s.B <= kRaggedDirect && few_items(s) ? 0 : packed_plan_bytes(s.B, 1, 1);
 }

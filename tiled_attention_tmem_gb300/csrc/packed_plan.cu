@@ -9,12 +9,12 @@
 namespace fa {
 namespace {
 
-constexpr int kPlanThreads = 1024;
-
-__global__ void __launch_bounds__(kPlanThreads) ragged_plan_kernel(const __grid_constant__ RaggedPlanParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) ragged_plan_kernel(const __grid_constant__ RaggedPlanParams p) {
   grid_dep_wait();
-  if (blockIdx.x == 0) plan_schedule<kPlanThreads>(p);
-  else plan_maps<kPlanThreads>(p, blockIdx.x - 1, gridDim.x - 1);
+  grid_dep_launch();  // (the forward's blocks set up beside the plan)
+  if (blockIdx.x == 0) plan_schedule<THREADS>(p);
+  else plan_maps<THREADS>(p, blockIdx.x - 1, gridDim.x - 1);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -65,8 +65,11 @@ int packed_map_blocks(int B, int nmaps, int threads) {
 }
 
 fa_status run_packed_plan(const RaggedPlanParams& p, cudaStream_t st) {
-  return launch(FA_KERNEL_PACKED_PLAN, ragged_plan_kernel, dim3(1 + packed_map_blocks(p.B, p.nmaps, kPlanThreads)),
-                dim3(kPlanThreads), 0, st, p);
+  // Few sequences: a small block, whose barriers are cheaper.
+  const bool few = p.B <= kPlanCounted;
+  const int threads = few ? 256 : 1024;
+  return launch(FA_KERNEL_PACKED_PLAN, few ? ragged_plan_kernel<256> : ragged_plan_kernel<1024>,
+                dim3(1 + packed_map_blocks(p.B, p.nmaps, threads)), dim3(threads), 0, st, p);
 }
 
 // A dimension of one element may have any stride; it gets a dense one, which the encoder takes.

@@ -38,6 +38,9 @@ __device__ __forceinline__ uint32_t warp_id() {
 // lets the next kernel's waiting CTAs take SMs and costs ~7 %; the trigger at
 // CTA exit gains ~3.5 % per fwd+bwd step).
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel's blocks start, and wait in grid_dep_wait, once all blocks of this one have come here.  After
+// this kernel's own grid_dep_wait only, so that they do not start beside what ran before it.
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------ mbarrier
 
