@@ -13,7 +13,7 @@
 // A warp takes one token and U times 32 lanes of its heads, all loads first, with the
 // token's cosines and sines in registers: what bounds the passes is memory.  Measured at 16384 tokens, 32 heads and 8
 // of 128, all channels turned: the pass 56 us (335 MB: 6.0 TB/s, of 6.8 that a copy reaches), the gradients 90 us (503 MB:
-// 5.6 TB/s) and their sum 3, the append to the cache 66 us (354 MB: 5.4 TB/s); at 8 tokens 1.9 us and 3.4.
+// 5.6 TB/s) and their sum 3, the append to the cache 66 us (354 MB: 5.4 TB/s); at 64 tokens the pass 1.9 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
