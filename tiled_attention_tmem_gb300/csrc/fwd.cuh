@@ -46,8 +46,8 @@
 // A scheduling warp claims the items; every other line of the pipeline is shared, and so are its tiles, since
 // what bounds it is the same: the matrix pipe, and around it an item's start and end (about 3000 cycles, that of a key
 // tile's MMAs being 2048 at d = 128).  Measured, causal, 32 heads on 8 of 128: one sequence of 16384 1180 us (1860
-// TFLOP/s, 0.97 of the measured matrix peak), 16 up to 2048 150 us (157 in the tiles of two); 14 on 2 of 256, five up to 1999,
-// 55 us.
+// TFLOP/s, 0.97 of the measured matrix peak), 16 up to 2048 155 us, of which the item changes are a third; 14 on 2 of 256,
+// five up to 1999, 55 us.
 #pragma once
 #include <cuda_bf16.h>
 

@@ -57,15 +57,15 @@ bool few_items(const PackedShape& s) {
 // Measured, tiles of two (with one of them used where items are few) / two CTAs in us, d = 128.  Few items, causal: one
 // sequence of 2048, eight heads on one, 24.9 / 20.1; one of 16384, one head, 156 / 123; two of 2048, eight on eight, 41 /
 // 27; at d = 96 41 / 33, at the worst one of 8192, four on two, 81 / 93.  Above that, one of 6000, 32 on one: 176 /
-// 203.  Many, 32 heads on 8, lengths at random around the mean: causal, 64 of 256: 99 / 80, 16 of 1024: 183 / 179, 12 of
-// 1536: 257 / 262, 4 of 4096: 608 / 672; without the mask, where an item has twice the keys and both of its tiles the same
-// ones, 128 of 128: 103 / 92, 64 of 256: 120 / 114, 32 of 512: 149 / 155.  At d = 96, whose tiles' last quarter is
-// loaded as zeros, by half of that: causal, 32 of 512: 103 / 99, 24 of 768: 146 / 165.
-// (d = 64 always runs two: 128 of 128 86 / 60 us, 8 of 2048 202 / 181, 2 of 8192 395 / 378; at the worst eight heads on
-// eight without the mask, 2 around 8192: 207 / 224.)
+// 203.  Many, 32 heads on 8, lengths at random, means in a loop at the power limit: causal, 42 of 431: 115 / 100, 21 of 758:
+// 139 / 135, 16 of 1160: 191 / 195, 4 of 5001: 669 / 745; without the mask, where an item has twice the keys and both of
+// its tiles the same ones, 128 of 129: 100 / 89, 64 of 257: 118 / 113, 32 of 475: 153 / 161.  d = 96, whose tiles' last
+// quarter is loaded as zeros: causal, 32 of 475: 101 / 100, 21 of 758: 132 / 150; without the mask 85 of 206: 109 / 103, 32
+// of 475: 144 / 168.  (d = 64 always runs two: causal, 32 of 475: 90 / 74, 8 of 2182: 198 / 186, 4 of 5001: 497 / 505; without the
+// mask 930 / 971.)
 bool two_ctas(const PackedShape& s, int causal) {
   const long long mean = s.T / s.B;
-  return few_items(s) || (causal ? mean : 4 * mean) <= (s.d == 96 ? 640 : 1280);
+  return few_items(s) || (causal ? mean : 3 * mean) <= (s.d == 96 ? 576 : 960);
 }
 
 template <class P>
