@@ -203,6 +203,40 @@ def test_append_in_slots_given_twice_and_two_at_once():
     assert torch.equal(cache.k_codes, ref.k_codes) and torch.equal(cache.v_scales, ref.v_scales)
 
 
+def test_offsets_past_32_bits():
+    """Arrays of over 2^31 elements and a pool of over 2^32 bytes: the first and the last tokens are those of a short call."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    T, n = 530000, 40
+    q, k, rotary, pos, wq, wk, v = make(n, 32, 1, 128, 128, value=True, loose=False)
+    long = [torch.zeros((T, t.shape[1], 128), dtype=torch.bfloat16, device="cuda:0") for t in (q, k)]
+    assert long[0].numel() > 2 ** 31
+    at = torch.full((T,), -1, dtype=torch.int32, device="cuda:0")
+    for part in (slice(0, n), slice(T - n, T)):
+        long[0][part], long[1][part], at[part] = q, k, pos
+    short = api.qk_norm_rope(q, k, rotary, pos, wq, wk)
+    back = api.qk_norm_rope_backward(q, k, q, k, rotary, pos, wq, wk)
+    got = api.qk_norm_rope(*long, rotary, at, wq, wk, out=[t.clone() for t in long])
+    grads = api.qk_norm_rope_backward(*long, *long, rotary, at, wq, wk)
+    for part in (slice(0, n), slice(T - n, T)):
+        assert all(torch.equal(t[part], r) for t, r in zip(got, short))
+        assert all(torch.equal(t[part], r) for t, r in zip(grads[:2], back[:2]))
+    assert not bool(got[0][n:T - n].any()) and not bool(grads[0][n:T - n].any())
+    for dw, x, w in zip(grads[2:], (q, k), (wq, wk)):  # twice the short call's sums
+        _, _, ref_w, size_w = R.backward(x, x, w, 1e-6, rotary, pos, False)
+        R.check_weight(dw, 2 * ref_w, 2 * size_w, 2 * n * x.shape[1])
+    del got, grads, long
+    torch.cuda.empty_cache()
+    big, small = api.KV4Cache.empty(525000, 1, 128, 128), api.KV4Cache.empty(1, 1, 128, 128)
+    assert big.k_codes.numel() > 2 ** 32
+    slots = 524990 * 128 + torch.arange(n, device="cuda:0")
+    y = api.kv4_append(q, k, v, rotary, pos, slots, big, wq, wk)
+    assert torch.equal(y, api.kv4_append(q, k, v, rotary, pos, slots - 524990 * 128, small, wq, wk))
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(big, name)[524990], getattr(small, name)[0])
+    assert not bool(big.k_codes[0].any()) and not bool(big.k_codes[524989].any())
+
+
 # ------------------------------------------------------------------ calls
 
 def test_refused_by_the_torch_layer():
