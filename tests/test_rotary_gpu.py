@@ -123,6 +123,36 @@ def test_strides_empty_calls_and_tables_without_rows():
     assert not bool(y.any())
 
 
+@pytest.mark.parametrize("d,turned,interleaved", [(64, 64, False), (96, 32, True), (128, 128, False), (128, 64, True), (192, 160, False),
+                                                  (256, 256, False), (384, 384, True)])
+def test_each_product_and_sum_is_rounded_alone(d, turned, interleaved):
+    """Without weights the results are those of fp32 products and sums taken one after the other, bit for bit, and so are the
+    gradients and what an append gives.  (Taken together, two of 10^5 results come out otherwise.)"""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    T, H, Hkv = 3001, 6, 2
+    q, k, rotary, pos, _, _, v = make(T, H, Hkv, d, turned, seed=d, weights=False, positions=32768, loose=False, value=True)
+    a, b = R.channels(turned, interleaved, "cuda:0")
+    row = rotary[pos.long()][:, None]
+    c, s = row[..., :turned // 2], row[..., turned // 2:]
+
+    def turn(x, s):
+        x = x.float()
+        y = x.clone()
+        y[..., a] = x[..., a] * c - x[..., b] * s
+        y[..., b] = x[..., b] * c + x[..., a] * s
+        return y.to(torch.bfloat16)
+
+    want = turn(q, s), turn(k, s)
+    got = api.qk_norm_rope(q, k, rotary, pos, interleaved=interleaved)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    back = api.qk_norm_rope_backward(q, k, q, k, rotary, pos, interleaved=interleaved)
+    assert torch.equal(back[0], turn(q, -s)) and torch.equal(back[1], turn(k, -s))
+    cache, turned_k = api.KV4Cache.empty(-(-T // 16), Hkv, 16, d), torch.empty_like(k)
+    y = api.kv4_append(q, k, v, rotary, pos, torch.arange(T, device="cuda:0"), cache, interleaved=interleaved, k_out=turned_k)
+    assert torch.equal(y, want[0]) and torch.equal(turned_k, want[1])
+
+
 # ------------------------------------------------------------------ append
 
 @pytest.mark.parametrize("d", DIMS)

@@ -102,22 +102,28 @@ __device__ __forceinline__ int angle_at(const HeadLanes<D>& at, int h) {
   return NEXT ? 4 * at.chunk[h] : 8 * at.u + 4 * h;
 }
 
+// The sum of two products that are rounded on their own.  (An add.rn of single values is never taken together with a product;
+// of pairs it is, even where both are written with their rounding: that gave other bits in two of 10^5 results.)
+__device__ __forceinline__ float2 add_alone(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
 // Turns a lane's 16 channels (two chunks of 8).  Each product and sum is rounded on its own, in this order, so
-// that the result does not depend on how they are fused.
+// that the result is that of the formula's operations one after the other.
 template <bool NEXT>
 __device__ __forceinline__ void turn(float2* x, const Angles& a) {
   if constexpr (NEXT) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float c = i & 1 ? a.c[i / 2].y : a.c[i / 2].x, s = i & 1 ? a.s[i / 2].y : a.s[i / 2].x;
-      x[i] = fadd2(fmul2(x[i], both(c)), fmul2(make_float2(x[i].y, x[i].x), make_float2(-s, s)));
+      x[i] = add_alone(fmul2(x[i], both(c)), fmul2(make_float2(x[i].y, x[i].x), make_float2(-s, s)));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 u = x[i], v = x[4 + i];
-      x[i] = fadd2(fmul2(u, a.c[i]), fmul2(v, neg2(a.s[i])));
-      x[4 + i] = fadd2(fmul2(v, a.c[i]), fmul2(u, a.s[i]));
+      x[i] = add_alone(fmul2(u, a.c[i]), fmul2(v, neg2(a.s[i])));
+      x[4 + i] = add_alone(fmul2(v, a.c[i]), fmul2(u, a.s[i]));
     }
   }
 }
