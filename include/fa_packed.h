@@ -71,7 +71,8 @@ size_t fa_packed_fwd_workspace_size(int B, int T, int H, int Hkv, int d);
  *   dv_j = sum P_ij dO_i,  dk_j = scale sum dS_ij q_i,  dq_i = scale sum_j dS_ij k_j
  * o and lse as fa_packed_fwd wrote them for the same arguments.  P and dS are rounded to bf16
  * where they enter the products, the gradients once.  Rows of no sequence (before the first
- * and behind the last that lies in [0, T)) get gradients of zero; with B = 0 every row is one.  A NaN or
+ * and behind the last that lies in [0, T)) get gradients of zero; with B = 0 every row is one.
+ * With H = 0 nothing is read or written (dk and dv, sums over no heads, are the caller's to clear).  A NaN or
  * infinity in a row of one sequence never reaches another.  The gradients must not overlap
  * one another or the inputs.
  * variant: FA_BWD_5GEMM (d <= 128; dq is summed by reductions in fp32 whose order is not fixed),

@@ -210,6 +210,25 @@ def test_calls_without_work():
     api.check_device_error()
 
 
+def test_gradients_of_keys_and_values_of_no_queries():
+    """kv heads that serve no head: sums over none, zeros in new tensors and in given ones."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, v, cu, _ = make([5, 6], 4, 2, 64)
+    none = q[:, :0]
+    lse = torch.empty((11, 0), device="cuda:0")
+    k_new = torch.full((12, 2, 72), 5.0, device="cuda:0").to(torch.bfloat16)
+    given = torch.empty_like(none), k_new[:11, :, :64], torch.full_like(v, 5.0)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for kw in (dict(grads=given), {}, dict(variant=7, stream=stream.cuda_stream)):
+        dq, dk, dv = api.packed_attention_backward(none, k, v, none, none, lse, cu, **kw)
+        torch.cuda.synchronize()
+        assert dq.shape == (11, 0, 64) and dk.shape == dv.shape == (11, 2, 64)
+        assert not bool(dk.any()) and not bool(dv.any())
+    assert bool((k_new[11] == 5).all()) and bool((k_new[..., 64:] == 5).all())
+
+
 def test_sequences_outside_the_tokens_have_none():
     import torch
     from tiled_attention_tmem_gb300 import api

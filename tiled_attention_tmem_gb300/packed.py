@@ -163,4 +163,6 @@ def packed_attention_backward(q, k, v, o, do, lse, cu, scale: float | None = Non
                           _current_stream(index))
     if st:
         _check(st, "fa_packed_bwd")
+    if H == 0:  # (no work for the library: sums over no heads)
+        dk.zero_(), dv.zero_()
     return dq, dk, dv
