@@ -87,6 +87,26 @@ def test_one_weight_of_two_and_rows_of_zeros():
     assert all(bool(torch.isfinite(t).all()) for t in back)
 
 
+def test_tokens_without_a_position_beside_weights_that_are_not_finite():
+    """Their gradients are zeros all the same, and they put nothing into the weights' sums."""
+    import math
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    for d in (64, 96, 384):
+        for interleaved in (False, True):
+            q, k, rotary, pos, wq, wk = make(40, 3, 2, d, 32, weights=True)
+            mine = R.live(pos, rotary)
+            ref = api.qk_norm_rope_backward(q, k, q, k, rotary, pos, wq, wk, interleaved=interleaved)
+            bad = [wq.clone(), wk.clone()]
+            bad[0][3], bad[0][d - 1], bad[1][0] = math.nan, math.inf, -math.inf
+            grads = [torch.full(t.shape, 5.0, device="cuda:0").to(torch.bfloat16) for t in (q, k)]
+            got = api.qk_norm_rope_backward(q, k, q, k, rotary, pos, *bad, interleaved=interleaved, grads=grads)
+            for x, y in zip(got[:2], ref):
+                assert not bool(x[~mine].any()) and not bool(torch.isfinite(x[mine]).all()) and bool((y[~mine] == 0).all())
+            # The weights' gradients have no weight in them.
+            assert torch.equal(got[2], ref[2]) and torch.equal(got[3], ref[3])
+
+
 def test_far_positions_and_large_magnitudes():
     import torch
     from tiled_attention_tmem_gb300 import api

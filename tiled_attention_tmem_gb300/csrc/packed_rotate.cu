@@ -276,12 +276,24 @@ __global__ void __launch_bounds__(256, 2) rotate_bwd_kernel(const __grid_constan
   int pos = position(job);
   while (job.tok < p.T) {
     const int tok = job.tok, first = job.at * U * L::ROWS + sub;
-    const bool live = is_live(pos);
+    if (!is_live(pos)) {  // (not as zeros through what follows: 0 times a weight that is not finite is a NaN)
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int head = first + i * L::ROWS;
+        if (!at.active || head >= gy.heads) continue;
+        uint16_t* dst = gy.out + tok * gy.out_token + head * gy.out_head;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(dst + 8 * at.chunk[h]) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      pos = position(next);
+      job = next, next = after(next);
+      continue;
+    }
     uint4 rg[U][2], rx[U][2];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int head = first + i * L::ROWS;
-      const bool have = at.active && live && head < gy.heads;
+      const bool have = at.active && head < gy.heads;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         rg[i][h] = rx[i][h] = make_uint4(0u, 0u, 0u, 0u);
@@ -293,7 +305,7 @@ __global__ void __launch_bounds__(256, 2) rotate_bwd_kernel(const __grid_constan
       }
     }
     Angles angles;
-    if (at.turned && live) {
+    if (at.turned) {
       const float* row = p.rotary + (long long)pos * p.rot;
       load_angles<true>(angles, [&](int i) {
         return *reinterpret_cast<const float4*>(row + (i >> 1) * (p.rot / 2) + angle_at<D, NEXT>(at, i & 1));
@@ -306,7 +318,7 @@ __global__ void __launch_bounds__(256, 2) rotate_bwd_kernel(const __grid_constan
       float2 g[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) unpack8(rg[i][h], g + 4 * h);
-      if (at.turned && live) turn<NEXT>(g, angles);
+      if (at.turned) turn<NEXT>(g, angles);
       if (normed) {
         float2 x[8], z[8], sum = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
 #pragma unroll
@@ -321,8 +333,8 @@ __global__ void __launch_bounds__(256, 2) rotate_bwd_kernel(const __grid_constan
           dot = ffma2(x[e], z[e], dot);
         }
         const float total = head_sum<D>(sum.x + sum.y), inner = head_sum<D>(dot.x + dot.y);
-        // (a row that is not there must not turn eps = 0 into 0 * inf)
-        const float r = live && head < gy.heads ? rsqrtf(total * (1.f / D) + p.eps) : 0.f;
+        // (a head that is not there must not turn eps = 0 into 0 * inf)
+        const float r = head < gy.heads ? rsqrtf(total * (1.f / D) + p.eps) : 0.f;
         const float2 m = both(-inner * r * (1.f / D)), r2 = both(r);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
