@@ -13,7 +13,9 @@
  * cu (int32 [B + 1], device memory) must not decrease.  Its contents are checked
  * on the device: a sequence whose tokens do not lie in [0, T) has none.  Sequences
  * of no token are allowed.  Whatever cu holds, no call reads or writes
- * outside its arrays; the results of a call whose cu decreases are unspecified.
+ * outside its arrays, or does more work than T tokens are: where sequences overlap
+ * so that they hold more than T tokens together, none is attended to.  The results of a call whose cu decreases are
+ * unspecified otherwise.
  *
  * The calls take their arguments as a structure in host memory, which is read during
  * the call only; every call enqueues its work on `stream`.

@@ -246,6 +246,35 @@ def test_sequences_outside_the_tokens_have_none():
         api.check_device_error()
 
 
+@pytest.mark.parametrize("d", (64, 128, 256))
+@pytest.mark.parametrize("B", (3, 32, 40, 300, 2100))
+def test_no_attention_where_sequences_overlap(d, B):
+    """Sequences that overlap (all of the tokens again and again) would be many times the work of the tokens: without
+    a plan, and in each way that a plan puts sequences in order, nothing is attended to, and the next call is as ever."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    T = 300
+    q, k, v, whole, host = make([T], 4, 2, d)
+    do = _do(q)
+    again = [T * (i & 1) for i in range(B + 1)]
+    for bad in (again, [0, 200, 100] + [T] * (B - 2), [0] * (B - 2) + [T, T - 1, T]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda:0")
+        held = sum(n for _, n in R.bounds(bad, T))
+        assert cu.numel() == B + 1 and held > T
+        mark = torch.full(q.shape, 3.0, device="cuda:0").to(torch.bfloat16)
+        lse = torch.full(q.shape[:2], 3.0, device="cuda:0")
+        for causal in (True, False):
+            api.packed_attention_forward(q, k, v, cu, causal=causal, out=mark, lse=lse)
+            assert bool((mark == 3).all()) and bool((lse == 3).all())
+            for variant in (0, 7):
+                api.packed_attention_backward(q, k, v, mark, do, lse, cu, causal=causal, variant=variant)
+        api.check_device_error()
+    o, lse = api.packed_attention_forward(q, k, v, whole)
+    r = R.attend(q, k, v, host, d ** -0.5, True, do)
+    R.check_forward(o, lse, r, d)
+    R.check_backward(api.packed_attention_backward(q, k, v, o, do, lse, whole), r)
+
+
 @pytest.mark.parametrize("d,H,Hkv,T", [(64, 4, 2, 90), (128, 4, 1, 1500), (192, 2, 2, 90), (256, 8, 1, 1500), (384, 2, 1, 90)])
 def test_gradients_of_rows_of_sequences_that_lie_outside(d, H, Hkv, T):
     """cu that does not decrease, with sequences that begin below 0 or end past T: those have no tokens, their

@@ -62,13 +62,14 @@ __device__ __forceinline__ void plan_maps(const RaggedPlanParams& p, int block, 
 
 // One block: sequences by length, longest first (so that what is claimed last is short; by index where there
 // are over 2048: the longest is a small part of the work then, or the launch is long anyway), and the
-// running sum of their work items.  Latency bounds it (a count or a sort, a scan): a
+// running sum of their work items.  There are none where the sequences hold more than T tokens together: they overlap (cu
+// decreases), and could be B times the work of T tokens.  Latency bounds it (a count or a sort, a scan): a
 // forward of 16 sequences takes 2.5 us more with a plan than without (6 with a sort in a block of 1024 threads, before
 // the forward's blocks started beside it).
 template <int THREADS>
 __device__ __forceinline__ void plan_schedule(const RaggedPlanParams& p) {
   __shared__ unsigned long long keys[kPlanSorted];
-  __shared__ long long sums[THREADS / 32];
+  __shared__ long long sums[THREADS / 32], tokens[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool sorted = p.B <= kPlanSorted, counted = p.B <= kPlanCounted;
   auto key_of = [&](int i) {
@@ -110,18 +111,29 @@ __device__ __forceinline__ void plan_schedule(const RaggedPlanParams& p) {
     auto seq_of = [&](int r) { return sorted ? (int)(uint32_t)keys[r] : r; };
     long long sum = 0;
     int start;
-    for (int r = r0; r < r1; ++r) sum += tiles_of(plan_seq(p, seq_of(r), start)) * p.heads;
+    long long held = 0;
+    for (int r = r0; r < r1; ++r) {
+      const int len = plan_seq(p, seq_of(r), start);
+      held += len;
+      sum += tiles_of(len) * p.heads;
+    }
     long long before = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, before, d);
       if (lane >= d) before += y;
+      held += __shfl_xor_sync(0xffffffffu, held, d);
     }
-    if (lane == 31) sums[warp] = before;
+    if (lane == 31) sums[warp] = before, tokens[warp] = held;
     __syncthreads();
     before -= sum;
     for (int w = 0; w < warp; ++w) before += sums[w];
+    held = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) held += tokens[w];
     __syncthreads();
+    const bool valid = held <= p.T;
+    if (!valid) before = 0;
     for (int r = r0; r < r1; ++r) {
       const int b = seq_of(r), len = plan_seq(p, b, start);
       const long long tiles = tiles_of(len);
@@ -133,7 +145,7 @@ __device__ __forceinline__ void plan_schedule(const RaggedPlanParams& p) {
       const int groups = p.heads / (int)g;
       const_cast<int*>(s.base)[r] = (int)min(before, (long long)kPlanItems);
       const_cast<int4*>(s.seqs)[r] = make_int4(start, len, b, (p.heads + groups - 1) / groups);
-      before += tiles * p.heads;
+      if (valid) before += tiles * p.heads;
       if (r == p.B - 1) const_cast<int*>(s.base)[p.B] = (int)min(before, (long long)kPlanItems);
     }
     if (tid == 0) {

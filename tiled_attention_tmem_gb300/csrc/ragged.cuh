@@ -79,6 +79,8 @@ __device__ __forceinline__ void ragged_schedule(const RaggedSched& s, int tile_t
     }
     my_base = my_end - items;
     total = __shfl_sync(0xffffffffu, my_end, 31);
+    // (No work where they hold more than the tokens, as in plan_schedule; few items, so the sum stays below 2^31.)
+    if (__reduce_add_sync(0xffffffffu, (unsigned)my_len) > (unsigned)s.T) total = 0;
   } else {
     total = s.base[s.B];
   }
