@@ -238,6 +238,33 @@ def test_header_is_plain_c_and_its_structures_are_what_the_binding_packs(tmp_pat
     assert offsets[3] == at(b._QK_NORM_ROPE_BWD, 33)
 
 
+# ------------------------------------------------------------------ waits
+
+WAITS = r"""
+#include <stdio.h>
+#include "ragged.cuh"
+int main() {
+  for (long long n = 0; n <= 1LL << 28; n = n ? 4 * n : 1) printf("%lld %lld\n", n, fa::ragged_wait_limit((int)n));
+  return 0;
+}
+"""
+
+
+def test_the_scheduling_warp_waits_for_the_longest_item(tmp_path):
+    """An item of the dK/dV kernel takes a step for each query tile of its sequence; with 32 heads to a kv head a tile
+    of 32 or 64 rows is 1 or 2 tokens.  A step is 2200 cycles; twice that is to be waited for, beyond the
+    two seconds that every wait has, up to the longest sequence that is taken."""
+    src, exe = tmp_path / "waits.cu", tmp_path / "waits"
+    src.write_text(WAITS)
+    r = subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", f"-I{build.CSRC}", f"-I{build.INCLUDE}", str(src), "-o", str(exe)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    limits = {int(n): int(x) for n, x in (line.split() for line in out.stdout.splitlines())}
+    assert max(limits) == 1 << 28 and limits[0] >= 4e9
+    assert all(x >= 4e9 + 2 * 2200 * n for n, x in limits.items())
+
+
 # ------------------------------------------------------------------ the references
 
 def test_reference_attention_gradients_are_those_of_differences():

@@ -14,8 +14,9 @@ constexpr int kDevErrTimeout = 6;
 enum KernelId : int { kKFwd = 1, kKBwdKV = 2, kKBwdQ = 3, kKPre = 4, kKConv = 5, kKSelfTest = 6 };
 
 // About two seconds at the maximum SM clock: far longer than any legitimate
-// wait inside these kernels (microseconds), short enough to keep a broken
-// launch from holding the GPU.
+// wait for a step of these kernels (microseconds), short enough to keep a broken
+// launch from holding the GPU.  Waits that last a whole work item have a limit that
+// grows with it (ragged.cuh).
 constexpr long long kWaitLimitCycles = 4000000000LL;
 
 struct CtaAbort {
@@ -30,13 +31,13 @@ __device__ __forceinline__ void raise_timeout(const CtaAbort& ab, int where) {
 
 // Single-thread bounded wait for the phase of `bar` with the given parity.
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, const CtaAbort& ab,
-                                         int where) {
+                                         int where, long long limit = kWaitLimitCycles) {
   if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
     if (mbar_test(bar, parity)) return true;
     if (*ab.flag) return false;
-    if (clock64() - t0 > kWaitLimitCycles) {
+    if (clock64() - t0 > limit) {
       raise_timeout(ab, where);
       return false;
     }
@@ -47,8 +48,8 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, const Ct
 // lanes saw the phase complete, so the warp-collective tcgen05 instructions that
 // follow are executed by all lanes or by none.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const CtaAbort& ab,
-                                          int where) {
-  bool ok = wait_one(bar, parity, ab, where);
+                                          int where, long long limit = kWaitLimitCycles) {
+  bool ok = wait_one(bar, parity, ab, where, limit);
   return __all_sync(0xffffffffu, ok);
 }
 

@@ -37,6 +37,11 @@ struct RaggedItem {
 constexpr int kRaggedRing = 4;        // items between the scheduling warp and its slowest reader
 constexpr int kRaggedRingBytes = 32;  // a slot of the ring
 
+// The scheduling warp waits for as long as an item takes, and longer for a longer sequence: a step (one
+// query or key tile, 2200 cycles measured, of a token at least) for each of its tokens at most.  At 4 x 10^9 cycles, the limit of all other
+// waits, a correct dK/dV item of 10^8 rows would be reported as one that hangs.
+__host__ __device__ constexpr long long ragged_wait_limit(int longest) { return kWaitLimitCycles + 8192LL * longest; }
+
 // The scheduling warp of a persistent CTA: claims work items (the first is the CTA's own
 // index, the rest come from the counter, so that idle SMs take the next ones, longest sequences first),
 // looks up their sequences and passes them to the other roles through a ring in shared memory.  Each item
@@ -49,7 +54,7 @@ __device__ __forceinline__ void ragged_schedule(const RaggedSched& s, int tile_t
                                                 volatile int* ring, uint32_t full0, uint32_t empty0, uint32_t ask,
                                                 const CtaAbort& ab, int where) {
   const int lane = lane_id();
-  int total, rank = 0, w = blockIdx.x;
+  int total, rank = 0, w = blockIdx.x, longest = 0;  // longest: tokens of the longest sequence it has passed on
   // DIRECT: lane r holds the sequence of rank r and its first item.
   int my_start = 0, my_len = 0, my_seq = lane, my_base = 0, my_end = 0;
   if constexpr (DIRECT) {
@@ -86,11 +91,12 @@ __device__ __forceinline__ void ragged_schedule(const RaggedSched& s, int tile_t
   }
   for (int t = 0;; ++t) {
     const int k = t % kRaggedRing;
-    if (!wait_warp(empty0 + 8 * k, ((t / kRaggedRing) & 1) ^ 1, ab, where)) return;
+    const long long limit = DIRECT ? kWaitLimitCycles : ragged_wait_limit(longest);  // (few items are short ones)
+    if (!wait_warp(empty0 + 8 * k, ((t / kRaggedRing) & 1) ^ 1, ab, where, limit)) return;
     if (DIRECT && t > 0) {
       w = t * (int)gridDim.x + ((t & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x);
     } else if (t > 0) {
-      if (!wait_warp(ask, (t - 1) & 1, ab, where)) return;
+      if (!wait_warp(ask, (t - 1) & 1, ab, where, limit)) return;
       if (lane == 0) w = (int)gridDim.x + atomicAdd(s.counter, 1);
       w = __shfl_sync(0xffffffffu, w, 0);
     }
@@ -122,6 +128,7 @@ __device__ __forceinline__ void ragged_schedule(const RaggedSched& s, int tile_t
     }
     __syncwarp();
     if (start < 0) return;
+    longest = max(longest, len);
   }
 }
 
