@@ -566,6 +566,38 @@ def test_forward_on_both_sides_of_the_choice_of_tiles(lengths, causal, d):
             assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("causal", (True, False))
+@pytest.mark.parametrize("d", (96, 128))
+@pytest.mark.parametrize("H,Hkv,lengths", [(16, 4, [1504, 1473, 2900, 20, 2200, 1505]), (7, 1, [2900, 1501, 36, 2200, 19]),
+                                           (8, 8, [1500, 1281, 100, 1408, 1200])])
+def test_forward_in_items_of_two_tiles(H, Hkv, lengths, d, causal):
+    """Mean lengths and items a multiprocessor well above those where items of two query tiles begin (packed_fwd.cu:
+    two_ctas), with the second tile full, of one token and empty; rows of no sequence and one of the sequences hold NaN.  Behind many empty sequences
+    the same ones run in items of one tile: other bits, so these were of two."""
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert sum(lengths) / len(lengths) > 1.1 * 960 and sum(lengths) // (128 // (H // Hkv)) * Hkv > 2.1 * sms
+    q, k, v, cu, host = make(lengths, H, Hkv, d, seed=H + d, lead=2, tail=130, spread=1.5)
+    r = R.attend(q, k, v, host, d ** -0.5, causal)
+    dirty = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda:0")
+    dirty[:2], dirty[host[-1]:], dirty[host[2]:host[3]] = True, True, True
+    poison = [t.clone() for t in (q, k, v)]
+    for t in poison:
+        t[dirty] = math.nan
+    many = torch.tensor([2] * (40 * len(lengths)) + host, dtype=torch.int32, device="cuda:0")
+    mine = ~torch.isnan(r["lse"][:, 0])
+    got = []
+    for some in (cu, many):
+        o, lse = api.packed_attention_forward(q, k, v, some, causal=causal)
+        o2, lse2 = api.packed_attention_forward(*poison, some, causal=causal)
+        api.check_device_error()
+        R.check_forward(o, lse, r, d, f"{lengths} {H}/{Hkv} d={d}")
+        assert torch.equal(o[~dirty], o2[~dirty]) and torch.equal(lse[~dirty], lse2[~dirty])
+        got.append(o[mine])
+    assert not torch.equal(*got)
+
+
 def b_bytes(cu, q, k):
     from tiled_attention_tmem_gb300 import api
     return api.packed_forward_workspace_bytes(cu.numel() - 1, q.shape[0], q.shape[1], k.shape[1], q.shape[2])
