@@ -168,6 +168,7 @@ struct FwdCfg {
   static_assert(CTAS * TMEM_COLS <= 512, "TMEM budget");
   static_assert(BN % 32 == 0 && BN <= 256 && D % 64 == 0 && D <= 384 && PVN % 64 == 0, "tile shape");
   static_assert(!(QT && QSD), "Q lives in one place");
+  static_assert(QB == 1 || QSD, "issue_s reads the one buffer of a Q tile");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
@@ -565,8 +566,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) fwd_kernel(const __grid_c
         };
         int nq[NQ] = {};  // packed: items in which each Q tile has tokens
         auto issue_s = [&](int t, int s) {
-          uint32_t qa = sbase + C::OFF_Q + t * C::Q_TILE;
-          if constexpr (RAGGED && C::QB > 1) qa += nq[t] % C::QB * (NQ * C::Q_TILE);
+          const uint32_t qa = sbase + C::OFF_Q + t * C::Q_TILE;
           const uint32_t kb = sbase + C::OFF_KV + s * C::KV_TILE;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)

@@ -60,7 +60,7 @@ __device__ __forceinline__ void plan_maps(const RaggedPlanParams& p, int block, 
   }
 }
 
-// One block: sequences by length, longest first (so that what is claimed last is short; by index where there
+// One block, for one sequence or more: sequences by length, longest first (so that what is claimed last is short; by index where there
 // are over 2048: the longest is a small part of the work then, or the launch is long anyway), and the
 // running sum of their work items.  There are none where the sequences hold more than T tokens together: they overlap (cu
 // decreases), and could be B times the work of T tokens.  Latency bounds it (a count or a sort, a scan): a
@@ -148,10 +148,7 @@ __device__ __forceinline__ void plan_schedule(const RaggedPlanParams& p) {
       if (valid) before += tiles * p.heads;
       if (r == p.B - 1) const_cast<int*>(s.base)[p.B] = (int)min(before, (long long)kPlanItems);
     }
-    if (tid == 0) {
-      *s.counter = 0;
-      if (p.B == 0) const_cast<int*>(s.base)[0] = 0;
-    }
+    if (tid == 0) *s.counter = 0;
   }
 }
 
