@@ -29,10 +29,12 @@
 // from s / tokens + b on (tokens: of a tile, BM / G rounded down); rows of a tile past its
 // tokens or the sequence's end hold lse2 = -inf and dd = 0.
 // As for equal lengths, P and dS are rounded to bf16 to be MMA operands (relative 2^-8 each, where
-// fp32 operands would need three products for one): dQ and dK, sums of rounded dS, end up off by 3e-3 in the mean, of
-// which their own rounding is 1.7e-3.  Shared-memory bandwidth bounds the dK/dV kernel at d = 128: 289 KB a
-// step of 64 query rows, 2258 cycles at 128 bytes a cycle, measured 2150; 12 causal sequences up to 4096, 32 heads
-// on 8: 1590 us, 1085 TFLOP/s.
+// fp32 operands would need three products for one), and D is a sum over the forward's o, which is bf16 too.  Relative to 64 bits dQ
+// is off by 2.8e-3 to 3.1e-3: 1.7e-3 by its own rounding, 1.9e-3 by that of dS and 1.4e-3 to 1.7e-3 by o's; dK, the same, by 2.4e-3 to
+// 2.6e-3, dV by 2.3e-3.  The dK/dV kernel at d = 128 takes 2424 cycles a step of 64 query rows, items' starts and
+// ends included (one sequence of 8192, 32 heads on 8): 1280 of them the matrix pipe is busy, and 218 KB are read from and 83 KB
+// written to shared memory, 33 % and 12 % of what the banks' counters take for the most.  So neither is full, and the chain of a step
+// (S^T and dP^T, the softmax, dV, dK and dQ) is what is left.  12 causal sequences up to 4096, 32 heads on 8: 1590 us, 1085 TFLOP/s.
 #pragma once
 #include <cuda_bf16.h>
 

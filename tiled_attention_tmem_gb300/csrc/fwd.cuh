@@ -43,8 +43,9 @@
 //
 // Packed sequences (RaggedFwdParams): the same kernel over the tiles of sequences of
 // different lengths, with the G query heads of a kv head as rows of a token (ragged.cuh).
-// A scheduling warp claims the items; every other line of the pipeline is shared, and so are its tiles, since
-// what bounds it is the same: the matrix pipe, and around it an item's start and end (about 3000 cycles, that of a key
+// A scheduling warp claims the items.  The loops over key tiles are shared; of their own are an item's start and
+// end (Q tile by tile, or through the K/V ring where it goes to TMEM; the rows behind a sequence's end; O's way out) and, for short sequences, smaller
+// tiles (RaggedFwd64, RaggedFwd128).  What bounds long sequences is the matrix pipe, and around it an item's start and end (about 3000 cycles, that of a key
 // tile's MMAs being 2048 at d = 128).  Measured, causal, 32 heads on 8 of 128: one sequence of 16384 1180 us (1860
 // TFLOP/s, 0.97 of the measured matrix peak), 16 up to 2048 155 us, of which the item changes are a third; 14 on 2 of 256,
 // five up to 1999, 55 us.

@@ -62,7 +62,7 @@ bool few_items(const PackedShape& s) {
 // its tiles the same ones, 128 of 129: 100 / 89, 64 of 257: 118 / 113, 32 of 475: 153 / 161.  d = 96, whose tiles' last
 // quarter is loaded as zeros: causal, 32 of 475: 101 / 100, 21 of 758: 132 / 150; without the mask 85 of 206: 109 / 103, 32
 // of 475: 144 / 168.  (d = 64 always runs two: causal, 32 of 475: 90 / 74, 8 of 2182: 198 / 186, 4 of 5001: 497 / 505; without the
-// mask 930 / 971.)
+// mask 930 / 971: long sequences lose 2 to 4 % by it.)
 bool two_ctas(const PackedShape& s, int causal) {
   const long long mean = s.T / s.B;
   return few_items(s) || (causal ? mean : 3 * mean) <= (s.d == 96 ? 576 : 960);

@@ -439,7 +439,7 @@ void rotate_fill(RotateParams& p, const A& a, int Hkv) {
 
 // Steps of heads a warp: kRotateSteps where that leaves 32 warps an SM, else one.  Measured at the sizes above with
 // 1 / 2 / 4 steps: the pass 71 / 62 / 66 us, the append 80 / 68 / 75 (before the arithmetic went two channels an
-// instruction); two keep 8 KB of loads in flight a warp, four cost occupancy in registers.
+// instruction); two keep 2 KB of loads in flight a warp, four cost occupancy in registers.
 constexpr int kRotateSteps = 2;
 template <int D, bool NEXT, bool APPEND>
 fa_status run_rotate(const RotateParams& p, cudaStream_t st) {
