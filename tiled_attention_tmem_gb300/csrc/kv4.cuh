@@ -51,8 +51,9 @@ constexpr float kKv4Push = 1.f + 1.f / 8192.f;
 __device__ __forceinline__ float cut12(float x) { return __uint_as_float(__float_as_uint(x) & 0xfffff000u); }
 
 // Eight bf16 channels (four words), half of a scale's group whose other half is this warp's lane ^ 1:
-// returns their codes, and the scale's byte.  All lanes call it together.
-__device__ __forceinline__ uint32_t kv4_quantise(const uint32_t* w, float inv_gain, uint32_t& scale) {
+// returns their codes, and the scale's byte.  All lanes call it together.  (The gain by reference: by value the store of 16384 tokens
+// of 8 heads of 128, with their load, took 32.8 us instead of 32.0, in 64 registers instead of 60.)
+__device__ __forceinline__ uint32_t kv4_quantise(const uint32_t* w, const float& inv_gain, uint32_t& scale) {
   uint32_t pair = 0;  // (a NaN is passed over)
 #pragma unroll
   for (int k = 0; k < 4; ++k) asm("max.bf16x2 %0, %0, %1;" : "+r"(pair) : "r"(w[k] & 0x7fff7fffu));
