@@ -337,6 +337,17 @@ def test_refused_by_the_torch_layer():
     assert all(torch.equal(a, b) for a, b in zip(before, (q, k, cache.k_codes)))
 
 
+def test_append_refuses_what_is_no_tensor():
+    import torch
+    from tiled_attention_tmem_gb300 import api
+    q, k, rotary, pos, wq, wk, v = make(16, 4, 2, 64, 64, value=True, loose=False)
+    slots, cache = torch.arange(16, device="cuda:0"), api.KV4Cache.empty(1, 2, 16, 64)
+    for kw in (dict(k_out=5), dict(out=5), dict(k_out="k"), dict(k_out=k.tolist())):
+        with pytest.raises(TypeError, match="must be a torch tensor"):
+            api.kv4_append(q, k, v, rotary, pos, slots, cache, wq, wk, **kw)
+    assert not bool(cache.k_codes.any())
+
+
 def test_graphs_that_share_a_workspace():
     """Two captured steps, forward and backward, of different sizes and one workspace, replayed in turn after their
     inputs changed: each gives what an uncaptured call gives."""

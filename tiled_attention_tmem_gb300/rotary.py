@@ -157,8 +157,8 @@ def kv4_append(q, k, v, rotary, positions, slots, cache: KV4Cache, q_weight=None
         ot, oh = H * d, d
     else:
         ot, oh = _rows(out, "out", q.shape, index, written=True)
-    ko, (kot, koh) = (0, (0, 0)) if k_out is None else (
-        k_out.data_ptr(), _rows(k_out, "k_out", shape, index, written=True))
+    kot, koh = (0, 0) if k_out is None else _rows(k_out, "k_out", shape, index, written=True)
+    ko = 0 if k_out is None else k_out.data_ptr()
     st = _b.fa_kv4_append(c.address, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, out.data_ptr(), ot,
                           oh, ko, kot, koh, table, at, wq, wk, slots.data_ptr(), many, turned, _f32(eps),
                           bool(interleaved), T, H, _current_stream(index))
