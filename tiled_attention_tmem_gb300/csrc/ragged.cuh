@@ -37,9 +37,9 @@ struct RaggedItem {
 constexpr int kRaggedRing = 4;        // items between the scheduling warp and its slowest reader
 constexpr int kRaggedRingBytes = 32;  // a slot of the ring
 
-// The scheduling warp waits for as long as an item takes, and longer for a longer sequence: a step (one
-// query or key tile, 2200 cycles measured, of a token at least) for each of its tokens at most.  At 4 x 10^9 cycles, the limit of all other
-// waits, a correct dK/dV item of 10^8 rows would be reported as one that hangs.
+// The scheduling warp waits for as long as an item takes, and longer for a longer sequence: a step (a query or
+// key tile of one token or more; 2200 to 2500 cycles measured) for each of its tokens at most.  Under the limit of all other waits,
+// 4 x 10^9 cycles, a correct dK/dV item of 10^8 rows would be reported as one that hangs.
 __host__ __device__ constexpr long long ragged_wait_limit(int longest) { return kWaitLimitCycles + 8192LL * longest; }
 
 // The scheduling warp of a persistent CTA: claims work items (the first is the CTA's own
